@@ -3,6 +3,8 @@
 ``forward(q, k, v)`` computes ``softmax(q @ k^T) @ v`` per (batch, head) for
 f32 tensors of shape ``[batch, n_heads, n_patches, head_dim]`` (q already
 scaled by the caller), through the C ABI of ``libvattn.so`` (include/vattn.h).
+The calls of a decoder layer (norm and rotation of q and k, causal attention
+under a window with its gradients, attention over a cache) are in decoder.py.
 This module only marshals arguments: every step of the computation runs in
 the library's CUDA kernel.  There is no CPU fallback; if the library is
 missing or no GPU is present the calls raise.
@@ -14,9 +16,12 @@ from ._lib import (VattnError, _check, conv1d_step_status, device_status, export
                    forward_f16_raw, forward_f16io_status, forward_f32q_raw,
                    forward_noalloc_raw, forward_raw, forward_rope_status, lib_path,
                    load_library, rope_neox_status, status_string, version)
+from .decoder import (backward_window, forward_cached, forward_window, qk_norm_rope,
+                      qk_norm_rope_backward)
 
 __all__ = ["forward", "forward_accurate", "conv1d_step", "forward_f16", "forward_f16io",
-           "forward_f32q", "forward_rope", "rope_neox", "forward_raw",
+           "forward_f32q", "forward_rope", "rope_neox", "qk_norm_rope", "qk_norm_rope_backward",
+           "forward_window", "backward_window", "forward_cached", "forward_raw",
            "forward_f16_raw", "forward_f32q_raw", "forward_noalloc_raw",
            "device_status", "VattnError", "load_library",
            "lib_path", "exported_symbols", "status_string", "version"]

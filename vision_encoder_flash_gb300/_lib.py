@@ -8,6 +8,7 @@ import re
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_PKG)
 HEADER = os.path.join(_ROOT, "include", "vattn.h")
+DECODER_HEADER = os.path.join(_ROOT, "include", "vattn_decoder.h")
 
 _STATUS = {0: "VATTN_OK", 1: "VATTN_ERR_INVALID_ARG", 2: "VATTN_ERR_UNSUPPORTED",
            3: "VATTN_ERR_MISALIGNED", 4: "VATTN_ERR_CUDA", 5: "VATTN_ERR_DEVICE_TIMEOUT"}
@@ -79,6 +80,18 @@ def load_library():
     lib.vattn_last_error_string.restype = ctypes.c_char_p
     lib.vattn_version.argtypes = []
     lib.vattn_version.restype = ctypes.c_int
+    # decoder calls: tensors and arguments as packed structs (bytes), see decoder.py
+    cp = ctypes.c_char_p
+    lib.vattn_qk_norm_rope.argtypes = [cp, cp, cp, cp, cp, vp]
+    lib.vattn_qk_norm_rope.restype = ctypes.c_int
+    lib.vattn_qk_norm_rope_backward.argtypes = [cp, cp, cp, cp, cp, cp, vp, vp, cp, vp]
+    lib.vattn_qk_norm_rope_backward.restype = ctypes.c_int
+    lib.vattn_forward_window.argtypes = [cp, cp, cp, cp, vp, cp, vp]
+    lib.vattn_forward_window.restype = ctypes.c_int
+    lib.vattn_backward_window.argtypes = [cp, cp, cp, cp, cp, vp, cp, cp, cp, cp, vp]
+    lib.vattn_backward_window.restype = ctypes.c_int
+    lib.vattn_forward_cached.argtypes = [cp, cp, cp, cp, cp, vp]
+    lib.vattn_forward_cached.restype = ctypes.c_int
     _LIB = lib
     return lib
 
@@ -262,9 +275,9 @@ def version() -> int:
     return int(load_library().vattn_version())
 
 
-def exported_symbols() -> list[str]:
-    """Function names declared in include/vattn.h."""
-    with open(HEADER) as f:
+def exported_symbols(header: str = HEADER) -> list[str]:
+    """Function names declared in include/vattn.h (or another of its headers)."""
+    with open(header) as f:
         text = f.read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     return sorted(set(re.findall(r"\b(vattn_[a-z0-9_]+)\s*\(", text)))

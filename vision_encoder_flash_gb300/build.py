@@ -1,6 +1,6 @@
 """Build ``libvattn.so`` (the C-ABI library) in-tree with nvcc for sm_103a.
 
-One translation unit, one ``-gencode`` (compute_103a -> sm_103a), CUDA
+Two translation units compiled in parallel, one ``-gencode`` (compute_103a -> sm_103a), CUDA
 runtime linked statically so the library loads on hosts without a GPU
 driver (the tests check its exported symbols there).
 """
@@ -14,12 +14,17 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-SOURCES = [os.path.join(CSRC, "vattn_api.cu")]
+SOURCES = [os.path.join(CSRC, "vattn_api.cu"), os.path.join(CSRC, "decoder_api.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, "attn_kernel.cuh"), os.path.join(CSRC, "stage_kernel.cuh"),
                   os.path.join(CSRC, "rope_kernel.cuh"),
                   os.path.join(CSRC, "conv1d_kernel.cuh"),
                   os.path.join(CSRC, "ptx.cuh"),
-                  os.path.join(ROOT, "include", "vattn.h")]
+                  os.path.join(CSRC, "host_common.h"), os.path.join(CSRC, "elem.cuh"),
+                  os.path.join(CSRC, "qk_norm_rope_kernel.cuh"),
+                  os.path.join(CSRC, "window_common.cuh"),
+                  os.path.join(CSRC, "window_rows_kernel.cuh"),
+                  os.path.join(ROOT, "include", "vattn.h"),
+                  os.path.join(ROOT, "include", "vattn_decoder.h")]
 LIB = os.path.join(PKG, "libvattn.so")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
@@ -43,7 +48,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc_path(), ARCH, "-O3", "-std=c++17", "-lineinfo", "--cudart=static",
-           "-Xcompiler", "-fPIC", "-shared", "-I", os.path.join(ROOT, "include"),
+           "--threads", str(len(SOURCES)), "-Xcompiler", "-fPIC", "-shared", "-I", os.path.join(ROOT, "include"),
            "-o", tmp] + SOURCES
     if verbose:
         cmd.insert(1, "-Xptxas=-v")

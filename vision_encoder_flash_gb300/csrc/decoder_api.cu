@@ -1,0 +1,606 @@
+// decoder_api.cu -- the C ABI declared in include/vattn_decoder.h: argument
+// checks, variant choice and launches of the decoder calls on sm_103a.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/vattn_decoder.h"
+#include "host_common.h"
+#include "qk_norm_rope_kernel.cuh"
+#include "window_rows_kernel.cuh"
+
+namespace {
+
+using vattn::host::clear_error;
+using vattn::host::cuda_fail;
+using vattn::host::fail;
+using vattn::host::Workspace;
+
+constexpr int64_t kMaxRows = (int64_t{1} << 30) - 1;  // positions and their differences fit in 32 bits
+
+int elem_size(int32_t dtype) { return dtype == VATTN_F32 ? 4 : 2; }
+
+// ------------------------------------------------------------ tensor checks
+// A tensor of a call: its rows and the sizes of its dimensions.
+struct Tensor {
+  const char* name;
+  const vattn_rows* t;
+  int64_t size[3];  // batch, heads, rows
+  int64_t dim;
+  int esize;
+  bool out;
+
+  uintptr_t base() const { return reinterpret_cast<uintptr_t>(t->data); }
+  bool empty() const { return size[0] == 0 || size[1] == 0 || size[2] == 0; }
+  // bytes from the first element to the end of the last row (stride checks passed)
+  uint64_t extent() const {
+    uint64_t e = static_cast<uint64_t>(dim);
+    for (int i = 0; i < 3; ++i) e += static_cast<uint64_t>(size[i] - 1) * static_cast<uint64_t>(t->stride[i]);
+    return e * static_cast<uint64_t>(esize);
+  }
+};
+
+// Every element of a tensor of these sizes and strides has its own address:
+// from the innermost dimension outwards each stride passes all that is inside.
+bool distinct(const int64_t (&size)[3], const int64_t (&stride)[3], int64_t dim) {
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int a, int b) { return stride[a] < stride[b]; });
+  int64_t inside = dim;
+  for (int i : order) {
+    if (size[i] <= 1) continue;
+    if (stride[i] < inside) return false;
+    inside += (size[i] - 1) * stride[i];
+  }
+  return true;
+}
+
+vattn_status check_tensor(const Tensor& x, int row_align_bytes) {
+  if (x.empty()) return VATTN_OK;
+  if (!x.t || !x.t->data) return fail(VATTN_ERR_INVALID_ARG, "null %s", x.name);
+  const char* dims[3] = {"batch", "head", "row"};
+  for (int i = 0; i < 3; ++i) {
+    const int64_t s = x.t->stride[i];
+    if (x.size[i] <= 1) continue;
+    if (s < 0) return fail(VATTN_ERR_INVALID_ARG, "%s: negative %s stride", x.name, dims[i]);
+    if (s > (int64_t{1} << 38) || (x.size[i] - 1) > (int64_t{1} << 58) / (s > 0 ? s : 1))
+      return fail(VATTN_ERR_UNSUPPORTED, "%s: %s stride %lld too large", x.name, dims[i], (long long)s);
+    if (s * x.esize % row_align_bytes != 0)
+      return fail(VATTN_ERR_MISALIGNED, "%s: %s stride %lld is not a multiple of %d bytes", x.name,
+                  dims[i], (long long)s, row_align_bytes);
+  }
+  const int align = row_align_bytes > x.esize ? row_align_bytes : x.esize;
+  if (x.base() % static_cast<uintptr_t>(align) != 0)
+    return fail(VATTN_ERR_MISALIGNED, "%s must be %d-byte aligned", x.name, align);
+  if (x.out && !distinct(x.size, x.t->stride, x.dim))
+    return fail(VATTN_ERR_INVALID_ARG, "%s: elements share addresses (a broadcast or overlapping view)", x.name);
+  return VATTN_OK;
+}
+
+bool same_rows(const Tensor& a, const Tensor& b) {
+  if (a.base() != b.base() || a.dim != b.dim || a.esize != b.esize) return false;
+  for (int i = 0; i < 3; ++i)
+    if (a.size[i] != b.size[i] || (a.size[i] > 1 && a.t->stride[i] != b.t->stride[i])) return false;
+  return true;
+}
+
+// No element of a is an element of b: their byte ranges are apart, or they
+// are head ranges of one packed buffer (equal strides, b's heads some whole
+// number of head strides behind a's, and the union of both has distinct
+// elements).
+bool apart(const Tensor& a, const Tensor& b) {
+  if (a.empty() || b.empty()) return true;
+  if (a.base() + a.extent() <= b.base() || b.base() + b.extent() <= a.base()) return true;
+  const Tensor& lo = a.base() <= b.base() ? a : b;
+  const Tensor& hi = a.base() <= b.base() ? b : a;
+  if (lo.esize != hi.esize || lo.dim != hi.dim || lo.size[0] != hi.size[0] || lo.size[2] != hi.size[2]) return false;
+  for (int i = 0; i < 3; i += 2)
+    if (lo.size[i] > 1 && lo.t->stride[i] != hi.t->stride[i]) return false;
+  if (lo.size[1] > 1 && hi.size[1] > 1 && lo.t->stride[1] != hi.t->stride[1]) return false;
+  const uint64_t bytes = hi.base() - lo.base();
+  if (bytes % static_cast<uint64_t>(lo.esize) != 0) return false;
+  const int64_t delta = static_cast<int64_t>(bytes / static_cast<uint64_t>(lo.esize));
+  // head stride of the packed buffer (one head each: their distance)
+  const int64_t sh = lo.size[1] > 1 ? lo.t->stride[1] : (hi.size[1] > 1 ? hi.t->stride[1] : delta);
+  if (sh <= 0 || delta % sh != 0 || delta / sh < lo.size[1]) return false;
+  const int64_t size[3] = {lo.size[0], delta / sh + hi.size[1], lo.size[2]};
+  const int64_t stride[3] = {lo.t->stride[0], sh, lo.t->stride[2]};
+  return distinct(size, stride, lo.dim);
+}
+
+vattn_status check_apart(const Tensor& a, const Tensor& b) {
+  if (apart(a, b)) return VATTN_OK;
+  return fail(VATTN_ERR_INVALID_ARG, "%s overlaps %s", a.name, b.name);
+}
+
+// Plain memory [p, p + bytes) against a tensor's range.
+vattn_status check_apart_bytes(const void* p, uint64_t bytes, const char* name, const Tensor& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(p);
+  if (p == nullptr || bytes == 0 || b.empty()) return VATTN_OK;
+  if (x + bytes <= b.base() || b.base() + b.extent() <= x) return VATTN_OK;
+  return fail(VATTN_ERR_INVALID_ARG, "%s overlaps %s", name, b.name);
+}
+
+vattn_status current_device(int* device) {
+  const cudaError_t e = cudaGetDevice(device);
+  return e == cudaSuccess ? VATTN_OK : cuda_fail(e, "cudaGetDevice");
+}
+
+vattn_status launched(const char* what) {
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? VATTN_OK : cuda_fail(e, what);
+}
+
+// ------------------------------------------------------------ norm + rotation
+vattn_status check_qk(const vattn_qk_args* a) {
+  if (!a) return fail(VATTN_ERR_INVALID_ARG, "null args");
+  if (a->batch < 0 || a->n_q_heads < 0 || a->n_kv_heads < 0 || a->n_patches < 0)
+    return fail(VATTN_ERR_INVALID_ARG, "negative size (batch=%lld n_q_heads=%lld n_kv_heads=%lld n_patches=%lld)",
+                (long long)a->batch, (long long)a->n_q_heads, (long long)a->n_kv_heads, (long long)a->n_patches);
+  if (a->head_dim < 1) return fail(VATTN_ERR_INVALID_ARG, "head_dim must be >= 1");
+  if (a->head_dim > VATTN_MAX_HEAD_DIM)
+    return fail(VATTN_ERR_UNSUPPORTED, "head_dim %lld > %d", (long long)a->head_dim, VATTN_MAX_HEAD_DIM);
+  if (a->rope_dims < 0 || a->rope_dims > a->head_dim)
+    return fail(VATTN_ERR_INVALID_ARG, "rope_dims %lld outside [0, head_dim = %lld]", (long long)a->rope_dims,
+                (long long)a->head_dim);
+  if (!(a->base > 0.0) || !std::isfinite(a->base))
+    return fail(VATTN_ERR_INVALID_ARG, "base must be a finite positive number");
+  if (!(a->eps >= 0.0f) || !std::isfinite(a->eps))
+    return fail(VATTN_ERR_INVALID_ARG, "eps must be a finite number >= 0");
+  if (a->dtype < VATTN_F32 || a->dtype > VATTN_BF16)
+    return fail(VATTN_ERR_INVALID_ARG, "unknown dtype %d", (int)a->dtype);
+  if (a->weight_dtype != VATTN_F32 && a->weight_dtype != a->dtype)
+    return fail(VATTN_ERR_UNSUPPORTED, "weight_dtype must be VATTN_F32 or dtype");
+  if (a->batch > kMaxRows || a->n_patches > kMaxRows || a->n_q_heads > kMaxRows || a->n_kv_heads > kMaxRows ||
+      a->batch * a->n_patches > (int64_t{1} << 36))
+    return fail(VATTN_ERR_UNSUPPORTED, "sizes must stay below 2^30 each, 2^36 tokens together");
+  if (a->pos0 < 0) return fail(VATTN_ERR_INVALID_ARG, "pos0 must be >= 0");
+  if (a->pos0 > INT32_MAX - a->n_patches)
+    return fail(VATTN_ERR_UNSUPPORTED, "positions must fit in 32 bits");
+  if ((reinterpret_cast<uintptr_t>(a->positions) | reinterpret_cast<uintptr_t>(a->factors)) & 3u)
+    return fail(VATTN_ERR_MISALIGNED, "positions and factors must be 4-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(a->q_weight) | reinterpret_cast<uintptr_t>(a->k_weight)) %
+      static_cast<uintptr_t>(elem_size(a->weight_dtype)))
+    return fail(VATTN_ERR_MISALIGNED, "weights must be aligned to their element");
+  return VATTN_OK;
+}
+
+Tensor qk_tensor(const char* name, const vattn_rows* t, const vattn_qk_args* a, bool is_q, bool out) {
+  return Tensor{name, t, {a->batch, is_q ? a->n_q_heads : a->n_kv_heads, a->n_patches}, a->head_dim,
+                elem_size(a->dtype), out};
+}
+
+// Vector width V of a call: the widest of 16 bytes, 8 bytes (16-bit types)
+// and one element whose slots cut the row's two rotated halves and its rest
+// evenly and whose accesses are aligned in every tensor.
+int qk_vector(const Tensor* const* ts, int n, const vattn_qk_args* a) {
+  const int64_t half = a->rope_dims / 2, rest = a->head_dim - 2 * half;
+  const int es = elem_size(a->dtype);
+  for (int v : {16 / es, 4}) {
+    bool ok = half % v == 0 && rest % (2 * v) == 0;
+    for (int i = 0; ok && i < n; ++i) {
+      ok = ts[i]->base() % static_cast<uintptr_t>(v * es) == 0;
+      for (int d = 0; ok && d < 3; ++d) ok = ts[i]->size[d] <= 1 || ts[i]->t->stride[d] % v == 0;
+    }
+    if (ok) return v;
+  }
+  return 1;
+}
+
+void qk_strides(long long (&to)[3], const vattn_rows* t) {
+  for (int i = 0; i < 3; ++i) to[i] = t ? t->stride[i] : 0;
+}
+
+// Sizes, angles and the split of the heads: 8 heads per block and token
+// (angles shared by them), fewer while that leaves under four blocks per
+// multiprocessor.
+void qk_plan(vattn::QkParams* p, const vattn_qk_args* a, int v, int sms, int64_t* blocks_x) {
+  p->positions = a->positions;
+  p->factors = a->factors;
+  p->tokens = a->batch * a->n_patches;
+  p->pos0 = a->pos0;
+  p->n = static_cast<int>(a->n_patches);
+  p->D = static_cast<int>(a->head_dim);
+  p->half = static_cast<int>(a->rope_dims / 2);
+  p->w_f32 = a->weight_dtype == VATTN_F32;
+  p->eps = a->eps;
+  const double two_pi = 6.283185307179586476925286766559;
+  for (int i = 0; i < p->half; ++i)
+    p->turns[i] = std::pow(a->base, -2.0 * i / static_cast<double>(a->rope_dims)) / two_pi;
+  const int rest = p->D - 2 * p->half;
+  p->slots = p->half / v + (rest / 2 + v - 1) / v + (v == 1 ? rest & 1 : 0);
+  p->log_lanes = 0;
+  while ((1 << p->log_lanes) < p->slots && p->log_lanes < 5) ++p->log_lanes;
+  const int groups = vattn::kQkThreads >> p->log_lanes;
+  *blocks_x = (p->tokens + groups - 1) / groups;
+  int per = 8;
+  for (;; per /= 2) {
+    int64_t slices = 0;
+    for (int i = 0; i < 2; ++i) slices += (p->t[i].heads + per - 1) / per;
+    if (per == 1 || slices * *blocks_x >= 4LL * sms) break;
+  }
+  for (int i = 0; i < 2; ++i) {
+    int hp = per;
+    while ((p->t[i].heads + hp - 1) / hp > 16384) hp *= 2;  // grid limit in y
+    p->t[i].heads_per_slice = hp;
+    p->t[i].slices = (p->t[i].heads + hp - 1) / hp;
+  }
+}
+
+template <typename T, bool kBackward>
+vattn_status qk_launch(const vattn::QkParams& p, int v, dim3 grid, cudaStream_t stream) {
+  auto go = [&](auto kernel) {
+    kernel<<<grid, vattn::kQkThreads, 0, stream>>>(p);
+    return launched("norm and rotation kernel launch");
+  };
+  if constexpr (kBackward) {
+    if constexpr (sizeof(T) == 2)
+      if (v == 8) return go(vattn::vattn_qk_norm_rope_backward_kernel<T, 8, 1>);
+    if (v == 4) return go(vattn::vattn_qk_norm_rope_backward_kernel<T, 4, 1>);
+    return go(vattn::vattn_qk_norm_rope_backward_kernel<T, 1, 2>);
+  } else {
+    if constexpr (sizeof(T) == 2)
+      if (v == 8) return go(vattn::vattn_qk_norm_rope_kernel<T, 8, 1>);
+    if (v == 4) return go(vattn::vattn_qk_norm_rope_kernel<T, 4, 1>);
+    return go(vattn::vattn_qk_norm_rope_kernel<T, 1, 2>);
+  }
+}
+
+template <bool kBackward>
+vattn_status qk_dispatch(const vattn::QkParams& p, int32_t dtype, int v, dim3 grid, cudaStream_t stream) {
+  switch (dtype) {
+    case VATTN_F32: return qk_launch<float, kBackward>(p, v, grid, stream);
+    case VATTN_F16: return qk_launch<__half, kBackward>(p, v, grid, stream);
+    default: return qk_launch<__nv_bfloat16, kBackward>(p, v, grid, stream);
+  }
+}
+
+// ------------------------------------------------------------ attention
+vattn_status check_window_args(const vattn_window_args* a) {
+  if (!a) return fail(VATTN_ERR_INVALID_ARG, "null args");
+  if (a->batch < 0 || a->n_q_heads < 0 || a->n_kv_heads < 0 || a->n_queries < 0 || a->n_keys < 0)
+    return fail(VATTN_ERR_INVALID_ARG,
+                "negative size (batch=%lld n_q_heads=%lld n_kv_heads=%lld n_queries=%lld n_keys=%lld)",
+                (long long)a->batch, (long long)a->n_q_heads, (long long)a->n_kv_heads,
+                (long long)a->n_queries, (long long)a->n_keys);
+  if (a->head_dim < 1) return fail(VATTN_ERR_INVALID_ARG, "head_dim must be >= 1");
+  if (a->head_dim > VATTN_MAX_HEAD_DIM || a->head_dim % 8 != 0)
+    return fail(VATTN_ERR_UNSUPPORTED, "head_dim %lld: a multiple of 8 up to %d is needed (16-byte rows)",
+                (long long)a->head_dim, VATTN_MAX_HEAD_DIM);
+  if (a->dtype != VATTN_F16 && a->dtype != VATTN_BF16)
+    return fail(VATTN_ERR_UNSUPPORTED, "dtype must be VATTN_F16 or VATTN_BF16");
+  if (a->n_kv_heads == 0 ? a->n_q_heads != 0 : a->n_q_heads % a->n_kv_heads != 0)
+    return fail(VATTN_ERR_INVALID_ARG, "n_q_heads %lld is not a multiple of n_kv_heads %lld",
+                (long long)a->n_q_heads, (long long)a->n_kv_heads);
+  if (a->n_queries > kMaxRows || a->n_keys > kMaxRows)
+    return fail(VATTN_ERR_UNSUPPORTED, "n_queries and n_keys must stay below 2^30");
+  if (a->n_q_heads > kMaxRows || a->batch > kMaxRows || a->batch * a->n_q_heads > kMaxRows)
+    return fail(VATTN_ERR_UNSUPPORTED, "batch * n_q_heads must stay below 2^30");
+  if (a->window < 0) return fail(VATTN_ERR_INVALID_ARG, "window must be >= 0");
+  if (a->n_sinks < 0) return fail(VATTN_ERR_INVALID_ARG, "n_sinks must be >= 0");
+  if (!(a->scale > 0.0f) || !std::isfinite(a->scale))
+    return fail(VATTN_ERR_INVALID_ARG, "scale must be a finite positive number");
+  if ((reinterpret_cast<uintptr_t>(a->kv_len) | reinterpret_cast<uintptr_t>(a->q_start)) & 3u)
+    return fail(VATTN_ERR_MISALIGNED, "kv_len and q_start must be 4-byte aligned");
+  if (reinterpret_cast<uintptr_t>(a->tree) & 7u)
+    return fail(VATTN_ERR_MISALIGNED, "tree must be 8-byte aligned");
+  return VATTN_OK;
+}
+
+Tensor window_tensor(const char* name, const vattn_rows* t, const vattn_window_args* a, bool is_q, bool out) {
+  return Tensor{name, t, {a->batch, is_q ? a->n_q_heads : a->n_kv_heads, is_q ? a->n_queries : a->n_keys},
+                a->head_dim, 2, out};
+}
+
+vattn::WindowParams window_params(const vattn_window_args* a) {
+  vattn::WindowParams w{};
+  w.kv_len = a->kv_len;
+  w.q_start = a->q_start;
+  w.tree = a->tree;
+  w.batch = static_cast<int>(a->batch);
+  w.heads = static_cast<int>(a->n_q_heads);
+  w.kv_heads = static_cast<int>(a->n_kv_heads);
+  w.group = a->n_kv_heads > 0 ? static_cast<int>(a->n_q_heads / a->n_kv_heads) : 0;
+  w.n_queries = static_cast<int>(a->n_queries);
+  w.n_keys = static_cast<int>(a->n_keys);
+  w.dim = static_cast<int>(a->head_dim);
+  const int64_t none = int64_t{1} << 30;
+  w.window = static_cast<int>(a->window == 0 || a->window > none ? none : a->window);
+  w.sinks = static_cast<int>(a->n_sinks > none ? none : a->n_sinks);
+  w.scale = a->scale;
+  return w;
+}
+
+vattn::RowsTensor rows_tensor(const vattn_rows* t) {
+  vattn::RowsTensor r{};
+  if (t) {
+    r.p = t->data;
+    for (int i = 0; i < 3; ++i) r.s[i] = t->stride[i];
+  }
+  return r;
+}
+
+unsigned rows_grid(int64_t rows) {
+  return static_cast<unsigned>((rows + vattn::kRowsWarps - 1) / vattn::kRowsWarps);
+}
+
+vattn_status forward_checks(const vattn_rows* q, const vattn_rows* k, const vattn_rows* v,
+                            const vattn_rows* out, const float* lse, const vattn_window_args* a) {
+  const Tensor tq = window_tensor("q", q, a, true, false), tk = window_tensor("k", k, a, false, false),
+               tv = window_tensor("v", v, a, false, false), to = window_tensor("out", out, a, true, true);
+  for (const Tensor* t : {&tq, &tk, &tv, &to}) {
+    const vattn_status st = check_tensor(*t, 16);
+    if (st != VATTN_OK) return st;
+  }
+  for (const Tensor* t : {&tq, &tk, &tv}) {
+    const vattn_status st = check_apart(to, *t);
+    if (st != VATTN_OK) return st;
+  }
+  if (reinterpret_cast<uintptr_t>(lse) & 3u) return fail(VATTN_ERR_MISALIGNED, "lse must be 4-byte aligned");
+  const uint64_t bytes = static_cast<uint64_t>(a->batch) * a->n_q_heads * a->n_queries * 4u;
+  for (const Tensor* t : {&tq, &tk, &tv, &to}) {
+    const vattn_status st = check_apart_bytes(lse, bytes, "lse", *t);
+    if (st != VATTN_OK) return st;
+  }
+  return VATTN_OK;
+}
+
+vattn_status forward_rows(const vattn_rows* q, const vattn_rows* k, const vattn_rows* v,
+                          const vattn_rows* out, float* lse, const vattn_window_args* a,
+                          cudaStream_t stream) {
+  vattn::RowsParams p{};
+  p.w = window_params(a);
+  p.q = rows_tensor(q);
+  p.k = rows_tensor(k);
+  p.v = rows_tensor(v);
+  p.out = rows_tensor(out);
+  p.lse = lse;
+  const unsigned grid = rows_grid(a->batch * a->n_q_heads * a->n_queries);
+  if (a->dtype == VATTN_F16)
+    vattn::vattn_window_rows_kernel<__half><<<grid, vattn::kRowsWarps * 32, 0, stream>>>(p);
+  else
+    vattn::vattn_window_rows_kernel<__nv_bfloat16><<<grid, vattn::kRowsWarps * 32, 0, stream>>>(p);
+  return launched("attention kernel launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+vattn_status vattn_qk_norm_rope(const vattn_rows* q, const vattn_rows* k, const vattn_rows* q_out,
+                                const vattn_rows* k_out, const vattn_qk_args* a, void* stream_ptr) {
+  clear_error();
+  vattn_status st = check_qk(a);
+  if (st != VATTN_OK) return st;
+  const Tensor tq = qk_tensor("q", q, a, true, false), tk = qk_tensor("k", k, a, false, false),
+               oq = qk_tensor("q_out", q_out, a, true, true), ok = qk_tensor("k_out", k_out, a, false, true);
+  const Tensor* all[4] = {&tq, &tk, &oq, &ok};
+  for (const Tensor* t : all)
+    if ((st = check_tensor(*t, elem_size(a->dtype))) != VATTN_OK) return st;
+  if (!oq.empty() && !same_rows(oq, tq) && (st = check_apart(oq, tq)) != VATTN_OK) return st;
+  if (!ok.empty() && !same_rows(ok, tk) && (st = check_apart(ok, tk)) != VATTN_OK) return st;
+  if ((st = check_apart(oq, tk)) != VATTN_OK || (st = check_apart(ok, tq)) != VATTN_OK ||
+      (st = check_apart(oq, ok)) != VATTN_OK)
+    return st;
+  if (tq.empty() && tk.empty()) return VATTN_OK;
+
+  int device = 0, sms = 0;
+  if ((st = current_device(&device)) != VATTN_OK) return st;
+  if ((st = vattn::host::sm_count(device, &sms)) != VATTN_OK) return st;
+  const Tensor* used[4];
+  int n_used = 0;
+  for (const Tensor* t : all)
+    if (!t->empty()) used[n_used++] = t;
+  const int v = qk_vector(used, n_used, a);
+  vattn::QkParams p{};
+  const vattn_rows* in[2] = {q, k};
+  const vattn_rows* out[2] = {q_out, k_out};
+  const void* w[2] = {a->q_weight, a->k_weight};
+  for (int i = 0; i < 2; ++i) {
+    vattn::QkTensor& t = p.t[i];
+    t.heads = static_cast<int>(i == 0 ? a->n_q_heads : a->n_kv_heads);
+    if (t.heads == 0) continue;
+    t.x = in[i]->data;
+    t.y = out[i]->data;
+    t.w = w[i];
+    qk_strides(t.xs, in[i]);
+    qk_strides(t.ys, out[i]);
+  }
+  int64_t bx = 0;
+  qk_plan(&p, a, v, sms, &bx);
+  if (bx > INT32_MAX) return fail(VATTN_ERR_UNSUPPORTED, "too many tokens");
+  const dim3 grid(static_cast<unsigned>(bx), static_cast<unsigned>(p.t[0].slices + p.t[1].slices));
+  return qk_dispatch<false>(p, a->dtype, v, grid, static_cast<cudaStream_t>(stream_ptr));
+}
+
+vattn_status vattn_qk_norm_rope_backward(const vattn_rows* dq_out, const vattn_rows* dk_out,
+                                         const vattn_rows* q, const vattn_rows* k,
+                                         const vattn_rows* dq, const vattn_rows* dk,
+                                         float* dq_weight, float* dk_weight, const vattn_qk_args* a,
+                                         void* stream_ptr) {
+  clear_error();
+  vattn_status st = check_qk(a);
+  if (st != VATTN_OK) return st;
+  const Tensor gq = qk_tensor("dq_out", dq_out, a, true, false), gk = qk_tensor("dk_out", dk_out, a, false, false),
+               tq = qk_tensor("q", q, a, true, false), tk = qk_tensor("k", k, a, false, false),
+               oq = qk_tensor("dq", dq, a, true, true), ok = qk_tensor("dk", dk, a, false, true);
+  const Tensor* all[6] = {&gq, &gk, &tq, &tk, &oq, &ok};
+  for (const Tensor* t : all)
+    if ((st = check_tensor(*t, elem_size(a->dtype))) != VATTN_OK) return st;
+  for (const Tensor* t : {&gq, &tq})
+    if (!oq.empty() && !same_rows(oq, *t) && (st = check_apart(oq, *t)) != VATTN_OK) return st;
+  for (const Tensor* t : {&gk, &tk})
+    if (!ok.empty() && !same_rows(ok, *t) && (st = check_apart(ok, *t)) != VATTN_OK) return st;
+  for (const Tensor* t : {&gk, &tk})
+    if ((st = check_apart(oq, *t)) != VATTN_OK) return st;
+  for (const Tensor* t : {&gq, &tq, &oq})
+    if ((st = check_apart(ok, *t)) != VATTN_OK) return st;
+  if ((reinterpret_cast<uintptr_t>(dq_weight) | reinterpret_cast<uintptr_t>(dk_weight)) & 3u)
+    return fail(VATTN_ERR_MISALIGNED, "dq_weight and dk_weight must be 4-byte aligned");
+  float* dw[2] = {a->q_weight ? dq_weight : nullptr, a->k_weight ? dk_weight : nullptr};
+  const uint64_t w_bytes = static_cast<uint64_t>(a->head_dim) * 4u;
+  for (int i = 0; i < 2; ++i)
+    for (const Tensor* t : all)
+      if ((st = check_apart_bytes(dw[i], w_bytes, i == 0 ? "dq_weight" : "dk_weight", *t)) != VATTN_OK) return st;
+  if (dw[0] && dw[1] &&
+      reinterpret_cast<uintptr_t>(dw[0]) < reinterpret_cast<uintptr_t>(dw[1]) + w_bytes &&
+      reinterpret_cast<uintptr_t>(dw[1]) < reinterpret_cast<uintptr_t>(dw[0]) + w_bytes)
+    return fail(VATTN_ERR_INVALID_ARG, "dq_weight overlaps dk_weight");
+
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  if (tq.empty() && tk.empty()) {  // sums over no rows
+    for (float* d : dw)
+      if (d) {
+        const cudaError_t e = cudaMemsetAsync(d, 0, w_bytes, stream);
+        if (e != cudaSuccess) return cuda_fail(e, "clearing a weight gradient");
+      }
+    return VATTN_OK;
+  }
+  int device = 0, sms = 0;
+  if ((st = current_device(&device)) != VATTN_OK) return st;
+  if ((st = vattn::host::sm_count(device, &sms)) != VATTN_OK) return st;
+  const Tensor* used[6];
+  int n_used = 0;
+  for (const Tensor* t : all)
+    if (!t->empty()) used[n_used++] = t;
+  const int v = qk_vector(used, n_used, a);
+  vattn::QkParams p{};
+  const vattn_rows* in[2] = {q, k};
+  const vattn_rows* grad[2] = {dq_out, dk_out};
+  const vattn_rows* out[2] = {dq, dk};
+  const void* w[2] = {a->q_weight, a->k_weight};
+  for (int i = 0; i < 2; ++i) {
+    vattn::QkTensor& t = p.t[i];
+    t.heads = static_cast<int>(i == 0 ? a->n_q_heads : a->n_kv_heads);
+    if (t.heads == 0) continue;
+    t.x = in[i]->data;
+    t.g = grad[i]->data;
+    t.y = out[i]->data;
+    t.w = w[i];
+    qk_strides(t.xs, in[i]);
+    qk_strides(t.gs, grad[i]);
+    qk_strides(t.ys, out[i]);
+  }
+  int64_t bx = 0;
+  qk_plan(&p, a, v, sms, &bx);
+  const int slices = p.t[0].slices + p.t[1].slices;
+  // at most eight blocks per multiprocessor: they walk over the tokens, and
+  // each leaves one row of weight gradient
+  const int64_t most = std::max<int64_t>(1, 8LL * sms / slices);
+  bx = std::min(bx, most);
+  const dim3 grid(static_cast<unsigned>(bx), static_cast<unsigned>(slices));
+  Workspace ws;
+  if (dw[0] || dw[1]) {
+    if ((st = ws.take(static_cast<size_t>(bx) * slices * p.D * 4, device, stream)) != VATTN_OK) return st;
+    p.part = reinterpret_cast<float*>(ws.data());
+  }
+  if ((st = qk_dispatch<true>(p, a->dtype, v, grid, stream)) != VATTN_OK) return st;
+  if (!p.part) return VATTN_OK;
+  vattn::QkWeightSum s{};
+  s.part = p.part;
+  s.D = p.D;
+  for (int i = 0; i < 2; ++i) s.dw[i] = dw[i];
+  s.row1[0] = s.row0[1] = bx * p.t[0].slices;
+  s.row1[1] = bx * slices;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((p.D + 31) / 32), 2);
+  cfg.blockDim = dim3(32, 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, vattn::vattn_qk_weight_sum_kernel, s);
+  if (e != cudaSuccess) return cuda_fail(e, "weight gradient kernel launch");
+  return ws.release();
+}
+
+vattn_status vattn_forward_window(const vattn_rows* q, const vattn_rows* k, const vattn_rows* v,
+                                  const vattn_rows* out, float* lse, const vattn_window_args* a,
+                                  void* stream_ptr) {
+  clear_error();
+  vattn_status st = check_window_args(a);
+  if (st != VATTN_OK) return st;
+  if (a->tree) return fail(VATTN_ERR_INVALID_ARG, "tree is for vattn_forward_cached");
+  if ((st = forward_checks(q, k, v, out, lse, a)) != VATTN_OK) return st;
+  if (a->batch * a->n_q_heads == 0 || a->n_queries == 0) return VATTN_OK;
+  return forward_rows(q, k, v, out, lse, a, static_cast<cudaStream_t>(stream_ptr));
+}
+
+vattn_status vattn_backward_window(const vattn_rows* dout, const vattn_rows* q, const vattn_rows* k,
+                                   const vattn_rows* v, const vattn_rows* out, const float* lse,
+                                   const vattn_rows* dq, const vattn_rows* dk, const vattn_rows* dv,
+                                   const vattn_window_args* a, void* stream_ptr) {
+  clear_error();
+  vattn_status st = check_window_args(a);
+  if (st != VATTN_OK) return st;
+  if (a->tree) return fail(VATTN_ERR_INVALID_ARG, "tree is for vattn_forward_cached");
+  const Tensor tg = window_tensor("dout", dout, a, true, false), tq = window_tensor("q", q, a, true, false),
+               tk = window_tensor("k", k, a, false, false), tv = window_tensor("v", v, a, false, false),
+               to = window_tensor("out", out, a, true, false), oq = window_tensor("dq", dq, a, true, true),
+               ok = window_tensor("dk", dk, a, false, true), ov = window_tensor("dv", dv, a, false, true);
+  const Tensor* ins[5] = {&tg, &tq, &tk, &tv, &to};
+  const Tensor* outs[3] = {&oq, &ok, &ov};
+  for (const Tensor* t : ins)
+    if ((st = check_tensor(*t, 16)) != VATTN_OK) return st;
+  for (const Tensor* t : outs)
+    if ((st = check_tensor(*t, 16)) != VATTN_OK) return st;
+  for (const Tensor* t : outs)
+    for (const Tensor* u : ins)
+      if ((st = check_apart(*t, *u)) != VATTN_OK) return st;
+  for (int i = 0; i < 3; ++i)
+    for (int j = 0; j < i; ++j)
+      if ((st = check_apart(*outs[i], *outs[j])) != VATTN_OK) return st;
+  if (!tq.empty() && !lse) return fail(VATTN_ERR_INVALID_ARG, "null lse");
+  if (reinterpret_cast<uintptr_t>(lse) & 3u) return fail(VATTN_ERR_MISALIGNED, "lse must be 4-byte aligned");
+  const uint64_t bytes = static_cast<uint64_t>(a->batch) * a->n_q_heads * a->n_queries * 4u;
+  for (const Tensor* t : outs)
+    if ((st = check_apart_bytes(lse, bytes, "lse", *t)) != VATTN_OK) return st;
+  if (tq.empty() && tk.empty()) return VATTN_OK;
+  vattn::RowsParams p{};
+  p.w = window_params(a);
+  p.q = rows_tensor(q);
+  p.k = rows_tensor(k);
+  p.v = rows_tensor(v);
+  p.out = rows_tensor(out);
+  p.dout = rows_tensor(dout);
+  p.dq = rows_tensor(dq);
+  p.dk = rows_tensor(dk);
+  p.dv = rows_tensor(dv);
+  p.lse = const_cast<float*>(lse);
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  const unsigned gq = rows_grid(a->batch * a->n_q_heads * a->n_queries),
+                 gk = rows_grid(a->batch * a->n_kv_heads * a->n_keys), threads = vattn::kRowsWarps * 32;
+  const bool f16 = a->dtype == VATTN_F16;
+  if (gk > 0) {
+    if (f16) vattn::vattn_window_rows_dkv_kernel<__half><<<gk, threads, 0, stream>>>(p);
+    else vattn::vattn_window_rows_dkv_kernel<__nv_bfloat16><<<gk, threads, 0, stream>>>(p);
+    if ((st = launched("key gradient kernel launch")) != VATTN_OK) return st;
+  }
+  if (gq > 0) {
+    if (f16) vattn::vattn_window_rows_dq_kernel<__half><<<gq, threads, 0, stream>>>(p);
+    else vattn::vattn_window_rows_dq_kernel<__nv_bfloat16><<<gq, threads, 0, stream>>>(p);
+    if ((st = launched("query gradient kernel launch")) != VATTN_OK) return st;
+  }
+  return VATTN_OK;
+}
+
+vattn_status vattn_forward_cached(const vattn_rows* q, const vattn_rows* k, const vattn_rows* v,
+                                  const vattn_rows* out, const vattn_window_args* a, void* stream_ptr) {
+  clear_error();
+  vattn_status st = check_window_args(a);
+  if (st != VATTN_OK) return st;
+  if (a->q_start) return fail(VATTN_ERR_INVALID_ARG, "q_start must be null: new tokens end the sequence");
+  if (a->n_queries > VATTN_MAX_NEW_TOKENS)
+    return fail(VATTN_ERR_UNSUPPORTED, "%lld new tokens > %d: use vattn_forward_window", (long long)a->n_queries,
+                VATTN_MAX_NEW_TOKENS);
+  if (a->batch > 0 && !a->kv_len) return fail(VATTN_ERR_INVALID_ARG, "null kv_len");
+  if ((st = forward_checks(q, k, v, out, nullptr, a)) != VATTN_OK) return st;
+  if (a->batch * a->n_q_heads == 0 || a->n_queries == 0) return VATTN_OK;
+  return forward_rows(q, k, v, out, nullptr, a, static_cast<cudaStream_t>(stream_ptr));
+}
+
+}  // extern "C"

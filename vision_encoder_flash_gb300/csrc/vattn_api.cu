@@ -20,6 +20,7 @@
 #include "../../include/vattn.h"
 #include "attn_kernel.cuh"
 #include "conv1d_kernel.cuh"
+#include "host_common.h"
 #include "rope_kernel.cuh"
 #include "stage_kernel.cuh"
 
@@ -1616,3 +1617,73 @@ extern "C" vattn_status vattn_forward_noalloc(const float* q, const float* k, co
                      reinterpret_cast<float*>(wp + pl.sync_bytes), ws,
                      static_cast<cudaStream_t>(stream_ptr), device);
 }
+
+// ---- what decoder_api.cu shares (host_common.h)
+namespace {
+std::atomic<uint32_t*> g_status_addr[kMaxDevices];
+}
+
+namespace vattn {
+namespace host {
+
+static_assert(kMaxDevices == ::kMaxDevices, "one device limit");
+
+void clear_error() { g_last_error[0] = '\0'; }
+
+vattn_status fail(vattn_status st, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
+  va_end(ap);
+  return st;
+}
+
+vattn_status cuda_fail(cudaError_t e, const char* what) { return ::cuda_fail(e, what); }
+
+vattn_status sm_count(int device, int* out) { return ::sm_count(device, out); }
+
+vattn_status status_word(int device, uint32_t** out) {
+  if (device < 0 || device >= kMaxDevices)
+    return fail(VATTN_ERR_CUDA, "device index %d out of range", device);
+  uint32_t* addr = g_status_addr[device].load(std::memory_order_acquire);
+  if (!addr) {
+    void* a = nullptr;
+    const cudaError_t e = cudaGetSymbolAddress(&a, vattn::g_vattn_status);
+    if (e != cudaSuccess) return ::cuda_fail(e, "cudaGetSymbolAddress of the status word");
+    addr = static_cast<uint32_t*>(a);
+    g_status_addr[device].store(addr, std::memory_order_release);
+  }
+  *out = addr;
+  return VATTN_OK;
+}
+
+vattn_status tensor_map_encoder(EncodeTiledFn* out) {
+  *out = encode_fn();
+  if (*out) return VATTN_OK;
+  if (g_encode_err != cudaSuccess) return ::cuda_fail(g_encode_err, "cuTensorMapEncodeTiled lookup");
+  return fail(VATTN_ERR_CUDA, "cuTensorMapEncodeTiled not available from the driver");
+}
+
+vattn_status Workspace::take(size_t bytes, int device, cudaStream_t stream) {
+  cudaMemPool_t pool = nullptr;
+  const vattn_status st = pool_for(device, &pool);
+  if (st != VATTN_OK) return st;
+  const cudaError_t e = cudaMallocFromPoolAsync(&ptr_, bytes, pool, stream);
+  if (e != cudaSuccess) {
+    ptr_ = nullptr;
+    (void)cudaGetLastError();
+    return ::cuda_fail(e, "workspace allocation");
+  }
+  stream_ = stream;
+  return VATTN_OK;
+}
+
+vattn_status Workspace::release() {
+  if (!ptr_) return VATTN_OK;
+  const cudaError_t e = cudaFreeAsync(ptr_, stream_);
+  ptr_ = nullptr;
+  return e == cudaSuccess ? VATTN_OK : ::cuda_fail(e, "workspace release");
+}
+
+}  // namespace host
+}  // namespace vattn
