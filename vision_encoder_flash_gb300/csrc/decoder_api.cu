@@ -4,12 +4,14 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
 #include "../../include/vattn_decoder.h"
 #include "host_common.h"
 #include "qk_norm_rope_kernel.cuh"
+#include "window_fwd_kernel.cuh"
 #include "window_rows_kernel.cuh"
 
 namespace {
@@ -365,6 +367,93 @@ vattn_status forward_rows(const vattn_rows* q, const vattn_rows* k, const vattn_
   return launched("attention kernel launch");
 }
 
+// Tensor map {dim, rows, heads, batch} of 16-bit rows with boxes of 64
+// columns x `box_rows` rows, 128-byte swizzle; what is outside reads 0.  A
+// head or batch dimension of stride 0 (or size 1) becomes a single one, and
+// *mul zeroes its coordinate.
+vattn_status make_rows_map(CUtensorMap* tm, vattn::MapMul* mul, const Tensor& x, int32_t dtype, int box_rows) {
+  vattn::host::EncodeTiledFn enc = nullptr;
+  const vattn_status st = vattn::host::tensor_map_encoder(&enc);
+  if (st != VATTN_OK) return st;
+  const bool one_h = x.size[1] <= 1 || x.t->stride[1] == 0, one_b = x.size[0] <= 1 || x.t->stride[0] == 0;
+  mul->h = one_h ? 0 : 1;
+  mul->b = one_b ? 0 : 1;
+  const cuuint64_t row = static_cast<cuuint64_t>(x.dim) * 2u;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(x.dim), static_cast<cuuint64_t>(x.size[2]),
+                              static_cast<cuuint64_t>(one_h ? 1 : x.size[1]),
+                              static_cast<cuuint64_t>(one_b ? 1 : x.size[0])};
+  const cuuint64_t strides[3] = {x.size[2] <= 1 ? row : static_cast<cuuint64_t>(x.t->stride[2]) * 2u,
+                                 one_h ? row : static_cast<cuuint64_t>(x.t->stride[1]) * 2u,
+                                 one_b ? row : static_cast<cuuint64_t>(x.t->stride[0]) * 2u};
+  const cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(box_rows), 1u, 1u};
+  const cuuint32_t steps[4] = {1u, 1u, 1u, 1u};
+  const CUresult r = enc(tm, dtype == VATTN_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                         4, x.t->data, dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(VATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed with CUresult %d", static_cast<int>(r));
+  return VATTN_OK;
+}
+
+// Opts a kernel in to its dynamic shared memory, once per device.
+template <typename K>
+vattn_status allow_smem(K kernel, int bytes, std::atomic<uint8_t>* done, int device) {
+  if (done[device].load(std::memory_order_acquire)) return VATTN_OK;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+  done[device].store(1, std::memory_order_release);
+  return VATTN_OK;
+}
+
+template <typename T, int NKB>
+vattn_status window_fwd_launch(const CUtensorMap (&tm)[3], const vattn::WindowFwdParams& p, int sms, int device,
+                               cudaStream_t stream) {
+  using P = vattn::WindowFwdPlan<NKB>;
+  auto kernel = vattn::vattn_window_fwd_kernel<T, NKB>;
+  static std::atomic<uint8_t> done[vattn::host::kMaxDevices];
+  const vattn_status st = allow_smem(kernel, P::kSmemBytes, done, device);
+  if (st != VATTN_OK) return st;
+  const unsigned grid = static_cast<unsigned>(std::min<long long>(p.items, sms));
+  kernel<<<grid, P::kThreads, P::kSmemBytes, stream>>>(tm[0], tm[1], tm[2], p);
+  return launched("window attention kernel launch");
+}
+
+// The tensor-core forward pass (checks passed, at least one query row).
+vattn_status forward_window(const vattn_rows* q, const vattn_rows* k, const vattn_rows* v, const vattn_rows* out,
+                            float* lse, const vattn_window_args* a, cudaStream_t stream) {
+  int device = 0, sms = 0;
+  vattn_status st;
+  if ((st = current_device(&device)) != VATTN_OK) return st;
+  if ((st = vattn::host::sm_count(device, &sms)) != VATTN_OK) return st;
+  vattn::WindowFwdParams p{};
+  p.w = window_params(a);
+  p.q = rows_tensor(q);
+  p.k = rows_tensor(k);
+  p.v = rows_tensor(v);
+  p.out = rows_tensor(out);
+  p.lse = lse;
+  if ((st = vattn::host::status_word(device, &p.status)) != VATTN_OK) return st;
+  p.row_blocks = static_cast<int>((a->n_queries + vattn::kTile - 1) / vattn::kTile);
+  p.pairs = (static_cast<long long>(p.row_blocks) * p.w.group + 1) / 2;
+  p.items = p.pairs * p.w.batch * p.w.kv_heads;
+  p.scale_log2 = a->scale * vattn::kLog2E;
+  CUtensorMap tm[3];
+  if ((st = make_rows_map(&tm[0], &p.mq, window_tensor("q", q, a, true, false), a->dtype, vattn::kTile)) != VATTN_OK)
+    return st;
+  if (a->n_keys == 0) {  // no key tile is ever loaded: any valid map does
+    tm[1] = tm[2] = tm[0];
+  } else if ((st = make_rows_map(&tm[1], &p.mk, window_tensor("k", k, a, false, false), a->dtype, vattn::kTile)) != VATTN_OK ||
+             (st = make_rows_map(&tm[2], &p.mv, window_tensor("v", v, a, false, false), a->dtype, vattn::kTile)) != VATTN_OK) {
+    return st;
+  }
+  if (a->dtype == VATTN_F16)
+    return a->head_dim <= 64 ? window_fwd_launch<__half, 1>(tm, p, sms, device, stream)
+                             : window_fwd_launch<__half, 2>(tm, p, sms, device, stream);
+  return a->head_dim <= 64 ? window_fwd_launch<__nv_bfloat16, 1>(tm, p, sms, device, stream)
+                           : window_fwd_launch<__nv_bfloat16, 2>(tm, p, sms, device, stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -527,7 +616,7 @@ vattn_status vattn_forward_window(const vattn_rows* q, const vattn_rows* k, cons
   if (a->tree) return fail(VATTN_ERR_INVALID_ARG, "tree is for vattn_forward_cached");
   if ((st = forward_checks(q, k, v, out, lse, a)) != VATTN_OK) return st;
   if (a->batch * a->n_q_heads == 0 || a->n_queries == 0) return VATTN_OK;
-  return forward_rows(q, k, v, out, lse, a, static_cast<cudaStream_t>(stream_ptr));
+  return forward_window(q, k, v, out, lse, a, static_cast<cudaStream_t>(stream_ptr));
 }
 
 vattn_status vattn_backward_window(const vattn_rows* dout, const vattn_rows* q, const vattn_rows* k,

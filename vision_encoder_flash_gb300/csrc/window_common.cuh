@@ -39,4 +39,30 @@ __device__ __forceinline__ bool window_sees(const WindowParams& p, const Seq& s,
   return j <= pos && pos < s.len && (j > pos - p.window || j < p.sinks);
 }
 
+// A tensor [batch, heads, rows, dim] with its first three strides.
+struct RowsTensor {
+  const void* p;
+  long long s[3];
+};
+
+template <typename T>
+__device__ __forceinline__ const T* rows_at(const RowsTensor& t, long long b, long long h, long long i) {
+  return static_cast<const T*>(t.p) + b * t.s[0] + h * t.s[1] + i * t.s[2];
+}
+template <typename T>
+__device__ __forceinline__ T* rows_at_mut(const RowsTensor& t, long long b, long long h, long long i) {
+  return const_cast<T*>(rows_at<T>(t, b, h, i));
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
 }  // namespace vattn

@@ -1,0 +1,486 @@
+// window_fwd_kernel.cuh -- causal attention under a sliding window with
+// visible first keys (vattn_forward_window), on the tensor cores.
+//
+// A unit is 128 query rows of one head.  Its row at position p sees keys j
+// <= p with j > p - window or j < sinks, so it reads the key tiles of the
+// first keys and those from its first row's window to its last row; no other
+// tile is loaded.  A work item is two units of one key head, consecutive in
+// (row block, head of the group): with an even group both have the same
+// rows, hence the same tiles, and each K and V tile that comes from L2
+// serves 256 query rows.  The grid is one block per multiprocessor, each
+// walking over items from the longest to the shortest (late rows first).
+//
+//   warp 0   K and V tiles by TMA into a ring (K0 V0 K1 V1 ...)
+//   warp 2   the item's two Q tiles by TMA
+//   warp 1   issues S_t = Q_t K^T and O_t += P_t V (tcgen05.mma, TMEM
+//            accumulators): P0 V, next S0, P1 V, next S1, so that one unit's
+//            softmax runs while the tensor core works for the other
+//   warps 4-7, 8-11   online softmax of unit 0, 1: thread = query row
+//
+// TMEM (512 columns): S_t at 128 t, O_t at 256 + 128 t.  P_t (16-bit)
+// overwrites S_t once it is in registers; one thread issues all MMAs, which
+// run in order, so S_t of the next tile follows the P_t V that reads P_t.
+//
+// Statistics and accumulators are f32.  The weights are rounded to the
+// tensors' type for the second product (relative 2^-9 / 2^-12 at most, the
+// sum l takes them unrounded), as the product needs; O is rescaled in TMEM
+// only when a row's maximum grew by more than 2^8 (exact after the final
+// 1 / l).  A masked score is -infinity by selection, so nothing that K holds
+// there gets through; V rows behind the sequence are zeroed in shared memory
+// before the product, and a row whose result is not finite although its
+// weights are is computed again by its warp over the keys it sees, since 0 x
+// infinity from a masked V row of the same tile would otherwise stay in it.
+#pragma once
+
+#include "window_pipe.cuh"
+
+namespace vattn {
+
+struct WindowFwdParams {
+  WindowParams w;
+  RowsTensor q, k, v, out;
+  float* lse;
+  uint32_t* status;
+  MapMul mq, mk, mv;
+  int row_blocks;      // ceil(n_queries / 128)
+  long long pairs;     // items of one (batch, key head)
+  long long items;
+  float scale_log2;    // scale * log2(e)
+};
+
+// Key tiles [0, ns) and [a, b] of one unit (b < a: none).
+struct UnitRange {
+  int ns, a, b;
+  __device__ __forceinline__ bool empty() const { return b < a; }
+  __device__ __forceinline__ bool uses(int j) const { return j < ns || (j >= a && j <= b); }
+};
+
+__device__ __forceinline__ UnitRange unit_range(const WindowParams& w, const Seq& s, int row0) {
+  UnitRange u{0, 0, -1};
+  const int lo = max(0, s.start + row0);
+  const int hi = min(s.start + min(row0 + kTile, w.n_queries), s.len) - 1;
+  if (hi < lo) return u;
+  u.a = max(0, lo - w.window + 1) / kTile;
+  u.b = hi / kTile;
+  u.ns = min((min(w.sinks, s.len) + kTile - 1) / kTile, u.a);
+  return u;
+}
+
+// One item: its two units and the tiles that either uses, in order.
+struct WindowItem {
+  int b, kh;
+  int head[2], row0[2];
+  bool on[2];
+  UnitRange u[2];
+  Seq s;
+  int first_n, second, n;  // tiles 0 .. first_n - 1, then second, second + 1, ...
+  __device__ __forceinline__ int tile(int x) const { return x < first_n ? x : second + (x - first_n); }
+};
+
+__device__ __forceinline__ WindowItem window_item(const WindowFwdParams& p, long long item) {
+  WindowItem it;
+  const long long seqs = static_cast<long long>(p.w.batch) * p.w.kv_heads;
+  const long long pair = p.pairs - 1 - item / seqs;
+  const long long bk = item % seqs;
+  it.b = static_cast<int>(bk / p.w.kv_heads);
+  it.kh = static_cast<int>(bk - static_cast<long long>(it.b) * p.w.kv_heads);
+  it.s = window_seq(p.w, it.b);
+  const long long units = static_cast<long long>(p.row_blocks) * p.w.group;
+  int last = -1, first = 0x7fffffff;
+  it.first_n = 0;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const long long unit = 2 * pair + t;
+    it.on[t] = unit < units;
+    const int r = static_cast<int>(unit / p.w.group);
+    it.row0[t] = r * kTile;
+    it.head[t] = it.kh * p.w.group + static_cast<int>(unit - static_cast<long long>(r) * p.w.group);
+    it.u[t] = it.on[t] ? unit_range(p.w, it.s, it.row0[t]) : UnitRange{0, 0, -1};
+    if (!it.u[t].empty()) {
+      it.first_n = max(it.first_n, it.u[t].ns);
+      first = min(first, it.u[t].a);
+      last = max(last, it.u[t].b);
+    }
+  }
+  it.second = max(first, it.first_n);
+  it.n = last < 0 ? 0 : it.first_n + max(0, last - it.second + 1);
+  return it;
+}
+
+template <int NKB>
+struct WindowFwdPlan {
+  static constexpr int kTileBytes = NKB * kBlockBytes;
+  static constexpr int kStages = NKB == 1 ? 8 : 4;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffKv = 2 * kTileBytes;
+  static constexpr int kOffBar = kOffKv + kStages * kTileBytes;
+  static constexpr int kSmemBytes = kOffBar + 256 + 1024;  // + alignment slack
+  static constexpr int kThreads = 384;
+  // registers: 72 + 2 x 216 a thread = 3 x 168, what the launch has
+  static constexpr uint32_t kRegsOther = 72, kRegsSoftmax = 216;
+  static_assert(kSmemBytes <= 232448, "shared memory");
+};
+
+enum WindowBar : int {
+  kWbQFull = 0, kWbQEmpty = 1, kWbKvFull = 2, kWbKvEmpty = 10, kWbSFull = 18, kWbPFull = 20,
+  kWbOFull = 22, kWbMmaDone = 24, kWbCount = 25,
+};
+
+// Row `row` of the call once more, over the keys that it sees alone (one
+// warp): the weights are exp2(score - m) / l of the tiles' pass.
+template <typename T>
+__device__ __noinline__ void window_row_again(const WindowFwdParams& p, const Seq& s, int b, int h,
+                                              int row, float m, float l) {
+  const int lane = threadIdx.x & 31, D = p.w.dim, pos = s.start + row;
+  const int kh = h / p.w.group;
+  const T* q = rows_at<T>(p.q, b, h, row);
+  float x[4], o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int c = 0; c < 4; ++c) x[c] = lane + 32 * c < D ? Elem<T>::widen(q[lane + 32 * c]) : 0.0f;
+  const int first = max(0, pos - p.w.window + 1), sinks = min(p.w.sinks, first);
+  for (int i = 0; i < sinks + (pos - first + 1); ++i) {
+    const int j = i < sinks ? i : first + (i - sinks);
+    const T* k = rows_at<T>(p.k, b, kh, j);
+    const T* v = rows_at<T>(p.v, b, kh, j);
+    float dot = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (lane + 32 * c < D) dot = fmaf(x[c], Elem<T>::widen(k[lane + 32 * c]), dot);
+#pragma unroll
+    for (int o2 = 16; o2 > 0; o2 >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o2);
+    const float e = ptx::ex2_approx(fmaf(dot, p.scale_log2, -m));
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (lane + 32 * c < D) o[c] = fmaf(e, Elem<T>::widen(v[lane + 32 * c]), o[c]);
+  }
+  T* out = rows_at_mut<T>(p.out, b, h, row);
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    if (lane + 32 * c < D) out[lane + 32 * c] = Elem<T>::narrow(o[c] / l);
+}
+
+template <typename T, int NKB>
+__global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
+    vattn_window_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
+                            const __grid_constant__ CUtensorMap tm_k,
+                            const __grid_constant__ CUtensorMap tm_v,
+                            const __grid_constant__ WindowFwdParams p) {
+  using P = WindowFwdPlan<NKB>;
+  constexpr int S = P::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_s = ptx::smem_addr(smem_raw);
+  const uint32_t base_s = (raw_s + 1023u) & ~1023u;
+  uint8_t* const base = smem_raw + (base_s - raw_s);
+  const uint32_t bar0 = base_s + P::kOffBar;
+  auto bar = [bar0](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(base + P::kOffBar + 8 * kWbCount);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  const Pipe pipe{abort_flag, p.status};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    ptx::mbar_init(bar(kWbQFull), 1);
+    ptx::mbar_init(bar(kWbQEmpty), 1);
+    for (int i = 0; i < S; ++i) {
+      ptx::mbar_init(bar(kWbKvFull + i), 1);
+      ptx::mbar_init(bar(kWbKvEmpty + i), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      ptx::mbar_init(bar(kWbSFull + t), 1);
+      ptx::mbar_init(bar(kWbPFull + t), 4);
+      ptx::mbar_init(bar(kWbOFull + t), 1);
+    }
+    ptx::mbar_init(bar(kWbMmaDone), 1);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tensormap(&tm_q);
+    ptx::prefetch_tensormap(&tm_k);
+    ptx::prefetch_tensormap(&tm_v);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_addr(const_cast<uint32_t*>(tmem_slot)), 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  ptx::grid_dep_wait();  // what earlier kernels of the stream wrote is visible
+
+  if (warp < 4) {
+    ptx::regs_decrease<P::kRegsOther>();
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------- K and V tiles
+      const uint64_t keep = ptx::policy_evict_last();  // read again by other heads and rows
+      long long c = 0;  // ring entries so far
+      bool ok = true;
+      for (long long item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+        const WindowItem it = window_item(p, item);
+        for (int x = 0; ok && x < it.n; ++x) {
+          const int row = it.tile(x) * kTile;
+          for (int kv = 0; kv < 2; ++kv, ++c) {
+            const int st = static_cast<int>(c % S);
+            if (!(ok = pipe.wait(bar(kWbKvEmpty + st), static_cast<uint32_t>((c / S) & 1) ^ 1u, kSiteWinKv))) break;
+            ptx::mbar_arrive_expect_tx(bar(kWbKvFull + st), P::kTileBytes);
+            const MapMul m = kv ? p.mv : p.mk;
+            for (int kb = 0; kb < NKB; ++kb)
+              ptx::tma_load_4d_hint(base_s + P::kOffKv + st * P::kTileBytes + kb * kBlockBytes,
+                                    kv ? &tm_v : &tm_k, bar(kWbKvFull + st), kb * 64, row,
+                                    it.kh * m.h, it.b * m.b, keep);
+          }
+        }
+      }
+      for (long long d = c > S ? c - S : 0; d < c; ++d)
+        pipe.drain(bar(kWbKvFull + static_cast<int>(d % S)), static_cast<uint32_t>((d / S) & 1), kSiteWinDrain);
+    } else if (warp == 2 && lane == 0) {
+      // ------------------------------------------------------- Q tiles
+      const uint64_t once = ptx::policy_evict_first();
+      uint32_t n_q = 0;
+      for (long long item = blockIdx.x; item < p.items; item += gridDim.x) {
+        const WindowItem it = window_item(p, item);
+        if (it.n == 0) continue;
+        if (n_q > 0 && !pipe.wait(bar(kWbQEmpty), (n_q - 1) & 1u, kSiteWinQ)) break;
+        ptx::mbar_arrive_expect_tx(bar(kWbQFull), (it.on[1] ? 2 : 1) * P::kTileBytes);
+        for (int t = 0; t < (it.on[1] ? 2 : 1); ++t)
+          for (int kb = 0; kb < NKB; ++kb)
+            ptx::tma_load_4d_hint(base_s + P::kOffQ + t * P::kTileBytes + kb * kBlockBytes, &tm_q,
+                                  bar(kWbQFull), kb * 64, it.row0[t], it.head[t] * p.mq.h,
+                                  it.b * p.mq.b, once);
+        ++n_q;
+      }
+      if (n_q > 0) pipe.drain(bar(kWbQFull), (n_q - 1) & 1u, kSiteWinDrain);
+    } else if (warp == 1) {
+      // ------------------------------------------------------ MMA issue
+      // The whole warp walks and waits; lane 0 issues.
+      const int ksteps = (p.w.dim + 15) >> 4;
+      const uint32_t idesc_s = ptx::idesc_16bit_f32(kTile, kTile, false, Elem<T>::kBf16);
+      const uint32_t idesc_o = ptx::idesc_16bit_f32(kTile, static_cast<uint32_t>(ksteps) * 16u, true, Elem<T>::kBf16);
+      constexpr uint32_t hi = ptx::smem_desc_hi(1024, ptx::kSwizzle128B);
+      auto stage = [&](long long c) -> uint32_t {
+        return base_s + P::kOffKv + static_cast<uint32_t>(c % S) * P::kTileBytes;
+      };
+      auto wait_kv = [&](long long c) -> bool {
+        return pipe.wait_warp(bar(kWbKvFull + static_cast<int>(c % S)), static_cast<uint32_t>((c / S) & 1), kSiteWinMma);
+      };
+      auto issue_s = [&](int t, long long c) {
+        if (lane == 0) {
+          const uint32_t q = ptx::smem_desc_lo(base_s + P::kOffQ + t * P::kTileBytes, 16);
+          const uint32_t k = ptx::smem_desc_lo(stage(c), 16);
+          for (int ks = 0; ks < ksteps; ++ks) {
+            const uint32_t off = static_cast<uint32_t>((ks >> 2) * kBlockBytes + (ks & 3) * 32) >> 4;
+            ptx::mma_ss(tmem + t * 128u, ptx::smem_desc_join(q + off, hi), ptx::smem_desc_join(k + off, hi),
+                        idesc_s, ks > 0);
+          }
+          ptx::mma_commit(bar(kWbSFull + t));
+        }
+      };
+      auto issue_o = [&](int t, long long c, bool first) {
+        if (lane == 0) {
+          const uint32_t v = ptx::smem_desc_lo(stage(c), kBlockBytes);
+          for (int ks = 0; ks < kTile / 16; ++ks)
+            ptx::mma_ts(tmem + 256u + t * 128u, tmem + t * 128u + ks * 8u,
+                        ptx::smem_desc_join(v + ks * (2048u >> 4), hi), idesc_o, !first || ks > 0);
+        }
+      };
+      auto commit = [&](int b) {
+        if (lane == 0) ptx::mma_commit(bar(b));
+      };
+      long long g = 0;  // key tiles of this block so far; K of tile g is ring entry 2 g, V 2 g + 1
+      uint32_t n_q = 0, n_p[2] = {0, 0};
+      bool ok = true;
+      for (long long item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+        const WindowItem it = window_item(p, item);
+        if (it.n == 0) continue;
+        if (!(ok = pipe.wait_warp(bar(kWbQFull), n_q & 1u, kSiteWinMma))) break;
+        ++n_q;
+        if (!(ok = wait_kv(2 * g))) break;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (it.u[t].uses(it.tile(0))) issue_s(t, 2 * g);
+        commit(kWbKvEmpty + static_cast<int>((2 * g) % S));
+        if (it.n == 1) commit(kWbQEmpty);
+        bool begun[2] = {false, false};
+        for (int x = 0; ok && x < it.n; ++x, ++g) {
+          const int j = it.tile(x), jn = x + 1 < it.n ? it.tile(x + 1) : -1;
+          if (!(ok = wait_kv(2 * g + 1))) break;
+          const int left = it.s.len - j * kTile;  // V rows of the sequence in this tile
+          if (left < kTile && it.s.len < p.w.n_keys) {
+            const uint32_t v = stage(2 * g + 1);
+            for (int kb = 0; kb < NKB; ++kb)
+              for (int i = left * 8 + lane; i < kTile * 8; i += 32)
+                ptx::st_shared_v4(v + kb * kBlockBytes + i * 16, 0.0f, 0.0f, 0.0f, 0.0f);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+          }
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (it.u[t].uses(j)) {
+              if (!(ok = pipe.wait_warp(bar(kWbPFull + t), n_p[t] & 1u, kSiteWinMma))) break;
+              ++n_p[t];
+              ptx::tc_fence_after();
+              issue_o(t, 2 * g + 1, !begun[t]);
+              begun[t] = true;
+              if (j == it.u[t].b) commit(kWbOFull + t);
+            }
+            if (jn >= 0) {
+              if (t == 0 && !(ok = wait_kv(2 * g + 2))) break;
+              if (it.u[t].uses(jn)) issue_s(t, 2 * g + 2);
+            }
+          }
+          if (!ok) break;
+          commit(kWbKvEmpty + static_cast<int>((2 * g + 1) % S));
+          if (jn >= 0) commit(kWbKvEmpty + static_cast<int>((2 * g + 2) % S));
+          if (x + 2 == it.n) commit(kWbQEmpty);
+        }
+      }
+      commit(kWbMmaDone);
+    }
+  } else {
+    ptx::regs_increase<P::kRegsSoftmax>();
+    // ------------------------------------------------------------ softmax
+    const int t = (warp - 4) >> 2;
+    const int r = (warp & 3) * 32 + lane;  // row of the unit
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem + lanes + t * 128u, o_addr = s_addr + 256u;
+    const int D = p.w.dim, W = p.w.window;
+    uint32_t n_s = 0, n_o = 0;
+    bool ok = true;
+    for (long long item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+      const WindowItem it = window_item(p, item);
+      if (!it.on[t]) continue;
+      const UnitRange u = it.u[t];
+      const int p0 = it.s.start + it.row0[t], pos = p0 + r;
+      const bool row_on = pos >= 0 && pos < it.s.len;
+      float m = -INFINITY, l = 0.0f;  // m: running maximum in log2 units, may lag by < 8
+      bool begun = false;
+      for (int x = 0; x < it.n; ++x) {
+        const int j = it.tile(x);
+        if (!u.uses(j)) continue;
+        if (!(ok = pipe.wait_warp(bar(kWbSFull + t), n_s & 1u, kSiteWinSoft))) break;
+        ++n_s;
+        ptx::tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ptx::tmem_ld_32x32b_x32(s_addr + c * 32, s[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ptx::tmem_wait_ld_dep(s[c]);
+        const int k0 = j * kTile;
+        // every row of the unit sees every key of the tile?
+        const bool full = p0 >= k0 + kTile - 1 && p0 + kTile <= it.s.len &&
+                          (p0 + kTile - 1 - W < k0 || k0 + kTile <= p.w.sinks);
+        if (!full) {
+          const int c_hi = row_on ? pos - k0 : -1, c_lo = pos - W - k0, c_sink = p.w.sinks - 1 - k0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t see = bits_upto(c_hi, c) & (~bits_upto(c_lo, c) | bits_upto(c_sink, c));
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((see >> e) & 1u)) s[c][e] = 0xff800000u;
+          }
+        }
+        float mc[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float a = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            a = ptx::max3(a, __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+          mc[c] = a;
+        }
+        const float mt = ptx::max3(mc[0], mc[1], fmaxf(mc[2], mc[3])) * p.scale_log2;
+        const bool grew = mt > m + kLazyLog2;
+        const float alpha = grew ? ptx::ex2_approx(m - mt) : 1.0f;  // 0 for the row's first keys
+        if (grew) m = mt;
+        const float ref = m == -INFINITY ? 0.0f : -m;  // a row that saw nothing yet: all weights 0
+        const float2 scale = make_float2(p.scale_log2, p.scale_log2), shift = make_float2(ref, ref);
+        float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 y = __ffma2_rn(
+                make_float2(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1])), scale, shift);
+            const float2 w = make_float2(ptx::ex2_approx(y.x), ptx::ex2_approx(y.y));
+            acc[e & 3] = __fadd2_rn(acc[e & 3], w);
+            s[c][e] = pack2<T>(w.x, w.y);
+          }
+        const float2 s01 = __fadd2_rn(acc[0], acc[1]), s23 = __fadd2_rn(acc[2], acc[3]);
+        l = fmaf(l, alpha, (s01.x + s01.y) + (s23.x + s23.y));
+        // S of this tile follows the unit's previous P V in issue order, so O is stable
+        if (begun && __any_sync(0xffffffffu, grew)) {
+          for (int c = 0; c < D; c += 16) {
+            uint32_t y[16];
+            ptx::tmem_ld_32x32b_x16(o_addr + c, y);
+            ptx::tmem_wait_ld_dep16(y);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * alpha);
+            ptx::tmem_st_32x32b_x16(o_addr + c, y);
+          }
+        }
+        begun = true;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          ptx::tmem_st_32x32b_x16(s_addr + c * 16, *reinterpret_cast<uint32_t(*)[16]>(s[c]));
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        pipe_warp_arrive(bar(kWbPFull + t));
+      }
+      if (!ok) break;
+      // ------------------------------------------------- out = O / l, lse
+      const int row = it.row0[t] + r;
+      const bool store = row < p.w.n_queries;
+      T* out = store ? rows_at_mut<T>(p.out, it.b, it.head[t], row) : nullptr;
+      if (u.empty()) {
+        if (store)
+          for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4*>(out + d) = make_uint4(0, 0, 0, 0);
+      } else {
+        if (!(ok = pipe.wait_warp(bar(kWbOFull + t), n_o & 1u, kSiteWinOut))) break;
+        ++n_o;
+        ptx::tc_fence_after();
+        const float inv = 1.0f / l;
+        float check = 0.0f;  // NaN once an element is not finite
+        for (int c = 0; c < D; c += 16) {
+          uint32_t y[16];
+          ptx::tmem_ld_32x32b_x16(o_addr + c, y);
+          ptx::tmem_wait_ld_dep16(y);
+          uint32_t h[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float a = l == 0.0f ? 0.0f : __uint_as_float(y[2 * e]) * inv;
+            const float b = l == 0.0f ? 0.0f : __uint_as_float(y[2 * e + 1]) * inv;
+            check = fmaf(a, 0.0f, fmaf(b, 0.0f, check));
+            h[e] = pack2<T>(a, b);
+          }
+          if (store) {
+            *reinterpret_cast<uint4*>(out + c) = make_uint4(h[0], h[1], h[2], h[3]);
+            if (c + 8 < D) *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(h[4], h[5], h[6], h[7]);
+          }
+        }
+        // finite weights, but not the result: see window_row_again
+        uint32_t again = __ballot_sync(0xffffffffu, store && row_on && check != 0.0f && l - l == 0.0f);
+        __syncwarp();
+        for (; again != 0; again &= again - 1) {
+          const int src = __ffs(again) - 1;
+          window_row_again<T>(p, it.s, it.b, it.head[t], __shfl_sync(0xffffffffu, row, src),
+                              __shfl_sync(0xffffffffu, m, src), __shfl_sync(0xffffffffu, l, src));
+        }
+        ptx::tc_fence_before();
+      }
+      if (store && p.lse != nullptr)
+        p.lse[(static_cast<long long>(it.b) * p.w.heads + it.head[t]) * p.w.n_queries + row] =
+            l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    if (lane == 0) pipe.drain(bar(kWbMmaDone), 0, kSiteWinDrain);
+    __syncwarp();
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace vattn

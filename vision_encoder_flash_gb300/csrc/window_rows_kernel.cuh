@@ -10,36 +10,11 @@ namespace vattn {
 constexpr int kRowsWarps = 4;
 constexpr int kRowsMaxDim = 128;
 
-struct RowsTensor {
-  const void* p;
-  long long s[3];
-};
-
 struct RowsParams {
   WindowParams w;
   RowsTensor q, k, v, out, dout, dq, dk, dv;
   float* lse;
 };
-
-template <typename T>
-__device__ __forceinline__ const T* rows_at(const RowsTensor& t, long long b, long long h, long long i) {
-  return static_cast<const T*>(t.p) + b * t.s[0] + h * t.s[1] + i * t.s[2];
-}
-template <typename T>
-__device__ __forceinline__ T* rows_at_mut(const RowsTensor& t, long long b, long long h, long long i) {
-  return const_cast<T*>(rows_at<T>(t, b, h, i));
-}
-
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
-}
 
 template <typename T>
 __device__ __forceinline__ float rows_dot(const float* a, const T* b, int D) {
