@@ -122,7 +122,7 @@ typedef struct {
  * n_keys, head_dim], out as q: 16-byte aligned, strides multiples of 8
  * elements.  lse: NULL or f32 [batch, n_q_heads, n_queries] contiguous, the
  * natural logarithm of the sum of the row's exponentials (for
- * vattn_backward_window).  n_queries, n_keys < 2^30; q_start is held to
+ * vattn_backward_window).  n_queries, n_keys < 2^29; q_start is held to
  * +-2^30.
  */
 vattn_status vattn_forward_window(const vattn_rows* q, const vattn_rows* k, const vattn_rows* v,

@@ -11,6 +11,7 @@
 #include "../../include/vattn_decoder.h"
 #include "host_common.h"
 #include "qk_norm_rope_kernel.cuh"
+#include "window_bwd_kernel.cuh"
 #include "window_fwd_kernel.cuh"
 #include "window_rows_kernel.cuh"
 
@@ -21,7 +22,8 @@ using vattn::host::cuda_fail;
 using vattn::host::fail;
 using vattn::host::Workspace;
 
-constexpr int64_t kMaxRows = (int64_t{1} << 30) - 1;  // positions and their differences fit in 32 bits
+constexpr int64_t kMaxRows = (int64_t{1} << 30) - 1;
+constexpr int64_t kMaxKeys = (int64_t{1} << 29) - 1;  // positions and their differences fit in 32 bits
 
 int elem_size(int32_t dtype) { return dtype == VATTN_F32 ? 4 : 2; }
 
@@ -276,8 +278,8 @@ vattn_status check_window_args(const vattn_window_args* a) {
   if (a->n_kv_heads == 0 ? a->n_q_heads != 0 : a->n_q_heads % a->n_kv_heads != 0)
     return fail(VATTN_ERR_INVALID_ARG, "n_q_heads %lld is not a multiple of n_kv_heads %lld",
                 (long long)a->n_q_heads, (long long)a->n_kv_heads);
-  if (a->n_queries > kMaxRows || a->n_keys > kMaxRows)
-    return fail(VATTN_ERR_UNSUPPORTED, "n_queries and n_keys must stay below 2^30");
+  if (a->n_queries > kMaxKeys || a->n_keys > kMaxKeys)
+    return fail(VATTN_ERR_UNSUPPORTED, "n_queries and n_keys must stay below 2^29");
   if (a->n_q_heads > kMaxRows || a->batch > kMaxRows || a->batch * a->n_q_heads > kMaxRows)
     return fail(VATTN_ERR_UNSUPPORTED, "batch * n_q_heads must stay below 2^30");
   if (a->window < 0) return fail(VATTN_ERR_INVALID_ARG, "window must be >= 0");
@@ -308,7 +310,7 @@ vattn::WindowParams window_params(const vattn_window_args* a) {
   w.n_queries = static_cast<int>(a->n_queries);
   w.n_keys = static_cast<int>(a->n_keys);
   w.dim = static_cast<int>(a->head_dim);
-  const int64_t none = int64_t{1} << 30;
+  const int64_t none = kMaxKeys + 1;
   w.window = static_cast<int>(a->window == 0 || a->window > none ? none : a->window);
   w.sinks = static_cast<int>(a->n_sinks > none ? none : a->n_sinks);
   w.scale = a->scale;
@@ -350,15 +352,13 @@ vattn_status forward_checks(const vattn_rows* q, const vattn_rows* k, const vatt
 }
 
 vattn_status forward_rows(const vattn_rows* q, const vattn_rows* k, const vattn_rows* v,
-                          const vattn_rows* out, float* lse, const vattn_window_args* a,
-                          cudaStream_t stream) {
+                          const vattn_rows* out, const vattn_window_args* a, cudaStream_t stream) {
   vattn::RowsParams p{};
   p.w = window_params(a);
   p.q = rows_tensor(q);
   p.k = rows_tensor(k);
   p.v = rows_tensor(v);
   p.out = rows_tensor(out);
-  p.lse = lse;
   const unsigned grid = rows_grid(a->batch * a->n_q_heads * a->n_queries);
   if (a->dtype == VATTN_F16)
     vattn::vattn_window_rows_kernel<__half><<<grid, vattn::kRowsWarps * 32, 0, stream>>>(p);
@@ -452,6 +452,96 @@ vattn_status forward_window(const vattn_rows* q, const vattn_rows* k, const vatt
                              : window_fwd_launch<__half, 2>(tm, p, sms, device, stream);
   return a->head_dim <= 64 ? window_fwd_launch<__nv_bfloat16, 1>(tm, p, sms, device, stream)
                            : window_fwd_launch<__nv_bfloat16, 2>(tm, p, sms, device, stream);
+}
+
+template <typename T, int NKB, bool kKeys>
+vattn_status grad_launch(const CUtensorMap& x1, const CUtensorMap& x2, const CUtensorMap& y1, const CUtensorMap& y2,
+                         const vattn::WindowGradParams& p, long long blocks, int device, cudaStream_t stream) {
+  using P = vattn::GradPlan<NKB>;
+  auto kernel = vattn::vattn_window_bwd_kernel<T, NKB, kKeys>;
+  static std::atomic<uint8_t> done[vattn::host::kMaxDevices];
+  const vattn_status st = allow_smem(kernel, P::kSmemBytes, done, device);
+  if (st != VATTN_OK) return st;
+  if (blocks > INT32_MAX) return fail(VATTN_ERR_UNSUPPORTED, "too many tiles of 128 rows");
+  kernel<<<static_cast<unsigned>(blocks), P::kThreads, P::kSmemBytes, stream>>>(x1, x2, y1, y2, p);
+  return launched("gradient kernel launch");
+}
+
+// The three gradients (checks passed; queries or keys may be none).
+template <typename T, int NKB>
+vattn_status backward_window(const Tensor& tg, const Tensor& tq, const Tensor& tk, const Tensor& tv,
+                             vattn::WindowGradParams p, int32_t dtype, int sms, int device, cudaStream_t stream) {
+  using vattn::kGradCols;
+  using vattn::kTile;
+  vattn_status st;
+  const long long seqs = static_cast<long long>(p.w.batch) * p.w.kv_heads;
+  const int row_tiles = (p.w.n_queries + kTile - 1) / kTile;
+  p.stat_tiles = 2 * row_tiles;
+  p.key_tiles = (p.w.n_keys + kTile - 1) / kTile;
+  // Items (query tiles of all heads of the group) of an ordinary key tile,
+  // and of one of the first keys, which every later query sees.  The key
+  // tiles are cut so that there are two blocks a multiprocessor, but none
+  // under 8 items; those of the first keys into chunks of the same length.
+  const long long all_items = static_cast<long long>(p.w.group) * ((p.w.n_queries + kGradCols - 1) / kGradCols);
+  const long long items = std::min<long long>(
+      all_items, static_cast<long long>(p.w.group) * ((static_cast<long long>(p.w.window) + kTile - 1) / kGradCols + 2));
+  p.sink_tiles = items < all_items ? std::min(p.key_tiles, (p.w.sinks - 1) / kTile + (p.w.sinks > 0)) : 0;
+  const long long tiles = std::max<long long>(1, seqs * p.key_tiles);
+  p.chunks = static_cast<int>(std::max<long long>(1, std::min((2LL * sms + tiles - 1) / tiles, items / 8)));
+  const long long share = std::max<long long>(8, items / p.chunks);
+  p.sink_chunks = p.sink_tiles > 0 ? static_cast<int>(std::max<long long>(1, std::min<long long>(256, (all_items + share - 1) / share))) : 1;
+  const long long sink_blocks = seqs * p.sink_tiles * p.sink_chunks;
+  const long long rest_blocks = seqs * (p.key_tiles - p.sink_tiles) * p.chunks;
+  const long long slots = (p.sink_chunks > 1 ? sink_blocks : 0) + (p.chunks > 1 ? rest_blocks : 0);
+  const size_t stat_bytes = static_cast<size_t>(p.w.batch) * p.w.heads * p.stat_tiles * vattn::kGradStat * 4;
+  const size_t part_bytes = static_cast<size_t>(slots) * 2 * kTile * p.w.dim * 4;
+  Workspace ws;
+  if (stat_bytes + part_bytes > 0) {
+    if ((st = ws.take(stat_bytes + part_bytes, device, stream)) != VATTN_OK) return st;
+    p.stat = reinterpret_cast<float*>(ws.data());
+    p.part = reinterpret_cast<float*>(ws.data() + stat_bytes);
+  }
+  if (stat_bytes > 0) {
+    const long long rows = static_cast<long long>(p.w.batch) * p.w.heads * p.stat_tiles * kGradCols;
+    if (rows / 16 > INT32_MAX) return fail(VATTN_ERR_UNSUPPORTED, "too many query rows");
+    vattn::vattn_window_stat_kernel<T><<<static_cast<unsigned>(rows / 16), 256, 0, stream>>>(p);
+    if ((st = launched("gradient statistics kernel launch")) != VATTN_OK) return st;
+  }
+  // each tensor as an X tile (128 rows) and as a Y tile (64 rows); one that
+  // is empty is never loaded, and another's map stands in for it
+  const Tensor* t[4] = {&tq, &tg, &tk, &tv};
+  CUtensorMap x[4], y[4];
+  vattn::MapMul mul[4] = {};
+  for (int i = 0; i < 4; ++i) {
+    const Tensor& u = !t[i]->empty() ? *t[i] : (i < 2 ? tk : tq);
+    if ((st = make_rows_map(&x[i], &mul[i], u, dtype, kTile)) != VATTN_OK ||
+        (st = make_rows_map(&y[i], &mul[i], u, dtype, kGradCols)) != VATTN_OK)
+      return st;
+  }
+  if (!tk.empty()) {
+    p.mx1 = mul[2];
+    p.mx2 = mul[3];
+    p.my1 = mul[0];
+    p.my2 = mul[1];
+    if ((st = grad_launch<T, NKB, true>(x[2], x[3], y[0], y[1], p, sink_blocks + rest_blocks, device, stream)) != VATTN_OK)
+      return st;
+  }
+  if (!tq.empty()) {
+    p.mx1 = mul[0];
+    p.mx2 = mul[1];
+    p.my1 = mul[2];
+    p.my2 = mul[3];
+    if ((st = grad_launch<T, NKB, false>(x[0], x[1], y[2], y[3], p,
+                                         static_cast<long long>(p.w.batch) * p.w.heads * row_tiles, device, stream)) != VATTN_OK)
+      return st;
+  }
+  if (slots > 0) {
+    const long long joined = seqs * ((p.sink_chunks > 1 ? p.sink_tiles : 0) + (p.chunks > 1 ? p.key_tiles - p.sink_tiles : 0));
+    const dim3 grid(static_cast<unsigned>(joined), static_cast<unsigned>((2 * kTile * (p.w.dim / 8) + 255) / 256));
+    vattn::vattn_window_join_kernel<T><<<grid, 256, 0, stream>>>(p);
+    if ((st = launched("gradient join kernel launch")) != VATTN_OK) return st;
+  }
+  return ws.release();
 }
 
 }  // namespace
@@ -649,7 +739,10 @@ vattn_status vattn_backward_window(const vattn_rows* dout, const vattn_rows* q, 
   for (const Tensor* t : outs)
     if ((st = check_apart_bytes(lse, bytes, "lse", *t)) != VATTN_OK) return st;
   if (tq.empty() && tk.empty()) return VATTN_OK;
-  vattn::RowsParams p{};
+  int device = 0, sms = 0;
+  if ((st = current_device(&device)) != VATTN_OK) return st;
+  if ((st = vattn::host::sm_count(device, &sms)) != VATTN_OK) return st;
+  vattn::WindowGradParams p{};
   p.w = window_params(a);
   p.q = rows_tensor(q);
   p.k = rows_tensor(k);
@@ -659,22 +752,15 @@ vattn_status vattn_backward_window(const vattn_rows* dout, const vattn_rows* q, 
   p.dq = rows_tensor(dq);
   p.dk = rows_tensor(dk);
   p.dv = rows_tensor(dv);
-  p.lse = const_cast<float*>(lse);
+  p.lse = lse;
+  p.scale_log2 = a->scale * vattn::kLog2E;
+  if ((st = vattn::host::status_word(device, &p.status)) != VATTN_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-  const unsigned gq = rows_grid(a->batch * a->n_q_heads * a->n_queries),
-                 gk = rows_grid(a->batch * a->n_kv_heads * a->n_keys), threads = vattn::kRowsWarps * 32;
-  const bool f16 = a->dtype == VATTN_F16;
-  if (gk > 0) {
-    if (f16) vattn::vattn_window_rows_dkv_kernel<__half><<<gk, threads, 0, stream>>>(p);
-    else vattn::vattn_window_rows_dkv_kernel<__nv_bfloat16><<<gk, threads, 0, stream>>>(p);
-    if ((st = launched("key gradient kernel launch")) != VATTN_OK) return st;
-  }
-  if (gq > 0) {
-    if (f16) vattn::vattn_window_rows_dq_kernel<__half><<<gq, threads, 0, stream>>>(p);
-    else vattn::vattn_window_rows_dq_kernel<__nv_bfloat16><<<gq, threads, 0, stream>>>(p);
-    if ((st = launched("query gradient kernel launch")) != VATTN_OK) return st;
-  }
-  return VATTN_OK;
+  if (a->dtype == VATTN_F16)
+    return a->head_dim <= 64 ? backward_window<__half, 1>(tg, tq, tk, tv, p, a->dtype, sms, device, stream)
+                             : backward_window<__half, 2>(tg, tq, tk, tv, p, a->dtype, sms, device, stream);
+  return a->head_dim <= 64 ? backward_window<__nv_bfloat16, 1>(tg, tq, tk, tv, p, a->dtype, sms, device, stream)
+                           : backward_window<__nv_bfloat16, 2>(tg, tq, tk, tv, p, a->dtype, sms, device, stream);
 }
 
 vattn_status vattn_forward_cached(const vattn_rows* q, const vattn_rows* k, const vattn_rows* v,
@@ -689,7 +775,7 @@ vattn_status vattn_forward_cached(const vattn_rows* q, const vattn_rows* k, cons
   if (a->batch > 0 && !a->kv_len) return fail(VATTN_ERR_INVALID_ARG, "null kv_len");
   if ((st = forward_checks(q, k, v, out, nullptr, a)) != VATTN_OK) return st;
   if (a->batch * a->n_q_heads == 0 || a->n_queries == 0) return VATTN_OK;
-  return forward_rows(q, k, v, out, nullptr, a, static_cast<cudaStream_t>(stream_ptr));
+  return forward_rows(q, k, v, out, a, static_cast<cudaStream_t>(stream_ptr));
 }
 
 }  // extern "C"

@@ -1,0 +1,518 @@
+// window_bwd_kernel.cuh -- gradients of the windowed attention
+// (vattn_backward_window) on the tensor cores.
+//
+// With s_ij = scale q_i . k_j, p_ij = exp(s_ij - lse_i) on the visible pairs
+// (0 elsewhere) and delta_i = dout_i . out_i:
+//   dp_ij = dout_i . v_j,   ds_ij = p_ij (dp_ij - delta_i),
+//   dv_j = sum_i p_ij dout_i,  dk_j = scale sum_i ds_ij q_i,  dq_i = scale sum_j ds_ij k_j.
+// The sums of dk and dv run over queries (of all heads of the group), that of
+// dq over keys.  Two walks recompute s and dp rather than share them: seven
+// products instead of five, but no atomics, so the order of every sum is
+// fixed and the same call gives the same bits.
+//
+// Both walks are one kernel body: a block keeps a 128-row tile X (keys: K
+// and V; queries: Q and dout) and streams 64-row tiles Y of the other side
+// that its rows see:
+//   S = X1 Y1^T, G = X2 Y2^T           (128 x 64, f32 in TMEM)
+//   P = 2^(S scale log2e - lse2), D = P (G - delta), rounded to the type
+//   keys:     dV += P Y2, dK += D Y1     queries:  dQ += D Y1
+// P and D overwrite S and G in TMEM and are the A operands of the second
+// products; Y is read K-major for the first and MN-major for the second, so
+// nothing is transposed.  Two S/G buffers, each with a warpgroup of its own,
+// alternate: the tensor core works on one while the other is turned into P
+// and D.  TMEM (512 columns): S 128 b, G 128 b + 64, sums at 256 and 384.
+//
+// A key tile's walk is cut into chunks (f32 partial sums in a workspace,
+// added in order by vattn_window_join_kernel) where tiles are few or, for the
+// tiles of the first keys, the walk is long.
+//
+// Rounding: P and D go to the tensors' type for the second products; all
+// sums, lse and delta are f32.
+#pragma once
+
+#include "window_pipe.cuh"
+
+namespace vattn {
+
+constexpr int kGradCols = 64;                       // rows of a Y tile
+constexpr int kGradBlock = kGradCols * 128;         // 64 rows x 64 elements, 128-byte swizzle
+constexpr int kGradStat = 2 * kGradCols;            // floats of a tile's -lse2, -delta
+
+struct WindowGradParams {
+  WindowParams w;
+  RowsTensor q, k, v, out, dout, dq, dk, dv;
+  const float* lse;
+  float* stat;     // [batch * heads][stat_tiles][-lse2 x 64 | -delta x 64]
+  float* part;     // [slot][dv, dk][128][dim] partial sums of the chunks
+  uint32_t* status;
+  MapMul mx1, mx2, my1, my2;
+  int stat_tiles;  // Y tiles of the queries, to a multiple of two
+  int key_tiles;   // ceil(n_keys / 128)
+  int sink_tiles;  // of these, the first with keys < sinks, cut into sink_chunks
+  int sink_chunks, chunks;
+  float scale_log2;
+};
+
+// -lse2 = -lse log2(e) and -delta of every query row; rows that see nothing
+// (and those that fill the last tile) get -infinity and 0, hence weights 0.
+template <typename T>
+__global__ void __launch_bounds__(256) vattn_window_stat_kernel(const __grid_constant__ WindowGradParams p) {
+  const int lane16 = threadIdx.x & 15;
+  const long long rows = static_cast<long long>(p.stat_tiles) * kGradCols;
+  const long long total = rows * p.w.batch * p.w.heads;
+  const long long idx = static_cast<long long>(blockIdx.x) * 16 + (threadIdx.x >> 4);
+  if (idx >= total) return;  // whole half-warps
+  const long long bh = idx / rows;
+  const int i = static_cast<int>(idx - bh * rows);
+  const int b = static_cast<int>(bh / p.w.heads), h = static_cast<int>(bh - static_cast<long long>(b) * p.w.heads);
+  const Seq s = window_seq(p.w, b);
+  const int pos = s.start + i;
+  const bool on = i < p.w.n_queries && pos >= 0 && pos < s.len;
+  float sum = 0.0f;
+  if (on && lane16 * 8 < p.w.dim) {
+    float x[8], y[8];
+    reinterpret_cast<const Vec<T, 8>*>(rows_at<T>(p.dout, b, h, i) + lane16 * 8)->widen(x);
+    reinterpret_cast<const Vec<T, 8>*>(rows_at<T>(p.out, b, h, i) + lane16 * 8)->widen(y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = fmaf(x[e], y[e], sum);
+  }
+  const uint32_t mask = 0xffffu << (threadIdx.x & 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(mask, sum, o);
+  if (lane16 != 0) return;
+  const float lse = on ? p.lse[bh * p.w.n_queries + i] : -INFINITY;
+  float* to = p.stat + (bh * p.stat_tiles + i / kGradCols) * kGradStat + i % kGradCols;
+  const bool empty = lse == -INFINITY;
+  to[0] = empty ? -INFINITY : -lse * kLog2E;
+  to[kGradCols] = empty ? 0.0f : -sum;
+}
+
+template <int NKB>
+struct GradPlan {
+  static constexpr int kXBytes = NKB * kBlockBytes;
+  static constexpr int kYBytes = NKB * kGradBlock;
+  static constexpr int kStageBytes = 2 * kYBytes + 1024;  // Y1, Y2, the queries' stats
+  static constexpr int kStages = NKB == 1 ? 8 : 4;
+  static constexpr int kOffX = 0;
+  static constexpr int kOffY = 2 * kXBytes;
+  static constexpr int kOffBar = kOffY + kStages * kStageBytes;
+  static constexpr int kSmemBytes = kOffBar + 256 + 1024;
+  static constexpr int kThreads = 384;
+  static constexpr uint32_t kRegsOther = 72, kRegsMath = 216;  // 72 + 2 x 216 = 3 x 168
+  static_assert(kSmemBytes <= 232448, "shared memory");
+};
+
+enum GradBar : int {
+  kGbXFull = 0, kGbYFull = 1, kGbYEmpty = 9, kGbSFull = 17, kGbPFull = 19, kGbAcc = 21, kGbCount = 22,
+};
+
+// What a block walks over: Y tiles 0 .. n - 1 of its share.
+template <bool kKeys>
+struct GradWalk {
+  int b, h;         // h: key head (keys) or query head (queries)
+  int row0;         // first row of the X tile
+  Seq s;
+  long long slot;   // of the partial sums, -1: none
+  // keys: item -> head g of the group and query tile; queries: key tiles [0, ns) and [first, ..)
+  int first, per_head, begin, n, ns;
+
+  // Y tile (in units of 64 rows) and query head of item x
+  __device__ __forceinline__ int tile(int x, int* g) const {
+    if (kKeys) {
+      const int i = begin + x;
+      *g = i / per_head;
+      return first + (i - *g * per_head);
+    }
+    *g = 0;
+    return x < ns ? x : first + (x - ns);
+  }
+};
+
+__device__ __forceinline__ GradWalk<true> grad_walk_keys(const WindowGradParams& p, long long block) {
+  GradWalk<true> k;
+  const long long seqs = static_cast<long long>(p.w.batch) * p.w.kv_heads;
+  const long long sink_blocks = seqs * p.sink_tiles * p.sink_chunks;
+  const bool sink = block < sink_blocks;
+  const long long at = sink ? block : block - sink_blocks;
+  const int chunks = sink ? p.sink_chunks : p.chunks;
+  const int chunk = static_cast<int>(at % chunks);
+  const long long t = at / chunks;
+  const long long bk = t % seqs;
+  const int tile = static_cast<int>(t / seqs) + (sink ? 0 : p.sink_tiles);
+  k.b = static_cast<int>(bk / p.w.kv_heads);
+  k.h = static_cast<int>(bk - static_cast<long long>(k.b) * p.w.kv_heads);
+  k.row0 = tile * kTile;
+  k.s = window_seq(p.w, k.b);
+  // slots: those of the first keys' tiles, then the others' (where cut)
+  k.slot = chunks == 1 ? -1 : (sink || p.sink_chunks == 1 ? at : sink_blocks + at);
+  k.ns = 0;
+  k.n = k.begin = k.first = 0;
+  k.per_head = 1;
+  const int hi_pos = k.row0 < p.w.sinks ? k.s.len - 1 : min(k.s.len - 1, k.row0 + kTile - 1 + p.w.window - 1);
+  const int lo = max(0, k.row0 - k.s.start), hi = min(p.w.n_queries - 1, hi_pos - k.s.start);
+  if (k.row0 < k.s.len && hi >= lo) {
+    k.first = lo / kGradCols;
+    k.per_head = hi / kGradCols - k.first + 1;
+    const long long all = static_cast<long long>(k.per_head) * p.w.group;
+    k.begin = static_cast<int>(all * chunk / chunks);
+    k.n = static_cast<int>(all * (chunk + 1) / chunks) - k.begin;
+  }
+  return k;
+}
+
+__device__ __forceinline__ GradWalk<false> grad_walk_queries(const WindowGradParams& p, long long block) {
+  GradWalk<false> k;
+  const long long bhs = static_cast<long long>(p.w.batch) * p.w.heads;
+  const int tiles = p.stat_tiles / 2;
+  const long long bh = block % bhs;
+  k.row0 = (tiles - 1 - static_cast<int>(block / bhs)) * kTile;  // late rows see most: first
+  k.b = static_cast<int>(bh / p.w.heads);
+  k.h = static_cast<int>(bh - static_cast<long long>(k.b) * p.w.heads);
+  k.s = window_seq(p.w, k.b);
+  k.slot = -1;
+  k.begin = 0;
+  k.per_head = 1;
+  k.n = k.ns = k.first = 0;
+  const int lo = max(0, k.s.start + k.row0);
+  const int hi = min(k.s.start + min(k.row0 + kTile, p.w.n_queries), k.s.len) - 1;
+  if (hi >= lo) {
+    k.first = max(0, lo - p.w.window + 1) / kGradCols;
+    k.ns = min((min(p.w.sinks, k.s.len) + kGradCols - 1) / kGradCols, k.first);
+    k.n = k.ns + hi / kGradCols - k.first + 1;
+  }
+  return k;
+}
+
+template <typename T, int NKB, bool kKeys>
+__device__ __forceinline__ void grad_block(const CUtensorMap* tm_x1, const CUtensorMap* tm_x2,
+                                           const CUtensorMap* tm_y1, const CUtensorMap* tm_y2,
+                                           const WindowGradParams& p, long long block) {
+  using P = GradPlan<NKB>;
+  constexpr int S = P::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_s = ptx::smem_addr(smem_raw);
+  const uint32_t base_s = (raw_s + 1023u) & ~1023u;
+  uint8_t* const base = smem_raw + (base_s - raw_s);
+  const uint32_t bar0 = base_s + P::kOffBar;
+  auto bar = [bar0](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(base + P::kOffBar + 8 * kGbCount);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  const Pipe pipe{abort_flag, p.status};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    ptx::mbar_init(bar(kGbXFull), 1);
+    for (int i = 0; i < S; ++i) {
+      ptx::mbar_init(bar(kGbYFull + i), 1);
+      ptx::mbar_init(bar(kGbYEmpty + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(bar(kGbSFull + i), 1);
+      ptx::mbar_init(bar(kGbPFull + i), 4);
+    }
+    ptx::mbar_init(bar(kGbAcc), 1);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tensormap(tm_x1);
+    ptx::prefetch_tensormap(tm_x2);
+    ptx::prefetch_tensormap(tm_y1);
+    ptx::prefetch_tensormap(tm_y2);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_addr(const_cast<uint32_t*>(tmem_slot)), 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  ptx::grid_dep_wait();
+  GradWalk<kKeys> wk;
+  if constexpr (kKeys) wk = grad_walk_keys(p, block);
+  else wk = grad_walk_queries(p, block);
+  const int group = p.w.group;
+  auto stage = [&](int n) -> uint32_t { return base_s + P::kOffY + static_cast<uint32_t>(n % S) * P::kStageBytes; };
+
+  if (warp < 4) {
+    ptx::regs_decrease<P::kRegsOther>();
+    if (warp == 0 && lane == 0 && wk.n > 0) {
+      // ------------------------------------------------------ X and Y tiles
+      const uint64_t keep = ptx::policy_evict_last(), once = ptx::policy_evict_first();
+      ptx::mbar_arrive_expect_tx(bar(kGbXFull), 2 * P::kXBytes);
+      for (int i = 0; i < 2; ++i)
+        for (int kb = 0; kb < NKB; ++kb) {
+          const MapMul m = i ? p.mx2 : p.mx1;
+          ptx::tma_load_4d_hint(base_s + P::kOffX + i * P::kXBytes + kb * kBlockBytes, i ? tm_x2 : tm_x1,
+                                bar(kGbXFull), kb * 64, wk.row0, wk.h * m.h, wk.b * m.b, once);
+        }
+      int n = 0;
+      for (; n < wk.n; ++n) {
+        const int st = n % S;
+        if (!pipe.wait(bar(kGbYEmpty + st), (static_cast<uint32_t>(n / S) & 1u) ^ 1u, kSiteGradLoad)) break;
+        ptx::mbar_arrive_expect_tx(bar(kGbYFull + st), 2 * P::kYBytes + (kKeys ? kGradStat * 4 : 0));
+        int g;
+        const int tile = wk.tile(n, &g);
+        const int h = kKeys ? wk.h * group + g : wk.h / group;
+        for (int i = 0; i < 2; ++i)
+          for (int kb = 0; kb < NKB; ++kb) {
+            const MapMul m = i ? p.my2 : p.my1;
+            ptx::tma_load_4d_hint(stage(n) + i * P::kYBytes + kb * kGradBlock, i ? tm_y2 : tm_y1,
+                                  bar(kGbYFull + st), kb * 64, tile * kGradCols, h * m.h, wk.b * m.b, keep);
+          }
+        if (kKeys)
+          ptx::bulk_load(stage(n) + 2 * P::kYBytes,
+                         p.stat + ((static_cast<long long>(wk.b) * p.w.heads + h) * p.stat_tiles + tile) * kGradStat,
+                         kGradStat * 4, bar(kGbYFull + st));
+      }
+      pipe.drain(bar(kGbXFull), 0, kSiteGradDrain);
+      for (int d = n > S ? n - S : 0; d < n; ++d)
+        pipe.drain(bar(kGbYFull + d % S), static_cast<uint32_t>(d / S) & 1u, kSiteGradDrain);
+    } else if (warp == 1 && wk.n > 0) {
+      // --------------------------------------------------------- MMA issue
+      const int ksteps = (p.w.dim + 15) >> 4;
+      const uint32_t idesc_s = ptx::idesc_16bit_f32(kTile, kGradCols, false, Elem<T>::kBf16);
+      const uint32_t idesc_a = ptx::idesc_16bit_f32(kTile, static_cast<uint32_t>(ksteps) * 16u, true, Elem<T>::kBf16);
+      constexpr uint32_t hi = ptx::smem_desc_hi(1024, ptx::kSwizzle128B);
+      auto issue_s = [&](int n) -> bool {
+        if (!pipe.wait_warp(bar(kGbYFull + n % S), static_cast<uint32_t>(n / S) & 1u, kSiteGradMma)) return false;
+        // Y rows outside the sequence may hold anything: zero, so that they
+        // add nothing to the second products
+        int g;
+        const int row0 = wk.tile(n, &g) * kGradCols;
+        const int first = kKeys ? -wk.s.start - row0 : 0;            // rows of the sequence: [first, last)
+        const int last = (kKeys ? wk.s.len - wk.s.start : wk.s.len) - row0;
+        if (first > 0 || last < kGradCols) {
+          for (int kb = 0; kb < 2 * NKB; ++kb)
+            for (int i = lane; i < kGradCols * 8; i += 32)
+              if ((i >> 3) < first || (i >> 3) >= last)
+                ptx::st_shared_v4(stage(n) + kb * kGradBlock + i * 16, 0.0f, 0.0f, 0.0f, 0.0f);
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+        }
+        ptx::tc_fence_after();
+        if (lane == 0) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t x = ptx::smem_desc_lo(base_s + P::kOffX + i * P::kXBytes, 16);
+            const uint32_t y = ptx::smem_desc_lo(stage(n) + i * P::kYBytes, 16);
+            for (int ks = 0; ks < ksteps; ++ks)
+              ptx::mma_ss(tmem + (n & 1) * 128u + i * 64u,
+                          ptx::smem_desc_join(x + (((ks >> 2) * kBlockBytes + (ks & 3) * 32) >> 4), hi),
+                          ptx::smem_desc_join(y + (((ks >> 2) * kGradBlock + (ks & 3) * 32) >> 4), hi), idesc_s, ks > 0);
+          }
+          ptx::mma_commit(bar(kGbSFull + (n & 1)));
+        }
+        return true;
+      };
+      bool ok = pipe.wait_warp(bar(kGbXFull), 0, kSiteGradMma);
+      for (int n = 0; ok && n < 2 && n < wk.n; ++n) ok = issue_s(n);
+      for (int n = 0; ok && n < wk.n; ++n) {
+        const int b = n & 1;
+        if (!(ok = pipe.wait_warp(bar(kGbPFull + b), static_cast<uint32_t>(n >> 1) & 1u, kSiteGradMma))) break;
+        ptx::tc_fence_after();
+        if (lane == 0) {
+          const uint32_t y1 = ptx::smem_desc_lo(stage(n), kGradBlock);
+          const uint32_t y2 = ptx::smem_desc_lo(stage(n) + P::kYBytes, kGradBlock);
+#pragma unroll
+          for (int ks = 0; ks < kGradCols / 16; ++ks) {
+            if (kKeys)
+              ptx::mma_ts(tmem + 256u, tmem + b * 128u + ks * 8u, ptx::smem_desc_join(y2 + ks * (2048u >> 4), hi),
+                          idesc_a, n > 0 || ks > 0);
+            ptx::mma_ts(tmem + 384u, tmem + b * 128u + 64u + ks * 8u,
+                        ptx::smem_desc_join(y1 + ks * (2048u >> 4), hi), idesc_a, n > 0 || ks > 0);
+          }
+          ptx::mma_commit(bar(kGbYEmpty + n % S));
+        }
+        if (n + 2 < wk.n) ok = issue_s(n + 2);
+      }
+      if (lane == 0) ptx::mma_commit(bar(kGbAcc));
+    }
+  } else {
+    ptx::regs_increase<P::kRegsMath>();
+    // ------------------------------------------------- P and D, then results
+    const int wg = (warp - 4) >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem + lanes + wg * 128u, g_addr = s_addr + 64u;
+    const int row = wk.row0 + r;  // key, or query row of the call
+    const int W = p.w.window;
+    float row_lse = -INFINITY, row_delta = 0.0f;
+    if (!kKeys && wk.n > 0) {
+      const float* st = p.stat + ((static_cast<long long>(wk.b) * p.w.heads + wk.h) * p.stat_tiles +
+                                  row / kGradCols) * kGradStat + row % kGradCols;
+      row_lse = st[0];
+      row_delta = st[kGradCols];
+    }
+    const float2 scale = make_float2(p.scale_log2, p.scale_log2);
+    bool ok = true;
+    for (int n = wg; n < wk.n; n += 2) {
+      int gh;
+      const int y0 = wk.tile(n, &gh) * kGradCols;
+      if (!(ok = pipe.wait_warp(bar(kGbSFull + wg), static_cast<uint32_t>(n >> 1) & 1u, kSiteGradSoft))) break;
+      ptx::tc_fence_after();
+      uint32_t s[2][32], g[2][32];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        ptx::tmem_ld_32x32b_x32(s_addr + c * 32, s[c]);
+        ptx::tmem_ld_32x32b_x32(g_addr + c * 32, g[c]);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        ptx::tmem_wait_ld_dep(s[c]);
+        ptx::tmem_wait_ld_dep(g[c]);
+      }
+      // columns [c_lo, c_hi] of the row are visible, and those <= c_sink
+      int c_lo, c_hi, c_sink = -1;
+      bool full;
+      if (kKeys) {
+        const int p0 = wk.s.start + y0;
+        c_lo = row < wk.s.len ? row - p0 : kGradCols;
+        c_hi = row < p.w.sinks ? kGradCols - 1 : row + W - 1 - p0;
+        full = p0 >= wk.row0 + kTile - 1 && p0 + kGradCols <= wk.s.len &&
+               (p0 + kGradCols - 1 < wk.row0 + W || wk.row0 + kTile <= p.w.sinks);
+      } else {
+        const int pos = wk.s.start + row, p0 = wk.s.start + wk.row0;
+        c_hi = pos >= 0 && pos < wk.s.len ? pos - y0 : -1;
+        c_lo = pos - W + 1 - y0;
+        c_sink = min(p.w.sinks - 1 - y0, c_hi);
+        full = p0 >= y0 + kGradCols - 1 && p0 + kTile <= wk.s.len &&
+               (p0 + kTile - 1 - W < y0 || y0 + kGradCols <= p.w.sinks);
+      }
+      if (!full) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t see = (bits_upto(c_hi, c) & ~bits_upto(c_lo - 1, c)) | bits_upto(c_sink, c);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!((see >> e) & 1u)) {
+              s[c][e] = 0xff800000u;
+              g[c][e] = 0u;
+            }
+        }
+      }
+      const uint32_t stats = stage(n) + 2 * P::kYBytes;
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float4 nl, nd;
+          if (kKeys) {
+            nl = ptx::ld_shared_v4(stats + (c * 32 + e * 4) * 4);
+            nd = ptx::ld_shared_v4(stats + (kGradCols + c * 32 + e * 4) * 4);
+          } else {
+            nl = make_float4(row_lse, row_lse, row_lse, row_lse);
+            nd = make_float4(row_delta, row_delta, row_delta, row_delta);
+          }
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            const int i = e * 4 + f * 2;
+            const float2 y = __ffma2_rn(make_float2(__uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1])), scale,
+                                        f ? make_float2(nl.z, nl.w) : make_float2(nl.x, nl.y));
+            const float2 w = make_float2(ptx::ex2_approx(y.x), ptx::ex2_approx(y.y));
+            const float2 d = __fmul2_rn(
+                w, __fadd2_rn(make_float2(__uint_as_float(g[c][i]), __uint_as_float(g[c][i + 1])),
+                              f ? make_float2(nd.z, nd.w) : make_float2(nd.x, nd.y)));
+            if (kKeys) s[c][i / 2] = pack2<T>(w.x, w.y);
+            g[c][i / 2] = pack2<T>(d.x, d.y);
+          }
+        }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        if (kKeys) ptx::tmem_st_32x32b_x16(s_addr + c * 16, *reinterpret_cast<uint32_t(*)[16]>(s[c]));
+        ptx::tmem_st_32x32b_x16(g_addr + c * 16, *reinterpret_cast<uint32_t(*)[16]>(g[c]));
+      }
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      pipe_warp_arrive(bar(kGbPFull + wg));
+    }
+    // keys: warpgroup 0 stores dV (unscaled), 1 dK; queries: each every other 16 columns of dQ
+    if (ok && wk.n > 0) ok = pipe.wait_warp(bar(kGbAcc), 0, kSiteGradOut);
+    if (ok) {
+      ptx::tc_fence_after();
+      const int D = p.w.dim;
+      const uint32_t a_addr = tmem + lanes + (kKeys && wg == 0 ? 256u : 384u);
+      const bool live = wk.n > 0 && (kKeys ? row < wk.s.len : (wk.s.start + row >= 0 && wk.s.start + row < wk.s.len));
+      const float f = kKeys && wg == 0 ? 1.0f : p.w.scale;
+      const bool store = row < (kKeys ? p.w.n_keys : p.w.n_queries);
+      T* to = nullptr;
+      float* part = nullptr;
+      if (wk.slot >= 0) part = p.part + ((wk.slot * 2 + wg) * kTile + r) * static_cast<long long>(D);
+      else if (store) to = rows_at_mut<T>(kKeys ? (wg == 0 ? p.dv : p.dk) : p.dq, wk.b, wk.h, row);
+      for (int c = kKeys ? 0 : wg * 16; c < D; c += kKeys ? 16 : 32) {
+        uint32_t y[16];
+        if (wk.n > 0) {
+          ptx::tmem_ld_32x32b_x16(a_addr + c, y);
+          ptx::tmem_wait_ld_dep16(y);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[e] = live ? __float_as_uint(__uint_as_float(y[e]) * f) : 0u;
+        if (part != nullptr) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            if (c + e < D) *reinterpret_cast<uint4*>(part + c + e) = make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+        } else if (to != nullptr) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 8)
+            if (c + e < D) {
+              uint32_t h[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                h[k] = pack2<T>(__uint_as_float(y[e + 2 * k]), __uint_as_float(y[e + 2 * k + 1]));
+              *reinterpret_cast<uint4*>(to + c + e) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+        }
+      }
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    if (lane == 0 && wk.n > 0) pipe.drain(bar(kGbAcc), 0, kSiteGradDrain);
+    __syncwarp();
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <typename T, int NKB, bool kKeys>
+__global__ void __launch_bounds__(GradPlan<NKB>::kThreads, 1)
+    vattn_window_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_constant__ CUtensorMap tm_x2,
+                            const __grid_constant__ CUtensorMap tm_y1, const __grid_constant__ CUtensorMap tm_y2,
+                            const __grid_constant__ WindowGradParams p) {
+  grad_block<T, NKB, kKeys>(&tm_x1, &tm_x2, &tm_y1, &tm_y2, p, blockIdx.x);
+}
+
+// dk and dv of the key tiles that were cut: their chunks' partial sums added
+// in order.  blockIdx.x = (tile, sequence and key head); a thread takes 8
+// consecutive elements of one row.
+template <typename T>
+__global__ void __launch_bounds__(256) vattn_window_join_kernel(const __grid_constant__ WindowGradParams p) {
+  const long long seqs = static_cast<long long>(p.w.batch) * p.w.kv_heads;
+  const long long bk = blockIdx.x % seqs;
+  const int tile = static_cast<int>(blockIdx.x / seqs) + (p.sink_chunks > 1 ? 0 : p.sink_tiles);
+  const bool sink = tile < p.sink_tiles;
+  const int chunks = sink ? p.sink_chunks : p.chunks;
+  if (chunks == 1) return;
+  const long long sink_blocks = seqs * p.sink_tiles * p.sink_chunks;
+  const long long at = ((static_cast<long long>(tile) - (sink ? 0 : p.sink_tiles)) * seqs + bk) * chunks;
+  const long long slot = sink || p.sink_chunks == 1 ? at : sink_blocks + at;
+  const int b = static_cast<int>(bk / p.w.kv_heads), h = static_cast<int>(bk - static_cast<long long>(b) * p.w.kv_heads);
+  const int D = p.w.dim, per_row = D / 8;
+  const int e = blockIdx.y * 256 + threadIdx.x;
+  if (e >= 2 * kTile * per_row) return;
+  const int which = e / (kTile * per_row), r = e / per_row % kTile, d = e % per_row * 8;
+  const int row = tile * kTile + r;
+  if (row >= p.w.n_keys) return;
+  ptx::grid_dep_wait();
+  const float* from = p.part + ((slot * 2 + which) * kTile + r) * static_cast<long long>(D) + d;
+  float x[8] = {};
+  for (int c = 0; c < chunks; ++c, from += 2 * kTile * static_cast<long long>(D)) {
+    const float4 lo = *reinterpret_cast<const float4*>(from), hi = *reinterpret_cast<const float4*>(from + 4);
+    x[0] += lo.x; x[1] += lo.y; x[2] += lo.z; x[3] += lo.w;
+    x[4] += hi.x; x[5] += hi.y; x[6] += hi.z; x[7] += hi.w;
+  }
+  reinterpret_cast<Vec<T, 8>*>(rows_at_mut<T>(which ? p.dk : p.dv, b, h, row) + d)->narrow(x);
+}
+
+}  // namespace vattn
