@@ -24,7 +24,7 @@ DEPS = SOURCES + [os.path.join(CSRC, "attn_kernel.cuh"), os.path.join(CSRC, "sta
                   os.path.join(CSRC, "window_common.cuh"),
                   os.path.join(CSRC, "window_pipe.cuh"), os.path.join(CSRC, "window_fwd_kernel.cuh"),
                   os.path.join(CSRC, "window_bwd_kernel.cuh"),
-                  os.path.join(CSRC, "window_rows_kernel.cuh"),
+                  os.path.join(CSRC, "cached_kernel.cuh"),
                   os.path.join(ROOT, "include", "vattn.h"),
                   os.path.join(ROOT, "include", "vattn_decoder.h")]
 LIB = os.path.join(PKG, "libvattn.so")

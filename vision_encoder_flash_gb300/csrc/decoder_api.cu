@@ -9,11 +9,11 @@
 #include <cstdint>
 
 #include "../../include/vattn_decoder.h"
+#include "cached_kernel.cuh"
 #include "host_common.h"
 #include "qk_norm_rope_kernel.cuh"
 #include "window_bwd_kernel.cuh"
 #include "window_fwd_kernel.cuh"
-#include "window_rows_kernel.cuh"
 
 namespace {
 
@@ -326,10 +326,6 @@ vattn::RowsTensor rows_tensor(const vattn_rows* t) {
   return r;
 }
 
-unsigned rows_grid(int64_t rows) {
-  return static_cast<unsigned>((rows + vattn::kRowsWarps - 1) / vattn::kRowsWarps);
-}
-
 vattn_status forward_checks(const vattn_rows* q, const vattn_rows* k, const vattn_rows* v,
                             const vattn_rows* out, const float* lse, const vattn_window_args* a) {
   const Tensor tq = window_tensor("q", q, a, true, false), tk = window_tensor("k", k, a, false, false),
@@ -349,22 +345,6 @@ vattn_status forward_checks(const vattn_rows* q, const vattn_rows* k, const vatt
     if (st != VATTN_OK) return st;
   }
   return VATTN_OK;
-}
-
-vattn_status forward_rows(const vattn_rows* q, const vattn_rows* k, const vattn_rows* v,
-                          const vattn_rows* out, const vattn_window_args* a, cudaStream_t stream) {
-  vattn::RowsParams p{};
-  p.w = window_params(a);
-  p.q = rows_tensor(q);
-  p.k = rows_tensor(k);
-  p.v = rows_tensor(v);
-  p.out = rows_tensor(out);
-  const unsigned grid = rows_grid(a->batch * a->n_q_heads * a->n_queries);
-  if (a->dtype == VATTN_F16)
-    vattn::vattn_window_rows_kernel<__half><<<grid, vattn::kRowsWarps * 32, 0, stream>>>(p);
-  else
-    vattn::vattn_window_rows_kernel<__nv_bfloat16><<<grid, vattn::kRowsWarps * 32, 0, stream>>>(p);
-  return launched("attention kernel launch");
 }
 
 // Tensor map {dim, rows, heads, batch} of 16-bit rows with boxes of 64
@@ -542,6 +522,59 @@ vattn_status backward_window(const Tensor& tg, const Tensor& tq, const Tensor& t
     if ((st = launched("gradient join kernel launch")) != VATTN_OK) return st;
   }
   return ws.release();
+}
+
+template <typename T, int DP, int RW>
+vattn_status cached_launch(vattn::CachedParams p, int sms, int device, cudaStream_t stream) {
+  using P = vattn::CachedPlan<DP, RW>;
+  auto kernel = vattn::vattn_cached_kernel<T, DP, RW>;
+  static std::atomic<uint8_t> done[vattn::host::kMaxDevices];
+  vattn_status st = allow_smem(kernel, P::kSmemBytes, done, device);
+  if (st != VATTN_OK) return st;
+  const long long seqs = static_cast<long long>(p.w.batch) * p.w.kv_heads;
+  p.row_blocks = (p.rows + 16 * RW - 1) / (16 * RW);
+  if (p.row_blocks > 65535) return fail(VATTN_ERR_UNSUPPORTED, "too many query heads for one key head");
+  // shares of the keys: eight blocks a multiprocessor, none under 256 keys
+  const long long most_keys = std::min<long long>(p.w.n_keys, static_cast<long long>(p.w.sinks) + p.w.window + p.w.n_queries);
+  const long long blocks = seqs * p.row_blocks;
+  p.splits = static_cast<int>(std::max<long long>(1, std::min((8LL * sms + blocks - 1) / blocks, (most_keys + 255) / 256)));
+  Workspace ws;
+  if (p.splits > 1) {
+    const size_t rows = static_cast<size_t>(blocks) * p.splits * 16 * RW;
+    if ((st = ws.take(rows * (p.w.dim + 2) * 4, device, stream)) != VATTN_OK) return st;
+    p.part_o = reinterpret_cast<float*>(ws.data());
+    p.part_ml = p.part_o + rows * p.w.dim;
+  }
+  const dim3 grid(static_cast<unsigned>(p.splits), static_cast<unsigned>(p.row_blocks),
+                  static_cast<unsigned>(std::min<long long>(seqs, 65535)));
+  kernel<<<grid, vattn::kCachedThreads, P::kSmemBytes, stream>>>(p);
+  if ((st = launched("cached attention kernel launch")) != VATTN_OK) return st;
+  if (p.splits == 1) return VATTN_OK;
+  if ((seqs * p.rows + 3) / 4 > INT32_MAX) return fail(VATTN_ERR_UNSUPPORTED, "too many query rows");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((seqs * p.rows + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, vattn::vattn_cached_join_kernel<T, RW>, p);
+  if (e != cudaSuccess) return cuda_fail(e, "cached attention join kernel launch");
+  return ws.release();
+}
+
+template <typename T>
+vattn_status cached_dispatch(const vattn::CachedParams& p, int sms, int device, cudaStream_t stream) {
+  const int rw = p.rows <= 16 ? 1 : (p.rows <= 32 ? 2 : 4);
+  if (p.w.dim <= 64)
+    return rw == 1   ? cached_launch<T, 64, 1>(p, sms, device, stream)
+           : rw == 2 ? cached_launch<T, 64, 2>(p, sms, device, stream)
+                     : cached_launch<T, 64, 4>(p, sms, device, stream);
+  return rw == 1   ? cached_launch<T, 128, 1>(p, sms, device, stream)
+         : rw == 2 ? cached_launch<T, 128, 2>(p, sms, device, stream)
+                   : cached_launch<T, 128, 4>(p, sms, device, stream);
 }
 
 }  // namespace
@@ -775,7 +808,22 @@ vattn_status vattn_forward_cached(const vattn_rows* q, const vattn_rows* k, cons
   if (a->batch > 0 && !a->kv_len) return fail(VATTN_ERR_INVALID_ARG, "null kv_len");
   if ((st = forward_checks(q, k, v, out, nullptr, a)) != VATTN_OK) return st;
   if (a->batch * a->n_q_heads == 0 || a->n_queries == 0) return VATTN_OK;
-  return forward_rows(q, k, v, out, a, static_cast<cudaStream_t>(stream_ptr));
+  if (a->n_q_heads / a->n_kv_heads > INT32_MAX / VATTN_MAX_NEW_TOKENS / 2)
+    return fail(VATTN_ERR_UNSUPPORTED, "too many query heads for one key head");
+  int device = 0, sms = 0;
+  if ((st = current_device(&device)) != VATTN_OK) return st;
+  if ((st = vattn::host::sm_count(device, &sms)) != VATTN_OK) return st;
+  vattn::CachedParams p{};
+  p.w = window_params(a);
+  p.q = rows_tensor(q);
+  p.k = rows_tensor(k);
+  p.v = rows_tensor(v);
+  p.out = rows_tensor(out);
+  p.rows = p.w.group * p.w.n_queries;
+  p.scale_log2 = a->scale * vattn::kLog2E;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  return a->dtype == VATTN_F16 ? cached_dispatch<__half>(p, sms, device, stream)
+                               : cached_dispatch<__nv_bfloat16>(p, sms, device, stream);
 }
 
 }  // extern "C"

@@ -34,11 +34,6 @@ __device__ __forceinline__ Seq window_seq(const WindowParams& p, int b) {
   return s;
 }
 
-__device__ __forceinline__ bool window_sees(const WindowParams& p, const Seq& s, int i, int j) {
-  const int pos = s.start + i;
-  return j <= pos && pos < s.len && (j > pos - p.window || j < p.sinks);
-}
-
 // A tensor [batch, heads, rows, dim] with its first three strides.
 struct RowsTensor {
   const void* p;
