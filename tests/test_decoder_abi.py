@@ -30,12 +30,12 @@ def test_exports_every_declared_symbol(lib):
 
 def rows(i, heads=2, n=16, dim=64, off=0, strides=None):
     """vattn_rows of the i-th of some buffers 1 GB apart."""
-    return decoder._ROWS.pack(FAKE + i * G + off, *(strides or (heads * n * dim, n * dim, dim)))
+    return decoder._ROWS(FAKE + i * G + off, *(strides or (heads * n * dim, n * dim, dim)))
 
 
 def qk_args(batch=1, hq=2, hk=2, n=16, dim=64, rope=64, pos0=0, positions=0, factors=0, wq=0, wk=0, base=1e4,
             eps=1e-6, dtype=2, wdtype=0):
-    return decoder._QK.pack(batch, hq, hk, n, dim, rope, pos0, positions, factors, wq, wk, base, eps, dtype, wdtype)
+    return decoder._QK(batch, hq, hk, n, dim, rope, pos0, positions, factors, wq, wk, base, eps, dtype, wdtype)
 
 
 def qk(lib, args=None, q=None, k=None, qo=None, ko=None):
@@ -61,7 +61,7 @@ def test_qk_refuses_sizes_and_numbers(lib, kw, status):
 
 
 def test_qk_refuses_tensors(lib):
-    assert qk(lib, q=decoder._ROWS.pack(0, 1, 1, 1)) == 1
+    assert qk(lib, q=decoder._ROWS(0, 1, 1, 1)) == 1
     assert qk(lib, q=rows(0, off=1)) == 3
     assert qk(lib, qo=rows(0, off=64)) == 1                       # over q, not q itself
     assert qk(lib, qo=rows(1)) == 1 and qk(lib, ko=rows(0)) == 1  # over the other input
@@ -87,7 +87,7 @@ def test_empty_qk_is_a_no_op(lib):
 
 def win_args(batch=1, hq=4, hk=2, m=16, n=16, dim=64, window=0, sinks=0, kv_len=0, q_start=0, tree=0, scale=1.0,
              dtype=1):
-    return decoder._WINDOW.pack(batch, hq, hk, m, n, dim, window, sinks, kv_len, q_start, tree, scale, dtype)
+    return decoder._WINDOW(batch, hq, hk, m, n, dim, window, sinks, kv_len, q_start, tree, scale, dtype)
 
 
 def window(lib, args=None, q=None, k=None, v=None, out=None, lse=0):
@@ -133,7 +133,7 @@ def test_attention_refuses_what_belongs_to_another_call(lib):
 
 
 def test_attention_refuses_tensors(lib):
-    null = decoder._ROWS.pack(0, 1024, 1024, 64)
+    null = decoder._ROWS(0, 1024, 1024, 64)
     for call in (window, cached):
         assert call(lib, q=null) == 1 and call(lib, v=null) == 1 and call(lib, out=null) == 1
         assert call(lib, q=rows(0, 4, off=8)) == 3                       # not on 16 bytes

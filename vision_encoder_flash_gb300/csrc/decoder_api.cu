@@ -347,11 +347,13 @@ vattn_status forward_checks(const vattn_rows* q, const vattn_rows* k, const vatt
   return VATTN_OK;
 }
 
-// Tensor map {dim, rows, heads, batch} of 16-bit rows with boxes of 64
-// columns x `box_rows` rows, 128-byte swizzle; what is outside reads 0.  A
+// Tensor map {dim, rows, heads, batch} of 16-bit rows with boxes of
+// `box_cols` columns (64: 128-byte swizzle, 32: 64-byte) x `box_rows` rows;
+// what is outside reads 0 and is not written.  A
 // head or batch dimension of stride 0 (or size 1) becomes a single one, and
 // *mul zeroes its coordinate.
-vattn_status make_rows_map(CUtensorMap* tm, vattn::MapMul* mul, const Tensor& x, int32_t dtype, int box_rows) {
+vattn_status make_rows_map(CUtensorMap* tm, vattn::MapMul* mul, const Tensor& x, int32_t dtype, int box_rows,
+                           int box_cols = 64) {
   vattn::host::EncodeTiledFn enc = nullptr;
   const vattn_status st = vattn::host::tensor_map_encoder(&enc);
   if (st != VATTN_OK) return st;
@@ -365,12 +367,12 @@ vattn_status make_rows_map(CUtensorMap* tm, vattn::MapMul* mul, const Tensor& x,
   const cuuint64_t strides[3] = {x.size[2] <= 1 ? row : static_cast<cuuint64_t>(x.t->stride[2]) * 2u,
                                  one_h ? row : static_cast<cuuint64_t>(x.t->stride[1]) * 2u,
                                  one_b ? row : static_cast<cuuint64_t>(x.t->stride[0]) * 2u};
-  const cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(box_rows), 1u, 1u};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1u, 1u};
   const cuuint32_t steps[4] = {1u, 1u, 1u, 1u};
   const CUresult r = enc(tm, dtype == VATTN_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                          4, x.t->data, dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                         box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
     return fail(VATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed with CUresult %d", static_cast<int>(r));
   return VATTN_OK;
@@ -387,7 +389,7 @@ vattn_status allow_smem(K kernel, int bytes, std::atomic<uint8_t>* done, int dev
 }
 
 template <typename T, int NKB>
-vattn_status window_fwd_launch(const CUtensorMap (&tm)[3], const vattn::WindowFwdParams& p, int sms, int device,
+vattn_status window_fwd_launch(const CUtensorMap (&tm)[4], const vattn::WindowFwdParams& p, int sms, int device,
                                cudaStream_t stream) {
   using P = vattn::WindowFwdPlan<NKB>;
   auto kernel = vattn::vattn_window_fwd_kernel<T, NKB>;
@@ -395,7 +397,7 @@ vattn_status window_fwd_launch(const CUtensorMap (&tm)[3], const vattn::WindowFw
   const vattn_status st = allow_smem(kernel, P::kSmemBytes, done, device);
   if (st != VATTN_OK) return st;
   const unsigned grid = static_cast<unsigned>(std::min<long long>(p.items, sms));
-  kernel<<<grid, P::kThreads, P::kSmemBytes, stream>>>(tm[0], tm[1], tm[2], p);
+  kernel<<<grid, P::kThreads, P::kSmemBytes, stream>>>(tm[0], tm[1], tm[2], tm[3], p);
   return launched("window attention kernel launch");
 }
 
@@ -418,8 +420,9 @@ vattn_status forward_window(const vattn_rows* q, const vattn_rows* k, const vatt
   p.pairs = (static_cast<long long>(p.row_blocks) * p.w.group + 1) / 2;
   p.items = p.pairs * p.w.batch * p.w.kv_heads;
   p.scale_log2 = a->scale * vattn::kLog2E;
-  CUtensorMap tm[3];
-  if ((st = make_rows_map(&tm[0], &p.mq, window_tensor("q", q, a, true, false), a->dtype, vattn::kTile)) != VATTN_OK)
+  CUtensorMap tm[4];
+  if ((st = make_rows_map(&tm[0], &p.mq, window_tensor("q", q, a, true, false), a->dtype, vattn::kTile)) != VATTN_OK ||
+      (st = make_rows_map(&tm[3], &p.mo, window_tensor("out", out, a, true, true), a->dtype, 32, 32)) != VATTN_OK)
     return st;
   if (a->n_keys == 0) {  // no key tile is ever loaded: any valid map does
     tm[1] = tm[2] = tm[0];

@@ -13,13 +13,17 @@
 //   warp 0   K and V tiles by TMA into a ring (K0 V0 K1 V1 ...)
 //   warp 2   the item's two Q tiles by TMA
 //   warp 1   issues S_t = Q_t K^T and O_t += P_t V (tcgen05.mma, TMEM
-//            accumulators): P0 V, next S0, P1 V, next S1, so that one unit's
-//            softmax runs while the tensor core works for the other
+//            accumulators) from one thread, so they run in order; its loops
+//            are unrolled with the descriptors as 32-bit halves: 65 cycles a
+//            128 x 128 x 16 product, the tensor core's rate, where a rolled
+//            loop took 100 to 130
 //   warps 4-7, 8-11   online softmax of unit 0, 1: thread = query row
 //
-// TMEM (512 columns): S_t at 128 t, O_t at 256 + 128 t.  P_t (16-bit)
-// overwrites S_t once it is in registers; one thread issues all MMAs, which
-// run in order, so S_t of the next tile follows the P_t V that reads P_t.
+// TMEM (512 columns).  head_dim <= 64: S_t at 128 t, P_t at 256 + 64 t, O_t at
+// 384 + 64 t; the next S_t is issued as soon as this one is in registers.
+// Above: S_t at 128 t, O_t at 256 + 128 t, and P_t (16-bit) overwrites S_t; the
+// next S_t is issued behind the P_t V that reads P_t, and one unit's softmax
+// runs while the tensor core works for the other.
 //
 // Statistics and accumulators are f32.  The weights are rounded to the
 // tensors' type for the second product (relative 2^-9 / 2^-12 at most, the
@@ -41,7 +45,7 @@ struct WindowFwdParams {
   RowsTensor q, k, v, out;
   float* lse;
   uint32_t* status;
-  MapMul mq, mk, mv;
+  MapMul mq, mk, mv, mo;
   int row_blocks;      // ceil(n_queries / 128)
   long long pairs;     // items of one (batch, key head)
   long long items;
@@ -110,12 +114,17 @@ __device__ __forceinline__ WindowItem window_item(const WindowFwdParams& p, long
 template <int NKB>
 struct WindowFwdPlan {
   static constexpr int kTileBytes = NKB * kBlockBytes;
-  static constexpr int kStages = NKB == 1 ? 8 : 4;
+  static constexpr int kStages = NKB == 1 ? 8 : 4;  // K and V tiles
   static constexpr int kOffQ = 0;
   static constexpr int kOffKv = 2 * kTileBytes;
-  static constexpr int kOffBar = kOffKv + kStages * kTileBytes;
+  // results: two buffers a softmax warp of 32 rows x 32 elements (64-byte swizzle)
+  static constexpr int kOffOut = kOffKv + kStages * kTileBytes;
+  static constexpr int kOffBar = kOffOut + 8 * 4096;
   static constexpr int kSmemBytes = kOffBar + 256 + 1024;  // + alignment slack
   static constexpr int kThreads = 384;
+  static constexpr bool kOwnP = NKB == 1;  // P has TMEM columns of its own
+  static constexpr uint32_t kColP = kOwnP ? 256 : 0, kStrideP = kOwnP ? 64 : 128;
+  static constexpr uint32_t kColO = kOwnP ? 384 : 256, kStrideO = kOwnP ? 64 : 128;
   // registers: 72 + 2 x 216 a thread = 3 x 168, what the launch has
   static constexpr uint32_t kRegsOther = 72, kRegsSoftmax = 216;
   static_assert(kSmemBytes <= 232448, "shared memory");
@@ -123,7 +132,7 @@ struct WindowFwdPlan {
 
 enum WindowBar : int {
   kWbQFull = 0, kWbQEmpty = 1, kWbKvFull = 2, kWbKvEmpty = 10, kWbSFull = 18, kWbPFull = 20,
-  kWbOFull = 22, kWbMmaDone = 24, kWbCount = 25,
+  kWbPvDone = 22, kWbSFree = 24, kWbMmaDone = 26, kWbCount = 27,
 };
 
 // Row `row` of the call once more, over the keys that it sees alone (one
@@ -164,6 +173,7 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
     vattn_window_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                             const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_v,
+                            const __grid_constant__ CUtensorMap tm_o,
                             const __grid_constant__ WindowFwdParams p) {
   using P = WindowFwdPlan<NKB>;
   constexpr int S = P::kStages;
@@ -188,7 +198,8 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
     for (int t = 0; t < 2; ++t) {
       ptx::mbar_init(bar(kWbSFull + t), 1);
       ptx::mbar_init(bar(kWbPFull + t), 4);
-      ptx::mbar_init(bar(kWbOFull + t), 1);
+      ptx::mbar_init(bar(kWbPvDone + t), 1);
+      ptx::mbar_init(bar(kWbSFree + t), 4);
     }
     ptx::mbar_init(bar(kWbMmaDone), 1);
     *abort_flag = 0;
@@ -196,6 +207,7 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
     ptx::prefetch_tensormap(&tm_q);
     ptx::prefetch_tensormap(&tm_k);
     ptx::prefetch_tensormap(&tm_v);
+    ptx::prefetch_tensormap(&tm_o);
   }
   if (warp == 1) {
     ptx::tmem_alloc(ptx::smem_addr(const_cast<uint32_t*>(tmem_slot)), 512);
@@ -251,42 +263,59 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
       if (n_q > 0) pipe.drain(bar(kWbQFull), (n_q - 1) & 1u, kSiteWinDrain);
     } else if (warp == 1) {
       // ------------------------------------------------------ MMA issue
-      // The whole warp walks and waits; lane 0 issues.
+      // The whole warp walks and waits; one elected lane issues.
       const int ksteps = (p.w.dim + 15) >> 4;
       const uint32_t idesc_s = ptx::idesc_16bit_f32(kTile, kTile, false, Elem<T>::kBf16);
       const uint32_t idesc_o = ptx::idesc_16bit_f32(kTile, static_cast<uint32_t>(ksteps) * 16u, true, Elem<T>::kBf16);
       constexpr uint32_t hi = ptx::smem_desc_hi(1024, ptx::kSwizzle128B);
-      auto stage = [&](long long c) -> uint32_t {
-        return base_s + P::kOffKv + static_cast<uint32_t>(c % S) * P::kTileBytes;
-      };
+      const uint32_t q_lo = ptx::smem_desc_lo(base_s + P::kOffQ, 16);
+      const uint32_t k_lo = ptx::smem_desc_lo(base_s + P::kOffKv, 16);
+      const uint32_t v_lo = ptx::smem_desc_lo(base_s + P::kOffKv, kBlockBytes);
       auto wait_kv = [&](long long c) -> bool {
         return pipe.wait_warp(bar(kWbKvFull + static_cast<int>(c % S)), static_cast<uint32_t>((c / S) & 1), kSiteWinMma);
       };
-      auto issue_s = [&](int t, long long c) {
-        if (lane == 0) {
-          const uint32_t q = ptx::smem_desc_lo(base_s + P::kOffQ + t * P::kTileBytes, 16);
-          const uint32_t k = ptx::smem_desc_lo(stage(c), 16);
-          for (int ks = 0; ks < ksteps; ++ks) {
-            const uint32_t off = static_cast<uint32_t>((ks >> 2) * kBlockBytes + (ks & 3) * 32) >> 4;
-            ptx::mma_ss(tmem + t * 128u, ptx::smem_desc_join(q + off, hi), ptx::smem_desc_join(k + off, hi),
-                        idesc_s, ks > 0);
+      auto commit = [&](int b) {
+        if (ptx::elect_one()) ptx::mma_commit(bar(b));
+      };
+      uint32_t n_q = 0, n_s[2] = {0, 0}, n_p[2] = {0, 0};
+      // S_t of ring entry c; with P of its own, once the softmax has read the last S_t
+      auto issue_s = [&](int t, long long c) -> bool {
+        if (P::kOwnP && n_s[t] > 0) {
+          if (!pipe.wait_warp(bar(kWbSFree + t), (n_s[t] - 1) & 1u, kSiteWinMma)) return false;
+          ptx::tc_fence_after();
+        }
+        ++n_s[t];
+        const uint32_t q = q_lo + t * (P::kTileBytes >> 4);
+        const uint32_t k = k_lo + static_cast<uint32_t>(c % S) * (P::kTileBytes >> 4);
+        if (ptx::elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < 4 * NKB; ++ks) {
+            constexpr int kStep = 32 >> 4, kBlock = kBlockBytes >> 4;
+            const uint32_t off = (ks >> 2) * kBlock + (ks & 3) * kStep;
+            if (ks < ksteps)
+              ptx::mma_ss(tmem + t * 128u, ptx::smem_desc_join(q + off, hi), ptx::smem_desc_join(k + off, hi),
+                          idesc_s, ks > 0);
           }
           ptx::mma_commit(bar(kWbSFull + t));
         }
+        return true;
       };
-      auto issue_o = [&](int t, long long c, bool first) {
-        if (lane == 0) {
-          const uint32_t v = ptx::smem_desc_lo(stage(c), kBlockBytes);
+      // O_t += P_t V of ring entry c, once P_t is written
+      auto issue_o = [&](int t, long long c, bool first) -> bool {
+        if (!pipe.wait_warp(bar(kWbPFull + t), n_p[t] & 1u, kSiteWinMma)) return false;
+        ++n_p[t];
+        ptx::tc_fence_after();
+        const uint32_t v = v_lo + static_cast<uint32_t>(c % S) * (P::kTileBytes >> 4);
+        if (ptx::elect_one()) {
+#pragma unroll
           for (int ks = 0; ks < kTile / 16; ++ks)
-            ptx::mma_ts(tmem + 256u + t * 128u, tmem + t * 128u + ks * 8u,
+            ptx::mma_ts(tmem + P::kColO + t * P::kStrideO, tmem + P::kColP + t * P::kStrideP + ks * 8u,
                         ptx::smem_desc_join(v + ks * (2048u >> 4), hi), idesc_o, !first || ks > 0);
+          ptx::mma_commit(bar(kWbPvDone + t));
         }
-      };
-      auto commit = [&](int b) {
-        if (lane == 0) ptx::mma_commit(bar(b));
+        return true;
       };
       long long g = 0;  // key tiles of this block so far; K of tile g is ring entry 2 g, V 2 g + 1
-      uint32_t n_q = 0, n_p[2] = {0, 0};
       bool ok = true;
       for (long long item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
         const WindowItem it = window_item(p, item);
@@ -294,19 +323,27 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
         if (!(ok = pipe.wait_warp(bar(kWbQFull), n_q & 1u, kSiteWinMma))) break;
         ++n_q;
         if (!(ok = wait_kv(2 * g))) break;
-        ptx::tc_fence_after();
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-          if (it.u[t].uses(it.tile(0))) issue_s(t, 2 * g);
+          if (ok && it.u[t].uses(it.tile(0))) ok = issue_s(t, 2 * g);
         commit(kWbKvEmpty + static_cast<int>((2 * g) % S));
         if (it.n == 1) commit(kWbQEmpty);
         bool begun[2] = {false, false};
         for (int x = 0; ok && x < it.n; ++x, ++g) {
           const int j = it.tile(x), jn = x + 1 < it.n ? it.tile(x + 1) : -1;
+          if (P::kOwnP && jn >= 0) {
+            if (!(ok = wait_kv(2 * g + 2))) break;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+              if (ok && it.u[t].uses(jn)) ok = issue_s(t, 2 * g + 2);
+            if (!ok) break;
+            commit(kWbKvEmpty + static_cast<int>((2 * g + 2) % S));
+            if (x + 2 == it.n) commit(kWbQEmpty);
+          }
           if (!(ok = wait_kv(2 * g + 1))) break;
           const int left = it.s.len - j * kTile;  // V rows of the sequence in this tile
           if (left < kTile && it.s.len < p.w.n_keys) {
-            const uint32_t v = stage(2 * g + 1);
+            const uint32_t v = base_s + P::kOffKv + static_cast<uint32_t>((2 * g + 1) % S) * P::kTileBytes;
             for (int kb = 0; kb < NKB; ++kb)
               for (int i = left * 8 + lane; i < kTile * 8; i += 32)
                 ptx::st_shared_v4(v + kb * kBlockBytes + i * 16, 0.0f, 0.0f, 0.0f, 0.0f);
@@ -315,23 +352,19 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
           }
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            if (it.u[t].uses(j)) {
-              if (!(ok = pipe.wait_warp(bar(kWbPFull + t), n_p[t] & 1u, kSiteWinMma))) break;
-              ++n_p[t];
-              ptx::tc_fence_after();
-              issue_o(t, 2 * g + 1, !begun[t]);
+            if (ok && it.u[t].uses(j)) {
+              ok = issue_o(t, 2 * g + 1, !begun[t]);
               begun[t] = true;
-              if (j == it.u[t].b) commit(kWbOFull + t);
             }
-            if (jn >= 0) {
-              if (t == 0 && !(ok = wait_kv(2 * g + 2))) break;
-              if (it.u[t].uses(jn)) issue_s(t, 2 * g + 2);
+            if (!P::kOwnP && ok && jn >= 0) {
+              if (t == 0) ok = wait_kv(2 * g + 2);
+              if (ok && it.u[t].uses(jn)) ok = issue_s(t, 2 * g + 2);
             }
           }
           if (!ok) break;
           commit(kWbKvEmpty + static_cast<int>((2 * g + 1) % S));
-          if (jn >= 0) commit(kWbKvEmpty + static_cast<int>((2 * g + 2) % S));
-          if (x + 2 == it.n) commit(kWbQEmpty);
+          if (!P::kOwnP && jn >= 0) commit(kWbKvEmpty + static_cast<int>((2 * g + 2) % S));
+          if (!P::kOwnP && x + 2 == it.n) commit(kWbQEmpty);
         }
       }
       commit(kWbMmaDone);
@@ -342,15 +375,21 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
     const int t = (warp - 4) >> 2;
     const int r = (warp & 3) * 32 + lane;  // row of the unit
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t s_addr = tmem + lanes + t * 128u, o_addr = s_addr + 256u;
+    const uint32_t s_addr = tmem + lanes + t * 128u;
+    const uint32_t p_addr = tmem + lanes + P::kColP + t * P::kStrideP;
+    const uint32_t o_addr = tmem + lanes + P::kColO + t * P::kStrideO;
+    const uint32_t stage_out = base_s + P::kOffOut + static_cast<uint32_t>(warp - 4) * 4096u;
+    const uint64_t once = ptx::policy_evict_first();
     const int D = p.w.dim, W = p.w.window;
-    uint32_t n_s = 0, n_o = 0;
+    uint32_t n_s = 0;  // tiles of this unit so far
+    int n_out = 0;     // result boxes of this warp so far
     bool ok = true;
     for (long long item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
       const WindowItem it = window_item(p, item);
-      if (!it.on[t]) continue;
-      const UnitRange u = it.u[t];
-      const int p0 = it.s.start + it.row0[t], pos = p0 + r;
+      if (!(t == 0 ? it.on[0] : it.on[1])) continue;
+      const UnitRange u = t == 0 ? it.u[0] : it.u[1];
+      const int row0 = t == 0 ? it.row0[0] : it.row0[1], head = t == 0 ? it.head[0] : it.head[1];
+      const int p0 = it.s.start + row0, pos = p0 + r;
       const bool row_on = pos >= 0 && pos < it.s.len;
       float m = -INFINITY, l = 0.0f;  // m: running maximum in log2 units, may lag by < 8
       bool begun = false;
@@ -358,13 +397,16 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
         const int j = it.tile(x);
         if (!u.uses(j)) continue;
         if (!(ok = pipe.wait_warp(bar(kWbSFull + t), n_s & 1u, kSiteWinSoft))) break;
-        ++n_s;
         ptx::tc_fence_after();
         uint32_t s[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) ptx::tmem_ld_32x32b_x32(s_addr + c * 32, s[c]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) ptx::tmem_wait_ld_dep(s[c]);
+        if (P::kOwnP) {
+          ptx::tc_fence_before();
+          pipe_warp_arrive(bar(kWbSFree + t));
+        }
         const int k0 = j * kTile;
         // every row of the unit sees every key of the tile?
         const bool full = p0 >= k0 + kTile - 1 && p0 + kTile <= it.s.len &&
@@ -374,6 +416,7 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const uint32_t see = bits_upto(c_hi, c) & (~bits_upto(c_lo, c) | bits_upto(c_sink, c));
+            if (__all_sync(0xffffffffu, see == 0xffffffffu)) continue;
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (!((see >> e) & 1u)) s[c][e] = 0xff800000u;
@@ -407,7 +450,12 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
           }
         const float2 s01 = __fadd2_rn(acc[0], acc[1]), s23 = __fadd2_rn(acc[2], acc[3]);
         l = fmaf(l, alpha, (s01.x + s01.y) + (s23.x + s23.y));
-        // S of this tile follows the unit's previous P V in issue order, so O is stable
+        // P free and O stable: with P over S, S of this tile follows the unit's
+        // previous P V in issue order; else that product has to be awaited
+        if (P::kOwnP && begun) {
+          if (!(ok = pipe.wait_warp(bar(kWbPvDone + t), (n_s - 1) & 1u, kSiteWinSoft))) break;
+          ptx::tc_fence_after();
+        }
         if (begun && __any_sync(0xffffffffu, grew)) {
           for (int c = 0; c < D; c += 16) {
             uint32_t y[16];
@@ -419,58 +467,72 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
           }
         }
         begun = true;
+        ++n_s;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          ptx::tmem_st_32x32b_x16(s_addr + c * 16, *reinterpret_cast<uint32_t(*)[16]>(s[c]));
+          ptx::tmem_st_32x32b_x16(p_addr + c * 16, *reinterpret_cast<uint32_t(*)[16]>(s[c]));
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         pipe_warp_arrive(bar(kWbPFull + t));
       }
       if (!ok) break;
       // ------------------------------------------------- out = O / l, lse
-      const int row = it.row0[t] + r;
-      const bool store = row < p.w.n_queries;
-      T* out = store ? rows_at_mut<T>(p.out, it.b, it.head[t], row) : nullptr;
-      if (u.empty()) {
-        if (store)
-          for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4*>(out + d) = make_uint4(0, 0, 0, 0);
-      } else {
-        if (!(ok = pipe.wait_warp(bar(kWbOFull + t), n_o & 1u, kSiteWinOut))) break;
-        ++n_o;
+      // 32 columns at a time: TMEM, registers, a swizzled buffer, one TMA
+      // store of the warp's rows (rows >= n_queries and columns >= head_dim
+      // are not written), which completes behind the next item's work
+      if (!u.empty()) {
+        if (!(ok = pipe.wait_warp(bar(kWbPvDone + t), (n_s - 1) & 1u, kSiteWinOut))) break;
         ptx::tc_fence_after();
-        const float inv = 1.0f / l;
-        float check = 0.0f;  // NaN once an element is not finite
-        for (int c = 0; c < D; c += 16) {
-          uint32_t y[16];
-          ptx::tmem_ld_32x32b_x16(o_addr + c, y);
-          ptx::tmem_wait_ld_dep16(y);
-          uint32_t h[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float a = l == 0.0f ? 0.0f : __uint_as_float(y[2 * e]) * inv;
-            const float b = l == 0.0f ? 0.0f : __uint_as_float(y[2 * e + 1]) * inv;
-            check = fmaf(a, 0.0f, fmaf(b, 0.0f, check));
-            h[e] = pack2<T>(a, b);
-          }
-          if (store) {
-            *reinterpret_cast<uint4*>(out + c) = make_uint4(h[0], h[1], h[2], h[3]);
-            if (c + 8 < D) *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(h[4], h[5], h[6], h[7]);
-          }
+      }
+      const float inv = 1.0f / l;
+      float check = 0.0f;  // NaN once an element is not finite
+      for (int c = 0; c < D; c += 32) {
+        uint32_t y[32];
+        if (!u.empty()) {
+          ptx::tmem_ld_32x32b_x32(o_addr + c, y);
+          ptx::tmem_wait_ld_dep(y);
         }
-        // finite weights, but not the result: see window_row_again
-        uint32_t again = __ballot_sync(0xffffffffu, store && row_on && check != 0.0f && l - l == 0.0f);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float a = l == 0.0f ? 0.0f : __uint_as_float(y[2 * e]) * inv;
+          const float b = l == 0.0f ? 0.0f : __uint_as_float(y[2 * e + 1]) * inv;
+          if (c + 2 * e < D) check = fmaf(a, 0.0f, fmaf(b, 0.0f, check));
+          y[e] = pack2<T>(a, b);
+        }
+        const uint32_t buf = stage_out + static_cast<uint32_t>(n_out & 1) * 2048u;
+        if (lane == 0) ptx::bulk_wait_group_read<1>();  // the box before the last has left this buffer
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          ptx::st_shared_v4(buf + static_cast<uint32_t>(lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)),
+                            __uint_as_float(y[4 * k]), __uint_as_float(y[4 * k + 1]),
+                            __uint_as_float(y[4 * k + 2]), __uint_as_float(y[4 * k + 3]));
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::tma_store_4d_hint(&tm_o, buf, c, row0 + (warp & 3) * 32, head * p.mo.h, it.b * p.mo.b, once);
+          ptx::bulk_commit_group();
+        }
+        ++n_out;
+      }
+      ptx::tc_fence_before();
+      const int row = row0 + r;
+      // finite weights, but not the result: see window_row_again
+      uint32_t again = __ballot_sync(0xffffffffu, row < p.w.n_queries && row_on && check != 0.0f && l - l == 0.0f);
+      if (again != 0) {
+        if (lane == 0) ptx::bulk_wait_group_all();  // the rows as stored are there
         __syncwarp();
         for (; again != 0; again &= again - 1) {
           const int src = __ffs(again) - 1;
-          window_row_again<T>(p, it.s, it.b, it.head[t], __shfl_sync(0xffffffffu, row, src),
+          window_row_again<T>(p, it.s, it.b, head, __shfl_sync(0xffffffffu, row, src),
                               __shfl_sync(0xffffffffu, m, src), __shfl_sync(0xffffffffu, l, src));
         }
-        ptx::tc_fence_before();
       }
-      if (store && p.lse != nullptr)
-        p.lse[(static_cast<long long>(it.b) * p.w.heads + it.head[t]) * p.w.n_queries + row] =
+      if (row < p.w.n_queries && p.lse != nullptr)
+        p.lse[(static_cast<long long>(it.b) * p.w.heads + head) * p.w.n_queries + row] =
             l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
+    if (lane == 0) ptx::bulk_wait_group_all();  // before the block's shared memory goes
   }
 
   ptx::tc_fence_before();

@@ -12,13 +12,15 @@ inputs must be ready on it.  There is no CPU fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import struct
 
 from ._lib import _check, load_library
 
-_ROWS = struct.Struct("=4q")          # vattn_rows
-_QK = struct.Struct("=7q4Qdf2i4x")    # vattn_qk_args
-_WINDOW = struct.Struct("=8q3Qfi")    # vattn_window_args
+_ROWS = struct.Struct("=4q").pack          # vattn_rows
+_QK = struct.Struct("=7q4Qdf2i4x").pack    # vattn_qk_args
+_WINDOW = struct.Struct("=8q3Qfi").pack    # vattn_window_args
+_HERE = contextlib.nullcontext()
 
 _TORCH = None
 _DTYPES = {}
@@ -33,82 +35,75 @@ def _torch():
     return _TORCH
 
 
-def _tensor(name, t, dtypes, device=None):
-    """Type, rank and device of a [batch, heads, rows, head_dim] tensor; its dtype code."""
-    torch = _TORCH
-    if not isinstance(t, torch.Tensor):
+def _tensor(name, t, dtypes):
+    """Type and rank of a [batch, heads, rows, head_dim] CUDA tensor: (dtype code, device index)."""
+    if not isinstance(t, _TORCH.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     code = _DTYPES.get(t.dtype, -1)
     if code not in dtypes:
         raise TypeError(f"{name} has unsupported dtype {t.dtype}")
     if t.dim() != 4:
         raise ValueError(f"{name} must be [batch, heads, rows, head_dim]")
-    if not t.is_cuda:
+    index = t.get_device()
+    if index < 0 or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}, is on {t.device}")
-    return code
+    return code, index
 
 
-def _like(name, t, ref, shape, code):
-    """t has ref's dtype and device, and the shape."""
-    if _tensor(name, t, (code,), ref.device) != code or t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, is {tuple(t.shape)}")
+def _like(name, t, ref, shape=None):
+    """t has ref's dtype and device, and the shape (default: ref's)."""
+    if not isinstance(t, _TORCH.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != ref.dtype:
+        raise TypeError(f"{name} must be {ref.dtype}, is {t.dtype}")
+    if t.get_device() != ref.get_device():
+        raise ValueError(f"{name} must be on {ref.device}, is on {t.device}")
+    if t.shape != (ref.shape if shape is None else shape):
+        raise ValueError(f"{name} must be {tuple(ref.shape if shape is None else shape)}, is {tuple(t.shape)}")
 
 
 def _rows(name, t):
     """vattn_rows of a tensor."""
-    s = t.stride()
-    if s[3] != 1 and t.shape[3] > 1 and t.numel() > 0:
+    b, h, i, d = t.stride()
+    if d != 1 and t.shape[3] > 1 and t.numel() > 0:
         raise ValueError(f"{name} must be contiguous in its last dimension")
-    return _ROWS.pack(t.data_ptr(), s[0], s[1], s[2])
+    return _ROWS(t.data_ptr(), b, h, i)
 
 
-def _ints(name, t, dtype, shape, device):
-    """Address of a contiguous integer tensor, 0 for None."""
+def _ints(name, t, dtype, shape, ref):
+    """Address of a contiguous integer tensor on ref's device, 0 for None."""
     if t is None:
         return 0
     if not isinstance(t, _TORCH.Tensor) or t.dtype != dtype:
         raise TypeError(f"{name} must be a {dtype} tensor")
-    if t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor on {device}")
+    if t.shape != shape or t.get_device() != ref.get_device() or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor on {ref.device}")
     return t.data_ptr()
 
 
-class _On:
-    """The device and stream of a call: makes the tensors' device current
-    where it is not, and a caller's own stream the one that allocates results
-    (so that their memory is not handed out while that stream still uses it)
-    and that the inputs are recorded on."""
-
-    def __init__(self, device, stream, inputs):
-        torch = _TORCH
-        if stream is None:
-            self.stream = torch.cuda.current_stream(device)
-            self.ctx = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-        else:
-            if stream.device != device:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-            self.stream = stream
-            self.ctx = torch.cuda.stream(stream)  # makes the stream's device current too
-            for t in inputs:
-                if t is not None:
-                    t.record_stream(stream)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.stream.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _on(index, stream, inputs):
+    """(stream handle, context) of a call on device `index`.  The context makes
+    the tensors' device current where it is not.  A stream of the caller's own
+    becomes the one that allocates results, so that their memory is not handed
+    out while that stream still uses it, and the inputs are recorded on it."""
+    torch = _TORCH
+    if stream is None:
+        # the handle without a Stream object around it: microseconds of a call
+        handle = torch._C._cuda_getCurrentRawStream(index)
+        return handle, _HERE if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
+    if stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+    for t in inputs:
+        if t is not None:
+            t.record_stream(stream)
+    return stream.cuda_stream, torch.cuda.stream(stream)
 
 
 def _qk_args(q, k, q_weight, k_weight, rope_dims, pos0, positions, base, factors, eps, code):
     torch = _TORCH
     B, H, N, D = q.shape
-    if k.shape[0] != B or k.shape[2] != N or k.shape[3] != D:
+    Bk, K, Nk, Dk = k.shape
+    if Bk != B or Nk != N or Dk != D:
         raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}")
     if rope_dims is None:
         rope_dims = D
@@ -118,7 +113,7 @@ def _qk_args(q, k, q_weight, k_weight, rope_dims, pos0, positions, base, factors
             continue
         if not isinstance(w, torch.Tensor) or w.dtype not in (torch.float32, q.dtype):
             raise TypeError(f"{name} must be a float32 or {q.dtype} tensor")
-        if w.shape != (D,) or w.device != q.device or not w.is_contiguous():
+        if w.shape != (D,) or w.get_device() != q.get_device() or not w.is_contiguous():
             raise ValueError(f"{name} must be a contiguous ({D},) tensor on {q.device}")
         wcode = _DTYPES[w.dtype]
     if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
@@ -127,13 +122,13 @@ def _qk_args(q, k, q_weight, k_weight, rope_dims, pos0, positions, base, factors
     if factors is not None:
         if not isinstance(factors, torch.Tensor) or factors.dtype != torch.float32:
             raise TypeError("factors must be a float32 tensor")
-        if factors.device != q.device or factors.numel() < rope_dims // 2 or not factors.is_contiguous():
+        if factors.get_device() != q.get_device() or factors.numel() < rope_dims // 2 or not factors.is_contiguous():
             raise ValueError("factors must hold rope_dims // 2 contiguous floats on the tensors' device")
         fptr = factors.data_ptr()
-    pptr = _ints("positions", positions, torch.int32, (B, N), q.device)
-    return _QK.pack(B, H, k.shape[1], N, D, rope_dims, pos0, pptr, fptr,
-                    0 if q_weight is None else q_weight.data_ptr(),
-                    0 if k_weight is None else k_weight.data_ptr(), base, eps, code, wcode)
+    pptr = _ints("positions", positions, torch.int32, (B, N), q)
+    return _QK(B, H, K, N, D, rope_dims, pos0, pptr, fptr,
+               0 if q_weight is None else q_weight.data_ptr(),
+               0 if k_weight is None else k_weight.data_ptr(), base, eps, code, wcode)
 
 
 def qk_norm_rope(q, k, q_weight=None, k_weight=None, rope_dims=None, pos0=0, positions=None,
@@ -148,18 +143,20 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, rope_dims=None, pos0=0, pos
     the angles.  ``q_out`` / ``k_out``: where the results go (new contiguous
     tensors by default; may be q / k themselves, or rows of a cache)."""
     torch = _torch()
-    code = _tensor("q", q, (0, 1, 2))
-    _tensor("k", k, (code,), q.device)
+    code, index = _tensor("q", q, (0, 1, 2))
+    if _tensor("k", k, (code,))[1] != index:
+        raise ValueError("q and k must be on one device")
     args = _qk_args(q, k, q_weight, k_weight, rope_dims, pos0, positions, base, factors, eps, code)
     if q_out is not None:
-        _like("q_out", q_out, q, q.shape, code)
+        _like("q_out", q_out, q)
     if k_out is not None:
-        _like("k_out", k_out, q, k.shape, code)
-    with _On(q.device, stream, (q, k, q_weight, k_weight, positions, factors, q_out, k_out)) as s:
+        _like("k_out", k_out, k)
+    s, ctx = _on(index, stream, (q, k, q_weight, k_weight, positions, factors, q_out, k_out))
+    with ctx:
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = q.new_empty(q.shape)
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+            k_out = k.new_empty(k.shape)
         _check(load_library().vattn_qk_norm_rope(_rows("q", q), _rows("k", k), _rows("q_out", q_out),
                                                  _rows("k_out", k_out), args, s))
     return q_out, k_out
@@ -173,23 +170,24 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight=None, k_weight=None, ro
     ``[D]`` (None for a weight that is None), summed in a fixed order.
     ``dq`` / ``dk``: where the results go (may be dq_out or q, dk_out or k)."""
     torch = _torch()
-    code = _tensor("q", q, (0, 1, 2))
-    _tensor("k", k, (code,), q.device)
+    code, index = _tensor("q", q, (0, 1, 2))
+    if _tensor("k", k, (code,))[1] != index:
+        raise ValueError("q and k must be on one device")
     args = _qk_args(q, k, q_weight, k_weight, rope_dims, pos0, positions, base, factors, eps, code)
-    _like("dq_out", dq_out, q, q.shape, code)
-    _like("dk_out", dk_out, q, k.shape, code)
+    _like("dq_out", dq_out, q)
+    _like("dk_out", dk_out, k)
     if dq is not None:
-        _like("dq", dq, q, q.shape, code)
+        _like("dq", dq, q)
     if dk is not None:
-        _like("dk", dk, q, k.shape, code)
-    with _On(q.device, stream,
-             (dq_out, dk_out, q, k, q_weight, k_weight, positions, factors, dq, dk)) as s:
+        _like("dk", dk, k)
+    s, ctx = _on(index, stream, (dq_out, dk_out, q, k, q_weight, k_weight, positions, factors, dq, dk))
+    with ctx:
         if dq is None:
-            dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            dq = q.new_empty(q.shape)
         if dk is None:
-            dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-        dwq = None if q_weight is None else torch.empty(q.shape[3], dtype=torch.float32, device=q.device)
-        dwk = None if k_weight is None else torch.empty(q.shape[3], dtype=torch.float32, device=q.device)
+            dk = k.new_empty(k.shape)
+        dwq = None if q_weight is None else q.new_empty(q.shape[3], dtype=torch.float32)
+        dwk = None if k_weight is None else q.new_empty(q.shape[3], dtype=torch.float32)
         _check(load_library().vattn_qk_norm_rope_backward(
             _rows("dq_out", dq_out), _rows("dk_out", dk_out), _rows("q", q), _rows("k", k), _rows("dq", dq),
             _rows("dk", dk), 0 if dwq is None else dwq.data_ptr(), 0 if dwk is None else dwk.data_ptr(),
@@ -197,22 +195,23 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight=None, k_weight=None, ro
     return dq, dk, dwq, dwk
 
 
-def _window_args(q, k, v, window, n_sinks, scale, kv_len, q_start, tree, code):
+def _window_args(q, k, v, window, n_sinks, scale, kv_len, q_start, tree):
+    """(device index, packed vattn_window_args)."""
     torch = _TORCH
-    _tensor("k", k, (code,), q.device)
-    _tensor("v", v, (code,), q.device)
+    code, index = _tensor("q", q, (1, 2))
+    if _tensor("k", k, (code,))[1] != index or _tensor("v", v, (code,))[1] != index:
+        raise ValueError("q, k and v must be on one device")
     B, H, M, D = q.shape
-    if k.shape != v.shape or k.shape[0] != B or k.shape[3] != D:
+    Bk, K, N, Dk = k.shape
+    if k.shape != v.shape or Bk != B or Dk != D:
         raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
     if window is None:
         window = 0
     elif window < 1:
         raise ValueError("window must be at least 1 (None: no limit)")
-    dev = q.device
-    return _WINDOW.pack(B, H, k.shape[1], M, k.shape[2], D, window, n_sinks,
-                        _ints("kv_len", kv_len, torch.int32, (B,), dev),
-                        _ints("q_start", q_start, torch.int32, (B,), dev),
-                        _ints("tree_mask", tree, torch.int64, (B, M), dev), scale, code)
+    return index, _WINDOW(B, H, K, M, N, D, window, n_sinks, _ints("kv_len", kv_len, torch.int32, (B,), q),
+                          _ints("q_start", q_start, torch.int32, (B,), q),
+                          _ints("tree_mask", tree, torch.int64, (B, M), q), scale, code)
 
 
 def forward_window(q, k, v, window=None, n_sinks=0, scale=1.0, kv_len=None, q_start=None, out=None,
@@ -229,14 +228,14 @@ def forward_window(q, k, v, window=None, n_sinks=0, scale=1.0, kv_len=None, q_st
     already scaled).  Returns ``out`` (q's dtype), with ``return_lse``
     ``(out, lse)``, lse f32 ``[B, Hq, M]`` for ``backward_window``."""
     torch = _torch()
-    code = _tensor("q", q, (1, 2))
-    args = _window_args(q, k, v, window, n_sinks, scale, kv_len, q_start, None, code)
+    index, args = _window_args(q, k, v, window, n_sinks, scale, kv_len, q_start, None)
     if out is not None:
-        _like("out", out, q, q.shape, code)
-    with _On(q.device, stream, (q, k, v, kv_len, q_start, out)) as s:
+        _like("out", out, q)
+    s, ctx = _on(index, stream, (q, k, v, kv_len, q_start, out))
+    with ctx:
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device) if return_lse else None
+            out = q.new_empty(q.shape)
+        lse = q.new_empty(q.shape[:3], dtype=torch.float32) if return_lse else None
         _check(load_library().vattn_forward_window(_rows("q", q), _rows("k", k), _rows("v", v),
                                                    _rows("out", out), lse.data_ptr() if return_lse else 0,
                                                    args, s))
@@ -249,24 +248,24 @@ def backward_window(dout, q, k, v, out, lse, window=None, n_sinks=0, scale=1.0, 
     inputs, its ``out`` and its ``lse``.  dk and dv are summed over the query
     heads that share a key head; the same call gives the same bits."""
     torch = _torch()
-    code = _tensor("q", q, (1, 2))
-    args = _window_args(q, k, v, window, n_sinks, scale, kv_len, q_start, None, code)
-    _like("dout", dout, q, q.shape, code)
-    _like("out", out, q, q.shape, code)
+    index, args = _window_args(q, k, v, window, n_sinks, scale, kv_len, q_start, None)
+    _like("dout", dout, q)
+    _like("out", out, q)
     if not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32:
         raise TypeError("lse must be a float32 tensor")
-    if lse.shape != q.shape[:3] or lse.device != q.device or not lse.is_contiguous():
+    if lse.shape != q.shape[:3] or lse.get_device() != index or not lse.is_contiguous():
         raise ValueError(f"lse must be a contiguous {tuple(q.shape[:3])} tensor on {q.device}")
     for name, t, ref in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
         if t is not None:
-            _like(name, t, q, ref.shape, code)
-    with _On(q.device, stream, (dout, q, k, v, out, lse, kv_len, q_start, dq, dk, dv)) as s:
+            _like(name, t, ref)
+    s, ctx = _on(index, stream, (dout, q, k, v, out, lse, kv_len, q_start, dq, dk, dv))
+    with ctx:
         if dq is None:
-            dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            dq = q.new_empty(q.shape)
         if dk is None:
-            dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+            dk = k.new_empty(k.shape)
         if dv is None:
-            dv = torch.empty(v.shape, dtype=q.dtype, device=q.device)
+            dv = v.new_empty(v.shape)
         _check(load_library().vattn_backward_window(
             _rows("dout", dout), _rows("q", q), _rows("k", k), _rows("v", v), _rows("out", out),
             lse.data_ptr(), _rows("dq", dq), _rows("dk", dk), _rows("dv", dv), args, s))
@@ -283,16 +282,16 @@ def forward_cached(q, k_cache, v_cache, kv_len, tree_mask=None, window=None, n_s
     an ancestor of t or t itself; a token's position is that of the first new
     token plus the number of its ancestors.  None: the new tokens follow each
     other.  Window, first keys and scale as in ``forward_window``."""
-    torch = _torch()
-    code = _tensor("q", q, (1, 2))
+    _torch()
     if kv_len is None:
         raise TypeError("kv_len must be an int32 tensor")
-    args = _window_args(q, k_cache, v_cache, window, n_sinks, scale, kv_len, None, tree_mask, code)
+    index, args = _window_args(q, k_cache, v_cache, window, n_sinks, scale, kv_len, None, tree_mask)
     if out is not None:
-        _like("out", out, q, q.shape, code)
-    with _On(q.device, stream, (q, k_cache, v_cache, kv_len, tree_mask, out)) as s:
+        _like("out", out, q)
+    s, ctx = _on(index, stream, (q, k_cache, v_cache, kv_len, tree_mask, out))
+    with ctx:
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out = q.new_empty(q.shape)
         _check(load_library().vattn_forward_cached(_rows("q", q), _rows("k_cache", k_cache),
                                                    _rows("v_cache", v_cache), _rows("out", out), args, s))
     return out
