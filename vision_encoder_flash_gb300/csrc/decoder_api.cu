@@ -396,7 +396,7 @@ vattn_status window_fwd_launch(const CUtensorMap (&tm)[4], const vattn::WindowFw
   static std::atomic<uint8_t> done[vattn::host::kMaxDevices];
   const vattn_status st = allow_smem(kernel, P::kSmemBytes, done, device);
   if (st != VATTN_OK) return st;
-  const unsigned grid = static_cast<unsigned>(std::min<long long>(p.items, sms));
+  const unsigned grid = static_cast<unsigned>(std::min(p.items, sms));
   kernel<<<grid, P::kThreads, P::kSmemBytes, stream>>>(tm[0], tm[1], tm[2], tm[3], p);
   return launched("window attention kernel launch");
 }
@@ -416,9 +416,15 @@ vattn_status forward_window(const vattn_rows* q, const vattn_rows* k, const vatt
   p.out = rows_tensor(out);
   p.lse = lse;
   if ((st = vattn::host::status_word(device, &p.status)) != VATTN_OK) return st;
-  p.row_blocks = static_cast<int>((a->n_queries + vattn::kTile - 1) / vattn::kTile);
-  p.pairs = (static_cast<long long>(p.row_blocks) * p.w.group + 1) / 2;
-  p.items = p.pairs * p.w.batch * p.w.kv_heads;
+  const int64_t units = (a->n_queries + vattn::kTile - 1) / vattn::kTile * p.w.group;
+  const int64_t seqs = a->batch * a->n_kv_heads;
+  if ((units + 1) / 2 > kMaxKeys / seqs) return fail(VATTN_ERR_UNSUPPORTED, "too many tiles of 128 rows");
+  p.units = static_cast<int>(units);
+  p.pairs = static_cast<int>((units + 1) / 2);
+  p.items = static_cast<int>(p.pairs * seqs);
+  p.seqs = vattn::FastDiv::make(static_cast<uint32_t>(seqs));
+  p.kv_heads = vattn::FastDiv::make(static_cast<uint32_t>(p.w.kv_heads));
+  p.group = vattn::FastDiv::make(static_cast<uint32_t>(p.w.group));
   p.scale_log2 = a->scale * vattn::kLog2E;
   CUtensorMap tm[4];
   if ((st = make_rows_map(&tm[0], &p.mq, window_tensor("q", q, a, true, false), a->dtype, vattn::kTile)) != VATTN_OK ||
@@ -437,19 +443,6 @@ vattn_status forward_window(const vattn_rows* q, const vattn_rows* k, const vatt
                            : window_fwd_launch<__nv_bfloat16, 2>(tm, p, sms, device, stream);
 }
 
-template <typename T, int NKB, bool kKeys>
-vattn_status grad_launch(const CUtensorMap& x1, const CUtensorMap& x2, const CUtensorMap& y1, const CUtensorMap& y2,
-                         const vattn::WindowGradParams& p, long long blocks, int device, cudaStream_t stream) {
-  using P = vattn::GradPlan<NKB>;
-  auto kernel = vattn::vattn_window_bwd_kernel<T, NKB, kKeys>;
-  static std::atomic<uint8_t> done[vattn::host::kMaxDevices];
-  const vattn_status st = allow_smem(kernel, P::kSmemBytes, done, device);
-  if (st != VATTN_OK) return st;
-  if (blocks > INT32_MAX) return fail(VATTN_ERR_UNSUPPORTED, "too many tiles of 128 rows");
-  kernel<<<static_cast<unsigned>(blocks), P::kThreads, P::kSmemBytes, stream>>>(x1, x2, y1, y2, p);
-  return launched("gradient kernel launch");
-}
-
 // The three gradients (checks passed; queries or keys may be none).
 template <typename T, int NKB>
 vattn_status backward_window(const Tensor& tg, const Tensor& tq, const Tensor& tk, const Tensor& tv,
@@ -462,19 +455,36 @@ vattn_status backward_window(const Tensor& tg, const Tensor& tq, const Tensor& t
   p.stat_tiles = 2 * row_tiles;
   p.key_tiles = (p.w.n_keys + kTile - 1) / kTile;
   // Items (query tiles of all heads of the group) of an ordinary key tile,
-  // and of one of the first keys, which every later query sees.  The key
-  // tiles are cut so that there are two blocks a multiprocessor, but none
-  // under 8 items; those of the first keys into chunks of the same length.
+  // and of one of the first keys, which every later query sees.  A key tile
+  // is cut so that no block has more than a third of a multiprocessor's share
+  // of the call (the walk over query tiles is about as long as that over key
+  // tiles; without a window a tile sees half the rows on average), but not
+  // under 8 items.
   const long long all_items = static_cast<long long>(p.w.group) * ((p.w.n_queries + kGradCols - 1) / kGradCols);
   const long long items = std::min<long long>(
       all_items, static_cast<long long>(p.w.group) * ((static_cast<long long>(p.w.window) + kTile - 1) / kGradCols + 2));
   p.sink_tiles = items < all_items ? std::min(p.key_tiles, (p.w.sinks - 1) / kTile + (p.w.sinks > 0)) : 0;
-  const long long tiles = std::max<long long>(1, seqs * p.key_tiles);
-  p.chunks = static_cast<int>(std::max<long long>(1, std::min((2LL * sms + tiles - 1) / tiles, items / 8)));
-  const long long share = std::max<long long>(8, items / p.chunks);
-  p.sink_chunks = p.sink_tiles > 0 ? static_cast<int>(std::max<long long>(1, std::min<long long>(256, (all_items + share - 1) / share))) : 1;
+  const long long bhs = static_cast<long long>(p.w.batch) * p.w.heads;
+  const long long key_tiles = std::max<long long>(1, seqs * p.key_tiles), query_tiles = bhs * row_tiles;
+  const double total = static_cast<double>(key_tiles) * static_cast<double>(items) * (items < all_items ? 2.0 : 1.0);
+  const long long most = std::max(8LL, static_cast<long long>(total / (3.0 * sms)));
+  auto cut = [most](long long n) { return static_cast<int>(std::max(1LL, std::min(256LL, (n + most - 1) / most))); };
+  p.chunks = cut(items);
+  p.sink_chunks = p.sink_tiles > 0 ? cut(all_items) : 1;
   const long long sink_blocks = seqs * p.sink_tiles * p.sink_chunks;
   const long long rest_blocks = seqs * (p.key_tiles - p.sink_tiles) * p.chunks;
+  if (sink_blocks + rest_blocks + query_tiles > kMaxRows || bhs * p.stat_tiles > kMaxRows)
+    return fail(VATTN_ERR_UNSUPPORTED, "too many tiles of 128 rows");
+  p.sink_blocks = static_cast<int>(sink_blocks);
+  p.key_blocks = static_cast<int>(sink_blocks + rest_blocks);
+  auto div = [](long long d) { return vattn::FastDiv::make(static_cast<uint32_t>(std::max(1LL, d))); };
+  p.d_sink_chunks = div(p.sink_chunks);
+  p.d_chunks = div(p.chunks);
+  p.d_seqs = div(seqs);
+  p.d_kv_heads = div(p.w.kv_heads);
+  p.d_bhs = div(bhs);
+  p.d_heads = div(p.w.heads);
+  p.d_stat_tiles = div(p.stat_tiles);
   const long long slots = (p.sink_chunks > 1 ? sink_blocks : 0) + (p.chunks > 1 ? rest_blocks : 0);
   const size_t stat_bytes = static_cast<size_t>(p.w.batch) * p.w.heads * p.stat_tiles * vattn::kGradStat * 4;
   const size_t part_bytes = static_cast<size_t>(slots) * 2 * kTile * p.w.dim * 4;
@@ -485,9 +495,9 @@ vattn_status backward_window(const Tensor& tg, const Tensor& tq, const Tensor& t
     p.part = reinterpret_cast<float*>(ws.data() + stat_bytes);
   }
   if (stat_bytes > 0) {
-    const long long rows = static_cast<long long>(p.w.batch) * p.w.heads * p.stat_tiles * kGradCols;
-    if (rows / 16 > INT32_MAX) return fail(VATTN_ERR_UNSUPPORTED, "too many query rows");
-    vattn::vattn_window_stat_kernel<T><<<static_cast<unsigned>(rows / 16), 256, 0, stream>>>(p);
+    const unsigned grid = static_cast<unsigned>(bhs * p.stat_tiles);
+    if (p.w.dim <= 64) vattn::vattn_window_stat_kernel<T, 8><<<grid, 256, 0, stream>>>(p);
+    else vattn::vattn_window_stat_kernel<T, 16><<<grid, 256, 0, stream>>>(p);
     if ((st = launched("gradient statistics kernel launch")) != VATTN_OK) return st;
   }
   // each tensor as an X tile (128 rows) and as a Y tile (64 rows); one that
@@ -501,23 +511,17 @@ vattn_status backward_window(const Tensor& tg, const Tensor& tq, const Tensor& t
         (st = make_rows_map(&y[i], &mul[i], u, dtype, kGradCols)) != VATTN_OK)
       return st;
   }
-  if (!tk.empty()) {
-    p.mx1 = mul[2];
-    p.mx2 = mul[3];
-    p.my1 = mul[0];
-    p.my2 = mul[1];
-    if ((st = grad_launch<T, NKB, true>(x[2], x[3], y[0], y[1], p, sink_blocks + rest_blocks, device, stream)) != VATTN_OK)
-      return st;
-  }
-  if (!tq.empty()) {
-    p.mx1 = mul[0];
-    p.mx2 = mul[1];
-    p.my1 = mul[2];
-    p.my2 = mul[3];
-    if ((st = grad_launch<T, NKB, false>(x[0], x[1], y[2], y[3], p,
-                                         static_cast<long long>(p.w.batch) * p.w.heads * row_tiles, device, stream)) != VATTN_OK)
-      return st;
-  }
+  p.mq = mul[0];
+  p.mg = mul[1];
+  p.mk = mul[2];
+  p.mv = mul[3];
+  using P = vattn::GradPlan<NKB>;
+  auto kernel = vattn::vattn_window_bwd_kernel<T, NKB>;
+  static std::atomic<uint8_t> done[vattn::host::kMaxDevices];
+  if ((st = allow_smem(kernel, P::kSmemBytes, done, device)) != VATTN_OK) return st;
+  kernel<<<static_cast<unsigned>(p.key_blocks + query_tiles), P::kThreads, P::kSmemBytes, stream>>>(
+      x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3], p);
+  if ((st = launched("gradient kernel launch")) != VATTN_OK) return st;
   if (slots > 0) {
     const long long joined = seqs * ((p.sink_chunks > 1 ? p.sink_tiles : 0) + (p.chunks > 1 ? p.key_tiles - p.sink_tiles : 0));
     const dim3 grid(static_cast<unsigned>(joined), static_cast<unsigned>((2 * kTile * (p.w.dim / 8) + 255) / 256));

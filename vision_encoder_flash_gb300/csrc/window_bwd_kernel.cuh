@@ -45,46 +45,60 @@ struct WindowGradParams {
   float* stat;     // [batch * heads][stat_tiles][-lse2 x 64 | -delta x 64]
   float* part;     // [slot][dv, dk][128][dim] partial sums of the chunks
   uint32_t* status;
-  MapMul mx1, mx2, my1, my2;
+  MapMul mq, mg, mk, mv;  // q, dout, k, v
   int stat_tiles;  // Y tiles of the queries, to a multiple of two
   int key_tiles;   // ceil(n_keys / 128)
   int sink_tiles;  // of these, the first with keys < sinks, cut into sink_chunks
   int sink_chunks, chunks;
+  int sink_blocks, key_blocks;  // blocks of the first keys' tiles, of all key tiles; the rest have query tiles
+  FastDiv d_sink_chunks, d_chunks, d_seqs, d_kv_heads, d_bhs, d_heads, d_stat_tiles;
   float scale_log2;
 };
 
 // -lse2 = -lse log2(e) and -delta of every query row; rows that see nothing
 // (and those that fill the last tile) get -infinity and 0, hence weights 0.
-template <typename T>
+// A block has one tile of 64 rows; LR lanes, 16 bytes each, hold one row, and
+// the loads of a lane's LR / 4 rows are all in flight before the sums.
+template <typename T, int LR>
 __global__ void __launch_bounds__(256) vattn_window_stat_kernel(const __grid_constant__ WindowGradParams p) {
-  const int lane16 = threadIdx.x & 15;
-  const long long rows = static_cast<long long>(p.stat_tiles) * kGradCols;
-  const long long total = rows * p.w.batch * p.w.heads;
-  const long long idx = static_cast<long long>(blockIdx.x) * 16 + (threadIdx.x >> 4);
-  if (idx >= total) return;  // whole half-warps
-  const long long bh = idx / rows;
-  const int i = static_cast<int>(idx - bh * rows);
-  const int b = static_cast<int>(bh / p.w.heads), h = static_cast<int>(bh - static_cast<long long>(b) * p.w.heads);
+  constexpr int R = kGradCols * LR / 256;
+  uint32_t tile, h;
+  const uint32_t bh = p.d_stat_tiles.div(blockIdx.x, &tile);
+  const int b = static_cast<int>(p.d_heads.div(bh, &h));
+  const int lane = threadIdx.x % LR, c = lane * 8;
   const Seq s = window_seq(p.w, b);
-  const int pos = s.start + i;
-  const bool on = i < p.w.n_queries && pos >= 0 && pos < s.len;
-  float sum = 0.0f;
-  if (on && lane16 * 8 < p.w.dim) {
-    float x[8], y[8];
-    reinterpret_cast<const Vec<T, 8>*>(rows_at<T>(p.dout, b, h, i) + lane16 * 8)->widen(x);
-    reinterpret_cast<const Vec<T, 8>*>(rows_at<T>(p.out, b, h, i) + lane16 * 8)->widen(y);
+  Vec<T, 8> x[R], y[R];
+  bool on[R];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum = fmaf(x[e], y[e], sum);
+  for (int k = 0; k < R; ++k) {
+    const int i = static_cast<int>(tile) * kGradCols + threadIdx.x / LR + k * (256 / LR);
+    const int pos = s.start + i;
+    on[k] = i < p.w.n_queries && pos >= 0 && pos < s.len;
+    if (on[k] && c < p.w.dim) {
+      x[k] = *reinterpret_cast<const Vec<T, 8>*>(rows_at<T>(p.dout, b, h, i) + c);
+      y[k] = *reinterpret_cast<const Vec<T, 8>*>(rows_at<T>(p.out, b, h, i) + c);
+    }
   }
-  const uint32_t mask = 0xffffu << (threadIdx.x & 16);
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(mask, sum, o);
-  if (lane16 != 0) return;
-  const float lse = on ? p.lse[bh * p.w.n_queries + i] : -INFINITY;
-  float* to = p.stat + (bh * p.stat_tiles + i / kGradCols) * kGradStat + i % kGradCols;
-  const bool empty = lse == -INFINITY;
-  to[0] = empty ? -INFINITY : -lse * kLog2E;
-  to[kGradCols] = empty ? 0.0f : -sum;
+  for (int k = 0; k < R; ++k) {
+    float sum = 0.0f;
+    if (on[k] && c < p.w.dim) {
+      float fx[8], fy[8];
+      x[k].widen(fx);
+      y[k].widen(fy);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = fmaf(fx[e], fy[e], sum);
+    }
+#pragma unroll
+    for (int o = LR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane != 0) continue;
+    const int r = threadIdx.x / LR + k * (256 / LR), i = static_cast<int>(tile) * kGradCols + r;
+    const float lse = on[k] ? p.lse[static_cast<long long>(bh) * p.w.n_queries + i] : -INFINITY;
+    const bool empty = lse == -INFINITY;
+    float* to = p.stat + static_cast<long long>(blockIdx.x) * kGradStat + r;
+    to[0] = empty ? -INFINITY : -lse * kLog2E;
+    to[kGradCols] = empty ? 0.0f : -sum;
+  }
 }
 
 template <int NKB>
@@ -112,7 +126,7 @@ struct GradWalk {
   int b, h;         // h: key head (keys) or query head (queries)
   int row0;         // first row of the X tile
   Seq s;
-  long long slot;   // of the partial sums, -1: none
+  int slot;   // of the partial sums, -1: none
   // keys: item -> head g of the group and query tile; queries: key tiles [0, ns) and [first, ..)
   int first, per_head, begin, n, ns;
 
@@ -128,23 +142,20 @@ struct GradWalk {
   }
 };
 
-__device__ __forceinline__ GradWalk<true> grad_walk_keys(const WindowGradParams& p, long long block) {
+__device__ __forceinline__ GradWalk<true> grad_walk_keys(const WindowGradParams& p, int block) {
   GradWalk<true> k;
-  const long long seqs = static_cast<long long>(p.w.batch) * p.w.kv_heads;
-  const long long sink_blocks = seqs * p.sink_tiles * p.sink_chunks;
-  const bool sink = block < sink_blocks;
-  const long long at = sink ? block : block - sink_blocks;
+  const bool sink = block < p.sink_blocks;
+  const int at = sink ? block : block - p.sink_blocks;
   const int chunks = sink ? p.sink_chunks : p.chunks;
-  const int chunk = static_cast<int>(at % chunks);
-  const long long t = at / chunks;
-  const long long bk = t % seqs;
-  const int tile = static_cast<int>(t / seqs) + (sink ? 0 : p.sink_tiles);
-  k.b = static_cast<int>(bk / p.w.kv_heads);
-  k.h = static_cast<int>(bk - static_cast<long long>(k.b) * p.w.kv_heads);
+  uint32_t chunk, bk, kh;
+  const uint32_t t = (sink ? p.d_sink_chunks : p.d_chunks).div(static_cast<uint32_t>(at), &chunk);
+  const int tile = static_cast<int>(p.d_seqs.div(t, &bk)) + (sink ? 0 : p.sink_tiles);
+  k.b = static_cast<int>(p.d_kv_heads.div(bk, &kh));
+  k.h = static_cast<int>(kh);
   k.row0 = tile * kTile;
   k.s = window_seq(p.w, k.b);
   // slots: those of the first keys' tiles, then the others' (where cut)
-  k.slot = chunks == 1 ? -1 : (sink || p.sink_chunks == 1 ? at : sink_blocks + at);
+  k.slot = chunks == 1 ? -1 : (sink || p.sink_chunks == 1 ? at : p.sink_blocks + at);
   k.ns = 0;
   k.n = k.begin = k.first = 0;
   k.per_head = 1;
@@ -155,19 +166,18 @@ __device__ __forceinline__ GradWalk<true> grad_walk_keys(const WindowGradParams&
     k.per_head = hi / kGradCols - k.first + 1;
     const long long all = static_cast<long long>(k.per_head) * p.w.group;
     k.begin = static_cast<int>(all * chunk / chunks);
-    k.n = static_cast<int>(all * (chunk + 1) / chunks) - k.begin;
+    k.n = static_cast<int>(all * (chunk + 1LL) / chunks) - k.begin;
   }
   return k;
 }
 
-__device__ __forceinline__ GradWalk<false> grad_walk_queries(const WindowGradParams& p, long long block) {
+__device__ __forceinline__ GradWalk<false> grad_walk_queries(const WindowGradParams& p, int block) {
   GradWalk<false> k;
-  const long long bhs = static_cast<long long>(p.w.batch) * p.w.heads;
-  const int tiles = p.stat_tiles / 2;
-  const long long bh = block % bhs;
-  k.row0 = (tiles - 1 - static_cast<int>(block / bhs)) * kTile;  // late rows see most: first
-  k.b = static_cast<int>(bh / p.w.heads);
-  k.h = static_cast<int>(bh - static_cast<long long>(k.b) * p.w.heads);
+  uint32_t bh, h;
+  const int tile = static_cast<int>(p.d_bhs.div(static_cast<uint32_t>(block), &bh));
+  k.row0 = (p.stat_tiles / 2 - 1 - tile) * kTile;  // late rows see most: first
+  k.b = static_cast<int>(p.d_heads.div(bh, &h));
+  k.h = static_cast<int>(h);
   k.s = window_seq(p.w, k.b);
   k.slot = -1;
   k.begin = 0;
@@ -186,7 +196,8 @@ __device__ __forceinline__ GradWalk<false> grad_walk_queries(const WindowGradPar
 template <typename T, int NKB, bool kKeys>
 __device__ __forceinline__ void grad_block(const CUtensorMap* tm_x1, const CUtensorMap* tm_x2,
                                            const CUtensorMap* tm_y1, const CUtensorMap* tm_y2,
-                                           const WindowGradParams& p, long long block) {
+                                           const MapMul& mx1, const MapMul& mx2, const MapMul& my1,
+                                           const MapMul& my2, const WindowGradParams& p, int block) {
   using P = GradPlan<NKB>;
   constexpr int S = P::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -241,7 +252,7 @@ __device__ __forceinline__ void grad_block(const CUtensorMap* tm_x1, const CUten
       ptx::mbar_arrive_expect_tx(bar(kGbXFull), 2 * P::kXBytes);
       for (int i = 0; i < 2; ++i)
         for (int kb = 0; kb < NKB; ++kb) {
-          const MapMul m = i ? p.mx2 : p.mx1;
+          const MapMul m = i ? mx2 : mx1;
           ptx::tma_load_4d_hint(base_s + P::kOffX + i * P::kXBytes + kb * kBlockBytes, i ? tm_x2 : tm_x1,
                                 bar(kGbXFull), kb * 64, wk.row0, wk.h * m.h, wk.b * m.b, once);
         }
@@ -255,7 +266,7 @@ __device__ __forceinline__ void grad_block(const CUtensorMap* tm_x1, const CUten
         const int h = kKeys ? wk.h * group + g : wk.h / group;
         for (int i = 0; i < 2; ++i)
           for (int kb = 0; kb < NKB; ++kb) {
-            const MapMul m = i ? p.my2 : p.my1;
+            const MapMul m = i ? my2 : my1;
             ptx::tma_load_4d_hint(stage(n) + i * P::kYBytes + kb * kGradBlock, i ? tm_y2 : tm_y1,
                                   bar(kGbYFull + st), kb * 64, tile * kGradCols, h * m.h, wk.b * m.b, keep);
           }
@@ -290,16 +301,19 @@ __device__ __forceinline__ void grad_block(const CUtensorMap* tm_x1, const CUten
           __syncwarp();
         }
         ptx::tc_fence_after();
-        if (lane == 0) {
+        const uint32_t x_lo = ptx::smem_desc_lo(base_s + P::kOffX, 16), y_lo = ptx::smem_desc_lo(stage(n), 16);
+        const uint32_t d = tmem + (n & 1) * 128u;
+        if (ptx::elect_one()) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t x = ptx::smem_desc_lo(base_s + P::kOffX + i * P::kXBytes, 16);
-            const uint32_t y = ptx::smem_desc_lo(stage(n) + i * P::kYBytes, 16);
-            for (int ks = 0; ks < ksteps; ++ks)
-              ptx::mma_ss(tmem + (n & 1) * 128u + i * 64u,
-                          ptx::smem_desc_join(x + (((ks >> 2) * kBlockBytes + (ks & 3) * 32) >> 4), hi),
-                          ptx::smem_desc_join(y + (((ks >> 2) * kGradBlock + (ks & 3) * 32) >> 4), hi), idesc_s, ks > 0);
-          }
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int ks = 0; ks < 4 * NKB; ++ks) {
+              const uint32_t x_off = (i * P::kXBytes + (ks >> 2) * kBlockBytes + (ks & 3) * 32) >> 4;
+              const uint32_t y_off = (i * P::kYBytes + (ks >> 2) * kGradBlock + (ks & 3) * 32) >> 4;
+              if (ks < ksteps)
+                ptx::mma_ss(d + i * 64u, ptx::smem_desc_join(x_lo + x_off, hi), ptx::smem_desc_join(y_lo + y_off, hi),
+                            idesc_s, ks > 0);
+            }
           ptx::mma_commit(bar(kGbSFull + (n & 1)));
         }
         return true;
@@ -310,9 +324,9 @@ __device__ __forceinline__ void grad_block(const CUtensorMap* tm_x1, const CUten
         const int b = n & 1;
         if (!(ok = pipe.wait_warp(bar(kGbPFull + b), static_cast<uint32_t>(n >> 1) & 1u, kSiteGradMma))) break;
         ptx::tc_fence_after();
-        if (lane == 0) {
-          const uint32_t y1 = ptx::smem_desc_lo(stage(n), kGradBlock);
-          const uint32_t y2 = ptx::smem_desc_lo(stage(n) + P::kYBytes, kGradBlock);
+        const uint32_t y1 = ptx::smem_desc_lo(stage(n), kGradBlock);
+        const uint32_t y2 = ptx::smem_desc_lo(stage(n) + P::kYBytes, kGradBlock);
+        if (ptx::elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < kGradCols / 16; ++ks) {
             if (kKeys)
@@ -325,7 +339,7 @@ __device__ __forceinline__ void grad_block(const CUtensorMap* tm_x1, const CUten
         }
         if (n + 2 < wk.n) ok = issue_s(n + 2);
       }
-      if (lane == 0) ptx::mma_commit(bar(kGbAcc));
+      if (ptx::elect_one()) ptx::mma_commit(bar(kGbAcc));
     }
   } else {
     ptx::regs_increase<P::kRegsMath>();
@@ -436,7 +450,7 @@ __device__ __forceinline__ void grad_block(const CUtensorMap* tm_x1, const CUten
       const bool store = row < (kKeys ? p.w.n_keys : p.w.n_queries);
       T* to = nullptr;
       float* part = nullptr;
-      if (wk.slot >= 0) part = p.part + ((wk.slot * 2 + wg) * kTile + r) * static_cast<long long>(D);
+      if (wk.slot >= 0) part = p.part + ((wk.slot * 2LL + wg) * kTile + r) * D;
       else if (store) to = rows_at_mut<T>(kKeys ? (wg == 0 ? p.dv : p.dk) : p.dq, wk.b, wk.h, row);
       for (int c = kKeys ? 0 : wg * 16; c < D; c += kKeys ? 16 : 32) {
         uint32_t y[16];
@@ -475,12 +489,21 @@ __device__ __forceinline__ void grad_block(const CUtensorMap* tm_x1, const CUten
   }
 }
 
-template <typename T, int NKB, bool kKeys>
+// Key tiles first, then the query tiles: their blocks are shorter and fill
+// the multiprocessors that the last key tiles leave idle.  tm_*: tiles of 128
+// rows (x) and of 64 (y).
+template <typename T, int NKB>
 __global__ void __launch_bounds__(GradPlan<NKB>::kThreads, 1)
-    vattn_window_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_constant__ CUtensorMap tm_x2,
-                            const __grid_constant__ CUtensorMap tm_y1, const __grid_constant__ CUtensorMap tm_y2,
+    vattn_window_bwd_kernel(const __grid_constant__ CUtensorMap tm_qx, const __grid_constant__ CUtensorMap tm_gx,
+                            const __grid_constant__ CUtensorMap tm_kx, const __grid_constant__ CUtensorMap tm_vx,
+                            const __grid_constant__ CUtensorMap tm_qy, const __grid_constant__ CUtensorMap tm_gy,
+                            const __grid_constant__ CUtensorMap tm_ky, const __grid_constant__ CUtensorMap tm_vy,
                             const __grid_constant__ WindowGradParams p) {
-  grad_block<T, NKB, kKeys>(&tm_x1, &tm_x2, &tm_y1, &tm_y2, p, blockIdx.x);
+  const int block = static_cast<int>(blockIdx.x);
+  if (block < p.key_blocks)
+    grad_block<T, NKB, true>(&tm_kx, &tm_vx, &tm_qy, &tm_gy, p.mk, p.mv, p.mq, p.mg, p, block);
+  else
+    grad_block<T, NKB, false>(&tm_qx, &tm_gx, &tm_ky, &tm_vy, p.mq, p.mg, p.mk, p.mv, p, block - p.key_blocks);
 }
 
 // dk and dv of the key tiles that were cut: their chunks' partial sums added
@@ -494,9 +517,8 @@ __global__ void __launch_bounds__(256) vattn_window_join_kernel(const __grid_con
   const bool sink = tile < p.sink_tiles;
   const int chunks = sink ? p.sink_chunks : p.chunks;
   if (chunks == 1) return;
-  const long long sink_blocks = seqs * p.sink_tiles * p.sink_chunks;
   const long long at = ((static_cast<long long>(tile) - (sink ? 0 : p.sink_tiles)) * seqs + bk) * chunks;
-  const long long slot = sink || p.sink_chunks == 1 ? at : sink_blocks + at;
+  const long long slot = sink || p.sink_chunks == 1 ? at : p.sink_blocks + at;
   const int b = static_cast<int>(bk / p.w.kv_heads), h = static_cast<int>(bk - static_cast<long long>(b) * p.w.kv_heads);
   const int D = p.w.dim, per_row = D / 8;
   const int e = blockIdx.y * 256 + threadIdx.x;

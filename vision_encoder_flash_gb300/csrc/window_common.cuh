@@ -8,6 +8,27 @@
 
 namespace vattn {
 
+// Division of n < 2^31 by a divisor known on the host, as a multiplication: q
+// = hi32(n * m) >> s with m = floor(2^(32 + s) / d) + 1, s = floor(log2(d - 1)),
+// exact because n (m d - 2^(32 + s)) < 2^(32 + s).
+struct FastDiv {
+  uint32_t d, m, s;
+  __host__ static FastDiv make(uint32_t d) {
+    FastDiv f{d, 0, 0};
+    if (d > 1) {
+      while ((2u << f.s) < d) ++f.s;
+      f.m = static_cast<uint32_t>((uint64_t{1} << (32 + f.s)) / d + 1);
+    }
+    return f;
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return d == 1 ? n : __umulhi(n, m) >> s; }
+  __device__ __forceinline__ uint32_t div(uint32_t n, uint32_t* rest) const {
+    const uint32_t q = div(n);
+    *rest = n - q * d;
+    return q;
+  }
+};
+
 // Window and sizes of one call.
 struct WindowParams {
   const int32_t* kv_len;   // [batch] or null: n_keys

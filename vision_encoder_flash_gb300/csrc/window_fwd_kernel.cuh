@@ -46,9 +46,10 @@ struct WindowFwdParams {
   float* lse;
   uint32_t* status;
   MapMul mq, mk, mv, mo;
-  int row_blocks;      // ceil(n_queries / 128)
-  long long pairs;     // items of one (batch, key head)
-  long long items;
+  int pairs;           // items of one (batch, key head): its units by twos
+  int units;           // ceil(n_queries / 128) * group
+  int items;           // < 2^30
+  FastDiv seqs, kv_heads, group;  // batch * kv_heads, kv_heads, group
   float scale_log2;    // scale * log2(e)
 };
 
@@ -81,24 +82,22 @@ struct WindowItem {
   __device__ __forceinline__ int tile(int x) const { return x < first_n ? x : second + (x - first_n); }
 };
 
-__device__ __forceinline__ WindowItem window_item(const WindowFwdParams& p, long long item) {
+__device__ __forceinline__ WindowItem window_item(const WindowFwdParams& p, int item) {
   WindowItem it;
-  const long long seqs = static_cast<long long>(p.w.batch) * p.w.kv_heads;
-  const long long pair = p.pairs - 1 - item / seqs;
-  const long long bk = item % seqs;
-  it.b = static_cast<int>(bk / p.w.kv_heads);
-  it.kh = static_cast<int>(bk - static_cast<long long>(it.b) * p.w.kv_heads);
+  uint32_t bk, kh;
+  const int pair = p.pairs - 1 - static_cast<int>(p.seqs.div(static_cast<uint32_t>(item), &bk));
+  it.b = static_cast<int>(p.kv_heads.div(bk, &kh));
+  it.kh = static_cast<int>(kh);
   it.s = window_seq(p.w, it.b);
-  const long long units = static_cast<long long>(p.row_blocks) * p.w.group;
   int last = -1, first = 0x7fffffff;
   it.first_n = 0;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const long long unit = 2 * pair + t;
-    it.on[t] = unit < units;
-    const int r = static_cast<int>(unit / p.w.group);
-    it.row0[t] = r * kTile;
-    it.head[t] = it.kh * p.w.group + static_cast<int>(unit - static_cast<long long>(r) * p.w.group);
+    const int unit = 2 * pair + t;
+    uint32_t g;
+    it.on[t] = unit < p.units;
+    it.row0[t] = static_cast<int>(p.group.div(static_cast<uint32_t>(unit), &g)) * kTile;
+    it.head[t] = it.kh * p.w.group + static_cast<int>(g);
     it.u[t] = it.on[t] ? unit_range(p.w, it.s, it.row0[t]) : UnitRange{0, 0, -1};
     if (!it.u[t].empty()) {
       it.first_n = max(it.first_n, it.u[t].ns);
@@ -226,7 +225,7 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
       const uint64_t keep = ptx::policy_evict_last();  // read again by other heads and rows
       long long c = 0;  // ring entries so far
       bool ok = true;
-      for (long long item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+      for (int item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
         const WindowItem it = window_item(p, item);
         for (int x = 0; ok && x < it.n; ++x) {
           const int row = it.tile(x) * kTile;
@@ -248,7 +247,7 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
       // ------------------------------------------------------- Q tiles
       const uint64_t once = ptx::policy_evict_first();
       uint32_t n_q = 0;
-      for (long long item = blockIdx.x; item < p.items; item += gridDim.x) {
+      for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
         const WindowItem it = window_item(p, item);
         if (it.n == 0) continue;
         if (n_q > 0 && !pipe.wait(bar(kWbQEmpty), (n_q - 1) & 1u, kSiteWinQ)) break;
@@ -317,7 +316,7 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
       };
       long long g = 0;  // key tiles of this block so far; K of tile g is ring entry 2 g, V 2 g + 1
       bool ok = true;
-      for (long long item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+      for (int item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
         const WindowItem it = window_item(p, item);
         if (it.n == 0) continue;
         if (!(ok = pipe.wait_warp(bar(kWbQFull), n_q & 1u, kSiteWinMma))) break;
@@ -384,7 +383,7 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
     uint32_t n_s = 0;  // tiles of this unit so far
     int n_out = 0;     // result boxes of this warp so far
     bool ok = true;
-    for (long long item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+    for (int item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
       const WindowItem it = window_item(p, item);
       if (!(t == 0 ? it.on[0] : it.on[1])) continue;
       const UnitRange u = t == 0 ? it.u[0] : it.u[1];
