@@ -137,6 +137,25 @@ vattn_status launched(const char* what) {
   return e == cudaSuccess ? VATTN_OK : cuda_fail(e, what);
 }
 
+// Launches a kernel whose blocks may start while the kernel before it on the
+// stream ends (they wait with griddepcontrol.wait before they read its work).
+template <typename K, typename... A>
+vattn_status launch_behind(const char* what, K kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                           const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return e == cudaSuccess ? VATTN_OK : cuda_fail(e, what);
+}
+
 // ------------------------------------------------------------ norm + rotation
 vattn_status check_qk(const vattn_qk_args* a) {
   if (!a) return fail(VATTN_ERR_INVALID_ARG, "null args");
@@ -477,6 +496,7 @@ vattn_status backward_window(const Tensor& tg, const Tensor& tq, const Tensor& t
     return fail(VATTN_ERR_UNSUPPORTED, "too many tiles of 128 rows");
   p.sink_blocks = static_cast<int>(sink_blocks);
   p.key_blocks = static_cast<int>(sink_blocks + rest_blocks);
+  p.blocks = static_cast<int>(sink_blocks + rest_blocks + query_tiles);
   auto div = [](long long d) { return vattn::FastDiv::make(static_cast<uint32_t>(std::max(1LL, d))); };
   p.d_sink_chunks = div(p.sink_chunks);
   p.d_chunks = div(p.chunks);
@@ -519,14 +539,16 @@ vattn_status backward_window(const Tensor& tg, const Tensor& tq, const Tensor& t
   auto kernel = vattn::vattn_window_bwd_kernel<T, NKB>;
   static std::atomic<uint8_t> done[vattn::host::kMaxDevices];
   if ((st = allow_smem(kernel, P::kSmemBytes, done, device)) != VATTN_OK) return st;
-  kernel<<<static_cast<unsigned>(p.key_blocks + query_tiles), P::kThreads, P::kSmemBytes, stream>>>(
-      x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3], p);
-  if ((st = launched("gradient kernel launch")) != VATTN_OK) return st;
+  if ((st = launch_behind("gradient kernel launch", kernel, dim3(static_cast<unsigned>(std::min(p.blocks, sms))),
+                          dim3(P::kThreads), P::kSmemBytes, stream, x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3],
+                          p)) != VATTN_OK)
+    return st;
   if (slots > 0) {
     const long long joined = seqs * ((p.sink_chunks > 1 ? p.sink_tiles : 0) + (p.chunks > 1 ? p.key_tiles - p.sink_tiles : 0));
     const dim3 grid(static_cast<unsigned>(joined), static_cast<unsigned>((2 * kTile * (p.w.dim / 8) + 255) / 256));
-    vattn::vattn_window_join_kernel<T><<<grid, 256, 0, stream>>>(p);
-    if ((st = launched("gradient join kernel launch")) != VATTN_OK) return st;
+    if ((st = launch_behind("gradient join kernel launch", vattn::vattn_window_join_kernel<T>, grid, dim3(256), 0,
+                            stream, p)) != VATTN_OK)
+      return st;
   }
   return ws.release();
 }
@@ -558,17 +580,9 @@ vattn_status cached_launch(vattn::CachedParams p, int sms, int device, cudaStrea
   if ((st = launched("cached attention kernel launch")) != VATTN_OK) return st;
   if (p.splits == 1) return VATTN_OK;
   if ((seqs * p.rows + 3) / 4 > INT32_MAX) return fail(VATTN_ERR_UNSUPPORTED, "too many query rows");
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((seqs * p.rows + 3) / 4));
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, vattn::vattn_cached_join_kernel<T, RW>, p);
-  if (e != cudaSuccess) return cuda_fail(e, "cached attention join kernel launch");
+  if ((st = launch_behind("cached attention join kernel launch", vattn::vattn_cached_join_kernel<T, RW>,
+                          dim3(static_cast<unsigned>((seqs * p.rows + 3) / 4)), dim3(128), 0, stream, p)) != VATTN_OK)
+    return st;
   return ws.release();
 }
 
@@ -723,17 +737,9 @@ vattn_status vattn_qk_norm_rope_backward(const vattn_rows* dq_out, const vattn_r
   for (int i = 0; i < 2; ++i) s.dw[i] = dw[i];
   s.row1[0] = s.row0[1] = bx * p.t[0].slices;
   s.row1[1] = bx * slices;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((p.D + 31) / 32), 2);
-  cfg.blockDim = dim3(32, 32);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, vattn::vattn_qk_weight_sum_kernel, s);
-  if (e != cudaSuccess) return cuda_fail(e, "weight gradient kernel launch");
+  if ((st = launch_behind("weight gradient kernel launch", vattn::vattn_qk_weight_sum_kernel,
+                          dim3(static_cast<unsigned>((p.D + 31) / 32), 2), dim3(32, 32), 0, stream, s)) != VATTN_OK)
+    return st;
   return ws.release();
 }
 

@@ -18,9 +18,16 @@
 //   keys:     dV += P Y2, dK += D Y1     queries:  dQ += D Y1
 // P and D overwrite S and G in TMEM and are the A operands of the second
 // products; Y is read K-major for the first and MN-major for the second, so
-// nothing is transposed.  Two S/G buffers, each with a warpgroup of its own,
-// alternate: the tensor core works on one while the other is turned into P
-// and D.  TMEM (512 columns): S 128 b, G 128 b + 64, sums at 256 and 384.
+// nothing is transposed.  The grid is one block per multiprocessor, each
+// walking over X tiles, key tiles (longer) first:
+//   warp 0   X and Y tiles by TMA (Y through a ring, ahead across X tiles)
+//   warp 1   issues S and G of item n into buffer n mod NB
+//   warp 2   issues the second products once P and D are there; an issuing
+//            thread is held while its products run, so with two of them S and
+//            G of later items run between
+//   warps 4-7, 8-11   P and D of every other item, then the tile's results
+// TMEM (512 columns): NB buffers of S and G (64 columns each) from 0, three up
+// to head_dim 64, two above; the sums behind them.
 //
 // A key tile's walk is cut into chunks (f32 partial sums in a workspace,
 // added in order by vattn_window_join_kernel) where tiles are few or, for the
@@ -50,7 +57,7 @@ struct WindowGradParams {
   int key_tiles;   // ceil(n_keys / 128)
   int sink_tiles;  // of these, the first with keys < sinks, cut into sink_chunks
   int sink_chunks, chunks;
-  int sink_blocks, key_blocks;  // blocks of the first keys' tiles, of all key tiles; the rest have query tiles
+  int sink_blocks, key_blocks, blocks;  // X tiles: the first keys' (with their chunks), all keys', all
   FastDiv d_sink_chunks, d_chunks, d_seqs, d_kv_heads, d_bhs, d_heads, d_stat_tiles;
   float scale_log2;
 };
@@ -62,6 +69,7 @@ struct WindowGradParams {
 template <typename T, int LR>
 __global__ void __launch_bounds__(256) vattn_window_stat_kernel(const __grid_constant__ WindowGradParams p) {
   constexpr int R = kGradCols * LR / 256;
+  ptx::grid_dep_launch();  // the gradient kernel sets itself up meanwhile, and waits for this one's end
   uint32_t tile, h;
   const uint32_t bh = p.d_stat_tiles.div(blockIdx.x, &tile);
   const int b = static_cast<int>(p.d_heads.div(bh, &h));
@@ -113,11 +121,16 @@ struct GradPlan {
   static constexpr int kSmemBytes = kOffBar + 256 + 1024;
   static constexpr int kThreads = 384;
   static constexpr uint32_t kRegsOther = 72, kRegsMath = 216;  // 72 + 2 x 216 = 3 x 168
+  static constexpr int kBufs = NKB == 1 ? 3 : 2;
+  static constexpr uint32_t kColSum = kBufs * 128u;      // dV; behind it dK or dQ
+  static constexpr uint32_t kSumCols = NKB == 1 ? 64u : 128u;
   static_assert(kSmemBytes <= 232448, "shared memory");
+  static_assert(kColSum + 2 * kSumCols <= 512, "TMEM");
 };
 
 enum GradBar : int {
-  kGbXFull = 0, kGbYFull = 1, kGbYEmpty = 9, kGbSFull = 17, kGbPFull = 19, kGbAcc = 21, kGbCount = 22,
+  kGbXFull = 0, kGbXEmpty = 1, kGbYFull = 2, kGbYEmpty = 10, kGbSFull = 18, kGbPFull = 21, kGbPFree = 24,
+  kGbSum = 27, kGbSumFree = 28, kGbDoneS = 29, kGbCount = 30,
 };
 
 // What a block walks over: Y tiles 0 .. n - 1 of its share.
@@ -130,19 +143,40 @@ struct GradWalk {
   // keys: item -> head g of the group and query tile; queries: key tiles [0, ns) and [first, ..)
   int first, per_head, begin, n, ns;
 
-  // Y tile (in units of 64 rows) and query head of item x
-  __device__ __forceinline__ int tile(int x, int* g) const {
+};
+
+// Item x of a walk: its Y tile (in units of 64 rows) and query head of the group.
+template <bool kKeys>
+struct GradItem {
+  int x, g, tile;
+  __device__ __forceinline__ GradItem(const GradWalk<kKeys>& w, int x0) : x(x0), g(0), tile(0) {
     if (kKeys) {
-      const int i = begin + x;
-      *g = i / per_head;
-      return first + (i - *g * per_head);
+      const int i = w.begin + x0;
+      g = i / w.per_head;
+      tile = w.first + (i - g * w.per_head);
+    } else {
+      tile = x0 < w.ns ? x0 : w.first + (x0 - w.ns);
     }
-    *g = 0;
-    return x < ns ? x : first + (x - ns);
+  }
+  __device__ __forceinline__ void step(const GradWalk<kKeys>& w, int by) {
+    x += by;
+    if (kKeys) {
+      tile += by;
+      while (tile >= w.first + w.per_head) {
+        tile -= w.per_head;
+        ++g;
+      }
+    } else {
+      tile = x < w.ns ? x : w.first + (x - w.ns);
+    }
   }
 };
 
-__device__ __forceinline__ GradWalk<true> grad_walk_keys(const WindowGradParams& p, int block) {
+template <bool kKeys>
+__device__ __forceinline__ GradWalk<kKeys> grad_walk(const WindowGradParams& p, int block);
+
+template <>
+__device__ __forceinline__ GradWalk<true> grad_walk<true>(const WindowGradParams& p, int block) {
   GradWalk<true> k;
   const bool sink = block < p.sink_blocks;
   const int at = sink ? block : block - p.sink_blocks;
@@ -171,10 +205,11 @@ __device__ __forceinline__ GradWalk<true> grad_walk_keys(const WindowGradParams&
   return k;
 }
 
-__device__ __forceinline__ GradWalk<false> grad_walk_queries(const WindowGradParams& p, int block) {
+template <>
+__device__ __forceinline__ GradWalk<false> grad_walk<false>(const WindowGradParams& p, int block) {
   GradWalk<false> k;
   uint32_t bh, h;
-  const int tile = static_cast<int>(p.d_bhs.div(static_cast<uint32_t>(block), &bh));
+  const int tile = static_cast<int>(p.d_bhs.div(static_cast<uint32_t>(block - p.key_blocks), &bh));
   k.row0 = (p.stat_tiles / 2 - 1 - tile) * kTile;  // late rows see most: first
   k.b = static_cast<int>(p.d_heads.div(bh, &h));
   k.h = static_cast<int>(h);
@@ -193,176 +228,183 @@ __device__ __forceinline__ GradWalk<false> grad_walk_queries(const WindowGradPar
   return k;
 }
 
-template <typename T, int NKB, bool kKeys>
-__device__ __forceinline__ void grad_block(const CUtensorMap* tm_x1, const CUtensorMap* tm_x2,
-                                           const CUtensorMap* tm_y1, const CUtensorMap* tm_y2,
-                                           const MapMul& mx1, const MapMul& mx2, const MapMul& my1,
-                                           const MapMul& my2, const WindowGradParams& p, int block) {
+// The block's roles, one X tile at a time; `at` counts the items (Y tiles) of
+// the block so far, `tiles` its X tiles with items.
+struct GradCtx {
+  const WindowGradParams& p;
+  Pipe pipe;
+  uint32_t base_s, bar0, tmem;
+  int warp, lane;
+  __device__ __forceinline__ uint32_t bar(int i) const { return bar0 + 8u * static_cast<uint32_t>(i); }
+};
+
+template <int NKB, bool kKeys>
+__device__ __forceinline__ bool grad_load(const GradCtx& x, const CUtensorMap* tm_x1, const CUtensorMap* tm_x2,
+                                          const CUtensorMap* tm_y1, const CUtensorMap* tm_y2, const MapMul& mx1,
+                                          const MapMul& mx2, const MapMul& my1, const MapMul& my2, int block,
+                                          uint32_t& at, uint32_t& tiles) {
   using P = GradPlan<NKB>;
-  constexpr int S = P::kStages;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw_s = ptx::smem_addr(smem_raw);
-  const uint32_t base_s = (raw_s + 1023u) & ~1023u;
-  uint8_t* const base = smem_raw + (base_s - raw_s);
-  const uint32_t bar0 = base_s + P::kOffBar;
-  auto bar = [bar0](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
-  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(base + P::kOffBar + 8 * kGbCount);
-  volatile uint32_t* abort_flag = tmem_slot + 1;
-  const Pipe pipe{abort_flag, p.status};
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  if (threadIdx.x == 0) {
-    ptx::mbar_init(bar(kGbXFull), 1);
-    for (int i = 0; i < S; ++i) {
-      ptx::mbar_init(bar(kGbYFull + i), 1);
-      ptx::mbar_init(bar(kGbYEmpty + i), 1);
+  const WindowGradParams& p = x.p;
+  const GradWalk<kKeys> wk = grad_walk<kKeys>(p, block);
+  if (wk.n == 0) return true;
+  const uint64_t keep = ptx::policy_evict_last(), once = ptx::policy_evict_first();
+  GradItem<kKeys> it(wk, 0);
+  for (int n = 0; n < wk.n; ++n, ++at, it.step(wk, 1)) {
+    const uint32_t st = at % P::kStages;
+    if (!x.pipe.wait(x.bar(kGbYEmpty + st), ((at / P::kStages) & 1u) ^ 1u, kSiteGradLoad)) return false;
+    ptx::mbar_arrive_expect_tx(x.bar(kGbYFull + st), 2 * P::kYBytes + (kKeys ? kGradStat * 4 : 0));
+    const int h = kKeys ? wk.h * p.w.group + it.g : wk.h / p.w.group;
+    const uint32_t to = x.base_s + P::kOffY + st * P::kStageBytes;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int kb = 0; kb < NKB; ++kb) {
+        const MapMul m = i ? my2 : my1;
+        ptx::tma_load_4d_hint(to + i * P::kYBytes + kb * kGradBlock, i ? tm_y2 : tm_y1, x.bar(kGbYFull + st), kb * 64,
+                              it.tile * kGradCols, h * m.h, wk.b * m.b, keep);
+      }
+    if (kKeys)
+      ptx::bulk_load(to + 2 * P::kYBytes,
+                     p.stat + ((static_cast<long long>(wk.b) * p.w.heads + h) * p.stat_tiles + it.tile) * kGradStat,
+                     kGradStat * 4, x.bar(kGbYFull + st));
+    if (n > 0) continue;
+    // X behind the first Y: it waits for the last tile's S and G
+    if (!x.pipe.wait(x.bar(kGbXEmpty), (tiles & 1u) ^ 1u, kSiteGradLoad)) {
+      ++at;  // drained with the others
+      return false;
     }
-    for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(bar(kGbSFull + i), 1);
-      ptx::mbar_init(bar(kGbPFull + i), 4);
-    }
-    ptx::mbar_init(bar(kGbAcc), 1);
-    *abort_flag = 0;
-    ptx::fence_mbar_init();
-    ptx::prefetch_tensormap(tm_x1);
-    ptx::prefetch_tensormap(tm_x2);
-    ptx::prefetch_tensormap(tm_y1);
-    ptx::prefetch_tensormap(tm_y2);
+    ptx::mbar_arrive_expect_tx(x.bar(kGbXFull), 2 * P::kXBytes);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int kb = 0; kb < NKB; ++kb) {
+        const MapMul m = i ? mx2 : mx1;
+        ptx::tma_load_4d_hint(x.base_s + P::kOffX + i * P::kXBytes + kb * kBlockBytes, i ? tm_x2 : tm_x1,
+                              x.bar(kGbXFull), kb * 64, wk.row0, wk.h * m.h, wk.b * m.b, once);
+      }
+    ++tiles;
   }
-  if (warp == 1) {
-    ptx::tmem_alloc(ptx::smem_addr(const_cast<uint32_t*>(tmem_slot)), 512);
-    ptx::tmem_relinquish();
-  }
-  ptx::tc_fence_before();
-  __syncthreads();
-  ptx::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  ptx::grid_dep_wait();
-  GradWalk<kKeys> wk;
-  if constexpr (kKeys) wk = grad_walk_keys(p, block);
-  else wk = grad_walk_queries(p, block);
-  const int group = p.w.group;
-  auto stage = [&](int n) -> uint32_t { return base_s + P::kOffY + static_cast<uint32_t>(n % S) * P::kStageBytes; };
+  return true;
+}
 
-  if (warp < 4) {
-    ptx::regs_decrease<P::kRegsOther>();
-    if (warp == 0 && lane == 0 && wk.n > 0) {
-      // ------------------------------------------------------ X and Y tiles
-      const uint64_t keep = ptx::policy_evict_last(), once = ptx::policy_evict_first();
-      ptx::mbar_arrive_expect_tx(bar(kGbXFull), 2 * P::kXBytes);
+// S = X1 Y1^T, G = X2 Y2^T of every item (a whole warp; one lane issues).
+template <typename T, int NKB, bool kKeys>
+__device__ __forceinline__ bool grad_scores(const GradCtx& x, int block, uint32_t& at, uint32_t& tiles) {
+  using P = GradPlan<NKB>;
+  const WindowGradParams& p = x.p;
+  const GradWalk<kKeys> wk = grad_walk<kKeys>(p, block);
+  if (wk.n == 0) return true;
+  const int ksteps = (p.w.dim + 15) >> 4;
+  constexpr uint32_t idesc = ptx::idesc_16bit_f32(kTile, kGradCols, false, Elem<T>::kBf16);
+  constexpr uint32_t hi = ptx::smem_desc_hi(1024, ptx::kSwizzle128B);
+  const uint32_t x_lo = ptx::smem_desc_lo(x.base_s + P::kOffX, 16);
+  if (!x.pipe.wait_warp(x.bar(kGbXFull), tiles & 1u, kSiteGradMma)) return false;
+  ++tiles;
+  GradItem<kKeys> it(wk, 0);
+  for (int n = 0; n < wk.n; ++n, ++at, it.step(wk, 1)) {
+    const uint32_t st = at % P::kStages, buf = at % P::kBufs;
+    const uint32_t y = x.base_s + P::kOffY + st * P::kStageBytes;
+    if (!x.pipe.wait_warp(x.bar(kGbYFull + st), (at / P::kStages) & 1u, kSiteGradMma)) return false;
+    // Y rows outside the sequence may hold anything: zero, so that they add
+    // nothing to the second products
+    const int row0 = it.tile * kGradCols;
+    const int first = kKeys ? -wk.s.start - row0 : 0;  // rows of the sequence: [first, last)
+    const int last = (kKeys ? wk.s.len - wk.s.start : wk.s.len) - row0;
+    if (first > 0 || last < kGradCols) {
+      for (int kb = 0; kb < 2 * NKB; ++kb)
+        for (int i = x.lane; i < kGradCols * 8; i += 32)
+          if ((i >> 3) < first || (i >> 3) >= last)
+            ptx::st_shared_v4(y + kb * kGradBlock + i * 16, 0.0f, 0.0f, 0.0f, 0.0f);
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+    }
+    // the buffer's last P and D have been read
+    if (!x.pipe.wait_warp(x.bar(kGbPFree + buf), ((at / P::kBufs) & 1u) ^ 1u, kSiteGradMma)) return false;
+    ptx::tc_fence_after();
+    const uint32_t y_lo = ptx::smem_desc_lo(y, 16), d = x.tmem + buf * 128u;
+    if (ptx::elect_one()) {
+#pragma unroll
       for (int i = 0; i < 2; ++i)
-        for (int kb = 0; kb < NKB; ++kb) {
-          const MapMul m = i ? mx2 : mx1;
-          ptx::tma_load_4d_hint(base_s + P::kOffX + i * P::kXBytes + kb * kBlockBytes, i ? tm_x2 : tm_x1,
-                                bar(kGbXFull), kb * 64, wk.row0, wk.h * m.h, wk.b * m.b, once);
+#pragma unroll
+        for (int ks = 0; ks < 4 * NKB; ++ks) {
+          const uint32_t x_off = (i * P::kXBytes + (ks >> 2) * kBlockBytes + (ks & 3) * 32) >> 4;
+          const uint32_t y_off = (i * P::kYBytes + (ks >> 2) * kGradBlock + (ks & 3) * 32) >> 4;
+          if (ks < ksteps)
+            ptx::mma_ss(d + i * 64u, ptx::smem_desc_join(x_lo + x_off, hi), ptx::smem_desc_join(y_lo + y_off, hi),
+                        idesc, ks > 0);
         }
-      int n = 0;
-      for (; n < wk.n; ++n) {
-        const int st = n % S;
-        if (!pipe.wait(bar(kGbYEmpty + st), (static_cast<uint32_t>(n / S) & 1u) ^ 1u, kSiteGradLoad)) break;
-        ptx::mbar_arrive_expect_tx(bar(kGbYFull + st), 2 * P::kYBytes + (kKeys ? kGradStat * 4 : 0));
-        int g;
-        const int tile = wk.tile(n, &g);
-        const int h = kKeys ? wk.h * group + g : wk.h / group;
-        for (int i = 0; i < 2; ++i)
-          for (int kb = 0; kb < NKB; ++kb) {
-            const MapMul m = i ? my2 : my1;
-            ptx::tma_load_4d_hint(stage(n) + i * P::kYBytes + kb * kGradBlock, i ? tm_y2 : tm_y1,
-                                  bar(kGbYFull + st), kb * 64, tile * kGradCols, h * m.h, wk.b * m.b, keep);
-          }
+      ptx::mma_commit(x.bar(kGbSFull + buf));
+      if (n + 1 == wk.n) ptx::mma_commit(x.bar(kGbXEmpty));
+    }
+  }
+  return true;
+}
+
+// keys: dV += P Y2, dK += D Y1;  queries: dQ += D Y1.
+template <typename T, int NKB, bool kKeys>
+__device__ __forceinline__ bool grad_sums(const GradCtx& x, int block, uint32_t& at, uint32_t& tiles) {
+  using P = GradPlan<NKB>;
+  const WindowGradParams& p = x.p;
+  const GradWalk<kKeys> wk = grad_walk<kKeys>(p, block);
+  if (wk.n == 0) return true;
+  const uint32_t idesc =
+      ptx::idesc_16bit_f32(kTile, static_cast<uint32_t>((p.w.dim + 15) >> 4) * 16u, true, Elem<T>::kBf16);
+  constexpr uint32_t hi = ptx::smem_desc_hi(1024, ptx::kSwizzle128B);
+  // the last tile's sums have been read
+  if (!x.pipe.wait_warp(x.bar(kGbSumFree), (tiles & 1u) ^ 1u, kSiteGradMma)) return false;
+  ++tiles;
+  for (int n = 0; n < wk.n; ++n, ++at) {
+    const uint32_t st = at % P::kStages, buf = at % P::kBufs;
+    if (!x.pipe.wait_warp(x.bar(kGbYFull + st), (at / P::kStages) & 1u, kSiteGradMma)) return false;
+    if (!x.pipe.wait_warp(x.bar(kGbPFull + buf), (at / P::kBufs) & 1u, kSiteGradMma)) return false;
+    ptx::tc_fence_after();
+    const uint32_t y1 = ptx::smem_desc_lo(x.base_s + P::kOffY + st * P::kStageBytes, kGradBlock);
+    const uint32_t y2 = y1 + (P::kYBytes >> 4);
+    const uint32_t a = x.tmem + buf * 128u, d = x.tmem + P::kColSum;
+    if (ptx::elect_one()) {
+#pragma unroll
+      for (int ks = 0; ks < kGradCols / 16; ++ks) {
         if (kKeys)
-          ptx::bulk_load(stage(n) + 2 * P::kYBytes,
-                         p.stat + ((static_cast<long long>(wk.b) * p.w.heads + h) * p.stat_tiles + tile) * kGradStat,
-                         kGradStat * 4, bar(kGbYFull + st));
+          ptx::mma_ts(d, a + ks * 8u, ptx::smem_desc_join(y2 + ks * (2048u >> 4), hi), idesc, n > 0 || ks > 0);
+        ptx::mma_ts(d + P::kSumCols, a + 64u + ks * 8u, ptx::smem_desc_join(y1 + ks * (2048u >> 4), hi), idesc,
+                    n > 0 || ks > 0);
       }
-      pipe.drain(bar(kGbXFull), 0, kSiteGradDrain);
-      for (int d = n > S ? n - S : 0; d < n; ++d)
-        pipe.drain(bar(kGbYFull + d % S), static_cast<uint32_t>(d / S) & 1u, kSiteGradDrain);
-    } else if (warp == 1 && wk.n > 0) {
-      // --------------------------------------------------------- MMA issue
-      const int ksteps = (p.w.dim + 15) >> 4;
-      const uint32_t idesc_s = ptx::idesc_16bit_f32(kTile, kGradCols, false, Elem<T>::kBf16);
-      const uint32_t idesc_a = ptx::idesc_16bit_f32(kTile, static_cast<uint32_t>(ksteps) * 16u, true, Elem<T>::kBf16);
-      constexpr uint32_t hi = ptx::smem_desc_hi(1024, ptx::kSwizzle128B);
-      auto issue_s = [&](int n) -> bool {
-        if (!pipe.wait_warp(bar(kGbYFull + n % S), static_cast<uint32_t>(n / S) & 1u, kSiteGradMma)) return false;
-        // Y rows outside the sequence may hold anything: zero, so that they
-        // add nothing to the second products
-        int g;
-        const int row0 = wk.tile(n, &g) * kGradCols;
-        const int first = kKeys ? -wk.s.start - row0 : 0;            // rows of the sequence: [first, last)
-        const int last = (kKeys ? wk.s.len - wk.s.start : wk.s.len) - row0;
-        if (first > 0 || last < kGradCols) {
-          for (int kb = 0; kb < 2 * NKB; ++kb)
-            for (int i = lane; i < kGradCols * 8; i += 32)
-              if ((i >> 3) < first || (i >> 3) >= last)
-                ptx::st_shared_v4(stage(n) + kb * kGradBlock + i * 16, 0.0f, 0.0f, 0.0f, 0.0f);
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
-        }
-        ptx::tc_fence_after();
-        const uint32_t x_lo = ptx::smem_desc_lo(base_s + P::kOffX, 16), y_lo = ptx::smem_desc_lo(stage(n), 16);
-        const uint32_t d = tmem + (n & 1) * 128u;
-        if (ptx::elect_one()) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int ks = 0; ks < 4 * NKB; ++ks) {
-              const uint32_t x_off = (i * P::kXBytes + (ks >> 2) * kBlockBytes + (ks & 3) * 32) >> 4;
-              const uint32_t y_off = (i * P::kYBytes + (ks >> 2) * kGradBlock + (ks & 3) * 32) >> 4;
-              if (ks < ksteps)
-                ptx::mma_ss(d + i * 64u, ptx::smem_desc_join(x_lo + x_off, hi), ptx::smem_desc_join(y_lo + y_off, hi),
-                            idesc_s, ks > 0);
-            }
-          ptx::mma_commit(bar(kGbSFull + (n & 1)));
-        }
-        return true;
-      };
-      bool ok = pipe.wait_warp(bar(kGbXFull), 0, kSiteGradMma);
-      for (int n = 0; ok && n < 2 && n < wk.n; ++n) ok = issue_s(n);
-      for (int n = 0; ok && n < wk.n; ++n) {
-        const int b = n & 1;
-        if (!(ok = pipe.wait_warp(bar(kGbPFull + b), static_cast<uint32_t>(n >> 1) & 1u, kSiteGradMma))) break;
-        ptx::tc_fence_after();
-        const uint32_t y1 = ptx::smem_desc_lo(stage(n), kGradBlock);
-        const uint32_t y2 = ptx::smem_desc_lo(stage(n) + P::kYBytes, kGradBlock);
-        if (ptx::elect_one()) {
-#pragma unroll
-          for (int ks = 0; ks < kGradCols / 16; ++ks) {
-            if (kKeys)
-              ptx::mma_ts(tmem + 256u, tmem + b * 128u + ks * 8u, ptx::smem_desc_join(y2 + ks * (2048u >> 4), hi),
-                          idesc_a, n > 0 || ks > 0);
-            ptx::mma_ts(tmem + 384u, tmem + b * 128u + 64u + ks * 8u,
-                        ptx::smem_desc_join(y1 + ks * (2048u >> 4), hi), idesc_a, n > 0 || ks > 0);
-          }
-          ptx::mma_commit(bar(kGbYEmpty + n % S));
-        }
-        if (n + 2 < wk.n) ok = issue_s(n + 2);
-      }
-      if (ptx::elect_one()) ptx::mma_commit(bar(kGbAcc));
+      ptx::mma_commit(x.bar(kGbPFree + buf));
+      ptx::mma_commit(x.bar(kGbYEmpty + st));
+      if (n + 1 == wk.n) ptx::mma_commit(x.bar(kGbSum));
     }
-  } else {
-    ptx::regs_increase<P::kRegsMath>();
-    // ------------------------------------------------- P and D, then results
-    const int wg = (warp - 4) >> 2;
-    const int r = (warp & 3) * 32 + lane;
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t s_addr = tmem + lanes + wg * 128u, g_addr = s_addr + 64u;
-    const int row = wk.row0 + r;  // key, or query row of the call
-    const int W = p.w.window;
-    float row_lse = -INFINITY, row_delta = 0.0f;
-    if (!kKeys && wk.n > 0) {
-      const float* st = p.stat + ((static_cast<long long>(wk.b) * p.w.heads + wk.h) * p.stat_tiles +
-                                  row / kGradCols) * kGradStat + row % kGradCols;
-      row_lse = st[0];
-      row_delta = st[kGradCols];
-    }
-    const float2 scale = make_float2(p.scale_log2, p.scale_log2);
-    bool ok = true;
-    for (int n = wg; n < wk.n; n += 2) {
-      int gh;
-      const int y0 = wk.tile(n, &gh) * kGradCols;
-      if (!(ok = pipe.wait_warp(bar(kGbSFull + wg), static_cast<uint32_t>(n >> 1) & 1u, kSiteGradSoft))) break;
+  }
+  return true;
+}
+
+// P and D of every other item, then the X tile's results (one warpgroup).
+template <typename T, int NKB, bool kKeys>
+__device__ __forceinline__ bool grad_math(const GradCtx& x, int block, uint32_t& at, uint32_t& tiles) {
+  using P = GradPlan<NKB>;
+  const WindowGradParams& p = x.p;
+  const GradWalk<kKeys> wk = grad_walk<kKeys>(p, block);
+  const int wg = (x.warp - 4) >> 2;
+  const int r = (x.warp & 3) * 32 + x.lane;
+  const uint32_t lanes = static_cast<uint32_t>((x.warp & 3) * 32) << 16;
+  const int row = wk.row0 + r;  // key, or query row of the call
+  const int W = p.w.window;
+  float row_lse = -INFINITY, row_delta = 0.0f;
+  if (!kKeys && wk.n > 0) {
+    const float* st = p.stat + ((static_cast<long long>(wk.b) * p.w.heads + wk.h) * p.stat_tiles + row / kGradCols) *
+                                   kGradStat + row % kGradCols;
+    row_lse = st[0];
+    row_delta = st[kGradCols];
+  }
+  const float2 scale = make_float2(p.scale_log2, p.scale_log2);
+  const uint32_t end = at + static_cast<uint32_t>(wk.n);
+  uint32_t n = at + ((at ^ static_cast<uint32_t>(wg)) & 1u);  // this warpgroup's items have its parity
+  if (wk.n > 0) {
+    GradItem<kKeys> it(wk, static_cast<int>(n - at));
+    for (; n < end; n += 2, it.step(wk, 2)) {
+      const uint32_t buf = n % P::kBufs;
+      const uint32_t s_addr = x.tmem + lanes + buf * 128u, g_addr = s_addr + 64u;
+      const int y0 = it.tile * kGradCols;
+      if (!x.pipe.wait_warp(x.bar(kGbSFull + buf), (n / P::kBufs) & 1u, kSiteGradSoft)) return false;
       ptx::tc_fence_after();
       uint32_t s[2][32], g[2][32];
 #pragma unroll
@@ -396,6 +438,7 @@ __device__ __forceinline__ void grad_block(const CUtensorMap* tm_x1, const CUten
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const uint32_t see = (bits_upto(c_hi, c) & ~bits_upto(c_lo - 1, c)) | bits_upto(c_sink, c);
+          if (__all_sync(0xffffffffu, see == 0xffffffffu)) continue;
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (!((see >> e) & 1u)) {
@@ -404,7 +447,7 @@ __device__ __forceinline__ void grad_block(const CUtensorMap* tm_x1, const CUten
             }
         }
       }
-      const uint32_t stats = stage(n) + 2 * P::kYBytes;
+      const uint32_t stats = x.base_s + P::kOffY + (n % P::kStages) * P::kStageBytes + 2 * P::kYBytes;
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -437,61 +480,59 @@ __device__ __forceinline__ void grad_block(const CUtensorMap* tm_x1, const CUten
       }
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
-      pipe_warp_arrive(bar(kGbPFull + wg));
-    }
-    // keys: warpgroup 0 stores dV (unscaled), 1 dK; queries: each every other 16 columns of dQ
-    if (ok && wk.n > 0) ok = pipe.wait_warp(bar(kGbAcc), 0, kSiteGradOut);
-    if (ok) {
-      ptx::tc_fence_after();
-      const int D = p.w.dim;
-      const uint32_t a_addr = tmem + lanes + (kKeys && wg == 0 ? 256u : 384u);
-      const bool live = wk.n > 0 && (kKeys ? row < wk.s.len : (wk.s.start + row >= 0 && wk.s.start + row < wk.s.len));
-      const float f = kKeys && wg == 0 ? 1.0f : p.w.scale;
-      const bool store = row < (kKeys ? p.w.n_keys : p.w.n_queries);
-      T* to = nullptr;
-      float* part = nullptr;
-      if (wk.slot >= 0) part = p.part + ((wk.slot * 2LL + wg) * kTile + r) * D;
-      else if (store) to = rows_at_mut<T>(kKeys ? (wg == 0 ? p.dv : p.dk) : p.dq, wk.b, wk.h, row);
-      for (int c = kKeys ? 0 : wg * 16; c < D; c += kKeys ? 16 : 32) {
-        uint32_t y[16];
-        if (wk.n > 0) {
-          ptx::tmem_ld_32x32b_x16(a_addr + c, y);
-          ptx::tmem_wait_ld_dep16(y);
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) y[e] = live ? __float_as_uint(__uint_as_float(y[e]) * f) : 0u;
-        if (part != nullptr) {
-#pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            if (c + e < D) *reinterpret_cast<uint4*>(part + c + e) = make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
-        } else if (to != nullptr) {
-#pragma unroll
-          for (int e = 0; e < 16; e += 8)
-            if (c + e < D) {
-              uint32_t h[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                h[k] = pack2<T>(__uint_as_float(y[e + 2 * k]), __uint_as_float(y[e + 2 * k + 1]));
-              *reinterpret_cast<uint4*>(to + c + e) = make_uint4(h[0], h[1], h[2], h[3]);
-            }
-        }
-      }
+      pipe_warp_arrive(x.bar(kGbPFull + buf));
     }
   }
-
-  ptx::tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
-    if (lane == 0 && wk.n > 0) pipe.drain(bar(kGbAcc), 0, kSiteGradDrain);
-    __syncwarp();
+  at = end;
+  // keys: warpgroup 0 stores dV (unscaled), 1 dK; queries: each every other 16 columns of dQ
+  if (wk.n > 0) {
+    if (!x.pipe.wait_warp(x.bar(kGbSum), tiles & 1u, kSiteGradOut)) return false;
+    ++tiles;
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, 512);
   }
+  const int D = p.w.dim;
+  const uint32_t a_addr = x.tmem + lanes + P::kColSum + (kKeys && wg == 0 ? 0u : P::kSumCols);
+  const bool live = wk.n > 0 && (kKeys ? row < wk.s.len : (wk.s.start + row >= 0 && wk.s.start + row < wk.s.len));
+  const float f = kKeys && wg == 0 ? 1.0f : p.w.scale;
+  const bool store = row < (kKeys ? p.w.n_keys : p.w.n_queries);
+  T* to = nullptr;
+  float* part = nullptr;
+  if (wk.slot >= 0) part = p.part + ((wk.slot * 2LL + wg) * kTile + r) * D;
+  else if (store) to = rows_at_mut<T>(kKeys ? (wg == 0 ? p.dv : p.dk) : p.dq, wk.b, wk.h, row);
+  for (int c = kKeys ? 0 : wg * 16; c < D; c += kKeys ? 16 : 32) {
+    uint32_t y[16];
+    if (wk.n > 0) {
+      ptx::tmem_ld_32x32b_x16(a_addr + c, y);
+      ptx::tmem_wait_ld_dep16(y);
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) y[e] = live ? __float_as_uint(__uint_as_float(y[e]) * f) : 0u;
+    if (part != nullptr) {
+#pragma unroll
+      for (int e = 0; e < 16; e += 4)
+        if (c + e < D) *reinterpret_cast<uint4*>(part + c + e) = make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+    } else if (to != nullptr) {
+#pragma unroll
+      for (int e = 0; e < 16; e += 8)
+        if (c + e < D) {
+          uint32_t h[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            h[k] = pack2<T>(__uint_as_float(y[e + 2 * k]), __uint_as_float(y[e + 2 * k + 1]));
+          *reinterpret_cast<uint4*>(to + c + e) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+    }
+  }
+  if (wk.n > 0) {
+    ptx::tc_fence_before();
+    pipe_warp_arrive(x.bar(kGbSumFree));
+  }
+  return true;
 }
 
-// Key tiles first, then the query tiles: their blocks are shorter and fill
-// the multiprocessors that the last key tiles leave idle.  tm_*: tiles of 128
-// rows (x) and of 64 (y).
+// X tiles blockIdx.x, + gridDim.x, ...: key tiles first, then the query
+// tiles, which are shorter and even out what the key tiles leave.  tm_*:
+// boxes of 128 rows (x) and of 64 (y).
 template <typename T, int NKB>
 __global__ void __launch_bounds__(GradPlan<NKB>::kThreads, 1)
     vattn_window_bwd_kernel(const __grid_constant__ CUtensorMap tm_qx, const __grid_constant__ CUtensorMap tm_gx,
@@ -499,11 +540,84 @@ __global__ void __launch_bounds__(GradPlan<NKB>::kThreads, 1)
                             const __grid_constant__ CUtensorMap tm_qy, const __grid_constant__ CUtensorMap tm_gy,
                             const __grid_constant__ CUtensorMap tm_ky, const __grid_constant__ CUtensorMap tm_vy,
                             const __grid_constant__ WindowGradParams p) {
-  const int block = static_cast<int>(blockIdx.x);
-  if (block < p.key_blocks)
-    grad_block<T, NKB, true>(&tm_kx, &tm_vx, &tm_qy, &tm_gy, p.mk, p.mv, p.mq, p.mg, p, block);
-  else
-    grad_block<T, NKB, false>(&tm_qx, &tm_gx, &tm_ky, &tm_vy, p.mq, p.mg, p.mk, p.mv, p, block - p.key_blocks);
+  using P = GradPlan<NKB>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_s = ptx::smem_addr(smem_raw);
+  const uint32_t base_s = (raw_s + 1023u) & ~1023u;
+  uint8_t* const base = smem_raw + (base_s - raw_s);
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(base + P::kOffBar + 8 * kGbCount);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  const uint32_t bar0 = base_s + P::kOffBar;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    auto init = [bar0](int i, uint32_t count) { ptx::mbar_init(bar0 + 8u * static_cast<uint32_t>(i), count); };
+    init(kGbXFull, 1);
+    init(kGbXEmpty, 1);
+    for (int i = 0; i < P::kStages; ++i) {
+      init(kGbYFull + i, 1);
+      init(kGbYEmpty + i, 1);
+    }
+    for (int i = 0; i < P::kBufs; ++i) {
+      init(kGbSFull + i, 1);
+      init(kGbPFull + i, 4);
+      init(kGbPFree + i, 1);
+    }
+    init(kGbSum, 1);
+    init(kGbSumFree, 8);
+    init(kGbDoneS, 2);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_addr(const_cast<uint32_t*>(tmem_slot)), 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const GradCtx x{p, Pipe{abort_flag, p.status}, base_s, bar0, *tmem_slot, warp, lane};
+  ptx::grid_dep_wait();
+  uint32_t at = 0, tiles = 0;
+  bool ok = true;
+  if (warp < 4) {
+    ptx::regs_decrease<P::kRegsOther>();
+    if (warp == 0 && lane == 0) {
+      for (int block = blockIdx.x; ok && block < p.blocks; block += gridDim.x) {
+        if (block < p.key_blocks)
+          ok = grad_load<NKB, true>(x, &tm_kx, &tm_vx, &tm_qy, &tm_gy, p.mk, p.mv, p.mq, p.mg, block, at, tiles);
+        else
+          ok = grad_load<NKB, false>(x, &tm_qx, &tm_gx, &tm_ky, &tm_vy, p.mq, p.mg, p.mk, p.mv, block, at, tiles);
+      }
+      // every copy has landed before the block exits
+      if (tiles > 0) x.pipe.drain(x.bar(kGbXFull), (tiles - 1) & 1u, kSiteGradDrain);
+      for (uint32_t d = at > P::kStages ? at - P::kStages : 0; d < at; ++d)
+        x.pipe.drain(x.bar(kGbYFull + d % P::kStages), (d / P::kStages) & 1u, kSiteGradDrain);
+    } else if (warp == 1) {
+      for (int block = blockIdx.x; ok && block < p.blocks; block += gridDim.x)
+        ok = block < p.key_blocks ? grad_scores<T, NKB, true>(x, block, at, tiles)
+                                  : grad_scores<T, NKB, false>(x, block, at, tiles);
+      if (ptx::elect_one()) ptx::mma_commit(x.bar(kGbDoneS));
+    } else if (warp == 2) {
+      for (int block = blockIdx.x; ok && block < p.blocks; block += gridDim.x)
+        ok = block < p.key_blocks ? grad_sums<T, NKB, true>(x, block, at, tiles)
+                                  : grad_sums<T, NKB, false>(x, block, at, tiles);
+      if (ptx::elect_one()) ptx::mma_commit(x.bar(kGbDoneS));
+    }
+  } else {
+    ptx::regs_increase<P::kRegsMath>();
+    for (int block = blockIdx.x; ok && block < p.blocks; block += gridDim.x)
+      ok = block < p.key_blocks ? grad_math<T, NKB, true>(x, block, at, tiles)
+                                : grad_math<T, NKB, false>(x, block, at, tiles);
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    if (lane == 0) x.pipe.drain(x.bar(kGbDoneS), 0, kSiteGradDrain);
+    __syncwarp();
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(x.tmem, 512);
+  }
 }
 
 // dk and dv of the key tiles that were cut: their chunks' partial sums added
