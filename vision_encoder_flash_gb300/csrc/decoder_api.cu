@@ -478,15 +478,15 @@ vattn_status backward_window(const Tensor& tg, const Tensor& tq, const Tensor& t
   // is cut so that no block has more than a third of a multiprocessor's share
   // of the call (the walk over query tiles is about as long as that over key
   // tiles; without a window a tile sees half the rows on average), but not
-  // under 8 items.
-  const long long all_items = static_cast<long long>(p.w.group) * ((p.w.n_queries + kGradCols - 1) / kGradCols);
+  // under 4 items.
+  const long long all_items = static_cast<long long>(p.w.group) * row_tiles;
   const long long items = std::min<long long>(
-      all_items, static_cast<long long>(p.w.group) * ((static_cast<long long>(p.w.window) + kTile - 1) / kGradCols + 2));
+      all_items, static_cast<long long>(p.w.group) * ((static_cast<long long>(p.w.window) + kTile - 2) / kTile + 1));
   p.sink_tiles = items < all_items ? std::min(p.key_tiles, (p.w.sinks - 1) / kTile + (p.w.sinks > 0)) : 0;
   const long long bhs = static_cast<long long>(p.w.batch) * p.w.heads;
   const long long key_tiles = std::max<long long>(1, seqs * p.key_tiles), query_tiles = bhs * row_tiles;
   const double total = static_cast<double>(key_tiles) * static_cast<double>(items) * (items < all_items ? 2.0 : 1.0);
-  const long long most = std::max(8LL, static_cast<long long>(total / (3.0 * sms)));
+  const long long most = std::max(4LL, static_cast<long long>(total / (3.0 * sms)));
   auto cut = [most](long long n) { return static_cast<int>(std::max(1LL, std::min(256LL, (n + most - 1) / most))); };
   p.chunks = cut(items);
   p.sink_chunks = p.sink_tiles > 0 ? cut(all_items) : 1;

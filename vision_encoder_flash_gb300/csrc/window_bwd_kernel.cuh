@@ -11,23 +11,29 @@
 // fixed and the same call gives the same bits.
 //
 // Both walks are one kernel body: a block keeps a 128-row tile X (keys: K
-// and V; queries: Q and dout) and streams 64-row tiles Y of the other side
+// and V; queries: Q and dout) and streams 128-row tiles Y of the other side
 // that its rows see:
-//   S = X1 Y1^T, G = X2 Y2^T           (128 x 64, f32 in TMEM)
+//   S = X1 Y1^T, G = X2 Y2^T           (128 x 128 each, f32 in TMEM)
 //   P = 2^(S scale log2e - lse2), D = P (G - delta), rounded to the type
 //   keys:     dV += P Y2, dK += D Y1     queries:  dQ += D Y1
-// P and D overwrite S and G in TMEM and are the A operands of the second
-// products; Y is read K-major for the first and MN-major for the second, so
-// nothing is transposed.  The grid is one block per multiprocessor, each
-// walking over X tiles, key tiles (longer) first:
-//   warp 0   X and Y tiles by TMA (Y through a ring, ahead across X tiles)
-//   warp 1   issues S and G of item n into buffer n mod NB
+// P and D overwrite S in TMEM and are the A operands of the second products;
+// Y is read K-major for the first and MN-major for the second, so nothing is
+// transposed.  The grid is one block per multiprocessor, each walking over X
+// tiles, key tiles (longer) first:
+//   warp 0   X and Y tiles by TMA; Y through a ring of half tiles (64 rows),
+//            ahead across X tiles
+//   warp 1   issues G, then S of each tile (128 columns a product: a 128 x 64
+//            one takes 50 cycles, a 128 x 128 one 65)
 //   warp 2   issues the second products once P and D are there; an issuing
-//            thread is held while its products run, so with two of them S and
-//            G of later items run between
-//   warps 4-7, 8-11   P and D of every other item, then the tile's results
-// TMEM (512 columns): NB buffers of S and G (64 columns each) from 0, three up
-// to head_dim 64, two above; the sums behind them.
+//            thread is held while its products run, so with two of them the
+//            next tile's G and S run between
+//   warps 4-7, 8-11   P and D of columns 0..63, 64..127 of every tile, then
+//            the X tile's results
+// G is overwritten as soon as it is in registers, S once its P and D have
+// been used.  TMEM columns (512), A: S, then P and D; B: G:
+//   head_dim <= 64         A 0 and 128 in turn, B 256, dV 384, dK / dQ 448
+//   above, X of keys       A 0, B 128, dV 256, dK 384
+//   above, X of queries    A 0 and 256 in turn, B 128, dQ 384
 //
 // A key tile's walk is cut into chunks (f32 partial sums in a workspace,
 // added in order by vattn_window_join_kernel) where tiles are few or, for the
@@ -41,9 +47,9 @@
 
 namespace vattn {
 
-constexpr int kGradCols = 64;                       // rows of a Y tile
-constexpr int kGradBlock = kGradCols * 128;         // 64 rows x 64 elements, 128-byte swizzle
-constexpr int kGradStat = 2 * kGradCols;            // floats of a tile's -lse2, -delta
+constexpr int kGradCols = 64;                // columns of a math warpgroup, rows of half a Y tile
+constexpr int kGradBlock = kGradCols * 128;  // 64 rows x 64 elements, 128-byte swizzle
+constexpr int kGradStat = 2 * kGradCols;     // floats of half a tile's -lse2, -delta
 
 struct WindowGradParams {
   WindowParams w;
@@ -53,7 +59,7 @@ struct WindowGradParams {
   float* part;     // [slot][dv, dk][128][dim] partial sums of the chunks
   uint32_t* status;
   MapMul mq, mg, mk, mv;  // q, dout, k, v
-  int stat_tiles;  // Y tiles of the queries, to a multiple of two
+  int stat_tiles;  // half tiles (64 rows) of the queries, an even number
   int key_tiles;   // ceil(n_keys / 128)
   int sink_tiles;  // of these, the first with keys < sinks, cut into sink_chunks
   int sink_chunks, chunks;
@@ -64,7 +70,7 @@ struct WindowGradParams {
 
 // -lse2 = -lse log2(e) and -delta of every query row; rows that see nothing
 // (and those that fill the last tile) get -infinity and 0, hence weights 0.
-// A block has one tile of 64 rows; LR lanes, 16 bytes each, hold one row, and
+// A block has half a tile, 64 rows; LR lanes, 16 bytes each, hold one row, and
 // the loads of a lane's LR / 4 rows are all in flight before the sums.
 template <typename T, int LR>
 __global__ void __launch_bounds__(256) vattn_window_stat_kernel(const __grid_constant__ WindowGradParams p) {
@@ -112,25 +118,30 @@ __global__ void __launch_bounds__(256) vattn_window_stat_kernel(const __grid_con
 template <int NKB>
 struct GradPlan {
   static constexpr int kXBytes = NKB * kBlockBytes;
-  static constexpr int kYBytes = NKB * kGradBlock;
-  static constexpr int kStageBytes = 2 * kYBytes + 1024;  // Y1, Y2, the queries' stats
-  static constexpr int kStages = NKB == 1 ? 8 : 4;
+  static constexpr int kYBytes = NKB * kBlockBytes;       // a Y tile: per 64 columns, 128 rows of 128 bytes
+  static constexpr int kSlotBytes = 2 * kYBytes + 1024;   // Y1, Y2, the queries' stats
+  static constexpr int kSlots = NKB == 1 ? 4 : 2;
+  static constexpr int kHalves = 2 * kSlots;              // ring entries: half h of slot e / 2
   static constexpr int kOffX = 0;
   static constexpr int kOffY = 2 * kXBytes;
-  static constexpr int kOffBar = kOffY + kStages * kStageBytes;
+  static constexpr int kOffBar = kOffY + kSlots * kSlotBytes;
   static constexpr int kSmemBytes = kOffBar + 256 + 1024;
   static constexpr int kThreads = 384;
   static constexpr uint32_t kRegsOther = 72, kRegsMath = 216;  // 72 + 2 x 216 = 3 x 168
-  static constexpr int kBufs = NKB == 1 ? 3 : 2;
-  static constexpr uint32_t kColSum = kBufs * 128u;      // dV; behind it dK or dQ
-  static constexpr uint32_t kSumCols = NKB == 1 ? 64u : 128u;
+  static constexpr uint32_t kColG = NKB == 1 ? 256 : 128;
+  static constexpr uint32_t kColDv = NKB == 1 ? 384 : 256;
+  static constexpr uint32_t kColD = NKB == 1 ? 448 : 384;     // dK or dQ
+  // two A columns in turn, or one
+  template <bool kKeys> static constexpr bool kTurns = NKB == 1 || !kKeys;
+  template <bool kKeys> static __device__ __forceinline__ uint32_t col_a(uint32_t tile) {
+    return kTurns<kKeys> && (tile & 1u) ? (NKB == 1 ? 128u : 256u) : 0u;
+  }
   static_assert(kSmemBytes <= 232448, "shared memory");
-  static_assert(kColSum + 2 * kSumCols <= 512, "TMEM");
 };
 
 enum GradBar : int {
-  kGbXFull = 0, kGbXEmpty = 1, kGbYFull = 2, kGbYEmpty = 10, kGbSFull = 18, kGbPFull = 21, kGbPFree = 24,
-  kGbSum = 27, kGbSumFree = 28, kGbDoneS = 29, kGbCount = 30,
+  kGbXFull = 0, kGbXEmpty = 1, kGbYFull = 2, kGbYEmpty = 10, kGbSFull = 18, kGbGFree = 19, kGbPFull = 20,
+  kGbPFree = 22, kGbSum = 24, kGbSumFree = 25, kGbDone = 26, kGbCount = 27,
 };
 
 // What a block walks over: Y tiles 0 .. n - 1 of its share.
@@ -140,12 +151,12 @@ struct GradWalk {
   int row0;         // first row of the X tile
   Seq s;
   int slot;   // of the partial sums, -1: none
-  // keys: item -> head g of the group and query tile; queries: key tiles [0, ns) and [first, ..)
+  // (tiles of 128 rows) keys: item -> head g of the group and query tile; queries: key tiles [0, ns) and [first, ..)
   int first, per_head, begin, n, ns;
 
 };
 
-// Item x of a walk: its Y tile (in units of 64 rows) and query head of the group.
+// Item x of a walk: its Y tile and query head of the group.
 template <bool kKeys>
 struct GradItem {
   int x, g, tile;
@@ -196,8 +207,8 @@ __device__ __forceinline__ GradWalk<true> grad_walk<true>(const WindowGradParams
   const int hi_pos = k.row0 < p.w.sinks ? k.s.len - 1 : min(k.s.len - 1, k.row0 + kTile - 1 + p.w.window - 1);
   const int lo = max(0, k.row0 - k.s.start), hi = min(p.w.n_queries - 1, hi_pos - k.s.start);
   if (k.row0 < k.s.len && hi >= lo) {
-    k.first = lo / kGradCols;
-    k.per_head = hi / kGradCols - k.first + 1;
+    k.first = lo / kTile;
+    k.per_head = hi / kTile - k.first + 1;
     const long long all = static_cast<long long>(k.per_head) * p.w.group;
     k.begin = static_cast<int>(all * chunk / chunks);
     k.n = static_cast<int>(all * (chunk + 1LL) / chunks) - k.begin;
@@ -221,15 +232,15 @@ __device__ __forceinline__ GradWalk<false> grad_walk<false>(const WindowGradPara
   const int lo = max(0, k.s.start + k.row0);
   const int hi = min(k.s.start + min(k.row0 + kTile, p.w.n_queries), k.s.len) - 1;
   if (hi >= lo) {
-    k.first = max(0, lo - p.w.window + 1) / kGradCols;
-    k.ns = min((min(p.w.sinks, k.s.len) + kGradCols - 1) / kGradCols, k.first);
-    k.n = k.ns + hi / kGradCols - k.first + 1;
+    k.first = max(0, lo - p.w.window + 1) / kTile;
+    k.ns = min((min(p.w.sinks, k.s.len) + kTile - 1) / kTile, k.first);
+    k.n = k.ns + hi / kTile - k.first + 1;
   }
   return k;
 }
 
-// The block's roles, one X tile at a time; `at` counts the items (Y tiles) of
-// the block so far, `tiles` its X tiles with items.
+// The block's roles, one X tile at a time; `at` counts the Y tiles of the
+// block so far, `tiles` its X tiles with items.
 struct GradCtx {
   const WindowGradParams& p;
   Pipe pipe;
@@ -249,30 +260,31 @@ __device__ __forceinline__ bool grad_load(const GradCtx& x, const CUtensorMap* t
   if (wk.n == 0) return true;
   const uint64_t keep = ptx::policy_evict_last(), once = ptx::policy_evict_first();
   GradItem<kKeys> it(wk, 0);
-  for (int n = 0; n < wk.n; ++n, ++at, it.step(wk, 1)) {
-    const uint32_t st = at % P::kStages;
-    if (!x.pipe.wait(x.bar(kGbYEmpty + st), ((at / P::kStages) & 1u) ^ 1u, kSiteGradLoad)) return false;
-    ptx::mbar_arrive_expect_tx(x.bar(kGbYFull + st), 2 * P::kYBytes + (kKeys ? kGradStat * 4 : 0));
+  for (int n = 0; n < wk.n; ++n, it.step(wk, 1)) {
     const int h = kKeys ? wk.h * p.w.group + it.g : wk.h / p.w.group;
-    const uint32_t to = x.base_s + P::kOffY + st * P::kStageBytes;
+    for (int half = 0; half < 2; ++half, ++at) {  // at: halves here
+      const uint32_t e = at % P::kHalves;
+      if (!x.pipe.wait(x.bar(kGbYEmpty + e), ((at / P::kHalves) & 1u) ^ 1u, kSiteGradLoad)) return false;
+      ptx::mbar_arrive_expect_tx(x.bar(kGbYFull + e), 2 * NKB * kGradBlock + (kKeys ? kGradStat * 4 : 0));
+      const uint32_t slot = x.base_s + P::kOffY + (e >> 1) * P::kSlotBytes;
+      const int row = it.tile * kTile + half * kGradCols;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int kb = 0; kb < NKB; ++kb) {
-        const MapMul m = i ? my2 : my1;
-        ptx::tma_load_4d_hint(to + i * P::kYBytes + kb * kGradBlock, i ? tm_y2 : tm_y1, x.bar(kGbYFull + st), kb * 64,
-                              it.tile * kGradCols, h * m.h, wk.b * m.b, keep);
-      }
-    if (kKeys)
-      ptx::bulk_load(to + 2 * P::kYBytes,
-                     p.stat + ((static_cast<long long>(wk.b) * p.w.heads + h) * p.stat_tiles + it.tile) * kGradStat,
-                     kGradStat * 4, x.bar(kGbYFull + st));
-    if (n > 0) continue;
-    // X behind the first Y: it waits for the last tile's S and G
-    if (!x.pipe.wait(x.bar(kGbXEmpty), (tiles & 1u) ^ 1u, kSiteGradLoad)) {
-      ++at;  // drained with the others
-      return false;
+        for (int kb = 0; kb < NKB; ++kb) {
+          const MapMul m = i ? my2 : my1;
+          ptx::tma_load_4d_hint(slot + i * P::kYBytes + kb * kBlockBytes + half * kGradBlock, i ? tm_y2 : tm_y1,
+                                x.bar(kGbYFull + e), kb * 64, row, h * m.h, wk.b * m.b, keep);
+        }
+      if (kKeys)
+        ptx::bulk_load(slot + 2 * P::kYBytes + half * kGradStat * 4,
+                       p.stat + ((static_cast<long long>(wk.b) * p.w.heads + h) * p.stat_tiles + 2 * it.tile + half) *
+                                    kGradStat,
+                       kGradStat * 4, x.bar(kGbYFull + e));
     }
+    if (n > 0) continue;
+    // X behind the first Y: it waits for the last X tile's S and G
+    if (!x.pipe.wait(x.bar(kGbXEmpty), (tiles & 1u) ^ 1u, kSiteGradLoad)) return false;
     ptx::mbar_arrive_expect_tx(x.bar(kGbXFull), 2 * P::kXBytes);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -287,54 +299,71 @@ __device__ __forceinline__ bool grad_load(const GradCtx& x, const CUtensorMap* t
   return true;
 }
 
-// S = X1 Y1^T, G = X2 Y2^T of every item (a whole warp; one lane issues).
+// G = X2 Y2^T and S = X1 Y1^T of every tile (a whole warp; one lane issues).
+// `keys_before`: the last X tile with items was one of keys.
 template <typename T, int NKB, bool kKeys>
-__device__ __forceinline__ bool grad_scores(const GradCtx& x, int block, uint32_t& at, uint32_t& tiles) {
+__device__ __forceinline__ bool grad_scores(const GradCtx& x, int block, uint32_t& at, uint32_t& tiles,
+                                            bool& keys_before) {
   using P = GradPlan<NKB>;
   const WindowGradParams& p = x.p;
   const GradWalk<kKeys> wk = grad_walk<kKeys>(p, block);
   if (wk.n == 0) return true;
   const int ksteps = (p.w.dim + 15) >> 4;
-  constexpr uint32_t idesc = ptx::idesc_16bit_f32(kTile, kGradCols, false, Elem<T>::kBf16);
+  constexpr uint32_t idesc = ptx::idesc_16bit_f32(kTile, kTile, false, Elem<T>::kBf16);
   constexpr uint32_t hi = ptx::smem_desc_hi(1024, ptx::kSwizzle128B);
   const uint32_t x_lo = ptx::smem_desc_lo(x.base_s + P::kOffX, 16);
   if (!x.pipe.wait_warp(x.bar(kGbXFull), tiles & 1u, kSiteGradMma)) return false;
+  // from keys to queries the second A column takes dV's place: its last sums have been read
+  if (NKB == 2 && !kKeys && keys_before &&
+      !x.pipe.wait_warp(x.bar(kGbSumFree), (tiles - 1) & 1u, kSiteGradMma))
+    return false;
+  keys_before = kKeys;
   ++tiles;
   GradItem<kKeys> it(wk, 0);
   for (int n = 0; n < wk.n; ++n, ++at, it.step(wk, 1)) {
-    const uint32_t st = at % P::kStages, buf = at % P::kBufs;
-    const uint32_t y = x.base_s + P::kOffY + st * P::kStageBytes;
-    if (!x.pipe.wait_warp(x.bar(kGbYFull + st), (at / P::kStages) & 1u, kSiteGradMma)) return false;
+    const uint32_t slot = at % P::kSlots, turn = (at / P::kSlots) & 1u;
+    const uint32_t y = x.base_s + P::kOffY + slot * P::kSlotBytes;
+    if (!x.pipe.wait_warp(x.bar(kGbYFull + 2 * slot), turn, kSiteGradMma) ||
+        !x.pipe.wait_warp(x.bar(kGbYFull + 2 * slot + 1), turn, kSiteGradMma))
+      return false;
     // Y rows outside the sequence may hold anything: zero, so that they add
     // nothing to the second products
-    const int row0 = it.tile * kGradCols;
+    const int row0 = it.tile * kTile;
     const int first = kKeys ? -wk.s.start - row0 : 0;  // rows of the sequence: [first, last)
     const int last = (kKeys ? wk.s.len - wk.s.start : wk.s.len) - row0;
-    if (first > 0 || last < kGradCols) {
+    if (first > 0 || last < kTile) {
       for (int kb = 0; kb < 2 * NKB; ++kb)
-        for (int i = x.lane; i < kGradCols * 8; i += 32)
+        for (int i = x.lane; i < kTile * 8; i += 32)
           if ((i >> 3) < first || (i >> 3) >= last)
-            ptx::st_shared_v4(y + kb * kGradBlock + i * 16, 0.0f, 0.0f, 0.0f, 0.0f);
+            ptx::st_shared_v4(y + kb * kBlockBytes + i * 16, 0.0f, 0.0f, 0.0f, 0.0f);
       ptx::fence_proxy_async_smem();
       __syncwarp();
     }
-    // the buffer's last P and D have been read
-    if (!x.pipe.wait_warp(x.bar(kGbPFree + buf), ((at / P::kBufs) & 1u) ^ 1u, kSiteGradMma)) return false;
-    ptx::tc_fence_after();
-    const uint32_t y_lo = ptx::smem_desc_lo(y, 16), d = x.tmem + buf * 128u;
-    if (ptx::elect_one()) {
+    const uint32_t y_lo = ptx::smem_desc_lo(y, 16);
+    // i = 1: G, once the last one is in registers; i = 0: S, once the P and D there have been used
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+    for (int i = 1; i >= 0; --i) {
+      if (i == 1) {
+        if (at > 0 && !x.pipe.wait_warp(x.bar(kGbGFree), (at - 1) & 1u, kSiteGradMma)) return false;
+      } else {
+        const uint32_t before = P::template kTurns<kKeys> ? 2u : 1u;  // tile `before` back used these columns
+        if (at >= before && !x.pipe.wait_warp(x.bar(kGbPFree + ((at - before) & 1u)), ((at - before) >> 1) & 1u, kSiteGradMma))
+          return false;
+      }
+      ptx::tc_fence_after();
+      const uint32_t d = x.tmem + (i == 1 ? P::kColG : P::template col_a<kKeys>(at));
+      if (ptx::elect_one()) {
 #pragma unroll
         for (int ks = 0; ks < 4 * NKB; ++ks) {
-          const uint32_t x_off = (i * P::kXBytes + (ks >> 2) * kBlockBytes + (ks & 3) * 32) >> 4;
-          const uint32_t y_off = (i * P::kYBytes + (ks >> 2) * kGradBlock + (ks & 3) * 32) >> 4;
+          const uint32_t off = (i * P::kXBytes + (ks >> 2) * kBlockBytes + (ks & 3) * 32) >> 4;
           if (ks < ksteps)
-            ptx::mma_ss(d + i * 64u, ptx::smem_desc_join(x_lo + x_off, hi), ptx::smem_desc_join(y_lo + y_off, hi),
-                        idesc, ks > 0);
+            ptx::mma_ss(d, ptx::smem_desc_join(x_lo + off, hi), ptx::smem_desc_join(y_lo + off, hi), idesc, ks > 0);
         }
-      ptx::mma_commit(x.bar(kGbSFull + buf));
-      if (n + 1 == wk.n) ptx::mma_commit(x.bar(kGbXEmpty));
+        if (i == 0) {
+          ptx::mma_commit(x.bar(kGbSFull));
+          if (n + 1 == wk.n) ptx::mma_commit(x.bar(kGbXEmpty));
+        }
+      }
     }
   }
   return true;
@@ -350,34 +379,39 @@ __device__ __forceinline__ bool grad_sums(const GradCtx& x, int block, uint32_t&
   const uint32_t idesc =
       ptx::idesc_16bit_f32(kTile, static_cast<uint32_t>((p.w.dim + 15) >> 4) * 16u, true, Elem<T>::kBf16);
   constexpr uint32_t hi = ptx::smem_desc_hi(1024, ptx::kSwizzle128B);
-  // the last tile's sums have been read
+  // the last X tile's sums have been read
   if (!x.pipe.wait_warp(x.bar(kGbSumFree), (tiles & 1u) ^ 1u, kSiteGradMma)) return false;
   ++tiles;
   for (int n = 0; n < wk.n; ++n, ++at) {
-    const uint32_t st = at % P::kStages, buf = at % P::kBufs;
-    if (!x.pipe.wait_warp(x.bar(kGbYFull + st), (at / P::kStages) & 1u, kSiteGradMma)) return false;
-    if (!x.pipe.wait_warp(x.bar(kGbPFull + buf), (at / P::kBufs) & 1u, kSiteGradMma)) return false;
+    const uint32_t slot = at % P::kSlots, turn = (at / P::kSlots) & 1u;
+    if (!x.pipe.wait_warp(x.bar(kGbYFull + 2 * slot), turn, kSiteGradMma) ||
+        !x.pipe.wait_warp(x.bar(kGbYFull + 2 * slot + 1), turn, kSiteGradMma) ||
+        !x.pipe.wait_warp(x.bar(kGbPFull + (at & 1u)), (at >> 1) & 1u, kSiteGradMma))
+      return false;
     ptx::tc_fence_after();
-    const uint32_t y1 = ptx::smem_desc_lo(x.base_s + P::kOffY + st * P::kStageBytes, kGradBlock);
+    const uint32_t y1 = ptx::smem_desc_lo(x.base_s + P::kOffY + slot * P::kSlotBytes, kBlockBytes);
     const uint32_t y2 = y1 + (P::kYBytes >> 4);
-    const uint32_t a = x.tmem + buf * 128u, d = x.tmem + P::kColSum;
+    const uint32_t a = x.tmem + P::template col_a<kKeys>(at);
     if (ptx::elect_one()) {
 #pragma unroll
-      for (int ks = 0; ks < kGradCols / 16; ++ks) {
+      for (int ks = 0; ks < kTile / 16; ++ks) {
+        const uint32_t a_ks = a + (ks >> 2) * 64u + (ks & 3) * 8u;  // P of columns 16 ks ..; D 32 further
         if (kKeys)
-          ptx::mma_ts(d, a + ks * 8u, ptx::smem_desc_join(y2 + ks * (2048u >> 4), hi), idesc, n > 0 || ks > 0);
-        ptx::mma_ts(d + P::kSumCols, a + 64u + ks * 8u, ptx::smem_desc_join(y1 + ks * (2048u >> 4), hi), idesc,
+          ptx::mma_ts(x.tmem + P::kColDv, a_ks, ptx::smem_desc_join(y2 + ks * (2048u >> 4), hi), idesc,
+                      n > 0 || ks > 0);
+        ptx::mma_ts(x.tmem + P::kColD, a_ks + 32u, ptx::smem_desc_join(y1 + ks * (2048u >> 4), hi), idesc,
                     n > 0 || ks > 0);
+        if (ks == 3) ptx::mma_commit(x.bar(kGbYEmpty + 2 * slot));
       }
-      ptx::mma_commit(x.bar(kGbPFree + buf));
-      ptx::mma_commit(x.bar(kGbYEmpty + st));
+      ptx::mma_commit(x.bar(kGbYEmpty + 2 * slot + 1));
+      ptx::mma_commit(x.bar(kGbPFree + (at & 1u)));
       if (n + 1 == wk.n) ptx::mma_commit(x.bar(kGbSum));
     }
   }
   return true;
 }
 
-// P and D of every other item, then the X tile's results (one warpgroup).
+// P and D of 64 columns of every tile, then the X tile's results (one warpgroup).
 template <typename T, int NKB, bool kKeys>
 __device__ __forceinline__ bool grad_math(const GradCtx& x, int block, uint32_t& at, uint32_t& tiles) {
   using P = GradPlan<NKB>;
@@ -396,15 +430,13 @@ __device__ __forceinline__ bool grad_math(const GradCtx& x, int block, uint32_t&
     row_delta = st[kGradCols];
   }
   const float2 scale = make_float2(p.scale_log2, p.scale_log2);
-  const uint32_t end = at + static_cast<uint32_t>(wk.n);
-  uint32_t n = at + ((at ^ static_cast<uint32_t>(wg)) & 1u);  // this warpgroup's items have its parity
   if (wk.n > 0) {
-    GradItem<kKeys> it(wk, static_cast<int>(n - at));
-    for (; n < end; n += 2, it.step(wk, 2)) {
-      const uint32_t buf = n % P::kBufs;
-      const uint32_t s_addr = x.tmem + lanes + buf * 128u, g_addr = s_addr + 64u;
-      const int y0 = it.tile * kGradCols;
-      if (!x.pipe.wait_warp(x.bar(kGbSFull + buf), (n / P::kBufs) & 1u, kSiteGradSoft)) return false;
+    GradItem<kKeys> it(wk, 0);
+    for (int n = 0; n < wk.n; ++n, ++at, it.step(wk, 1)) {
+      const uint32_t s_addr = x.tmem + lanes + P::template col_a<kKeys>(at) + wg * 64u;
+      const uint32_t g_addr = x.tmem + lanes + P::kColG + wg * 64u;
+      const int y0 = it.tile * kTile + wg * kGradCols;
+      if (!x.pipe.wait_warp(x.bar(kGbSFull), at & 1u, kSiteGradSoft)) return false;
       ptx::tc_fence_after();
       uint32_t s[2][32], g[2][32];
 #pragma unroll
@@ -417,6 +449,8 @@ __device__ __forceinline__ bool grad_math(const GradCtx& x, int block, uint32_t&
         ptx::tmem_wait_ld_dep(s[c]);
         ptx::tmem_wait_ld_dep(g[c]);
       }
+      ptx::tc_fence_before();
+      pipe_warp_arrive(x.bar(kGbGFree));
       // columns [c_lo, c_hi] of the row are visible, and those <= c_sink
       int c_lo, c_hi, c_sink = -1;
       bool full;
@@ -447,7 +481,7 @@ __device__ __forceinline__ bool grad_math(const GradCtx& x, int block, uint32_t&
             }
         }
       }
-      const uint32_t stats = x.base_s + P::kOffY + (n % P::kStages) * P::kStageBytes + 2 * P::kYBytes;
+      const uint32_t stats = x.base_s + P::kOffY + (at % P::kSlots) * P::kSlotBytes + 2 * P::kYBytes + wg * kGradStat * 4;
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -476,14 +510,13 @@ __device__ __forceinline__ bool grad_math(const GradCtx& x, int block, uint32_t&
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         if (kKeys) ptx::tmem_st_32x32b_x16(s_addr + c * 16, *reinterpret_cast<uint32_t(*)[16]>(s[c]));
-        ptx::tmem_st_32x32b_x16(g_addr + c * 16, *reinterpret_cast<uint32_t(*)[16]>(g[c]));
+        ptx::tmem_st_32x32b_x16(s_addr + 32 + c * 16, *reinterpret_cast<uint32_t(*)[16]>(g[c]));
       }
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
-      pipe_warp_arrive(x.bar(kGbPFull + buf));
+      pipe_warp_arrive(x.bar(kGbPFull + (at & 1u)));
     }
   }
-  at = end;
   // keys: warpgroup 0 stores dV (unscaled), 1 dK; queries: each every other 16 columns of dQ
   if (wk.n > 0) {
     if (!x.pipe.wait_warp(x.bar(kGbSum), tiles & 1u, kSiteGradOut)) return false;
@@ -491,7 +524,7 @@ __device__ __forceinline__ bool grad_math(const GradCtx& x, int block, uint32_t&
     ptx::tc_fence_after();
   }
   const int D = p.w.dim;
-  const uint32_t a_addr = x.tmem + lanes + P::kColSum + (kKeys && wg == 0 ? 0u : P::kSumCols);
+  const uint32_t a_addr = x.tmem + lanes + (kKeys && wg == 0 ? P::kColDv : P::kColD);
   const bool live = wk.n > 0 && (kKeys ? row < wk.s.len : (wk.s.start + row >= 0 && wk.s.start + row < wk.s.len));
   const float f = kKeys && wg == 0 ? 1.0f : p.w.scale;
   const bool store = row < (kKeys ? p.w.n_keys : p.w.n_queries);
@@ -553,18 +586,19 @@ __global__ void __launch_bounds__(GradPlan<NKB>::kThreads, 1)
     auto init = [bar0](int i, uint32_t count) { ptx::mbar_init(bar0 + 8u * static_cast<uint32_t>(i), count); };
     init(kGbXFull, 1);
     init(kGbXEmpty, 1);
-    for (int i = 0; i < P::kStages; ++i) {
+    for (int i = 0; i < P::kHalves; ++i) {
       init(kGbYFull + i, 1);
       init(kGbYEmpty + i, 1);
     }
-    for (int i = 0; i < P::kBufs; ++i) {
-      init(kGbSFull + i, 1);
-      init(kGbPFull + i, 4);
+    init(kGbSFull, 1);
+    init(kGbGFree, 8);
+    for (int i = 0; i < 2; ++i) {
+      init(kGbPFull + i, 8);
       init(kGbPFree + i, 1);
     }
     init(kGbSum, 1);
     init(kGbSumFree, 8);
-    init(kGbDoneS, 2);
+    init(kGbDone, 2);
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -590,18 +624,19 @@ __global__ void __launch_bounds__(GradPlan<NKB>::kThreads, 1)
       }
       // every copy has landed before the block exits
       if (tiles > 0) x.pipe.drain(x.bar(kGbXFull), (tiles - 1) & 1u, kSiteGradDrain);
-      for (uint32_t d = at > P::kStages ? at - P::kStages : 0; d < at; ++d)
-        x.pipe.drain(x.bar(kGbYFull + d % P::kStages), (d / P::kStages) & 1u, kSiteGradDrain);
+      for (uint32_t d = at > P::kHalves ? at - P::kHalves : 0; d < at; ++d)
+        x.pipe.drain(x.bar(kGbYFull + d % P::kHalves), (d / P::kHalves) & 1u, kSiteGradDrain);
     } else if (warp == 1) {
+      bool keys_before = false;
       for (int block = blockIdx.x; ok && block < p.blocks; block += gridDim.x)
-        ok = block < p.key_blocks ? grad_scores<T, NKB, true>(x, block, at, tiles)
-                                  : grad_scores<T, NKB, false>(x, block, at, tiles);
-      if (ptx::elect_one()) ptx::mma_commit(x.bar(kGbDoneS));
+        ok = block < p.key_blocks ? grad_scores<T, NKB, true>(x, block, at, tiles, keys_before)
+                                  : grad_scores<T, NKB, false>(x, block, at, tiles, keys_before);
+      if (ptx::elect_one()) ptx::mma_commit(x.bar(kGbDone));
     } else if (warp == 2) {
       for (int block = blockIdx.x; ok && block < p.blocks; block += gridDim.x)
         ok = block < p.key_blocks ? grad_sums<T, NKB, true>(x, block, at, tiles)
                                   : grad_sums<T, NKB, false>(x, block, at, tiles);
-      if (ptx::elect_one()) ptx::mma_commit(x.bar(kGbDoneS));
+      if (ptx::elect_one()) ptx::mma_commit(x.bar(kGbDone));
     }
   } else {
     ptx::regs_increase<P::kRegsMath>();
@@ -613,7 +648,7 @@ __global__ void __launch_bounds__(GradPlan<NKB>::kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   if (warp == 1) {
-    if (lane == 0) x.pipe.drain(x.bar(kGbDoneS), 0, kSiteGradDrain);
+    if (lane == 0) x.pipe.drain(x.bar(kGbDone), 0, kSiteGradDrain);
     __syncwarp();
     ptx::tc_fence_after();
     ptx::tmem_dealloc(x.tmem, 512);
