@@ -509,13 +509,13 @@ vattn_status backward_window(const Tensor& tg, const Tensor& tq, const Tensor& t
   const size_t stat_bytes = static_cast<size_t>(p.w.batch) * p.w.heads * p.stat_tiles * vattn::kGradStat * 4;
   const size_t part_bytes = static_cast<size_t>(slots) * 2 * kTile * p.w.dim * 4;
   Workspace ws;
-  if (stat_bytes + part_bytes > 0) {
-    if ((st = ws.take(stat_bytes + part_bytes, device, stream)) != VATTN_OK) return st;
-    p.stat = reinterpret_cast<float*>(ws.data());
-    p.part = reinterpret_cast<float*>(ws.data() + stat_bytes);
-  }
-  if (stat_bytes > 0) {
-    const unsigned grid = static_cast<unsigned>(bhs * p.stat_tiles);
+  if ((st = ws.take(256 + stat_bytes + part_bytes, device, stream)) != VATTN_OK) return st;
+  p.next = reinterpret_cast<uint32_t*>(ws.data());
+  p.stat = reinterpret_cast<float*>(ws.data() + 256);
+  p.part = reinterpret_cast<float*>(ws.data() + 256 + stat_bytes);
+  {
+    // (one block for the counter alone where there are no queries)
+    const unsigned grid = static_cast<unsigned>(std::max(1LL, bhs * p.stat_tiles));
     if (p.w.dim <= 64) vattn::vattn_window_stat_kernel<T, 8><<<grid, 256, 0, stream>>>(p);
     else vattn::vattn_window_stat_kernel<T, 16><<<grid, 256, 0, stream>>>(p);
     if ((st = launched("gradient statistics kernel launch")) != VATTN_OK) return st;

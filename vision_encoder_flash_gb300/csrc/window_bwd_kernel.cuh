@@ -18,8 +18,9 @@
 //   keys:     dV += P Y2, dK += D Y1     queries:  dQ += D Y1
 // P and D overwrite S in TMEM and are the A operands of the second products;
 // Y is read K-major for the first and MN-major for the second, so nothing is
-// transposed.  The grid is one block per multiprocessor, each walking over X
-// tiles, key tiles (longer) first:
+// transposed.  The grid is one block per multiprocessor.  Each takes X tiles
+// from a counter, key tiles (longer) first (with tiles dealt out in turn, the
+// blocks that got one more key tile ended last: 30 us of 190):
 //   warp 0   X and Y tiles by TMA; Y through a ring of half tiles (64 rows),
 //            ahead across X tiles
 //   warp 1   issues G, then S of each tile (128 columns a product: a 128 x 64
@@ -27,6 +28,7 @@
 //   warp 2   issues the second products once P and D are there; an issuing
 //            thread is held while its products run, so with two of them the
 //            next tile's G and S run between
+//   warp 3   takes the next X tile and tells the others
 //   warps 4-7, 8-11   P and D of columns 0..63, 64..127 of every tile, then
 //            the X tile's results
 // G is overwritten as soon as it is in registers, S once its P and D have
@@ -57,6 +59,7 @@ struct WindowGradParams {
   const float* lse;
   float* stat;     // [batch * heads][stat_tiles][-lse2 x 64 | -delta x 64]
   float* part;     // [slot][dv, dk][128][dim] partial sums of the chunks
+  uint32_t* next;  // X tiles taken from the counter so far; zeroed by the statistics kernel
   uint32_t* status;
   MapMul mq, mg, mk, mv;  // q, dout, k, v
   int stat_tiles;  // half tiles (64 rows) of the queries, an even number
@@ -76,6 +79,8 @@ template <typename T, int LR>
 __global__ void __launch_bounds__(256) vattn_window_stat_kernel(const __grid_constant__ WindowGradParams p) {
   constexpr int R = kGradCols * LR / 256;
   ptx::grid_dep_launch();  // the gradient kernel sets itself up meanwhile, and waits for this one's end
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.next = 0;
+  if (p.stat_tiles == 0) return;
   uint32_t tile, h;
   const uint32_t bh = p.d_stat_tiles.div(blockIdx.x, &tile);
   const int b = static_cast<int>(p.d_heads.div(bh, &h));
@@ -125,7 +130,7 @@ struct GradPlan {
   static constexpr int kOffX = 0;
   static constexpr int kOffY = 2 * kXBytes;
   static constexpr int kOffBar = kOffY + kSlots * kSlotBytes;
-  static constexpr int kSmemBytes = kOffBar + 256 + 1024;
+  static constexpr int kSmemBytes = kOffBar + 512 + 1024;
   static constexpr int kThreads = 384;
   static constexpr uint32_t kRegsOther = 72, kRegsMath = 216;  // 72 + 2 x 216 = 3 x 168
   static constexpr uint32_t kColG = NKB == 1 ? 256 : 128;
@@ -141,7 +146,7 @@ struct GradPlan {
 
 enum GradBar : int {
   kGbXFull = 0, kGbXEmpty = 1, kGbYFull = 2, kGbYEmpty = 10, kGbSFull = 18, kGbGFree = 19, kGbPFull = 20,
-  kGbPFree = 22, kGbSum = 24, kGbSumFree = 25, kGbDone = 26, kGbCount = 27,
+  kGbPFree = 22, kGbSum = 24, kGbSumFree = 25, kGbNext = 26, kGbTaken = 28, kGbDone = 30, kGbCount = 31,
 };
 
 // What a block walks over: Y tiles 0 .. n - 1 of its share.
@@ -580,6 +585,7 @@ __global__ void __launch_bounds__(GradPlan<NKB>::kThreads, 1)
   uint8_t* const base = smem_raw + (base_s - raw_s);
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(base + P::kOffBar + 8 * kGbCount);
   volatile uint32_t* abort_flag = tmem_slot + 1;
+  volatile int* taken = reinterpret_cast<volatile int*>(tmem_slot + 2);  // [2] X tiles handed out
   const uint32_t bar0 = base_s + P::kOffBar;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -595,6 +601,8 @@ __global__ void __launch_bounds__(GradPlan<NKB>::kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       init(kGbPFull + i, 8);
       init(kGbPFree + i, 1);
+      init(kGbNext + i, 1);
+      init(kGbTaken + i, 11);  // loader, two issuers, eight math warps
     }
     init(kGbSum, 1);
     init(kGbSumFree, 8);
@@ -613,10 +621,24 @@ __global__ void __launch_bounds__(GradPlan<NKB>::kThreads, 1)
   ptx::grid_dep_wait();
   uint32_t at = 0, tiles = 0;
   bool ok = true;
+  // The block's next X tile (its first is blockIdx.x), -1 after the last: by
+  // one thread, or by all lanes of a warp.
+  uint32_t n_taken = 0;
+  auto next = [&](bool whole_warp) -> int {
+    const uint32_t i = n_taken & 1u, phase = (n_taken >> 1) & 1u;
+    ++n_taken;
+    if (whole_warp ? !x.pipe.wait_warp(x.bar(kGbNext + i), phase, kSiteGradNext)
+                   : !x.pipe.wait(x.bar(kGbNext + i), phase, kSiteGradNext))
+      return -1;
+    const int block = taken[i];
+    if (whole_warp) pipe_warp_arrive(x.bar(kGbTaken + i));
+    else ptx::mbar_arrive(x.bar(kGbTaken + i));
+    return block < p.blocks ? block : -1;
+  };
   if (warp < 4) {
     ptx::regs_decrease<P::kRegsOther>();
     if (warp == 0 && lane == 0) {
-      for (int block = blockIdx.x; ok && block < p.blocks; block += gridDim.x) {
+      for (int block = next(false); ok && block >= 0; block = ok ? next(false) : -1) {
         if (block < p.key_blocks)
           ok = grad_load<NKB, true>(x, &tm_kx, &tm_vx, &tm_qy, &tm_gy, p.mk, p.mv, p.mq, p.mg, block, at, tiles);
         else
@@ -628,19 +650,28 @@ __global__ void __launch_bounds__(GradPlan<NKB>::kThreads, 1)
         x.pipe.drain(x.bar(kGbYFull + d % P::kHalves), (d / P::kHalves) & 1u, kSiteGradDrain);
     } else if (warp == 1) {
       bool keys_before = false;
-      for (int block = blockIdx.x; ok && block < p.blocks; block += gridDim.x)
+      for (int block = next(true); ok && block >= 0; block = ok ? next(true) : -1)
         ok = block < p.key_blocks ? grad_scores<T, NKB, true>(x, block, at, tiles, keys_before)
                                   : grad_scores<T, NKB, false>(x, block, at, tiles, keys_before);
       if (ptx::elect_one()) ptx::mma_commit(x.bar(kGbDone));
     } else if (warp == 2) {
-      for (int block = blockIdx.x; ok && block < p.blocks; block += gridDim.x)
+      for (int block = next(true); ok && block >= 0; block = ok ? next(true) : -1)
         ok = block < p.key_blocks ? grad_sums<T, NKB, true>(x, block, at, tiles)
                                   : grad_sums<T, NKB, false>(x, block, at, tiles);
       if (ptx::elect_one()) ptx::mma_commit(x.bar(kGbDone));
+    } else if (warp == 3 && lane == 0) {
+      int block = static_cast<int>(blockIdx.x);
+      for (uint32_t i = 0;; ++i) {
+        if (!x.pipe.wait(x.bar(kGbTaken + (i & 1u)), ((i >> 1) & 1u) ^ 1u, kSiteGradNext)) break;
+        taken[i & 1u] = block;
+        ptx::mbar_arrive(x.bar(kGbNext + (i & 1u)));
+        if (block >= p.blocks) break;
+        block = static_cast<int>(gridDim.x + atomicAdd(p.next, 1u));
+      }
     }
   } else {
     ptx::regs_increase<P::kRegsMath>();
-    for (int block = blockIdx.x; ok && block < p.blocks; block += gridDim.x)
+    for (int block = next(true); ok && block >= 0; block = ok ? next(true) : -1)
       ok = block < p.key_blocks ? grad_math<T, NKB, true>(x, block, at, tiles)
                                 : grad_math<T, NKB, false>(x, block, at, tiles);
   }

@@ -22,6 +22,7 @@ enum PipeSite : uint32_t {
   kSiteWinKv = 32, kSiteWinQ = 33, kSiteWinMma = 34, kSiteWinSoft = 35, kSiteWinOut = 36,
   kSiteWinDrain = 37,
   kSiteGradLoad = 40, kSiteGradMma = 41, kSiteGradSoft = 42, kSiteGradOut = 43, kSiteGradDrain = 44,
+  kSiteGradNext = 45,
 };
 
 // Bounded waits on mbarriers: one that runs out records its site in the
