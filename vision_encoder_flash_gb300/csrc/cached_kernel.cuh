@@ -96,11 +96,6 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4
                : "r"(addr)
                : "memory");
 }
-// 16 bytes global -> shared, or 16 zero bytes.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-
 template <int DP, int RW>
 struct CachedPlan {
   static constexpr int kKw = 4 / RW;                   // warps that share a tile's keys
@@ -149,11 +144,11 @@ __global__ void __launch_bounds__(kCachedThreads)
           const long long j = sp.key(i < v1 ? i : v0);
           const uint32_t at = static_cast<uint32_t>(r * DP * 2 + ((ch ^ (r & 7)) << 4));
           const int c = on ? ch * 8 : 0;
-          cp_async16(st + at, kbase + j * p.k.s[2] + c, on);
-          cp_async16(st + P::kTileBytes + at, vbase + j * p.v.s[2] + c, on);
+          ptx::cp_async<16>(st + at, kbase + j * p.k.s[2] + c, on);
+          ptx::cp_async<16>(st + P::kTileBytes + at, vbase + j * p.v.s[2] + c, on);
         }
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
+      ptx::cp_async_commit();
     };
     load(0);
     load(1);
@@ -188,7 +183,7 @@ __global__ void __launch_bounds__(kCachedThreads)
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 
     for (int tile = 0; tile < tiles; ++tile) {
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      ptx::cp_async_wait<1>();
       __syncthreads();
       load(tile + 2);
       const uint32_t ks_s = smem_s + static_cast<uint32_t>(tile % kCachedStages) * P::kStageBytes;
@@ -338,7 +333,7 @@ __global__ void __launch_bounds__(kCachedThreads)
         __syncwarp();
       }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    ptx::cp_async_wait<0>();
     __syncthreads();  // the ring is free: the warps' results go there
 
     // ---- join the warps that shared the keys

@@ -156,6 +156,16 @@ vattn_status launch_behind(const char* what, K kernel, dim3 grid, dim3 block, si
   return e == cudaSuccess ? VATTN_OK : cuda_fail(e, what);
 }
 
+// Opts a kernel in to its dynamic shared memory, once per device.
+template <typename K>
+vattn_status allow_smem(K kernel, int bytes, std::atomic<uint8_t>* done, int device) {
+  if (done[device].load(std::memory_order_acquire)) return VATTN_OK;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+  done[device].store(1, std::memory_order_release);
+  return VATTN_OK;
+}
+
 // ------------------------------------------------------------ norm + rotation
 vattn_status check_qk(const vattn_qk_args* a) {
   if (!a) return fail(VATTN_ERR_INVALID_ARG, "null args");
@@ -216,8 +226,9 @@ void qk_strides(long long (&to)[3], const vattn_rows* t) {
   for (int i = 0; i < 3; ++i) to[i] = t ? t->stride[i] : 0;
 }
 
-// Sizes, angles and the split of the heads: 8 heads per block and token
-// (angles shared by them), fewer while that leaves under four blocks per
+// Sizes, angles and the split of the heads: 16 heads per block and token
+// (angles shared by them: 52.7 us for 4 x 40 heads x 4096 x 128, with 8 heads
+// 53.9, with 4 69), fewer while that leaves under four blocks per
 // multiprocessor.
 void qk_plan(vattn::QkParams* p, const vattn_qk_args* a, int v, int sms, int64_t* blocks_x) {
   p->positions = a->positions;
@@ -225,6 +236,7 @@ void qk_plan(vattn::QkParams* p, const vattn_qk_args* a, int v, int sms, int64_t
   p->tokens = a->batch * a->n_patches;
   p->pos0 = a->pos0;
   p->n = static_cast<int>(a->n_patches);
+  p->d_n = vattn::FastDiv::make(static_cast<uint32_t>(a->n_patches));
   p->D = static_cast<int>(a->head_dim);
   p->half = static_cast<int>(a->rope_dims / 2);
   p->w_f32 = a->weight_dtype == VATTN_F32;
@@ -238,7 +250,7 @@ void qk_plan(vattn::QkParams* p, const vattn_qk_args* a, int v, int sms, int64_t
   while ((1 << p->log_lanes) < p->slots && p->log_lanes < 5) ++p->log_lanes;
   const int groups = vattn::kQkThreads >> p->log_lanes;
   *blocks_x = (p->tokens + groups - 1) / groups;
-  int per = 8;
+  int per = 16;
   for (;; per /= 2) {
     int64_t slices = 0;
     for (int i = 0; i < 2; ++i) slices += (p->t[i].heads + per - 1) / per;
@@ -250,33 +262,40 @@ void qk_plan(vattn::QkParams* p, const vattn_qk_args* a, int v, int sms, int64_t
     p->t[i].heads_per_slice = hp;
     p->t[i].slices = (p->t[i].heads + hp - 1) / hp;
   }
+  // up to eight rounds of what is resident at a time (a block in flight for
+  // each that ends), behind that the blocks walk over several tokens: with
+  // gradients, each leaves one row of weight gradient
+  const int64_t most = 8 * (v == 8 ? 2LL : 3LL) * sms / (p->t[0].slices + p->t[1].slices);
+  *blocks_x = std::min(*blocks_x, std::max<int64_t>(1, most));
+}
+
+template <typename T, int V, int SL, bool kBackward>
+vattn_status qk_go(const vattn::QkParams& p, dim3 grid, int device, cudaStream_t stream) {
+  constexpr int kSmem = vattn::QkRing<T, V, SL, kBackward ? 2 : 1>::kSmemBytes;
+  void (*kernel)(vattn::QkParams);
+  if constexpr (kBackward) kernel = vattn::vattn_qk_norm_rope_backward_kernel<T, V, SL>;
+  else kernel = vattn::vattn_qk_norm_rope_kernel<T, V, SL>;
+  static std::atomic<uint8_t> done[vattn::host::kMaxDevices];
+  const vattn_status st = allow_smem(kernel, kSmem, done, device);
+  if (st != VATTN_OK) return st;
+  kernel<<<grid, vattn::kQkThreads, kSmem, stream>>>(p);
+  return launched("norm and rotation kernel launch");
 }
 
 template <typename T, bool kBackward>
-vattn_status qk_launch(const vattn::QkParams& p, int v, dim3 grid, cudaStream_t stream) {
-  auto go = [&](auto kernel) {
-    kernel<<<grid, vattn::kQkThreads, 0, stream>>>(p);
-    return launched("norm and rotation kernel launch");
-  };
-  if constexpr (kBackward) {
-    if constexpr (sizeof(T) == 2)
-      if (v == 8) return go(vattn::vattn_qk_norm_rope_backward_kernel<T, 8, 1>);
-    if (v == 4) return go(vattn::vattn_qk_norm_rope_backward_kernel<T, 4, 1>);
-    return go(vattn::vattn_qk_norm_rope_backward_kernel<T, 1, 2>);
-  } else {
-    if constexpr (sizeof(T) == 2)
-      if (v == 8) return go(vattn::vattn_qk_norm_rope_kernel<T, 8, 1>);
-    if (v == 4) return go(vattn::vattn_qk_norm_rope_kernel<T, 4, 1>);
-    return go(vattn::vattn_qk_norm_rope_kernel<T, 1, 2>);
-  }
+vattn_status qk_launch(const vattn::QkParams& p, int v, dim3 grid, int device, cudaStream_t stream) {
+  if constexpr (sizeof(T) == 2)
+    if (v == 8) return qk_go<T, 8, 1, kBackward>(p, grid, device, stream);
+  if (v == 4) return qk_go<T, 4, 1, kBackward>(p, grid, device, stream);
+  return qk_go<T, 1, 2, kBackward>(p, grid, device, stream);
 }
 
 template <bool kBackward>
-vattn_status qk_dispatch(const vattn::QkParams& p, int32_t dtype, int v, dim3 grid, cudaStream_t stream) {
+vattn_status qk_dispatch(const vattn::QkParams& p, int32_t dtype, int v, dim3 grid, int device, cudaStream_t stream) {
   switch (dtype) {
-    case VATTN_F32: return qk_launch<float, kBackward>(p, v, grid, stream);
-    case VATTN_F16: return qk_launch<__half, kBackward>(p, v, grid, stream);
-    default: return qk_launch<__nv_bfloat16, kBackward>(p, v, grid, stream);
+    case VATTN_F32: return qk_launch<float, kBackward>(p, v, grid, device, stream);
+    case VATTN_F16: return qk_launch<__half, kBackward>(p, v, grid, device, stream);
+    default: return qk_launch<__nv_bfloat16, kBackward>(p, v, grid, device, stream);
   }
 }
 
@@ -394,16 +413,6 @@ vattn_status make_rows_map(CUtensorMap* tm, vattn::MapMul* mul, const Tensor& x,
                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
     return fail(VATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed with CUresult %d", static_cast<int>(r));
-  return VATTN_OK;
-}
-
-// Opts a kernel in to its dynamic shared memory, once per device.
-template <typename K>
-vattn_status allow_smem(K kernel, int bytes, std::atomic<uint8_t>* done, int device) {
-  if (done[device].load(std::memory_order_acquire)) return VATTN_OK;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-  done[device].store(1, std::memory_order_release);
   return VATTN_OK;
 }
 
@@ -643,9 +652,8 @@ vattn_status vattn_qk_norm_rope(const vattn_rows* q, const vattn_rows* k, const 
   }
   int64_t bx = 0;
   qk_plan(&p, a, v, sms, &bx);
-  if (bx > INT32_MAX) return fail(VATTN_ERR_UNSUPPORTED, "too many tokens");
   const dim3 grid(static_cast<unsigned>(bx), static_cast<unsigned>(p.t[0].slices + p.t[1].slices));
-  return qk_dispatch<false>(p, a->dtype, v, grid, static_cast<cudaStream_t>(stream_ptr));
+  return qk_dispatch<false>(p, a->dtype, v, grid, device, static_cast<cudaStream_t>(stream_ptr));
 }
 
 vattn_status vattn_qk_norm_rope_backward(const vattn_rows* dq_out, const vattn_rows* dk_out,
@@ -719,17 +727,13 @@ vattn_status vattn_qk_norm_rope_backward(const vattn_rows* dq_out, const vattn_r
   int64_t bx = 0;
   qk_plan(&p, a, v, sms, &bx);
   const int slices = p.t[0].slices + p.t[1].slices;
-  // at most eight blocks per multiprocessor: they walk over the tokens, and
-  // each leaves one row of weight gradient
-  const int64_t most = std::max<int64_t>(1, 8LL * sms / slices);
-  bx = std::min(bx, most);
   const dim3 grid(static_cast<unsigned>(bx), static_cast<unsigned>(slices));
   Workspace ws;
   if (dw[0] || dw[1]) {
     if ((st = ws.take(static_cast<size_t>(bx) * slices * p.D * 4, device, stream)) != VATTN_OK) return st;
     p.part = reinterpret_cast<float*>(ws.data());
   }
-  if ((st = qk_dispatch<true>(p, a->dtype, v, grid, stream)) != VATTN_OK) return st;
+  if ((st = qk_dispatch<true>(p, a->dtype, v, grid, device, stream)) != VATTN_OK) return st;
   if (!p.part) return VATTN_OK;
   vattn::QkWeightSum s{};
   s.part = p.part;

@@ -57,8 +57,14 @@ struct alignas(sizeof(T) * V) Vec {
     for (int i = 0; i < V; ++i) x[i] = Elem<T>::widen(e[i]);
   }
   __device__ __forceinline__ void narrow(const float (&x)[V]) {
+    if constexpr (sizeof(T) == 2 && V % 2 == 0) {  // one conversion for two elements
+      uint32_t* w = reinterpret_cast<uint32_t*>(e);
 #pragma unroll
-    for (int i = 0; i < V; ++i) e[i] = Elem<T>::narrow(x[i]);
+      for (int i = 0; i < V / 2; ++i) w[i] = pack2<T>(x[2 * i], x[2 * i + 1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) e[i] = Elem<T>::narrow(x[i]);
+    }
   }
 };
 

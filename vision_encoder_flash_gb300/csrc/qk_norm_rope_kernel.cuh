@@ -13,21 +13,28 @@
 // Angles: in turns, position * f_i only counts modulo 1, so f_i is held as a
 // 64-bit binary fraction (from f64) and position * f_i is one wrapping
 // integer product: exact to 2^-33 turns at any 32-bit position, where an f32
-// product loses all digits.  sincospif of the remainder does the rest.
+// product loses all digits.  The fraction is cut to the nearest quarter turn
+// and the rest goes through two short polynomials (qk_sincos).
 //
 // Work split: a group of lanes holds one row, lane = slot of V pairs (two
-// 16-byte loads where the sizes allow), so the rotation needs no exchange
-// and the sums a few shuffles.  A group stays on one token and walks over
-// that token's heads of one tensor (a slice of them): the angles are computed
-// once per token and slice and stay in registers, and the four rows in flight
-// per thread keep the loads ahead of the arithmetic.  Memory bound: each row
-// is read once and written once.
+// 16-byte accesses where the sizes allow), so the rotation needs no exchange
+// and the sums a few shuffles.  A group walks over tokens, and for each over a
+// slice of the heads of one tensor: the angles, multiplied with the weights,
+// stay in registers meanwhile.  Each row is read once and written once.  What
+// bounds it is bytes in flight: each thread keeps its next rows coming
+// through a ring of its own in shared memory (cp.async; no barrier, a thread
+// reads what it asked for).  4 x 40 heads x 4096 x 128 bf16: 52.7 us, 6.4 TB/s (94
+// % of the measured copy rate), with two rows a thread in registers 74 us; its
+// gradient at 4 x 20 heads 48.7 us, 5.2 TB/s, weight sums included, from 105
+// us.  The arithmetic, in packed f32 pairs, is about 80 instructions for the
+// 64 bytes of a lane and row.
 #pragma once
 
 #include <cstdint>
 
 #include "elem.cuh"
 #include "ptx.cuh"
+#include "window_common.cuh"
 
 namespace vattn {
 
@@ -52,6 +59,7 @@ struct QkParams {
   float* part;  // backward: [gridDim.y * gridDim.x][D] weight gradient of each block
   long long tokens;
   long long pos0;
+  FastDiv d_n;
   int n;  // rows of a sequence
   int D;
   int half;
@@ -94,6 +102,24 @@ __device__ __forceinline__ void qk_weight(const QkSlot<V>& s, const void* w, int
   }
 }
 
+// sin and cos of a 32-bit fraction of a turn, to 1.3 x 2^-24: quadrant and
+// remainder y in [-pi/4, pi/4] from the integer, then sin y = y + y^3 A(y^2) and
+// cos y = 1 - y^2/2 + y^4 B(y^2) with A and B of degree 2, the interpolation of
+// (sin y / y - 1) / y^2 and (cos y - 1 + y^2/2) / y^4 at the Chebyshev points
+// of [0, (pi/4)^2].
+__device__ __forceinline__ void qk_sincos(uint32_t phase, float& sn, float& cs) {
+  const uint32_t k = (phase + 0x20000000u) >> 30;  // quarter turns
+  const float y = static_cast<float>(static_cast<int32_t>(phase - (k << 30))) * 0x1.921fb6p-30f;  // 2 pi / 2^32
+  const float z = y * y;
+  const float a = fmaf(fmaf(-0.000195878909f, z, 0.00833274797f), z, -0.166666642f);
+  const float b = fmaf(fmaf(2.45479423e-05f, z, -0.00138883025f), z, 0.0416666642f);
+  const float s = fmaf(y * z, a, y);
+  const float c = fmaf(z * z, b, fmaf(-0.5f, z, 1.0f));
+  const float s1 = (k & 1u) ? c : s, c1 = (k & 1u) ? s : c;
+  sn = (k & 2u) ? -s1 : s1;
+  cs = ((k + 1u) & 2u) ? -c1 : c1;
+}
+
 template <int V>
 __device__ __forceinline__ void qk_angles(const QkSlot<V>& s, const uint64_t* turn, int c,
                                           long long pos, float (&cs)[V], float (&sn)[V]) {
@@ -101,13 +127,52 @@ __device__ __forceinline__ void qk_angles(const QkSlot<V>& s, const uint64_t* tu
   for (int e = 0; e < V; ++e) {
     cs[e] = 1.0f;
     sn[e] = 0.0f;
-    if (s.rot) {
-      const uint64_t phase = static_cast<uint64_t>(pos) * turn[c * V + e];
-      // half turns in [-1, 1)
-      const float h = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f;
-      sincospif(h, &sn[e], &cs[e]);
-    }
+    if (s.rot) qk_sincos(static_cast<uint32_t>((static_cast<uint64_t>(pos) * turn[c * V + e]) >> 32), sn[e], cs[e]);
   }
+}
+
+// d = a * b, d = a * b + c over V lanes' worth, in pairs where V is even.
+template <int V>
+__device__ __forceinline__ void vmul(float (&d)[V], const float (&a)[V], const float (&b)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int e = 0; e < V; e += 2) {
+      const float2 r = __fmul2_rn(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]));
+      d[e] = r.x;
+      d[e + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) d[e] = a[e] * b[e];
+  }
+}
+template <int V>
+__device__ __forceinline__ void vfma(float (&d)[V], const float (&a)[V], const float (&b)[V], const float (&c)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int e = 0; e < V; e += 2) {
+      const float2 r = __ffma2_rn(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]), make_float2(c[e], c[e + 1]));
+      d[e] = r.x;
+      d[e + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) d[e] = fmaf(a[e], b[e], c[e]);
+  }
+}
+template <int V>
+__device__ __forceinline__ void vscale(float (&d)[V], const float (&a)[V], float b) {
+  float bb[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) bb[e] = b;
+  vmul<V>(d, a, bb);
+}
+template <int V>
+__device__ __forceinline__ float vsum(const float (&a)[V]) {
+  float s = 0.0f;
+#pragma unroll
+  for (int e = 0; e < V; ++e) s += a[e];
+  return s;
 }
 
 __device__ __forceinline__ void qk_turns(const QkParams& p, uint64_t* turn) {
@@ -138,179 +203,293 @@ __device__ __forceinline__ float qk_group_sum(float x, int lanes) {
   return x;
 }
 
+// The rows of a group in the order it takes them: tokens first, + stride, ...,
+// for each the heads [h0, h1).  N tensors of one shape are read (x, or x and
+// g), kStages rows ahead through the thread's ring where an access has 8 bytes
+// or more, else in place.
+template <typename T, int V, int SL, int N>
+struct QkRing {
+  static constexpr int kBytes = V * static_cast<int>(sizeof(T));
+  static constexpr bool kAsync = kBytes >= 8 && SL == 1;
+  static constexpr int kStages = kAsync ? (N == 1 ? 6 : 4) : 1;
+  static constexpr int kSmemBytes = kAsync ? kStages * N * 2 * kBytes * kQkThreads : 0;
+
+  const QkParams& p;
+  const QkTensor& t;
+  const QkSlot<V> (&s)[SL];
+  int h0, h1;
+  long long stride;
+  uint32_t base;
+  // the next row to ask for
+  long long token;
+  const T* row[N];
+  int h, stage;
+
+  __device__ __forceinline__ QkRing(const QkParams& p_, const QkTensor& t_, const QkSlot<V> (&s_)[SL], int h0_, int h1_,
+                                    long long first, long long stride_, uint32_t smem)
+      : p(p_), t(t_), s(s_), h0(h0_), h1(h1_), stride(stride_), base(smem + threadIdx.x * kBytes), token(first), h(h0_),
+        stage(0) {
+    rows(token);
+    if constexpr (kAsync)
+      for (int i = 0; i < kStages; ++i) ask();
+  }
+  // rows of a token's first head
+  __device__ __forceinline__ void rows(long long tk) {
+    if (tk >= p.tokens) tk = p.tokens - 1;
+    const long long b = p.tokens <= 0x7fffffffLL ? static_cast<long long>(p.d_n.div(static_cast<uint32_t>(tk))) : tk / p.n;
+    const long long n = tk - b * p.n;
+    row[0] = static_cast<const T*>(t.x) + b * t.xs[0] + n * t.xs[2] + h0 * t.xs[1];
+    if constexpr (N == 2) row[1] = static_cast<const T*>(t.g) + b * t.gs[0] + n * t.gs[2] + h0 * t.gs[1];
+  }
+  __device__ __forceinline__ void advance() {
+    row[0] += t.xs[1];
+    if constexpr (N == 2) row[1] += t.gs[1];
+    if (++h == h1) {
+      h = h0;
+      token += stride;
+      if (token < p.tokens) rows(token);
+    }
+  }
+  // Asks for the next row (an empty group behind the last).
+  __device__ __forceinline__ void ask() {
+    static_assert(SL == 1, "one slot a lane");
+    if (token < p.tokens) {
+      const uint32_t at = base + static_cast<uint32_t>(stage) * (N * 2 * kBytes * kQkThreads);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        ptx::cp_async<kBytes>(at + (2 * i) * kBytes * kQkThreads, row[i] + (s[0].here ? s[0].ia : 0), s[0].here);
+        ptx::cp_async<kBytes>(at + (2 * i + 1) * kBytes * kQkThreads, row[i] + (s[0].pair ? s[0].ib : 0), s[0].pair);
+      }
+      advance();
+    }
+    ptx::cp_async_commit();
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+  }
+  // The oldest row asked for; more() once its values have been used.
+  __device__ __forceinline__ void take(Vec<T, V> (&a)[N][SL], Vec<T, V> (&b)[N][SL]) {
+    if constexpr (kAsync) {
+      ptx::cp_async_wait<kStages - 1>();
+      const uint32_t at = base + static_cast<uint32_t>(stage) * (N * 2 * kBytes * kQkThreads);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        get(a[i][0], at + (2 * i) * kBytes * kQkThreads);
+        get(b[i][0], at + (2 * i + 1) * kBytes * kQkThreads);
+      }
+    } else {
+      const bool on = token < p.tokens;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int k = 0; k < SL; ++k) {
+          a[i][k] = qk_load<T, V>(row[i], s[k].ia, on && s[k].here);
+          b[i][k] = qk_load<T, V>(row[i], s[k].ib, on && s[k].pair);
+        }
+    }
+  }
+  __device__ __forceinline__ void more() {
+    if constexpr (kAsync) ask();
+    else if (token < p.tokens) advance();
+  }
+  static __device__ __forceinline__ void get(Vec<T, V>& v, uint32_t at) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+    if constexpr (kBytes == 16)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+    else
+      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
+  }
+};
+
+// A block's tensor, heads and tokens.
+struct QkShare {
+  int which, h0, h1;
+  long long first, stride;  // of this thread's group
+  __device__ __forceinline__ explicit QkShare(const QkParams& p) {
+    which = static_cast<int>(blockIdx.y) < p.t[0].slices ? 0 : 1;
+    const int slice = static_cast<int>(blockIdx.y) - (which == 0 ? 0 : p.t[0].slices);
+    h0 = slice * p.t[which].heads_per_slice;
+    h1 = min(p.t[which].heads, h0 + p.t[which].heads_per_slice);
+    const int groups = kQkThreads >> p.log_lanes;
+    first = static_cast<long long>(blockIdx.x) * groups + (threadIdx.x >> p.log_lanes);
+    stride = static_cast<long long>(gridDim.x) * groups;
+  }
+};
+
 // SL slots per lane (2 only where V == 1 needs up to 64 slots of a warp).
+// All groups of a block take the same number of tokens: those past the end
+// work on zeros and store nothing.
 template <typename T, int V, int SL>
-__global__ void __launch_bounds__(kQkThreads)
+__global__ void __launch_bounds__(kQkThreads, V == 8 ? 2 : 3)
     vattn_qk_norm_rope_kernel(const __grid_constant__ QkParams p) {
-  constexpr int U = SL == 1 ? 4 : 2;  // rows in flight
+  extern __shared__ __align__(16) uint8_t qk_smem[];
   __shared__ uint64_t turn[kQkMaxDim / 2];
-  qk_turns(p, turn);
-  const bool is_q = static_cast<int>(blockIdx.y) < p.t[0].slices;
-  const QkTensor& t = p.t[is_q ? 0 : 1];
-  const int slice = static_cast<int>(blockIdx.y) - (is_q ? 0 : p.t[0].slices);
-  const int h0 = slice * t.heads_per_slice;
-  const int h1 = min(t.heads, h0 + t.heads_per_slice);
+  const QkShare sh(p);
+  const QkTensor& t = p.t[sh.which];
   const int lanes = 1 << p.log_lanes;
   const int c0 = static_cast<int>(threadIdx.x) & (lanes - 1);
-  const long long token = static_cast<long long>(blockIdx.x) * (kQkThreads >> p.log_lanes) +
-                          (threadIdx.x >> p.log_lanes);
-  const bool valid = token < p.tokens;
-  const long long tk = valid ? token : p.tokens - 1;
-  const long long b = tk / p.n, n = tk - b * p.n;
-  const long long pos = p.positions != nullptr ? p.positions[tk] : p.pos0 + n;
   QkSlot<V> s[SL];
-  float cs[SL][V], sn[SL][V], wa[SL][V], wb[SL][V];
 #pragma unroll
-  for (int k = 0; k < SL; ++k) {
-    s[k].set(p, c0 + k * lanes);
-    qk_angles<V>(s[k], turn, c0 + k * lanes, pos, cs[k], sn[k]);
-    qk_weight<V>(s[k], t.w, p.w_f32, Elem<T>::kBf16, wa[k], wb[k]);
-  }
-  const T* x0 = static_cast<const T*>(t.x) + b * t.xs[0] + n * t.xs[2];
-  T* y0 = static_cast<T*>(t.y) + b * t.ys[0] + n * t.ys[2];
+  for (int k = 0; k < SL; ++k) s[k].set(p, c0 + k * lanes);
+  QkRing<T, V, SL, 1> ring(p, t, s, sh.h0, sh.h1, sh.first, sh.stride, ptx::smem_addr(qk_smem));
+  qk_turns(p, turn);
+  float wa[SL][V], wb[SL][V];
+#pragma unroll
+  for (int k = 0; k < SL; ++k) qk_weight<V>(s[k], t.w, p.w_f32, Elem<T>::kBf16, wa[k], wb[k]);
   const float inv_d = 1.0f / static_cast<float>(p.D);
-  for (int h = h0; h < h1; h += U) {
-    Vec<T, V> a[U][SL], c[U][SL];
+  const long long block_first = static_cast<long long>(blockIdx.x) * (kQkThreads >> p.log_lanes);
+  long long token = sh.first;
+  for (long long f = block_first; f < p.tokens; f += sh.stride, token += sh.stride) {
+    const bool valid = token < p.tokens;
+    const long long tk = valid ? token : p.tokens - 1;
+    const long long b = p.tokens <= 0x7fffffffLL ? static_cast<long long>(p.d_n.div(static_cast<uint32_t>(tk))) : tk / p.n;
+    const long long n = tk - b * p.n;
+    const long long pos = p.positions != nullptr ? p.positions[tk] : p.pos0 + n;
+    // out_a = r (x_a [w_a cos] - x_b [w_b sin]), out_b = r (x_a [w_a sin] + x_b [w_b cos])
+    float ac[SL][V], as[SL][V], bc[SL][V], bs[SL][V];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const T* row = x0 + (h + u < h1 ? h + u : h) * t.xs[1];
-#pragma unroll
-      for (int k = 0; k < SL; ++k) {
-        a[u][k] = qk_load<T, V>(row, s[k].ia, s[k].here);
-        c[u][k] = qk_load<T, V>(row, s[k].ib, s[k].pair);
-      }
+    for (int k = 0; k < SL; ++k) {
+      float cs[V], sn[V];
+      qk_angles<V>(s[k], turn, c0 + k * lanes, pos, cs, sn);
+      vmul<V>(ac[k], wa[k], cs);
+      vmul<V>(as[k], wa[k], sn);
+      vmul<V>(bc[k], wb[k], cs);
+      vscale<V>(sn, sn, -1.0f);
+      vmul<V>(bs[k], wb[k], sn);
     }
+    T* row = static_cast<T*>(t.y) + b * t.ys[0] + n * t.ys[2] + sh.h0 * t.ys[1];
+    for (int h = sh.h0; h < sh.h1; ++h, row += t.ys[1]) {
+      Vec<T, V> xa[1][SL], xb[1][SL];
+      ring.take(xa, xb);
+      float fa[SL][V], fb[SL][V], sq[V];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float xa[SL][V], xb[SL][V], sum = 0.0f;
+      for (int e = 0; e < V; ++e) sq[e] = 0.0f;
 #pragma unroll
       for (int k = 0; k < SL; ++k) {
-        a[u][k].widen(xa[k]);
-        c[u][k].widen(xb[k]);
-#pragma unroll
-        for (int e = 0; e < V; ++e) sum = fmaf(xa[k][e], xa[k][e], fmaf(xb[k][e], xb[k][e], sum));
+        xa[0][k].widen(fa[k]);
+        xb[0][k].widen(fb[k]);
+        vfma<V>(sq, fa[k], fa[k], sq);
+        vfma<V>(sq, fb[k], fb[k], sq);
       }
-      const float r = __frsqrt_rn(fmaf(qk_group_sum(sum, lanes), inv_d, p.eps));
-      if (!valid || h + u >= h1) continue;
-      T* row = y0 + (h + u) * t.ys[1];
+      const float r = rsqrtf(fmaf(qk_group_sum(vsum<V>(sq), lanes), inv_d, p.eps));
+      ring.more();
+      if (!valid) continue;
 #pragma unroll
       for (int k = 0; k < SL; ++k) {
-        float ya[V], yb[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float va = xa[k][e] * r * wa[k][e], vb = xb[k][e] * r * wb[k][e];
-          ya[e] = va * cs[k][e] - vb * sn[k][e];
-          yb[e] = va * sn[k][e] + vb * cs[k][e];
-        }
-        Vec<T, V> oa, ob;
-        oa.narrow(ya);
-        ob.narrow(yb);
-        if (s[k].here) *reinterpret_cast<Vec<T, V>*>(row + s[k].ia) = oa;
-        if (s[k].pair) *reinterpret_cast<Vec<T, V>*>(row + s[k].ib) = ob;
+        float oa[V], ob[V], ta[V], tb[V];
+        vscale<V>(ta, fa[k], r);
+        vscale<V>(tb, fb[k], r);
+        vmul<V>(oa, tb, bs[k]);
+        vfma<V>(oa, ta, ac[k], oa);
+        vmul<V>(ob, tb, bc[k]);
+        vfma<V>(ob, ta, as[k], ob);
+        Vec<T, V> va, vb;
+        va.narrow(oa);
+        vb.narrow(ob);
+        if (s[k].here) *reinterpret_cast<Vec<T, V>*>(row + s[k].ia) = va;
+        if (s[k].pair) *reinterpret_cast<Vec<T, V>*>(row + s[k].ib) = vb;
       }
     }
   }
 }
 
-// The gradient.  A block walks over the tokens with a stride of the grid and
-// keeps its slice's share of dw in registers: lane sums, then the groups of a
-// warp by shuffles, the warps through shared memory, and one row of `part`
-// per block that vattn_qk_weight_sum_kernel adds in a fixed order.
+// The gradient.  A block keeps its slice's share of dw in registers: lane
+// sums, then the groups of a warp by shuffles, the warps through shared
+// memory, and one row of `part` per block that vattn_qk_weight_sum_kernel
+// adds in a fixed order.
 template <typename T, int V, int SL>
-__global__ void __launch_bounds__(kQkThreads)
+__global__ void __launch_bounds__(kQkThreads, V == 8 ? 2 : 3)
     vattn_qk_norm_rope_backward_kernel(const __grid_constant__ QkParams p) {
-  constexpr int U = SL == 1 ? 2 : 1;  // rows in flight (two tensors are read)
+  extern __shared__ __align__(16) uint8_t qk_smem[];
   __shared__ uint64_t turn[kQkMaxDim / 2];
   __shared__ float red[kQkThreads / 32][kQkMaxDim];
-  qk_turns(p, turn);
-  const bool is_q = static_cast<int>(blockIdx.y) < p.t[0].slices;
-  const QkTensor& t = p.t[is_q ? 0 : 1];
-  const int slice = static_cast<int>(blockIdx.y) - (is_q ? 0 : p.t[0].slices);
-  const int h0 = slice * t.heads_per_slice;
-  const int h1 = min(t.heads, h0 + t.heads_per_slice);
+  const QkShare sh(p);
+  const QkTensor& t = p.t[sh.which];
   const int lanes = 1 << p.log_lanes;
   const int c0 = static_cast<int>(threadIdx.x) & (lanes - 1);
-  const int groups = kQkThreads >> p.log_lanes;
   const float inv_d = 1.0f / static_cast<float>(p.D);
   QkSlot<V> s[SL];
+#pragma unroll
+  for (int k = 0; k < SL; ++k) s[k].set(p, c0 + k * lanes);
+  QkRing<T, V, SL, 2> ring(p, t, s, sh.h0, sh.h1, sh.first, sh.stride, ptx::smem_addr(qk_smem));
   float wa[SL][V], wb[SL][V], da[SL][V], db[SL][V];
+  qk_turns(p, turn);
 #pragma unroll
   for (int k = 0; k < SL; ++k) {
-    s[k].set(p, c0 + k * lanes);
     qk_weight<V>(s[k], t.w, p.w_f32, Elem<T>::kBf16, wa[k], wb[k]);
 #pragma unroll
     for (int e = 0; e < V; ++e) da[k][e] = db[k][e] = 0.0f;
   }
-  for (long long first = static_cast<long long>(blockIdx.x) * groups; first < p.tokens;
-       first += static_cast<long long>(gridDim.x) * groups) {
-    const long long token = first + (threadIdx.x >> p.log_lanes);
+  const long long block_first = static_cast<long long>(blockIdx.x) * (kQkThreads >> p.log_lanes);
+  long long token = sh.first;
+  for (long long f = block_first; f < p.tokens; f += sh.stride, token += sh.stride) {
     const bool valid = token < p.tokens;
     const long long tk = valid ? token : p.tokens - 1;
-    const long long b = tk / p.n, n = tk - b * p.n;
+    const long long b = p.tokens <= 0x7fffffffLL ? static_cast<long long>(p.d_n.div(static_cast<uint32_t>(tk))) : tk / p.n;
+    const long long n = tk - b * p.n;
     const long long pos = p.positions != nullptr ? p.positions[tk] : p.pos0 + n;
     float cs[SL][V], sn[SL][V];
 #pragma unroll
     for (int k = 0; k < SL; ++k) qk_angles<V>(s[k], turn, c0 + k * lanes, pos, cs[k], sn[k]);
-    const T* x0 = static_cast<const T*>(t.x) + b * t.xs[0] + n * t.xs[2];
-    const T* g0 = static_cast<const T*>(t.g) + b * t.gs[0] + n * t.gs[2];
-    T* y0 = static_cast<T*>(t.y) + b * t.ys[0] + n * t.ys[2];
-    for (int h = h0; h < h1; h += U) {
-      Vec<T, V> xv[U][SL][2], gv[U][SL][2];
+    T* row = static_cast<T*>(t.y) + b * t.ys[0] + n * t.ys[2] + sh.h0 * t.ys[1];
+    for (int h = sh.h0; h < sh.h1; ++h, row += t.ys[1]) {
+      Vec<T, V> va[2][SL], vb[2][SL];
+      ring.take(va, vb);
+      // g' = R(-theta) g, and the row's two sums
+      float xa[SL][V], xb[SL][V], ga[SL][V], gb[SL][V], sq[V], dt[V];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int hh = h + u < h1 ? h + u : h;
+      for (int e = 0; e < V; ++e) sq[e] = dt[e] = 0.0f;
 #pragma unroll
-        for (int k = 0; k < SL; ++k) {
-          xv[u][k][0] = qk_load<T, V>(x0 + hh * t.xs[1], s[k].ia, s[k].here);
-          xv[u][k][1] = qk_load<T, V>(x0 + hh * t.xs[1], s[k].ib, s[k].pair);
-          gv[u][k][0] = qk_load<T, V>(g0 + hh * t.gs[1], s[k].ia, s[k].here);
-          gv[u][k][1] = qk_load<T, V>(g0 + hh * t.gs[1], s[k].ib, s[k].pair);
-        }
+      for (int k = 0; k < SL; ++k) {
+        float fa[V], fb[V], tmp[V];
+        va[0][k].widen(xa[k]);
+        vb[0][k].widen(xb[k]);
+        va[1][k].widen(fa);
+        vb[1][k].widen(fb);
+        vmul<V>(tmp, fb, sn[k]);
+        vfma<V>(ga[k], fa, cs[k], tmp);
+        vscale<V>(fa, fa, -1.0f);
+        vmul<V>(tmp, fa, sn[k]);
+        vfma<V>(gb[k], fb, cs[k], tmp);
+        vfma<V>(sq, xa[k], xa[k], sq);
+        vfma<V>(sq, xb[k], xb[k], sq);
+        vmul<V>(tmp, ga[k], wa[k]);
+        vfma<V>(dt, tmp, xa[k], dt);
+        vmul<V>(tmp, gb[k], wb[k]);
+        vfma<V>(dt, tmp, xb[k], dt);
+      }
+      const float sum = qk_group_sum(vsum<V>(sq), lanes), dot = qk_group_sum(vsum<V>(dt), lanes);
+      ring.more();
+      if (!valid) continue;
+      const float r = rsqrtf(fmaf(sum, inv_d, p.eps));
+      const float back = -dot * inv_d * r * r;  // times x r: the norm's own share
+      float rr[V], kk[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        rr[e] = r;
+        kk[e] = back;
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float xa[SL][V], xb[SL][V], ga[SL][V], gb[SL][V];
-        float sum = 0.0f, dot = 0.0f;
-#pragma unroll
-        for (int k = 0; k < SL; ++k) {
-          xv[u][k][0].widen(xa[k]);
-          xv[u][k][1].widen(xb[k]);
-          float fa[V], fb[V];
-          gv[u][k][0].widen(fa);
-          gv[u][k][1].widen(fb);
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            ga[k][e] = fa[e] * cs[k][e] + fb[e] * sn[k][e];
-            gb[k][e] = fb[e] * cs[k][e] - fa[e] * sn[k][e];
-            sum = fmaf(xa[k][e], xa[k][e], fmaf(xb[k][e], xb[k][e], sum));
-            dot = fmaf(ga[k][e] * wa[k][e], xa[k][e], fmaf(gb[k][e] * wb[k][e], xb[k][e], dot));
-          }
-        }
-        sum = qk_group_sum(sum, lanes);
-        dot = qk_group_sum(dot, lanes);
-        if (!valid || h + u >= h1) continue;
-        const float r = __frsqrt_rn(fmaf(sum, inv_d, p.eps));
-        const float back = dot * inv_d * r * r;  // times x r: the norm's own share
-        T* row = y0 + (h + u) * t.ys[1];
-#pragma unroll
-        for (int k = 0; k < SL; ++k) {
-          float oa[V], ob[V];
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            da[k][e] = fmaf(ga[k][e], xa[k][e] * r, da[k][e]);
-            db[k][e] = fmaf(gb[k][e], xb[k][e] * r, db[k][e]);
-            oa[e] = r * (ga[k][e] * wa[k][e] - xa[k][e] * back);
-            ob[e] = r * (gb[k][e] * wb[k][e] - xb[k][e] * back);
-          }
-          Vec<T, V> va, vb;
-          va.narrow(oa);
-          vb.narrow(ob);
-          if (s[k].here) *reinterpret_cast<Vec<T, V>*>(row + s[k].ia) = va;
-          if (s[k].pair) *reinterpret_cast<Vec<T, V>*>(row + s[k].ib) = vb;
-        }
+      for (int k = 0; k < SL; ++k) {
+        // x r, dw += g' (x r), dx = r (g' w) + (x r) back
+        float tmp[V];
+        Vec<T, V> oa, ob;
+        vmul<V>(xa[k], xa[k], rr);
+        vmul<V>(xb[k], xb[k], rr);
+        vfma<V>(da[k], ga[k], xa[k], da[k]);
+        vfma<V>(db[k], gb[k], xb[k], db[k]);
+        vmul<V>(tmp, ga[k], wa[k]);
+        vmul<V>(xa[k], xa[k], kk);
+        vfma<V>(tmp, tmp, rr, xa[k]);
+        oa.narrow(tmp);
+        vmul<V>(tmp, gb[k], wb[k]);
+        vmul<V>(xb[k], xb[k], kk);
+        vfma<V>(tmp, tmp, rr, xb[k]);
+        ob.narrow(tmp);
+        if (s[k].here) *reinterpret_cast<Vec<T, V>*>(row + s[k].ia) = oa;
+        if (s[k].pair) *reinterpret_cast<Vec<T, V>*>(row + s[k].ib) = ob;
       }
     }
   }
+  ptx::grid_dep_launch();
   if (p.part == nullptr) return;
   const int warp = static_cast<int>(threadIdx.x) >> 5;
 #pragma unroll
@@ -353,6 +532,7 @@ __global__ void __launch_bounds__(1024) vattn_qk_weight_sum_kernel(const QkWeigh
   if (p.dw[which] == nullptr) return;
   float a = 0.0f;
   if (d < p.D)
+#pragma unroll 8
     for (long long r = p.row0[which] + threadIdx.y; r < p.row1[which]; r += 32) a += p.part[r * p.D + d];
   red[threadIdx.y][threadIdx.x] = a;
   __syncthreads();
