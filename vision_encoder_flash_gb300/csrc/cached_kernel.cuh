@@ -33,6 +33,7 @@ namespace vattn {
 constexpr int kCachedThreads = 128;
 constexpr int kCachedKeys = 64;  // keys of a tile
 constexpr int kCachedStages = 3;
+constexpr int kCachedMaxSplits = 512;
 
 struct CachedParams {
   WindowParams w;
@@ -104,6 +105,7 @@ struct CachedPlan {
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kOffP = kCachedStages * kStageBytes;  // weights of the loops' path, per warp
   static constexpr int kSmemBytes = kOffP + 4 * 16 * kWarpKeys * 4;
+  static constexpr int kResident = 232448 / (kSmemBytes + 1536) < 4 ? 232448 / (kSmemBytes + 1536) : 4;  // blocks a multiprocessor
   static_assert(4 * 16 * (DP + 2) * 4 <= kOffP, "the warps' results reuse the ring");
 };
 
@@ -387,48 +389,75 @@ __global__ void __launch_bounds__(kCachedThreads)
   ptx::grid_dep_launch();
 }
 
-// Merges the shares of a row, in order.  One warp per row, 4 dims a lane.
+// Merges the shares of a row, one block per row: the weight of every share
+// first, then the four warps add a quarter of the shares each (4 dims a
+// lane), in a fixed order.
 template <typename T, int RW>
 __global__ void __launch_bounds__(128) vattn_cached_join_kernel(const __grid_constant__ CachedParams p) {
+  __shared__ float weight[kCachedMaxSplits];
+  __shared__ float red[8];
+  __shared__ float4 acc_s[4][32];
   const WindowParams& w = p.w;
-  const int lane = threadIdx.x & 31, D = w.dim;
-  const long long x = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const long long bk = x / p.rows;
-  const int rr = static_cast<int>(x - bk * p.rows);
-  if (bk >= static_cast<long long>(w.batch) * w.kv_heads) return;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, D = w.dim;
+  const long long bk = blockIdx.x / p.rows;
+  const int rr = static_cast<int>(blockIdx.x - bk * p.rows);
   const int b = static_cast<int>(bk / w.kv_heads), kh = static_cast<int>(bk - static_cast<long long>(b) * w.kv_heads);
+  const int t = rr / w.group;
   ptx::grid_dep_wait();
   const CachedSpan sp = CachedSpan::make(w, b, p.splits);
   const int shares = sp.shares();
   if (shares == 1) return;  // written by its block
+  const bool none = cached_word(w, b, t, sp.base) == 0;
   const long long at0 = (bk * p.row_blocks + rr / (16 * RW)) * p.splits * 16 * RW + rr % (16 * RW);
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + at0;
   float mx = -INFINITY;
-  for (int s = lane; s < shares; s += 32) mx = fmaxf(mx, p.part_ml[(at0 + s * 16LL * RW) * 2]);
+  for (int s = tid; s < shares; s += 128) mx = fmaxf(mx, ml[s * 16LL * RW].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if (lane == 0) red[warp] = mx;
+  __syncthreads();
+  mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
   const float ref = mx == -INFINITY ? 0.0f : mx;
-  float sum = 0.0f, acc[4] = {};
-#pragma unroll 4
-  for (int s = 0; s < shares; ++s) {
-    const long long at = at0 + s * 16LL * RW;
-    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
-    const float a = ptx::ex2_approx(ml.x - ref);
-    sum = fmaf(a, ml.y, sum);
-    if (lane * 4 < D) {
-      const float4 f = *reinterpret_cast<const float4*>(p.part_o + at * D + lane * 4);
+  float sum = 0.0f;
+  for (int s = tid; s < shares; s += 128) {
+    const float2 f = ml[s * 16LL * RW];
+    const float a = ptx::ex2_approx(f.x - ref);
+    weight[s] = a;
+    sum = fmaf(a, f.y, sum);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) red[4 + warp] = sum;
+  __syncthreads();
+  sum = (red[4] + red[5]) + (red[6] + red[7]);
+  float acc[4] = {};
+  if (lane * 4 < D) {
+    const float* from = p.part_o + at0 * D + lane * 4;
+#pragma unroll 8
+    for (int s = warp; s < shares; s += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(from + s * 16LL * RW * D);
+      const float a = weight[s];
       acc[0] = fmaf(a, f.x, acc[0]);
       acc[1] = fmaf(a, f.y, acc[1]);
       acc[2] = fmaf(a, f.z, acc[2]);
       acc[3] = fmaf(a, f.w, acc[3]);
     }
   }
-  const int t = rr / w.group;
-  const bool none = sum == 0.0f || cached_word(w, b, t, sp.base) == 0;
+  acc_s[warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+  __syncthreads();
+  if (warp != 0 || lane * 4 >= D) return;
   const float inv = 1.0f / sum;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) acc[e] = none ? 0.0f : acc[e] * inv;
-  if (lane * 4 < D)
-    reinterpret_cast<Vec<T, 4>*>(rows_at_mut<T>(p.out, b, kh * w.group + (rr - t * w.group), t) + lane * 4)->narrow(acc);
+  for (int k = 1; k < 4; ++k) {
+    const float4 f = acc_s[k][lane];
+    acc[0] += f.x;
+    acc[1] += f.y;
+    acc[2] += f.z;
+    acc[3] += f.w;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) acc[e] = none || sum == 0.0f ? 0.0f : acc[e] * inv;
+  reinterpret_cast<Vec<T, 4>*>(rows_at_mut<T>(p.out, b, kh * w.group + (rr - t * w.group), t) + lane * 4)->narrow(acc);
 }
 
 }  // namespace vattn

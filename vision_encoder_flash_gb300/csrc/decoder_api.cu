@@ -571,11 +571,19 @@ vattn_status cached_launch(vattn::CachedParams p, int sms, int device, cudaStrea
   if (st != VATTN_OK) return st;
   const long long seqs = static_cast<long long>(p.w.batch) * p.w.kv_heads;
   p.row_blocks = (p.rows + 16 * RW - 1) / (16 * RW);
-  if (p.row_blocks > 65535) return fail(VATTN_ERR_UNSUPPORTED, "too many query heads for one key head");
-  // shares of the keys: eight blocks a multiprocessor, none under 256 keys
+  if (p.row_blocks > 65535 || seqs * p.rows > INT32_MAX)
+    return fail(VATTN_ERR_UNSUPPORTED, "too many query rows");
+  // Shares of the keys: as many blocks as are resident at a time (32 sequences
+  // x 8 key heads x 16385 keys of 128, lengths from 5.4 k: 218 us with two a
+  // head, 307 with one, 229 with five; a tree of 31 over 4096 keys: 21 us in one
+  // round, 27 in two), of 256 keys at least, or of 128 where that makes no more
+  // than 32 shares (500 keys: 8.0 us against 10.6; 30000 keys: 12 us with 118
+  // shares, 16 with 235).
   const long long most_keys = std::min<long long>(p.w.n_keys, static_cast<long long>(p.w.sinks) + p.w.window + p.w.n_queries);
-  const long long blocks = seqs * p.row_blocks;
-  p.splits = static_cast<int>(std::max<long long>(1, std::min((8LL * sms + blocks - 1) / blocks, (most_keys + 255) / 256)));
+  const long long blocks = seqs * p.row_blocks, room = static_cast<long long>(P::kResident) * sms;
+  const long long fill = room / blocks >= 4 ? room / blocks : (room + blocks - 1) / blocks;
+  const long long fine = std::max(std::min(32LL, (most_keys + 127) / 128), (most_keys + 255) / 256);
+  p.splits = static_cast<int>(std::max(1LL, std::min({fill, fine, static_cast<long long>(vattn::kCachedMaxSplits)})));
   Workspace ws;
   if (p.splits > 1) {
     const size_t rows = static_cast<size_t>(blocks) * p.splits * 16 * RW;
@@ -588,9 +596,8 @@ vattn_status cached_launch(vattn::CachedParams p, int sms, int device, cudaStrea
   kernel<<<grid, vattn::kCachedThreads, P::kSmemBytes, stream>>>(p);
   if ((st = launched("cached attention kernel launch")) != VATTN_OK) return st;
   if (p.splits == 1) return VATTN_OK;
-  if ((seqs * p.rows + 3) / 4 > INT32_MAX) return fail(VATTN_ERR_UNSUPPORTED, "too many query rows");
   if ((st = launch_behind("cached attention join kernel launch", vattn::vattn_cached_join_kernel<T, RW>,
-                          dim3(static_cast<unsigned>((seqs * p.rows + 3) / 4)), dim3(128), 0, stream, p)) != VATTN_OK)
+                          dim3(static_cast<unsigned>(seqs * p.rows)), dim3(128), 0, stream, p)) != VATTN_OK)
     return st;
   return ws.release();
 }
