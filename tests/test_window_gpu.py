@@ -42,6 +42,8 @@ CASES = [
     ("f16", (1, 7, 7, 150, 150, 120), 40, 0, None, None, "packed"),
     ("bf16", (2, 3, 3, 33, 500, 64), 16, 3, [500, 17], [480, -20], "plain"),
     ("f16", (1, 1, 1, 5, 0, 16), None, 0, None, None, "plain"),          # no keys at all
+    ("f16", (2, 5, 1, 1111, 1111, 96), None, 0, [1111, 737], [0, 0], "plain"),  # key tiles cut into many chunks
+    ("bf16", (1, 6, 2, 1300, 1300, 128), 300, 140, None, None, "packed"),       # chunks of the first keys' tiles
 ]
 
 
@@ -217,6 +219,29 @@ def test_streams_and_graphs(td):
     for _, out in graphs:
         assert all(torch.equal(a, b) for a, b in zip(out, want))
     assert vef.device_status() == 0
+
+
+@pytest.mark.parametrize("dim", [64, 80, 96, 128])
+def test_short_walks_do_not_race(td, dim):
+    """Key tiles cut down to single items, then query tiles, by the same
+    blocks: twelve calls, all alike."""
+    torch, dev = td
+    x = [normal(torch, s, "f16", 140 + i, dev) for i, s in enumerate(((2, 5, 1111, dim), (2, 1, 1111, dim), (2, 1, 1111, dim), (2, 5, 1111, dim)))]
+    out, lse = vef.forward_window(*x[:3], return_lse=True, scale=dim ** -0.5)
+    first = vef.backward_window(x[3], *x[:3], out, lse, scale=dim ** -0.5)
+    for _ in range(11):
+        again = vef.backward_window(x[3], *x[:3], out, lse, scale=dim ** -0.5)
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+    # against the formula in f32: P and D are rounded by 2^-11 (dq, dk, dv are
+    # sums of about 500 of them, of random sign), the results once more
+    s = [t.float() for t in x]
+    k, v = (t.expand(2, 5, 1111, dim) for t in s[1:3])
+    mask = torch.ones(1111, 1111, dtype=torch.bool, device=dev).tril()
+    w = torch.softmax((s[0] @ k.transpose(2, 3) * dim ** -0.5).masked_fill(~mask, float("-inf")), -1)
+    ds = w * (s[3] @ v.transpose(2, 3) - (s[3] * (w @ v)).sum(-1, keepdim=True)) * dim ** -0.5
+    wants = (ds @ k, (ds.transpose(2, 3) @ s[0]).sum(1, keepdim=True), (w.transpose(2, 3) @ s[3]).sum(1, keepdim=True))
+    for got, want in zip(first, wants):
+        assert float((got.float() - want).norm() / want.norm()) <= 2.0 ** -9
 
 
 def test_lengths_outside_the_buffer_are_held(td):

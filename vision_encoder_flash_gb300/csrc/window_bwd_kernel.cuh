@@ -146,8 +146,13 @@ struct GradPlan {
 
 enum GradBar : int {
   kGbXFull = 0, kGbXEmpty = 1, kGbYFull = 2, kGbYEmpty = 10, kGbSFull = 18, kGbGFree = 19, kGbPFull = 20,
-  kGbPFree = 22, kGbSum = 24, kGbSumFree = 25, kGbNext = 26, kGbTaken = 28, kGbDone = 30, kGbCount = 31,
+  kGbPFree = 22, kGbSum = 24, kGbSumFree = 25, kGbNext = 27, kGbTaken = 29, kGbDone = 31, kGbCount = 32,
 };
+// A wait names a phase by its parity, so whoever waits on a barrier has seen
+// the phase before the one it waits for.  The score issuer does not look at
+// every X tile's sums, hence two SumFree barriers in turn: when it waits for
+// the last tile's, those of the tile two before are done (the last tile's first
+// S needed the tile before to have used P and D, whose sums needed them).
 
 // What a block walks over: Y tiles 0 .. n - 1 of its share.
 template <bool kKeys>
@@ -320,7 +325,7 @@ __device__ __forceinline__ bool grad_scores(const GradCtx& x, int block, uint32_
   if (!x.pipe.wait_warp(x.bar(kGbXFull), tiles & 1u, kSiteGradMma)) return false;
   // from keys to queries the second A column takes dV's place: its last sums have been read
   if (NKB == 2 && !kKeys && keys_before &&
-      !x.pipe.wait_warp(x.bar(kGbSumFree), (tiles - 1) & 1u, kSiteGradMma))
+      !x.pipe.wait_warp(x.bar(kGbSumFree + ((tiles - 1) & 1u)), ((tiles - 1) >> 1) & 1u, kSiteGradMma))
     return false;
   keys_before = kKeys;
   ++tiles;
@@ -385,7 +390,8 @@ __device__ __forceinline__ bool grad_sums(const GradCtx& x, int block, uint32_t&
       ptx::idesc_16bit_f32(kTile, static_cast<uint32_t>((p.w.dim + 15) >> 4) * 16u, true, Elem<T>::kBf16);
   constexpr uint32_t hi = ptx::smem_desc_hi(1024, ptx::kSwizzle128B);
   // the last X tile's sums have been read
-  if (!x.pipe.wait_warp(x.bar(kGbSumFree), (tiles & 1u) ^ 1u, kSiteGradMma)) return false;
+  if (tiles > 0 && !x.pipe.wait_warp(x.bar(kGbSumFree + ((tiles - 1) & 1u)), ((tiles - 1) >> 1) & 1u, kSiteGradMma))
+    return false;
   ++tiles;
   for (int n = 0; n < wk.n; ++n, ++at) {
     const uint32_t slot = at % P::kSlots, turn = (at / P::kSlots) & 1u;
@@ -563,7 +569,7 @@ __device__ __forceinline__ bool grad_math(const GradCtx& x, int block, uint32_t&
   }
   if (wk.n > 0) {
     ptx::tc_fence_before();
-    pipe_warp_arrive(x.bar(kGbSumFree));
+    pipe_warp_arrive(x.bar(kGbSumFree + ((tiles - 1) & 1u)));
   }
   return true;
 }
@@ -601,11 +607,11 @@ __global__ void __launch_bounds__(GradPlan<NKB>::kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       init(kGbPFull + i, 8);
       init(kGbPFree + i, 1);
+      init(kGbSumFree + i, 8);
       init(kGbNext + i, 1);
       init(kGbTaken + i, 11);  // loader, two issuers, eight math warps
     }
     init(kGbSum, 1);
-    init(kGbSumFree, 8);
     init(kGbDone, 2);
     *abort_flag = 0;
     ptx::fence_mbar_init();
