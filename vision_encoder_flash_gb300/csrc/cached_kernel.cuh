@@ -5,10 +5,13 @@
 // token, query head of the group) of its key head together.  A block takes
 // up to 16 RW rows and a share of the keys, 64 keys at a time, through a
 // three-stage cp.async ring; the two products are mma.sync m16n8k16, whose 16
-// rows fit the few that there are (a tcgen05 tile has 128).  RW of the four
-// warps' groups take 16 rows each, the other factor shares the tile's keys:
+// rows fit the few that there are (a tcgen05 tile has 128).  RW groups of
+// warps take 16 rows each, the warps of a group share the tile's keys:
 //   rows <= 16: four warps, 16 keys of the tile each
-//   rows <= 32: two by two, 32 keys each;   more: 16 rows a warp, all 64 keys
+//   rows <= 32: two groups of four, 16 keys each (above 64 dims of two, 32
+//               keys: eight warps' registers would leave one block resident)
+//   more:       four groups of two, 32 keys each (a tree of 31 tokens, 4 heads
+//               a key head, over 4096 keys: see cached_launch)
 //
 // The keys that any row sees are numbered through: first the first keys that
 // lie before the lowest window, then those from that window to the end.  The
@@ -30,7 +33,6 @@
 
 namespace vattn {
 
-constexpr int kCachedThreads = 128;
 constexpr int kCachedKeys = 64;  // keys of a tile
 constexpr int kCachedStages = 3;
 constexpr int kCachedMaxSplits = 512;
@@ -99,22 +101,26 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4
 }
 template <int DP, int RW>
 struct CachedPlan {
-  static constexpr int kKw = 4 / RW;                   // warps that share a tile's keys
+  static constexpr int kWarps = RW == 1 || (RW == 2 && DP == 128) ? 4 : 8;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kKw = kWarps / RW;              // warps that share a tile's keys
   static constexpr int kWarpKeys = kCachedKeys / kKw;
   static constexpr int kTileBytes = kCachedKeys * DP * 2;
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kOffP = kCachedStages * kStageBytes;  // weights of the loops' path, per warp
-  static constexpr int kSmemBytes = kOffP + 4 * 16 * kWarpKeys * 4;
-  static constexpr int kResident = 232448 / (kSmemBytes + 1536) < 4 ? 232448 / (kSmemBytes + 1536) : 4;  // blocks a multiprocessor
-  static_assert(4 * 16 * (DP + 2) * 4 <= kOffP, "the warps' results reuse the ring");
+  static constexpr int kSmemBytes = kOffP + kWarps * 16 * kWarpKeys * 4;
+  // blocks a multiprocessor, by shared memory (4 warps) or registers (8)
+  static constexpr int kResident = (kWarps == 4 ? 4 : 2) / (DP == 64 ? 1 : 2);
+  static_assert(kWarps * 16 * (DP + 2) * 4 <= kOffP, "the warps' results reuse the ring");
 };
 
 template <typename T, int DP, int RW>
-__global__ void __launch_bounds__(kCachedThreads)
+__global__ void __launch_bounds__(CachedPlan<DP, RW>::kThreads)
     vattn_cached_kernel(const __grid_constant__ CachedParams p) {
   using P = CachedPlan<DP, RW>;
   constexpr int KN = P::kWarpKeys / 8;  // 8-key blocks of a warp's tile share
   constexpr int CH = DP / 8;            // 16-byte chunks of a shared row
+  constexpr int kThreads = P::kThreads;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int kpos[VATTN_MAX_NEW_TOKENS];
   const uint32_t smem_s = ptx::smem_addr(smem);
@@ -132,7 +138,7 @@ __global__ void __launch_bounds__(kCachedThreads)
     __syncthreads();  // the previous sequence's reads of the ring and kpos
     if (tid < w.n_queries) kpos[tid] = sp.base + __popcll(cached_word(w, b, tid, sp.base)) - 1;
 
-    // ---- the ring: thread = 16-byte chunk tid % CH of rows tid / CH, + 128 / CH, ...
+    // ---- the ring: thread = 16-byte chunk tid % CH of rows tid / CH, + kThreads / CH, ...
     const T* kbase = rows_at<T>(p.k, b, kh, 0);
     const T* vbase = rows_at<T>(p.v, b, kh, 0);
     const int ch = tid % CH, tiles = (max(v1 - v0, 0) + kCachedKeys - 1) / kCachedKeys;
@@ -140,7 +146,7 @@ __global__ void __launch_bounds__(kCachedThreads)
       if (tile < tiles && ch * 8 < ((D + 15) & ~15)) {
         const uint32_t st = smem_s + static_cast<uint32_t>(tile % kCachedStages) * P::kStageBytes;
 #pragma unroll 4
-        for (int r = tid / CH; r < kCachedKeys; r += kCachedThreads / CH) {
+        for (int r = tid / CH; r < kCachedKeys; r += kThreads / CH) {
           const int i = v0 + tile * kCachedKeys + r;
           const bool on = i < v1 && ch * 8 < D;
           const long long j = sp.key(i < v1 ? i : v0);
@@ -352,7 +358,7 @@ __global__ void __launch_bounds__(kCachedThreads)
     }
     __syncthreads();
     const bool alone = p.splits == 1 || sp.shares() == 1;
-    for (int x = tid; x < 16 * RW * (D / 8); x += kCachedThreads) {
+    for (int x = tid; x < 16 * RW * (D / 8); x += kThreads) {
       const int r = x / (D / 8), d = x % (D / 8) * 8;
       const int rr = rb * 16 * RW + r;
       if (rr >= p.rows) continue;

@@ -593,7 +593,7 @@ vattn_status cached_launch(vattn::CachedParams p, int sms, int device, cudaStrea
   }
   const dim3 grid(static_cast<unsigned>(p.splits), static_cast<unsigned>(p.row_blocks),
                   static_cast<unsigned>(std::min<long long>(seqs, 65535)));
-  kernel<<<grid, vattn::kCachedThreads, P::kSmemBytes, stream>>>(p);
+  kernel<<<grid, P::kThreads, P::kSmemBytes, stream>>>(p);
   if ((st = launched("cached attention kernel launch")) != VATTN_OK) return st;
   if (p.splits == 1) return VATTN_OK;
   if ((st = launch_behind("cached attention join kernel launch", vattn::vattn_cached_join_kernel<T, RW>,
