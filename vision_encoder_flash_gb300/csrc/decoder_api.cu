@@ -487,7 +487,9 @@ vattn_status backward_window(const Tensor& tg, const Tensor& tq, const Tensor& t
   // is cut so that no block has more than a third of a multiprocessor's share
   // of the call (the walk over query tiles is about as long as that over key
   // tiles; without a window a tile sees half the rows on average), but not
-  // under 4 items.
+  // under 8 items unless there are fewer blocks than multiprocessors.  (2 x
+  // 5(1) x 1111 x 96: 36 us, with 4 items 41; 1 x 8(1) x 200 x 64: 15 us, with 8
+  // items 21; 2 x 16(4) x 4096 x 64, window 1024: a half 154 us, a third 142, a fifth 159.)
   const long long all_items = static_cast<long long>(p.w.group) * row_tiles;
   const long long items = std::min<long long>(
       all_items, static_cast<long long>(p.w.group) * ((static_cast<long long>(p.w.window) + kTile - 2) / kTile + 1));
@@ -495,8 +497,9 @@ vattn_status backward_window(const Tensor& tg, const Tensor& tq, const Tensor& t
   const long long bhs = static_cast<long long>(p.w.batch) * p.w.heads;
   const long long key_tiles = std::max<long long>(1, seqs * p.key_tiles), query_tiles = bhs * row_tiles;
   const double total = static_cast<double>(key_tiles) * static_cast<double>(items) * (items < all_items ? 2.0 : 1.0);
-  const long long most = std::max(4LL, static_cast<long long>(total / (3.0 * sms)));
-  auto cut = [most](long long n) { return static_cast<int>(std::max(1LL, std::min(256LL, (n + most - 1) / most))); };
+  long long most = std::max(8LL, static_cast<long long>(total / (3.0 * sms)));
+  auto cut = [&most](long long n) { return static_cast<int>(std::max(1LL, std::min(256LL, (n + most - 1) / most))); };
+  while (most > 2 && key_tiles * cut(items) + query_tiles < sms) most /= 2;
   p.chunks = cut(items);
   p.sink_chunks = p.sink_tiles > 0 ? cut(all_items) : 1;
   const long long sink_blocks = seqs * p.sink_tiles * p.sink_chunks;
