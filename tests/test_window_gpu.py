@@ -253,6 +253,24 @@ def test_lengths_outside_the_buffer_are_held(td):
     assert torch.equal(got, want) and not f64(got[1:]).any()
 
 
+def test_no_query_heads_and_no_keys(td):
+    """Key heads without query heads (their gradients are zeros; there is no
+    row of out and lse to read), and query rows without keys."""
+    torch, dev = td
+    k = normal(torch, (2, 2, 300, 64), "bf16", 160, dev)
+    q = k.new_empty(2, 0, 200, 64)
+    out, lse = vef.forward_window(q, k, k, return_lse=True)
+    dq, dk, dv = vef.backward_window(q, q, k, k, out, lse, dk=torch.full_like(k, 7.0), dv=torch.full_like(k, 7.0))
+    assert out.shape == dq.shape == q.shape and lse.shape == (2, 0, 200)
+    assert not dk.any() and not dv.any()
+    none = k[:, :, :0]
+    out, lse = vef.forward_window(k, none, none, return_lse=True)
+    assert not out.any() and bool(torch.isneginf(lse).all())
+    dq, dk, dv = vef.backward_window(k, k, none, none, out, lse)
+    assert not dq.any() and dk.shape == dv.shape == none.shape
+    assert vef.device_status() == 0
+
+
 @pytest.mark.parametrize("bad", [dict(window=0), dict(scale=0.0), dict(n_sinks=-1)])
 def test_refusals(td, bad):
     torch, dev = td

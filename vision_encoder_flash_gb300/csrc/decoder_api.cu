@@ -479,7 +479,8 @@ vattn_status backward_window(const Tensor& tg, const Tensor& tq, const Tensor& t
   using vattn::kTile;
   vattn_status st;
   const long long seqs = static_cast<long long>(p.w.batch) * p.w.kv_heads;
-  const int row_tiles = (p.w.n_queries + kTile - 1) / kTile;
+  // (no query heads: no query rows either, and dk and dv are zeros)
+  const int row_tiles = p.w.heads > 0 ? (p.w.n_queries + kTile - 1) / kTile : 0;
   p.stat_tiles = 2 * row_tiles;
   p.key_tiles = (p.w.n_keys + kTile - 1) / kTile;
   // Items (query tiles of all heads of the group) of an ordinary key tile,
