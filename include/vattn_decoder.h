@@ -120,7 +120,9 @@ typedef struct {
  *
  * q [batch, n_q_heads, n_queries, head_dim], k and v [batch, n_kv_heads,
  * n_keys, head_dim], out as q: 16-byte aligned, strides multiples of 8
- * elements.  lse: NULL or f32 [batch, n_q_heads, n_queries] contiguous, the
+ * elements, and (here and in vattn_backward_window) a row stride of at least
+ * head_dim: broadcast heads and sequences are read as they are, broadcast
+ * rows are refused.  lse: NULL or f32 [batch, n_q_heads, n_queries] contiguous, the
  * natural logarithm of the sum of the row's exponentials (for
  * vattn_backward_window).  n_queries, n_keys < 2^29; q_start is held to
  * +-2^30.

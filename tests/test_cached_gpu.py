@@ -156,6 +156,17 @@ def test_streams_graphs_and_views(td):
     assert torch.equal(big[:, :, 1:9].transpose(1, 2), want) and bool((big[:, :, [0, 9]] == 3).all())
 
 
+def test_broadcast_rows(td):
+    """A cache whose rows, heads or sequences are one (strides of zero)."""
+    torch, dev = td
+    q = normal(torch, (2, 4, 3, 64), "f16", 150, dev)
+    lens = torch.tensor([70, 12], dtype=torch.int32, device=dev)
+    for shape in ((2, 2, 1, 64), (1, 1, 70, 64), (1, 1, 1, 64)):
+        wide = [normal(torch, shape, "f16", 151 + i, dev).expand(2, 2, 70, 64) for i in range(2)]
+        got = vef.forward_cached(q, *wide, lens, scale=0.125)
+        assert torch.equal(got, vef.forward_cached(q, *[t.contiguous() for t in wide], lens, scale=0.125))
+
+
 def test_refusals(td):
     torch, dev = td
     q, k = (normal(torch, s, "f16", 1, dev) for s in ((1, 2, 65, 16), (1, 2, 100, 16)))

@@ -147,6 +147,15 @@ def test_attention_refuses_tensors(lib):
     assert backward(lib, dk=rows(6, strides=(0, 0, 64))) == 1
 
 
+def test_window_refuses_rows_that_share_addresses(lib):
+    for stride in (0, 56):
+        for call, name, h in ((window, "q", 4), (window, "k", 2), (window, "v", 2), (backward, "dout", 4),
+                              (backward, "q", 4), (backward, "k", 2), (backward, "v", 2)):
+            i = dict(q=0, k=1, v=2)[name] if call is window else dict(dout=0, q=1, k=2, v=3)[name]
+            assert call(lib, **{name: rows(i, h, strides=(h * 1024, 1024, stride))}) == 2
+            assert "row stride" in lib.vattn_last_error_string().decode()
+
+
 def test_empty_attention_is_a_no_op(lib):
     for kw in (dict(batch=0), dict(hq=0, hk=0), dict(m=0)):
         assert window(lib, win_args(**kw)) == 0

@@ -364,6 +364,14 @@ vattn::RowsTensor rows_tensor(const vattn_rows* t) {
   return r;
 }
 
+// Tensors that are read through a tensor map have their rows apart: a map's
+// row stride is not below the row's own length.
+vattn_status check_map_rows(const Tensor& x) {
+  if (x.empty() || x.size[2] <= 1 || x.t->stride[2] >= x.dim) return VATTN_OK;
+  return fail(VATTN_ERR_UNSUPPORTED, "%s: row stride %lld below head_dim (rows broadcast or overlapping)", x.name,
+              (long long)x.t->stride[2]);
+}
+
 vattn_status forward_checks(const vattn_rows* q, const vattn_rows* k, const vattn_rows* v,
                             const vattn_rows* out, const float* lse, const vattn_window_args* a) {
   const Tensor tq = window_tensor("q", q, a, true, false), tk = window_tensor("k", k, a, false, false),
@@ -766,6 +774,9 @@ vattn_status vattn_forward_window(const vattn_rows* q, const vattn_rows* k, cons
   if (st != VATTN_OK) return st;
   if (a->tree) return fail(VATTN_ERR_INVALID_ARG, "tree is for vattn_forward_cached");
   if ((st = forward_checks(q, k, v, out, lse, a)) != VATTN_OK) return st;
+  for (const Tensor& t : {window_tensor("q", q, a, true, false), window_tensor("k", k, a, false, false),
+                          window_tensor("v", v, a, false, false)})
+    if ((st = check_map_rows(t)) != VATTN_OK) return st;
   if (a->batch * a->n_q_heads == 0 || a->n_queries == 0) return VATTN_OK;
   return forward_window(q, k, v, out, lse, a, static_cast<cudaStream_t>(stream_ptr));
 }
@@ -785,7 +796,7 @@ vattn_status vattn_backward_window(const vattn_rows* dout, const vattn_rows* q, 
   const Tensor* ins[5] = {&tg, &tq, &tk, &tv, &to};
   const Tensor* outs[3] = {&oq, &ok, &ov};
   for (const Tensor* t : ins)
-    if ((st = check_tensor(*t, 16)) != VATTN_OK) return st;
+    if ((st = check_tensor(*t, 16)) != VATTN_OK || (st = check_map_rows(*t)) != VATTN_OK) return st;
   for (const Tensor* t : outs)
     if ((st = check_tensor(*t, 16)) != VATTN_OK) return st;
   for (const Tensor* t : outs)

@@ -5,7 +5,8 @@ over a cache (C ABI: include/vattn_decoder.h).
 Tensors are ``[batch, heads, rows, head_dim]`` with a contiguous last
 dimension and any strides otherwise, so views of a packed projection
 ``[batch, rows, heads, head_dim]`` (``.transpose(1, 2)``) and of a cache go in
-as they are.  Every call runs on ``stream`` (default: the current torch
+as they are (rows that are a broadcast of one: ``forward_cached`` and
+``qk_norm_rope`` only).  Every call runs on ``stream`` (default: the current torch
 stream of the tensors' device) and returns without synchronising; results
 that it allocates belong to that stream.  With a ``stream`` of one's own, the
 inputs must be ready on it.  There is no CPU fallback.
