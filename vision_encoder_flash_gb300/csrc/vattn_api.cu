@@ -157,11 +157,18 @@ vattn_status pool_for(int device, cudaMemPool_t* out) {
     props.allocType = cudaMemAllocationTypePinned;
     props.location.type = cudaMemLocationTypeDevice;
     props.location.id = device;
+    // creating a pool touches no stream, but is refused while a stream of the
+    // process captures unless this thread says that it knows
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    dp.err = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (dp.err != cudaSuccess) return;
     dp.err = cudaMemPoolCreate(&dp.pool, &props);
     if (dp.err == cudaSuccess) {
       uint64_t keep = UINT64_MAX;
       dp.err = cudaMemPoolSetAttribute(dp.pool, cudaMemPoolAttrReleaseThreshold, &keep);
     }
+    const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (dp.err == cudaSuccess) dp.err = back;
   });
   if (dp.err != cudaSuccess) return cuda_fail(dp.err, "creating the workspace memory pool");
   *out = dp.pool;
