@@ -181,6 +181,26 @@ def test_shared_keys_of_a_broadcast(td):
     assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
+def test_first_keys_without_end(td):
+    """Every key is a first key, and the window one key wide: as without a
+    window, in a workspace of the size of the call's tensors, not of its
+    tiles' product."""
+    torch, dev = td
+    x = [normal(torch, (1, 1, 24577, 128), "bf16", 105 + i, dev) for i in range(4)]
+    out, lse = vef.forward_window(*x[:3], window=1, n_sinks=24577, scale=0.1, return_lse=True)
+    wout, wlse = vef.forward_window(*x[:3], scale=0.1, return_lse=True)
+    assert torch.equal(out, wout) and torch.equal(lse, wlse)
+    torch.cuda.synchronize(dev)
+    free = torch.cuda.mem_get_info(dev)[0]
+    got = vef.backward_window(x[3], *x[:3], out, lse, window=1, n_sinks=24577, scale=0.1)
+    torch.cuda.synchronize(dev)
+    # 192 key tiles in up to seven pieces of 128 KiB, and the results
+    assert free - torch.cuda.mem_get_info(dev)[0] < 2 ** 28
+    want = vef.backward_window(x[3], *x[:3], out, lse, scale=0.1)
+    for a, b in zip(got, want):  # the same products, cut into other chunks: rounded once from sums in f32
+        assert torch.allclose(a.float(), b.float(), rtol=2 ** -7, atol=2 ** -7 * float(b.float().abs().max()))
+
+
 def test_streams_and_graphs(td):
     torch, dev = td
     x = [normal(torch, (2, 4, 260, 64), "bf16", 110 + i, dev) for i in range(4)]

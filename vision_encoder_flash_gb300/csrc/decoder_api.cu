@@ -510,6 +510,9 @@ vattn_status backward_window(const Tensor& tg, const Tensor& tq, const Tensor& t
   auto cut = [&most](long long n) { return static_cast<int>(std::max(1LL, std::min(256LL, (n + most - 1) / most))); };
   while (most > 2 && key_tiles * cut(items) + query_tiles < sms) most /= 2;
   p.chunks = cut(items);
+  // The first keys' tiles together into eight pieces a multiprocessor at most:
+  // 160 MB of partial sums, where every key as a first key would take gigabytes.
+  most = std::max(most, static_cast<long long>(static_cast<double>(seqs * p.sink_tiles) * static_cast<double>(all_items) / (8.0 * sms)));
   p.sink_chunks = p.sink_tiles > 0 ? cut(all_items) : 1;
   const long long sink_blocks = seqs * p.sink_tiles * p.sink_chunks;
   const long long rest_blocks = seqs * (p.key_tiles - p.sink_tiles) * p.chunks;
