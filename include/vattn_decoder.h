@@ -38,7 +38,8 @@ typedef enum { VATTN_F32 = 0, VATTN_F16 = 1, VATTN_BF16 = 2 } vattn_dtype;
  * data + (b * stride[0] + h * stride[1] + i * stride[2] + d) elements.
  * Strides are >= 0; an input may have stride 0 (a broadcast), an output's
  * elements are distinct.  Outputs do not overlap inputs or each other (views
- * of one packed buffer that interleave without sharing elements are fine).
+ * of one packed buffer with equal strides that interleave without sharing
+ * elements are fine).
  */
 typedef struct {
   void* data;

@@ -91,27 +91,45 @@ bool same_rows(const Tensor& a, const Tensor& b) {
 }
 
 // No element of a is an element of b: their byte ranges are apart, or they
-// are head ranges of one packed buffer (equal strides, b's heads some whole
-// number of head strides behind a's, and the union of both has distinct
-// elements).
+// are parts of one packed buffer: equal strides, the one's first element some
+// whole number of strides behind the other's, a box around both whose elements
+// are distinct, and a dimension in which one's indexes end before the other's
+// begin.
 bool apart(const Tensor& a, const Tensor& b) {
   if (a.empty() || b.empty()) return true;
   if (a.base() + a.extent() <= b.base() || b.base() + b.extent() <= a.base()) return true;
   const Tensor& lo = a.base() <= b.base() ? a : b;
   const Tensor& hi = a.base() <= b.base() ? b : a;
-  if (lo.esize != hi.esize || lo.dim != hi.dim || lo.size[0] != hi.size[0] || lo.size[2] != hi.size[2]) return false;
-  for (int i = 0; i < 3; i += 2)
-    if (lo.size[i] > 1 && lo.t->stride[i] != hi.t->stride[i]) return false;
-  if (lo.size[1] > 1 && hi.size[1] > 1 && lo.t->stride[1] != hi.t->stride[1]) return false;
+  if (lo.esize != hi.esize || lo.dim != hi.dim) return false;
   const uint64_t bytes = hi.base() - lo.base();
   if (bytes % static_cast<uint64_t>(lo.esize) != 0) return false;
-  const int64_t delta = static_cast<int64_t>(bytes / static_cast<uint64_t>(lo.esize));
-  // head stride of the packed buffer (one head each: their distance)
-  const int64_t sh = lo.size[1] > 1 ? lo.t->stride[1] : (hi.size[1] > 1 ? hi.t->stride[1] : delta);
-  if (sh <= 0 || delta % sh != 0 || delta / sh < lo.size[1]) return false;
-  const int64_t size[3] = {lo.size[0], delta / sh + hi.size[1], lo.size[2]};
-  const int64_t stride[3] = {lo.t->stride[0], sh, lo.t->stride[2]};
-  return distinct(size, stride, lo.dim);
+  int64_t delta = static_cast<int64_t>(bytes / static_cast<uint64_t>(lo.esize));
+  int64_t size[3], stride[3] = {0, 0, 0}, off[3] = {0, 0, 0};
+  int order[3] = {0, 1, 2};
+  for (int i = 0; i < 3; ++i) {
+    if (lo.size[i] > 1 && hi.size[i] > 1 && lo.t->stride[i] != hi.t->stride[i]) return false;
+    if (lo.size[i] > 1 || hi.size[i] > 1) {
+      stride[i] = lo.size[i] > 1 ? lo.t->stride[i] : hi.t->stride[i];
+      if (stride[i] <= 0) return false;
+    }
+  }
+  std::sort(order, order + 3, [&](int x, int y) { return stride[x] > stride[y]; });
+  for (int i : order)
+    if (stride[i] > 0) {
+      off[i] = delta / stride[i];
+      delta -= off[i] * stride[i];
+    }
+  if (delta > 0) {  // one head each: their distance is the buffer's head stride
+    if (stride[1] > 0) return false;
+    stride[1] = delta;
+    off[1] = 1;
+  }
+  bool clear = false;
+  for (int i = 0; i < 3; ++i) {
+    size[i] = std::max(lo.size[i], off[i] + hi.size[i]);
+    clear |= off[i] >= lo.size[i];
+  }
+  return clear && distinct(size, stride, lo.dim);
 }
 
 vattn_status check_apart(const Tensor& a, const Tensor& b) {
