@@ -244,10 +244,32 @@ void qk_strides(long long (&to)[3], const vattn_rows* t) {
   for (int i = 0; i < 3; ++i) to[i] = t ? t->stride[i] : 0;
 }
 
-// Sizes, angles and the split of the heads: 16 heads per block and token
-// (angles shared by them: 52.7 us for 4 x 40 heads x 4096 x 128, with 8 heads
-// 53.9, with 4 69), fewer while that leaves under four blocks per
-// multiprocessor.
+// Heads that a block takes for each of its tokens, 16 or fewer.  More heads
+// share the angles, fewer leave shorter blocks: in units of one head's row, the
+// angles cost about eight, and a call lasts as long as its blocks' share on one
+// place of the resident ones, and its last block.  Halved while that gains 5 %.
+// (16 heads against 8: 4 x 40 heads x 4096 x 128 bf16 52.4 us and 53.9, 16 + 16 x
+// 4100 x 72 f32 17.5 and 15.2; 20 x 3000 x 128 bf16 7.3 us with 8, 9.4 with 4; 2 x
+// 8 x 1025 x 80 f16, gradient, 10.2 with 2, 12.5 with 8.)
+int qk_heads_per_block(const vattn::QkParams& p, double blocks_x, int resident) {
+  int best = 16;
+  double best_cost = 0.0;
+  for (int per = 16; per >= 1; per /= 2) {
+    double work = 0.0, longest = 0.0;
+    for (int i = 0; i < 2; ++i) {
+      const int heads = p.t[i].heads, slices = (heads + per - 1) / per;
+      work += heads + 8.0 * slices;
+      longest = std::max(longest, std::min(per, heads) + 8.0);
+    }
+    const double cost = work * blocks_x / resident + longest;
+    if (per < 16 && cost > 0.95 * best_cost) continue;
+    best = per;
+    best_cost = cost;
+  }
+  return best;
+}
+
+// Sizes, angles and the split of the heads over blocks.
 void qk_plan(vattn::QkParams* p, const vattn_qk_args* a, int v, int sms, int64_t* blocks_x) {
   p->positions = a->positions;
   p->factors = a->factors;
@@ -268,12 +290,9 @@ void qk_plan(vattn::QkParams* p, const vattn_qk_args* a, int v, int sms, int64_t
   while ((1 << p->log_lanes) < p->slots && p->log_lanes < 5) ++p->log_lanes;
   const int groups = vattn::kQkThreads >> p->log_lanes;
   *blocks_x = (p->tokens + groups - 1) / groups;
-  int per = 16;
-  for (;; per /= 2) {
-    int64_t slices = 0;
-    for (int i = 0; i < 2; ++i) slices += (p->t[i].heads + per - 1) / per;
-    if (per == 1 || slices * *blocks_x >= 4LL * sms) break;
-  }
+  const bool backward = p->t[0].g != nullptr || p->t[1].g != nullptr;
+  const int resident = vattn::qk_resident(v, backward) * sms;
+  const int per = qk_heads_per_block(*p, static_cast<double>(*blocks_x), resident);
   for (int i = 0; i < 2; ++i) {
     int hp = per;
     while ((p->t[i].heads + hp - 1) / hp > 16384) hp *= 2;  // grid limit in y
@@ -283,7 +302,7 @@ void qk_plan(vattn::QkParams* p, const vattn_qk_args* a, int v, int sms, int64_t
   // up to eight rounds of what is resident at a time (a block in flight for
   // each that ends), behind that the blocks walk over several tokens: with
   // gradients, each leaves one row of weight gradient
-  const int64_t most = 8 * (v == 8 ? 2LL : 3LL) * sms / (p->t[0].slices + p->t[1].slices);
+  const int64_t most = 8LL * resident / (p->t[0].slices + p->t[1].slices);
   *blocks_x = std::min(*blocks_x, std::max<int64_t>(1, most));
 }
 

@@ -40,6 +40,8 @@ namespace vattn {
 
 constexpr int kQkThreads = 256;
 constexpr int kQkMaxDim = 128;
+// Blocks a multiprocessor holds, by registers, for V pairs a lane.
+constexpr int qk_resident(int v, bool backward) { return v == 8 ? 2 : (backward ? 3 : 4); }
 
 struct QkTensor {
   const void* x;   // input rows
@@ -211,7 +213,7 @@ template <typename T, int V, int SL, int N>
 struct QkRing {
   static constexpr int kBytes = V * static_cast<int>(sizeof(T));
   static constexpr bool kAsync = kBytes >= 8 && SL == 1;
-  static constexpr int kStages = kAsync ? (N == 1 ? 6 : 4) : 1;
+  static constexpr int kStages = kAsync ? (N == 1 && V == 8 ? 6 : 4) : 1;
   static constexpr int kSmemBytes = kAsync ? kStages * N * 2 * kBytes * kQkThreads : 0;
 
   const QkParams& p;
@@ -318,7 +320,7 @@ struct QkShare {
 // All groups of a block take the same number of tokens: those past the end
 // work on zeros and store nothing.
 template <typename T, int V, int SL>
-__global__ void __launch_bounds__(kQkThreads, V == 8 ? 2 : 3)
+__global__ void __launch_bounds__(kQkThreads, qk_resident(V, false))
     vattn_qk_norm_rope_kernel(const __grid_constant__ QkParams p) {
   extern __shared__ __align__(16) uint8_t qk_smem[];
   __shared__ uint64_t turn[kQkMaxDim / 2];
@@ -396,7 +398,7 @@ __global__ void __launch_bounds__(kQkThreads, V == 8 ? 2 : 3)
 // memory, and one row of `part` per block that vattn_qk_weight_sum_kernel
 // adds in a fixed order.
 template <typename T, int V, int SL>
-__global__ void __launch_bounds__(kQkThreads, V == 8 ? 2 : 3)
+__global__ void __launch_bounds__(kQkThreads, qk_resident(V, true))
     vattn_qk_norm_rope_backward_kernel(const __grid_constant__ QkParams p) {
   extern __shared__ __align__(16) uint8_t qk_smem[];
   __shared__ uint64_t turn[kQkMaxDim / 2];
