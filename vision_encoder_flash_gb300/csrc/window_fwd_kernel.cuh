@@ -8,7 +8,8 @@
 // (row block, head of the group): with an even group both have the same
 // rows, hence the same tiles, and each K and V tile that comes from L2
 // serves 256 query rows.  The grid is one block per multiprocessor, each
-// walking over items from the longest to the shortest (late rows first).
+// walking over items from the longest to the shortest (late rows first).  A
+// call with few items takes each unit by itself.
 //
 //   warp 0   K and V tiles by TMA into a ring (K0 V0 K1 V1 ...)
 //   warp 2   the item's two Q tiles by TMA
@@ -49,6 +50,7 @@ struct WindowFwdParams {
   int pairs;           // items of one (batch, key head): its units by twos
   int units;           // ceil(n_queries / 128) * group
   int items;           // < 2^30
+  int whole;           // items from here on are single units (none of them, or all)
   FastDiv seqs, kv_heads, group;  // batch * kv_heads, kv_heads, group
   float scale_log2;    // scale * log2(e)
 };
@@ -82,9 +84,20 @@ struct WindowItem {
   __device__ __forceinline__ int tile(int x) const { return x < first_n ? x : second + (x - first_n); }
 };
 
-__device__ __forceinline__ WindowItem window_item(const WindowFwdParams& p, int item) {
+// The block's item of round r: back and forth over the blocks, so that none
+// has the longer item of every round (1 x 32(8) x 2048 x 128 without a window:
+// 33.2 us, in the same order every round 46.6; 2 x 16(4) x 4096 x 64, window
+// 1024: 52.6 and 59.0).
+__device__ __forceinline__ int window_entry(int r) {
+  const int grid = static_cast<int>(gridDim.x), k = static_cast<int>(blockIdx.x);
+  return r * grid + ((r & 1) ? grid - 1 - k : k);
+}
+
+__device__ __forceinline__ WindowItem window_item(const WindowFwdParams& p, int entry) {
   WindowItem it;
   uint32_t bk, kh;
+  const bool pair_on = entry < p.whole;
+  const int item = pair_on ? entry : p.whole + (entry - p.whole) / 2, only = (entry - p.whole) & 1;
   const int pair = p.pairs - 1 - static_cast<int>(p.seqs.div(static_cast<uint32_t>(item), &bk));
   it.b = static_cast<int>(p.kv_heads.div(bk, &kh));
   it.kh = static_cast<int>(kh);
@@ -95,7 +108,7 @@ __device__ __forceinline__ WindowItem window_item(const WindowFwdParams& p, int 
   for (int t = 0; t < 2; ++t) {
     const int unit = 2 * pair + t;
     uint32_t g;
-    it.on[t] = unit < p.units;
+    it.on[t] = unit < p.units && (pair_on || only == t);
     it.row0[t] = static_cast<int>(p.group.div(static_cast<uint32_t>(unit), &g)) * kTile;
     it.head[t] = it.kh * p.w.group + static_cast<int>(g);
     it.u[t] = it.on[t] ? unit_range(p.w, it.s, it.row0[t]) : UnitRange{0, 0, -1};
@@ -225,7 +238,7 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
       const uint64_t keep = ptx::policy_evict_last();  // read again by other heads and rows
       long long c = 0;  // ring entries so far
       bool ok = true;
-      for (int item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+      for (int r = 0, item; ok && (item = window_entry(r)) < p.items; ++r) {
         const WindowItem it = window_item(p, item);
         for (int x = 0; ok && x < it.n; ++x) {
           const int row = it.tile(x) * kTile;
@@ -247,13 +260,14 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
       // ------------------------------------------------------- Q tiles
       const uint64_t once = ptx::policy_evict_first();
       uint32_t n_q = 0;
-      for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
+      for (int r = 0, item; (item = window_entry(r)) < p.items; ++r) {
         const WindowItem it = window_item(p, item);
         if (it.n == 0) continue;
         if (n_q > 0 && !pipe.wait(bar(kWbQEmpty), (n_q - 1) & 1u, kSiteWinQ)) break;
-        ptx::mbar_arrive_expect_tx(bar(kWbQFull), (it.on[1] ? 2 : 1) * P::kTileBytes);
-        for (int t = 0; t < (it.on[1] ? 2 : 1); ++t)
-          for (int kb = 0; kb < NKB; ++kb)
+        ptx::mbar_arrive_expect_tx(bar(kWbQFull), (it.on[0] && it.on[1] ? 2 : 1) * P::kTileBytes);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          for (int kb = 0; it.on[t] && kb < NKB; ++kb)
             ptx::tma_load_4d_hint(base_s + P::kOffQ + t * P::kTileBytes + kb * kBlockBytes, &tm_q,
                                   bar(kWbQFull), kb * 64, it.row0[t], it.head[t] * p.mq.h,
                                   it.b * p.mq.b, once);
@@ -316,7 +330,7 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
       };
       long long g = 0;  // key tiles of this block so far; K of tile g is ring entry 2 g, V 2 g + 1
       bool ok = true;
-      for (int item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+      for (int r = 0, item; ok && (item = window_entry(r)) < p.items; ++r) {
         const WindowItem it = window_item(p, item);
         if (it.n == 0) continue;
         if (!(ok = pipe.wait_warp(bar(kWbQFull), n_q & 1u, kSiteWinMma))) break;
@@ -383,7 +397,7 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
     uint32_t n_s = 0;  // tiles of this unit so far
     int n_out = 0;     // result boxes of this warp so far
     bool ok = true;
-    for (int item = blockIdx.x; ok && item < p.items; item += gridDim.x) {
+    for (int round = 0, item; ok && (item = window_entry(round)) < p.items; ++round) {
       const WindowItem it = window_item(p, item);
       if (!(t == 0 ? it.on[0] : it.on[1])) continue;
       const UnitRange u = t == 0 ? it.u[0] : it.u[1];
