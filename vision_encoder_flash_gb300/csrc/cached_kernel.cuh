@@ -16,9 +16,10 @@
 // The keys that any row sees are numbered through: first the first keys that
 // lie before the lowest window, then those from that window to the end.  The
 // shares of the blocks are equal parts of that list, cut on the device from
-// the sequence's own length; where there is more than one, each leaves its
-// unnormalised O, maximum and sum in f32, and vattn_cached_join_kernel merges
-// them in order.
+// the sequence's own length.  Up to four shares are a cluster: each block
+// leaves its unnormalised O, maximum and sum in its shared memory, and all of
+// them merge a part of the rows from there, in the order of the shares.  More
+// shares go through a workspace and vattn_cached_join_kernel, likewise in order.
 //
 // Weights are rounded to the tensors' type for the second product, as in
 // window_fwd_kernel.cuh; everything else is f32.  Rows differ in what they
@@ -36,6 +37,10 @@ namespace vattn {
 constexpr int kCachedKeys = 64;  // keys of a tile
 constexpr int kCachedStages = 3;
 constexpr int kCachedMaxSplits = 512;
+// Shares that a cluster of blocks joins by itself (4 x 4 key heads x 31 tokens in a
+// tree over 200 keys of 64, two shares: 11.4 us, through a workspace 13.8; over 600
+// keys, five shares: 16.4 and 15.5, since larger clusters find less room).
+constexpr int kCachedCluster = 4;
 
 struct CachedParams {
   WindowParams w;
@@ -129,12 +134,14 @@ __global__ void __launch_bounds__(CachedPlan<DP, RW>::kThreads)
   const WindowParams& w = p.w;
   const int D = w.dim;
   const int split = blockIdx.x, rb = blockIdx.y;
+  const bool clustered = p.splits > 1 && p.splits <= kCachedCluster;
   ptx::grid_dep_wait();
   for (long long bk = blockIdx.z; bk < static_cast<long long>(w.batch) * w.kv_heads; bk += gridDim.z) {
     const int b = static_cast<int>(bk / w.kv_heads), kh = static_cast<int>(bk - static_cast<long long>(b) * w.kv_heads);
     const CachedSpan sp = CachedSpan::make(w, b, p.splits);
     const int v0 = split * sp.per, v1 = min(sp.n, v0 + sp.per);
-    if (split >= sp.shares()) continue;
+    const int shares = sp.shares();
+    if (!clustered && split >= shares) continue;  // (in a cluster: with no keys, but at its barriers)
     __syncthreads();  // the previous sequence's reads of the ring and kpos
     if (tid < w.n_queries) kpos[tid] = sp.base + __popcll(cached_word(w, b, tid, sp.base)) - 1;
 
@@ -357,12 +364,12 @@ __global__ void __launch_bounds__(CachedPlan<DP, RW>::kThreads)
       if ((lane & 3) == 0) *reinterpret_cast<float2*>(to + DP) = make_float2(m[e], l[e]);
     }
     __syncthreads();
-    const bool alone = p.splits == 1 || sp.shares() == 1;
+    const bool alone = p.splits == 1 || (shares == 1 && !clustered);
     for (int x = tid; x < 16 * RW * (D / 8); x += kThreads) {
       const int r = x / (D / 8), d = x % (D / 8) * 8;
       const int rr = rb * 16 * RW + r;
       if (rr >= p.rows) continue;
-      const float* from = res + ((r >> 4) * 16 + (r & 15)) * (DP + 2);  // warp r / 16, + RW for the next key share
+      float* from = res + r * (DP + 2);  // warp r / 16, + RW for the next key share
       float mx = -INFINITY;
 #pragma unroll
       for (int y = 0; y < P::kKw; ++y) mx = fmaxf(mx, from[y * RW * 16 * (DP + 2) + DP]);
@@ -375,6 +382,11 @@ __global__ void __launch_bounds__(CachedPlan<DP, RW>::kThreads)
         sum = fmaf(a, f[DP + 1], sum);
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = fmaf(a, f[d + e], acc[e]);
+      }
+      if (clustered) {  // in place of the first key share's
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) *reinterpret_cast<float2*>(from + d + e) = make_float2(acc[e], acc[e + 1]);
+        continue;
       }
       const int t = rr / w.group;
       if (alone) {
@@ -391,6 +403,57 @@ __global__ void __launch_bounds__(CachedPlan<DP, RW>::kThreads)
         if (d == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(mx, sum);
       }
     }
+    if (!clustered) continue;
+    __syncthreads();
+    if (tid < 16 * RW) {
+      float* row = res + tid * (DP + 2);
+      float mx = -INFINITY, sum = 0.0f;
+#pragma unroll
+      for (int y = 0; y < P::kKw; ++y) mx = fmaxf(mx, row[y * RW * 16 * (DP + 2) + DP]);
+      const float ref = mx == -INFINITY ? 0.0f : mx;
+#pragma unroll
+      for (int y = 0; y < P::kKw; ++y) {
+        const float* f = row + y * RW * 16 * (DP + 2) + DP;
+        sum = fmaf(ptx::ex2_approx(f[0] - ref), f[1], sum);
+      }
+      *reinterpret_cast<float2*>(row + DP) = make_float2(mx, sum);
+    }
+    ptx::cluster_sync();
+    for (int x = split * kThreads + tid; x < 16 * RW * (D / 8); x += p.splits * kThreads) {
+      const int r = x / (D / 8), d = x % (D / 8) * 8;
+      const int rr = rb * 16 * RW + r;
+      if (rr >= p.rows) continue;
+      const uint32_t row = smem_s + static_cast<uint32_t>(r * (DP + 2) * 4);
+      float2 ml[kCachedCluster];
+      float mx = -INFINITY;
+#pragma unroll
+      for (int s = 0; s < kCachedCluster; ++s) {
+        ml[s] = s < shares ? ptx::ld_cluster_v2(ptx::cluster_map(row + DP * 4, s)) : make_float2(-INFINITY, 0.0f);
+        mx = fmaxf(mx, ml[s].x);
+      }
+      const float ref = mx == -INFINITY ? 0.0f : mx;
+      float sum = 0.0f, acc[8] = {};
+#pragma unroll
+      for (int s = 0; s < kCachedCluster; ++s) {
+        if (s >= shares) break;
+        const float a = ptx::ex2_approx(ml[s].x - ref);
+        sum = fmaf(a, ml[s].y, sum);
+        const uint32_t from = ptx::cluster_map(row + static_cast<uint32_t>(d) * 4, s);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const float2 f = ptx::ld_cluster_v2(from + e * 4);
+          acc[e] = fmaf(a, f.x, acc[e]);
+          acc[e + 1] = fmaf(a, f.y, acc[e + 1]);
+        }
+      }
+      const int t = rr / w.group;
+      const bool none = sum == 0.0f || cached_word(w, b, t, sp.base) == 0;
+      const float inv = 1.0f / sum;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = none ? 0.0f : acc[e] * inv;
+      reinterpret_cast<Vec<T, 8>*>(rows_at_mut<T>(p.out, b, kh * w.group + (rr - t * w.group), t) + d)->narrow(acc);
+    }
+    ptx::cluster_sync();  // before the shared memory that others read goes
   }
   ptx::grid_dep_launch();
 }

@@ -643,7 +643,8 @@ vattn_status cached_launch(vattn::CachedParams p, int sms, int device, cudaStrea
   const long long fine = std::max(std::min(32LL, (most_keys + 127) / 128), (most_keys + 255) / 256);
   p.splits = static_cast<int>(std::max(1LL, std::min({fill, fine, static_cast<long long>(vattn::kCachedMaxSplits)})));
   Workspace ws;
-  if (p.splits > 1) {
+  const bool clustered = p.splits > 1 && p.splits <= vattn::kCachedCluster;
+  if (p.splits > 1 && !clustered) {
     const size_t rows = static_cast<size_t>(blocks) * p.splits * 16 * RW;
     if ((st = ws.take(rows * (p.w.dim + 2) * 4, device, stream)) != VATTN_OK) return st;
     p.part_o = reinterpret_cast<float*>(ws.data());
@@ -651,6 +652,21 @@ vattn_status cached_launch(vattn::CachedParams p, int sms, int device, cudaStrea
   }
   const dim3 grid(static_cast<unsigned>(p.splits), static_cast<unsigned>(p.row_blocks),
                   static_cast<unsigned>(std::min<long long>(seqs, 65535)));
+  if (clustered) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(P::kThreads);
+    cfg.dynamicSmemBytes = P::kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = grid.x;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+    return e == cudaSuccess ? VATTN_OK : cuda_fail(e, "cached attention kernel launch");
+  }
   kernel<<<grid, P::kThreads, P::kSmemBytes, stream>>>(p);
   if ((st = launched("cached attention kernel launch")) != VATTN_OK) return st;
   if (p.splits == 1) return VATTN_OK;
