@@ -21,6 +21,11 @@
 // them merge a part of the rows from there, in the order of the shares.  More
 // shares go through a workspace and vattn_cached_join_kernel, likewise in order.
 //
+// 32 sequences x 8 key heads x up to 16385 keys of 128 bf16: 214.8 us, 6.75 TB/s
+// (99 % of the measured copy rate).  A tree of 31 tokens over 4 x 4 heads x 4100
+// keys of 64 f16: 21 us, bound by latency: about 420 instructions a warp and
+// tile, seven tiles a block, the rest its start and the join.
+//
 // Weights are rounded to the tensors' type for the second product, as in
 // window_fwd_kernel.cuh; everything else is f32.  Rows differ in what they
 // see only at the window's edge and among the new tokens: tiles there are

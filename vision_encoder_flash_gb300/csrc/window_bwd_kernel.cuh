@@ -41,8 +41,19 @@
 // added in order by vattn_window_join_kernel) where tiles are few or, for the
 // tiles of the first keys, the walk is long.
 //
-// Rounding: P and D go to the tensors' type for the second products; all
-// sums, lse and delta are f32.
+// Rounding: P and D go to the tensors' type for the second products, as these
+// need (relative 2^-9 / 2^-12 at most of each term; with f16 a D beyond 65504
+// is infinite, as dq, dk and dv of that size would be), and delta comes from
+// `out` as rounded; all sums, lse and delta are f32.  For long rows that stays
+// below the rounding of the results; for rows of a few keys dq and dk are off by
+// up to twice as much as their own rounding.
+//
+// What bounds it: for a tile of 128 x 128 pairs the products take 2080 cycles at
+// head_dim 128 (keys; queries 1560) and half of that at 64, the arithmetic on
+// the pairs about 1100 a warpgroup, and S, G, P, D and the sums follow each
+// other through TMEM, where head_dim 128 leaves one pair of S and G.  2 x 16(4) x
+// 4096 x 64, window 1024, 4 first keys: 142 us, 531 TFLOP/s counted as 10 D flops
+// a visible pair, 743 with the products that are computed twice.
 #pragma once
 
 #include "window_pipe.cuh"

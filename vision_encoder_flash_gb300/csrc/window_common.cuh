@@ -36,7 +36,7 @@ struct WindowParams {
   const uint64_t* tree;    // [batch, n_queries] or null (cached form)
   int batch, heads, kv_heads, group;  // group = heads / kv_heads
   int n_queries, n_keys, dim;
-  int window;  // >= 1; no limit: 2^30 (positions that matter are < n_keys < 2^30)
+  int window;  // >= 1; no limit: 2^29 (positions that matter are < n_keys < 2^29)
   int sinks;
   float scale;
 };
