@@ -269,8 +269,12 @@ int qk_heads_per_block(const vattn::QkParams& p, double blocks_x, int resident) 
   return best;
 }
 
-// Sizes, angles and the split of the heads over blocks.
-void qk_plan(vattn::QkParams* p, const vattn_qk_args* a, int v, int sms, int64_t* blocks_x) {
+// Sizes, angles and the split of rows over lanes and of heads over blocks.
+// *odd: forward, a row takes as many lanes as it has slots where more rows fit a
+// warp than with a power of two (3, 5, 6, 9, 10 slots; 32 heads x 3000 x 80 f16
+// 13.7 us, else 17.2; 72 f32 14.7 and 15.1).  The gradient has two sums a row, to
+// which the extra shuffles come (32 x 3000 x 80 f32 38.5 us, 34.8).
+void qk_plan(vattn::QkParams* p, const vattn_qk_args* a, int v, int sms, int64_t* blocks_x, bool* odd) {
   p->positions = a->positions;
   p->factors = a->factors;
   p->tokens = a->batch * a->n_patches;
@@ -288,9 +292,10 @@ void qk_plan(vattn::QkParams* p, const vattn_qk_args* a, int v, int sms, int64_t
   p->slots = p->half / v + (rest / 2 + v - 1) / v + (v == 1 ? rest & 1 : 0);
   p->log_lanes = 0;
   while ((1 << p->log_lanes) < p->slots && p->log_lanes < 5) ++p->log_lanes;
-  const int groups = vattn::kQkThreads >> p->log_lanes;
-  *blocks_x = (p->tokens + groups - 1) / groups;
   const bool backward = p->t[0].g != nullptr || p->t[1].g != nullptr;
+  *odd = !backward && v > 1 && 32 / p->slots > 32 >> p->log_lanes;
+  const int groups = *odd ? vattn::kQkThreads / 32 * (32 / p->slots) : vattn::kQkThreads >> p->log_lanes;
+  *blocks_x = (p->tokens + groups - 1) / groups;
   const int resident = vattn::qk_resident(v, backward) * sms;
   const int per = qk_heads_per_block(*p, static_cast<double>(*blocks_x), resident);
   for (int i = 0; i < 2; ++i) {
@@ -306,12 +311,12 @@ void qk_plan(vattn::QkParams* p, const vattn_qk_args* a, int v, int sms, int64_t
   *blocks_x = std::min(*blocks_x, std::max<int64_t>(1, most));
 }
 
-template <typename T, int V, int SL, bool kBackward>
+template <typename T, int V, int SL, bool kBackward, bool kOdd>
 vattn_status qk_go(const vattn::QkParams& p, dim3 grid, int device, cudaStream_t stream) {
   constexpr int kSmem = vattn::QkRing<T, V, SL, kBackward ? 2 : 1>::kSmemBytes;
   void (*kernel)(vattn::QkParams);
   if constexpr (kBackward) kernel = vattn::vattn_qk_norm_rope_backward_kernel<T, V, SL>;
-  else kernel = vattn::vattn_qk_norm_rope_kernel<T, V, SL>;
+  else kernel = vattn::vattn_qk_norm_rope_kernel<T, V, SL, kOdd>;
   static std::atomic<uint8_t> done[vattn::host::kMaxDevices];
   const vattn_status st = allow_smem(kernel, kSmem, done, device);
   if (st != VATTN_OK) return st;
@@ -320,19 +325,23 @@ vattn_status qk_go(const vattn::QkParams& p, dim3 grid, int device, cudaStream_t
 }
 
 template <typename T, bool kBackward>
-vattn_status qk_launch(const vattn::QkParams& p, int v, dim3 grid, int device, cudaStream_t stream) {
-  if constexpr (sizeof(T) == 2)
-    if (v == 8) return qk_go<T, 8, 1, kBackward>(p, grid, device, stream);
-  if (v == 4) return qk_go<T, 4, 1, kBackward>(p, grid, device, stream);
-  return qk_go<T, 1, 2, kBackward>(p, grid, device, stream);
+vattn_status qk_launch(const vattn::QkParams& p, int v, bool odd, dim3 grid, int device, cudaStream_t stream) {
+  if constexpr (sizeof(T) == 2) {
+    if (v == 8 && odd) return qk_go<T, 8, 1, kBackward, !kBackward>(p, grid, device, stream);
+    if (v == 8) return qk_go<T, 8, 1, kBackward, false>(p, grid, device, stream);
+  }
+  if (v == 4 && odd) return qk_go<T, 4, 1, kBackward, !kBackward>(p, grid, device, stream);
+  if (v == 4) return qk_go<T, 4, 1, kBackward, false>(p, grid, device, stream);
+  return qk_go<T, 1, 2, kBackward, false>(p, grid, device, stream);
 }
 
 template <bool kBackward>
-vattn_status qk_dispatch(const vattn::QkParams& p, int32_t dtype, int v, dim3 grid, int device, cudaStream_t stream) {
+vattn_status qk_dispatch(const vattn::QkParams& p, int32_t dtype, int v, bool odd, dim3 grid, int device,
+                         cudaStream_t stream) {
   switch (dtype) {
-    case VATTN_F32: return qk_launch<float, kBackward>(p, v, grid, device, stream);
-    case VATTN_F16: return qk_launch<__half, kBackward>(p, v, grid, device, stream);
-    default: return qk_launch<__nv_bfloat16, kBackward>(p, v, grid, device, stream);
+    case VATTN_F32: return qk_launch<float, kBackward>(p, v, odd, grid, device, stream);
+    case VATTN_F16: return qk_launch<__half, kBackward>(p, v, odd, grid, device, stream);
+    default: return qk_launch<__nv_bfloat16, kBackward>(p, v, odd, grid, device, stream);
   }
 }
 
@@ -732,9 +741,10 @@ vattn_status vattn_qk_norm_rope(const vattn_rows* q, const vattn_rows* k, const 
     qk_strides(t.ys, out[i]);
   }
   int64_t bx = 0;
-  qk_plan(&p, a, v, sms, &bx);
+  bool odd = false;
+  qk_plan(&p, a, v, sms, &bx, &odd);
   const dim3 grid(static_cast<unsigned>(bx), static_cast<unsigned>(p.t[0].slices + p.t[1].slices));
-  return qk_dispatch<false>(p, a->dtype, v, grid, device, static_cast<cudaStream_t>(stream_ptr));
+  return qk_dispatch<false>(p, a->dtype, v, odd, grid, device, static_cast<cudaStream_t>(stream_ptr));
 }
 
 vattn_status vattn_qk_norm_rope_backward(const vattn_rows* dq_out, const vattn_rows* dk_out,
@@ -806,7 +816,8 @@ vattn_status vattn_qk_norm_rope_backward(const vattn_rows* dq_out, const vattn_r
     qk_strides(t.ys, out[i]);
   }
   int64_t bx = 0;
-  qk_plan(&p, a, v, sms, &bx);
+  bool odd = false;
+  qk_plan(&p, a, v, sms, &bx, &odd);
   const int slices = p.t[0].slices + p.t[1].slices;
   const dim3 grid(static_cast<unsigned>(bx), static_cast<unsigned>(slices));
   Workspace ws;
@@ -814,7 +825,7 @@ vattn_status vattn_qk_norm_rope_backward(const vattn_rows* dq_out, const vattn_r
     if ((st = ws.take(static_cast<size_t>(bx) * slices * p.D * 4, device, stream)) != VATTN_OK) return st;
     p.part = reinterpret_cast<float*>(ws.data());
   }
-  if ((st = qk_dispatch<true>(p, a->dtype, v, grid, device, stream)) != VATTN_OK) return st;
+  if ((st = qk_dispatch<true>(p, a->dtype, v, odd, grid, device, stream)) != VATTN_OK) return st;
   if (!p.part) return VATTN_OK;
   vattn::QkWeightSum s{};
   s.part = p.part;

@@ -27,7 +27,9 @@
 // % of the measured copy rate), with two rows a thread in registers 74 us; its
 // gradient at 4 x 20 heads 48.7 us, 5.2 TB/s, weight sums included, from 105
 // us.  The arithmetic, in packed f32 pairs, is about 80 instructions for the
-// 64 bytes of a lane and row.
+// 64 bytes of a lane and row.  16 + 16 heads x 4100 x 72 f32, 32 bytes a lane and
+// row: 14.7 us, 5.1 TB/s, bound by its instructions (2.7 a cycle), with three
+// blocks a multiprocessor and groups of 16 lanes 15.9.
 #pragma once
 
 #include <cstdint>
@@ -66,7 +68,7 @@ struct QkParams {
   int D;
   int half;
   int slots;  // pair slots of a row
-  int log_lanes;
+  int log_lanes;  // lanes of a row, where these are a power of two
   int w_f32;
   float eps;
   double turns[kQkMaxDim / 2];  // turns per position
@@ -199,11 +201,42 @@ __device__ __forceinline__ Vec<T, V> qk_load(const T* row, int i, bool here) {
   return v;
 }
 
-// Sum over the lanes of a group (xor below the group's size stays inside).
-__device__ __forceinline__ float qk_group_sum(float x, int lanes) {
-  for (int o = lanes >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
+// A thread's group (lanes that hold one row) and place in it.  kOdd: a group has
+// as many lanes as the row has slots, 3 to 10; what is left of the warp is group
+// -1 and has no slot.  Else a power of two.
+template <bool kOdd>
+struct QkLane {
+  int lanes, c0, group, groups;  // groups of a block
+  __device__ __forceinline__ explicit QkLane(const QkParams& p) {
+    const int tid = static_cast<int>(threadIdx.x);
+    if constexpr (kOdd) {
+      lanes = p.slots;
+      const int rows = 32 / lanes, row = (tid & 31) / lanes;
+      groups = kQkThreads / 32 * rows;
+      group = row < rows ? (tid >> 5) * rows + row : -1;
+      c0 = row < rows ? (tid & 31) - row * lanes : 32;
+    } else {
+      lanes = 1 << p.log_lanes;
+      groups = kQkThreads >> p.log_lanes;
+      group = tid >> p.log_lanes;
+      c0 = tid & (lanes - 1);
+    }
+  }
+  // Sum over the group.  kOdd: down to its first lane (which adds, in each step,
+  // what its partner had before it) and back; else xor, which stays inside.
+  __device__ __forceinline__ float sum(float x) const {
+    if constexpr (kOdd) {
+      for (int o = lanes > 8 ? 8 : 4; o > 0; o >>= 1) {
+        const float y = __shfl_down_sync(0xffffffffu, x, o);
+        if (c0 + o < lanes) x += y;
+      }
+      return __shfl_sync(0xffffffffu, x, (static_cast<int>(threadIdx.x) & 31) - (c0 & 31));
+    } else {
+      for (int o = lanes >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      return x;
+    }
+  }
+};
 
 // The rows of a group in the order it takes them: tokens first, + stride, ...,
 // for each the heads [h0, h1).  N tensors of one shape are read (x, or x and
@@ -304,30 +337,31 @@ struct QkRing {
 // A block's tensor, heads and tokens.
 struct QkShare {
   int which, h0, h1;
-  long long first, stride;  // of this thread's group
-  __device__ __forceinline__ explicit QkShare(const QkParams& p) {
+  long long block_first, first, stride;  // tokens of the block, of this thread's group (p.tokens: none)
+  template <bool kOdd>
+  __device__ __forceinline__ QkShare(const QkParams& p, const QkLane<kOdd>& lane) {
     which = static_cast<int>(blockIdx.y) < p.t[0].slices ? 0 : 1;
     const int slice = static_cast<int>(blockIdx.y) - (which == 0 ? 0 : p.t[0].slices);
     h0 = slice * p.t[which].heads_per_slice;
     h1 = min(p.t[which].heads, h0 + p.t[which].heads_per_slice);
-    const int groups = kQkThreads >> p.log_lanes;
-    first = static_cast<long long>(blockIdx.x) * groups + (threadIdx.x >> p.log_lanes);
-    stride = static_cast<long long>(gridDim.x) * groups;
+    block_first = static_cast<long long>(blockIdx.x) * lane.groups;
+    first = kOdd && lane.group < 0 ? p.tokens : block_first + lane.group;
+    stride = static_cast<long long>(gridDim.x) * lane.groups;
   }
 };
 
 // SL slots per lane (2 only where V == 1 needs up to 64 slots of a warp).
 // All groups of a block take the same number of tokens: those past the end
 // work on zeros and store nothing.
-template <typename T, int V, int SL>
+template <typename T, int V, int SL, bool kOdd>
 __global__ void __launch_bounds__(kQkThreads, qk_resident(V, false))
     vattn_qk_norm_rope_kernel(const __grid_constant__ QkParams p) {
   extern __shared__ __align__(16) uint8_t qk_smem[];
   __shared__ uint64_t turn[kQkMaxDim / 2];
-  const QkShare sh(p);
+  const QkLane<kOdd> lane(p);
+  const QkShare sh(p, lane);
   const QkTensor& t = p.t[sh.which];
-  const int lanes = 1 << p.log_lanes;
-  const int c0 = static_cast<int>(threadIdx.x) & (lanes - 1);
+  const int lanes = lane.lanes, c0 = lane.c0;
   QkSlot<V> s[SL];
 #pragma unroll
   for (int k = 0; k < SL; ++k) s[k].set(p, c0 + k * lanes);
@@ -337,9 +371,8 @@ __global__ void __launch_bounds__(kQkThreads, qk_resident(V, false))
 #pragma unroll
   for (int k = 0; k < SL; ++k) qk_weight<V>(s[k], t.w, p.w_f32, Elem<T>::kBf16, wa[k], wb[k]);
   const float inv_d = 1.0f / static_cast<float>(p.D);
-  const long long block_first = static_cast<long long>(blockIdx.x) * (kQkThreads >> p.log_lanes);
   long long token = sh.first;
-  for (long long f = block_first; f < p.tokens; f += sh.stride, token += sh.stride) {
+  for (long long f = sh.block_first; f < p.tokens; f += sh.stride, token += sh.stride) {
     const bool valid = token < p.tokens;
     const long long tk = valid ? token : p.tokens - 1;
     const long long b = p.tokens <= 0x7fffffffLL ? static_cast<long long>(p.d_n.div(static_cast<uint32_t>(tk))) : tk / p.n;
@@ -371,7 +404,7 @@ __global__ void __launch_bounds__(kQkThreads, qk_resident(V, false))
         vfma<V>(sq, fa[k], fa[k], sq);
         vfma<V>(sq, fb[k], fb[k], sq);
       }
-      const float r = rsqrtf(fmaf(qk_group_sum(vsum<V>(sq), lanes), inv_d, p.eps));
+      const float r = rsqrtf(fmaf(lane.sum(vsum<V>(sq)), inv_d, p.eps));
       ring.more();
       if (!valid) continue;
 #pragma unroll
@@ -403,10 +436,10 @@ __global__ void __launch_bounds__(kQkThreads, qk_resident(V, true))
   extern __shared__ __align__(16) uint8_t qk_smem[];
   __shared__ uint64_t turn[kQkMaxDim / 2];
   __shared__ float red[kQkThreads / 32][kQkMaxDim];
-  const QkShare sh(p);
+  const QkLane<false> lane(p);
+  const QkShare sh(p, lane);
   const QkTensor& t = p.t[sh.which];
-  const int lanes = 1 << p.log_lanes;
-  const int c0 = static_cast<int>(threadIdx.x) & (lanes - 1);
+  const int lanes = lane.lanes, c0 = lane.c0;
   const float inv_d = 1.0f / static_cast<float>(p.D);
   QkSlot<V> s[SL];
 #pragma unroll
@@ -420,9 +453,8 @@ __global__ void __launch_bounds__(kQkThreads, qk_resident(V, true))
 #pragma unroll
     for (int e = 0; e < V; ++e) da[k][e] = db[k][e] = 0.0f;
   }
-  const long long block_first = static_cast<long long>(blockIdx.x) * (kQkThreads >> p.log_lanes);
   long long token = sh.first;
-  for (long long f = block_first; f < p.tokens; f += sh.stride, token += sh.stride) {
+  for (long long f = sh.block_first; f < p.tokens; f += sh.stride, token += sh.stride) {
     const bool valid = token < p.tokens;
     const long long tk = valid ? token : p.tokens - 1;
     const long long b = p.tokens <= 0x7fffffffLL ? static_cast<long long>(p.d_n.div(static_cast<uint32_t>(tk))) : tk / p.n;
@@ -458,7 +490,7 @@ __global__ void __launch_bounds__(kQkThreads, qk_resident(V, true))
         vmul<V>(tmp, gb[k], wb[k]);
         vfma<V>(dt, tmp, xb[k], dt);
       }
-      const float sum = qk_group_sum(vsum<V>(sq), lanes), dot = qk_group_sum(vsum<V>(dt), lanes);
+      const float sum = lane.sum(vsum<V>(sq)), dot = lane.sum(vsum<V>(dt));
       ring.more();
       if (!valid) continue;
       const float r = rsqrtf(fmaf(sum, inv_d, p.eps));
