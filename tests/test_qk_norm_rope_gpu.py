@@ -77,6 +77,21 @@ def test_forward(td, i):
         assert_within(y, want, bound, what, HALF_STEP[name], TINY[name])
 
 
+@pytest.mark.parametrize("name,D", [("f16", 24), ("bf16", 48), ("f32", 24), ("f32", 40), ("f16", 80), ("f32", 48),
+                                    ("bf16", 96), ("f32", 72), ("f16", 72), ("f32", 80), ("f32", 56)])
+def test_lanes_without_a_power_of_two(td, name, D):
+    """Rows of 3, 5, 6, 9, 10 and (no gain, padded to 8) 7 vectors, several in
+    a warp: against the oracle, and in place."""
+    case = (name, (2, 5, 3, 70, D), D, "packed", "f32", "random")
+    q, k, w, pos, factors, how = build(td, case, 500 + D)
+    got = vef.qk_norm_rope(q, k, w[0], w[1], **how)
+    for x, weight, y, what in ((q, w[0], got[0], "q"), (k, w[1], got[1], "k")):
+        want, bound = od.qk_norm_rope(f64(x), f64(weight), pos, D, how["base"], factors, float(np.float32(how["eps"])))
+        assert_within(y, want, bound, what, HALF_STEP[name], TINY[name])
+    vef.qk_norm_rope(q, k, w[0], w[1], q_out=q, k_out=k, **how)
+    assert td[0].equal(q, got[0]) and td[0].equal(k, got[1])
+
+
 @pytest.mark.parametrize("i", range(len(CASES)))
 def test_backward(td, i):
     torch, dev = td
