@@ -78,6 +78,20 @@ def test_against_the_oracle(td, i):
     assert torch.equal(out, vef.forward_cached(*x, **how))
 
 
+@pytest.mark.parametrize("D", [8, 24, 32, 40, 64, 72, 120, 128])
+@pytest.mark.parametrize("H,T", [(1, 1), (4, 4), (5, 5), (8, 4), (11, 3), (7, 11)])
+def test_rows_and_widths(td, H, T, D):
+    """Rows for one, two and four groups of warps, of every width of a shared
+    row, in two layouts, one a tree under a window."""
+    for i, (window, tree, layout) in enumerate(((None, False, "packed"), (50, True, "padded"))):
+        case = ("f16" if i else "bf16", (2, 2 * H, 2, T, 333, D), [333, 70], window, 2 * i, tree, layout)
+        x, seen, how = build(td, case, 700 + D + H)
+        out = vef.forward_cached(*x, **how)
+        want, _, _, bound, _, _ = od.attention(*(f64(t) for t in x[:3]), seen, float(np.float32(how["scale"])),
+                                               HALF_STEP[case[0]])
+        assert_within(out, want, bound, "out", tiny=2 * TINY[case[0]])
+
+
 def test_words_without_bits_and_stray_bits(td):
     torch, dev = td
     q, k, v = (normal(torch, s, "bf16", 5 + i, dev) for i, s in enumerate(((1, 2, 4, 32), (1, 1, 50, 32), (1, 1, 50, 32))))

@@ -13,6 +13,10 @@
 //   more:       four groups of two, 32 keys each (a tree of 31 tokens, 4 heads
 //               a key head, over 4096 keys: see cached_launch)
 //
+// Rows of 32, 64 or 128 dims in shared memory and registers, zeros behind
+// head_dim: loops without a bound in them are 5 to 20 % faster (32 x 8 key heads x
+// 8000 keys: 72 dims 78.6 us, else 92.8; 80 dims in a tree 30.9, else 29.6).
+//
 // The keys that any row sees are numbered through: first the first keys that
 // lie before the lowest window, then those from that window to the end.  The
 // shares of the blocks are equal parts of that list, cut on the device from
@@ -21,11 +25,11 @@
 // them merge a part of the rows from there, in the order of the shares.  More
 // shares go through a workspace and vattn_cached_join_kernel, likewise in order.
 //
-// 32 sequences x 8 key heads x up to 16385 keys of 128 bf16: 205.7 us, 7.0 TB/s
-// (the measured copy rate is 6.8; 216.9 us while every row's address was formed
-// by itself and O rescaled in every tile).  A tree of 31 tokens over 4 x 4 heads x 4100
-// keys of 64 f16: 21 us, bound by latency: about 420 instructions a warp and
-// tile, seven tiles a block, the rest its start and the join.
+// 32 sequences x 8 key heads x up to 16385 keys of 128 bf16: 201 us, 7.2 TB/s
+// (the measured copy rate is 6.8; 217 us while every row's address was formed by
+// itself, O rescaled in every tile, and the loops bounded by head_dim).  A tree of 31 tokens over 4 x 4 heads x 4100
+// keys of 64 f16: 19.4 us, bound by latency: seven tiles a block of about 1.2 us,
+// 2.3 us before the first, the rest the joins.
 //
 // Weights are rounded to the tensors' type for the second product, as in
 // window_fwd_kernel.cuh; everything else is f32.  Rows differ in what they
@@ -110,6 +114,13 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4
                : "r"(addr)
                : "memory");
 }
+// Place of 16-byte chunk c in shared row r of CH chunks: eight consecutive
+// rows have it in eight different banks' groups.
+template <int CH>
+__device__ __forceinline__ int swizzled(int r, int c) {
+  return CH >= 8 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
+}
+
 template <int DP, int RW>
 struct CachedPlan {
   static constexpr int kWarps = RW == 1 || (RW == 2 && DP == 128) ? 4 : 8;
@@ -121,7 +132,7 @@ struct CachedPlan {
   static constexpr int kOffP = kCachedStages * kStageBytes;  // weights of the loops' path, per warp
   static constexpr int kSmemBytes = kOffP + kWarps * 16 * kWarpKeys * 4;
   // blocks a multiprocessor, by shared memory (4 warps) or registers (8)
-  static constexpr int kResident = (kWarps == 4 ? 4 : 2) / (DP == 64 ? 1 : 2);
+  static constexpr int kResident = (kWarps == 4 ? 4 : 2) / (DP <= 64 ? 1 : 2);
   static_assert(kWarps * 16 * (DP + 2) * 4 <= kOffP, "the warps' results reuse the ring");
 };
 
@@ -156,12 +167,12 @@ __global__ void __launch_bounds__(CachedPlan<DP, RW>::kThreads)
     const T* vbase = rows_at<T>(p.v, b, kh, 0);
     const int ch = tid % CH, tiles = (max(v1 - v0, 0) + kCachedKeys - 1) / kCachedKeys;
     auto load = [&](int tile) {
-      if (tile < tiles && ch * 8 < ((D + 15) & ~15)) {
+      if (tile < tiles) {
         constexpr int kStep = kThreads / CH;  // rows; a multiple of 8, so a thread's swizzle is one
         static_assert(kStep % 8 == 0, "rows of a thread");
         const int r0 = tid / CH, i0 = v0 + tile * kCachedKeys;
         const uint32_t at = smem_s + static_cast<uint32_t>(tile % kCachedStages) * P::kStageBytes +
-                            static_cast<uint32_t>(r0 * DP * 2 + ((ch ^ (r0 & 7)) << 4));
+                            static_cast<uint32_t>(r0 * DP * 2 + (swizzled<CH>(r0, ch) << 4));
         if (i0 >= sp.sinks && i0 + kCachedKeys <= v1) {  // rows that follow each other
           const bool on = ch * 8 < D;
           const long long j = sp.key(i0) + r0;
@@ -236,14 +247,13 @@ __global__ void __launch_bounds__(CachedPlan<DP, RW>::kThreads)
         for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
 #pragma unroll
       for (int ks = 0; ks < DP / 16; ++ks) {
-        if (ks * 16 >= D) break;
 #pragma unroll
         for (int n = 0; n < KN; n += 2) {
           // rows: 16 keys; matrices (keys 0-7, dims 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15)
           const int r = key0 + n * 8 + (lane & 7) + ((lane >> 4) & 1) * 8;
           const int c = ks * 2 + ((lane >> 3) & 1);
           uint32_t kf[4];
-          ldmatrix_x4(ks_s + static_cast<uint32_t>(r * DP * 2 + ((c ^ (r & 7)) << 4)), kf);
+          ldmatrix_x4(ks_s + static_cast<uint32_t>(r * DP * 2 + (swizzled<CH>(r, c) << 4)), kf);
           mma_16816<T>(s[n], qf[ks], kf[0], kf[1]);
           mma_16816<T>(s[n + 1], qf[ks], kf[2], kf[3]);
         }
@@ -314,7 +324,7 @@ __global__ void __launch_bounds__(CachedPlan<DP, RW>::kThreads)
         for (int x = lane; x < P::kWarpKeys * CH; x += 32) {
           const int r = key0 + x / CH, c = x % CH;
           if (c * 8 >= D) continue;
-          const float4 y = ptx::ld_shared_v4(vs_s + static_cast<uint32_t>(r * DP * 2 + ((c ^ (r & 7)) << 4)));
+          const float4 y = ptx::ld_shared_v4(vs_s + static_cast<uint32_t>(r * DP * 2 + (swizzled<CH>(r, c) << 4)));
           const uint32_t z[4] = {__float_as_uint(y.x), __float_as_uint(y.y), __float_as_uint(y.z), __float_as_uint(y.w)};
 #pragma unroll
           for (int f = 0; f < 4; ++f)
@@ -331,10 +341,9 @@ __global__ void __launch_bounds__(CachedPlan<DP, RW>::kThreads)
           const int r = key0 + kk * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
           for (int n = 0; n < DP / 8; n += 2) {
-            if (n * 8 >= D) break;
             const int c = n + (lane >> 4);
             uint32_t vf[4];
-            ldmatrix_x4_trans(vs_s + static_cast<uint32_t>(r * DP * 2 + ((c ^ (r & 7)) << 4)), vf);
+            ldmatrix_x4_trans(vs_s + static_cast<uint32_t>(r * DP * 2 + (swizzled<CH>(r, c) << 4)), vf);
             mma_16816<T>(o[n], pf, vf[0], vf[1]);
             mma_16816<T>(o[n + 1], pf, vf[2], vf[3]);
           }
@@ -362,7 +371,7 @@ __global__ void __launch_bounds__(CachedPlan<DP, RW>::kThreads)
 #pragma unroll
           for (int n = 0; n < DP / 8; ++n) {
             if (n * 8 >= D) break;
-            const T* vv = reinterpret_cast<const T*>(smem + (vs_s - smem_s) + r * DP * 2 + ((n ^ (r & 7)) << 4)) + (lane & 3) * 2;
+            const T* vv = reinterpret_cast<const T*>(smem + (vs_s - smem_s) + r * DP * 2 + (swizzled<CH>(r, n) << 4)) + (lane & 3) * 2;
             const float va = Elem<T>::widen(vv[0]), vb = Elem<T>::widen(vv[1]);
             if (!(pa < 0.0f)) {
               o[n][0] = fmaf(pa, va, o[n][0]);

@@ -688,6 +688,10 @@ vattn_status cached_launch(vattn::CachedParams p, int sms, int device, cudaStrea
 template <typename T>
 vattn_status cached_dispatch(const vattn::CachedParams& p, int sms, int device, cudaStream_t stream) {
   const int rw = p.rows <= 16 ? 1 : (p.rows <= 32 ? 2 : 4);
+  if (p.w.dim <= 32)
+    return rw == 1   ? cached_launch<T, 32, 1>(p, sms, device, stream)
+           : rw == 2 ? cached_launch<T, 32, 2>(p, sms, device, stream)
+                     : cached_launch<T, 32, 4>(p, sms, device, stream);
   if (p.w.dim <= 64)
     return rw == 1   ? cached_launch<T, 64, 1>(p, sms, device, stream)
            : rw == 2 ? cached_launch<T, 64, 2>(p, sms, device, stream)
