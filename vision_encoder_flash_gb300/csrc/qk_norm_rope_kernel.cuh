@@ -23,10 +23,10 @@
 // stay in registers meanwhile.  Each row is read once and written once.  What
 // bounds it is bytes in flight: each thread keeps its next rows coming
 // through a ring of its own in shared memory (cp.async; no barrier, a thread
-// reads what it asked for).  4 x 40 heads x 4096 x 128 bf16: 52.7 us, 6.4 TB/s (94
+// reads what it asked for).  4 x 40 heads x 4096 x 128 bf16: 52.3 us, 6.4 TB/s (94
 // % of the measured copy rate), with two rows a thread in registers 74 us; its
-// gradient at 4 x 20 heads 48.7 us, 5.2 TB/s, weight sums included, from 105
-// us.  The arithmetic, in packed f32 pairs, is about 80 instructions for the
+// gradient at 4 x 20 heads 46.0 us, 5.5 TB/s, weight sums included, from 105
+// us (48.3 with its two sums one after the other).  The arithmetic, in packed f32 pairs, is about 80 instructions for the
 // 64 bytes of a lane and row.  16 + 16 heads x 4100 x 72 f32, 32 bytes a lane and
 // row: 14.7 us, 5.1 TB/s, bound by its instructions (2.7 a cycle), with three
 // blocks a multiprocessor and groups of 16 lanes 15.9.
@@ -232,8 +232,21 @@ struct QkLane {
       }
       return __shfl_sync(0xffffffffu, x, (static_cast<int>(threadIdx.x) & 31) - (c0 & 31));
     } else {
-      for (int o = lanes >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+        if (o < lanes) x += __shfl_xor_sync(0xffffffffu, x, o);
       return x;
+    }
+  }
+  // Two sums at once (a power of two of lanes).
+  __device__ __forceinline__ void sum2(float& x, float& y) const {
+    static_assert(!kOdd, "a power of two");
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      if (o >= lanes) continue;
+      const float a = __shfl_xor_sync(0xffffffffu, x, o), b = __shfl_xor_sync(0xffffffffu, y, o);
+      x += a;
+      y += b;
     }
   }
 };
@@ -490,33 +503,29 @@ __global__ void __launch_bounds__(kQkThreads, qk_resident(V, true))
         vmul<V>(tmp, gb[k], wb[k]);
         vfma<V>(dt, tmp, xb[k], dt);
       }
-      const float sum = lane.sum(vsum<V>(sq)), dot = lane.sum(vsum<V>(dt));
+      float sum = vsum<V>(sq), dot = vsum<V>(dt);
+      lane.sum2(sum, dot);
       ring.more();
       if (!valid) continue;
       const float r = rsqrtf(fmaf(sum, inv_d, p.eps));
-      const float back = -dot * inv_d * r * r;  // times x r: the norm's own share
-      float rr[V], kk[V];
+      const float back = -dot * inv_d * r * r * r;  // times x: the norm's own share
+      float kk[V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        rr[e] = r;
-        kk[e] = back;
-      }
+      for (int e = 0; e < V; ++e) kk[e] = back;
 #pragma unroll
       for (int k = 0; k < SL; ++k) {
-        // x r, dw += g' (x r), dx = r (g' w) + (x r) back
+        // u = g' r, dw += u x, dx = u w + x back
         float tmp[V];
         Vec<T, V> oa, ob;
-        vmul<V>(xa[k], xa[k], rr);
-        vmul<V>(xb[k], xb[k], rr);
+        vscale<V>(ga[k], ga[k], r);
+        vscale<V>(gb[k], gb[k], r);
         vfma<V>(da[k], ga[k], xa[k], da[k]);
         vfma<V>(db[k], gb[k], xb[k], db[k]);
         vmul<V>(tmp, ga[k], wa[k]);
-        vmul<V>(xa[k], xa[k], kk);
-        vfma<V>(tmp, tmp, rr, xa[k]);
+        vfma<V>(tmp, xa[k], kk, tmp);
         oa.narrow(tmp);
         vmul<V>(tmp, gb[k], wb[k]);
-        vmul<V>(xb[k], xb[k], kk);
-        vfma<V>(tmp, tmp, rr, xb[k]);
+        vfma<V>(tmp, xb[k], kk, tmp);
         ob.narrow(tmp);
         if (s[k].here) *reinterpret_cast<Vec<T, V>*>(row + s[k].ia) = oa;
         if (s[k].pair) *reinterpret_cast<Vec<T, V>*>(row + s[k].ib) = ob;
