@@ -92,6 +92,35 @@ def test_rows_and_widths(td, H, T, D):
         assert_within(out, want, bound, "out", tiny=2 * TINY[case[0]])
 
 
+@pytest.mark.parametrize("N", [150, 260, 390, 510])
+def test_few_shares(td, N):
+    """Two to four shares of the keys, some of them without a key in short
+    sequences: against the oracle, on three streams at once, and replayed with
+    other lengths."""
+    torch, dev = td
+    case = ("f16", (5, 8, 2, 3, N, 72), [N, 129, 40, 3, 0], None, 2, True, "plain")
+    x, seen, how = build(td, case, 900 + N)
+    out = vef.forward_cached(*x, **how)
+    want, _, _, bound, _, _ = od.attention(*(f64(t) for t in x[:3]), seen, float(np.float32(how["scale"])), HALF_STEP["f16"])
+    assert_within(out, want, bound, "out", tiny=2 * TINY["f16"])
+    streams = [torch.cuda.Stream(dev) for _ in range(3)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream(dev))
+    got = [vef.forward_cached(*x, stream=s, **how) for s in streams]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize(dev)
+    assert all(torch.equal(t, out) for t in got)
+    with torch.cuda.graph(graph):
+        again = vef.forward_cached(*x, **how)
+    for t in x[1:3]:
+        t.copy_(normal(torch, t.shape, "f16", 950, dev))
+    x[3].copy_(torch.tensor([0, N, 3, 131, 64], dtype=torch.int32))
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize(dev)
+    assert torch.equal(again, vef.forward_cached(*x, **how))
+
+
 def test_words_without_bits_and_stray_bits(td):
     torch, dev = td
     q, k, v = (normal(torch, s, "bf16", 5 + i, dev) for i, s in enumerate(((1, 2, 4, 32), (1, 1, 50, 32), (1, 1, 50, 32))))
