@@ -20,7 +20,7 @@ constexpr uint64_t kPipeTimeoutNs = 2000000000ull;
 // Wait sites in the low byte of the status word (attn_kernel.cuh has 1..18).
 enum PipeSite : uint32_t {
   kSiteWinKv = 32, kSiteWinQ = 33, kSiteWinMma = 34, kSiteWinSoft = 35, kSiteWinOut = 36,
-  kSiteWinDrain = 37,
+  kSiteWinDrain = 37, kSiteWinClean = 38,
   kSiteGradLoad = 40, kSiteGradMma = 41, kSiteGradSoft = 42, kSiteGradOut = 43, kSiteGradDrain = 44,
   kSiteGradNext = 45,
 };
