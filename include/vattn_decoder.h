@@ -140,8 +140,9 @@ vattn_status vattn_forward_window(const vattn_rows* q, const vattn_rows* k, cons
  * every time (no atomics).  k, v behind kv_len and q, dout of rows that see
  * nothing may hold anything; a NaN or infinity elsewhere may reach the
  * gradients of rows within 128 of its own.  The softmax weights p and the
- * score gradients p (dp - delta) are rounded to the tensors' type on the way
- * (f16: the latter within +-65504).
+ * score gradients p (dp - delta) are rounded to the tensors' type on the way,
+ * in f16 times powers of two: neither overflows, and terms keep their digits
+ * down to 2^-29 of the largest that 128 rows or keys can give.
  * dq as q, dk as k, dv as v; dout as out.
  */
 vattn_status vattn_backward_window(const vattn_rows* dout, const vattn_rows* q, const vattn_rows* k,

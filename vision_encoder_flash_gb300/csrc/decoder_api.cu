@@ -585,13 +585,19 @@ vattn_status backward_window(const Tensor& tg, const Tensor& tq, const Tensor& t
   const size_t stat_bytes = static_cast<size_t>(p.w.batch) * p.w.heads * p.stat_tiles * vattn::kGradStat * 4;
   const size_t part_bytes = static_cast<size_t>(slots) * 2 * kTile * p.w.dim * 4;
   Workspace ws;
-  if ((st = ws.take(256 + stat_bytes + part_bytes, device, stream)) != VATTN_OK) return st;
+  // f16: the largest values of every 64 rows too, of V by blocks of their own
+  const long long v_halves = dtype == VATTN_F16 ? 2 * seqs * p.key_tiles : 0;
+  if (bhs * p.stat_tiles + v_halves > kMaxRows) return fail(VATTN_ERR_UNSUPPORTED, "too many tiles of 128 rows");
+  const size_t peak_bytes = dtype == VATTN_F16 ? (static_cast<size_t>(bhs) * p.stat_tiles * 8 + v_halves * 4 + 255) / 256 * 256 : 0;
+  if ((st = ws.take(256 + stat_bytes + peak_bytes + part_bytes, device, stream)) != VATTN_OK) return st;
   p.next = reinterpret_cast<uint32_t*>(ws.data());
   p.stat = reinterpret_cast<float*>(ws.data() + 256);
-  p.part = reinterpret_cast<float*>(ws.data() + 256 + stat_bytes);
+  p.peak = reinterpret_cast<float2*>(ws.data() + 256 + stat_bytes);
+  p.v_peak = reinterpret_cast<float*>(p.peak + bhs * p.stat_tiles);
+  p.part = reinterpret_cast<float*>(ws.data() + 256 + stat_bytes + peak_bytes);
   {
-    // (one block for the counter alone where there are no queries)
-    const unsigned grid = static_cast<unsigned>(std::max(1LL, bhs * p.stat_tiles));
+    // (one block for the counter alone where there are neither queries nor V's)
+    const unsigned grid = static_cast<unsigned>(std::max(1LL, bhs * p.stat_tiles + v_halves));
     if (p.w.dim <= 64) vattn::vattn_window_stat_kernel<T, 8><<<grid, 256, 0, stream>>>(p);
     else vattn::vattn_window_stat_kernel<T, 16><<<grid, 256, 0, stream>>>(p);
     if ((st = launched("gradient statistics kernel launch")) != VATTN_OK) return st;

@@ -28,7 +28,7 @@
 //   warp 2   issues the second products once P and D are there; an issuing
 //            thread is held while its products run, so with two of them the
 //            next tile's G and S run between
-//   warp 3   takes the next X tile and tells the others
+//   warp 3   takes the next X tile and tells the others, and the power of its D
 //   warps 4-7, 8-11   P and D of columns 0..63, 64..127 of every tile, then
 //            the X tile's results
 // G is overwritten as soon as it is in registers, S once its P and D have
@@ -42,11 +42,21 @@
 // tiles of the first keys, the walk is long.
 //
 // Rounding: P and D go to the tensors' type for the second products, as these
-// need (relative 2^-9 / 2^-12 at most of each term; with f16 a D beyond 65504
-// is infinite, as dq, dk and dv of that size would be), and delta comes from
-// `out` as rounded; all sums, lse and delta are f32.  For long rows that stays
-// below the rounding of the results; for rows of a few keys dq and dk are off by
-// up to twice as much as their own rounding.
+// need (relative 2^-9 / 2^-12 at most of each term), and delta comes from `out` as
+// rounded; all sums, lse and delta are f32.  For long rows that stays below the
+// rounding of the results; for rows of a few keys dq and dk are off by up to twice
+// as much as their own rounding.
+//
+// f16 keeps that relative error down to 2^-14 only, which a weight p of a long row
+// and a D of an ordinary gradient (dout of 1e-3 over 4096 keys) are below, and ends
+// at 65504.  So P is held as 2^15 p <= 2^15, and D as 2^e D with the power e of the
+// walk that takes the largest value it can have, |dout_i| |v_j| + |delta_i| over
+// the rows and keys of the walk, to 2^14 .. 2^15: no D overflows, and terms keep
+// their digits down to 2^-29 of the largest.  The results are divided by 2^15 and
+// 2^e in f32.  The statistics kernel leaves the largest |dout|^2, |delta| and |v|^2 of
+// every 64 rows, and warp 3 looks up those of an X tile's walk while the tile
+// before is worked on.  (2 x 16(4) x 4096 x 64, window 1024: 153 us, bf16, which
+// needs none of it, 140.)
 //
 // What bounds it: for a tile of 128 x 128 pairs the products take 2080 cycles at
 // head_dim 128 (keys; queries 1560) and half of that at 64, the arithmetic on
@@ -63,12 +73,15 @@ namespace vattn {
 constexpr int kGradCols = 64;                // columns of a math warpgroup, rows of half a Y tile
 constexpr int kGradBlock = kGradCols * 128;  // 64 rows x 64 elements, 128-byte swizzle
 constexpr int kGradStat = 2 * kGradCols;     // floats of half a tile's -lse2, -delta
+constexpr int kGradPBits = 15;               // f16: P is held as 2^15 p
 
 struct WindowGradParams {
   WindowParams w;
   RowsTensor q, k, v, out, dout, dq, dk, dv;
   const float* lse;
-  float* stat;     // [batch * heads][stat_tiles][-lse2 x 64 | -delta x 64]
+  float* stat;     // [batch * heads][stat_tiles][-lse2 x 64 | -delta x 64] (f16: -lse2 + 15)
+  float2* peak;    // f16: [batch * heads][stat_tiles] largest |dout|^2 and |delta| of the 64 rows
+  float* v_peak;   // f16: [batch * kv_heads][2 key_tiles] largest |v|^2 of the 64 rows
   float* part;     // [slot][dv, dk][128][dim] partial sums of the chunks
   uint32_t* next;  // X tiles taken from the counter so far; zeroed by the statistics kernel
   uint32_t* status;
@@ -85,17 +98,68 @@ struct WindowGradParams {
 // -lse2 = -lse log2(e) and -delta of every query row; rows that see nothing
 // (and those that fill the last tile) get -infinity and 0, hence weights 0.
 // A block has half a tile, 64 rows; LR lanes, 16 bytes each, hold one row, and
-// the loads of a lane's LR / 4 rows are all in flight before the sums.
+// the loads of a lane's LR / 4 rows are all in flight before the sums.  f16: the
+// blocks behind those have 64 rows of V each, of which they leave the largest
+// square.  A row that is not finite counts as 0 there.
 template <typename T, int LR>
 __global__ void __launch_bounds__(256) vattn_window_stat_kernel(const __grid_constant__ WindowGradParams p) {
   constexpr int R = kGradCols * LR / 256;
   ptx::grid_dep_launch();  // the gradient kernel sets itself up meanwhile, and waits for this one's end
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.next = 0;
-  if (p.stat_tiles == 0) return;
+  constexpr bool kPowers = !Elem<T>::kBf16;
+  __shared__ float2 peak_s[8];
+  const int lane = threadIdx.x % LR, c = lane * 8;
+  auto leave = [&](float2 top, float2* to_pair, float* to_one) {  // the block's largest
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      top.x = fmaxf(top.x, __shfl_xor_sync(0xffffffffu, top.x, o));
+      top.y = fmaxf(top.y, __shfl_xor_sync(0xffffffffu, top.y, o));
+    }
+    if (threadIdx.x % 32 == 0) peak_s[threadIdx.x / 32] = top;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+#pragma unroll
+    for (int w = 1; w < 8; ++w) top = make_float2(fmaxf(top.x, peak_s[w].x), fmaxf(top.y, peak_s[w].y));
+    if (to_pair != nullptr) *to_pair = top;
+    else *to_one = top.x;
+  };
+  auto finite = [](float x) { return x - x == 0.0f ? x : 0.0f; };
+  const long long stat_blocks = static_cast<long long>(p.w.batch) * p.w.heads * p.stat_tiles;
+  if (blockIdx.x >= stat_blocks) {
+    if (!kPowers) return;
+    const long long at = blockIdx.x - stat_blocks;
+    if (at >= static_cast<long long>(p.w.batch) * p.w.kv_heads * 2 * p.key_tiles) return;
+    const int half = static_cast<int>(at % (2 * p.key_tiles));
+    const uint32_t bk = static_cast<uint32_t>(at / (2 * p.key_tiles));
+    uint32_t kh;
+    const int b = static_cast<int>(p.d_kv_heads.div(bk, &kh));
+    const Seq s = window_seq(p.w, b);
+    Vec<T, 8> x[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const int j = half * kGradCols + threadIdx.x / LR + k * (256 / LR);
+      const bool on = j < s.len && c < p.w.dim;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[k].e[e] = Elem<T>::narrow(0.0f);
+      if (on) x[k] = *reinterpret_cast<const Vec<T, 8>*>(rows_at<T>(p.v, b, kh, j) + c);
+    }
+    float top = 0.0f;
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      float f[8], sum = 0.0f;
+      x[k].widen(f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = fmaf(f[e], f[e], sum);
+#pragma unroll
+      for (int o = LR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      top = fmaxf(top, finite(sum));
+    }
+    leave(make_float2(top, 0.0f), nullptr, p.v_peak + at);
+    return;
+  }
   uint32_t tile, h;
   const uint32_t bh = p.d_stat_tiles.div(blockIdx.x, &tile);
   const int b = static_cast<int>(p.d_heads.div(bh, &h));
-  const int lane = threadIdx.x % LR, c = lane * 8;
   const Seq s = window_seq(p.w, b);
   Vec<T, 8> x[R], y[R];
   bool on[R];
@@ -109,26 +173,35 @@ __global__ void __launch_bounds__(256) vattn_window_stat_kernel(const __grid_con
       y[k] = *reinterpret_cast<const Vec<T, 8>*>(rows_at<T>(p.out, b, h, i) + c);
     }
   }
+  float2 top = make_float2(0.0f, 0.0f);
 #pragma unroll
   for (int k = 0; k < R; ++k) {
-    float sum = 0.0f;
+    float sum = 0.0f, square = 0.0f;
     if (on[k] && c < p.w.dim) {
       float fx[8], fy[8];
       x[k].widen(fx);
       y[k].widen(fy);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum = fmaf(fx[e], fy[e], sum);
+      for (int e = 0; e < 8; ++e) {
+        sum = fmaf(fx[e], fy[e], sum);
+        if (kPowers) square = fmaf(fx[e], fx[e], square);
+      }
     }
 #pragma unroll
-    for (int o = LR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = LR / 2; o > 0; o >>= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (kPowers) square += __shfl_xor_sync(0xffffffffu, square, o);
+    }
+    top = make_float2(fmaxf(top.x, finite(square)), fmaxf(top.y, finite(fabsf(sum))));
     if (lane != 0) continue;
     const int r = threadIdx.x / LR + k * (256 / LR), i = static_cast<int>(tile) * kGradCols + r;
     const float lse = on[k] ? p.lse[static_cast<long long>(bh) * p.w.n_queries + i] : -INFINITY;
     const bool empty = lse == -INFINITY;
     float* to = p.stat + static_cast<long long>(blockIdx.x) * kGradStat + r;
-    to[0] = empty ? -INFINITY : -lse * kLog2E;
+    to[0] = empty ? -INFINITY : fmaf(-lse, kLog2E, kPowers ? static_cast<float>(kGradPBits) : 0.0f);
     to[kGradCols] = empty ? 0.0f : -sum;
   }
+  if (kPowers) leave(top, p.peak + blockIdx.x, nullptr);
 }
 
 template <int NKB>
@@ -157,7 +230,7 @@ struct GradPlan {
 
 enum GradBar : int {
   kGbXFull = 0, kGbXEmpty = 1, kGbYFull = 2, kGbYEmpty = 10, kGbSFull = 18, kGbGFree = 19, kGbPFull = 20,
-  kGbPFree = 22, kGbSum = 24, kGbSumFree = 25, kGbNext = 27, kGbTaken = 29, kGbDone = 31, kGbCount = 32,
+  kGbPFree = 22, kGbSum = 24, kGbSumFree = 25, kGbNext = 27, kGbTaken = 29, kGbDone = 31, kGbPower = 32, kGbCount = 36,
 };
 // A wait names a phase by its parity, so whoever waits on a barrier has seen
 // the phase before the one it waits for.  The score issuer does not look at
@@ -258,6 +331,36 @@ __device__ __forceinline__ GradWalk<false> grad_walk<false>(const WindowGradPara
     k.n = k.ns + hi / kTile - k.first + 1;
   }
   return k;
+}
+
+// f16: 2^(e - 15) of the walk's D (a whole warp): e takes the bound |dout| |v| +
+// |delta| over the walk's rows and keys to 2^14 .. 2^15.
+template <bool kKeys>
+__device__ __forceinline__ float grad_power(const WindowGradParams& p, const GradWalk<kKeys>& wk, int lane) {
+  float2 g = make_float2(0.0f, 0.0f);
+  float v = 0.0f;
+  auto rows = [&](long long bh, int half) {
+    const float2 x = p.peak[bh * p.stat_tiles + half];
+    g = make_float2(fmaxf(g.x, x.x), fmaxf(g.y, x.y));
+  };
+  auto keys = [&](long long bk, int half) { v = fmaxf(v, p.v_peak[bk * 2 * p.key_tiles + half]); };
+  if constexpr (kKeys) {
+    const long long bk = static_cast<long long>(wk.b) * p.w.kv_heads + wk.h;
+    for (int i = lane; i < 2 * wk.n; i += 32) {
+      const GradItem<true> it(wk, i >> 1);
+      rows(bk * p.w.group + it.g, 2 * it.tile + (i & 1));
+    }
+    if (lane < 2) keys(bk, wk.row0 / kGradCols + lane);
+  } else {
+    const long long bh = static_cast<long long>(wk.b) * p.w.heads + wk.h;
+    for (int i = lane; i < 2 * wk.n; i += 32)
+      keys(static_cast<long long>(wk.b) * p.w.kv_heads + wk.h / p.w.group, 2 * GradItem<false>(wk, i >> 1).tile + (i & 1));
+    if (lane < 2) rows(bh, wk.row0 / kGradCols + lane);
+  }
+  const float most = sqrtf(warp_max(g.x)) * sqrtf(warp_max(v)) + warp_max(g.y);
+  int k = 0;
+  if (most > 0.0f) (void)frexpf(most, &k);  // most < 2^k
+  return __int_as_float((127 + min(max(-k, -60), 60)) << 23);
 }
 
 // The block's roles, one X tile at a time; `at` counts the Y tiles of the
@@ -435,7 +538,8 @@ __device__ __forceinline__ bool grad_sums(const GradCtx& x, int block, uint32_t&
 
 // P and D of 64 columns of every tile, then the X tile's results (one warpgroup).
 template <typename T, int NKB, bool kKeys>
-__device__ __forceinline__ bool grad_math(const GradCtx& x, int block, uint32_t& at, uint32_t& tiles) {
+__device__ __forceinline__ bool grad_math(const GradCtx& x, int block, uint32_t& at, uint32_t& tiles, float power) {
+  constexpr bool kPowers = !Elem<T>::kBf16;
   using P = GradPlan<NKB>;
   const WindowGradParams& p = x.p;
   const GradWalk<kKeys> wk = grad_walk<kKeys>(p, block);
@@ -449,8 +553,9 @@ __device__ __forceinline__ bool grad_math(const GradCtx& x, int block, uint32_t&
     const float* st = p.stat + ((static_cast<long long>(wk.b) * p.w.heads + wk.h) * p.stat_tiles + row / kGradCols) *
                                    kGradStat + row % kGradCols;
     row_lse = st[0];
-    row_delta = st[kGradCols];
+    row_delta = kPowers ? st[kGradCols] * power : st[kGradCols];
   }
+  const float2 power2 = make_float2(power, power);
   const float2 scale = make_float2(p.scale_log2, p.scale_log2);
   if (wk.n > 0) {
     GradItem<kKeys> it(wk, 0);
@@ -522,9 +627,11 @@ __device__ __forceinline__ bool grad_math(const GradCtx& x, int block, uint32_t&
             const float2 y = __ffma2_rn(make_float2(__uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1])), scale,
                                         f ? make_float2(nl.z, nl.w) : make_float2(nl.x, nl.y));
             const float2 w = make_float2(ptx::ex2_approx(y.x), ptx::ex2_approx(y.y));
-            const float2 d = __fmul2_rn(
-                w, __fadd2_rn(make_float2(__uint_as_float(g[c][i]), __uint_as_float(g[c][i + 1])),
-                              f ? make_float2(nd.z, nd.w) : make_float2(nd.x, nd.y)));
+            const float2 dp = make_float2(__uint_as_float(g[c][i]), __uint_as_float(g[c][i + 1]));
+            const float2 delta = f ? make_float2(nd.z, nd.w) : make_float2(nd.x, nd.y);
+            const float2 d = __fmul2_rn(w, !kPowers ? __fadd2_rn(dp, delta)
+                                           : kKeys  ? __fmul2_rn(__fadd2_rn(dp, delta), power2)
+                                                    : __ffma2_rn(dp, power2, delta));
             if (kKeys) s[c][i / 2] = pack2<T>(w.x, w.y);
             g[c][i / 2] = pack2<T>(d.x, d.y);
           }
@@ -548,7 +655,9 @@ __device__ __forceinline__ bool grad_math(const GradCtx& x, int block, uint32_t&
   const int D = p.w.dim;
   const uint32_t a_addr = x.tmem + lanes + (kKeys && wg == 0 ? P::kColDv : P::kColD);
   const bool live = wk.n > 0 && (kKeys ? row < wk.s.len : (wk.s.start + row >= 0 && wk.s.start + row < wk.s.len));
-  const float f = kKeys && wg == 0 ? 1.0f : p.w.scale;
+  constexpr float kBack = kPowers ? 0x1p-15f : 1.0f;
+  static_assert(kGradPBits == 15, "kBack");
+  const float f = kKeys && wg == 0 ? kBack : (kPowers ? p.w.scale * (kBack / power) : p.w.scale);
   const bool store = row < (kKeys ? p.w.n_keys : p.w.n_queries);
   T* to = nullptr;
   float* part = nullptr;
@@ -596,13 +705,14 @@ __global__ void __launch_bounds__(GradPlan<NKB>::kThreads, 1)
                             const __grid_constant__ CUtensorMap tm_ky, const __grid_constant__ CUtensorMap tm_vy,
                             const __grid_constant__ WindowGradParams p) {
   using P = GradPlan<NKB>;
+  constexpr bool kPowers = !Elem<T>::kBf16;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_s = ptx::smem_addr(smem_raw);
   const uint32_t base_s = (raw_s + 1023u) & ~1023u;
   uint8_t* const base = smem_raw + (base_s - raw_s);
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(base + P::kOffBar + 8 * kGbCount);
-  volatile uint32_t* abort_flag = tmem_slot + 1;
   volatile int* taken = reinterpret_cast<volatile int*>(tmem_slot + 2);  // [2] X tiles handed out
+  volatile float* powers = reinterpret_cast<volatile float*>(tmem_slot + 4);  // [4] and their grad_power
   const uint32_t bar0 = base_s + P::kOffBar;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -622,9 +732,10 @@ __global__ void __launch_bounds__(GradPlan<NKB>::kThreads, 1)
       init(kGbNext + i, 1);
       init(kGbTaken + i, 11);  // loader, two issuers, eight math warps
     }
+    for (int i = 0; i < 4; ++i) init(kGbPower + i, 1);
     init(kGbSum, 1);
     init(kGbDone, 2);
-    *abort_flag = 0;
+    tmem_slot[1] = 0;  // the abort flag
     ptx::fence_mbar_init();
   }
   if (warp == 1) {
@@ -634,7 +745,7 @@ __global__ void __launch_bounds__(GradPlan<NKB>::kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const GradCtx x{p, Pipe{abort_flag, p.status}, base_s, bar0, *tmem_slot, warp, lane};
+  const GradCtx x{p, Pipe{ptx::smem_addr(const_cast<uint32_t*>(tmem_slot + 1)), p.status}, base_s, bar0, *tmem_slot, warp, lane};
   ptx::grid_dep_wait();
   uint32_t at = 0, tiles = 0;
   bool ok = true;
@@ -676,21 +787,36 @@ __global__ void __launch_bounds__(GradPlan<NKB>::kThreads, 1)
         ok = block < p.key_blocks ? grad_sums<T, NKB, true>(x, block, at, tiles)
                                   : grad_sums<T, NKB, false>(x, block, at, tiles);
       if (ptx::elect_one()) ptx::mma_commit(x.bar(kGbDone));
-    } else if (warp == 3 && lane == 0) {
+    } else if (warp == 3) {
       int block = static_cast<int>(blockIdx.x);
       for (uint32_t i = 0;; ++i) {
-        if (!x.pipe.wait(x.bar(kGbTaken + (i & 1u)), ((i >> 1) & 1u) ^ 1u, kSiteGradNext)) break;
-        taken[i & 1u] = block;
-        ptx::mbar_arrive(x.bar(kGbNext + (i & 1u)));
+        if (!x.pipe.wait_warp(x.bar(kGbTaken + (i & 1u)), ((i >> 1) & 1u) ^ 1u, kSiteGradNext)) break;
+        if (lane == 0) taken[i & 1u] = block;
+        pipe_warp_arrive(x.bar(kGbNext + (i & 1u)));
         if (block >= p.blocks) break;
-        block = static_cast<int>(gridDim.x + atomicAdd(p.next, 1u));
+        if (kPowers) {
+          const float power = block < p.key_blocks ? grad_power<true>(p, grad_walk<true>(p, block), lane)
+                                                   : grad_power<false>(p, grad_walk<false>(p, block), lane);
+          if (lane == 0) powers[i & 3u] = power;
+          pipe_warp_arrive(x.bar(kGbPower + (i & 3u)));
+        }
+        int taken_now = 0;
+        if (lane == 0) taken_now = static_cast<int>(gridDim.x + atomicAdd(p.next, 1u));
+        block = __shfl_sync(0xffffffffu, taken_now, 0);
       }
     }
   } else {
     ptx::regs_increase<P::kRegsMath>();
-    for (int block = next(true); ok && block >= 0; block = ok ? next(true) : -1)
-      ok = block < p.key_blocks ? grad_math<T, NKB, true>(x, block, at, tiles)
-                                : grad_math<T, NKB, false>(x, block, at, tiles);
+    for (int block = next(true); ok && block >= 0; block = ok ? next(true) : -1) {
+      float power = 1.0f;
+      if (kPowers) {  // (of four in turn: that of the tile after next is not written over one being read)
+        const uint32_t i = n_taken - 1;
+        if (!x.pipe.wait_warp(x.bar(kGbPower + (i & 3u)), (i >> 2) & 1u, kSiteGradNext)) break;
+        power = powers[i & 3u];
+      }
+      ok = block < p.key_blocks ? grad_math<T, NKB, true>(x, block, at, tiles, power)
+                                : grad_math<T, NKB, false>(x, block, at, tiles, power);
+    }
   }
 
   ptx::tc_fence_before();

@@ -177,16 +177,16 @@ struct WindowCtx {
   Pipe pipe;
   uint32_t base_s, tmem;
   int warp, lane;
-  __device__ __forceinline__ volatile int* again() const {
-    return const_cast<volatile int*>(reinterpret_cast<const volatile int*>(pipe.abort_flag + 1));
+  __device__ __forceinline__ int again(int i) const {
+    return static_cast<int>(ptx::ld_shared_volatile(pipe.abort_flag + 4 + 4 * i));
   }
-  __device__ __forceinline__ volatile uint32_t* notes() const { return pipe.abort_flag + 3; }
+  __device__ __forceinline__ uint32_t note_at(uint32_t i) const { return pipe.abort_flag + 12 + 4 * i; }
   // All threads of the block, after the first pass: is there a second?
   __device__ __forceinline__ bool second() const {
     ptx::tc_fence_before();
     ptx::named_barrier_sync(1, 384);
     ptx::tc_fence_after();
-    return again()[0] <= again()[1] && !*pipe.abort_flag;
+    return again(0) <= again(1) && ptx::ld_shared_volatile(pipe.abort_flag) == 0;
   }
 };
 
@@ -366,7 +366,7 @@ __device__ __forceinline__ void window_feed(const WindowCtx& x, uint32_t bar0, c
     const uint64_t keep = ptx::policy_evict_last();  // read again by other heads and rows
     long long c = 0;  // ring entries so far
     bool ok = true;
-    for (int r = kSecond ? x.again()[0] : 0, item; ok && (!kSecond || r <= x.again()[1]) && (item = window_entry(r)) < p.items; ++r) {
+    for (int r = kSecond ? x.again(0) : 0, item; ok && (!kSecond || r <= x.again(1)) && (item = window_entry(r)) < p.items; ++r) {
       const WindowItem it = window_item(p, item);
       for (int i = 0; ok && i < it.n; ++i) {
         const int row = it.tile(i) * kTile;
@@ -388,7 +388,7 @@ __device__ __forceinline__ void window_feed(const WindowCtx& x, uint32_t bar0, c
     // ------------------------------------------------------- Q tiles
     const uint64_t once = ptx::policy_evict_first();
     uint32_t n_q = 0;
-    for (int r = kSecond ? x.again()[0] : 0, item; (!kSecond || r <= x.again()[1]) && (item = window_entry(r)) < p.items; ++r) {
+    for (int r = kSecond ? x.again(0) : 0, item; (!kSecond || r <= x.again(1)) && (item = window_entry(r)) < p.items; ++r) {
       const WindowItem it = window_item(p, item);
       if (it.n == 0) continue;
       if (n_q > 0 && !pipe.wait(bar(kWbQEmpty), (n_q - 1) & 1u, kSiteWinQ)) break;
@@ -458,7 +458,7 @@ __device__ __forceinline__ void window_feed(const WindowCtx& x, uint32_t bar0, c
     };
     uint32_t g = 0;  // key tiles of this block so far (modulo 2^32); K of tile g is ring entry 2 g, V 2 g + 1
     bool ok = true;
-    for (int r = kSecond ? x.again()[0] : 0, item; ok && (!kSecond || r <= x.again()[1]) && (item = window_entry(r)) < p.items; ++r) {
+    for (int r = kSecond ? x.again(0) : 0, item; ok && (!kSecond || r <= x.again(1)) && (item = window_entry(r)) < p.items; ++r) {
       const WindowItem it = window_item(p, item);
       if (it.n == 0) continue;
       if (!(ok = pipe.wait_warp(bar(kWbQFull), n_q & 1u, kSiteWinMma))) break;
@@ -521,7 +521,7 @@ __device__ __forceinline__ void window_feed(const WindowCtx& x, uint32_t bar0, c
     // barrier has left its V stage by then.
     uint32_t g = 0, n_clean = 0, n_items = 0;  // tiles so far, of these cleaned, items with tiles
     bool ok = true;
-    for (int r = kSecond ? x.again()[0] : 0, item; ok && (!kSecond || r <= x.again()[1]) && (item = window_entry(r)) < p.items; ++r) {
+    for (int r = kSecond ? x.again(0) : 0, item; ok && (!kSecond || r <= x.again(1)) && (item = window_entry(r)) < p.items; ++r) {
       const WindowItem it = window_item(p, item);
       if (it.n == 0) continue;
       const WindowMasked masked(p.w, it);
@@ -539,7 +539,7 @@ __device__ __forceinline__ void window_feed(const WindowCtx& x, uint32_t bar0, c
         pipe_warp_arrive(bar(kWbVClean + n_clean % P::kVStages));
         ++n_clean;
       }
-      if (lane == 0) x.notes()[slot] = note;
+      if (lane == 0) ptx::st_shared_volatile(x.note_at(slot), note);
       pipe_warp_arrive(bar(kWbNotes + slot));
     }
   }
@@ -567,7 +567,7 @@ __device__ __forceinline__ void window_soft(const WindowCtx& x, uint32_t bar0, c
   int n_out = 0;     // result boxes of this warp so far
   bool ok = true;
   uint32_t n_items = 0;  // second pass: items with tiles so far
-  for (int round = kSecond ? x.again()[0] : 0, item; ok && (!kSecond || round <= x.again()[1]) && (item = window_entry(round)) < p.items; ++round) {
+  for (int round = kSecond ? x.again(0) : 0, item; ok && (!kSecond || round <= x.again(1)) && (item = window_entry(round)) < p.items; ++round) {
     const WindowItem it = window_item(p, item);
     if (!(t == 0 ? it.on[0] : it.on[1])) {
       if (kSecond && it.n > 0) pipe_warp_arrive(bar(kWbNotesFree + (n_items++ & 1u)));
@@ -674,7 +674,7 @@ __device__ __forceinline__ void window_soft(const WindowCtx& x, uint32_t bar0, c
       const uint32_t slot = n_items & 1u;
       if (!(ok = pipe.wait_warp(bar(kWbNotes + slot), (n_items >> 1) & 1u, kSiteWinOut))) break;
       ++n_items;
-      const uint32_t note = x.notes()[slot];
+      const uint32_t note = ptx::ld_shared_volatile(x.note_at(slot));
       pipe_warp_arrive(bar(kWbNotesFree + slot));
       if (note != 0 && !u.empty()) window_add_back<T>(p, item, t, note, o_addr);
     }
@@ -714,8 +714,8 @@ __device__ __forceinline__ void window_soft(const WindowCtx& x, uint32_t bar0, c
     // finite weights, but not the result: was it a hidden element of V?
     if (!kSecond && __any_sync(0xffffffffu, row < p.w.n_queries && row_on && check != 0.0f && l - l == 0.0f) &&
         window_leak<T>(p, item, t) && lane == 0) {
-      atomicMin(const_cast<int*>(x.again()), round);
-      atomicMax(const_cast<int*>(x.again()) + 1, round);
+      asm volatile("red.shared.min.s32 [%0], %1;" ::"r"(pipe.abort_flag + 4), "r"(round) : "memory");
+      asm volatile("red.shared.max.s32 [%0], %1;" ::"r"(pipe.abort_flag + 8), "r"(round) : "memory");
     }
     if (row < p.w.n_queries && p.lse != nullptr)
       p.lse[(static_cast<long long>(it.b) * p.w.heads + head) * p.w.n_queries + row] =
@@ -741,7 +741,6 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
   uint8_t* const base = smem_raw + (base_s - raw_s);
   const uint32_t bar0 = base_s + P::kOffBar;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(base + P::kOffBar + 8 * (kWbCount + kWbSecondCount));
-  volatile uint32_t* abort_flag = tmem_slot + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -763,10 +762,9 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
     }
     for (uint32_t i = kWbVClean; i < kWbSecondCount; ++i)
       ptx::mbar_init(bar0 + 8u * (kWbCount + i), i >= kWbNotesFree ? 8 : 1);
-    volatile int* again = reinterpret_cast<volatile int*>(abort_flag + 1);
-    again[0] = 0x7fffffff;
-    again[1] = -1;
-    *abort_flag = 0;
+    tmem_slot[1] = 0;  // the abort flag, and behind it:
+    reinterpret_cast<volatile int*>(tmem_slot)[2] = 0x7fffffff;
+    reinterpret_cast<volatile int*>(tmem_slot)[3] = -1;
     ptx::fence_mbar_init();
     ptx::prefetch_tensormap(&tm_q);
     ptx::prefetch_tensormap(&tm_k);
@@ -780,7 +778,7 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const WindowCtx x{p, Pipe{abort_flag, p.status}, base_s, *tmem_slot, warp, lane};
+  const WindowCtx x{p, Pipe{ptx::smem_addr(const_cast<uint32_t*>(tmem_slot + 1)), p.status}, base_s, *tmem_slot, warp, lane};
   ptx::grid_dep_wait();  // what earlier kernels of the stream wrote is visible
 
   bool two = false;

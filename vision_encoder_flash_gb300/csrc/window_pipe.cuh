@@ -28,7 +28,7 @@ enum PipeSite : uint32_t {
 // Bounded waits on mbarriers: one that runs out records its site in the
 // status word and raises the block's abort flag, which ends the others.
 struct Pipe {
-  volatile uint32_t* abort_flag;
+  uint32_t abort_flag;  // in shared memory
   uint32_t* status;
 
   __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, uint32_t site,
@@ -38,9 +38,9 @@ struct Pipe {
     for (uint32_t it = 1;; ++it) {
       if (ptx::mbar_try_wait(bar, parity)) return true;
       if ((it & 31u) == 0) {
-        if (heed_abort && *abort_flag) return false;
+        if (heed_abort && ptx::ld_shared_volatile(abort_flag) != 0) return false;
         if (ptx::global_timer_ns() - t0 > kPipeTimeoutNs) {
-          *abort_flag = 1;
+          ptx::st_shared_volatile(abort_flag, 1);
           atomicOr(status, 0x100u | site);
           return false;
         }
