@@ -485,6 +485,9 @@ __device__ __forceinline__ bool grad_scores(const GradCtx& x, int block, uint32_
         }
         if (i == 0) {
           ptx::mma_commit(x.bar(kGbSFull));
+          // the issuer's own arrival: what it saw of Y (the stats that the math warps
+          // read) and wrote there (zeros, which the second products read) goes with it
+          ptx::mbar_arrive(x.bar(kGbSFull));
           if (n + 1 == wk.n) ptx::mma_commit(x.bar(kGbXEmpty));
         }
       }
@@ -723,7 +726,7 @@ __global__ void __launch_bounds__(GradPlan<NKB>::kThreads, 1)
       init(kGbYFull + i, 1);
       init(kGbYEmpty + i, 1);
     }
-    init(kGbSFull, 1);
+    init(kGbSFull, 2);  // the products, and their issuer
     init(kGbGFree, 8);
     for (int i = 0; i < 2; ++i) {
       init(kGbPFull + i, 8);
