@@ -398,6 +398,9 @@ vattn::WindowParams window_params(const vattn_window_args* a) {
   w.window = static_cast<int>(a->window == 0 || a->window > none ? none : a->window);
   w.sinks = static_cast<int>(a->n_sinks > none ? none : a->n_sinks);
   w.scale = a->scale;
+  const uint64_t key_tiles = static_cast<uint64_t>(a->n_keys) / vattn::kTile + 1;
+  const uint64_t row_tiles = static_cast<uint64_t>(w.group) * (static_cast<uint64_t>(a->n_queries) / vattn::kTile + 1);
+  w.wait_ns = vattn::kPipeTimeoutNs + vattn::kPipeTileNs * (key_tiles + row_tiles);
   return w;
 }
 

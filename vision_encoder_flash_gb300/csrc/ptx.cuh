@@ -185,6 +185,14 @@ __device__ __forceinline__ uint32_t ld_shared_volatile(uint32_t addr) {
   asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
   return x;
 }
+__device__ __forceinline__ uint64_t ld_shared_volatile_u64(uint32_t addr) {
+  uint64_t x;
+  asm volatile("ld.volatile.shared.u64 %0, [%1];" : "=l"(x) : "r"(addr) : "memory");
+  return x;
+}
+__device__ __forceinline__ void st_shared_volatile_u64(uint32_t addr, uint64_t x) {
+  asm volatile("st.volatile.shared.u64 [%0], %1;" ::"r"(addr), "l"(x) : "memory");
+}
 __device__ __forceinline__ void st_shared_volatile(uint32_t addr, uint32_t x) {
   asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
 }

@@ -714,8 +714,9 @@ __global__ void __launch_bounds__(GradPlan<NKB>::kThreads, 1)
   const uint32_t base_s = (raw_s + 1023u) & ~1023u;
   uint8_t* const base = smem_raw + (base_s - raw_s);
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(base + P::kOffBar + 8 * kGbCount);
-  volatile int* taken = reinterpret_cast<volatile int*>(tmem_slot + 2);  // [2] X tiles handed out
-  volatile float* powers = reinterpret_cast<volatile float*>(tmem_slot + 4);  // [4] and their grad_power
+  const Pipe pipe{base_s + P::kOffBar + 8 * kGbCount + 8};
+  volatile int* taken = reinterpret_cast<volatile int*>(tmem_slot + 2 + kPipeBytes / 4);  // [2] X tiles handed out
+  volatile float* powers = reinterpret_cast<volatile float*>(taken + 2);                  // [4] and their grad_power
   const uint32_t bar0 = base_s + P::kOffBar;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -738,7 +739,7 @@ __global__ void __launch_bounds__(GradPlan<NKB>::kThreads, 1)
     for (int i = 0; i < 4; ++i) init(kGbPower + i, 1);
     init(kGbSum, 1);
     init(kGbDone, 2);
-    tmem_slot[1] = 0;  // the abort flag
+    pipe.init(p.w, p.status);
     ptx::fence_mbar_init();
   }
   if (warp == 1) {
@@ -748,7 +749,7 @@ __global__ void __launch_bounds__(GradPlan<NKB>::kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const GradCtx x{p, Pipe{ptx::smem_addr(const_cast<uint32_t*>(tmem_slot + 1)), p.status}, base_s, bar0, *tmem_slot, warp, lane};
+  const GradCtx x{p, pipe, base_s, bar0, *tmem_slot, warp, lane};
   ptx::grid_dep_wait();
   uint32_t at = 0, tiles = 0;
   bool ok = true;

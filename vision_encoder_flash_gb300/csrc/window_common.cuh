@@ -39,6 +39,7 @@ struct WindowParams {
   int window;  // >= 1; no limit: 2^29 (positions that matter are < n_keys < 2^29)
   int sinks;
   float scale;
+  unsigned long long wait_ns;  // limit of a wait inside the kernels (window_pipe.cuh)
 };
 
 // Length of sequence b and position of its query row 0.  Row i at p = start

@@ -169,7 +169,7 @@ enum WindowBar : int {
   kWbVClean = 27, kWbNotes = 31, kWbNotesFree = 33, kWbSecondCount = 35,
 };
 
-// What the roles of a block share, and behind the abort flag: the rounds of the
+// What the roles of a block share, and behind the pipe's words: the rounds of the
 // second pass, from and to, and [2] tiles of an item that were cleaned in it (see
 // window_add_back).
 struct WindowCtx {
@@ -178,15 +178,15 @@ struct WindowCtx {
   uint32_t base_s, tmem;
   int warp, lane;
   __device__ __forceinline__ int again(int i) const {
-    return static_cast<int>(ptx::ld_shared_volatile(pipe.abort_flag + 4 + 4 * i));
+    return static_cast<int>(ptx::ld_shared_volatile(pipe.at + kPipeBytes + 4 * i));
   }
-  __device__ __forceinline__ uint32_t note_at(uint32_t i) const { return pipe.abort_flag + 12 + 4 * i; }
+  __device__ __forceinline__ uint32_t note_at(uint32_t i) const { return pipe.at + kPipeBytes + 8 + 4 * i; }
   // All threads of the block, after the first pass: is there a second?
   __device__ __forceinline__ bool second() const {
     ptx::tc_fence_before();
     ptx::named_barrier_sync(1, 384);
     ptx::tc_fence_after();
-    return again(0) <= again(1) && ptx::ld_shared_volatile(pipe.abort_flag) == 0;
+    return again(0) <= again(1) && !pipe.aborted();
   }
 };
 
@@ -714,8 +714,8 @@ __device__ __forceinline__ void window_soft(const WindowCtx& x, uint32_t bar0, c
     // finite weights, but not the result: was it a hidden element of V?
     if (!kSecond && __any_sync(0xffffffffu, row < p.w.n_queries && row_on && check != 0.0f && l - l == 0.0f) &&
         window_leak<T>(p, item, t) && lane == 0) {
-      asm volatile("red.shared.min.s32 [%0], %1;" ::"r"(pipe.abort_flag + 4), "r"(round) : "memory");
-      asm volatile("red.shared.max.s32 [%0], %1;" ::"r"(pipe.abort_flag + 8), "r"(round) : "memory");
+      asm volatile("red.shared.min.s32 [%0], %1;" ::"r"(pipe.at + kPipeBytes), "r"(round) : "memory");
+      asm volatile("red.shared.max.s32 [%0], %1;" ::"r"(pipe.at + kPipeBytes + 4), "r"(round) : "memory");
     }
     if (row < p.w.n_queries && p.lse != nullptr)
       p.lse[(static_cast<long long>(it.b) * p.w.heads + head) * p.w.n_queries + row] =
@@ -734,13 +734,14 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
                             const __grid_constant__ WindowFwdParams p) {
   using P = WindowFwdPlan<NKB>;
   constexpr int S = P::kStages;
-  static_assert(8 * (kWbCount + kWbSecondCount) + 24 <= 640 && P::kVStages <= 4, "barriers");
+  static_assert(8 * (kWbCount + kWbSecondCount) + 8 + kPipeBytes + 16 <= 640 && P::kVStages <= 4, "barriers");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_s = ptx::smem_addr(smem_raw);
   const uint32_t base_s = (raw_s + 1023u) & ~1023u;
   uint8_t* const base = smem_raw + (base_s - raw_s);
   const uint32_t bar0 = base_s + P::kOffBar;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(base + P::kOffBar + 8 * (kWbCount + kWbSecondCount));
+  const Pipe pipe{base_s + P::kOffBar + 8 * (kWbCount + kWbSecondCount) + 8};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -762,9 +763,9 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
     }
     for (uint32_t i = kWbVClean; i < kWbSecondCount; ++i)
       ptx::mbar_init(bar0 + 8u * (kWbCount + i), i >= kWbNotesFree ? 8 : 1);
-    tmem_slot[1] = 0;  // the abort flag, and behind it:
-    reinterpret_cast<volatile int*>(tmem_slot)[2] = 0x7fffffff;
-    reinterpret_cast<volatile int*>(tmem_slot)[3] = -1;
+    pipe.init(p.w, p.status);
+    ptx::st_shared_volatile(pipe.at + kPipeBytes, 0x7fffffffu);  // rounds of the second pass: none
+    ptx::st_shared_volatile(pipe.at + kPipeBytes + 4, 0xffffffffu);
     ptx::fence_mbar_init();
     ptx::prefetch_tensormap(&tm_q);
     ptx::prefetch_tensormap(&tm_k);
@@ -778,7 +779,7 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const WindowCtx x{p, Pipe{ptx::smem_addr(const_cast<uint32_t*>(tmem_slot + 1)), p.status}, base_s, *tmem_slot, warp, lane};
+  const WindowCtx x{p, pipe, base_s, *tmem_slot, warp, lane};
   ptx::grid_dep_wait();  // what earlier kernels of the stream wrote is visible
 
   bool two = false;

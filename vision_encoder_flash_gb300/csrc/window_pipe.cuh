@@ -15,7 +15,10 @@ constexpr int kBlockBytes = kTile * 128;    // 128 rows x 64 elements, 128-byte 
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazyLog2 = 8.0f;           // O is rescaled once a row's maximum grew by 2^8
-constexpr uint64_t kPipeTimeoutNs = 2000000000ull;
+// Longest wait: some are for a whole walk (a loader's for the end of an item, the
+// counter's for the last X tile's roles), hence 2 s and 10 us for each tile of the
+// longest walk that a call can have, ten times what one takes.
+constexpr uint64_t kPipeTimeoutNs = 2000000000ull, kPipeTileNs = 10000ull;
 
 // Wait sites in the low byte of the status word (attn_kernel.cuh has 1..18).
 enum PipeSite : uint32_t {
@@ -26,11 +29,19 @@ enum PipeSite : uint32_t {
 };
 
 // Bounded waits on mbarriers: one that runs out records its site in the
-// status word and raises the block's abort flag, which ends the others.
+// status word and raises the block's abort flag, which ends the others.  What
+// that takes is in shared memory at `at`, kPipeBytes aligned to 8 (abort flag, limit,
+// address of the status word): registers are what these kernels are short of.
+constexpr uint32_t kPipeBytes = 24;
 struct Pipe {
-  uint32_t abort_flag;  // in shared memory
-  uint32_t* status;
+  uint32_t at;
 
+  __device__ __forceinline__ void init(const WindowParams& w, uint32_t* status) const {  // by one thread
+    ptx::st_shared_volatile(at, 0);
+    ptx::st_shared_volatile_u64(at + 8, w.wait_ns);
+    ptx::st_shared_volatile_u64(at + 16, reinterpret_cast<uint64_t>(status));
+  }
+  __device__ __forceinline__ bool aborted() const { return ptx::ld_shared_volatile(at) != 0; }
   __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, uint32_t site,
                                        bool heed_abort = true) const {
     if (ptx::mbar_try_wait(bar, parity)) return true;
@@ -38,10 +49,10 @@ struct Pipe {
     for (uint32_t it = 1;; ++it) {
       if (ptx::mbar_try_wait(bar, parity)) return true;
       if ((it & 31u) == 0) {
-        if (heed_abort && ptx::ld_shared_volatile(abort_flag) != 0) return false;
-        if (ptx::global_timer_ns() - t0 > kPipeTimeoutNs) {
-          ptx::st_shared_volatile(abort_flag, 1);
-          atomicOr(status, 0x100u | site);
+        if (heed_abort && aborted()) return false;
+        if (ptx::global_timer_ns() - t0 > ptx::ld_shared_volatile_u64(at + 8)) {
+          ptx::st_shared_volatile(at, 1);
+          atomicOr(reinterpret_cast<uint32_t*>(ptx::ld_shared_volatile_u64(at + 16)), 0x100u | site);
           return false;
         }
       }
