@@ -113,3 +113,66 @@ def test_no_number_among_the_rows(td):
     got = vef.backward_window(g, q, k, v, out, lse, **how)
     for x, y in zip(got, want):
         assert torch.equal(x[:, :, :256], y[:, :, :256]) and torch.equal(x[:, :, 768:], y[:, :, 768:])
+
+
+@pytest.mark.parametrize("call", ["window", "cached"])
+@pytest.mark.parametrize("name", ["f16", "bf16"])
+def test_many_small_weights_beside_a_large_one(td, name, call):
+    """One key of weight 1 and 2^19 of 2^-23.4, which f16 does not have: together
+    they are a twentieth of the result."""
+    torch, dev = td
+    N, D, score = 2 ** 19, 8, 16.22
+    k = torch.zeros(1, 1, N, D, device=dev)
+    k[:, :, 0] = 1.0
+    v = 1.0 + 0.5 * torch.rand(1, 1, N, D, generator=torch.Generator(device=dev).manual_seed(5), device=dev)
+    v[:, :, 0] = 0.25
+    k, v = (t.to(torch.float16 if name == "f16" else torch.bfloat16) for t in (k, v))
+    q = torch.ones(1, 1, 1, D, dtype=k.dtype, device=dev)
+    scale = float(np.float32(score / D))
+    if call == "window":
+        out, lse = vef.forward_window(q, k, v, scale=scale, return_lse=True)
+    else:  # so many sequences that none's keys are shared out
+        B = 700
+        lens = torch.full((B,), N, dtype=torch.int32, device=dev)
+        out = vef.forward_cached(q.expand(B, 1, 1, D), k.expand(B, 1, N, D), v.expand(B, 1, N, D), lens, scale=scale)
+        assert bool((out == out[:1]).all())
+        out = out[:1]
+    w = torch.full((N,), np.exp(-scale * D), dtype=torch.float64, device=dev)
+    w[0] = 1.0
+    want = (w[:, None] * v[0, 0].double()).sum(0) / w.sum()
+    # each weight is rounded (u, and in f16 2^-32 of the largest), so is the result.  How many products
+    # of a matrix instruction are added before a cut to f32 is not specified: each of the N additions
+    # may be cut by 2^-23 of the sum (to 24 digits, downwards); those of the weights go 128 at a time
+    u = HALF_STEP[name]
+    bound = (2 * u + N * 2.0 ** -23 + N / 128 * 2.0 ** -24 + 2.0 ** -16) * want
+    if name == "f16":
+        bound = bound + 2.0 ** -32 * 1.5 * N
+    assert bool(((out[0, 0, 0].double() - want).abs() <= bound).all()), (out[0, 0, 0], want, bound)
+    if call == "window":
+        assert abs(float(lse) - (scale * D + float(torch.log(w.sum())))) <= 2.0 ** -10
+
+
+@pytest.mark.parametrize("call", ["window", "cached"])
+def test_small_weights_add_up(td, call):
+    """The same with sums that are exact: 2^16 keys, the large weight on a V of 0,
+    the others on ones.  Held times 2^7 a weight is a multiple of 2^-24, and the
+    sum of them, below 1, has 24 digits."""
+    torch, dev = td
+    N, D, score = 2 ** 16, 8, 16.22
+    k = torch.zeros(1, 1, N, D, dtype=torch.float16, device=dev)
+    v = torch.ones_like(k)
+    k[:, :, 0], v[:, :, 0] = 1.0, 0.0
+    q = torch.ones(1, 1, 1, D, dtype=k.dtype, device=dev)
+    scale = float(np.float32(score / D))
+    if call == "window":
+        out = vef.forward_window(q, k, v, scale=scale)
+    else:
+        B = 700
+        lens = torch.full((B,), N, dtype=torch.int32, device=dev)
+        out = vef.forward_cached(q.expand(B, 1, 1, D), k.expand(B, 1, N, D), v.expand(B, 1, N, D), lens, scale=scale)
+    w = (N - 1) * np.exp(-scale * D)
+    want = w / (1 + w)
+    # a weight is off by 2^-32, the result by u, the f32 score and exponential by 2^-16 (16 is held to
+    # 2^-20, 2 D + 8 roundings), the sum of the weights, 128 at a time, by N / 128 2^-24
+    bound = (HALF_STEP["f16"] + 2.0 ** -16 + N / 128 * 2.0 ** -24) * want + 2.0 ** -32 * N
+    assert float((out.double() - want).abs().max()) <= bound, (out.flatten()[:2], want, bound)

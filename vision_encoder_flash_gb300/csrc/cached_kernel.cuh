@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(CachedPlan<DP, RW>::kThreads)
         for (int n = 0; n < KN; ++n)
 #pragma unroll
           for (int f = 0; f < 2; ++f) {
-            const float x = ptx::ex2_approx(fmaf(s[n][2 * e + f], p.scale_log2, -ref));
+            const float x = ptx::ex2_approx(fmaf(s[n][2 * e + f], p.scale_log2, kWeightLog2<T> - ref));
             sum += x;
             s[n][2 * e + f] = x;
           }

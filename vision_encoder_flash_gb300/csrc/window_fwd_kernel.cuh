@@ -37,10 +37,10 @@
 // runs while the tensor core works for the other.
 //
 // Statistics and accumulators are f32.  The weights are rounded to the
-// tensors' type for the second product (relative 2^-9 / 2^-12 at most, the
-// sum l takes them unrounded), as the product needs; O is rescaled in TMEM
-// only when a row's maximum grew by more than 2^8 (exact after the final
-// 1 / l).  A masked score is -infinity by selection, so nothing that K holds
+// tensors' type for the second product (relative 2^-9 / 2^-12 at most, and in f16
+// 2^-32 of the row's largest; the sum l takes them unrounded), as the product
+// needs; O is rescaled in TMEM only when a row's maximum grew by more than 2^8
+// (exact after the final 1 / l).  A masked score is -infinity by selection, so nothing that K holds
 // there gets through, and V rows behind the sequence are zeroed in shared memory
 // before the product.  Other masked V elements that are not finite would stay in
 // O as 0 x infinity.  A warp whose results are not finite although its weights
@@ -621,7 +621,7 @@ __device__ __forceinline__ void window_soft(const WindowCtx& x, uint32_t bar0, c
       const bool grew = mt > m + kLazyLog2;
       const float alpha = grew ? ptx::ex2_approx(m - mt) : 1.0f;  // 0 for the row's first keys
       if (grew) m = mt;
-      const float ref = m == -INFINITY ? 0.0f : -m;  // a row that saw nothing yet: all weights 0
+      const float ref = m == -INFINITY ? 0.0f : kWeightLog2<T> - m;  // a row that saw nothing yet: all weights 0
       const float2 scale = make_float2(p.scale_log2, p.scale_log2), shift = make_float2(ref, ref);
       float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -719,7 +719,7 @@ __device__ __forceinline__ void window_soft(const WindowCtx& x, uint32_t bar0, c
     }
     if (row < p.w.n_queries && p.lse != nullptr)
       p.lse[(static_cast<long long>(it.b) * p.w.heads + head) * p.w.n_queries + row] =
-          l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+          l == 0.0f ? -INFINITY : (m + (log2f(l) - kWeightLog2<T>)) * kLn2;
   }
   // before the rows are written again, or the block's shared memory goes
   if (lane == 0) ptx::bulk_wait_group_all();

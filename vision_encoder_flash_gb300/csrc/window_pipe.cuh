@@ -15,6 +15,10 @@ constexpr int kBlockBytes = kTile * 128;    // 128 rows x 64 elements, 128-byte 
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazyLog2 = 8.0f;           // O is rescaled once a row's maximum grew by 2^8
+// Weights of a row, its sum and its O are held times 2^this: f16 has no digits
+// below 2^-24, and rows of 2^20 keys have weights of 2^-20 that add up.
+template <typename T>
+constexpr float kWeightLog2 = Elem<T>::kBf16 ? 0.0f : 15.0f - kLazyLog2;
 // Longest wait: some are for a whole walk (a loader's for the end of an item, the
 // counter's for the last X tile's roles), hence 2 s and 10 us for each tile of the
 // longest walk that a call can have, ten times what one takes.
