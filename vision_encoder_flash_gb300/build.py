@@ -20,6 +20,7 @@ DEPS = SOURCES + [os.path.join(CSRC, "attn_kernel.cuh"), os.path.join(CSRC, "sta
                   os.path.join(CSRC, "conv1d_kernel.cuh"),
                   os.path.join(CSRC, "ptx.cuh"),
                   os.path.join(CSRC, "host_common.h"), os.path.join(CSRC, "elem.cuh"),
+                  os.path.join(CSRC, "rope_turns.h"),
                   os.path.join(CSRC, "qk_norm_rope_kernel.cuh"),
                   os.path.join(CSRC, "window_common.cuh"),
                   os.path.join(CSRC, "window_pipe.cuh"), os.path.join(CSRC, "window_fwd_kernel.cuh"),

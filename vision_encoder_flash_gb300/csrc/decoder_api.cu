@@ -12,6 +12,7 @@
 #include "cached_kernel.cuh"
 #include "host_common.h"
 #include "qk_norm_rope_kernel.cuh"
+#include "rope_turns.h"
 #include "window_bwd_kernel.cuh"
 #include "window_fwd_kernel.cuh"
 
@@ -285,9 +286,7 @@ void qk_plan(vattn::QkParams* p, const vattn_qk_args* a, int v, int sms, int64_t
   p->half = static_cast<int>(a->rope_dims / 2);
   p->w_f32 = a->weight_dtype == VATTN_F32;
   p->eps = a->eps;
-  const double two_pi = 6.283185307179586476925286766559;
-  for (int i = 0; i < p->half; ++i)
-    p->turns[i] = std::pow(a->base, -2.0 * i / static_cast<double>(a->rope_dims)) / two_pi;
+  vattn::host::rope_turns(a->base, static_cast<int>(a->rope_dims), p->turns, p->turns_rest);
   const int rest = p->D - 2 * p->half;
   p->slots = p->half / v + (rest / 2 + v - 1) / v + (v == 1 ? rest & 1 : 0);
   p->log_lanes = 0;

@@ -11,8 +11,9 @@
 //   g' = R(-theta) g,   dw += g' x r,   dx = r (g' w) - x r^3 / D sum(g' w x).
 //
 // Angles: in turns, position * f_i only counts modulo 1, so f_i is held as a
-// 64-bit binary fraction (from f64) and position * f_i is one wrapping
-// integer product: exact to 2^-33 turns at any 32-bit position, where an f32
+// 64-bit binary fraction (from 77 digits, rope_turns.h: those of an f64 alone leave
+// 2^-25 turns at positions near 2^31) and position * f_i is one wrapping
+// integer product: within 2^-31 turns at any 32-bit position, where an f32
 // product loses all digits.  The fraction is cut to the nearest quarter turn
 // and the rest goes through two short polynomials (qk_sincos).
 //
@@ -72,6 +73,7 @@ struct QkParams {
   int w_f32;
   float eps;
   double turns[kQkMaxDim / 2];  // turns per position
+  float turns_rest[kQkMaxDim / 2];  // what that rounds away
 };
 
 // One lane's place in a row: V pairs (a[ia ..], b[ib ..]).
@@ -182,9 +184,17 @@ __device__ __forceinline__ float vsum(const float (&a)[V]) {
 __device__ __forceinline__ void qk_turns(const QkParams& p, uint64_t* turn) {
   if (static_cast<int>(threadIdx.x) < p.half) {
     double f = p.turns[threadIdx.x];
-    if (p.factors != nullptr) f /= static_cast<double>(p.factors[threadIdx.x]);
+    float rest = p.turns_rest[threadIdx.x];  // 24 of its digits are enough: f64 arithmetic is slow
+    if (p.factors != nullptr) {
+      const float by = p.factors[threadIdx.x];
+      const double q = f / by;
+      rest = (static_cast<float>(fma(-q, static_cast<double>(by), f)) + rest) / by;
+      f = q;
+    }
+    // the fractions of both, times 2^64; their sum modulo that
     f -= floor(f);
-    turn[threadIdx.x] = static_cast<uint64_t>(f * 0x1p64);
+    rest -= rintf(rest);
+    turn[threadIdx.x] = static_cast<uint64_t>(f * 0x1p64) + static_cast<uint64_t>(static_cast<long long>(rest * 0x1p64f));
   }
   __syncthreads();
 }
