@@ -566,8 +566,8 @@ vattn_status backward_window(const Tensor& tg, const Tensor& tq, const Tensor& t
   p.chunks = cut(items);
   // The first keys' tiles together into eight pieces a multiprocessor at most:
   // 160 MB of partial sums, where every key as a first key would take gigabytes.
-  most = std::max(most, static_cast<long long>(static_cast<double>(seqs * p.sink_tiles) * static_cast<double>(all_items) / (8.0 * sms)));
-  p.sink_chunks = p.sink_tiles > 0 ? cut(all_items) : 1;
+  const long long budget = 8LL * sms / std::max(1LL, seqs * p.sink_tiles);
+  p.sink_chunks = p.sink_tiles > 0 ? static_cast<int>(std::max(1LL, std::min<long long>(cut(all_items), budget))) : 1;
   const long long sink_blocks = seqs * p.sink_tiles * p.sink_chunks;
   const long long rest_blocks = seqs * (p.key_tiles - p.sink_tiles) * p.chunks;
   if (sink_blocks + rest_blocks + query_tiles > kMaxRows || bhs * p.stat_tiles > kMaxRows)
