@@ -125,8 +125,8 @@ typedef struct {
  * head_dim: broadcast heads and sequences are read as they are, broadcast
  * rows are refused.  lse: NULL or f32 [batch, n_q_heads, n_queries] contiguous, the
  * natural logarithm of the sum of the row's exponentials (for
- * vattn_backward_window).  n_queries, n_keys < 2^29; q_start is held to
- * +-2^30.
+ * vattn_backward_window).  n_queries, n_keys < 2^29, batch times either
+ * number of heads < 2^30; q_start is held to +-2^30.
  */
 vattn_status vattn_forward_window(const vattn_rows* q, const vattn_rows* k, const vattn_rows* v,
                                   const vattn_rows* out, float* lse,

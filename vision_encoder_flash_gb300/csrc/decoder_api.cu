@@ -363,8 +363,9 @@ vattn_status check_window_args(const vattn_window_args* a) {
                 (long long)a->n_q_heads, (long long)a->n_kv_heads);
   if (a->n_queries > kMaxKeys || a->n_keys > kMaxKeys)
     return fail(VATTN_ERR_UNSUPPORTED, "n_queries and n_keys must stay below 2^29");
-  if (a->n_q_heads > kMaxRows || a->batch > kMaxRows || a->batch * a->n_q_heads > kMaxRows)
-    return fail(VATTN_ERR_UNSUPPORTED, "batch * n_q_heads must stay below 2^30");
+  if (a->n_q_heads > kMaxRows || a->n_kv_heads > kMaxRows || a->batch > kMaxRows ||
+      a->batch * std::max(a->n_q_heads, a->n_kv_heads) > kMaxRows)
+    return fail(VATTN_ERR_UNSUPPORTED, "batch * n_q_heads and batch * n_kv_heads must stay below 2^30");
   if (a->window < 0) return fail(VATTN_ERR_INVALID_ARG, "window must be >= 0");
   if (a->n_sinks < 0) return fail(VATTN_ERR_INVALID_ARG, "n_sinks must be >= 0");
   if (!(a->scale > 0.0f) || !std::isfinite(a->scale))
