@@ -117,7 +117,11 @@ typedef struct {
  *   j <= p < len  with  j > p - window  or  j < n_sinks.
  * A row that sees nothing (p < 0, p >= len) gets zeros, and lse = -infinity.
  * What k and v hold at keys that a row does not see does not reach the row,
- * infinities and NaN included.
+ * infinities and NaN included.  An infinity or NaN of v reaches the rows that
+ * see it, at the cost of a second look at a few tiles.  A row all of whose
+ * scores are -infinity counts as one that sees nothing.  The sum of the weights
+ * times v is divided by that of the weights at its end, and is f32 before: in
+ * bf16 |v| beyond 2^120 / keys may overflow it.
  *
  * q [batch, n_q_heads, n_queries, head_dim], k and v [batch, n_kv_heads,
  * n_keys, head_dim], out as q: 16-byte aligned, strides multiples of 8

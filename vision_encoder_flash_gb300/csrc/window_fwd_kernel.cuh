@@ -184,6 +184,7 @@ struct WindowCtx {
   // All threads of the block, after the first pass: is there a second?
   __device__ __forceinline__ bool second() const {
     ptx::tc_fence_before();
+    __syncwarp();  // the loaders' lanes come one by one
     ptx::named_barrier_sync(1, 384);
     ptx::tc_fence_after();
     return again(0) <= again(1) && !pipe.aborted();
