@@ -173,6 +173,7 @@ vattn_status vattn_backward_window(const vattn_rows* dout, const vattn_rows* q, 
  * window or < n_sinks.  A word without bits sees nothing.  Bits >= T are
  * ignored.  Tokens whose row base + t is negative see nothing and are seen
  * by none; they get zeros.  What other rows hold does not reach the result.
+ * Scores and values that are not finite: as in vattn_forward_window.
  *
  * q, out [batch, n_q_heads, T, head_dim]; alignment and strides as in
  * vattn_forward_window; q_start must be NULL.

@@ -697,7 +697,7 @@ __device__ __forceinline__ bool grad_math(const GradCtx& x, int block, uint32_t&
   return true;
 }
 
-// X tiles blockIdx.x, + gridDim.x, ...: key tiles first, then the query
+// X tiles: blockIdx.x, then from the counter: key tiles first, then the query
 // tiles, which are shorter and even out what the key tiles leave.  tm_*:
 // boxes of 128 rows (x) and of 64 (y).
 template <typename T, int NKB>

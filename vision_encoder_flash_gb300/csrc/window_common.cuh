@@ -71,11 +71,6 @@ __device__ __forceinline__ T* rows_at_mut(const RowsTensor& t, long long b, long
   return const_cast<T*>(rows_at<T>(t, b, h, i));
 }
 
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));

@@ -10,6 +10,11 @@ as they are (rows that are a broadcast of one: ``forward_cached`` and
 stream of the tensors' device) and returns without synchronising; results
 that it allocates belong to that stream.  With a ``stream`` of one's own, the
 inputs must be ready on it.  There is no CPU fallback.
+
+The calls are not recorded by autograd: results carry no gradient function, also
+where an input requires a gradient.  A training step calls
+``backward_window`` and ``qk_norm_rope_backward`` itself, or
+puts the pairs into a ``torch.autograd.Function`` of its own.
 """
 from __future__ import annotations
 
