@@ -155,10 +155,8 @@ struct WindowFwdPlan {
   static constexpr bool kOwnP = NKB == 1;  // P has TMEM columns of its own
   static constexpr uint32_t kColP = kOwnP ? 256 : 0, kStrideP = kOwnP ? 64 : 128;
   static constexpr uint32_t kColO = kOwnP ? 384 : 256, kStrideO = kOwnP ? 64 : 128;
-  // registers: 72 + 2 x 216, 104 + 2 x 200 a thread = 3 x 168, what the launch has (1 x
-  // 16(4) x 8192 x 128, window 1024: 72.2 us, with 72 + 2 x 216 73.8; 1 x 8 x 8192 x 64:
-  // 87.1 us, with 88 + 2 x 208 95.1)
-  static constexpr uint32_t kRegsOther = NKB == 1 ? 72 : 104, kRegsSoftmax = NKB == 1 ? 216 : 200;
+  // registers: 72 + 2 x 216 a thread = 3 x 168, what the launch has
+  static constexpr uint32_t kRegsOther = 72, kRegsSoftmax = 216;
   static_assert(kSmemBytes <= 232448, "shared memory");
 };
 
@@ -166,7 +164,7 @@ enum WindowBar : int {
   kWbQFull = 0, kWbQEmpty = 1, kWbKvFull = 2, kWbKvEmpty = 10, kWbSFull = 18, kWbPFull = 20,
   kWbPvDone = 22, kWbSFree = 24, kWbMmaDone = 26, kWbCount = 27,
   // second pass: a set of its own, and these
-  kWbVClean = 27, kWbNotes = 31, kWbNotesFree = 33, kWbSecondCount = 35,
+  kWbVLanded = 27, kWbNotes = 31, kWbNotesFree = 33, kWbSecondCount = 35,
 };
 
 // What the roles of a block share, and behind the pipe's words: the rounds of the
@@ -265,25 +263,23 @@ __device__ __noinline__ bool window_leak(const WindowFwdParams& p, int entry, in
   return __any_sync(0xffffffffu, leak);
 }
 
-// A V tile of which `left` rows belong to the sequence (one warp): the other
-// rows become zeros, and so do elements that are not finite.  Were there any?
+// Elements that are not finite in the `left` rows of a V tile that belong to the
+// sequence become zeros (one warp).  Were there any?
 template <typename T, int NKB>
 __device__ __forceinline__ bool window_clean_v(uint32_t v, int left) {
   constexpr uint32_t kExp = Elem<T>::kBf16 ? 0x7f80u : 0x7c00u;
   const int lane = static_cast<int>(threadIdx.x) & 31, end = min(left, kTile) * 8;  // 16-byte chunks of 64 columns
   bool any = false;
   for (int kb = 0; kb < NKB; ++kb)
-    for (int i = lane; i < kTile * 8; i += 32) {
+    for (int i = lane; i < end; i += 32) {
       const uint32_t at = v + kb * kBlockBytes + i * 16;
       const float4 x = ptx::ld_shared_v4(at);
       uint32_t y[4] = {__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(x.z), __float_as_uint(x.w)};
-      const bool bad = i < end && not_finite<T>(y[0], y[1], y[2], y[3]);
-      any |= bad;
-      if (i < end && !bad) continue;
+      if (!not_finite<T>(y[0], y[1], y[2], y[3])) continue;
+      any = true;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        y[e] = i >= end ? 0u
-                        : y[e] & (((y[e] & kExp) == kExp ? 0u : 0xffffu) | (((y[e] >> 16) & kExp) == kExp ? 0u : 0xffff0000u));
+        y[e] &= ((y[e] & kExp) == kExp ? 0u : 0xffffu) | (((y[e] >> 16) & kExp) == kExp ? 0u : 0xffff0000u);
       ptx::st_shared_v4(at, __uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2]), __uint_as_float(y[3]));
     }
   ptx::fence_proxy_async_smem();
@@ -352,9 +348,11 @@ __device__ __noinline__ void window_add_back(const WindowFwdParams& p, int entry
 }
 
 // Warps 0 to 3: loads, matrix products, and in the second pass clean V tiles.
-template <typename T, int NKB, bool kSecond>
-__device__ __forceinline__ void window_feed(const WindowCtx& x, uint32_t bar0, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
-                                            const CUtensorMap& tm_v) {
+// One code for both passes: a second instance, though never run, made calls
+// between other kernels 6 to 8 us slower.
+template <typename T, int NKB>
+__device__ __forceinline__ void window_feed(const WindowCtx& x, bool second, uint32_t bar0, const CUtensorMap& tm_q,
+                                            const CUtensorMap& tm_k, const CUtensorMap& tm_v) {
   using P = WindowFwdPlan<NKB>;
   constexpr int S = P::kStages;
   const WindowFwdParams& p = x.p;
@@ -362,34 +360,37 @@ __device__ __forceinline__ void window_feed(const WindowCtx& x, uint32_t bar0, c
   const uint32_t base_s = x.base_s, tmem = x.tmem;
   const int warp = x.warp, lane = x.lane;
   auto bar = [bar0](uint32_t i) -> uint32_t { return bar0 + 8u * i; };
+  const int from = second ? x.again(0) : 0, to = second ? x.again(1) : 0x7fffffff;
   if (warp == 0 && lane == 0) {
     // ---------------------------------------------------- K and V tiles
     const uint64_t keep = ptx::policy_evict_last();  // read again by other heads and rows
     long long c = 0;  // ring entries so far
     bool ok = true;
-    for (int r = kSecond ? x.again(0) : 0, item; ok && (!kSecond || r <= x.again(1)) && (item = window_entry(r)) < p.items; ++r) {
+    // where entry st arrives: V in the second pass at warp 3's, which passes it on
+    auto lands = [&](int st) { return bar(second && (st & 1) != 0 ? kWbVLanded + (st >> 1) : kWbKvFull + st); };
+    for (int r = from, item; ok && r <= to && (item = window_entry(r)) < p.items; ++r) {
       const WindowItem it = window_item(p, item);
       for (int i = 0; ok && i < it.n; ++i) {
         const int row = it.tile(i) * kTile;
         for (int kv = 0; kv < 2; ++kv, ++c) {
           const int st = static_cast<int>(c % S);
           if (!(ok = pipe.wait(bar(kWbKvEmpty + st), static_cast<uint32_t>((c / S) & 1) ^ 1u, kSiteWinKv))) break;
-          ptx::mbar_arrive_expect_tx(bar(kWbKvFull + st), P::kTileBytes);
+          ptx::mbar_arrive_expect_tx(lands(st), P::kTileBytes);
           const MapMul m = kv ? p.mv : p.mk;
           for (int kb = 0; kb < NKB; ++kb)
             ptx::tma_load_4d_hint(base_s + P::kOffKv + st * P::kTileBytes + kb * kBlockBytes,
-                                  kv ? &tm_v : &tm_k, bar(kWbKvFull + st), kb * 64, row,
+                                  kv ? &tm_v : &tm_k, lands(st), kb * 64, row,
                                   it.kh * m.h, it.b * m.b, keep);
         }
       }
     }
     for (long long d = c > S ? c - S : 0; d < c; ++d)
-      pipe.drain(bar(kWbKvFull + static_cast<int>(d % S)), static_cast<uint32_t>((d / S) & 1), kSiteWinDrain);
+      pipe.drain(lands(static_cast<int>(d % S)), static_cast<uint32_t>((d / S) & 1), kSiteWinDrain);
   } else if (warp == 2 && lane == 0) {
     // ------------------------------------------------------- Q tiles
     const uint64_t once = ptx::policy_evict_first();
     uint32_t n_q = 0;
-    for (int r = kSecond ? x.again(0) : 0, item; (!kSecond || r <= x.again(1)) && (item = window_entry(r)) < p.items; ++r) {
+    for (int r = from, item; r <= to && (item = window_entry(r)) < p.items; ++r) {
       const WindowItem it = window_item(p, item);
       if (it.n == 0) continue;
       if (n_q > 0 && !pipe.wait(bar(kWbQEmpty), (n_q - 1) & 1u, kSiteWinQ)) break;
@@ -419,7 +420,7 @@ __device__ __forceinline__ void window_feed(const WindowCtx& x, uint32_t bar0, c
     auto commit = [&](uint32_t b) {
       if (ptx::elect_one()) ptx::mma_commit(bar(b));
     };
-    uint32_t n_q = 0, n_s[2] = {0, 0}, n_p[2] = {0, 0}, n_clean = 0;
+    uint32_t n_q = 0, n_s[2] = {0, 0}, n_p[2] = {0, 0};
     // S_t of ring entry c; with P of its own, once the softmax has read the last S_t
     auto issue_s = [&](int t, uint32_t c) -> bool {
       if (P::kOwnP && n_s[t] > 0) {
@@ -459,11 +460,10 @@ __device__ __forceinline__ void window_feed(const WindowCtx& x, uint32_t bar0, c
     };
     uint32_t g = 0;  // key tiles of this block so far (modulo 2^32); K of tile g is ring entry 2 g, V 2 g + 1
     bool ok = true;
-    for (int r = kSecond ? x.again(0) : 0, item; ok && (!kSecond || r <= x.again(1)) && (item = window_entry(r)) < p.items; ++r) {
+    for (int r = from, item; ok && r <= to && (item = window_entry(r)) < p.items; ++r) {
       const WindowItem it = window_item(p, item);
       if (it.n == 0) continue;
       if (!(ok = pipe.wait_warp(bar(kWbQFull), n_q & 1u, kSiteWinMma))) break;
-      const WindowMasked masked(p.w, it);  // (second pass)
       ++n_q;
       if (!(ok = wait_kv(2 * g))) break;
 #pragma unroll
@@ -485,12 +485,7 @@ __device__ __forceinline__ void window_feed(const WindowCtx& x, uint32_t bar0, c
         }
         if (!(ok = wait_kv(2 * g + 1))) break;
         const int left = it.s.len - j * kTile;  // V rows of the sequence in this tile
-        if (kSecond) {
-          if (masked(j)) {
-            if (!(ok = pipe.wait_warp(bar(kWbVClean + n_clean % P::kVStages), (n_clean / P::kVStages) & 1u, kSiteWinMma))) break;
-            ++n_clean;
-          }
-        } else if (left < kTile && it.s.len < p.w.n_keys) {
+        if (left < kTile && it.s.len < p.w.n_keys) {
           const uint32_t v = base_s + P::kOffKv + (2 * g + 1) % S * P::kTileBytes;
           for (int kb = 0; kb < NKB; ++kb)
             for (int y = left * 8 + lane; y < kTile * 8; y += 32)
@@ -516,13 +511,11 @@ __device__ __forceinline__ void window_feed(const WindowCtx& x, uint32_t bar0, c
       }
     }
     commit(kWbMmaDone);
-  } else if (kSecond && warp == 3) {
-    // ------------------------------- V of partly masked tiles cleaned
-    // The c-th of them arrives on barrier c % kVStages: the one before on that
-    // barrier has left its V stage by then.
-    uint32_t g = 0, n_clean = 0, n_items = 0;  // tiles so far, of these cleaned, items with tiles
+  } else if (second && warp == 3) {
+    // ------------------------ V tiles passed on, partly masked ones cleaned
+    uint32_t g = 0, n_items = 0;  // tiles, items with tiles so far
     bool ok = true;
-    for (int r = kSecond ? x.again(0) : 0, item; ok && (!kSecond || r <= x.again(1)) && (item = window_entry(r)) < p.items; ++r) {
+    for (int r = from, item; ok && r <= to && (item = window_entry(r)) < p.items; ++r) {
       const WindowItem it = window_item(p, item);
       if (it.n == 0) continue;
       const WindowMasked masked(p.w, it);
@@ -532,13 +525,13 @@ __device__ __forceinline__ void window_feed(const WindowCtx& x, uint32_t bar0, c
       uint32_t note = 0, nth = 0;
       for (int i = 0; i < it.n; ++i, ++g) {
         const uint32_t vs = g % P::kVStages, st = 2 * vs + 1;
-        if (!(ok = pipe.wait_warp(bar(kWbKvFull + st), (g / P::kVStages) & 1u, kSiteWinClean))) break;
+        if (!(ok = pipe.wait_warp(bar(kWbVLanded + vs), (g / P::kVStages) & 1u, kSiteWinClean))) break;
         const int j = it.tile(i);
-        if (!masked(j)) continue;
-        if (window_clean_v<T, NKB>(base_s + P::kOffKv + st * P::kTileBytes, it.s.len - j * kTile)) note |= 1u << nth;
-        ++nth;
-        pipe_warp_arrive(bar(kWbVClean + n_clean % P::kVStages));
-        ++n_clean;
+        if (masked(j)) {
+          if (window_clean_v<T, NKB>(base_s + P::kOffKv + st * P::kTileBytes, it.s.len - j * kTile)) note |= 1u << nth;
+          ++nth;
+        }
+        pipe_warp_arrive(bar(kWbKvFull + st));
       }
       if (lane == 0) ptx::st_shared_volatile(x.note_at(slot), note);
       pipe_warp_arrive(bar(kWbNotes + slot));
@@ -762,7 +755,7 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
       }
       init(kWbMmaDone, 1);
     }
-    for (uint32_t i = kWbVClean; i < kWbSecondCount; ++i)
+    for (uint32_t i = kWbVLanded; i < kWbSecondCount; ++i)
       ptx::mbar_init(bar0 + 8u * (kWbCount + i), i >= kWbNotesFree ? 8 : 1);
     pipe.init(p.w, p.status);
     ptx::st_shared_volatile(pipe.at + kPipeBytes, 0x7fffffffu);  // rounds of the second pass: none
@@ -786,8 +779,8 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
   bool two = false;
   if (warp < 4) {
     ptx::regs_decrease<P::kRegsOther>();
-    window_feed<T, NKB, false>(x, bar0, tm_q, tm_k, tm_v);
-    if ((two = x.second())) window_feed<T, NKB, true>(x, bar0 + 8u * kWbCount, tm_q, tm_k, tm_v);
+    for (int pass = 0; pass == 0 || (pass == 1 && (two = x.second())); ++pass)
+      window_feed<T, NKB>(x, pass != 0, bar0 + (pass != 0 ? 8u * kWbCount : 0u), tm_q, tm_k, tm_v);
   } else {
     ptx::regs_increase<P::kRegsSoftmax>();
     window_soft<T, NKB, false>(x, bar0, tm_o);
