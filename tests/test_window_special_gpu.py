@@ -43,6 +43,8 @@ CASES = [
     ("bf16", (1, 2, 2, 384, 384, 32), 128, 128, None, None),               # every border on a tile's
     ("f16", (1, 1, 1, 90, 260, 8), 70, 1, None, [-20]),
     ("bf16", (1, 40, 4, 900, 900, 64), 200, 0, None, None),                # more units than blocks
+    ("bf16", (2, 16, 4, 3000, 3000, 128), 500, 5, None, None),             # several rounds of items, some taken again
+    ("f16", (2, 18, 6, 2500, 2500, 64), None, 0, [2500, 1700], [0, 0]),
 ]
 
 
