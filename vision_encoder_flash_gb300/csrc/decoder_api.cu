@@ -650,9 +650,9 @@ vattn_status cached_launch(vattn::CachedParams p, int sms, int device, cudaStrea
   if (p.row_blocks > 65535 || seqs * p.rows > INT32_MAX)
     return fail(VATTN_ERR_UNSUPPORTED, "too many query rows");
   // Shares of the keys: as many blocks as are resident at a time (32 sequences
-  // x 8 key heads x 16385 keys of 128, lengths from 5.4 k: 218 us with two a
-  // head, 307 with one, 229 with five; a tree of 31 over 4096 keys: 21 us in one
-  // round, 27 in two), of 256 keys at least, or of 128 where that makes no more
+  // x 8 key heads x 16385 keys of 128, lengths from 5.4 k: with two a head 0.71 of
+  // the time with one, 0.95 of that with five, now 201 us; a tree of 31 over 4096
+  // keys: one round 0.78 of two, now 19.6 us), of 256 keys at least, or of 128 where that makes no more
   // than 32 shares (500 keys: 8.0 us against 10.6; 30000 keys: 12 us with 118
   // shares, 16 with 235).
   const long long most_keys = std::min<long long>(p.w.n_keys, static_cast<long long>(p.w.sinks) + p.w.window + p.w.n_queries);

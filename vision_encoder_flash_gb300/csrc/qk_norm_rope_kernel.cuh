@@ -27,10 +27,10 @@
 // reads what it asked for).  4 x 40 heads x 4096 x 128 bf16: 52.3 us, 6.4 TB/s (94
 // % of the measured copy rate), with two rows a thread in registers 74 us; its
 // gradient at 4 x 20 heads 46.0 us, 5.5 TB/s, weight sums included, from 105
-// us (48.3 with its two sums one after the other).  The arithmetic, in packed f32 pairs, is about 80 instructions for the
-// 64 bytes of a lane and row.  16 + 16 heads x 4100 x 72 f32, 32 bytes a lane and
-// row: 14.7 us, 5.1 TB/s, bound by its instructions (2.7 a cycle), with three
-// blocks a multiprocessor and groups of 16 lanes 15.9.
+// us (48.3 with its two sums one after the other).  The arithmetic, in packed f32
+// pairs, is about 80 instructions for the 64 bytes of a lane and row.  16 + 16 heads
+// x 4100 x 72 f32, 32 bytes a lane and row: 13.7 us, 5.5 TB/s, at 2.5 instructions a
+// cycle; with three blocks a multiprocessor and groups of 16 lanes 15.9 (2.7).
 #pragma once
 
 #include <cstdint>

@@ -62,8 +62,8 @@
 // head_dim 128 (keys; queries 1560) and half of that at 64, the arithmetic on
 // the pairs about 1100 a warpgroup, and S, G, P, D and the sums follow each
 // other through TMEM, where head_dim 128 leaves one pair of S and G.  2 x 16(4) x
-// 4096 x 64, window 1024, 4 first keys: 142 us, 531 TFLOP/s counted as 10 D flops
-// a visible pair, 743 with the products that are computed twice.
+// 4096 x 64, window 1024, 4 first keys: 140 us, 537 TFLOP/s counted as 10 D flops
+// a visible pair, 751 with the products that are computed twice.
 #pragma once
 
 #include "window_pipe.cuh"

@@ -14,11 +14,11 @@
 // Two products of 2 D flops and one exponential a pair: the tensor core needs
 // 65 cycles for each 128 x 128 x 16, the four warps of a unit about 1300 for the
 // exponentials of a tile pair, and the two are coupled tile by tile.  1 x 32(8)
-// x 2048 x 128 without a window 33.1 us, 1040 TFLOP/s on the visible pairs (54 %
-// of the measured rate); 1 x 8 x 8192 x 64 86 us, 797 TFLOP/s.  Under a window
+// x 2048 x 128 without a window 32.6 us, 1056 TFLOP/s on the visible pairs (55 %
+// of the measured rate); 1 x 8 x 8192 x 64 90.8 us, 755 TFLOP/s.  Under a window
 // the first and the last tile of a row block are half masked and the tile of the
-// first keys nearly all: 1 x 16(4) x 8192 x 128, window 1024, 4 first keys, 73.8
-// us, 877 TFLOP/s.
+// first keys nearly all: 1 x 16(4) x 8192 x 128, window 1024, 4 first keys, 71.3
+// us, 908 TFLOP/s.
 //
 //   warp 0   K and V tiles by TMA into a ring (K0 V0 K1 V1 ...)
 //   warp 2   the item's two Q tiles by TMA
@@ -40,18 +40,20 @@
 // tensors' type for the second product (relative 2^-9 / 2^-12 at most, and in f16
 // 2^-32 of the row's largest; the sum l takes them unrounded), as the product
 // needs; O is rescaled in TMEM only when a row's maximum grew by more than 2^8
-// (exact after the final 1 / l).  A masked score is -infinity by selection, so nothing that K holds
-// there gets through, and V rows behind the sequence are zeroed in shared memory
-// before the product.  Other masked V elements that are not finite would stay in
-// O as 0 x infinity.  A warp whose results are not finite although its weights
-// are looks whether such an element, in a partly masked tile, is hidden from one
-// of its rows (window_leak); if so the block takes its items from the first such
-// one to the last once more, with every partly masked V tile cleaned by warp 3
-// before its product, and what was taken out added to the O of the rows that see
-// it.  Both looks are at two to five tiles of an item, whatever its length: 16(4)
-// heads x 8192 x 128, window 1024, 78 us; with a NaN at a first key 123; with
-// nothing but NaN in V 514.  (Cleaning in the only pass: clean calls 4 to 19 %
-// slower, by the look itself and by the registers that it takes from the softmax.)
+// (exact after the final 1 / l).  A masked score is -infinity by selection, so
+// nothing that K holds there gets through, and V rows behind the sequence are
+// zeroed in shared memory before the product.
+//
+// Other masked V elements that are not finite would stay in O as 0 x infinity.  A
+// warp whose results are not finite although its weights are looks whether such
+// an element, in a partly masked tile, is hidden from one of its rows
+// (window_leak); if so the block takes its items from the first such one to the
+// last once more, with every partly masked V tile cleaned by warp 3 before its
+// product, and what was taken out added to the O of the rows that see it.  Both
+// looks are at two to five tiles of an item, whatever its length: 16(4) heads x 8192
+// x 128, window 1024, as calls 77 us; with a NaN at a first key 122; with nothing
+// but NaN in V 513.  (Cleaning in the only pass: clean calls 4 to 19 % slower, by
+// the look itself and by the registers that it takes from the softmax.)
 #pragma once
 
 #include "window_pipe.cuh"
