@@ -19,7 +19,8 @@ DEPS = SOURCES + [os.path.join(CSRC, "attn_kernel.cuh"), os.path.join(CSRC, "sta
                   os.path.join(CSRC, "rope_kernel.cuh"),
                   os.path.join(CSRC, "conv1d_kernel.cuh"),
                   os.path.join(CSRC, "ptx.cuh"),
-                  os.path.join(CSRC, "host_common.h"), os.path.join(CSRC, "elem.cuh"),
+                  os.path.join(CSRC, "host_common.h"), os.path.join(CSRC, "rows_host.h"),
+                  os.path.join(CSRC, "elem.cuh"),
                   os.path.join(CSRC, "rope_turns.h"),
                   os.path.join(CSRC, "qk_norm_rope_kernel.cuh"),
                   os.path.join(CSRC, "window_common.cuh"),
