@@ -4,7 +4,9 @@
 f32 tensors of shape ``[batch, n_heads, n_patches, head_dim]`` (q already
 scaled by the caller), through the C ABI of ``libvattn.so`` (include/vattn.h).
 The calls of a decoder layer (norm and rotation of q and k, causal attention
-under a window with its gradients, attention over a cache) are in decoder.py.
+under a window with its gradients, attention over a cache) are in decoder.py,
+those of a server of many requests (packed prompts, a paged 8-bit cache) in
+serving.py.
 This module only marshals arguments: every step of the computation runs in
 the library's CUDA kernel.  There is no CPU fallback; if the library is
 missing or no GPU is present the calls raise.
@@ -18,10 +20,12 @@ from ._lib import (VattnError, _check, conv1d_step_status, device_status, export
                    load_library, rope_neox_status, status_string, version)
 from .decoder import (backward_window, forward_cached, forward_window, qk_norm_rope,
                       qk_norm_rope_backward)
+from .serving import append_paged, forward_packed, forward_paged
 
 __all__ = ["forward", "forward_accurate", "conv1d_step", "forward_f16", "forward_f16io",
            "forward_f32q", "forward_rope", "rope_neox", "qk_norm_rope", "qk_norm_rope_backward",
-           "forward_window", "backward_window", "forward_cached", "forward_raw",
+           "forward_window", "backward_window", "forward_cached",
+           "forward_packed", "append_paged", "forward_paged", "forward_raw",
            "forward_f16_raw", "forward_f32q_raw", "forward_noalloc_raw",
            "device_status", "VattnError", "load_library",
            "lib_path", "exported_symbols", "status_string", "version"]

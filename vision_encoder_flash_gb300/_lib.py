@@ -9,6 +9,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_PKG)
 HEADER = os.path.join(_ROOT, "include", "vattn.h")
 DECODER_HEADER = os.path.join(_ROOT, "include", "vattn_decoder.h")
+SERVING_HEADER = os.path.join(_ROOT, "include", "vattn_serving.h")
 
 _STATUS = {0: "VATTN_OK", 1: "VATTN_ERR_INVALID_ARG", 2: "VATTN_ERR_UNSUPPORTED",
            3: "VATTN_ERR_MISALIGNED", 4: "VATTN_ERR_CUDA", 5: "VATTN_ERR_DEVICE_TIMEOUT"}
@@ -92,6 +93,13 @@ def load_library():
     lib.vattn_backward_window.restype = ctypes.c_int
     lib.vattn_forward_cached.argtypes = [cp, cp, cp, cp, cp, vp]
     lib.vattn_forward_cached.restype = ctypes.c_int
+    # packed prompts and the paged cache, see serving.py
+    lib.vattn_append_paged.argtypes = [cp, cp, cp, cp, vp]
+    lib.vattn_append_paged.restype = ctypes.c_int
+    lib.vattn_forward_paged.argtypes = [cp, cp, cp, cp, vp]
+    lib.vattn_forward_paged.restype = ctypes.c_int
+    lib.vattn_forward_packed.argtypes = [cp, cp, cp, cp, vp, vp, i64, cp, vp]
+    lib.vattn_forward_packed.restype = ctypes.c_int
     _LIB = lib
     return lib
 

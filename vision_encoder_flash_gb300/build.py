@@ -1,6 +1,6 @@
 """Build ``libvattn.so`` (the C-ABI library) in-tree with nvcc for sm_103a.
 
-Two translation units compiled in parallel, one ``-gencode`` (compute_103a -> sm_103a), CUDA
+Three translation units compiled in parallel, one ``-gencode`` (compute_103a -> sm_103a), CUDA
 runtime linked statically so the library loads on hosts without a GPU
 driver (the tests check its exported symbols there).
 """
@@ -14,21 +14,24 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-SOURCES = [os.path.join(CSRC, "vattn_api.cu"), os.path.join(CSRC, "decoder_api.cu")]
+SOURCES = [os.path.join(CSRC, name) for name in ("vattn_api.cu", "decoder_api.cu", "serving_api.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, "attn_kernel.cuh"), os.path.join(CSRC, "stage_kernel.cuh"),
                   os.path.join(CSRC, "rope_kernel.cuh"),
                   os.path.join(CSRC, "conv1d_kernel.cuh"),
                   os.path.join(CSRC, "ptx.cuh"),
-                  os.path.join(CSRC, "host_common.h"), os.path.join(CSRC, "rows_host.h"),
+                  os.path.join(CSRC, "host_common.h"), os.path.join(CSRC, "rows_host.h"), os.path.join(CSRC, "window_host.h"),
                   os.path.join(CSRC, "elem.cuh"),
                   os.path.join(CSRC, "rope_turns.h"),
                   os.path.join(CSRC, "qk_norm_rope_kernel.cuh"),
                   os.path.join(CSRC, "window_common.cuh"),
                   os.path.join(CSRC, "window_pipe.cuh"), os.path.join(CSRC, "window_fwd_kernel.cuh"),
                   os.path.join(CSRC, "window_bwd_kernel.cuh"),
-                  os.path.join(CSRC, "cached_kernel.cuh"),
+                  os.path.join(CSRC, "cached_kernel.cuh"), os.path.join(CSRC, "rope_rows.cuh"),
+                  os.path.join(CSRC, "e4m3.cuh"), os.path.join(CSRC, "paged_append_kernel.cuh"),
+                  os.path.join(CSRC, "paged_kernel.cuh"), os.path.join(CSRC, "packed_list_kernel.cuh"),
                   os.path.join(ROOT, "include", "vattn.h"),
-                  os.path.join(ROOT, "include", "vattn_decoder.h")]
+                  os.path.join(ROOT, "include", "vattn_decoder.h"),
+                  os.path.join(ROOT, "include", "vattn_serving.h")]
 LIB = os.path.join(PKG, "libvattn.so")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 

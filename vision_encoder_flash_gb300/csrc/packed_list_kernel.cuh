@@ -1,0 +1,82 @@
+// packed_list_kernel.cuh -- the work list of attention over packed prompts
+// (vattn_forward_packed).
+//
+// The windowed forward kernel takes pairs of units (128 query rows of one head) of
+// one sequence, longest first.  With lengths on the device, one block writes
+// them down: a pair counts for the last row block that it holds, which its key
+// tiles follow, a counting sort puts the pairs of late row blocks first, and
+// pairs of one row block come in any order (no result depends on it).
+#pragma once
+
+#include "window_pipe.cuh"
+
+namespace vattn {
+
+constexpr int kListThreads = 1024;
+constexpr int kListBuckets = 8192;  // counts in shared memory up to here (2^20 rows), else in the workspace
+
+struct PackedListParams {
+  const int32_t* cu;
+  int n_seqs, total;
+  int group, kv_heads, sms;
+  int buckets;  // row blocks of the longest sequence there can be
+  int cap;      // pairs that the list has room for: enough where cu ascends
+  int* counts;  // [buckets] or null: shared memory
+  int4* list;   // {items, whole, 0, 0}, then {first row, rows, pair, 0} each
+};
+
+__global__ void __launch_bounds__(kListThreads) vattn_packed_list_kernel(const __grid_constant__ PackedListParams p) {
+  __shared__ int counts_s[kListBuckets];
+  __shared__ int warps_s[kListThreads / 32];
+  ptx::grid_dep_launch();  // the attention kernel sets itself up meanwhile, and waits for this one's end
+  const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  int* const counts = p.counts != nullptr ? p.counts : counts_s;
+  for (int i = tid; i < p.buckets; i += kListThreads) counts[i] = 0;
+  __syncthreads();
+  auto each = [&](auto&& take) {  // (first row, rows, pair, its last row block)
+    for (int b = warp; b < p.n_seqs; b += kListThreads / 32) {
+      const int first = min(max(p.cu[b], 0), p.total), rows = min(max(p.cu[b + 1], 0), p.total) - first;
+      if (rows <= 0) continue;
+      const int blocks = (rows + kTile - 1) / kTile;
+      const long long pairs = (static_cast<long long>(blocks) * p.group + 1) / 2;
+      for (long long i = lane; i < pairs; i += 32)
+        take(first, rows, static_cast<int>(i), min(blocks - 1, static_cast<int>((2 * i + 1) / p.group)));
+    }
+  };
+  each([&](int, int, int, int block) { atomicAdd(&counts[block], 1); });
+  __syncthreads();
+  // counts to places: behind the pairs of all later row blocks
+  const int per = (p.buckets + kListThreads - 1) / kListThreads;
+  int sum = 0;
+  for (int i = tid * per; i < min(p.buckets, (tid + 1) * per); ++i) sum += counts[p.buckets - 1 - i];
+  int upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 31) warps_s[warp] = upto;
+  __syncthreads();
+  int before = upto - sum, all = 0;
+  for (int i = 0; i < kListThreads / 32; ++i) {
+    if (i < warp) before += warps_s[i];
+    all += warps_s[i];
+  }
+  for (int i = tid * per; i < min(p.buckets, (tid + 1) * per); ++i) {
+    const int n = counts[p.buckets - 1 - i];
+    counts[p.buckets - 1 - i] = before;
+    before += n;
+  }
+  __syncthreads();
+  each([&](int first, int rows, int pair, int block) {
+    const int at = atomicAdd(&counts[block], 1);
+    if (at < p.cap) p.list[1 + at] = make_int4(first, rows, pair, 0);
+  });
+  if (tid == 0) {
+    const int items = min(all, p.cap) * p.kv_heads;
+    const bool single = 2 * items <= p.sms;  // every unit an item of its own, as forward_window does
+    p.list[0] = make_int4(single ? 2 * items : items, single ? 0 : items, 0, 0);
+  }
+}
+
+}  // namespace vattn

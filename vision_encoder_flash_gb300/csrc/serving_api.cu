@@ -1,0 +1,442 @@
+// serving_api.cu -- the C ABI declared in include/vattn_serving.h: argument
+// checks, variant choice and launches of the calls on packed prompts and the
+// paged cache on sm_103a.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/vattn_serving.h"
+#include "packed_list_kernel.cuh"
+#include "paged_append_kernel.cuh"
+#include "paged_kernel.cuh"
+#include "rope_turns.h"
+#include "window_fwd_kernel.cuh"
+#include "window_host.h"
+
+namespace {
+
+using namespace vattn::host;
+
+vattn::FastDiv fast_div(int64_t d) { return vattn::FastDiv::make(static_cast<uint32_t>(std::max<int64_t>(1, d))); }
+
+// ------------------------------------------------------------ the cache
+// The two pools of a cache as tensors [n_pages, heads, page_size, head_dim] of bytes.
+struct Pools {
+  vattn_rows k_rows, v_rows;
+  Tensor k, v;
+  Pools(const vattn_pages* c, int64_t heads, int64_t dim)
+      : k_rows{c->k, {c->k_stride[0], c->k_stride[1], c->k_stride[2]}},
+        v_rows{c->v, {c->v_stride[0], c->v_stride[1], c->v_stride[2]}},
+        k{"k pages", &k_rows, {c->n_pages, heads, c->page_size}, dim, 1, true},
+        v{"v pages", &v_rows, {c->n_pages, heads, c->page_size}, dim, 1, true} {}
+  Pools(const Pools&) = delete;
+};
+
+vattn_status check_pages(const vattn_pages* c, const Pools& pools, int64_t batch, int64_t heads) {
+  if (c->n_pages < 0 || c->n_pages >= INT32_MAX)
+    return fail(VATTN_ERR_INVALID_ARG, "n_pages %lld outside [0, 2^31 - 1)", (long long)c->n_pages);
+  if (c->page_size < 16 || c->page_size > 1024 || c->page_size % 16 != 0)
+    return fail(VATTN_ERR_UNSUPPORTED, "page_size %lld: a multiple of 16 from 16 to 1024 is needed",
+                (long long)c->page_size);
+  if (c->max_pages < 0 || c->max_pages > kMaxKeys / c->page_size)
+    return fail(VATTN_ERR_UNSUPPORTED, "max_pages * page_size must stay below 2^29");
+  vattn_status st;
+  if ((st = check_tensor(pools.k, 16)) != VATTN_OK || (st = check_tensor(pools.v, 16)) != VATTN_OK ||
+      (st = check_apart(pools.k, pools.v)) != VATTN_OK)
+    return st;
+  const uint64_t bytes = static_cast<uint64_t>(c->n_pages) * static_cast<uint64_t>(heads) * 4u;
+  const uintptr_t ks = reinterpret_cast<uintptr_t>(c->k_scale), vs = reinterpret_cast<uintptr_t>(c->v_scale);
+  if (bytes > 0) {
+    if (!c->k_scale || !c->v_scale) return fail(VATTN_ERR_INVALID_ARG, "null scales");
+    if ((ks | vs) & 3u) return fail(VATTN_ERR_MISALIGNED, "scales must be 4-byte aligned");
+    if (ks < vs + bytes && vs < ks + bytes) return fail(VATTN_ERR_INVALID_ARG, "k_scale overlaps v_scale");
+    for (const Tensor* t : {&pools.k, &pools.v})
+      if ((st = check_apart_bytes(c->k_scale, bytes, "k_scale", *t)) != VATTN_OK ||
+          (st = check_apart_bytes(c->v_scale, bytes, "v_scale", *t)) != VATTN_OK)
+        return st;
+  }
+  if (batch > 0 && !c->kv_len) return fail(VATTN_ERR_INVALID_ARG, "null kv_len");
+  if (batch > 0 && c->max_pages > 0 && !c->table) return fail(VATTN_ERR_INVALID_ARG, "null table");
+  if ((reinterpret_cast<uintptr_t>(c->kv_len) | reinterpret_cast<uintptr_t>(c->table)) & 3u)
+    return fail(VATTN_ERR_MISALIGNED, "kv_len and table must be 4-byte aligned");
+  return VATTN_OK;
+}
+
+// Tensor map {dim, rows of a page, heads, pages} of bytes with boxes of `cols`
+// columns (32, 64 or 128: swizzled as wide) x `box` rows; what is outside reads 0.
+vattn_status make_pages_map(CUtensorMap* tm, const Tensor& x, int cols, int box) {
+  EncodeTiledFn enc = nullptr;
+  const vattn_status st = tensor_map_encoder(&enc);
+  if (st != VATTN_OK) return st;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(x.dim), static_cast<cuuint64_t>(x.size[2]),
+                        static_cast<cuuint64_t>(x.size[1]), static_cast<cuuint64_t>(x.size[0])};
+  cuuint64_t strides[3];
+  const int order[3] = {2, 1, 0};
+  for (int i = 0; i < 3; ++i)
+    strides[i] = x.size[order[i]] <= 1 ? static_cast<cuuint64_t>(x.dim)
+                                       : static_cast<cuuint64_t>(x.t->stride[order[i]]);
+  const cuuint32_t boxes[4] = {static_cast<cuuint32_t>(cols), static_cast<cuuint32_t>(box), 1u, 1u};
+  const cuuint32_t steps[4] = {1u, 1u, 1u, 1u};
+  const CUresult r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, x.t->data, dims, strides, boxes, steps,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         cols == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                         : cols == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                      : CU_TENSOR_MAP_SWIZZLE_32B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(VATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed with CUresult %d", static_cast<int>(r));
+  return VATTN_OK;
+}
+
+// ------------------------------------------------------------ append
+vattn_status check_append(const vattn_append_args* a) {
+  if (a->batch < 0 || a->n_kv_heads < 0 || a->n_tokens < 0)
+    return fail(VATTN_ERR_INVALID_ARG, "negative size (batch=%lld n_kv_heads=%lld n_tokens=%lld)",
+                (long long)a->batch, (long long)a->n_kv_heads, (long long)a->n_tokens);
+  if (a->head_dim < 1) return fail(VATTN_ERR_INVALID_ARG, "head_dim must be >= 1");
+  if (a->head_dim > VATTN_MAX_HEAD_DIM || a->head_dim % 16 != 0)
+    return fail(VATTN_ERR_UNSUPPORTED, "head_dim %lld: a multiple of 16 up to %d is needed (16-byte rows)",
+                (long long)a->head_dim, VATTN_MAX_HEAD_DIM);
+  if (a->rope_dims < 0 || a->rope_dims > a->head_dim)
+    return fail(VATTN_ERR_INVALID_ARG, "rope_dims %lld outside [0, head_dim = %lld]", (long long)a->rope_dims,
+                (long long)a->head_dim);
+  if (!(a->base > 0.0) || !std::isfinite(a->base))
+    return fail(VATTN_ERR_INVALID_ARG, "base must be a finite positive number");
+  if (a->dtype != VATTN_F16 && a->dtype != VATTN_BF16)
+    return fail(VATTN_ERR_UNSUPPORTED, "dtype must be VATTN_F16 or VATTN_BF16");
+  if (a->batch > kMaxRows || a->n_kv_heads > kMaxRows || a->n_tokens > kMaxRows ||
+      (!a->cu_seqlens && a->batch * a->n_tokens > (int64_t{1} << 36)))
+    return fail(VATTN_ERR_UNSUPPORTED, "sizes must stay below 2^30 each, 2^36 tokens together");
+  if ((reinterpret_cast<uintptr_t>(a->cu_seqlens) | reinterpret_cast<uintptr_t>(a->positions) |
+       reinterpret_cast<uintptr_t>(a->factors)) & 3u)
+    return fail(VATTN_ERR_MISALIGNED, "cu_seqlens, positions and factors must be 4-byte aligned");
+  return VATTN_OK;
+}
+
+template <typename T, int V>
+vattn_status append_launch(const vattn::AppendParams& p, int64_t blocks, int threads, cudaStream_t stream) {
+  vattn::vattn_append_paged_kernel<T, V><<<static_cast<unsigned>(blocks), threads, 0, stream>>>(p);
+  return launched("cache append kernel launch");
+}
+
+// ------------------------------------------------------------ attention over the cache
+// Blocks of a kernel that a multiprocessor holds, asked once per device.
+template <typename K>
+vattn_status resident_blocks(K kernel, int threads, int smem, std::atomic<int>* known, int device, int* out) {
+  *out = known[device].load(std::memory_order_acquire);
+  if (*out > 0) return VATTN_OK;
+  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(out, kernel, threads, static_cast<size_t>(smem));
+  if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
+  *out = std::max(1, *out);
+  known[device].store(*out, std::memory_order_release);
+  return VATTN_OK;
+}
+
+template <typename T, int DP, int RW>
+vattn_status paged_launch(vattn::PagedParams p, const Pools& pools, int sms, int device, cudaStream_t stream) {
+  using P = vattn::PagedPlan<DP, RW>;
+  auto kernel = vattn::vattn_paged_kernel<T, DP, RW>;
+  static std::atomic<uint8_t> done[kMaxDevices];
+  static std::atomic<int> known[kMaxDevices];
+  vattn_status st = allow_smem(kernel, P::kSmemBytes, done, device);
+  if (st != VATTN_OK) return st;
+  int resident = 0;
+  if ((st = resident_blocks(kernel, P::kThreads, P::kSmemBytes, known, device, &resident)) != VATTN_OK) return st;
+  const long long seqs = static_cast<long long>(p.w.batch) * p.w.kv_heads;
+  p.row_blocks = (p.rows + 16 * RW - 1) / (16 * RW);
+  if (seqs * p.row_blocks > kMaxRows || seqs * p.rows > INT32_MAX)
+    return fail(VATTN_ERR_UNSUPPORTED, "too many query rows");
+  // Shares of the keys, as forward_cached has them.
+  const long long most_keys = std::min<long long>(p.w.n_keys, static_cast<long long>(p.w.sinks) + p.w.window + p.w.n_queries);
+  const long long blocks = seqs * p.row_blocks, room = static_cast<long long>(resident) * sms;
+  const long long fill = room / blocks >= 4 ? room / blocks : (room + blocks - 1) / blocks;
+  const long long fine = std::max(std::min(32LL, (most_keys + 127) / 128), (most_keys + 255) / 256);
+  p.splits = static_cast<int>(std::max(1LL, std::min({fill, fine, static_cast<long long>(vattn::kCachedMaxSplits)})));
+  if (blocks * p.splits > kMaxRows) p.splits = 1;
+  p.d_splits = fast_div(p.splits);
+  p.d_row_blocks = fast_div(p.row_blocks);
+  Workspace ws;
+  const bool clustered = p.splits > 1 && p.splits <= vattn::kCachedCluster;
+  if (p.splits > 1 && !clustered) {
+    const size_t rows = static_cast<size_t>(blocks) * p.splits * 16 * RW;
+    if ((st = ws.take(rows * (p.w.dim + 2) * 4, device, stream)) != VATTN_OK) return st;
+    p.part_o = reinterpret_cast<float*>(ws.data());
+    p.part_ml = p.part_o + rows * p.w.dim;
+  }
+  CUtensorMap tk, tv;
+  if (pools.k.empty()) {  // no box is ever loaded: any valid map does
+    vattn_rows any{const_cast<void*>(p.q.p), {0, 0, 0}};
+    const Tensor t{"q", &any, {1, 1, 1}, p.w.dim, 1, false};
+    if ((st = make_pages_map(&tk, t, DP, p.box)) != VATTN_OK) return st;
+    tv = tk;
+  } else if ((st = make_pages_map(&tk, pools.k, DP, p.box)) != VATTN_OK ||
+             (st = make_pages_map(&tv, pools.v, DP, p.box)) != VATTN_OK) {
+    return st;
+  }
+  const dim3 grid(static_cast<unsigned>(blocks * p.splits));
+  if (clustered) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(P::kThreads);
+    cfg.dynamicSmemBytes = P::kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(p.splits);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tk, tv, p);
+    return e == cudaSuccess ? VATTN_OK : cuda_fail(e, "paged attention kernel launch");
+  }
+  kernel<<<grid, P::kThreads, P::kSmemBytes, stream>>>(tk, tv, p);
+  if ((st = launched("paged attention kernel launch")) != VATTN_OK) return st;
+  if (p.splits == 1) return VATTN_OK;
+  if ((st = launch_behind("paged attention join kernel launch", vattn::vattn_paged_join_kernel<T, RW>,
+                          dim3(static_cast<unsigned>(seqs * p.rows)), dim3(128), 0, stream, p)) != VATTN_OK)
+    return st;
+  return ws.release();
+}
+
+template <typename T, int DP>
+vattn_status paged_rows(const vattn::PagedParams& p, const Pools& pools, int sms, int device, cudaStream_t stream) {
+  if (p.rows <= 16) return paged_launch<T, DP, 1>(p, pools, sms, device, stream);
+  if (p.rows <= 32) return paged_launch<T, DP, 2>(p, pools, sms, device, stream);
+  return paged_launch<T, DP, 4>(p, pools, sms, device, stream);
+}
+
+template <typename T>
+vattn_status paged_dispatch(const vattn::PagedParams& p, const Pools& pools, int sms, int device, cudaStream_t stream) {
+  if (p.w.dim <= 32) return paged_rows<T, 32>(p, pools, sms, device, stream);
+  if (p.w.dim <= 64) return paged_rows<T, 64>(p, pools, sms, device, stream);
+  return paged_rows<T, 128>(p, pools, sms, device, stream);
+}
+
+// ------------------------------------------------------------ packed prompts
+template <typename T, int NKB>
+vattn_status packed_launch(const CUtensorMap (&tm)[4], const vattn::WindowFwdParams& p, int64_t items, int sms, int device,
+                           cudaStream_t stream) {
+  using P = vattn::WindowFwdPlan<NKB>;
+  auto kernel = vattn::vattn_window_fwd_kernel<T, NKB, true>;
+  static std::atomic<uint8_t> done[kMaxDevices];
+  const vattn_status st = allow_smem(kernel, P::kSmemBytes, done, device);
+  if (st != VATTN_OK) return st;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, sms));
+  return launch_behind("packed attention kernel launch", kernel, dim3(grid), dim3(P::kThreads), P::kSmemBytes, stream,
+                       tm[0], tm[1], tm[2], tm[3], p);
+}
+
+}  // namespace
+
+extern "C" {
+
+vattn_status vattn_append_paged(const vattn_rows* k, const vattn_rows* v, const vattn_pages* cache,
+                                const vattn_append_args* a, void* stream_ptr) {
+  clear_error();
+  if (!a || !cache) return fail(VATTN_ERR_INVALID_ARG, "null args or cache");
+  vattn_status st = check_append(a);
+  if (st != VATTN_OK) return st;
+  const Pools pools(cache, a->n_kv_heads, a->head_dim);
+  if ((st = check_pages(cache, pools, a->batch, a->n_kv_heads)) != VATTN_OK) return st;
+  const int64_t batch = a->cu_seqlens ? std::min<int64_t>(1, a->batch) : a->batch;
+  const Tensor tk{"k", k, {batch, a->n_kv_heads, a->n_tokens}, a->head_dim, 2, false},
+      tv{"v", v, {batch, a->n_kv_heads, a->n_tokens}, a->head_dim, 2, false};
+  const uint64_t scale_bytes = static_cast<uint64_t>(cache->n_pages) * static_cast<uint64_t>(a->n_kv_heads) * 4u;
+  for (const Tensor* t : {&tk, &tv}) {
+    if ((st = check_tensor(*t, 2)) != VATTN_OK || (st = check_apart(pools.k, *t)) != VATTN_OK ||
+        (st = check_apart(pools.v, *t)) != VATTN_OK ||
+        (st = check_apart_bytes(cache->k_scale, scale_bytes, "k_scale", *t)) != VATTN_OK ||
+        (st = check_apart_bytes(cache->v_scale, scale_bytes, "v_scale", *t)) != VATTN_OK)
+      return st;
+  }
+  if (tk.empty() || cache->n_pages == 0 || cache->max_pages == 0) return VATTN_OK;
+
+  vattn::AppendParams p{};
+  p.x[0] = rows_tensor(k);
+  p.x[1] = rows_tensor(v);
+  p.pool[0] = static_cast<uint8_t*>(cache->k);
+  p.pool[1] = static_cast<uint8_t*>(cache->v);
+  for (int i = 0; i < 3; ++i) {
+    p.ps[0][i] = cache->k_stride[i];
+    p.ps[1][i] = cache->v_stride[i];
+  }
+  p.scale[0] = cache->k_scale;
+  p.scale[1] = cache->v_scale;
+  p.table = cache->table;
+  p.kv_len = cache->kv_len;
+  p.cu = a->cu_seqlens;
+  p.positions = a->positions;
+  p.factors = a->factors;
+  p.n_pages = cache->n_pages;
+  p.batch = static_cast<int>(a->batch);
+  p.heads = static_cast<int>(a->n_kv_heads);
+  p.n_tokens = static_cast<int>(a->n_tokens);
+  p.page = static_cast<int>(cache->page_size);
+  p.max_pages = static_cast<int>(cache->max_pages);
+  p.D = static_cast<int>(a->head_dim);
+  p.half = static_cast<int>(a->rope_dims / 2);
+  rope_turns(a->base, static_cast<int>(a->rope_dims), p.turns, p.turns_rest);
+  // 16-byte accesses where the rotated halves and the rest are cut evenly by them
+  bool wide = p.half % 8 == 0 && (p.D - 2 * p.half) % 16 == 0;
+  for (const Tensor* t : {&tk, &tv}) {
+    wide = wide && t->base() % 16 == 0;
+    for (int i = 0; i < 3; ++i) wide = wide && (t->size[i] <= 1 || t->t->stride[i] % 8 == 0);
+  }
+  p.slots = p.D / (wide ? 16 : 2);
+  // pages that n rows in a row can touch: one for the first, and for the others as if the next began
+  p.items = p.n_tokens <= 1 ? 1 : (p.n_tokens - 2) / p.page + 2;
+  const int64_t items = a->cu_seqlens ? a->n_tokens / p.page + 2 * a->batch : a->batch * p.items;
+  const int64_t blocks = items * p.heads * 2;
+  if (items > kMaxRows || blocks > INT32_MAX) return fail(VATTN_ERR_UNSUPPORTED, "too many pages and heads");
+  p.d_heads = fast_div(p.heads);
+  p.d_items = fast_div(p.items);
+  p.d_page = fast_div(p.page);
+  p.d_slots = fast_div(p.slots);
+  const int slots = std::min(p.page, p.n_tokens) * p.slots;
+  const int threads = std::min(vattn::kAppendThreads,
+                               (slots + 32 * vattn::kAppendHold - 1) / (32 * vattn::kAppendHold) * 32);
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  if (a->dtype == VATTN_F16)
+    return wide ? append_launch<__half, 8>(p, blocks, threads, stream) : append_launch<__half, 1>(p, blocks, threads, stream);
+  return wide ? append_launch<__nv_bfloat16, 8>(p, blocks, threads, stream)
+              : append_launch<__nv_bfloat16, 1>(p, blocks, threads, stream);
+}
+
+vattn_status vattn_forward_paged(const vattn_rows* q, const vattn_pages* cache, const vattn_rows* out,
+                                 const vattn_window_args* args, void* stream_ptr) {
+  clear_error();
+  if (!args || !cache) return fail(VATTN_ERR_INVALID_ARG, "null args or cache");
+  if (args->kv_len || args->q_start)
+    return fail(VATTN_ERR_INVALID_ARG, "kv_len is the cache's, and new tokens end the sequence: args' must be null");
+  vattn_window_args with = *args;
+  with.n_keys = 0;
+  vattn_status st = check_window_args(&with);
+  if (st != VATTN_OK) return st;
+  if (with.n_queries > VATTN_MAX_NEW_TOKENS)
+    return fail(VATTN_ERR_UNSUPPORTED, "%lld new tokens > %d", (long long)with.n_queries, VATTN_MAX_NEW_TOKENS);
+  if (with.head_dim % 16 != 0)
+    return fail(VATTN_ERR_UNSUPPORTED, "head_dim %lld: a multiple of 16 is needed (16-byte rows)", (long long)with.head_dim);
+  const Pools pools(cache, with.n_kv_heads, with.head_dim);
+  if ((st = check_pages(cache, pools, with.batch, with.n_kv_heads)) != VATTN_OK) return st;
+  with.n_keys = cache->max_pages * cache->page_size;
+  with.kv_len = cache->kv_len;
+  const vattn_window_args* a = &with;
+  const Tensor tq = window_tensor("q", q, a, true, false), to = window_tensor("out", out, a, true, true);
+  if ((st = check_tensor(tq, 16)) != VATTN_OK || (st = check_tensor(to, 16)) != VATTN_OK ||
+      (st = check_apart(to, tq)) != VATTN_OK || (st = check_apart(to, pools.k)) != VATTN_OK ||
+      (st = check_apart(to, pools.v)) != VATTN_OK)
+    return st;
+  const uint64_t scale_bytes = static_cast<uint64_t>(cache->n_pages) * static_cast<uint64_t>(a->n_kv_heads) * 4u;
+  if ((st = check_apart_bytes(cache->k_scale, scale_bytes, "k_scale", to)) != VATTN_OK ||
+      (st = check_apart_bytes(cache->v_scale, scale_bytes, "v_scale", to)) != VATTN_OK)
+    return st;
+  if (tq.empty()) return VATTN_OK;
+  if (a->n_q_heads / a->n_kv_heads > INT32_MAX / VATTN_MAX_NEW_TOKENS / 2)
+    return fail(VATTN_ERR_UNSUPPORTED, "too many query heads for one key head");
+  int device = 0, sms = 0;
+  if ((st = current_device(&device)) != VATTN_OK) return st;
+  if ((st = sm_count(device, &sms)) != VATTN_OK) return st;
+  vattn::PagedParams p{};
+  p.w = window_params(a);
+  if ((st = status_word(device, &p.status)) != VATTN_OK) return st;
+  p.q = rows_tensor(q);
+  p.out = rows_tensor(out);
+  p.k_scale = cache->k_scale;
+  p.v_scale = cache->v_scale;
+  p.table = cache->table;
+  p.n_pages = cache->n_pages;
+  p.max_pages = static_cast<int>(cache->max_pages);
+  p.page = static_cast<int>(cache->page_size);
+  p.log_box = p.page % 64 == 0 ? 6 : (p.page % 32 == 0 ? 5 : 4);
+  p.box = 1 << p.log_box;
+  p.rows = p.w.group * p.w.n_queries;
+  p.scale_log2 = a->scale * vattn::kLog2E;
+  p.d_page = fast_div(p.page);
+  p.d_kv_heads = fast_div(p.w.kv_heads);
+  p.d_group = fast_div(p.w.group);
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  return a->dtype == VATTN_F16 ? paged_dispatch<__half>(p, pools, sms, device, stream)
+                               : paged_dispatch<__nv_bfloat16>(p, pools, sms, device, stream);
+}
+
+vattn_status vattn_forward_packed(const vattn_rows* q, const vattn_rows* k, const vattn_rows* v, const vattn_rows* out,
+                                  float* lse, const int32_t* cu_seqlens, int64_t n_seqs, const vattn_window_args* a,
+                                  void* stream_ptr) {
+  clear_error();
+  vattn_status st = check_window_args(a);
+  if (st != VATTN_OK) return st;
+  if (a->kv_len || a->q_start || a->tree)
+    return fail(VATTN_ERR_INVALID_ARG, "kv_len, q_start and tree must be null: cu_seqlens says where sequences lie");
+  if (a->batch != 1 || a->n_keys != a->n_queries)
+    return fail(VATTN_ERR_INVALID_ARG, "packed prompts are one batch (is %lld) with as many keys (%lld) as queries (%lld)",
+                (long long)a->batch, (long long)a->n_keys, (long long)a->n_queries);
+  if (n_seqs < 0) return fail(VATTN_ERR_INVALID_ARG, "n_seqs must be >= 0");
+  if (n_seqs >= (int64_t{1} << 24)) return fail(VATTN_ERR_UNSUPPORTED, "n_seqs must stay below 2^24");
+  if (n_seqs > 0 && !cu_seqlens) return fail(VATTN_ERR_INVALID_ARG, "null cu_seqlens");
+  if (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) return fail(VATTN_ERR_MISALIGNED, "cu_seqlens must be 4-byte aligned");
+  if ((st = forward_checks(q, k, v, out, lse, a)) != VATTN_OK) return st;
+  const Tensor tq = window_tensor("q", q, a, true, false), tk = window_tensor("k", k, a, false, false),
+               tv = window_tensor("v", v, a, false, false), to = window_tensor("out", out, a, true, true);
+  for (const Tensor* t : {&tq, &tk, &tv})
+    if ((st = check_map_rows(*t)) != VATTN_OK) return st;
+  if (tq.empty() || n_seqs == 0) return VATTN_OK;
+
+  int device = 0, sms = 0;
+  if ((st = current_device(&device)) != VATTN_OK) return st;
+  if ((st = sm_count(device, &sms)) != VATTN_OK) return st;
+  vattn::WindowFwdParams p{};
+  p.w = window_params(a);
+  p.q = rows_tensor(q);
+  p.k = rows_tensor(k);
+  p.v = rows_tensor(v);
+  p.out = rows_tensor(out);
+  p.lse = lse;
+  if ((st = status_word(device, &p.status)) != VATTN_OK) return st;
+  // pairs: sequences of n rows have n / 128 row blocks and one more at most, their pairs half a unit more
+  const int64_t some = std::min(n_seqs, a->n_queries);
+  const int64_t cap = ((a->n_queries / vattn::kTile + some) * p.w.group + some) / 2 + 1;
+  if (cap > kMaxKeys / p.w.kv_heads) return fail(VATTN_ERR_UNSUPPORTED, "too many tiles of 128 rows");
+  p.kv_heads = fast_div(p.w.kv_heads);
+  p.group = fast_div(p.w.group);
+  p.scale_log2 = a->scale * vattn::kLog2E;
+  CUtensorMap tm[4];
+  if ((st = make_rows_map(&tm[0], &p.mq, tq, a->dtype, vattn::kTile)) != VATTN_OK ||
+      (st = make_rows_map(&tm[1], &p.mk, tk, a->dtype, vattn::kTile)) != VATTN_OK ||
+      (st = make_rows_map(&tm[2], &p.mv, tv, a->dtype, vattn::kTile)) != VATTN_OK ||
+      (st = make_rows_map(&tm[3], &p.mo, to, a->dtype, 32, 32)) != VATTN_OK)
+    return st;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  vattn::PackedListParams l{};
+  l.cu = cu_seqlens;
+  l.n_seqs = static_cast<int>(n_seqs);
+  l.total = static_cast<int>(a->n_queries);
+  l.group = p.w.group;
+  l.kv_heads = p.w.kv_heads;
+  l.sms = sms;
+  l.buckets = (l.total + vattn::kTile - 1) / vattn::kTile;
+  l.cap = static_cast<int>(cap);
+  const size_t list_bytes = static_cast<size_t>(1 + cap) * sizeof(int4);
+  const size_t count_bytes = l.buckets > vattn::kListBuckets ? static_cast<size_t>(l.buckets) * 4u : 0;
+  Workspace ws;
+  if ((st = ws.take(list_bytes + count_bytes, device, stream)) != VATTN_OK) return st;
+  l.list = reinterpret_cast<int4*>(ws.data());
+  if (count_bytes > 0) l.counts = reinterpret_cast<int*>(ws.data() + list_bytes);
+  p.list = l.list;
+  vattn::vattn_packed_list_kernel<<<1, vattn::kListThreads, 0, stream>>>(l);
+  if ((st = launched("packed list kernel launch")) != VATTN_OK) return st;
+  const int64_t items = 2 * cap * p.w.kv_heads;
+  if (a->dtype == VATTN_F16)
+    st = a->head_dim <= 64 ? packed_launch<__half, 1>(tm, p, items, sms, device, stream)
+                           : packed_launch<__half, 2>(tm, p, items, sms, device, stream);
+  else
+    st = a->head_dim <= 64 ? packed_launch<__nv_bfloat16, 1>(tm, p, items, sms, device, stream)
+                           : packed_launch<__nv_bfloat16, 2>(tm, p, items, sms, device, stream);
+  if (st != VATTN_OK) return st;
+  return ws.release();
+}
+
+}  // extern "C"

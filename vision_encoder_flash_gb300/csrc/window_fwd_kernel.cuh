@@ -70,6 +70,7 @@ struct WindowFwdParams {
   int units;           // ceil(n_queries / 128) * group
   int items;           // < 2^30
   int whole;           // items from here on are single units (none of them, or all)
+  const int4* list;    // packed prompts: {items, whole, 0, 0}, then the pairs (packed_list_kernel.cuh)
   FastDiv seqs, kv_heads, group;  // batch * kv_heads, kv_heads, group
   float scale_log2;    // scale * log2(e)
 };
@@ -81,10 +82,10 @@ struct UnitRange {
   __device__ __forceinline__ bool uses(int j) const { return j < ns || (j >= a && j <= b); }
 };
 
-__device__ __forceinline__ UnitRange unit_range(const WindowParams& w, const Seq& s, int row0) {
+__device__ __forceinline__ UnitRange unit_range(const WindowParams& w, const Seq& s, int row0, int rows) {
   UnitRange u{0, 0, -1};
   const int lo = max(0, s.start + row0);
-  const int hi = min(s.start + min(row0 + kTile, w.n_queries), s.len) - 1;
+  const int hi = min(s.start + min(row0 + kTile, rows), s.len) - 1;
   if (hi < lo) return u;
   u.a = max(0, lo - w.window + 1) / kTile;
   u.b = hi / kTile;
@@ -95,6 +96,7 @@ __device__ __forceinline__ UnitRange unit_range(const WindowParams& w, const Seq
 // One item: its two units and the tiles that either uses, in order.
 struct WindowItem {
   int b, kh;
+  int base, rows;  // first row of its sequence in the tensors, query rows of it
   int head[2], row0[2];
   bool on[2];
   UnitRange u[2];
@@ -112,25 +114,49 @@ __device__ __forceinline__ int window_entry(int r) {
   return r * grid + ((r & 1) ? grid - 1 - k : k);
 }
 
+// kPacked: prompts of different lengths in one buffer (vattn_forward_packed).  Two
+// consecutive units of one sequence are a pair of the list, late ones first, which
+// the list's kernel wrote; each makes an item of every key head.
+template <bool kPacked>
+__device__ __forceinline__ int window_items(const WindowFwdParams& p) {
+  return kPacked ? p.list[0].x : p.items;
+}
+
+template <bool kPacked>
 __device__ __forceinline__ WindowItem window_item(const WindowFwdParams& p, int entry) {
   WindowItem it;
   uint32_t bk, kh;
-  const bool pair_on = entry < p.whole;
-  const int item = pair_on ? entry : p.whole + (entry - p.whole) / 2, only = (entry - p.whole) & 1;
-  const int pair = p.pairs - 1 - static_cast<int>(p.seqs.div(static_cast<uint32_t>(item), &bk));
-  it.b = static_cast<int>(p.kv_heads.div(bk, &kh));
+  const int whole = kPacked ? p.list[0].y : p.whole;
+  const bool pair_on = entry < whole;
+  const int item = pair_on ? entry : whole + (entry - whole) / 2, only = (entry - whole) & 1;
+  int pair, units;
+  if constexpr (kPacked) {
+    const int4 x = p.list[1 + p.kv_heads.div(static_cast<uint32_t>(item), &kh)];
+    it.b = 0;
+    it.base = x.x;
+    it.rows = x.y;
+    it.s = Seq{x.y, 0};
+    pair = x.z;
+    units = (x.y + kTile - 1) / kTile * p.w.group;
+  } else {
+    pair = p.pairs - 1 - static_cast<int>(p.seqs.div(static_cast<uint32_t>(item), &bk));
+    it.b = static_cast<int>(p.kv_heads.div(bk, &kh));
+    it.base = 0;
+    it.rows = p.w.n_queries;
+    it.s = window_seq(p.w, it.b);
+    units = p.units;
+  }
   it.kh = static_cast<int>(kh);
-  it.s = window_seq(p.w, it.b);
   int last = -1, first = 0x7fffffff;
   it.first_n = 0;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int unit = 2 * pair + t;
     uint32_t g;
-    it.on[t] = unit < p.units && (pair_on || only == t);
+    it.on[t] = unit < units && (pair_on || only == t);
     it.row0[t] = static_cast<int>(p.group.div(static_cast<uint32_t>(unit), &g)) * kTile;
     it.head[t] = it.kh * p.w.group + static_cast<int>(g);
-    it.u[t] = it.on[t] ? unit_range(p.w, it.s, it.row0[t]) : UnitRange{0, 0, -1};
+    it.u[t] = it.on[t] ? unit_range(p.w, it.s, it.row0[t], it.rows) : UnitRange{0, 0, -1};
     if (!it.u[t].empty()) {
       it.first_n = max(it.first_n, it.u[t].ns);
       first = min(first, it.u[t].a);
@@ -212,7 +238,7 @@ struct WindowMasked {
   int full_first, full_last, sinks;
   __device__ __forceinline__ WindowMasked(const WindowParams& w, const WindowItem& it) : sinks(w.sinks) {
     const int lo = max(0, it.s.start + (it.on[0] ? it.row0[0] : it.row0[1]));
-    const int hi = min(it.s.start + min((it.on[1] ? it.row0[1] : it.row0[0]) + kTile, w.n_queries), it.s.len) - 1;
+    const int hi = min(it.s.start + min((it.on[1] ? it.row0[1] : it.row0[0]) + kTile, it.rows), it.s.len) - 1;
     full_last = (lo + 1) / kTile - 1;
     full_first = (max(0, hi - w.window + 1) + kTile - 1) / kTile;
   }
@@ -224,10 +250,10 @@ struct WindowMasked {
 // Keys of tile j that the thread's row of unit t sees, 32 a word.
 struct WindowSee {
   int pos;  // of the row; -1 where it sees nothing
-  __device__ __forceinline__ WindowSee(const WindowParams& w, const WindowItem& it, int t) {
+  __device__ __forceinline__ WindowSee(const WindowItem& it, int t) {
     const int row = (t == 0 ? it.row0[0] : it.row0[1]) + static_cast<int>(threadIdx.x & 127);
     const int at = it.s.start + row;
-    pos = row < w.n_queries && at >= 0 && at < it.s.len ? at : -1;
+    pos = row < it.rows && at >= 0 && at < it.s.len ? at : -1;
   }
   __device__ __forceinline__ uint32_t word(const WindowParams& w, int j, int c) const {
     const int k0 = j * kTile;
@@ -238,11 +264,11 @@ struct WindowSee {
 
 // Does V hold something that is not finite at a key which is hidden from one of
 // the warp's rows (unit t of an item), in a tile that the unit uses?
-template <typename T>
+template <typename T, bool kPacked>
 __device__ __noinline__ bool window_leak(const WindowFwdParams& p, int entry, int t) {
-  const WindowItem it = window_item(p, entry);
+  const WindowItem it = window_item<kPacked>(p, entry);
   const WindowMasked masked(p.w, it);
-  const WindowSee see(p.w, it, t);
+  const WindowSee see(it, t);
   const UnitRange u = t == 0 ? it.u[0] : it.u[1];
   const int lane = static_cast<int>(threadIdx.x) & 31, chunks = p.w.dim / 8;
   bool leak = false;
@@ -252,7 +278,7 @@ __device__ __noinline__ bool window_leak(const WindowFwdParams& p, int entry, in
     uint32_t hidden[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) hidden[c] = __reduce_or_sync(0xffffffffu, see.pos < 0 ? 0u : ~see.word(p.w, j, c));
-    const T* v = rows_at<T>(p.v, it.b, it.kh, j * kTile);
+    const T* v = rows_at<T>(p.v, it.b, it.kh, it.base + j * kTile);
     const int end = min(kTile, it.s.len - j * kTile) * chunks;
 #pragma unroll 8
     for (int i = lane; i < end; i += 32) {
@@ -291,13 +317,13 @@ __device__ __forceinline__ bool window_clean_v(uint32_t v, int left) {
 // What window_clean_v took out of the item's tiles, added to the O of unit t's
 // rows in TMEM (one warp, its 32 rows); bit i of `note`: the i-th partly masked
 // tile.  Every weight is positive, so an infinity stays what it is.
-template <typename T>
+template <typename T, bool kPacked>
 __device__ __noinline__ void window_add_back(const WindowFwdParams& p, int entry, int t, uint32_t note, uint32_t o_addr) {
   constexpr uint32_t kExp = Elem<T>::kBf16 ? 0x7f80u : 0x7c00u, kMan = Elem<T>::kBf16 ? 0x7fu : 0x3ffu;
   constexpr int kAhead = 8;
-  const WindowItem it = window_item(p, entry);
+  const WindowItem it = window_item<kPacked>(p, entry);
   const WindowMasked masked(p.w, it);
-  const WindowSee see(p.w, it, t);
+  const WindowSee see(it, t);
   const UnitRange u = t == 0 ? it.u[0] : it.u[1];
   const int lane = static_cast<int>(threadIdx.x) & 31, D = p.w.dim;
   // bit l of [e]: column 4 l + e gets +infinity, -infinity, NaN
@@ -306,7 +332,7 @@ __device__ __noinline__ void window_add_back(const WindowFwdParams& p, int entry
     const int j = it.tile(x);
     if (!masked(j)) continue;
     if (((note >> nth++) & 1u) == 0 || !u.uses(j)) continue;
-    const T* v = rows_at<T>(p.v, it.b, it.kh, j * kTile);
+    const T* v = rows_at<T>(p.v, it.b, it.kh, it.base + j * kTile);
     const int rows = min(kTile, it.s.len - j * kTile);
     for (int r0 = 0; r0 < rows; r0 += kAhead) {
       uint2 y[kAhead];
@@ -352,7 +378,7 @@ __device__ __noinline__ void window_add_back(const WindowFwdParams& p, int entry
 // Warps 0 to 3: loads, matrix products, and in the second pass clean V tiles.
 // One code for both passes: a second instance, though never run, made calls
 // between other kernels 6 to 8 us slower.
-template <typename T, int NKB>
+template <typename T, int NKB, bool kPacked>
 __device__ __forceinline__ void window_feed(const WindowCtx& x, bool second, uint32_t bar0, const CUtensorMap& tm_q,
                                             const CUtensorMap& tm_k, const CUtensorMap& tm_v) {
   using P = WindowFwdPlan<NKB>;
@@ -363,6 +389,7 @@ __device__ __forceinline__ void window_feed(const WindowCtx& x, bool second, uin
   const int warp = x.warp, lane = x.lane;
   auto bar = [bar0](uint32_t i) -> uint32_t { return bar0 + 8u * i; };
   const int from = second ? x.again(0) : 0, to = second ? x.again(1) : 0x7fffffff;
+  const int items = window_items<kPacked>(p);
   if (warp == 0 && lane == 0) {
     // ---------------------------------------------------- K and V tiles
     const uint64_t keep = ptx::policy_evict_last();  // read again by other heads and rows
@@ -370,10 +397,10 @@ __device__ __forceinline__ void window_feed(const WindowCtx& x, bool second, uin
     bool ok = true;
     // where entry st arrives: V in the second pass at warp 3's, which passes it on
     auto lands = [&](int st) { return bar(second && (st & 1) != 0 ? kWbVLanded + (st >> 1) : kWbKvFull + st); };
-    for (int r = from, item; ok && r <= to && (item = window_entry(r)) < p.items; ++r) {
-      const WindowItem it = window_item(p, item);
+    for (int r = from, item; ok && r <= to && (item = window_entry(r)) < items; ++r) {
+      const WindowItem it = window_item<kPacked>(p, item);
       for (int i = 0; ok && i < it.n; ++i) {
-        const int row = it.tile(i) * kTile;
+        const int row = it.base + it.tile(i) * kTile;
         for (int kv = 0; kv < 2; ++kv, ++c) {
           const int st = static_cast<int>(c % S);
           if (!(ok = pipe.wait(bar(kWbKvEmpty + st), static_cast<uint32_t>((c / S) & 1) ^ 1u, kSiteWinKv))) break;
@@ -392,8 +419,8 @@ __device__ __forceinline__ void window_feed(const WindowCtx& x, bool second, uin
     // ------------------------------------------------------- Q tiles
     const uint64_t once = ptx::policy_evict_first();
     uint32_t n_q = 0;
-    for (int r = from, item; r <= to && (item = window_entry(r)) < p.items; ++r) {
-      const WindowItem it = window_item(p, item);
+    for (int r = from, item; r <= to && (item = window_entry(r)) < items; ++r) {
+      const WindowItem it = window_item<kPacked>(p, item);
       if (it.n == 0) continue;
       if (n_q > 0 && !pipe.wait(bar(kWbQEmpty), (n_q - 1) & 1u, kSiteWinQ)) break;
       ptx::mbar_arrive_expect_tx(bar(kWbQFull), (it.on[0] && it.on[1] ? 2 : 1) * P::kTileBytes);
@@ -401,7 +428,7 @@ __device__ __forceinline__ void window_feed(const WindowCtx& x, bool second, uin
       for (int t = 0; t < 2; ++t)
         for (int kb = 0; it.on[t] && kb < NKB; ++kb)
           ptx::tma_load_4d_hint(base_s + P::kOffQ + t * P::kTileBytes + kb * kBlockBytes, &tm_q,
-                                bar(kWbQFull), kb * 64, it.row0[t], it.head[t] * p.mq.h,
+                                bar(kWbQFull), kb * 64, it.base + it.row0[t], it.head[t] * p.mq.h,
                                 it.b * p.mq.b, once);
       ++n_q;
     }
@@ -462,8 +489,8 @@ __device__ __forceinline__ void window_feed(const WindowCtx& x, bool second, uin
     };
     uint32_t g = 0;  // key tiles of this block so far (modulo 2^32); K of tile g is ring entry 2 g, V 2 g + 1
     bool ok = true;
-    for (int r = from, item; ok && r <= to && (item = window_entry(r)) < p.items; ++r) {
-      const WindowItem it = window_item(p, item);
+    for (int r = from, item; ok && r <= to && (item = window_entry(r)) < items; ++r) {
+      const WindowItem it = window_item<kPacked>(p, item);
       if (it.n == 0) continue;
       if (!(ok = pipe.wait_warp(bar(kWbQFull), n_q & 1u, kSiteWinMma))) break;
       ++n_q;
@@ -487,7 +514,7 @@ __device__ __forceinline__ void window_feed(const WindowCtx& x, bool second, uin
         }
         if (!(ok = wait_kv(2 * g + 1))) break;
         const int left = it.s.len - j * kTile;  // V rows of the sequence in this tile
-        if (left < kTile && it.s.len < p.w.n_keys) {
+        if (left < kTile && (kPacked || it.s.len < p.w.n_keys)) {
           const uint32_t v = base_s + P::kOffKv + (2 * g + 1) % S * P::kTileBytes;
           for (int kb = 0; kb < NKB; ++kb)
             for (int y = left * 8 + lane; y < kTile * 8; y += 32)
@@ -517,8 +544,8 @@ __device__ __forceinline__ void window_feed(const WindowCtx& x, bool second, uin
     // ------------------------ V tiles passed on, partly masked ones cleaned
     uint32_t g = 0, n_items = 0;  // tiles, items with tiles so far
     bool ok = true;
-    for (int r = from, item; ok && r <= to && (item = window_entry(r)) < p.items; ++r) {
-      const WindowItem it = window_item(p, item);
+    for (int r = from, item; ok && r <= to && (item = window_entry(r)) < items; ++r) {
+      const WindowItem it = window_item<kPacked>(p, item);
       if (it.n == 0) continue;
       const WindowMasked masked(p.w, it);
       const uint32_t slot = n_items & 1u;
@@ -542,7 +569,7 @@ __device__ __forceinline__ void window_feed(const WindowCtx& x, bool second, uin
 }
 
 // Warps 4 to 11: softmax and results.
-template <typename T, int NKB, bool kSecond>
+template <typename T, int NKB, bool kSecond, bool kPacked>
 __device__ __forceinline__ void window_soft(const WindowCtx& x, uint32_t bar0, const CUtensorMap& tm_o) {
   using P = WindowFwdPlan<NKB>;
   const WindowFwdParams& p = x.p;
@@ -558,13 +585,13 @@ __device__ __forceinline__ void window_soft(const WindowCtx& x, uint32_t bar0, c
   const uint32_t o_addr = tmem + lanes + P::kColO + t * P::kStrideO;
   const uint32_t stage_out = base_s + P::kOffOut + static_cast<uint32_t>(warp - 4) * 4096u;
   const uint64_t once = ptx::policy_evict_first();
-  const int D = p.w.dim, W = p.w.window;
+  const int D = p.w.dim, W = p.w.window, items = window_items<kPacked>(p);
   uint32_t n_s = 0;  // tiles of this unit so far
   int n_out = 0;     // result boxes of this warp so far
   bool ok = true;
   uint32_t n_items = 0;  // second pass: items with tiles so far
-  for (int round = kSecond ? x.again(0) : 0, item; ok && (!kSecond || round <= x.again(1)) && (item = window_entry(round)) < p.items; ++round) {
-    const WindowItem it = window_item(p, item);
+  for (int round = kSecond ? x.again(0) : 0, item; ok && (!kSecond || round <= x.again(1)) && (item = window_entry(round)) < items; ++round) {
+    const WindowItem it = window_item<kPacked>(p, item);
     if (!(t == 0 ? it.on[0] : it.on[1])) {
       if (kSecond && it.n > 0) pipe_warp_arrive(bar(kWbNotesFree + (n_items++ & 1u)));
       continue;
@@ -672,7 +699,7 @@ __device__ __forceinline__ void window_soft(const WindowCtx& x, uint32_t bar0, c
       ++n_items;
       const uint32_t note = ptx::ld_shared_volatile(x.note_at(slot));
       pipe_warp_arrive(bar(kWbNotesFree + slot));
-      if (note != 0 && !u.empty()) window_add_back<T>(p, item, t, note, o_addr);
+      if (note != 0 && !u.empty()) window_add_back<T, kPacked>(p, item, t, note, o_addr);
     }
     const float inv = 1.0f / l;
     float check = 0.0f;  // NaN once an element is not finite
@@ -689,6 +716,15 @@ __device__ __forceinline__ void window_soft(const WindowCtx& x, uint32_t bar0, c
         if (c + 2 * e < D) check = fmaf(a, 0.0f, fmaf(b, 0.0f, check));
         y[e] = pack2<T>(a, b);
       }
+      if (kPacked && row0 + (warp & 3) * 32 + 32 > it.rows) {  // the rows behind are another sequence's
+        if (row0 + r < it.rows) {
+          T* to = rows_at_mut<T>(p.out, 0, head, static_cast<long long>(it.base) + row0 + r) + c;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (c + 8 * k < D) *reinterpret_cast<uint4*>(to + 8 * k) = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+        }
+        continue;
+      }
       const uint32_t buf = stage_out + static_cast<uint32_t>(n_out & 1) * 2048u;
       if (lane == 0) ptx::bulk_wait_group_read<1>();  // the box before the last has left this buffer
       __syncwarp();
@@ -700,7 +736,7 @@ __device__ __forceinline__ void window_soft(const WindowCtx& x, uint32_t bar0, c
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        ptx::tma_store_4d_hint(&tm_o, buf, c, row0 + (warp & 3) * 32, head * p.mo.h, it.b * p.mo.b, once);
+        ptx::tma_store_4d_hint(&tm_o, buf, c, it.base + row0 + (warp & 3) * 32, head * p.mo.h, it.b * p.mo.b, once);
         ptx::bulk_commit_group();
       }
       ++n_out;
@@ -708,20 +744,20 @@ __device__ __forceinline__ void window_soft(const WindowCtx& x, uint32_t bar0, c
     ptx::tc_fence_before();
     const int row = row0 + r;
     // finite weights, but not the result: was it a hidden element of V?
-    if (!kSecond && __any_sync(0xffffffffu, row < p.w.n_queries && row_on && check != 0.0f && l - l == 0.0f) &&
-        window_leak<T>(p, item, t) && lane == 0) {
+    if (!kSecond && __any_sync(0xffffffffu, row < it.rows && row_on && check != 0.0f && l - l == 0.0f) &&
+        window_leak<T, kPacked>(p, item, t) && lane == 0) {
       asm volatile("red.shared.min.s32 [%0], %1;" ::"r"(pipe.at + kPipeBytes), "r"(round) : "memory");
       asm volatile("red.shared.max.s32 [%0], %1;" ::"r"(pipe.at + kPipeBytes + 4), "r"(round) : "memory");
     }
-    if (row < p.w.n_queries && p.lse != nullptr)
-      p.lse[(static_cast<long long>(it.b) * p.w.heads + head) * p.w.n_queries + row] =
+    if (row < it.rows && p.lse != nullptr)
+      p.lse[(static_cast<long long>(it.b) * p.w.heads + head) * p.w.n_queries + it.base + row] =
           l == 0.0f ? -INFINITY : (m + (log2f(l) - kWeightLog2<T>)) * kLn2;
   }
   // before the rows are written again, or the block's shared memory goes
   if (lane == 0) ptx::bulk_wait_group_all();
 }
 
-template <typename T, int NKB>
+template <typename T, int NKB, bool kPacked>
 __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
     vattn_window_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                             const __grid_constant__ CUtensorMap tm_k,
@@ -782,11 +818,11 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
   if (warp < 4) {
     ptx::regs_decrease<P::kRegsOther>();
     for (int pass = 0; pass == 0 || (pass == 1 && (two = x.second())); ++pass)
-      window_feed<T, NKB>(x, pass != 0, bar0 + (pass != 0 ? 8u * kWbCount : 0u), tm_q, tm_k, tm_v);
+      window_feed<T, NKB, kPacked>(x, pass != 0, bar0 + (pass != 0 ? 8u * kWbCount : 0u), tm_q, tm_k, tm_v);
   } else {
     ptx::regs_increase<P::kRegsSoftmax>();
-    window_soft<T, NKB, false>(x, bar0, tm_o);
-    if (x.second()) window_soft<T, NKB, true>(x, bar0 + 8u * kWbCount, tm_o);
+    window_soft<T, NKB, false, kPacked>(x, bar0, tm_o);
+    if (x.second()) window_soft<T, NKB, true, kPacked>(x, bar0 + 8u * kWbCount, tm_o);
   }
 
   ptx::tc_fence_before();

@@ -29,7 +29,7 @@ enum PipeSite : uint32_t {
   kSiteWinKv = 32, kSiteWinQ = 33, kSiteWinMma = 34, kSiteWinSoft = 35, kSiteWinOut = 36,
   kSiteWinDrain = 37, kSiteWinClean = 38,
   kSiteGradLoad = 40, kSiteGradMma = 41, kSiteGradSoft = 42, kSiteGradOut = 43, kSiteGradDrain = 44,
-  kSiteGradNext = 45,
+  kSiteGradNext = 45, kSitePagedLoad = 48, kSitePagedMath = 49, kSitePagedDrain = 50,
 };
 
 // Bounded waits on mbarriers: one that runs out records its site in the
