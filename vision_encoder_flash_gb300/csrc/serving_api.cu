@@ -136,10 +136,10 @@ vattn_status resident_blocks(K kernel, int threads, int smem, std::atomic<int>* 
   return VATTN_OK;
 }
 
-template <typename T, int DP, int RW>
+template <typename T, int DP, int NB, int RW>
 vattn_status paged_launch(vattn::PagedParams p, const Pools& pools, int sms, int device, cudaStream_t stream) {
-  using P = vattn::PagedPlan<DP, RW>;
-  auto kernel = vattn::vattn_paged_kernel<T, DP, RW>;
+  using P = vattn::PagedPlan<DP, NB, RW>;
+  auto kernel = vattn::vattn_paged_kernel<T, DP, NB, RW>;
   static std::atomic<uint8_t> done[kMaxDevices];
   static std::atomic<int> known[kMaxDevices];
   vattn_status st = allow_smem(kernel, P::kSmemBytes, done, device);
@@ -147,7 +147,7 @@ vattn_status paged_launch(vattn::PagedParams p, const Pools& pools, int sms, int
   int resident = 0;
   if ((st = resident_blocks(kernel, P::kThreads, P::kSmemBytes, known, device, &resident)) != VATTN_OK) return st;
   const long long seqs = static_cast<long long>(p.w.batch) * p.w.kv_heads;
-  p.row_blocks = (p.rows + 16 * RW - 1) / (16 * RW);
+  p.row_blocks = (p.rows + P::kRows - 1) / P::kRows;
   if (seqs * p.row_blocks > kMaxRows || seqs * p.rows > INT32_MAX)
     return fail(VATTN_ERR_UNSUPPORTED, "too many query rows");
   // Shares of the keys, as forward_cached has them.
@@ -162,7 +162,7 @@ vattn_status paged_launch(vattn::PagedParams p, const Pools& pools, int sms, int
   Workspace ws;
   const bool clustered = p.splits > 1 && p.splits <= vattn::kCachedCluster;
   if (p.splits > 1 && !clustered) {
-    const size_t rows = static_cast<size_t>(blocks) * p.splits * 16 * RW;
+    const size_t rows = static_cast<size_t>(blocks) * p.splits * P::kRows;
     if ((st = ws.take(rows * (p.w.dim + 2) * 4, device, stream)) != VATTN_OK) return st;
     p.part_o = reinterpret_cast<float*>(ws.data());
     p.part_ml = p.part_o + rows * p.w.dim;
@@ -196,7 +196,7 @@ vattn_status paged_launch(vattn::PagedParams p, const Pools& pools, int sms, int
   kernel<<<grid, P::kThreads, P::kSmemBytes, stream>>>(tk, tv, p);
   if ((st = launched("paged attention kernel launch")) != VATTN_OK) return st;
   if (p.splits == 1) return VATTN_OK;
-  if ((st = launch_behind("paged attention join kernel launch", vattn::vattn_paged_join_kernel<T, RW>,
+  if ((st = launch_behind("paged attention join kernel launch", vattn::vattn_paged_join_kernel<T, P::kRows, P::kKw>,
                           dim3(static_cast<unsigned>(seqs * p.rows)), dim3(128), 0, stream, p)) != VATTN_OK)
     return st;
   return ws.release();
@@ -204,9 +204,16 @@ vattn_status paged_launch(vattn::PagedParams p, const Pools& pools, int sms, int
 
 template <typename T, int DP>
 vattn_status paged_rows(const vattn::PagedParams& p, const Pools& pools, int sms, int device, cudaStream_t stream) {
-  if (p.rows <= 16) return paged_launch<T, DP, 1>(p, pools, sms, device, stream);
-  if (p.rows <= 32) return paged_launch<T, DP, 2>(p, pools, sms, device, stream);
-  return paged_launch<T, DP, 4>(p, pools, sms, device, stream);
+  if (p.rows <= 8) return paged_launch<T, DP, 1, 1>(p, pools, sms, device, stream);
+  if (p.rows <= 16) return paged_launch<T, DP, 2, 1>(p, pools, sms, device, stream);
+  if constexpr (DP <= 64) {
+    if (p.rows <= 32) return paged_launch<T, DP, 4, 1>(p, pools, sms, device, stream);
+    if (p.rows <= 64) return paged_launch<T, DP, 4, 2>(p, pools, sms, device, stream);
+    return paged_launch<T, DP, 4, 4>(p, pools, sms, device, stream);
+  } else {
+    if (p.rows <= 32) return paged_launch<T, DP, 2, 2>(p, pools, sms, device, stream);
+    return paged_launch<T, DP, 2, 4>(p, pools, sms, device, stream);
+  }
 }
 
 template <typename T>
@@ -351,7 +358,7 @@ vattn_status vattn_forward_paged(const vattn_rows* q, const vattn_pages* cache, 
   p.n_pages = cache->n_pages;
   p.max_pages = static_cast<int>(cache->max_pages);
   p.page = static_cast<int>(cache->page_size);
-  p.log_box = p.page % 64 == 0 ? 6 : (p.page % 32 == 0 ? 5 : 4);
+  p.log_box = p.page % 32 == 0 ? 5 : 4;
   p.box = 1 << p.log_box;
   p.rows = p.w.group * p.w.n_queries;
   p.scale_log2 = a->scale * vattn::kLog2E;
