@@ -38,6 +38,10 @@ namespace vattn {
 
 constexpr int kPagedKeys = 32;  // keys of a step
 constexpr int kPagedWarps = 4;
+#ifndef PCL
+#define PCL 4
+#endif
+constexpr int kPagedCluster = PCL;
 
 struct PagedParams {
   WindowParams w;  // n_keys: rows that the table has room for; kv_len: the cache's
@@ -144,7 +148,7 @@ __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads)
   const uint32_t bk = p.d_row_blocks.div(p.d_splits.div(blockIdx.x, &split_u), &rb_u);
   const int b = static_cast<int>(p.d_kv_heads.div(bk, &kh_u));
   const int split = static_cast<int>(split_u), rb = static_cast<int>(rb_u), kh = static_cast<int>(kh_u);
-  const bool clustered = p.splits > 1 && p.splits <= kCachedCluster;
+  const bool clustered = p.splits > 1 && p.splits <= kPagedCluster;
 
   if (tid == 0) {
     for (int i = 0; i < P::kKw * S; ++i) {
@@ -175,72 +179,90 @@ __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads)
   }
   __syncthreads();
 
-  // ---- the group's steps: 32 keys each, as `boxes` boxes; its boxes numbered through
-  const int boxes = kPagedKeys >> p.log_box;  // 1 or 2
-  const int all_steps = (max(v1 - v0, 0) + boxes - 1) / boxes;
+  // ---- the group's steps: 32 keys each, as one box or two; its boxes numbered through
+  const int log_boxes = 5 - p.log_box, boxes = 1 << log_boxes;
+  static_assert(kPagedKeys == 32, "log_boxes");
+  const int all_steps = (max(v1 - v0, 0) + boxes - 1) >> log_boxes;
   const int steps = (all_steps - kw + P::kKw - 1) / P::kKw;
-  auto box_of = [&](int i) -> int { return v0 + ((i / boxes) * P::kKw + kw) * boxes + i % boxes; };
+  auto box_of = [&](int i) -> int { return v0 + ((((i >> log_boxes) * P::kKw + kw) << log_boxes) | (i & (boxes - 1))); };
 
-  // ---- loads (the group's first warp): lane i has the table's entry and the
-  // scales of box i of 32, and the entry (half way: the scales too) of the 32 after
-  struct Scales {
-    float k, log2_v, inv_v;
+  // ---- loads (the group's first warp): lane i has what box i of 32 needs, page, row
+  // and scales, and of the 32 after (half way on: the scales too)
+  struct Box {
+    int page, row, key0;          // page: behind the last if it is not there, and reads as zeros
+    float k, log2_v, inv_v;       // k < 0: the keys are not there
   };
-  auto entry = [&](int i) -> int {  // page of the group's box i, -1 if it is not there
-    const int x = box_of(i);
-    if (x >= v1) return -1;
-    const int id = p.table[static_cast<long long>(b) * p.max_pages + p.d_page.div(static_cast<uint32_t>(sp.box(x) << p.log_box))];
-    return id >= 0 && id < p.n_pages ? id : -1;
-  };
-  auto scales = [&](int id) {
-    Scales s{-1.0f, 0.0f, 0.0f};  // k < 0: the keys are not there
-    if (id < 0) return s;
-    const long long at = static_cast<long long>(id) * w.kv_heads + kh;
-    const float v = p.v_scale[at];
-    s.k = p.k_scale[at];
-    s.log2_v = log2f(v);
-    s.inv_v = 1.0f / v;
-    return s;
-  };
-  int issued = 0;  // steps
-  int id = -1, id_next = -1;
-  Scales sc{}, sc_next{};
-  const uint64_t once = ptx::policy_evict_first();
-  auto issue = [&]() {
-    const int st = issued % S, i0 = issued * boxes, l0 = i0 & 31;
-    if (l0 == 0 && issued > 0) {
-      id = id_next;
-      sc = sc_next;
-      id_next = entry(i0 + 32 + lane);
-    } else if (l0 == 16) {
-      sc_next = scales(id_next);
+  auto place = [&](int i, Box& x) {  // of the group's box i
+    const int at = box_of(i);
+    x.key0 = sp.box(at) << p.log_box;
+    x.page = static_cast<int>(p.n_pages);
+    uint32_t row = 0;
+    if (at < v1) {
+      const uint32_t lp = p.d_page.div(static_cast<uint32_t>(x.key0), &row);
+      const int id = p.table[static_cast<long long>(b) * p.max_pages + lp];
+      if (id >= 0 && id < p.n_pages) x.page = id;
     }
-    const int x = box_of(i0 + (lane & 1));  // lanes l0, l0 + 1: l0 is even where there are two boxes
-    const int n = min(boxes, v1 - box_of(i0));
-    const bool mine = lane >= l0 && lane < l0 + n;
-    const int which = lane - l0;
-    if (mine)
-      ptx::st_shared_v4(smem_s + P::kOffMeta + static_cast<uint32_t>(((kw * S + st) * 2 + which) * 16), sc.k, sc.log2_v, sc.inv_v, 0.0f);
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive_expect_tx(full(st), static_cast<uint32_t>(n) * 2u * static_cast<uint32_t>(p.box * DP));
-    __syncwarp();
-    if (mine) {
-      const int key0 = sp.box(boxes == 2 ? x : box_of(i0)) << p.log_box;
-      const int row = key0 - static_cast<int>(p.d_page.div(static_cast<uint32_t>(key0))) * p.page;
-      const uint32_t to = smem_s + static_cast<uint32_t>((kw * S + st) * P::kStageBytes + which * p.box * DP);
-      // a page that is not there reads as zeros: behind the last
-      const int pg = id >= 0 ? id : static_cast<int>(p.n_pages);
+    x.row = static_cast<int>(row);
+  };
+  auto scales = [&](Box& x) {
+    x.k = -1.0f;
+    x.log2_v = x.inv_v = 0.0f;
+    if (x.page >= p.n_pages) return;
+    const long long at = static_cast<long long>(x.page) * w.kv_heads + kh;
+    const float v = p.v_scale[at];
+    x.k = p.k_scale[at];
+    x.log2_v = log2f(v);
+    x.inv_v = 1.0f / v;
+  };
+  int issued = 0, issue_st = 0;  // steps, and the next one's place in the ring
+  Box now{}, next{};
+  const uint64_t once = ptx::policy_evict_first();
+  // The copies of a step's boxes, lanes l0 and l0 + 1 of `now`, to place st.
+  auto copies = [&](int st, int l0) {
+    const int pg = __shfl_sync(0xffffffffu, now.page, l0), row = __shfl_sync(0xffffffffu, now.row, l0);
+    const uint32_t to = smem_s + static_cast<uint32_t>((kw * S + st) * P::kStageBytes);
+    if (ptx::elect_one()) {
       ptx::tma_load_4d_hint(to, &tm_k, full(st), 0, row, kh, pg, once);
       ptx::tma_load_4d_hint(to + P::kTileBytes, &tm_v, full(st), 0, row, kh, pg, once);
     }
+    if (log_boxes == 0) return;
+    const int pg1 = __shfl_sync(0xffffffffu, now.page, l0 + 1), row1 = __shfl_sync(0xffffffffu, now.row, l0 + 1);
+    if (ptx::elect_one()) {  // (of a box behind the share: zeros)
+      ptx::tma_load_4d_hint(to + 16 * DP, &tm_k, full(st), 0, row1, kh, pg1, once);
+      ptx::tma_load_4d_hint(to + P::kTileBytes + 16 * DP, &tm_v, full(st), 0, row1, kh, pg1, once);
+    }
+  };
+  // What the products need beside them, and the barrier's count, which the copies may be ahead of.
+  auto announce = [&](int st, int l0) {
+    const int which = lane - l0;
+    if (which >= 0 && which < boxes)
+      ptx::st_shared_v4(smem_s + P::kOffMeta + static_cast<uint32_t>(((kw * S + st) * 2 + which) * 16), now.k, now.log2_v,
+                        now.inv_v, __int_as_float(now.key0));
     __syncwarp();
+    if (ptx::elect_one()) ptx::mbar_arrive_expect_tx(full(st), P::kStageBytes);
+  };
+  auto issue = [&]() {
+    const int st = issue_st, i0 = issued << log_boxes, l0 = i0 & 31;
+    issue_st = st + 1 == S ? 0 : st + 1;
+    if (l0 == 0) {
+      now = next;
+      place(i0 + 32 + lane, next);
+    } else if (l0 == 16) {
+      scales(next);
+    }
+    announce(st, l0);
+    copies(st, l0);
     ++issued;
   };
   if (rw == 0 && steps > 0) {
-    id = entry(lane);
-    id_next = entry(32 + lane);
-    sc = scales(id);
-    while (issued < min(S, steps)) issue();
+    place(lane, now);
+    const int first = min(S, steps);  // S steps are 12 boxes at most
+    for (int i = 0; i < first; ++i) copies(i, i << log_boxes);
+    scales(now);
+    place(32 + lane, next);
+    for (int i = 0; i < first; ++i) announce(i, i << log_boxes);
+    issued = first;
+    issue_st = first == S ? 0 : first;
   }
 
   // ---- q as columns: lane / 4 of each eight rows, in the order of K's bytes
@@ -302,30 +324,32 @@ __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads)
       for (int e = 0; e < 4; ++e) o[n][nb][e] = 0.0f;
   }
 
-  int step = 0;
+  // keys j .. j + 15 need no mask: all rows see them
+  const int free_end = w.n_queries > 1 ? sp.base : sp.len;
+  const int free_begin = w.n_queries > 1 ? max(0, sp.base + w.n_queries - w.window) : sp.first;
+  int step = 0, st = 0;
+  uint32_t turn = 0;
   for (; step < steps; ++step) {
-    const int st = step % S;
-    if (!pipe.wait_warp(full(st), static_cast<uint32_t>((step / S) & 1), kSitePagedMath)) break;
+    if (!pipe.wait_warp(full(st), turn, kSitePagedMath)) break;
     const uint32_t ks_s = smem_s + static_cast<uint32_t>((kw * S + st) * P::kStageBytes);
     const uint32_t vs_s = ks_s + P::kTileBytes;
     // the step's keys by 16: first of each in the sequence, scales; those that are
     // not there, or that no row sees, count as masked throughout
     int j0[2];
     float4 meta[2];
-    bool masked[2], some = false;
-    const int x0 = box_of(step * boxes);
+    bool masked[2];
+    const uint32_t meta_s = smem_s + P::kOffMeta + static_cast<uint32_t>((kw * S + st) * 32);
+    meta[0] = ptx::ld_shared_v4(meta_s);
+    meta[1] = ptx::ld_shared_v4(meta_s + (log_boxes << 4));
 #pragma unroll
     for (int mb = 0; mb < 2; ++mb) {
-      const int at = (mb * 16) >> p.log_box;
-      meta[mb] = ptx::ld_shared_v4(smem_s + P::kOffMeta + static_cast<uint32_t>(((kw * S + st) * 2 + at) * 16));
-      const bool on = x0 + at < v1 && !(meta[mb].x < 0.0f);
-      const int j = (sp.box(x0 + at) << p.log_box) + ((mb * 16) & (p.box - 1)), j1 = j + 15;
+      const int j = __float_as_int(meta[mb].w) + (mb == 1 && log_boxes == 0 ? 16 : 0);
+      const bool on = !(meta[mb].x < 0.0f);
       j0[mb] = on ? j : 0x7fffff00;
       if (!on) meta[mb] = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
-      masked[mb] = !on || j1 >= sp.len || (w.n_queries > 1 && j1 >= sp.base) ||
-                   (j1 >= w.sinks && (j < sp.first || (w.n_queries > 1 && j <= sp.base + w.n_queries - 1 - w.window)));
-      some |= masked[mb];
+      masked[mb] = !on || j + 15 >= free_end || (j < free_begin && j + 15 >= w.sinks);
     }
+    const bool some = masked[0] || masked[1];
     // ---- S = K Q^T
     float s[2][NB][4];  // keys 16 mb + g, + 8 (e / 2) of rows 2 c4, + 1 (e % 2)
 #pragma unroll
@@ -367,45 +391,53 @@ __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads)
       }
     }
     // ---- online softmax, two rows a lane for each eight, eight lanes a row; a row is
-    // rescaled once its maximum grew by more than 2^8 (exact after the final 1 / l)
-    float alpha[NB][2];
+    // rescaled once its maximum grew by more than 2^8 (exact after the final 1 / l),
+    // and only then is the maximum over its lanes wanted
+    float c[2][NB][2], top[NB][2];
     bool grew = false;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float c[2];
 #pragma unroll
         for (int mb = 0; mb < 2; ++mb)  // not 0 or infinity, which -infinity or 0 make NaN
-          c[mb] = fminf(fmaxf(row_c[nb][e] * meta[mb].x, 0x1p-126f), 0x1p127f);
-        float top = fmaxf(fmaf(fmaxf(s[0][nb][e], s[0][nb][e + 2]), c[0], meta[0].y),
-                          fmaf(fmaxf(s[1][nb][e], s[1][nb][e + 2]), c[1], meta[1].y));
-#pragma unroll
-        for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-        const bool more = top > m[nb][e] + kLazyLog2;
-        const float mn = more ? top : m[nb][e];
-        const float ref = mn == -INFINITY ? 0.0f : mn;
-        alpha[nb][e] = more ? ptx::ex2_approx(m[nb][e] - ref) : 1.0f;
-        m[nb][e] = mn;
-        grew |= more;
-        float sum = 0.0f;
-#pragma unroll
-        for (int mb = 0; mb < 2; ++mb) {
-          const float shift = kWeightLog2<__half> - ref + meta[mb].y;
-          s[mb][nb][e] = ptx::ex2_approx(fmaf(s[mb][nb][e], c[mb], shift));
-          s[mb][nb][e + 2] = ptx::ex2_approx(fmaf(s[mb][nb][e + 2], c[mb], shift));
-          sum = fmaf(s[mb][nb][e] + s[mb][nb][e + 2], meta[mb].z, sum);
-        }
-        l[nb][e] = fmaf(l[nb][e], alpha[nb][e], sum);  // of this lane's keys
+          c[mb][nb][e] = fminf(fmaxf(row_c[nb][e] * meta[mb].x, 0x1p-126f), 0x1p127f);
+        top[nb][e] = fmaxf(fmaf(fmaxf(s[0][nb][e], s[0][nb][e + 2]), c[0][nb][e], meta[0].y),
+                           fmaf(fmaxf(s[1][nb][e], s[1][nb][e + 2]), c[1][nb][e], meta[1].y));
+        grew |= top[nb][e] > m[nb][e] + kLazyLog2;
       }
     if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-      for (int n = 0; n < CH; ++n)
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+        for (int e = 0; e < 2; ++e) {
+          float y = top[nb][e];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[n][nb][e] *= alpha[nb][e & 1];
+          for (int x = 4; x < 32; x *= 2) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, x));
+          const bool more = y > m[nb][e] + kLazyLog2;
+          const float alpha = more ? ptx::ex2_approx(m[nb][e] - y) : 1.0f;
+          if (more) m[nb][e] = y;
+          l[nb][e] *= alpha;
+#pragma unroll
+          for (int n = 0; n < CH; ++n) {
+            o[n][nb][e] *= alpha;
+            o[n][nb][e + 2] *= alpha;
+          }
+        }
     }
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float ref = kWeightLog2<__half> - (m[nb][e] == -INFINITY ? 0.0f : m[nb][e]);
+#pragma unroll
+        for (int mb = 0; mb < 2; ++mb) {
+          const float shift = ref + meta[mb].y;
+          s[mb][nb][e] = ptx::ex2_approx(fmaf(s[mb][nb][e], c[mb][nb][e], shift));
+          s[mb][nb][e + 2] = ptx::ex2_approx(fmaf(s[mb][nb][e + 2], c[mb][nb][e], shift));
+          l[nb][e] = fmaf(s[mb][nb][e] + s[mb][nb][e + 2], meta[mb].z, l[nb][e]);  // of this lane's keys
+        }
+      }
     // ---- O += V P
     bool loops = false;
     if (some) {
@@ -493,11 +525,15 @@ __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads)
     if (RW > 1) pipe_warp_arrive(empty(st));
     else __syncwarp();
     if (rw == 0 && issued < steps) {
-      if (RW > 1 && !pipe.wait_warp(empty(st), static_cast<uint32_t>((step / S) & 1), kSitePagedLoad)) {
+      if (RW > 1 && !pipe.wait_warp(empty(st), turn, kSitePagedLoad)) {
         ++step;
         break;
       }
       issue();
+    }
+    if (++st == S) {
+      st = 0;
+      turn ^= 1;
     }
   }
   if (rw == 0 && lane == 0)  // after a wait that ran out: the copies in flight land before the block exits
@@ -584,17 +620,17 @@ __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads)
     const int rr = rb * P::kRows + r;
     if (rr >= p.rows) continue;
     const uint32_t row = smem_s + static_cast<uint32_t>(r * RS * 4);
-    float2 ml[kCachedCluster];
+    float2 ml[kPagedCluster];
     float mx = -INFINITY;
 #pragma unroll
-    for (int s = 0; s < kCachedCluster; ++s) {
+    for (int s = 0; s < kPagedCluster; ++s) {
       ml[s] = s < shares ? ptx::ld_cluster_v2(ptx::cluster_map(row + DP * 4, s)) : make_float2(-INFINITY, 0.0f);
       mx = fmaxf(mx, ml[s].x);
     }
     const float ref = mx == -INFINITY ? 0.0f : mx;
     float sum = 0.0f, acc[8] = {};
 #pragma unroll
-    for (int s = 0; s < kCachedCluster; ++s) {
+    for (int s = 0; s < kPagedCluster; ++s) {
       if (s >= shares) break;
       const float a = ptx::ex2_approx(ml[s].x - ref);
       sum = fmaf(a, ml[s].y, sum);
@@ -612,18 +648,103 @@ __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads)
   ptx::grid_dep_launch();
 }
 
-// Merges the shares of a row, one block per row: the weight of every share
-// first, then the four warps add a quarter of the shares each (4 dims a
-// lane), in a fixed order.
+// Merges the shares of 32 dims of a row, one block each: the weight of every share
+// first, then eight lanes a share, 16 bytes a lane, add up every 32nd one, and the
+// block their sums, in a fixed order.
 template <typename T, int ROWS, int KW>
-__global__ void __launch_bounds__(128) vattn_paged_join_kernel(const __grid_constant__ PagedParams p) {
+__global__ void __launch_bounds__(256) vattn_paged_join_kernel(const __grid_constant__ PagedParams p) {
   __shared__ float weight[kCachedMaxSplits];
-  __shared__ float red[8];
-  __shared__ float4 acc_s[4][32];
+  __shared__ float red[16];
+  __shared__ float4 acc_s[8][8];
   const WindowParams& w = p.w;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, D = w.dim;
   const long long bk = blockIdx.x / p.rows;
   const int rr = static_cast<int>(blockIdx.x - bk * p.rows);
+  const int b = static_cast<int>(bk / w.kv_heads), kh = static_cast<int>(bk - static_cast<long long>(b) * w.kv_heads);
+  const int t = rr / w.group, d = static_cast<int>(blockIdx.y) * 32 + (lane & 7) * 4;
+  ptx::grid_dep_wait();
+  const PagedSpan sp = PagedSpan::make(w, p.log_box, KW, b, p.splits);
+  const int shares = sp.shares();
+  if (shares == 1) return;  // written by its block
+  const bool none = cached_word(w, b, t, sp.base) == 0;
+  const long long at0 = (bk * p.row_blocks + rr / ROWS) * p.splits * ROWS + rr % ROWS;
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + at0;
+  static_assert(kCachedMaxSplits <= 512, "two shares a thread");
+  float2 f[2];
+  float mx = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int s = tid + 256 * i;
+    f[i] = s < shares ? ml[s * static_cast<long long>(ROWS)] : make_float2(-INFINITY, 0.0f);
+    mx = fmaxf(mx, f[i].x);
+  }
+  mx = warp_max(mx);
+  if (lane == 0) red[warp] = mx;
+  __syncthreads();
+  mx = red[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) mx = fmaxf(mx, red[i]);
+  const float ref = mx == -INFINITY ? 0.0f : mx;
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float a = ptx::ex2_approx(f[i].x - ref);
+    weight[tid + 256 * i] = a;
+    sum = fmaf(a, f[i].y, sum);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) red[8 + warp] = sum;
+  __syncthreads();
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (d < D) {
+    const float* from = p.part_o + at0 * D + d;
+#pragma unroll 4
+    for (int s = warp * 4 + (lane >> 3); s < shares; s += 32) {
+      const float4 y = *reinterpret_cast<const float4*>(from + s * static_cast<long long>(ROWS) * D);
+      const float a = weight[s];
+      acc.x = fmaf(a, y.x, acc.x);
+      acc.y = fmaf(a, y.y, acc.y);
+      acc.z = fmaf(a, y.z, acc.z);
+      acc.w = fmaf(a, y.w, acc.w);
+    }
+  }
+#pragma unroll
+  for (int o = 8; o < 32; o *= 2) {
+    acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
+    acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
+    acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o);
+    acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
+  }
+  if (lane < 8) acc_s[warp][lane] = acc;
+  __syncthreads();
+  if (tid >= 8 || d >= D) return;
+  sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum += red[8 + i];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    const float4 y = acc_s[i][lane];
+    acc.x += y.x;
+    acc.y += y.y;
+    acc.z += y.z;
+    acc.w += y.w;
+  }
+  const float inv = 1.0f / sum;
+  const bool zero = none || sum == 0.0f;
+  const float out[4] = {zero ? 0.0f : acc.x * inv, zero ? 0.0f : acc.y * inv, zero ? 0.0f : acc.z * inv, zero ? 0.0f : acc.w * inv};
+  reinterpret_cast<Vec<T, 4>*>(rows_at_mut<T>(p.out, b, kh * w.group + (rr - t * w.group), t) + d)->narrow(out);
+}
+
+// The same for few shares (32 at most): a warp has a row, lane i the weight of share i.
+template <typename T, int ROWS, int KW>
+__global__ void __launch_bounds__(256) vattn_paged_join_few_kernel(const __grid_constant__ PagedParams p) {
+  const WindowParams& w = p.w;
+  const int lane = static_cast<int>(threadIdx.x) & 31, D = w.dim;
+  const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (row >= static_cast<long long>(w.batch) * w.kv_heads * p.rows) return;
+  const long long bk = row / p.rows;
+  const int rr = static_cast<int>(row - bk * p.rows);
   const int b = static_cast<int>(bk / w.kv_heads), kh = static_cast<int>(bk - static_cast<long long>(b) * w.kv_heads);
   const int t = rr / w.group;
   ptx::grid_dep_wait();
@@ -632,54 +753,29 @@ __global__ void __launch_bounds__(128) vattn_paged_join_kernel(const __grid_cons
   if (shares == 1) return;  // written by its block
   const bool none = cached_word(w, b, t, sp.base) == 0;
   const long long at0 = (bk * p.row_blocks + rr / ROWS) * p.splits * ROWS + rr % ROWS;
-  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + at0;
-  float mx = -INFINITY;
-  for (int s = tid; s < shares; s += 128) mx = fmaxf(mx, ml[s * static_cast<long long>(ROWS)].x);
-  mx = warp_max(mx);
-  if (lane == 0) red[warp] = mx;
-  __syncthreads();
-  mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  const float ref = mx == -INFINITY ? 0.0f : mx;
-  float sum = 0.0f;
-  for (int s = tid; s < shares; s += 128) {
-    const float2 f = ml[s * static_cast<long long>(ROWS)];
-    const float a = ptx::ex2_approx(f.x - ref);
-    weight[s] = a;
-    sum = fmaf(a, f.y, sum);
-  }
+  const float2 ml = lane < shares ? reinterpret_cast<const float2*>(p.part_ml)[at0 + lane * static_cast<long long>(ROWS)]
+                                  : make_float2(-INFINITY, 0.0f);
+  const float mx = warp_max(ml.x), ref = mx == -INFINITY ? 0.0f : mx;
+  const float weight = ptx::ex2_approx(ml.x - ref);
+  float sum = weight * ml.y;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) red[4 + warp] = sum;
-  __syncthreads();
-  sum = (red[4] + red[5]) + (red[6] + red[7]);
-  float acc[4] = {};
-  if (lane * 4 < D) {
-    const float* from = p.part_o + at0 * D + lane * 4;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const float* from = p.part_o + at0 * D + (lane * 4 < D ? lane * 4 : 0);
 #pragma unroll 8
-    for (int s = warp; s < shares; s += 4) {
-      const float4 f = *reinterpret_cast<const float4*>(from + s * static_cast<long long>(ROWS) * D);
-      const float a = weight[s];
-      acc[0] = fmaf(a, f.x, acc[0]);
-      acc[1] = fmaf(a, f.y, acc[1]);
-      acc[2] = fmaf(a, f.z, acc[2]);
-      acc[3] = fmaf(a, f.w, acc[3]);
-    }
+  for (int s = 0; s < shares; ++s) {
+    const float4 y = *reinterpret_cast<const float4*>(from + s * static_cast<long long>(ROWS) * D);
+    const float a = __shfl_sync(0xffffffffu, weight, s);
+    acc.x = fmaf(a, y.x, acc.x);
+    acc.y = fmaf(a, y.y, acc.y);
+    acc.z = fmaf(a, y.z, acc.z);
+    acc.w = fmaf(a, y.w, acc.w);
   }
-  acc_s[warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-  __syncthreads();
-  if (warp != 0 || lane * 4 >= D) return;
+  if (lane * 4 >= D) return;
   const float inv = 1.0f / sum;
-#pragma unroll
-  for (int k = 1; k < 4; ++k) {
-    const float4 f = acc_s[k][lane];
-    acc[0] += f.x;
-    acc[1] += f.y;
-    acc[2] += f.z;
-    acc[3] += f.w;
-  }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) acc[e] = none || sum == 0.0f ? 0.0f : acc[e] * inv;
-  reinterpret_cast<Vec<T, 4>*>(rows_at_mut<T>(p.out, b, kh * w.group + (rr - t * w.group), t) + lane * 4)->narrow(acc);
+  const bool zero = none || sum == 0.0f;
+  const float out[4] = {zero ? 0.0f : acc.x * inv, zero ? 0.0f : acc.y * inv, zero ? 0.0f : acc.z * inv, zero ? 0.0f : acc.w * inv};
+  reinterpret_cast<Vec<T, 4>*>(rows_at_mut<T>(p.out, b, kh * w.group + (rr - t * w.group), t) + lane * 4)->narrow(out);
 }
 
 }  // namespace vattn

@@ -157,10 +157,13 @@ vattn_status paged_launch(vattn::PagedParams p, const Pools& pools, int sms, int
   const long long fine = std::max(std::min(32LL, (most_keys + 127) / 128), (most_keys + 255) / 256);
   p.splits = static_cast<int>(std::max(1LL, std::min({fill, fine, static_cast<long long>(vattn::kCachedMaxSplits)})));
   if (blocks * p.splits > kMaxRows) p.splits = 1;
+#ifdef PROBE
+  if (getenv("SPLITS")) p.splits = atoi(getenv("SPLITS"));
+#endif
   p.d_splits = fast_div(p.splits);
   p.d_row_blocks = fast_div(p.row_blocks);
   Workspace ws;
-  const bool clustered = p.splits > 1 && p.splits <= vattn::kCachedCluster;
+  const bool clustered = p.splits > 1 && p.splits <= vattn::kPagedCluster;
   if (p.splits > 1 && !clustered) {
     const size_t rows = static_cast<size_t>(blocks) * p.splits * P::kRows;
     if ((st = ws.take(rows * (p.w.dim + 2) * 4, device, stream)) != VATTN_OK) return st;
@@ -196,14 +199,31 @@ vattn_status paged_launch(vattn::PagedParams p, const Pools& pools, int sms, int
   kernel<<<grid, P::kThreads, P::kSmemBytes, stream>>>(tk, tv, p);
   if ((st = launched("paged attention kernel launch")) != VATTN_OK) return st;
   if (p.splits == 1) return VATTN_OK;
-  if ((st = launch_behind("paged attention join kernel launch", vattn::vattn_paged_join_kernel<T, P::kRows, P::kKw>,
-                          dim3(static_cast<unsigned>(seqs * p.rows)), dim3(128), 0, stream, p)) != VATTN_OK)
-    return st;
+  const long long out_rows = seqs * p.rows;
+  if (p.splits <= 32)
+    st = launch_behind("paged attention join kernel launch", vattn::vattn_paged_join_few_kernel<T, P::kRows, P::kKw>,
+                       dim3(static_cast<unsigned>((out_rows + 7) / 8)), dim3(256), 0, stream, p);
+  else
+    st = launch_behind("paged attention join kernel launch", vattn::vattn_paged_join_kernel<T, P::kRows, P::kKw>,
+                       dim3(static_cast<unsigned>(out_rows), static_cast<unsigned>((p.w.dim + 31) / 32)), dim3(256), 0,
+                       stream, p);
+  if (st != VATTN_OK) return st;
   return ws.release();
 }
 
 template <typename T, int DP>
 vattn_status paged_rows(const vattn::PagedParams& p, const Pools& pools, int sms, int device, cudaStream_t stream) {
+#ifdef PROBE
+  if (getenv("PV")) {
+    const int v = atoi(getenv("PV"));
+    if (v == 11) return paged_launch<T, DP, 1, 1>(p, pools, sms, device, stream);
+    if (v == 12) return paged_launch<T, DP, 1, 2>(p, pools, sms, device, stream);
+    if (v == 14) return paged_launch<T, DP, 1, 4>(p, pools, sms, device, stream);
+    if (v == 21) return paged_launch<T, DP, 2, 1>(p, pools, sms, device, stream);
+    if (v == 22) return paged_launch<T, DP, 2, 2>(p, pools, sms, device, stream);
+    if (v == 24) return paged_launch<T, DP, 2, 4>(p, pools, sms, device, stream);
+  }
+#endif
   if (p.rows <= 8) return paged_launch<T, DP, 1, 1>(p, pools, sms, device, stream);
   if (p.rows <= 16) return paged_launch<T, DP, 2, 1>(p, pools, sms, device, stream);
   if constexpr (DP <= 64) {
