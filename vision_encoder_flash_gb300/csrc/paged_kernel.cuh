@@ -3,11 +3,12 @@
 //
 // Memory bound: every visible key and value, one byte an element, is read once for
 // all rows (new token, query head of the group) of its key head together.  A
-// block takes up to 8 NB RW rows and a share of the keys.  Its four warps are RW
-// groups of rows times 4 / RW groups of keys; a group of keys takes every 4 / RW-th
-// 32 keys of the share through a ring of its own, filled by TMA in boxes of 32 or
-// 16 rows of one page (what divides the page) from the group's first warp, which
-// has the table's entries and the scales of its next 32 boxes in its lanes.
+// block takes up to 8 NB RW rows and a share of the keys.  Its four math warps are
+// RW groups of rows times 4 / RW groups of keys, each with 32 of a step's keys.
+// Four more warps fill a ring of steps by TMA, two of them K and two V, in boxes of
+// 128 to 16 rows of one page (what divides the page and the step), with the table's
+// entries of the next 32 boxes in their lanes, and give most of their registers to
+// the math warps.  (Copies from the math warps took 370 of the 1700 cycles of a step.)
 //
 // The products are mma.sync m16n8k16 in f16 with the keys, or the dims of values,
 // as the 16 rows and NB times 8 query rows as columns: few query rows leave little
@@ -36,8 +37,8 @@
 
 namespace vattn {
 
-constexpr int kPagedKeys = 32;  // keys of a step
-constexpr int kPagedWarps = 4;
+constexpr int kPagedKeys = 32;  // keys of a warp's part of a step
+constexpr int kPagedWarps = 4;  // math warps
 #ifndef PCL
 #define PCL 4
 #endif
@@ -68,9 +69,9 @@ struct PagedSpan {
   int base, len;    // new token t is row base + t; rows in use
   int first;        // no row sees keys in [sinks, first)
   int heads, begin; // listed: boxes [0, heads) and [begin, ..)
-  int per, n;       // boxes of a share (whole steps of all its groups of keys), of all
+  int per, n;       // boxes of a share (whole steps), of all
 
-  __device__ __forceinline__ static PagedSpan make(const WindowParams& w, int log_box, int groups, int b, int splits) {
+  __device__ __forceinline__ static PagedSpan make(const WindowParams& w, int log_box, int groups, int b, const FastDiv& splits) {
     PagedSpan s;
     const int box = 1 << log_box;
     s.len = min(max(w.kv_len[b], 0), w.n_keys);
@@ -79,11 +80,14 @@ struct PagedSpan {
     s.begin = s.first >> log_box;
     s.heads = min((min(w.sinks, s.len) + box - 1) >> log_box, s.begin);
     s.n = s.heads + ((s.len + box - 1) >> log_box) - s.begin;
-    const int unit = (groups * kPagedKeys) >> log_box;
-    s.per = ((s.n + splits - 1) / splits + unit - 1) / unit * unit;
+    const int unit = (groups * kPagedKeys) >> log_box;  // a step
+    const int some = static_cast<int>(splits.div(static_cast<uint32_t>(s.n) + splits.d - 1));
+    s.per = (some + unit - 1) & ~(unit - 1);  // (a power of two)
     return s;
   }
   __device__ __forceinline__ int box(int i) const { return i < heads ? i : begin + (i - heads); }
+  __device__ __forceinline__ bool has(int split) const { return split == 0 || split * per < n; }
+  __device__ __forceinline__ bool one() const { return per >= n; }
   __device__ __forceinline__ int shares() const { return n == 0 ? 1 : (n + per - 1) / per; }
 };
 
@@ -96,19 +100,22 @@ __device__ __forceinline__ int paged_swizzled(int r, int c) {
 
 template <int DP, int NB, int RW>
 struct PagedPlan {
-  static constexpr int kThreads = 32 * kPagedWarps;
+  static constexpr int kThreads = 256;
   static constexpr int kKw = kPagedWarps / RW;  // groups of keys
   static constexpr int kRows = 8 * NB * RW;
-  static constexpr int kTileBytes = kPagedKeys * DP;
+  static constexpr int kStepKeys = kKw * kPagedKeys, kLogStep = RW == 1 ? 7 : (RW == 2 ? 6 : 5);
+  static_assert(kStepKeys == 1 << kLogStep, "a power of two");
+  static constexpr int kTileBytes = kStepKeys * DP;
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kStages = DP == 128 ? 3 : (DP == 64 ? 4 : 6);
   static constexpr int kResultStride = DP + 4;  // floats of a row: O, maximum, sum
   static constexpr int kResultBytes = kPagedWarps * 8 * NB * kResultStride * 4;
-  static constexpr int kRingBytes = kKw * kStages * kStageBytes;
+  static constexpr int kRingBytes = kStages * kStageBytes;
   static constexpr int kOffRows = kRingBytes > kResultBytes ? kRingBytes : kResultBytes;  // what each row sees
-  static constexpr int kOffMeta = kOffRows + kRows * 16;  // [group][stage][2] scales of a step's boxes
-  static constexpr int kOffBar = kOffMeta + kKw * kStages * 32;
-  static constexpr int kSmemBytes = kOffBar + 16 * kKw * kStages + 32 + 1024;  // + alignment slack
+  static constexpr int kOffMeta = kOffRows + kRows * 16;  // [stage][8] scales and places of a step's boxes
+  static constexpr int kOffBar = kOffMeta + kStages * 128;
+  static constexpr int kSmemBytes = kOffBar + 16 * kStages + 32 + 1024;  // + alignment slack
+  static constexpr uint32_t kRegsOther = 40, kRegsMath = 216;  // their sum: what two blocks' launches have
 };
 
 // 8 x 8 16-bit elements, two neighbours of a row a lane, transposed.
@@ -118,175 +125,76 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   return r;
 }
 
-// What a row sees: new tokens by the word's bits, others above lo or below sinks.
+// What a row sees: new token u by bit u, and of the rows before the new tokens (before
+// old_end; 0: it sees nothing at all) what lies above lo or among the first keys.
 struct PagedRow {
-  uint64_t word;  // 0: nothing
-  int lo, sinks;
+  uint64_t news;
+  int lo, old_end;
 };
 
+__device__ __forceinline__ uint64_t bits64_upto(int hi) { return hi >= 63 ? ~0ull : (hi < 0 ? 0ull : (2ull << hi) - 1); }
+// Keys j .. j + 15 of these, bit i key j + i.
+__device__ __forceinline__ uint32_t paged_sees(const PagedRow& y, int j, int base, int sinks) {
+  const uint32_t old = bits_upto(y.old_end - 1 - j, 0) & (~bits_upto(y.lo - j, 0) | bits_upto(sinks - 1 - j, 0));
+  const int d = j - base;
+  const uint64_t at = d >= 0 ? (d < 64 ? y.news >> d : 0) : (d > -16 ? y.news << -d : 0);
+  return (old | static_cast<uint32_t>(at)) & 0xffffu;
+}
+
+// The math warps: all of the share's keys, then their results, joined.
 template <typename T, int DP, int NB, int RW>
-__global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads)
-    vattn_paged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                       const __grid_constant__ PagedParams p) {
+__device__ __forceinline__ void paged_math(const PagedParams& p, const Pipe& pipe, uint8_t* smem, uint32_t smem_s,
+                                           const PagedRow* rows, const PagedSpan& sp, uint32_t bk, int b,
+                                           int kh, int rb, int split) {
   using P = PagedPlan<DP, NB, RW>;
   constexpr int CH = DP / 16;  // 16-byte chunks of a shared row, 16-element steps of a product
   constexpr int RS = P::kResultStride, S = P::kStages;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ int kpos[VATTN_MAX_NEW_TOKENS];
-  const uint32_t raw_s = ptx::smem_addr(smem_raw);
-  const uint32_t smem_s = (raw_s + 1023u) & ~1023u;
-  uint8_t* const smem = smem_raw + (smem_s - raw_s);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   const int rw = warp % RW, kw = warp / RW;
   const uint32_t bar0 = smem_s + P::kOffBar;
-  auto full = [bar0, kw](int st) -> uint32_t { return bar0 + 8u * (kw * S + st); };
-  auto empty = [bar0, kw](int st) -> uint32_t { return bar0 + 8u * ((P::kKw + kw) * S + st); };
-  const Pipe pipe{bar0 + 16u * P::kKw * S};
+  auto full = [bar0](int st) -> uint32_t { return bar0 + 8u * st; };
+  auto empty = [bar0](int st) -> uint32_t { return bar0 + 8u * (S + st); };
   const WindowParams& w = p.w;
-  const int D = w.dim;
-  uint32_t split_u, rb_u, kh_u;
-  const uint32_t bk = p.d_row_blocks.div(p.d_splits.div(blockIdx.x, &split_u), &rb_u);
-  const int b = static_cast<int>(p.d_kv_heads.div(bk, &kh_u));
-  const int split = static_cast<int>(split_u), rb = static_cast<int>(rb_u), kh = static_cast<int>(kh_u);
+  const int D = w.dim, log_boxes = P::kLogStep - p.log_box;
   const bool clustered = p.splits > 1 && p.splits <= kPagedCluster;
-
-  if (tid == 0) {
-    for (int i = 0; i < P::kKw * S; ++i) {
-      ptx::mbar_init(bar0 + 8u * i, 1);
-      ptx::mbar_init(bar0 + 8u * (P::kKw * S + i), RW);
+  float* const res = reinterpret_cast<float*>(smem);  // results, over the ring: [group of keys][kRows][RS]
+  // ---- q's elements that this lane needs, on their way while the first boxes are
+  const int g = lane >> 2, c4 = lane & 3;
+  Vec<T, 4> q_raw[CH][NB];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const int rr = rb * P::kRows + rw * 8 * NB + nb * 8 + g;
+    uint32_t head;
+    const int t = static_cast<int>(p.d_group.div(static_cast<uint32_t>(rr), &head));
+    const T* q_row = rows_at<T>(p.q, b, kh * w.group + static_cast<int>(head), t) + c4 * 4;
+#pragma unroll
+    for (int ks = 0; ks < CH; ++ks) {
+#pragma unroll
+      for (int f = 0; f < 4; ++f) q_raw[ks][nb].e[f] = Elem<T>::narrow(0.0f);
+      if (rr < p.rows && ks * 16 < D) q_raw[ks][nb] = *reinterpret_cast<const Vec<T, 4>*>(q_row + ks * 16);
     }
-    pipe.init(w, p.status);
-    ptx::fence_mbar_init();
-    ptx::prefetch_tensormap(&tm_k);
-    ptx::prefetch_tensormap(&tm_v);
   }
-  ptx::grid_dep_wait();
-  const PagedSpan sp = PagedSpan::make(w, p.log_box, P::kKw, b, p.splits);
   const int v0 = split * sp.per, v1 = min(sp.n, v0 + sp.per);
-  const int shares = sp.shares();
-  if (!clustered && split >= shares) return;  // (in a cluster: with no keys, but at its barriers)
-  if (tid < w.n_queries) kpos[tid] = sp.base + __popcll(cached_word(w, b, tid, sp.base)) - 1;
-  PagedRow* const rows = reinterpret_cast<PagedRow*>(smem + P::kOffRows);
-  if (tid < P::kRows) {
-    const int rr = rb * P::kRows + tid;
-    PagedRow y{0, 0x7fffffff, 0};
-    if (rr < p.rows) y.word = cached_word(w, b, static_cast<int>(p.d_group.div(static_cast<uint32_t>(rr))), sp.base);
-    if (y.word != 0) {
-      y.lo = sp.base + __popcll(y.word) - 1 - w.window;
-      y.sinks = w.sinks;
-    }
-    rows[tid] = y;
-  }
-  __syncthreads();
-
-  // ---- the group's steps: 32 keys each, as one box or two; its boxes numbered through
-  const int log_boxes = 5 - p.log_box, boxes = 1 << log_boxes;
-  static_assert(kPagedKeys == 32, "log_boxes");
-  const int all_steps = (max(v1 - v0, 0) + boxes - 1) >> log_boxes;
-  const int steps = (all_steps - kw + P::kKw - 1) / P::kKw;
-  auto box_of = [&](int i) -> int { return v0 + ((((i >> log_boxes) * P::kKw + kw) << log_boxes) | (i & (boxes - 1))); };
-
-  // ---- loads (the group's first warp): lane i has what box i of 32 needs, page, row
-  // and scales, and of the 32 after (half way on: the scales too)
-  struct Box {
-    int page, row, key0;          // page: behind the last if it is not there, and reads as zeros
-    float k, log2_v, inv_v;       // k < 0: the keys are not there
-  };
-  auto place = [&](int i, Box& x) {  // of the group's box i
-    const int at = box_of(i);
-    x.key0 = sp.box(at) << p.log_box;
-    x.page = static_cast<int>(p.n_pages);
-    uint32_t row = 0;
-    if (at < v1) {
-      const uint32_t lp = p.d_page.div(static_cast<uint32_t>(x.key0), &row);
-      const int id = p.table[static_cast<long long>(b) * p.max_pages + lp];
-      if (id >= 0 && id < p.n_pages) x.page = id;
-    }
-    x.row = static_cast<int>(row);
-  };
-  auto scales = [&](Box& x) {
-    x.k = -1.0f;
-    x.log2_v = x.inv_v = 0.0f;
-    if (x.page >= p.n_pages) return;
-    const long long at = static_cast<long long>(x.page) * w.kv_heads + kh;
-    const float v = p.v_scale[at];
-    x.k = p.k_scale[at];
-    x.log2_v = log2f(v);
-    x.inv_v = 1.0f / v;
-  };
-  int issued = 0, issue_st = 0;  // steps, and the next one's place in the ring
-  Box now{}, next{};
-  const uint64_t once = ptx::policy_evict_first();
-  // The copies of a step's boxes, lanes l0 and l0 + 1 of `now`, to place st.
-  auto copies = [&](int st, int l0) {
-    const int pg = __shfl_sync(0xffffffffu, now.page, l0), row = __shfl_sync(0xffffffffu, now.row, l0);
-    const uint32_t to = smem_s + static_cast<uint32_t>((kw * S + st) * P::kStageBytes);
-    if (ptx::elect_one()) {
-      ptx::tma_load_4d_hint(to, &tm_k, full(st), 0, row, kh, pg, once);
-      ptx::tma_load_4d_hint(to + P::kTileBytes, &tm_v, full(st), 0, row, kh, pg, once);
-    }
-    if (log_boxes == 0) return;
-    const int pg1 = __shfl_sync(0xffffffffu, now.page, l0 + 1), row1 = __shfl_sync(0xffffffffu, now.row, l0 + 1);
-    if (ptx::elect_one()) {  // (of a box behind the share: zeros)
-      ptx::tma_load_4d_hint(to + 16 * DP, &tm_k, full(st), 0, row1, kh, pg1, once);
-      ptx::tma_load_4d_hint(to + P::kTileBytes + 16 * DP, &tm_v, full(st), 0, row1, kh, pg1, once);
-    }
-  };
-  // What the products need beside them, and the barrier's count, which the copies may be ahead of.
-  auto announce = [&](int st, int l0) {
-    const int which = lane - l0;
-    if (which >= 0 && which < boxes)
-      ptx::st_shared_v4(smem_s + P::kOffMeta + static_cast<uint32_t>(((kw * S + st) * 2 + which) * 16), now.k, now.log2_v,
-                        now.inv_v, __int_as_float(now.key0));
-    __syncwarp();
-    if (ptx::elect_one()) ptx::mbar_arrive_expect_tx(full(st), P::kStageBytes);
-  };
-  auto issue = [&]() {
-    const int st = issue_st, i0 = issued << log_boxes, l0 = i0 & 31;
-    issue_st = st + 1 == S ? 0 : st + 1;
-    if (l0 == 0) {
-      now = next;
-      place(i0 + 32 + lane, next);
-    } else if (l0 == 16) {
-      scales(next);
-    }
-    announce(st, l0);
-    copies(st, l0);
-    ++issued;
-  };
-  if (rw == 0 && steps > 0) {
-    place(lane, now);
-    const int first = min(S, steps);  // S steps are 12 boxes at most
-    for (int i = 0; i < first; ++i) copies(i, i << log_boxes);
-    scales(now);
-    place(32 + lane, next);
-    for (int i = 0; i < first; ++i) announce(i, i << log_boxes);
-    issued = first;
-    issue_st = first == S ? 0 : first;
-  }
+  const int steps = (max(v1 - v0, 0) + (1 << log_boxes) - 1) >> log_boxes;
+  ptx::named_barrier_sync(1, P::kThreads);  // barriers and rows are there
 
   // ---- q as columns: lane / 4 of each eight rows, in the order of K's bytes
-  const int g = lane >> 2, c4 = lane & 3;
   uint32_t qf[CH][NB][2];
   float row_c[NB][2];  // of rows 2 c4 and 2 c4 + 1: from a product's sum to log2 units, but for the key's scale
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
-    const int r = rw * 8 * NB + nb * 8 + g;
-    uint32_t head;
-    const int t = static_cast<int>(p.d_group.div(static_cast<uint32_t>(rb * P::kRows + r), &head));
-    const T* qrow = rows[r].word != 0 ? rows_at<T>(p.q, b, kh * w.group + static_cast<int>(head), t) : nullptr;
+    const PagedRow row = rows[rw * 8 * NB + nb * 8 + g];
+    const bool on = row.news != 0 || row.old_end != 0;
     float y[CH][4];
     float most = 0.0f, c = p.scale_log2;
 #pragma unroll
     for (int ks = 0; ks < CH; ++ks) {
-      Vec<T, 4> x;
+      q_raw[ks][nb].widen(y[ks]);
 #pragma unroll
-      for (int f = 0; f < 4; ++f) x.e[f] = Elem<T>::narrow(0.0f);
-      if (qrow != nullptr && ks * 16 < D) x = *reinterpret_cast<const Vec<T, 4>*>(qrow + ks * 16 + c4 * 4);
-      x.widen(y[ks]);
-      if constexpr (Elem<T>::kBf16)
-#pragma unroll
-        for (int f = 0; f < 4; ++f) most = fmaxf(most, fabsf(y[ks][f]) < INFINITY ? fabsf(y[ks][f]) : 0.0f);
+      for (int f = 0; f < 4; ++f) {
+        y[ks][f] = on ? y[ks][f] : 0.0f;
+        if constexpr (Elem<T>::kBf16) most = fmaxf(most, fabsf(y[ks][f]) < INFINITY ? fabsf(y[ks][f]) : 0.0f);
+      }
     }
     if constexpr (Elem<T>::kBf16) {
       most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
@@ -331,63 +239,102 @@ __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads)
   uint32_t turn = 0;
   for (; step < steps; ++step) {
     if (!pipe.wait_warp(full(st), turn, kSitePagedMath)) break;
-    const uint32_t ks_s = smem_s + static_cast<uint32_t>((kw * S + st) * P::kStageBytes);
+    const uint32_t ks_s = smem_s + static_cast<uint32_t>(st * P::kStageBytes + kw * kPagedKeys * DP);
     const uint32_t vs_s = ks_s + P::kTileBytes;
-    // the step's keys by 16: first of each in the sequence, scales; those that are
+    uint32_t kf[CH][4];
+#pragma unroll
+    for (int ks = 0; ks < CH; ++ks)  // matrices: keys 0-7, 8-15, 16-23, 24-31 by the 16 dims of chunk ks
+      ldmatrix_x4(ks_s + static_cast<uint32_t>(lane * DP + (paged_swizzled<CH>(lane, ks) << 4)), kf[ks]);
+    // the warp's keys by 16: first of each in the sequence, scales; those that are
     // not there, or that no row sees, count as masked throughout
     int j0[2];
     float4 meta[2];
     bool masked[2];
-    const uint32_t meta_s = smem_s + P::kOffMeta + static_cast<uint32_t>((kw * S + st) * 32);
-    meta[0] = ptx::ld_shared_v4(meta_s);
-    meta[1] = ptx::ld_shared_v4(meta_s + (log_boxes << 4));
 #pragma unroll
     for (int mb = 0; mb < 2; ++mb) {
-      const int j = __float_as_int(meta[mb].w) + (mb == 1 && log_boxes == 0 ? 16 : 0);
+      const int at = kw * kPagedKeys + mb * 16;
+      meta[mb] = ptx::ld_shared_v4(smem_s + P::kOffMeta + static_cast<uint32_t>((st * 8 + (at >> p.log_box)) * 16));
+      const int j = __float_as_int(meta[mb].w) + (at & (p.box - 1));
       const bool on = !(meta[mb].x < 0.0f);
-      j0[mb] = on ? j : 0x7fffff00;
+      j0[mb] = on ? j : 1 << 30;
       if (!on) meta[mb] = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
       masked[mb] = !on || j + 15 >= free_end || (j < free_begin && j + 15 >= w.sinks);
     }
     const bool some = masked[0] || masked[1];
-    // ---- S = K Q^T
-    float s[2][NB][4];  // keys 16 mb + g, + 8 (e / 2) of rows 2 c4, + 1 (e % 2)
+    // ---- S = K Q^T, over the even and the odd chunks by themselves where that
+    // leaves the tensor core fewer products in a row on one sum
+    constexpr int PART = NB == 1 ? 2 : 1;
+    float s[2][NB][4], s_odd[2][NB][4];  // keys 16 mb + g, + 8 (e / 2) of rows 2 c4, + 1 (e % 2)
 #pragma unroll
     for (int mb = 0; mb < 2; ++mb)
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[mb][nb][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) s[mb][nb][e] = s_odd[mb][nb][e] = 0.0f;
 #pragma unroll
-    for (int ks = 0; ks < CH; ++ks) {
-      // matrices: keys 0-7, 8-15, 16-23, 24-31 by the 16 dims of chunk ks
-      uint32_t kf[4];
-      ldmatrix_x4(ks_s + static_cast<uint32_t>(lane * DP + (paged_swizzled<CH>(lane, ks) << 4)), kf);
+    for (int ks = 0; ks < CH; ++ks)
 #pragma unroll
       for (int mb = 0; mb < 2; ++mb) {
-        const uint32_t a[4] = {e4m3_half2_lo(kf[2 * mb]), e4m3_half2_lo(kf[2 * mb + 1]), e4m3_half2_hi(kf[2 * mb]),
-                               e4m3_half2_hi(kf[2 * mb + 1])};
+        const uint32_t a[4] = {e4m3_half2_lo(kf[ks][2 * mb]), e4m3_half2_lo(kf[ks][2 * mb + 1]),
+                               e4m3_half2_hi(kf[ks][2 * mb]), e4m3_half2_hi(kf[ks][2 * mb + 1])};
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) mma_16816<__half>(s[mb][nb], a, qf[ks][nb][0], qf[ks][nb][1]);
+        for (int nb = 0; nb < NB; ++nb)
+          mma_16816<__half>(ks % PART ? s_odd[mb][nb] : s[mb][nb], a, qf[ks][nb][0], qf[ks][nb][1]);
       }
-    }
-    // ---- masks: at the sequence's end, the first keys' end, the window's edge, among the new tokens
-    auto sees = [&](int r, int j) {
-      const PagedRow y = rows[r];
-      const int u = j - sp.base;
-      const int at = u >= 0 && j < sp.len ? kpos[u] : j;
-      return j < sp.len && (u < 0 || ((y.word >> u) & 1)) && (at > y.lo || at < y.sinks);
-    };
-    const int r0 = rw * 8 * NB + 2 * c4;
-    if (some) {
+    if (PART == 2) {
 #pragma unroll
-      for (int mb = 0; mb < 2; ++mb) {
-        if (!masked[mb]) continue;
+      for (int mb = 0; mb < 2; ++mb)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (!sees(r0 + nb * 8 + (e & 1), j0[mb] + g + 8 * (e >> 1))) s[mb][nb][e] = -INFINITY;
+          for (int e = 0; e < 4; ++e) s[mb][nb][e] += s_odd[mb][nb][e];
+    }
+    uint32_t vf[CH][4];  // the same matrices of V, transposed by pairs of dims, ahead of their use
+#pragma unroll
+    for (int n = 0; n < CH; ++n)
+      ldmatrix_x4_trans(vs_s + static_cast<uint32_t>(lane * DP + (paged_swizzled<CH>(lane, n) << 4)), vf[n]);
+    // ---- masks: at the sequence's end, the first keys' end, the window's edge, among
+    // the new tokens.  Lane i looks up row i % 16 (of the warp) and keys i / 16.
+    bool loops = false;
+    uint32_t see[2][NB][2];  // of rows 2 c4 + e: 16 keys a word, where masked
+    if (some) {
+      const int mb = lane >> 4, r = lane & (8 * NB - 1), j = mb ? j0[1] : j0[0];
+      const PagedRow y = rows[rw * 8 * NB + r];
+      const uint32_t mine = paged_sees(y, j, sp.base, w.sinks);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            see[k][nb][e] = __shfl_sync(0xffffffffu, mine, 16 * k + nb * 8 + 2 * c4 + e) >> g;  // its keys g and g + 8
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (!((see[k][nb][e] >> (8 * h)) & 1u)) s[k][nb][2 * h + e] = -INFINITY;
+          }
+      // V of keys that no query sees may hold anything: zeros
+      const uint32_t alive = bits_upto(sp.len - 1 - j, 0) & (~bits_upto(sp.first - 1 - j, 0) | bits_upto(w.sinks - 1 - j, 0));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {  // keys 8 q + 2 c4, + 1: low and high halves
+        const uint32_t a = __shfl_sync(0xffffffffu, alive, 8 * q) >> (8 * (q & 1) + 2 * c4);
+        const uint32_t keep = (a & 1u ? 0xffffu : 0u) | (a & 2u ? 0xffff0000u : 0u);
+#pragma unroll
+        for (int n = 0; n < CH; ++n) vf[n][q] &= keep;
+      }
+      // a NaN in a key that some rows see and others do not: loops over the visible pairs
+      const bool live = y.old_end != 0 || y.news != 0;
+      const uint32_t any = live ? mine : 0u, every = live ? mine : 0xffffu;
+      const uint32_t half = mb ? 0xffff0000u : 0x0000ffffu;
+      const uint32_t any_w = __reduce_or_sync(0xffffffffu, (any << (16 * mb)) & half);
+      const uint32_t every_w = __reduce_and_sync(0xffffffffu, (every << (16 * mb)) | ~half);
+      if ((any_w & ~every_w) != 0) {
+        uint32_t bad = 0;
+#pragma unroll
+        for (int n = 0; n < CH; ++n)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)  // a byte's low seven bits all ones: a carry out of them
+            bad |= ((vf[n][q] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+        loops = __any_sync(0xffffffffu, bad != 0);
       }
     }
     // ---- online softmax, two rows a lane for each eight, eight lanes a row; a row is
@@ -439,30 +386,6 @@ __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads)
         }
       }
     // ---- O += V P
-    bool loops = false;
-    if (some) {
-      // rows that no query sees may hold anything: zeros; a NaN in another that
-      // some do not see: loops over the visible pairs
-      bool bad = false;
-#pragma unroll
-      for (int y = lane; y < kPagedKeys * CH; y += 32) {
-        const int r = y / CH, c = y % CH, mb = r >> 4, j = (mb ? j0[1] : j0[0]) + (r & 15);
-        if (!(mb ? masked[1] : masked[0])) continue;
-        const uint32_t at = vs_s + static_cast<uint32_t>(r * DP + (paged_swizzled<CH>(r, c) << 4));
-        if (j >= sp.len || (j < sp.first && j >= w.sinks)) {
-          ptx::st_shared_v4(at, 0.0f, 0.0f, 0.0f, 0.0f);
-          continue;
-        }
-        const float4 z = ptx::ld_shared_v4(at);
-        const uint32_t zs[4] = {__float_as_uint(z.x), __float_as_uint(z.y), __float_as_uint(z.z), __float_as_uint(z.w)};
-#pragma unroll
-        for (int f = 0; f < 4; ++f)  // a byte's low seven bits all ones: a carry out of them
-          bad |= (((zs[f] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
-      }
-      ptx::fence_proxy_async_smem();  // before the ring's next copy there
-      loops = __any_sync(0xffffffffu, bad);
-      __syncwarp();
-    }
     if (!loops) {
       uint32_t pf[2][NB][2];
 #pragma unroll
@@ -474,27 +397,24 @@ __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads)
             pf[mb][nb][e] = movmatrix_trans(pack2<__half>(s[mb][nb][2 * e], s[mb][nb][2 * e + 1]));
 #pragma unroll
       for (int n = 0; n < CH; ++n) {
-        // matrices: keys 0-7, 8-15, 16-23, 24-31 by the 16 dims of chunk n, transposed by pairs of dims
-        uint32_t vf[4];
-        ldmatrix_x4_trans(vs_s + static_cast<uint32_t>(lane * DP + (paged_swizzled<CH>(lane, n) << 4)), vf);
 #pragma unroll
-        for (int y = 0; y < 4; ++y) vf[y] = __byte_perm(vf[y], 0u, 0x3120);
+        for (int y = 0; y < 4; ++y) vf[n][y] = __byte_perm(vf[n][y], 0u, 0x3120);
 #pragma unroll
         for (int mb = 0; mb < 2; ++mb) {
-          const uint32_t a[4] = {e4m3_half2_lo(vf[2 * mb]), e4m3_half2_hi(vf[2 * mb]), e4m3_half2_lo(vf[2 * mb + 1]),
-                                 e4m3_half2_hi(vf[2 * mb + 1])};
+          const uint32_t a[4] = {e4m3_half2_lo(vf[n][2 * mb]), e4m3_half2_hi(vf[n][2 * mb]),
+                                 e4m3_half2_lo(vf[n][2 * mb + 1]), e4m3_half2_hi(vf[n][2 * mb + 1])};
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) mma_16816<__half>(o[n][nb], a, pf[mb][nb][0], pf[mb][nb][1]);
         }
       }
     } else {
 #pragma unroll
-      for (int mb = 0; mb < 2; ++mb)
+      for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (!sees(r0 + nb * 8 + (e & 1), j0[mb] + g + 8 * (e >> 1))) s[mb][nb][e] = -1.0f;
+            if (!((see[k][nb][e & 1] >> (8 * (e >> 1))) & 1u)) s[k][nb][e] = -1.0f;
 #pragma unroll 1
       for (int y = 0; y < 8; ++y)
 #pragma unroll
@@ -522,26 +442,13 @@ __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads)
           }
         }
     }
-    if (RW > 1) pipe_warp_arrive(empty(st));
-    else __syncwarp();
-    if (rw == 0 && issued < steps) {
-      if (RW > 1 && !pipe.wait_warp(empty(st), turn, kSitePagedLoad)) {
-        ++step;
-        break;
-      }
-      issue();
-    }
+    pipe_warp_arrive(empty(st));
     if (++st == S) {
       st = 0;
       turn ^= 1;
     }
   }
-  if (rw == 0 && lane == 0)  // after a wait that ran out: the copies in flight land before the block exits
-    for (; step < issued; ++step) pipe.drain(full(step % S), static_cast<uint32_t>((step / S) & 1), kSitePagedDrain);
-  __syncthreads();  // the rings are free: the warps' results go there
-
-  // ---- join the warps that shared the keys
-  float* res = reinterpret_cast<float*>(smem);  // [group of keys][kRows][RS]
+  ptx::named_barrier_sync(2, 32 * kPagedWarps);  // the ring is free: the warps' results go there
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -553,7 +460,8 @@ __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads)
       for (int n = 0; n < CH; ++n) *reinterpret_cast<float2*>(to + n * 16 + 2 * g) = make_float2(o[n][nb][e], o[n][nb][e + 2]);
       if (g == 0) *reinterpret_cast<float2*>(to + DP) = make_float2(m[nb][e], l[nb][e]);
     }
-  __syncthreads();
+  ptx::named_barrier_sync(2, 32 * kPagedWarps);
+  // ---- join the warps that shared the keys
   auto write = [&](int rr, int d, float sum, float (&acc)[8]) {
     uint32_t head;
     const int t = static_cast<int>(p.d_group.div(static_cast<uint32_t>(rr), &head));
@@ -563,9 +471,9 @@ __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads)
     for (int e = 0; e < 8; ++e) acc[e] = none ? 0.0f : acc[e] * inv;
     reinterpret_cast<Vec<T, 8>*>(rows_at_mut<T>(p.out, b, kh * w.group + static_cast<int>(head), t) + d)->narrow(acc);
   };
-  const bool alone = p.splits == 1 || (shares == 1 && !clustered);
+  const bool alone = p.splits == 1 || (sp.one() && !clustered);
   const int per_row = D / 8;
-  for (int x = tid; x < P::kRows * per_row; x += P::kThreads) {
+  for (int x = tid; x < P::kRows * per_row; x += 32 * kPagedWarps) {
     const int r = x / per_row, d = (x - r * per_row) * 8;
     const int rr = rb * P::kRows + r;
     if (rr >= p.rows) continue;
@@ -600,7 +508,7 @@ __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads)
     ptx::grid_dep_launch();
     return;
   }
-  __syncthreads();
+  ptx::named_barrier_sync(2, 32 * kPagedWarps);
   if (tid < P::kRows) {
     float* row = res + tid * RS;
     float mx = -INFINITY, sum = 0.0f;
@@ -615,7 +523,8 @@ __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads)
     *reinterpret_cast<float2*>(row + DP) = make_float2(mx, sum);
   }
   ptx::cluster_sync();
-  for (int x = split * P::kThreads + tid; x < P::kRows * per_row; x += p.splits * P::kThreads) {
+  const int shares = sp.shares();
+  for (int x = split * 32 * kPagedWarps + tid; x < P::kRows * per_row; x += p.splits * 32 * kPagedWarps) {
     const int r = x / per_row, d = (x - r * per_row) * 8;
     const int rr = rb * P::kRows + r;
     if (rr >= p.rows) continue;
@@ -648,6 +557,159 @@ __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads)
   ptx::grid_dep_launch();
 }
 
+template <typename T, int DP, int NB, int RW>
+__global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads, 2)
+    vattn_paged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                       const __grid_constant__ PagedParams p) {
+  using P = PagedPlan<DP, NB, RW>;
+  constexpr int S = P::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int kpos[VATTN_MAX_NEW_TOKENS];
+  const uint32_t raw_s = ptx::smem_addr(smem_raw);
+  const uint32_t smem_s = (raw_s + 1023u) & ~1023u;
+  uint8_t* const smem = smem_raw + (smem_s - raw_s);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t bar0 = smem_s + P::kOffBar;
+  auto full = [bar0](int st) -> uint32_t { return bar0 + 8u * st; };
+  auto empty = [bar0](int st) -> uint32_t { return bar0 + 8u * (S + st); };
+  const Pipe pipe{bar0 + 16u * S};
+  const WindowParams& w = p.w;
+  uint32_t split_u, rb_u, kh_u;
+  const uint32_t bk = p.d_row_blocks.div(p.d_splits.div(blockIdx.x, &split_u), &rb_u);
+  const int b = static_cast<int>(p.d_kv_heads.div(bk, &kh_u));
+  const int split = static_cast<int>(split_u), rb = static_cast<int>(rb_u), kh = static_cast<int>(kh_u);
+  const bool clustered = p.splits > 1 && p.splits <= kPagedCluster;
+
+  PagedRow* const rows = reinterpret_cast<PagedRow*>(smem + P::kOffRows);
+  const int log_boxes = P::kLogStep - p.log_box, boxes = 1 << log_boxes;  // of a step
+  if (warp == kPagedWarps && lane == 0) {
+    for (int i = 0; i < S; ++i) {
+      ptx::mbar_init(full(i), boxes > 1 ? 4 : 2);  // the loaders that have boxes
+      ptx::mbar_init(empty(i), kPagedWarps);
+    }
+    pipe.init(w, p.status);
+    ptx::fence_mbar_init();
+    ptx::prefetch_tensormap(&tm_k);
+    ptx::prefetch_tensormap(&tm_v);
+  }
+  ptx::grid_dep_wait();
+  const PagedSpan sp = PagedSpan::make(w, p.log_box, P::kKw, b, p.d_splits);
+  if (!clustered && !sp.has(split)) return;  // (in a cluster: with no keys, but at its barriers)
+  if (warp >= kPagedWarps) {
+    ptx::regs_decrease<P::kRegsOther>();
+    const int v0 = split * sp.per, v1 = min(sp.n, v0 + sp.per);
+    const int steps = (max(v1 - v0, 0) + boxes - 1) >> log_boxes;
+    // ------------------------------------------------------ boxes into the ring
+    // lane i has what box i of 32 needs, and of the 32 after
+    const int loader = warp - kPagedWarps, mine = boxes - (loader >> 1);  // boxes loader / 2, + 2, ... of a step's K or V
+    struct Box {
+      int page, row, key0;          // page: behind the last if it is not there, and reads as zeros
+      float k, log2_v, inv_v;       // k < 0: the keys are not there
+    };
+    auto place = [&](int i, Box& x) {  // of the share's box i
+      x.key0 = sp.box(v0 + i) << p.log_box;
+      x.page = static_cast<int>(p.n_pages);
+      uint32_t row = 0;
+      if (v0 + i < v1) {
+        const uint32_t lp = p.d_page.div(static_cast<uint32_t>(x.key0), &row);
+        const int id = p.table[static_cast<long long>(b) * p.max_pages + lp];
+        if (id >= 0 && id < p.n_pages) x.page = id;
+      }
+      x.row = static_cast<int>(row);
+    };
+    auto scales = [&](Box& x) {  // (the first loader's)
+      x.k = -1.0f;
+      x.log2_v = x.inv_v = 0.0f;
+      if (loader != 0 || x.page >= p.n_pages) return;
+      const long long at = static_cast<long long>(x.page) * w.kv_heads + kh;
+      const float v = p.v_scale[at];
+      x.k = p.k_scale[at];
+      x.log2_v = log2f(v);
+      x.inv_v = 1.0f / v;
+    };
+    Box now{}, next{};
+    const uint64_t once = ptx::policy_evict_first();
+    const CUtensorMap* const tm = (loader & 1) != 0 ? &tm_v : &tm_k;
+    // The copies of a step, whose boxes are with lanes l0, l0 + 1, ..., to place st.
+    auto copies = [&](int st, int l0) {
+      for (int i = loader >> 1; i < boxes; i += 2) {
+        const int pg = __shfl_sync(0xffffffffu, now.page, l0 + i), row = __shfl_sync(0xffffffffu, now.row, l0 + i);
+        const uint32_t to = smem_s + static_cast<uint32_t>(st * P::kStageBytes + (loader & 1) * P::kTileBytes + i * (DP << p.log_box));
+        if (ptx::elect_one()) ptx::tma_load_4d_hint(to, tm, full(st), 0, row, kh, pg, once);
+      }
+    };
+    // What the products need beside them, and the barrier's count, which the copies may be ahead of.
+    auto announce = [&](int st, int l0) {
+      const int which = lane - l0;
+      if (loader == 0 && which >= 0 && which < boxes)
+        ptx::st_shared_v4(smem_s + P::kOffMeta + static_cast<uint32_t>((st * 8 + which) * 16), now.k, now.log2_v, now.inv_v,
+                          __int_as_float(now.key0));
+      __syncwarp();
+      if (mine > 0 && ptx::elect_one())
+        ptx::mbar_arrive_expect_tx(full(st), static_cast<uint32_t>(((mine + 1) >> 1) * (DP << p.log_box)));
+    };
+    place(lane, now);
+    ptx::named_barrier_sync(3, P::kThreads - 32 * kPagedWarps);  // the barriers
+    const int first = min(min(S, steps), 32 >> log_boxes);
+    for (int i = 0; i < first; ++i) copies(i, i << log_boxes);
+    scales(now);
+    place(32 + lane, next);
+    // positions of the new tokens of a tree, then what each row sees
+    constexpr int kLoaderThreads = P::kThreads - 32 * kPagedWarps;
+    const int lt = tid - 32 * kPagedWarps;
+    if (w.tree != nullptr) {
+      if (lt < w.n_queries) kpos[lt] = sp.base + __popcll(cached_word(w, b, lt, sp.base)) - 1;
+      ptx::named_barrier_sync(3, kLoaderThreads);
+    }
+    static_assert(P::kRows <= kLoaderThreads && VATTN_MAX_NEW_TOKENS <= kLoaderThreads, "a thread each");
+    if (lt < P::kRows) {
+      const int rr = rb * P::kRows + lt;
+      const int t = static_cast<int>(p.d_group.div(static_cast<uint32_t>(rr)));
+      PagedRow y{rr < p.rows ? cached_word(w, b, t, sp.base) : 0, 0x7fffffff, 0};
+      if (y.news != 0) {
+        y.old_end = max(0, sp.base);
+        y.lo = sp.base + __popcll(y.news) - 1 - w.window;
+        if (w.tree == nullptr) {
+          y.news &= ~bits64_upto(t - w.window) | bits64_upto(w.sinks - 1 - sp.base);
+        } else if (y.lo >= sp.base) {  // a window inside the tree
+          for (uint64_t left = y.news; left != 0; left &= left - 1) {
+            const int u = __ffsll(static_cast<long long>(left)) - 1, at = kpos[u];
+            if (at <= y.lo && at >= w.sinks) y.news &= ~(1ull << u);
+          }
+        }
+      }
+      rows[lt] = y;
+    }
+    for (int i = 0; i < first; ++i) announce(i, i << log_boxes);
+    ptx::named_barrier_sync(1, P::kThreads);
+    int step = first, st = first == S ? 0 : first;
+    uint32_t turn = first == S ? 0u : 1u;  // of the place's last use, which is awaited
+    bool ok = true;
+    for (; step < steps; ++step) {
+      const int i0 = step << log_boxes, l0 = i0 & 31;
+      if (l0 == 0) {
+        now = next;
+        scales(now);
+        place(i0 + 32 + lane, next);
+      }
+      if (!(ok = pipe.wait_warp(empty(st), turn, kSitePagedLoad))) break;
+      announce(st, l0);
+      copies(st, l0);
+      if (++st == S) {
+        st = 0;
+        turn ^= 1u;
+      }
+    }
+    if (!ok && lane == 0)  // the copies in flight land before the block exits
+      for (int d = max(0, step - S); d < step; ++d)
+        pipe.drain(full(d % S), static_cast<uint32_t>((d / S) & 1), kSitePagedDrain);
+    __syncwarp();
+  } else {
+    ptx::regs_increase<P::kRegsMath>();
+    paged_math<T, DP, NB, RW>(p, pipe, smem, smem_s, rows, sp, bk, b, kh, rb, split);
+  }
+}
+
 // Merges the shares of 32 dims of a row, one block each: the weight of every share
 // first, then eight lanes a share, 16 bytes a lane, add up every 32nd one, and the
 // block their sums, in a fixed order.
@@ -663,7 +725,7 @@ __global__ void __launch_bounds__(256) vattn_paged_join_kernel(const __grid_cons
   const int b = static_cast<int>(bk / w.kv_heads), kh = static_cast<int>(bk - static_cast<long long>(b) * w.kv_heads);
   const int t = rr / w.group, d = static_cast<int>(blockIdx.y) * 32 + (lane & 7) * 4;
   ptx::grid_dep_wait();
-  const PagedSpan sp = PagedSpan::make(w, p.log_box, KW, b, p.splits);
+  const PagedSpan sp = PagedSpan::make(w, p.log_box, KW, b, p.d_splits);
   const int shares = sp.shares();
   if (shares == 1) return;  // written by its block
   const bool none = cached_word(w, b, t, sp.base) == 0;
@@ -748,7 +810,7 @@ __global__ void __launch_bounds__(256) vattn_paged_join_few_kernel(const __grid_
   const int b = static_cast<int>(bk / w.kv_heads), kh = static_cast<int>(bk - static_cast<long long>(b) * w.kv_heads);
   const int t = rr / w.group;
   ptx::grid_dep_wait();
-  const PagedSpan sp = PagedSpan::make(w, p.log_box, KW, b, p.splits);
+  const PagedSpan sp = PagedSpan::make(w, p.log_box, KW, b, p.d_splits);
   const int shares = sp.shares();
   if (shares == 1) return;  // written by its block
   const bool none = cached_word(w, b, t, sp.base) == 0;

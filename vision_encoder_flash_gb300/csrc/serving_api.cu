@@ -146,6 +146,9 @@ vattn_status paged_launch(vattn::PagedParams p, const Pools& pools, int sms, int
   if (st != VATTN_OK) return st;
   int resident = 0;
   if ((st = resident_blocks(kernel, P::kThreads, P::kSmemBytes, known, device, &resident)) != VATTN_OK) return st;
+  p.log_box = P::kLogStep;  // boxes as large as a step, if pages are
+  while (p.page % (1 << p.log_box) != 0) --p.log_box;
+  p.box = 1 << p.log_box;
   const long long seqs = static_cast<long long>(p.w.batch) * p.w.kv_heads;
   p.row_blocks = (p.rows + P::kRows - 1) / P::kRows;
   if (seqs * p.row_blocks > kMaxRows || seqs * p.rows > INT32_MAX)
@@ -200,7 +203,8 @@ vattn_status paged_launch(vattn::PagedParams p, const Pools& pools, int sms, int
   if ((st = launched("paged attention kernel launch")) != VATTN_OK) return st;
   if (p.splits == 1) return VATTN_OK;
   const long long out_rows = seqs * p.rows;
-  if (p.splits <= 32)
+  const long long join_blocks = out_rows * ((p.w.dim + 31) / 32);
+  if (p.splits <= 32 && join_blocks > 2 * sms)  // a warp a row, else blocks that share a row
     st = launch_behind("paged attention join kernel launch", vattn::vattn_paged_join_few_kernel<T, P::kRows, P::kKw>,
                        dim3(static_cast<unsigned>((out_rows + 7) / 8)), dim3(256), 0, stream, p);
   else
@@ -226,14 +230,8 @@ vattn_status paged_rows(const vattn::PagedParams& p, const Pools& pools, int sms
 #endif
   if (p.rows <= 8) return paged_launch<T, DP, 1, 1>(p, pools, sms, device, stream);
   if (p.rows <= 16) return paged_launch<T, DP, 2, 1>(p, pools, sms, device, stream);
-  if constexpr (DP <= 64) {
-    if (p.rows <= 32) return paged_launch<T, DP, 4, 1>(p, pools, sms, device, stream);
-    if (p.rows <= 64) return paged_launch<T, DP, 4, 2>(p, pools, sms, device, stream);
-    return paged_launch<T, DP, 4, 4>(p, pools, sms, device, stream);
-  } else {
-    if (p.rows <= 32) return paged_launch<T, DP, 2, 2>(p, pools, sms, device, stream);
-    return paged_launch<T, DP, 2, 4>(p, pools, sms, device, stream);
-  }
+  if (p.rows <= 32) return paged_launch<T, DP, 2, 2>(p, pools, sms, device, stream);
+  return paged_launch<T, DP, 2, 4>(p, pools, sms, device, stream);
 }
 
 template <typename T>
@@ -378,8 +376,6 @@ vattn_status vattn_forward_paged(const vattn_rows* q, const vattn_pages* cache, 
   p.n_pages = cache->n_pages;
   p.max_pages = static_cast<int>(cache->max_pages);
   p.page = static_cast<int>(cache->page_size);
-  p.log_box = p.page % 32 == 0 ? 5 : 4;
-  p.box = 1 << p.log_box;
   p.rows = p.w.group * p.w.n_queries;
   p.scale_log2 = a->scale * vattn::kLog2E;
   p.d_page = fast_div(p.page);
