@@ -98,6 +98,12 @@ __device__ __forceinline__ int paged_swizzled(int r, int c) {
   return c ^ (CH == 8 ? r & 7 : CH == 4 ? (r >> 1) & 3 : (r >> 2) & 1);
 }
 
+// The same in a row of q, 2 DP bytes.
+template <int DP>
+__device__ __forceinline__ int paged_swizzled_q(int r, int c) {
+  return c ^ (DP >= 64 ? r & 7 : (r >> 1) & 3);
+}
+
 template <int DP, int NB, int RW>
 struct PagedPlan {
   static constexpr int kThreads = 256;
@@ -112,7 +118,8 @@ struct PagedPlan {
   static constexpr int kResultBytes = kPagedWarps * 8 * NB * kResultStride * 4;
   static constexpr int kRingBytes = kStages * kStageBytes;
   static constexpr int kOffRows = kRingBytes > kResultBytes ? kRingBytes : kResultBytes;  // what each row sees
-  static constexpr int kOffMeta = kOffRows + kRows * 16;  // [stage][8] scales and places of a step's boxes
+  static constexpr int kOffQ = kOffRows + kRows * 16;  // q as f16, rows of 2 DP bytes, and behind it each row's factor
+  static constexpr int kOffMeta = kOffQ + kRows * (2 * DP + 16);  // [stage][8] scales and places of a step's boxes
   static constexpr int kOffBar = kOffMeta + kStages * 128;
   static constexpr int kSmemBytes = kOffBar + 16 * kStages + 32 + 1024;  // + alignment slack
   static constexpr uint32_t kRegsOther = 40, kRegsMath = 216;  // their sum: what two blocks' launches have
@@ -158,63 +165,66 @@ __device__ __forceinline__ void paged_math(const PagedParams& p, const Pipe& pip
   const int D = w.dim, log_boxes = P::kLogStep - p.log_box;
   const bool clustered = p.splits > 1 && p.splits <= kPagedCluster;
   float* const res = reinterpret_cast<float*>(smem);  // results, over the ring: [group of keys][kRows][RS]
-  // ---- q's elements that this lane needs, on their way while the first boxes are
   const int g = lane >> 2, c4 = lane & 3;
-  Vec<T, 4> q_raw[CH][NB];
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    const int rr = rb * P::kRows + rw * 8 * NB + nb * 8 + g;
+  // ---- q to f16 in shared memory, DP / 8 lanes a row, the 16 elements of a product's
+  // step in the order of K's bytes: 4 c, 4 c + 1 of c = 0 .. 3, then 4 c + 2, 4 c + 3
+  // (rolled loops: this runs once, and most of its time was that of fetching its code)
+  const uint32_t q_s = smem_s + P::kOffQ;
+  float* const row_factor = reinterpret_cast<float*>(smem + P::kOffQ + P::kRows * 2 * DP);
+#pragma unroll 1
+  for (int i = tid; i < P::kRows * (DP / 8); i += 32 * kPagedWarps) {
+    const int r = i / (DP / 8), d = i % (DP / 8);  // 8 elements from 8 d on
+    const int rr = rb * P::kRows + r;
     uint32_t head;
     const int t = static_cast<int>(p.d_group.div(static_cast<uint32_t>(rr), &head));
-    const T* q_row = rows_at<T>(p.q, b, kh * w.group + static_cast<int>(head), t) + c4 * 4;
+    Vec<T, 8> x;
 #pragma unroll
-    for (int ks = 0; ks < CH; ++ks) {
+    for (int f = 0; f < 8; ++f) x.e[f] = Elem<T>::narrow(0.0f);
+    if (rr < p.rows && d * 8 < D)
+      x = *reinterpret_cast<const Vec<T, 8>*>(rows_at<T>(p.q, b, kh * w.group + static_cast<int>(head), t) + d * 8);
+    float y[8], factor = p.scale_log2;
+    x.widen(y);
+    if constexpr (Elem<T>::kBf16) {
+      float most = 0.0f;
 #pragma unroll
-      for (int f = 0; f < 4; ++f) q_raw[ks][nb].e[f] = Elem<T>::narrow(0.0f);
-      if (rr < p.rows && ks * 16 < D) q_raw[ks][nb] = *reinterpret_cast<const Vec<T, 4>*>(q_row + ks * 16);
+      for (int f = 0; f < 8; ++f) most = fmaxf(most, fabsf(y[f]) < INFINITY ? fabsf(y[f]) : 0.0f);
+#pragma unroll
+      for (int o = DP / 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+      // 2^k most in 2^14 .. 2^15 (of rows near either end of the range, as far as f32 goes)
+      const int k = most == 0.0f ? 0 : min(max(14 + 127 - static_cast<int>(__float_as_uint(most) >> 23), -110), 110);
+      const float by = __int_as_float((127 + k) << 23);
+      factor = p.scale_log2 * __int_as_float((127 - k) << 23);
+#pragma unroll
+      for (int f = 0; f < 8; ++f) y[f] *= by;
     }
+    if (d == 0) row_factor[r] = factor;
+    const uint32_t at = q_s + static_cast<uint32_t>(r * 2 * DP + (d & 1) * 8);  // of the step's two 16-byte chunks
+    const int c = d & ~1;
+    ptx::st_shared_v2(at + (paged_swizzled_q<DP>(r, c) << 4), pack2<__half>(y[0], y[1]), pack2<__half>(y[4], y[5]));
+    ptx::st_shared_v2(at + (paged_swizzled_q<DP>(r, c + 1) << 4), pack2<__half>(y[2], y[3]), pack2<__half>(y[6], y[7]));
   }
   const int v0 = split * sp.per, v1 = min(sp.n, v0 + sp.per);
   const int steps = (max(v1 - v0, 0) + (1 << log_boxes) - 1) >> log_boxes;
   ptx::named_barrier_sync(1, P::kThreads);  // barriers and rows are there
 
-  // ---- q as columns: lane / 4 of each eight rows, in the order of K's bytes
+  // ---- q as columns: lane / 4 of each eight rows
   uint32_t qf[CH][NB][2];
   float row_c[NB][2];  // of rows 2 c4 and 2 c4 + 1: from a product's sum to log2 units, but for the key's scale
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
-    const PagedRow row = rows[rw * 8 * NB + nb * 8 + g];
-    const bool on = row.news != 0 || row.old_end != 0;
-    float y[CH][4];
-    float most = 0.0f, c = p.scale_log2;
+    const int r0 = rw * 8 * NB + nb * 8;
 #pragma unroll
-    for (int ks = 0; ks < CH; ++ks) {
-      q_raw[ks][nb].widen(y[ks]);
-#pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        y[ks][f] = on ? y[ks][f] : 0.0f;
-        if constexpr (Elem<T>::kBf16) most = fmaxf(most, fabsf(y[ks][f]) < INFINITY ? fabsf(y[ks][f]) : 0.0f);
-      }
-    }
-    if constexpr (Elem<T>::kBf16) {
-      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-      // 2^k most in 2^14 .. 2^15 (of rows near either end of the range, as far as f32 goes)
-      const int k = most == 0.0f ? 0 : min(max(14 + 127 - static_cast<int>(__float_as_uint(most) >> 23), -110), 110);
-      const float by = __int_as_float((127 + k) << 23);
-      c = p.scale_log2 * __int_as_float((127 - k) << 23);
-#pragma unroll
-      for (int ks = 0; ks < CH; ++ks)
-#pragma unroll
-        for (int f = 0; f < 4; ++f) y[ks][f] *= by;
+    for (int ks = 0; ks < CH; ks += 2) {  // matrices: the two halves of step ks, and of the next
+      uint32_t x[4];
+      const int r = r0 + (lane & 7);
+      ldmatrix_x4(q_s + static_cast<uint32_t>(r * 2 * DP + (paged_swizzled_q<DP>(r, 2 * ks + (lane >> 3)) << 4)), x);
+      qf[ks][nb][0] = x[0];
+      qf[ks][nb][1] = x[1];
+      qf[ks + 1][nb][0] = x[2];
+      qf[ks + 1][nb][1] = x[3];
     }
 #pragma unroll
-    for (int ks = 0; ks < CH; ++ks) {
-      qf[ks][nb][0] = pack2<__half>(y[ks][0], y[ks][1]);
-      qf[ks][nb][1] = pack2<__half>(y[ks][2], y[ks][3]);
-    }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) row_c[nb][e] = __shfl_sync(0xffffffffu, c, 8 * c4 + 4 * e);
+    for (int e = 0; e < 2; ++e) row_c[nb][e] = row_factor[r0 + 2 * c4 + e];
   }
 
   float m[NB][2], l[NB][2];

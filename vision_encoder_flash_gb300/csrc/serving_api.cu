@@ -153,12 +153,17 @@ vattn_status paged_launch(vattn::PagedParams p, const Pools& pools, int sms, int
   p.row_blocks = (p.rows + P::kRows - 1) / P::kRows;
   if (seqs * p.row_blocks > kMaxRows || seqs * p.rows > INT32_MAX)
     return fail(VATTN_ERR_UNSUPPORTED, "too many query rows");
-  // Shares of the keys, as forward_cached has them.
+  // Shares of the keys: as many blocks as are resident at a time, of 256 keys at
+  // least, or of 128 where that makes no more than 32 shares.  Four, which a cluster
+  // joins, where that leaves a warp five steps at most and enough blocks: as fast as
+  // more shares and their join on the device, and 4 us less host time for a call.
   const long long most_keys = std::min<long long>(p.w.n_keys, static_cast<long long>(p.w.sinks) + p.w.window + p.w.n_queries);
   const long long blocks = seqs * p.row_blocks, room = static_cast<long long>(resident) * sms;
   const long long fill = room / blocks >= 4 ? room / blocks : (room + blocks - 1) / blocks;
   const long long fine = std::max(std::min(32LL, (most_keys + 127) / 128), (most_keys + 255) / 256);
   p.splits = static_cast<int>(std::max(1LL, std::min({fill, fine, static_cast<long long>(vattn::kCachedMaxSplits)})));
+  if (p.splits > vattn::kPagedCluster && most_keys <= vattn::kPagedCluster * 5LL * P::kStepKeys && blocks * vattn::kPagedCluster >= sms / 4)
+    p.splits = vattn::kPagedCluster;
   if (blocks * p.splits > kMaxRows) p.splits = 1;
 #ifdef PROBE
   if (getenv("SPLITS")) p.splits = atoi(getenv("SPLITS"));
