@@ -1,17 +1,19 @@
 // paged_append_kernel.cuh -- new keys and values into the 8-bit paged cache
 // (vattn_append_paged).
 //
-// A block has one page of one sequence, for one head of k or of v: the scale
-// of a page and head belongs to one block, which no other waits for.  It takes
-// the largest finite magnitude of its new rows (keys turned by their angle
+// A block has one page of one sequence, for some heads of k or of v: the scale of a
+// page and head belongs to one block, which no other waits for.  For each head it
+// takes the largest finite magnitude of its new rows (keys turned by their angle
 // first, in f32), the scale from that and from the old one, rescales the rows
-// before the new ones where the scale grew, and rounds the new rows to e4m3.
-// With scales that are powers of two, rescaling moves exponents only: what was
-// rounded once stays as it is but for values that leave the normal range.
+// before the new ones where the scale grew, and rounds the new rows to e4m3.  With
+// scales that are powers of two, rescaling moves exponents only: what was rounded
+// once stays as it is but for values that leave the normal range.
 //
 // A thread holds slots of 2 x 8 elements of a row, a rotation pair each, in
-// registers between the two steps; what it has beyond kAppendHold of them it
-// reads again.
+// registers between the two steps (what it has beyond kAppendHold of them it reads
+// again), and the next heads' come through a cp.async ring of its own in shared
+// memory.  The angles' sines and cosines serve all heads of the block, likewise from
+// shared memory that only their thread uses.
 #pragma once
 
 #include "e4m3.cuh"
@@ -22,7 +24,8 @@
 namespace vattn {
 
 constexpr int kAppendThreads = 512;  // most
-constexpr int kAppendHold = 4;       // slots a thread holds
+constexpr int kAppendHold = 2;       // slots a thread holds
+constexpr int kAppendStages = 2;     // heads in its ring
 constexpr int kMinScaleExponent = -32;
 
 struct AppendParams {
@@ -40,8 +43,10 @@ struct AppendParams {
   int page, max_pages;
   int D, half, slots;        // slots of a row
   int items;                 // uniform: pages that a sequence's new rows may touch
-  FastDiv d_heads, d_items, d_page, d_slots;
-  double turns[kQkMaxDim / 2];
+  int slices, heads_per_slice;  // blocks that share the heads
+  FastDiv d_slices, d_items, d_page, d_slots;
+  uint64_t turn[kQkMaxDim / 2];  // without factors: each frequency's fraction of a turn (qk_turn)
+  double turns[kQkMaxDim / 2];   // with them: what qk_turn wants
   float turns_rest[kQkMaxDim / 2];
 };
 
@@ -77,20 +82,27 @@ __device__ __forceinline__ AppendSeq append_seq(const AppendParams& p, int item)
   return s;
 }
 
+// Shared memory of a block, bytes a thread: a held slot's eight (cos, sin), and its rows.
+template <int V>
+constexpr int append_smem(int threads) { return V == 8 ? threads * kAppendHold * (64 + kAppendStages * 32) : 0; }
+
 template <typename T, int V>
 __global__ void __launch_bounds__(kAppendThreads) vattn_append_paged_kernel(const __grid_constant__ AppendParams p) {
+  extern __shared__ float4 angle_s[];  // [4][held slot][thread]: two (cos, sin) each; then the rings
   __shared__ uint64_t turn[kQkMaxDim / 2];
-  __shared__ float top_s[kAppendThreads / 32];
+  __shared__ __align__(16) float top_s[2][kAppendThreads / 32];
+  constexpr int kHold = V == 8 ? kAppendHold : 0;
   ptx::grid_dep_wait();
   const int tid = static_cast<int>(threadIdx.x), threads = static_cast<int>(blockDim.x);
-  uint32_t head;
-  const uint32_t rest = p.d_heads.div(blockIdx.x, &head);
-  const int which = static_cast<int>(rest & 1u), h = static_cast<int>(head);
+  uint32_t slice;
+  const uint32_t rest = p.d_slices.div(blockIdx.x, &slice);
+  const int which = static_cast<int>(rest & 1u), h0 = static_cast<int>(slice) * p.heads_per_slice;
+  const int h1 = min(p.heads, h0 + p.heads_per_slice);
   const AppendSeq s = append_seq(p, static_cast<int>(rest >> 1));
   // new rows of the sequence's cache, and those of this page: [lo, hi)
-  const int limit = p.max_pages * p.page;
-  const int len = min(max(p.kv_len[s.b], 0), limit);
-  const long long start = static_cast<long long>(p.kv_len[s.b]) - s.n;  // row of the first new token
+  const int limit = p.max_pages * p.page, kv_len = p.kv_len[s.b];
+  const int len = min(max(kv_len, 0), limit);
+  const long long start = static_cast<long long>(kv_len) - s.n;  // row of the first new token
   const int begin = static_cast<int>(min(static_cast<long long>(limit), max(0LL, start)));
   const int lp = static_cast<int>(p.d_page.div(static_cast<uint32_t>(begin))) + s.nth;
   if (s.n <= 0 || s.nth < 0 || lp >= p.max_pages || static_cast<long long>(lp) * p.page >= len) return;
@@ -100,131 +112,240 @@ __global__ void __launch_bounds__(kAppendThreads) vattn_append_paged_kernel(cons
   if (P < 0 || P >= p.n_pages) return;
   const bool keys = which == 0;
   const int half = keys ? p.half : 0;
-  if (keys) {
-    for (int i = tid; i < half; i += threads) turn[i] = qk_turn(p.turns, p.turns_rest, p.factors, i);
-    __syncthreads();
-  }
   const RowsTensor& x = keys ? p.x[0] : p.x[1];
-  uint8_t* const page = (keys ? p.pool[0] : p.pool[1]) + P * p.ps[which][0] + h * p.ps[which][1];
-  const long long row_stride = p.ps[which][2];
-  float* const scale_at = (keys ? p.scale[0] : p.scale[1]) + P * p.heads + h;
+  uint8_t* const pool = (keys ? p.pool[0] : p.pool[1]) + P * p.ps[which][0];
+  const long long head_stride = p.ps[which][1], row_stride = p.ps[which][2];
+  float* const scales = (keys ? p.scale[0] : p.scale[1]) + P * p.heads;
+  const T* const first_row = p.cu != nullptr ? rows_at<T>(x, 0, 0, s.first - start) : rows_at<T>(x, s.b, 0, -start);  // + row: its place
 
-  // the f32 values of slot `at` of the new rows
+  // slot `at` of the new rows: row, place in it, and where it is in head 0
   const int all = (hi - lo) * p.slots;
   struct Slot {
     QkSlot<V> s;
-    int row;
+    int row, c;
   };
   auto slot = [&](int at) {
     Slot t;
     uint32_t c;
     t.row = lo + static_cast<int>(p.d_slots.div(static_cast<uint32_t>(at), &c));
-    t.s.set(p.D, half, p.slots, static_cast<int>(c));
+    t.c = static_cast<int>(c);
+    t.s.set(p.D, half, p.slots, t.c);
     return t;
   };
-  auto values = [&](int at, float (&a)[V], float (&b)[V]) {
-    const Slot t = slot(at);
-    const long long i = s.first + (t.row - start);
-    const T* from = p.cu != nullptr ? rows_at<T>(x, 0, h, i) : rows_at<T>(x, s.b, h, i);
+  auto position = [&](int row) -> long long {
+    if (p.positions == nullptr) return row;
+    return p.positions[(p.cu != nullptr ? 0LL : static_cast<long long>(s.b) * p.n_tokens) + s.first + (row - start)];
+  };
+  auto rotate = [](float (&a)[V], float (&b)[V], const float (&cs)[V], const float (&sn)[V]) {
+    float x[V], y[V], minus[V];
+    vmul<V>(x, a, cs);
+    vmul<V>(y, a, sn);
+#pragma unroll
+    for (int e = 0; e < V; ++e) minus[e] = -b[e];
+    vfma<V>(a, minus, sn, x);
+    vfma<V>(b, b, cs, y);
+  };
+  // the f32 values of a slot that no thread holds
+  auto values = [&](const Slot& t, int h, float (&a)[V], float (&b)[V]) {
+    const T* from = first_row + t.row * x.s[2] + h * x.s[1];
     qk_load<T, V>(from, t.s.ia, t.s.here).widen(a);
     qk_load<T, V>(from, t.s.ib, t.s.pair).widen(b);
-    if (t.s.rot) {
-      const long long pos =
-          p.positions == nullptr ? t.row : p.positions[(p.cu != nullptr ? 0LL : static_cast<long long>(s.b) * p.n_tokens) + i];
-      float cs[V], sn[V];
-      uint32_t c;
-      (void)p.d_slots.div(static_cast<uint32_t>(at), &c);
-      qk_angles<V>(t.s, turn, static_cast<int>(c), pos, cs, sn);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float ya = fmaf(-b[e], sn[e], a[e] * cs[e]), yb = fmaf(a[e], sn[e], b[e] * cs[e]);
-        a[e] = ya;
-        b[e] = yb;
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) {  // infinities become NaN
-      a[e] = fmaf(a[e], 0.0f, a[e]);
-      b[e] = fmaf(b[e], 0.0f, b[e]);
-    }
+    if (!t.s.rot) return;
+    float cs[V], sn[V];
+    qk_angles<V>(t.s, turn, t.c, position(t.row), cs, sn);
+    rotate(a, b, cs, sn);
   };
-  auto largest = [](float m, const float (&a)[V], const float (&b)[V]) {
+  auto largest = [](float m, const float (&a)[V], const float (&b)[V]) {  // (NaN is left out)
 #pragma unroll
-    for (int e = 0; e < V; ++e) m = fmaxf(m, fmaxf(fabsf(a[e]), fabsf(b[e])));  // (NaN is left out)
+    for (int e = 0; e < V; ++e) m = ptx::max3(m, fabsf(a[e]), fabsf(b[e]));
+    return m;
+  };
+  auto largest_finite = [](float m, const float (&a)[V], const float (&b)[V]) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      if (fabsf(a[e]) < INFINITY) m = fmaxf(m, fabsf(a[e]));
+      if (fabsf(b[e]) < INFINITY) m = fmaxf(m, fabsf(b[e]));
+    }
     return m;
   };
 
-  const float old = *scale_at;
-  float ha[kAppendHold][V], hb[kAppendHold][V], top = 0.0f;
-#pragma unroll
-  for (int n = 0; n < kAppendHold; ++n)
-    if (tid + n * threads < all) {
-      values(tid + n * threads, ha[n], hb[n]);
-      top = largest(top, ha[n], hb[n]);
-    }
-#pragma unroll 1
-  for (int at = tid + kAppendHold * threads; at < all; at += threads) {
-    float a[V], b[V];
-    values(at, a, b);
-    top = largest(top, a, b);
-  }
-  top = warp_max(top);
-  if (threads > 32) {
-    if ((tid & 31) == 0) top_s[tid >> 5] = top;
-    __syncthreads();
-    for (int w = 0; w < threads / 32; ++w) top = fmaxf(top, top_s[w]);
-  }
-  const float need = __int_as_float((max(e4m3_scale_exponent(top), kMinScaleExponent) + 127) << 23);
-  const float scale = lo == row0 ? need : fmaxf(old, need);
-  if (threads > 32) __syncthreads();  // every thread has read the old scale
-  else __syncwarp();
-  if (tid == 0) *scale_at = scale;
+  if (tid < kAppendThreads / 16) top_s[tid & 1][tid >> 1] = 0.0f;
+  if (threads > 32) __syncthreads();
 
-  // the rows before the new ones, 16 bytes at a time
-  if (lo > row0 && scale != old) {
-    const float by = old / scale;
-    const int chunks = p.D / 16;
-    for (int at = tid; at < (lo - row0) * chunks; at += threads) {
-      const int r = at / chunks;
-      uint4* to = reinterpret_cast<uint4*>(page + r * row_stride + (at - r * chunks) * 16);
-      uint4 y = *to;
-      uint32_t* w = reinterpret_cast<uint32_t*>(&y);
+  // ---- the first heads' rows on their way, then the angles
+  const T* from_a[kHold + 1];
+  const T* from_b[kHold + 1];
+  long long to_a[kHold + 1], to_b[kHold + 1];  // places in the page, from the head's first byte
+  bool rot[kHold + 1], on[kHold + 1];
+  const uint32_t ring = ptx::smem_addr(angle_s) + static_cast<uint32_t>(threads * kHold * 64 + tid * 16);
+  // a head's rows: ring[stage][slot][a, b]
+  auto ask = [&](int h) {
+    if (h < h1) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t lo2 = e4m3_half2_lo(w[i]), hi2 = e4m3_half2_hi(w[i]);
-        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo2));
-        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi2));
-        w[i] = e4m3_pack4(a.x * by, a.y * by, b.x * by, b.y * by);
+      for (int n = 0; n < kHold; ++n) {
+        const uint32_t to = ring + static_cast<uint32_t>((((h - h0) % kAppendStages * kHold + n) * 2) * threads * 16);
+        ptx::cp_async<16>(to, from_a[n], on[n]);
+        ptx::cp_async<16>(to + threads * 16, from_b[n], on[n]);
+        from_a[n] += x.s[1];
+        from_b[n] += x.s[1];
       }
-      *to = y;
+    }
+    ptx::cp_async_commit();
+  };
+  if constexpr (kHold > 0) {
+#pragma unroll
+    for (int n = 0; n < kHold; ++n) {
+      on[n] = tid + n * threads < all;
+      const Slot t = slot(on[n] ? tid + n * threads : 0);
+      const T* from = first_row + t.row * x.s[2] + h0 * x.s[1];
+      from_a[n] = from + t.s.ia;
+      from_b[n] = from + t.s.ib;
+      rot[n] = t.s.rot;
+      to_a[n] = (t.row - row0) * row_stride + t.s.ia;
+      to_b[n] = (t.row - row0) * row_stride + t.s.ib;
+    }
+    for (int i = 0; i < kAppendStages; ++i) ask(h0 + i);
+  }
+  if (half > 0) {
+    for (int i = tid; i < half; i += threads)
+      turn[i] = p.factors == nullptr ? p.turn[i] : qk_turn(p.turns, p.turns_rest, p.factors, i);
+    __syncthreads();
+    if constexpr (kHold > 0) {
+#pragma unroll 1
+      for (int n = 0; n < kHold; ++n) {
+        const Slot t = slot(min(tid + n * threads, all - 1));
+        if (!t.s.rot) continue;
+        float cs[V], sn[V];
+        qk_angles<V>(t.s, turn, t.c, position(t.row), cs, sn);
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k)
+          angle_s[(k * kHold + n) * threads + tid] = make_float4(cs[2 * k], sn[2 * k], cs[2 * k + 1], sn[2 * k + 1]);
+      }
     }
   }
-  const float by = 1.0f / scale;
-  auto store = [&](int at, const float (&a)[V], const float (&b)[V]) {
-    const Slot t = slot(at);
-    uint8_t* to = page + (t.row - row0) * row_stride;
-    if constexpr (V == 8) {
-      *reinterpret_cast<uint2*>(to + t.s.ia) = make_uint2(e4m3_pack4(a[0] * by, a[1] * by, a[2] * by, a[3] * by),
-                                                          e4m3_pack4(a[4] * by, a[5] * by, a[6] * by, a[7] * by));
-      *reinterpret_cast<uint2*>(to + t.s.ib) = make_uint2(e4m3_pack4(b[0] * by, b[1] * by, b[2] * by, b[3] * by),
-                                                          e4m3_pack4(b[4] * by, b[5] * by, b[6] * by, b[7] * by));
-    } else {
+
+#pragma unroll 1
+  for (int h = h0; h < h1; ++h) {
+    float* const scale_at = scales + h;
+    const float old = *scale_at;
+    uint8_t* const page = pool + h * head_stride;
+    float a[kHold + 1][V], b[kHold + 1][V], top = 0.0f;
+    if constexpr (kHold > 0) ptx::cp_async_wait<kAppendStages - 1>();
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const uint32_t y = e4m3_pack(a[e] * by, b[e] * by);
-        to[t.s.ia + e] = static_cast<uint8_t>(y);
-        to[t.s.ib + e] = static_cast<uint8_t>(y >> 8);
+    for (int n = 0; n < kHold; ++n) {
+      const uint32_t at = ring + static_cast<uint32_t>((((h - h0) % kAppendStages * kHold + n) * 2) * threads * 16);
+      Vec<T, V> ra, rb;
+      *reinterpret_cast<float4*>(&ra) = ptx::ld_shared_v4(at);
+      *reinterpret_cast<float4*>(&rb) = ptx::ld_shared_v4(at + threads * 16);
+      ra.widen(a[n]);
+      rb.widen(b[n]);
+      if (rot[n]) {
+        float cs[V], sn[V];
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k) {
+          const float4 y = angle_s[(k * kHold + n) * threads + tid];
+          cs[2 * k] = y.x;
+          sn[2 * k] = y.y;
+          cs[2 * k + 1] = y.z;
+          sn[2 * k + 1] = y.w;
+        }
+        rotate(a[n], b[n], cs, sn);
+      }
+      top = largest(top, a[n], b[n]);  // (zeros where there is no slot)
+    }
+    if constexpr (kHold > 0) ask(h + kAppendStages);
+#pragma unroll 1
+    for (int at = tid + kHold * threads; at < all; at += threads) {
+      float ya[V], yb[V];
+      values(slot(at), h, ya, yb);
+      top = largest(top, ya, yb);
+    }
+    // (h - h0) & 1: the warps that are late still read the last head's
+    auto over_block = [&](float m, float* to) {
+      m = warp_max(m);
+      if (threads == 32) return m;
+      if ((tid & 31) == 0) to[tid >> 5] = m;
+      __syncthreads();
+      const int warps = threads / 32;  // (others' places are zero)
+      for (int w = 0; w < warps; w += 4) {
+        const float4 y = *reinterpret_cast<const float4*>(to + w);
+        m = ptx::max3(m, y.x, y.y);
+        m = ptx::max3(m, y.z, y.w);
+      }
+      return m;
+    };
+    top = over_block(top, top_s[(h - h0) & 1]);
+    const bool infinite = top == INFINITY;  // (the whole block's)
+    if (infinite) {
+      float m = 0.0f;
+      for (int at = tid; at < all; at += threads) {
+        float ya[V], yb[V];
+        values(slot(at), h, ya, yb);
+        m = largest_finite(m, ya, yb);
+      }
+      if (threads > 32) __syncthreads();
+      top = over_block(m, top_s[(h - h0) & 1]);
+    }
+    const float need = __int_as_float((max(e4m3_scale_exponent(top), kMinScaleExponent) + 127) << 23);
+    const float scale = lo == row0 ? need : fmaxf(old, need);
+    __syncwarp();
+    if (tid == 0) *scale_at = scale;  // every thread has read the old one
+
+    // the rows before the new ones, 16 bytes at a time
+    if (lo > row0 && scale != old) {
+      const float by = old / scale;
+      const int chunks = p.D / 16;
+      for (int at = tid; at < (lo - row0) * chunks; at += threads) {
+        const int r = at / chunks;
+        uint4* to = reinterpret_cast<uint4*>(page + r * row_stride + (at - r * chunks) * 16);
+        uint4 y = *to;
+        uint32_t* w = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t lo2 = e4m3_half2_lo(w[i]), hi2 = e4m3_half2_hi(w[i]);
+          const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&lo2));
+          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&hi2));
+          w[i] = e4m3_pack4(u.x * by, u.y * by, v.x * by, v.y * by);
+        }
+        *to = y;
       }
     }
-  };
+    const float by = 1.0f / scale;
+    auto store = [&](uint8_t* at_a, uint8_t* at_b, float (&ya)[V], float (&yb)[V]) {
+      vscale<V>(ya, ya, by);
+      vscale<V>(yb, yb, by);
+      if (infinite) {  // infinities become NaN
 #pragma unroll
-  for (int n = 0; n < kAppendHold; ++n)
-    if (tid + n * threads < all) store(tid + n * threads, ha[n], hb[n]);
+        for (int e = 0; e < V; ++e) {
+          ya[e] = fmaf(ya[e], 0.0f, ya[e]);
+          yb[e] = fmaf(yb[e], 0.0f, yb[e]);
+        }
+      }
+      if constexpr (V == 8) {
+        *reinterpret_cast<uint2*>(at_a) =
+            make_uint2(e4m3_pack4(ya[0], ya[1], ya[2], ya[3]), e4m3_pack4(ya[4], ya[5], ya[6], ya[7]));
+        *reinterpret_cast<uint2*>(at_b) =
+            make_uint2(e4m3_pack4(yb[0], yb[1], yb[2], yb[3]), e4m3_pack4(yb[4], yb[5], yb[6], yb[7]));
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const uint32_t y = e4m3_pack(ya[e], yb[e]);
+          at_a[e] = static_cast<uint8_t>(y);
+          at_b[e] = static_cast<uint8_t>(y >> 8);
+        }
+      }
+    };
+#pragma unroll
+    for (int n = 0; n < kHold; ++n)
+      if (on[n]) store(page + to_a[n], page + to_b[n], a[n], b[n]);
 #pragma unroll 1
-  for (int at = tid + kAppendHold * threads; at < all; at += threads) {
-    float a[V], b[V];
-    values(at, a, b);
-    store(at, a, b);
+    for (int at = tid + kHold * threads; at < all; at += threads) {
+      float ya[V], yb[V];
+      const Slot t = slot(at);
+      values(t, h, ya, yb);
+      uint8_t* const to = page + (t.row - row0) * row_stride;
+      store(to + t.s.ia, to + t.s.ib, ya, yb);
+    }
   }
 }
 

@@ -92,42 +92,6 @@ __device__ __forceinline__ void qk_weight(const QkSlot<V>& s, const void* w, int
   }
 }
 
-// d = a * b, d = a * b + c over V lanes' worth, in pairs where V is even.
-template <int V>
-__device__ __forceinline__ void vmul(float (&d)[V], const float (&a)[V], const float (&b)[V]) {
-  if constexpr (V % 2 == 0) {
-#pragma unroll
-    for (int e = 0; e < V; e += 2) {
-      const float2 r = __fmul2_rn(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]));
-      d[e] = r.x;
-      d[e + 1] = r.y;
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e) d[e] = a[e] * b[e];
-  }
-}
-template <int V>
-__device__ __forceinline__ void vfma(float (&d)[V], const float (&a)[V], const float (&b)[V], const float (&c)[V]) {
-  if constexpr (V % 2 == 0) {
-#pragma unroll
-    for (int e = 0; e < V; e += 2) {
-      const float2 r = __ffma2_rn(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]), make_float2(c[e], c[e + 1]));
-      d[e] = r.x;
-      d[e + 1] = r.y;
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e) d[e] = fmaf(a[e], b[e], c[e]);
-  }
-}
-template <int V>
-__device__ __forceinline__ void vscale(float (&d)[V], const float (&a)[V], float b) {
-  float bb[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) bb[e] = b;
-  vmul<V>(d, a, bb);
-}
 template <int V>
 __device__ __forceinline__ float vsum(const float (&a)[V]) {
   float s = 0.0f;

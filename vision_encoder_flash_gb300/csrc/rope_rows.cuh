@@ -30,7 +30,7 @@ struct QkSlot {
 };
 
 // The rotation's frequency i as a 64-bit fraction of a turn; factors: null, or divisors.
-__device__ __forceinline__ uint64_t qk_turn(const double* turns, const float* turns_rest, const float* factors, int i) {
+__host__ __device__ __forceinline__ uint64_t qk_turn(const double* turns, const float* turns_rest, const float* factors, int i) {
   double f = turns[i];
   float rest = turns_rest[i];  // 24 of its digits are enough: f64 arithmetic is slow
   if (factors != nullptr) {
@@ -83,6 +83,43 @@ __device__ __forceinline__ Vec<T, V> qk_load(const T* row, int i, bool here) {
     for (int e = 0; e < V; ++e) v.e[e] = Elem<T>::narrow(0.0f);
   }
   return v;
+}
+
+// d = a * b, d = a * b + c over V lanes' worth, in pairs where V is even.
+template <int V>
+__device__ __forceinline__ void vmul(float (&d)[V], const float (&a)[V], const float (&b)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int e = 0; e < V; e += 2) {
+      const float2 r = __fmul2_rn(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]));
+      d[e] = r.x;
+      d[e + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) d[e] = a[e] * b[e];
+  }
+}
+template <int V>
+__device__ __forceinline__ void vfma(float (&d)[V], const float (&a)[V], const float (&b)[V], const float (&c)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int e = 0; e < V; e += 2) {
+      const float2 r = __ffma2_rn(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]), make_float2(c[e], c[e + 1]));
+      d[e] = r.x;
+      d[e + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) d[e] = fmaf(a[e], b[e], c[e]);
+  }
+}
+template <int V>
+__device__ __forceinline__ void vscale(float (&d)[V], const float (&a)[V], float b) {
+  float bb[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) bb[e] = b;
+  vmul<V>(d, a, bb);
 }
 
 }  // namespace vattn

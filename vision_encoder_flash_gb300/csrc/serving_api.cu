@@ -118,8 +118,12 @@ vattn_status check_append(const vattn_append_args* a) {
 }
 
 template <typename T, int V>
-vattn_status append_launch(const vattn::AppendParams& p, int64_t blocks, int threads, cudaStream_t stream) {
-  vattn::vattn_append_paged_kernel<T, V><<<static_cast<unsigned>(blocks), threads, 0, stream>>>(p);
+vattn_status append_launch(const vattn::AppendParams& p, int64_t blocks, int threads, int device, cudaStream_t stream) {
+  auto kernel = vattn::vattn_append_paged_kernel<T, V>;
+  static std::atomic<uint8_t> done[kMaxDevices];
+  const vattn_status st = allow_smem(kernel, vattn::append_smem<V>(vattn::kAppendThreads), done, device);
+  if (st != VATTN_OK) return st;
+  kernel<<<static_cast<unsigned>(blocks), threads, vattn::append_smem<V>(threads), stream>>>(p);
   return launched("cache append kernel launch");
 }
 
@@ -310,6 +314,7 @@ vattn_status vattn_append_paged(const vattn_rows* k, const vattn_rows* v, const 
   p.D = static_cast<int>(a->head_dim);
   p.half = static_cast<int>(a->rope_dims / 2);
   rope_turns(a->base, static_cast<int>(a->rope_dims), p.turns, p.turns_rest);
+  for (int i = 0; i < p.half; ++i) p.turn[i] = vattn::qk_turn(p.turns, p.turns_rest, nullptr, i);
   // 16-byte accesses where the rotated halves and the rest are cut evenly by them
   bool wide = p.half % 8 == 0 && (p.D - 2 * p.half) % 16 == 0;
   for (const Tensor* t : {&tk, &tv}) {
@@ -322,7 +327,17 @@ vattn_status vattn_append_paged(const vattn_rows* k, const vattn_rows* v, const 
   const int64_t items = a->cu_seqlens ? a->n_tokens / p.page + 2 * a->batch : a->batch * p.items;
   const int64_t blocks = items * p.heads * 2;
   if (items > kMaxRows || blocks > INT32_MAX) return fail(VATTN_ERR_UNSUPPORTED, "too many pages and heads");
-  p.d_heads = fast_div(p.heads);
+  int device = 0, sms = 0;
+  if ((st = current_device(&device)) != VATTN_OK) return st;
+  if ((st = sm_count(device, &sms)) != VATTN_OK) return st;
+  // heads of a block: more share the angles, fewer make more blocks
+  const int64_t per = std::min<int64_t>(p.heads, std::max<int64_t>(1, blocks / (3LL * sms)));
+  p.slices = static_cast<int>((p.heads + per - 1) / per);
+#ifdef PROBE
+  if (getenv("SLICES")) p.slices = atoi(getenv("SLICES"));
+#endif
+  p.heads_per_slice = (p.heads + p.slices - 1) / p.slices;
+  p.d_slices = fast_div(p.slices);
   p.d_items = fast_div(p.items);
   p.d_page = fast_div(p.page);
   p.d_slots = fast_div(p.slots);
@@ -330,10 +345,12 @@ vattn_status vattn_append_paged(const vattn_rows* k, const vattn_rows* v, const 
   const int threads = std::min(vattn::kAppendThreads,
                                (slots + 32 * vattn::kAppendHold - 1) / (32 * vattn::kAppendHold) * 32);
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  const int64_t grid = items * 2 * p.slices;
   if (a->dtype == VATTN_F16)
-    return wide ? append_launch<__half, 8>(p, blocks, threads, stream) : append_launch<__half, 1>(p, blocks, threads, stream);
-  return wide ? append_launch<__nv_bfloat16, 8>(p, blocks, threads, stream)
-              : append_launch<__nv_bfloat16, 1>(p, blocks, threads, stream);
+    return wide ? append_launch<__half, 8>(p, grid, threads, device, stream)
+                : append_launch<__half, 1>(p, grid, threads, device, stream);
+  return wide ? append_launch<__nv_bfloat16, 8>(p, grid, threads, device, stream)
+              : append_launch<__nv_bfloat16, 1>(p, grid, threads, device, stream);
 }
 
 vattn_status vattn_forward_paged(const vattn_rows* q, const vattn_pages* cache, const vattn_rows* out,
