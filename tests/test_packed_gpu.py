@@ -159,10 +159,11 @@ def test_starts_out_of_range(td):
     out.fill_(7.0)
     vef.forward_packed(q, k, v, ints(torch, [0, 100, 60, 60], dev), scale=0.1, out=out)
     assert torch.equal(out[:, :, :100], want[:, :, :100]) and bool((out[:, :, 100:] == 7).all())
-    # overlapping prompts, more of them than the list has room for: nothing else is touched
-    for bad in ([0, 300, 0, 300, 0, 300, 0, 300, 0, 300, 0, 300], [300, 0, 300, 0], [5] * 9):
+    # prompts with more rows than there are: none is computed
+    for bad in ([0, 300, 0, 300, 0, 300, 0, 300, 0, 300, 0, 300], [0, 200, 0, 200], [2 ** 31 - 1, -2 ** 31] * 2000 + [300], [5] * 9):
+        out.fill_(7.0)
         vef.forward_packed(q, k, v, ints(torch, bad, dev), scale=0.1, out=out)
-    torch.cuda.synchronize(dev)
+        assert bool((out == 7).all())
     assert vef.device_status() == 0
     for empty in (ints(torch, [0], dev), ints(torch, [0, 0], dev)):
         out.fill_(7.0)

@@ -5,14 +5,16 @@
 // one sequence, longest first.  With lengths on the device, one block writes
 // them down: a pair counts for the last row block that it holds, which its key
 // tiles follow, a counting sort puts the pairs of late row blocks first, and
-// pairs of one row block come in any order (no result depends on it).
+// pairs of one row block come in any order (no result depends on it).  Prompts that
+// together have more rows than there are (starts that do not ascend) make an empty
+// list: the room for it is that of prompts that do not overlap.
 #pragma once
 
 #include "window_pipe.cuh"
 
 namespace vattn {
 
-constexpr int kListThreads = 1024;
+constexpr int kListThreads = 1024;  // most; 256 for few prompts
 constexpr int kListBuckets = 8192;  // counts in shared memory up to here (2^20 rows), else in the workspace
 
 struct PackedListParams {
@@ -20,7 +22,6 @@ struct PackedListParams {
   int n_seqs, total;
   int group, kv_heads, sms;
   int buckets;  // row blocks of the longest sequence there can be
-  int cap;      // pairs that the list has room for: enough where cu ascends
   int* counts;  // [buckets] or null: shared memory
   int4* list;   // {items, whole, 0, 0}, then {first row, rows, pair, 0} each
 };
@@ -28,13 +29,15 @@ struct PackedListParams {
 __global__ void __launch_bounds__(kListThreads) vattn_packed_list_kernel(const __grid_constant__ PackedListParams p) {
   __shared__ int counts_s[kListBuckets];
   __shared__ int warps_s[kListThreads / 32];
+  __shared__ long long rows_s[kListThreads / 32];
   ptx::grid_dep_launch();  // the attention kernel sets itself up meanwhile, and waits for this one's end
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  const int threads = static_cast<int>(blockDim.x), warps = threads / 32;
   int* const counts = p.counts != nullptr ? p.counts : counts_s;
-  for (int i = tid; i < p.buckets; i += kListThreads) counts[i] = 0;
+  for (int i = tid; i < p.buckets; i += threads) counts[i] = 0;
   __syncthreads();
   auto each = [&](auto&& take) {  // (first row, rows, pair, its last row block)
-    for (int b = warp; b < p.n_seqs; b += kListThreads / 32) {
+    for (int b = warp; b < p.n_seqs; b += warps) {
       const int first = min(max(p.cu[b], 0), p.total), rows = min(max(p.cu[b + 1], 0), p.total) - first;
       if (rows <= 0) continue;
       const int blocks = (rows + kTile - 1) / kTile;
@@ -43,10 +46,15 @@ __global__ void __launch_bounds__(kListThreads) vattn_packed_list_kernel(const _
         take(first, rows, static_cast<int>(i), min(blocks - 1, static_cast<int>((2 * i + 1) / p.group)));
     }
   };
-  each([&](int, int, int, int block) { atomicAdd(&counts[block], 1); });
+  long long mine = 0;  // rows of the warp's prompts
+  each([&](int, int rows, int pair, int block) {
+    if (pair == 0) mine += rows;  // (lane 0)
+    atomicAdd(&counts[block], 1);
+  });
+  if (lane == 0) rows_s[warp] = mine;
   __syncthreads();
   // counts to places: behind the pairs of all later row blocks
-  const int per = (p.buckets + kListThreads - 1) / kListThreads;
+  const int per = (p.buckets + threads - 1) / threads;
   int sum = 0;
   for (int i = tid * per; i < min(p.buckets, (tid + 1) * per); ++i) sum += counts[p.buckets - 1 - i];
   int upto = sum;
@@ -58,9 +66,15 @@ __global__ void __launch_bounds__(kListThreads) vattn_packed_list_kernel(const _
   if (lane == 31) warps_s[warp] = upto;
   __syncthreads();
   int before = upto - sum, all = 0;
-  for (int i = 0; i < kListThreads / 32; ++i) {
+  long long rows = 0;
+  for (int i = 0; i < warps; ++i) {
     if (i < warp) before += warps_s[i];
     all += warps_s[i];
+    rows += rows_s[i];
+  }
+  if (rows > p.total) {
+    if (tid == 0) p.list[0] = make_int4(0, 0, 0, 0);
+    return;
   }
   for (int i = tid * per; i < min(p.buckets, (tid + 1) * per); ++i) {
     const int n = counts[p.buckets - 1 - i];
@@ -70,10 +84,10 @@ __global__ void __launch_bounds__(kListThreads) vattn_packed_list_kernel(const _
   __syncthreads();
   each([&](int first, int rows, int pair, int block) {
     const int at = atomicAdd(&counts[block], 1);
-    if (at < p.cap) p.list[1 + at] = make_int4(first, rows, pair, 0);
+    p.list[1 + at] = make_int4(first, rows, pair, 0);
   });
   if (tid == 0) {
-    const int items = min(all, p.cap) * p.kv_heads;
+    const int items = all * p.kv_heads;
     const bool single = 2 * items <= p.sms;  // every unit an item of its own, as forward_window does
     p.list[0] = make_int4(single ? 2 * items : items, single ? 0 : items, 0, 0);
   }

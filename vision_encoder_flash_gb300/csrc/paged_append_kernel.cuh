@@ -88,7 +88,7 @@ constexpr int append_smem(int threads) { return V == 8 ? threads * kAppendHold *
 
 template <typename T, int V>
 __global__ void __launch_bounds__(kAppendThreads) vattn_append_paged_kernel(const __grid_constant__ AppendParams p) {
-  extern __shared__ float4 angle_s[];  // [4][held slot][thread]: two (cos, sin) each; then the rings
+  extern __shared__ float4 angle_s[];  // [4][held slot][thread]: cosines, cosines, sines, sines; then the rings
   __shared__ uint64_t turn[kQkMaxDim / 2];
   __shared__ __align__(16) float top_s[2][kAppendThreads / 32];
   constexpr int kHold = V == 8 ? kAppendHold : 0;
@@ -173,9 +173,9 @@ __global__ void __launch_bounds__(kAppendThreads) vattn_append_paged_kernel(cons
   if (threads > 32) __syncthreads();
 
   // ---- the first heads' rows on their way, then the angles
-  const T* from_a[kHold + 1];
-  const T* from_b[kHold + 1];
-  long long to_a[kHold + 1], to_b[kHold + 1];  // places in the page, from the head's first byte
+  const T* from[kHold + 1];
+  long long to[kHold + 1];  // place in the page, from the head's first byte
+  int apart[kHold + 1];     // elements from a slot's first half to its second
   bool rot[kHold + 1], on[kHold + 1];
   const uint32_t ring = ptx::smem_addr(angle_s) + static_cast<uint32_t>(threads * kHold * 64 + tid * 16);
   // a head's rows: ring[stage][slot][a, b]
@@ -183,11 +183,10 @@ __global__ void __launch_bounds__(kAppendThreads) vattn_append_paged_kernel(cons
     if (h < h1) {
 #pragma unroll
       for (int n = 0; n < kHold; ++n) {
-        const uint32_t to = ring + static_cast<uint32_t>((((h - h0) % kAppendStages * kHold + n) * 2) * threads * 16);
-        ptx::cp_async<16>(to, from_a[n], on[n]);
-        ptx::cp_async<16>(to + threads * 16, from_b[n], on[n]);
-        from_a[n] += x.s[1];
-        from_b[n] += x.s[1];
+        const uint32_t at = ring + static_cast<uint32_t>((((h - h0) % kAppendStages * kHold + n) * 2) * threads * 16);
+        ptx::cp_async<16>(at, from[n], on[n]);
+        ptx::cp_async<16>(at + threads * 16, from[n] + apart[n], on[n]);
+        from[n] += x.s[1];
       }
     }
     ptx::cp_async_commit();
@@ -197,12 +196,10 @@ __global__ void __launch_bounds__(kAppendThreads) vattn_append_paged_kernel(cons
     for (int n = 0; n < kHold; ++n) {
       on[n] = tid + n * threads < all;
       const Slot t = slot(on[n] ? tid + n * threads : 0);
-      const T* from = first_row + t.row * x.s[2] + h0 * x.s[1];
-      from_a[n] = from + t.s.ia;
-      from_b[n] = from + t.s.ib;
+      from[n] = first_row + t.row * x.s[2] + h0 * x.s[1] + t.s.ia;
+      to[n] = (t.row - row0) * row_stride + t.s.ia;
+      apart[n] = t.s.ib - t.s.ia;
       rot[n] = t.s.rot;
-      to_a[n] = (t.row - row0) * row_stride + t.s.ia;
-      to_b[n] = (t.row - row0) * row_stride + t.s.ib;
     }
     for (int i = 0; i < kAppendStages; ++i) ask(h0 + i);
   }
@@ -218,8 +215,10 @@ __global__ void __launch_bounds__(kAppendThreads) vattn_append_paged_kernel(cons
         float cs[V], sn[V];
         qk_angles<V>(t.s, turn, t.c, position(t.row), cs, sn);
 #pragma unroll
-        for (int k = 0; k < V / 2; ++k)
-          angle_s[(k * kHold + n) * threads + tid] = make_float4(cs[2 * k], sn[2 * k], cs[2 * k + 1], sn[2 * k + 1]);
+        for (int k = 0; k < V / 4; ++k) {
+          angle_s[(k * kHold + n) * threads + tid] = make_float4(cs[4 * k], cs[4 * k + 1], cs[4 * k + 2], cs[4 * k + 3]);
+          angle_s[((k + 2) * kHold + n) * threads + tid] = make_float4(sn[4 * k], sn[4 * k + 1], sn[4 * k + 2], sn[4 * k + 3]);
+        }
       }
     }
   }
@@ -242,12 +241,16 @@ __global__ void __launch_bounds__(kAppendThreads) vattn_append_paged_kernel(cons
       if (rot[n]) {
         float cs[V], sn[V];
 #pragma unroll
-        for (int k = 0; k < V / 2; ++k) {
-          const float4 y = angle_s[(k * kHold + n) * threads + tid];
-          cs[2 * k] = y.x;
-          sn[2 * k] = y.y;
-          cs[2 * k + 1] = y.z;
-          sn[2 * k + 1] = y.w;
+        for (int k = 0; k < V / 4; ++k) {
+          const float4 y = angle_s[(k * kHold + n) * threads + tid], z = angle_s[((k + 2) * kHold + n) * threads + tid];
+          cs[4 * k] = y.x;
+          cs[4 * k + 1] = y.y;
+          cs[4 * k + 2] = y.z;
+          cs[4 * k + 3] = y.w;
+          sn[4 * k] = z.x;
+          sn[4 * k + 1] = z.y;
+          sn[4 * k + 2] = z.z;
+          sn[4 * k + 3] = z.w;
         }
         rotate(a[n], b[n], cs, sn);
       }
@@ -337,7 +340,7 @@ __global__ void __launch_bounds__(kAppendThreads) vattn_append_paged_kernel(cons
     };
 #pragma unroll
     for (int n = 0; n < kHold; ++n)
-      if (on[n]) store(page + to_a[n], page + to_b[n], a[n], b[n]);
+      if (on[n]) store(page + to[n], page + to[n] + apart[n], a[n], b[n]);
 #pragma unroll 1
     for (int at = tid + kHold * threads; at < all; at += threads) {
       float ya[V], yb[V];

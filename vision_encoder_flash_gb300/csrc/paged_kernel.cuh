@@ -39,10 +39,7 @@ namespace vattn {
 
 constexpr int kPagedKeys = 32;  // keys of a warp's part of a step
 constexpr int kPagedWarps = 4;  // math warps
-#ifndef PCL
-#define PCL 4
-#endif
-constexpr int kPagedCluster = PCL;
+constexpr int kPagedCluster = 4;  // shares that a cluster of blocks joins by itself
 
 struct PagedParams {
   WindowParams w;  // n_keys: rows that the table has room for; kv_len: the cache's

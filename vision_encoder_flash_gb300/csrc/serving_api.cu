@@ -169,9 +169,6 @@ vattn_status paged_launch(vattn::PagedParams p, const Pools& pools, int sms, int
   if (p.splits > vattn::kPagedCluster && most_keys <= vattn::kPagedCluster * 5LL * P::kStepKeys && blocks * vattn::kPagedCluster >= sms / 4)
     p.splits = vattn::kPagedCluster;
   if (blocks * p.splits > kMaxRows) p.splits = 1;
-#ifdef PROBE
-  if (getenv("SPLITS")) p.splits = atoi(getenv("SPLITS"));
-#endif
   p.d_splits = fast_div(p.splits);
   p.d_row_blocks = fast_div(p.row_blocks);
   Workspace ws;
@@ -226,17 +223,6 @@ vattn_status paged_launch(vattn::PagedParams p, const Pools& pools, int sms, int
 
 template <typename T, int DP>
 vattn_status paged_rows(const vattn::PagedParams& p, const Pools& pools, int sms, int device, cudaStream_t stream) {
-#ifdef PROBE
-  if (getenv("PV")) {
-    const int v = atoi(getenv("PV"));
-    if (v == 11) return paged_launch<T, DP, 1, 1>(p, pools, sms, device, stream);
-    if (v == 12) return paged_launch<T, DP, 1, 2>(p, pools, sms, device, stream);
-    if (v == 14) return paged_launch<T, DP, 1, 4>(p, pools, sms, device, stream);
-    if (v == 21) return paged_launch<T, DP, 2, 1>(p, pools, sms, device, stream);
-    if (v == 22) return paged_launch<T, DP, 2, 2>(p, pools, sms, device, stream);
-    if (v == 24) return paged_launch<T, DP, 2, 4>(p, pools, sms, device, stream);
-  }
-#endif
   if (p.rows <= 8) return paged_launch<T, DP, 1, 1>(p, pools, sms, device, stream);
   if (p.rows <= 16) return paged_launch<T, DP, 2, 1>(p, pools, sms, device, stream);
   if (p.rows <= 32) return paged_launch<T, DP, 2, 2>(p, pools, sms, device, stream);
@@ -333,9 +319,6 @@ vattn_status vattn_append_paged(const vattn_rows* k, const vattn_rows* v, const 
   // heads of a block: more share the angles, fewer make more blocks
   const int64_t per = std::min<int64_t>(p.heads, std::max<int64_t>(1, blocks / (3LL * sms)));
   p.slices = static_cast<int>((p.heads + per - 1) / per);
-#ifdef PROBE
-  if (getenv("SLICES")) p.slices = atoi(getenv("SLICES"));
-#endif
   p.heads_per_slice = (p.heads + p.slices - 1) / p.slices;
   p.d_slices = fast_div(p.slices);
   p.d_items = fast_div(p.items);
@@ -463,7 +446,6 @@ vattn_status vattn_forward_packed(const vattn_rows* q, const vattn_rows* k, cons
   l.kv_heads = p.w.kv_heads;
   l.sms = sms;
   l.buckets = (l.total + vattn::kTile - 1) / vattn::kTile;
-  l.cap = static_cast<int>(cap);
   const size_t list_bytes = static_cast<size_t>(1 + cap) * sizeof(int4);
   const size_t count_bytes = l.buckets > vattn::kListBuckets ? static_cast<size_t>(l.buckets) * 4u : 0;
   Workspace ws;
@@ -471,7 +453,8 @@ vattn_status vattn_forward_packed(const vattn_rows* q, const vattn_rows* k, cons
   l.list = reinterpret_cast<int4*>(ws.data());
   if (count_bytes > 0) l.counts = reinterpret_cast<int*>(ws.data() + list_bytes);
   p.list = l.list;
-  vattn::vattn_packed_list_kernel<<<1, vattn::kListThreads, 0, stream>>>(l);
+  const int list_threads = n_seqs <= 64 && cap <= 4096 ? 256 : vattn::kListThreads;
+  vattn::vattn_packed_list_kernel<<<1, list_threads, 0, stream>>>(l);
   if ((st = launched("packed list kernel launch")) != VATTN_OK) return st;
   const int64_t items = 2 * cap * p.w.kv_heads;
   if (a->dtype == VATTN_F16)
