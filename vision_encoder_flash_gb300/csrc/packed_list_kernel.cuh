@@ -36,21 +36,40 @@ __global__ void __launch_bounds__(kListThreads) vattn_packed_list_kernel(const _
   int* const counts = p.counts != nullptr ? p.counts : counts_s;
   for (int i = tid; i < p.buckets; i += threads) counts[i] = 0;
   __syncthreads();
-  auto each = [&](auto&& take) {  // (first row, rows, pair, its last row block)
-    for (int b = warp; b < p.n_seqs; b += warps) {
-      const int first = min(max(p.cu[b], 0), p.total), rows = min(max(p.cu[b + 1], 0), p.total) - first;
-      if (rows <= 0) continue;
-      const int blocks = (rows + kTile - 1) / kTile;
-      const long long pairs = (static_cast<long long>(blocks) * p.group + 1) / 2;
-      for (long long i = lane; i < pairs; i += 32)
-        take(first, rows, static_cast<int>(i), min(blocks - 1, static_cast<int>((2 * i + 1) / p.group)));
+  // (first row, rows, pair, its last row block): a warp has up to 32 prompts at a time, whose
+  // lanes take the pairs of short ones by themselves and of long ones together
+  const int at_a_time = min(32, (p.n_seqs + warps - 1) / warps);
+  auto pairs_of = [&](int rows) { return (static_cast<long long>((rows + kTile - 1) / kTile) * p.group + 1) / 2; };
+  auto block_of = [&](int rows, long long i) {
+    return min((rows + kTile - 1) / kTile - 1, static_cast<int>((2 * i + 1) / p.group));
+  };
+  auto each = [&](auto&& take) {
+    for (int b0 = warp * at_a_time; b0 < p.n_seqs; b0 += warps * at_a_time) {
+      const int b = b0 + lane;
+      int first = 0, rows = 0;
+      if (lane < at_a_time && b < p.n_seqs) {
+        first = min(max(p.cu[b], 0), p.total);
+        rows = min(max(p.cu[b + 1], 0), p.total) - first;
+      }
+      const long long pairs = rows > 0 ? pairs_of(rows) : 0;
+      const bool alone = pairs <= 8;
+      if (alone)
+        for (int i = 0; i < static_cast<int>(pairs); ++i) take(first, rows, i, block_of(rows, i));
+      for (uint32_t left = __ballot_sync(0xffffffffu, !alone); left != 0; left &= left - 1) {
+        const int l = __ffs(static_cast<int>(left)) - 1;
+        const int f = __shfl_sync(0xffffffffu, first, l), n = __shfl_sync(0xffffffffu, rows, l);
+        const long long all = pairs_of(n);
+        for (long long i = lane; i < all; i += 32) take(f, n, static_cast<int>(i), block_of(n, i));
+      }
     }
   };
-  long long mine = 0;  // rows of the warp's prompts
+  long long mine = 0;  // rows of the prompts whose first pair this lane had
   each([&](int, int rows, int pair, int block) {
-    if (pair == 0) mine += rows;  // (lane 0)
+    if (pair == 0) mine += rows;
     atomicAdd(&counts[block], 1);
   });
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   if (lane == 0) rows_s[warp] = mine;
   __syncthreads();
   // counts to places: behind the pairs of all later row blocks
