@@ -30,42 +30,62 @@ _APPEND = struct.Struct("=5q3Qdi4x").pack      # vattn_append_args
 _BYTES = ()                                    # dtypes of a pool
 
 
+# As in decoder.py the checks are written out: a call's host time is that of a few of them.
+
+def _odd_pool(name, t, heads, dim, index):
+    """Raises for a pool that is not one of the call's heads, width and device."""
+    if not isinstance(t, _d._TENSOR) or t.dtype not in _BYTES:
+        raise TypeError(f"{name} must be a float8_e4m3fn (or uint8) tensor")
+    if t.dim() != 4 or t.shape[1] != heads or t.shape[3] != dim:
+        raise ValueError(f"{name} must be [n_pages, {heads}, page_size, {dim}], is {tuple(t.shape)}")
+    raise ValueError(f"{name} must be on cuda:{index}, is on {t.device}")
+
+
+def _odd_floats(name, t, shape, index):
+    if not isinstance(t, _d._TENSOR) or t.dtype is not _d._F32:
+        raise TypeError(f"{name} must be a float32 tensor")
+    raise ValueError(f"{name} must be a contiguous {shape} tensor on cuda:{index}")
+
+
 def _pages(k_pages, v_pages, k_scale, v_scale, page_table, kv_len, batch, heads, dim, index):
     """Packed vattn_pages of a cache that is read or written by `batch` sequences."""
     global _BYTES
+    tensor, f32, i32 = _d._TENSOR, _d._F32, _d._I32
     if not _BYTES:
         _BYTES = (_d._TORCH.float8_e4m3fn, _d._TORCH.uint8)
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if not isinstance(t, _d._TENSOR) or t.dtype not in _BYTES:
-            raise TypeError(f"{name} must be a float8_e4m3fn (or uint8) tensor")
-        if t.dim() != 4 or t.shape[1] != heads or t.shape[3] != dim:
-            raise ValueError(f"{name} must be [n_pages, {heads}, page_size, {dim}], is {tuple(t.shape)}")
-        if t.get_device() != index:
-            raise ValueError(f"{name} must be on cuda:{index}, is on {t.device}")
+    if not isinstance(k_pages, tensor) or k_pages.dtype not in _BYTES or k_pages.dim() != 4 or \
+            k_pages.get_device() != index:
+        _odd_pool("k_pages", k_pages, heads, dim, index)
     shape = k_pages.shape
+    n_pages, pool_heads, page, pool_dim = shape
+    if pool_heads != heads or pool_dim != dim:
+        _odd_pool("k_pages", k_pages, heads, dim, index)
+    if not isinstance(v_pages, tensor) or v_pages.dtype not in _BYTES or v_pages.get_device() != index:
+        _odd_pool("v_pages", v_pages, heads, dim, index)
     if v_pages.shape != shape:
         raise ValueError(f"shape mismatch: k_pages {tuple(shape)}, v_pages {tuple(v_pages.shape)}")
-    n_pages, _, page, _ = shape
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if not isinstance(t, _d._TENSOR) or t.dtype is not _d._F32:
-            raise TypeError(f"{name} must be a float32 tensor")
-        if t.shape != (n_pages, heads) or t.get_device() != index or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {(n_pages, heads)} tensor on cuda:{index}")
-    if not isinstance(page_table, _d._TENSOR) or page_table.dim() != 2:
+    scales = (n_pages, heads)
+    if not isinstance(k_scale, tensor) or k_scale.dtype is not f32 or k_scale.shape != scales or \
+            k_scale.get_device() != index or not k_scale.is_contiguous():
+        _odd_floats("k_scale", k_scale, scales, index)
+    if not isinstance(v_scale, tensor) or v_scale.dtype is not f32 or v_scale.shape != scales or \
+            v_scale.get_device() != index or not v_scale.is_contiguous():
+        _odd_floats("v_scale", v_scale, scales, index)
+    if not isinstance(page_table, tensor) or page_table.dim() != 2:
         raise TypeError("page_table must be an int32 tensor [batch, max_pages]")
-    most = page_table.shape[1]
-    table = _d._ints("page_table", page_table, _d._I32, (batch, most), index)
+    rows, most = page_table.shape
+    if rows != batch or page_table.dtype is not i32 or page_table.get_device() != index or \
+            not page_table.is_contiguous():
+        _d._ints("page_table", page_table, i32, (batch, most), index)
     if kv_len is None:
         raise TypeError("kv_len must be an int32 tensor")
-    lens = _d._ints("kv_len", kv_len, _d._I32, (batch,), index)
-    strides = []
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        p, h, r, d = t.stride()
-        if d != 1 and dim > 1 and t.numel() > 0:
-            raise ValueError(f"{name} must be contiguous in its last dimension")
-        strides += (p, h, r)
-    return _PAGES(k_pages.data_ptr(), v_pages.data_ptr(), *strides, k_scale.data_ptr(), v_scale.data_ptr(), table,
-                  lens, n_pages, page, most)
+    lens = _d._ints("kv_len", kv_len, i32, (batch,), index)
+    kp, kh, kr, kd = k_pages.stride()
+    vp, vh, vr, vd = v_pages.stride()
+    if (kd != 1 or vd != 1) and dim > 1 and n_pages * heads * page > 0:
+        raise ValueError("k_pages and v_pages must be contiguous in their last dimension")
+    return _PAGES(k_pages.data_ptr(), v_pages.data_ptr(), kp, kh, kr, vp, vh, vr, k_scale.data_ptr(),
+                  v_scale.data_ptr(), page_table.data_ptr(), lens, n_pages, page, most)
 
 
 def _sequences(cu_seqlens, index):
