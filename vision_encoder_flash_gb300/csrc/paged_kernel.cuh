@@ -738,7 +738,18 @@ __global__ void __launch_bounds__(256) vattn_paged_join_kernel(const __grid_cons
   const bool none = cached_word(w, b, t, sp.base) == 0;
   const long long at0 = (bk * p.row_blocks + rr / ROWS) * p.splits * ROWS + rr % ROWS;
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + at0;
-  static_assert(kCachedMaxSplits <= 512, "two shares a thread");
+  static_assert(kCachedMaxSplits <= 512, "two shares a thread, 16 of its dims");
+  // all that the thread adds up, on its way while the weights are formed
+  float4 y[kCachedMaxSplits / 32];
+  {
+    const float* from = p.part_o + at0 * D + d;
+#pragma unroll
+    for (int i = 0; i < kCachedMaxSplits / 32; ++i) {
+      const int s = warp * 4 + (lane >> 3) + 32 * i;
+      y[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (d < D && s < shares) y[i] = *reinterpret_cast<const float4*>(from + s * static_cast<long long>(ROWS) * D);
+    }
+  }
   float2 f[2];
   float mx = -INFINITY;
 #pragma unroll
@@ -766,17 +777,13 @@ __global__ void __launch_bounds__(256) vattn_paged_join_kernel(const __grid_cons
   if (lane == 0) red[8 + warp] = sum;
   __syncthreads();
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (d < D) {
-    const float* from = p.part_o + at0 * D + d;
-#pragma unroll 4
-    for (int s = warp * 4 + (lane >> 3); s < shares; s += 32) {
-      const float4 y = *reinterpret_cast<const float4*>(from + s * static_cast<long long>(ROWS) * D);
-      const float a = weight[s];
-      acc.x = fmaf(a, y.x, acc.x);
-      acc.y = fmaf(a, y.y, acc.y);
-      acc.z = fmaf(a, y.z, acc.z);
-      acc.w = fmaf(a, y.w, acc.w);
-    }
+#pragma unroll
+  for (int i = 0; i < kCachedMaxSplits / 32; ++i) {  // (weights behind the last share are 0)
+    const float a = weight[warp * 4 + (lane >> 3) + 32 * i];
+    acc.x = fmaf(a, y[i].x, acc.x);
+    acc.y = fmaf(a, y[i].y, acc.y);
+    acc.z = fmaf(a, y[i].z, acc.z);
+    acc.w = fmaf(a, y[i].w, acc.w);
   }
 #pragma unroll
   for (int o = 8; o < 32; o *= 2) {
@@ -822,6 +829,13 @@ __global__ void __launch_bounds__(256) vattn_paged_join_few_kernel(const __grid_
   if (shares == 1) return;  // written by its block
   const bool none = cached_word(w, b, t, sp.base) == 0;
   const long long at0 = (bk * p.row_blocks + rr / ROWS) * p.splits * ROWS + rr % ROWS;
+  const float* from = p.part_o + at0 * D + (lane * 4 < D ? lane * 4 : 0);
+  constexpr int kAhead = 12;  // shares on their way while the weights are formed
+  float4 ahead[kAhead];
+#pragma unroll
+  for (int s = 0; s < kAhead; ++s)
+    ahead[s] = s < shares ? *reinterpret_cast<const float4*>(from + s * static_cast<long long>(ROWS) * D)
+                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   const float2 ml = lane < shares ? reinterpret_cast<const float2*>(p.part_ml)[at0 + lane * static_cast<long long>(ROWS)]
                                   : make_float2(-INFINITY, 0.0f);
   const float mx = warp_max(ml.x), ref = mx == -INFINITY ? 0.0f : mx;
@@ -830,16 +844,17 @@ __global__ void __launch_bounds__(256) vattn_paged_join_few_kernel(const __grid_
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  const float* from = p.part_o + at0 * D + (lane * 4 < D ? lane * 4 : 0);
-#pragma unroll 8
-  for (int s = 0; s < shares; ++s) {
-    const float4 y = *reinterpret_cast<const float4*>(from + s * static_cast<long long>(ROWS) * D);
-    const float a = __shfl_sync(0xffffffffu, weight, s);
+  auto add = [&](int s, const float4& y) {
+    const float a = __shfl_sync(0xffffffffu, weight, s);  // (0 behind the last share)
     acc.x = fmaf(a, y.x, acc.x);
     acc.y = fmaf(a, y.y, acc.y);
     acc.z = fmaf(a, y.z, acc.z);
     acc.w = fmaf(a, y.w, acc.w);
-  }
+  };
+#pragma unroll
+  for (int s = 0; s < kAhead; ++s) add(s, ahead[s]);
+#pragma unroll 4
+  for (int s = kAhead; s < shares; ++s) add(s, *reinterpret_cast<const float4*>(from + s * static_cast<long long>(ROWS) * D));
   if (lane * 4 >= D) return;
   const float inv = 1.0f / sum;
   const bool zero = none || sum == 0.0f;
