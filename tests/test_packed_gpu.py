@@ -106,6 +106,29 @@ def test_many_prompts(td):
     assert vef.device_status() == 0
 
 
+@pytest.mark.parametrize("n_seqs", [1, 2, 31, 32, 33, 64, 97, 127, 128, 129, 200])
+@pytest.mark.parametrize("heads", [(1, 1), (3, 1), (4, 2), (7, 1)])
+def test_blocks_find_what_the_list_has(td, heads, n_seqs):
+    """Around the most prompts for which blocks find their pairs themselves, several rounds of
+    them, odd and even groups: against each prompt alone."""
+    torch, dev = td
+    rng = np.random.default_rng(n_seqs)
+    lens = rng.integers(0, 700, size=n_seqs)
+    lens[rng.integers(0, n_seqs)] = 3000
+    lens = lens.tolist()
+    q, k, v = rows(td, "bf16", heads, sum(lens), 64, 4800 + n_seqs, "packed")
+    out = torch.full_like(q, 7.0)
+    vef.forward_packed(q, k, v, starts(torch, lens, dev), scale=0.125, out=out)
+    ends = np.cumsum(lens)
+    for b in {0, n_seqs - 1, int(np.argmax(lens)), *rng.integers(0, n_seqs, 8).tolist()}:
+        n, at = lens[b], int(ends[b]) - lens[b]
+        if n:
+            want = vef.forward_window(*(x[:, :, at:at + n].contiguous() for x in (q, k, v)), scale=0.125)
+            assert torch.equal(out[:, :, at:at + n], want), b
+    assert not bool((out == 7).all(-1).any())  # every row was computed
+    assert vef.device_status() == 0
+
+
 def test_a_buffer_longer_than_the_list_in_shared_memory(td):
     """Over 2^20 rows: the list is counted in the workspace."""
     torch, dev = td

@@ -29,6 +29,7 @@ DEPS = SOURCES + [os.path.join(CSRC, "attn_kernel.cuh"), os.path.join(CSRC, "sta
                   os.path.join(CSRC, "cached_kernel.cuh"), os.path.join(CSRC, "rope_rows.cuh"),
                   os.path.join(CSRC, "e4m3.cuh"), os.path.join(CSRC, "paged_append_kernel.cuh"),
                   os.path.join(CSRC, "paged_kernel.cuh"), os.path.join(CSRC, "packed_list_kernel.cuh"),
+                  os.path.join(CSRC, "packed_find.cuh"),
                   os.path.join(ROOT, "include", "vattn.h"),
                   os.path.join(ROOT, "include", "vattn_decoder.h"),
                   os.path.join(ROOT, "include", "vattn_serving.h")]

@@ -186,7 +186,7 @@ template <typename T, int NKB>
 vattn_status window_fwd_launch(const CUtensorMap (&tm)[4], const vattn::WindowFwdParams& p, int sms, int device,
                                cudaStream_t stream) {
   using P = vattn::WindowFwdPlan<NKB>;
-  auto kernel = vattn::vattn_window_fwd_kernel<T, NKB, false>;
+  auto kernel = vattn::vattn_window_fwd_kernel<T, NKB, vattn::kPadded>;
   static std::atomic<uint8_t> done[vattn::host::kMaxDevices];
   const vattn_status st = allow_smem(kernel, P::kSmemBytes, done, device);
   if (st != VATTN_OK) return st;

@@ -14,7 +14,7 @@
 
 namespace vattn {
 
-constexpr int kListThreads = 1024;  // most; 256 for few prompts
+constexpr int kListThreads = 1024;
 constexpr int kListBuckets = 8192;  // counts in shared memory up to here (2^20 rows), else in the workspace
 
 struct PackedListParams {
@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(kListThreads) vattn_packed_list_kernel(const _
   __shared__ long long rows_s[kListThreads / 32];
   ptx::grid_dep_launch();  // the attention kernel sets itself up meanwhile, and waits for this one's end
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
-  const int threads = static_cast<int>(blockDim.x), warps = threads / 32;
+  constexpr int threads = kListThreads, warps = threads / 32;
   int* const counts = p.counts != nullptr ? p.counts : counts_s;
   for (int i = tid; i < p.buckets; i += threads) counts[i] = 0;
   __syncthreads();

@@ -237,17 +237,26 @@ vattn_status paged_dispatch(const vattn::PagedParams& p, const Pools& pools, int
 }
 
 // ------------------------------------------------------------ packed prompts
-template <typename T, int NKB>
-vattn_status packed_launch(const CUtensorMap (&tm)[4], const vattn::WindowFwdParams& p, int64_t items, int sms, int device,
-                           cudaStream_t stream) {
+template <typename T, int NKB, int kMode>
+vattn_status packed_go(const CUtensorMap (&tm)[4], const vattn::WindowFwdParams& p, unsigned grid, int device,
+                       cudaStream_t stream) {
   using P = vattn::WindowFwdPlan<NKB>;
-  auto kernel = vattn::vattn_window_fwd_kernel<T, NKB, true>;
+  auto kernel = vattn::vattn_window_fwd_kernel<T, NKB, kMode>;
   static std::atomic<uint8_t> done[kMaxDevices];
   const vattn_status st = allow_smem(kernel, P::kSmemBytes, done, device);
   if (st != VATTN_OK) return st;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, sms));
-  return launch_behind("packed attention kernel launch", kernel, dim3(grid), dim3(P::kThreads), P::kSmemBytes, stream,
-                       tm[0], tm[1], tm[2], tm[3], p);
+  if (kMode == vattn::kPackedListed)
+    return launch_behind("packed attention kernel launch", kernel, dim3(grid), dim3(P::kThreads), P::kSmemBytes, stream,
+                         tm[0], tm[1], tm[2], tm[3], p);
+  kernel<<<grid, P::kThreads, P::kSmemBytes, stream>>>(tm[0], tm[1], tm[2], tm[3], p);
+  return launched("packed attention kernel launch");
+}
+
+template <typename T, int NKB>
+vattn_status packed_launch(const CUtensorMap (&tm)[4], const vattn::WindowFwdParams& p, unsigned grid, int device,
+                           cudaStream_t stream) {
+  return p.list != nullptr ? packed_go<T, NKB, vattn::kPackedListed>(tm, p, grid, device, stream)
+                           : packed_go<T, NKB, vattn::kPackedFound>(tm, p, grid, device, stream);
 }
 
 }  // namespace
@@ -438,31 +447,38 @@ vattn_status vattn_forward_packed(const vattn_rows* q, const vattn_rows* k, cons
       (st = make_rows_map(&tm[3], &p.mo, to, a->dtype, 32, 32)) != VATTN_OK)
     return st;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-  vattn::PackedListParams l{};
-  l.cu = cu_seqlens;
-  l.n_seqs = static_cast<int>(n_seqs);
-  l.total = static_cast<int>(a->n_queries);
-  l.group = p.w.group;
-  l.kv_heads = p.w.kv_heads;
-  l.sms = sms;
-  l.buckets = (l.total + vattn::kTile - 1) / vattn::kTile;
-  const size_t list_bytes = static_cast<size_t>(1 + cap) * sizeof(int4);
-  const size_t count_bytes = l.buckets > vattn::kListBuckets ? static_cast<size_t>(l.buckets) * 4u : 0;
+  const int64_t items = cap * p.w.kv_heads;  // pairs; single units only where all fit the blocks at once
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(2 * items, sms));
+  p.cu = cu_seqlens;
+  p.n_seqs = static_cast<int>(n_seqs);
+  p.sms = sms;
   Workspace ws;
-  if ((st = ws.take(list_bytes + count_bytes, device, stream)) != VATTN_OK) return st;
-  l.list = reinterpret_cast<int4*>(ws.data());
-  if (count_bytes > 0) l.counts = reinterpret_cast<int*>(ws.data() + list_bytes);
-  p.list = l.list;
-  const int list_threads = n_seqs <= 64 && cap <= 4096 ? 256 : vattn::kListThreads;
-  vattn::vattn_packed_list_kernel<<<1, list_threads, 0, stream>>>(l);
-  if ((st = launched("packed list kernel launch")) != VATTN_OK) return st;
-  const int64_t items = 2 * cap * p.w.kv_heads;
+  if (n_seqs <= vattn::kFindPrompts && items <= static_cast<int64_t>(vattn::kFindRounds) * grid) {
+    p.seqs = fast_div(grid);
+  } else {
+    vattn::PackedListParams l{};
+    l.cu = cu_seqlens;
+    l.n_seqs = static_cast<int>(n_seqs);
+    l.total = static_cast<int>(a->n_queries);
+    l.group = p.w.group;
+    l.kv_heads = p.w.kv_heads;
+    l.sms = sms;
+    l.buckets = (l.total + vattn::kTile - 1) / vattn::kTile;
+    const size_t list_bytes = static_cast<size_t>(1 + cap) * sizeof(int4);
+    const size_t count_bytes = l.buckets > vattn::kListBuckets ? static_cast<size_t>(l.buckets) * 4u : 0;
+    if ((st = ws.take(list_bytes + count_bytes, device, stream)) != VATTN_OK) return st;
+    l.list = reinterpret_cast<int4*>(ws.data());
+    if (count_bytes > 0) l.counts = reinterpret_cast<int*>(ws.data() + list_bytes);
+    p.list = l.list;
+    vattn::vattn_packed_list_kernel<<<1, vattn::kListThreads, 0, stream>>>(l);
+    if ((st = launched("packed list kernel launch")) != VATTN_OK) return st;
+  }
   if (a->dtype == VATTN_F16)
-    st = a->head_dim <= 64 ? packed_launch<__half, 1>(tm, p, items, sms, device, stream)
-                           : packed_launch<__half, 2>(tm, p, items, sms, device, stream);
+    st = a->head_dim <= 64 ? packed_launch<__half, 1>(tm, p, grid, device, stream)
+                           : packed_launch<__half, 2>(tm, p, grid, device, stream);
   else
-    st = a->head_dim <= 64 ? packed_launch<__nv_bfloat16, 1>(tm, p, items, sms, device, stream)
-                           : packed_launch<__nv_bfloat16, 2>(tm, p, items, sms, device, stream);
+    st = a->head_dim <= 64 ? packed_launch<__nv_bfloat16, 1>(tm, p, grid, device, stream)
+                           : packed_launch<__nv_bfloat16, 2>(tm, p, grid, device, stream);
   if (st != VATTN_OK) return st;
   return ws.release();
 }

@@ -56,6 +56,7 @@
 // the look itself and by the registers that it takes from the softmax.)
 #pragma once
 
+#include "packed_find.cuh"
 #include "window_pipe.cuh"
 
 namespace vattn {
@@ -70,8 +71,12 @@ struct WindowFwdParams {
   int units;           // ceil(n_queries / 128) * group
   int items;           // < 2^30
   int whole;           // items from here on are single units (none of them, or all)
-  const int4* list;    // packed prompts: {items, whole, 0, 0}, then the pairs (packed_list_kernel.cuh)
-  FastDiv seqs, kv_heads, group;  // batch * kv_heads, kv_heads, group
+  // packed prompts: {items, whole, 0, 0}, then the pairs (packed_list_kernel.cuh), or
+  // their starts and number, from which the block finds its own (packed_find.cuh)
+  const int4* list;
+  const int32_t* cu;
+  int n_seqs, sms;
+  FastDiv seqs, kv_heads, group;  // batch * kv_heads (kPackedFound: blocks), kv_heads, group
   float scale_log2;    // scale * log2(e)
 };
 
@@ -114,24 +119,35 @@ __device__ __forceinline__ int window_entry(int r) {
   return r * grid + ((r & 1) ? grid - 1 - k : k);
 }
 
-// kPacked: prompts of different lengths in one buffer (vattn_forward_packed).  Two
-// consecutive units of one sequence are a pair of the list, late ones first, which
-// the list's kernel wrote; each makes an item of every key head.
-template <bool kPacked>
+// Padded batches (vattn_forward_window), or prompts of different lengths in one
+// buffer (vattn_forward_packed).  Two consecutive units of one prompt are a pair,
+// pairs of late rows come first, and each makes an item of every key head: from a
+// list that a kernel before wrote, or found by the block.
+enum WindowMode : int { kPadded = 0, kPackedListed = 1, kPackedFound = 2 };
+
+template <int kMode>
 __device__ __forceinline__ int window_items(const WindowFwdParams& p) {
-  return kPacked ? p.list[0].x : p.items;
+  if constexpr (kMode == kPadded) return p.items;
+  else if constexpr (kMode == kPackedListed) return p.list[0].x;
+  else return found_pairs()[0].x;
 }
 
-template <bool kPacked>
+template <int kMode>
 __device__ __forceinline__ WindowItem window_item(const WindowFwdParams& p, int entry) {
   WindowItem it;
   uint32_t bk, kh;
-  const int whole = kPacked ? p.list[0].y : p.whole;
+  const int whole = kMode == kPadded ? p.whole : (kMode == kPackedListed ? p.list[0].y : found_pairs()[0].y);
   const bool pair_on = entry < whole;
   const int item = pair_on ? entry : whole + (entry - whole) / 2, only = (entry - whole) & 1;
   int pair, units;
-  if constexpr (kPacked) {
-    const int4 x = p.list[1 + p.kv_heads.div(static_cast<uint32_t>(item), &kh)];
+  if constexpr (kMode != kPadded) {
+    int4 x;
+    if constexpr (kMode == kPackedListed) {
+      x = p.list[1 + p.kv_heads.div(static_cast<uint32_t>(item), &kh)];
+    } else {
+      x = found_pairs()[1 + p.seqs.div(static_cast<uint32_t>(entry))];  // the block's round
+      kh = static_cast<uint32_t>(x.w);
+    }
     it.b = 0;
     it.base = x.x;
     it.rows = x.y;
@@ -264,9 +280,9 @@ struct WindowSee {
 
 // Does V hold something that is not finite at a key which is hidden from one of
 // the warp's rows (unit t of an item), in a tile that the unit uses?
-template <typename T, bool kPacked>
+template <typename T, int kMode>
 __device__ __noinline__ bool window_leak(const WindowFwdParams& p, int entry, int t) {
-  const WindowItem it = window_item<kPacked>(p, entry);
+  const WindowItem it = window_item<kMode>(p, entry);
   const WindowMasked masked(p.w, it);
   const WindowSee see(it, t);
   const UnitRange u = t == 0 ? it.u[0] : it.u[1];
@@ -317,11 +333,11 @@ __device__ __forceinline__ bool window_clean_v(uint32_t v, int left) {
 // What window_clean_v took out of the item's tiles, added to the O of unit t's
 // rows in TMEM (one warp, its 32 rows); bit i of `note`: the i-th partly masked
 // tile.  Every weight is positive, so an infinity stays what it is.
-template <typename T, bool kPacked>
+template <typename T, int kMode>
 __device__ __noinline__ void window_add_back(const WindowFwdParams& p, int entry, int t, uint32_t note, uint32_t o_addr) {
   constexpr uint32_t kExp = Elem<T>::kBf16 ? 0x7f80u : 0x7c00u, kMan = Elem<T>::kBf16 ? 0x7fu : 0x3ffu;
   constexpr int kAhead = 8;
-  const WindowItem it = window_item<kPacked>(p, entry);
+  const WindowItem it = window_item<kMode>(p, entry);
   const WindowMasked masked(p.w, it);
   const WindowSee see(it, t);
   const UnitRange u = t == 0 ? it.u[0] : it.u[1];
@@ -378,7 +394,7 @@ __device__ __noinline__ void window_add_back(const WindowFwdParams& p, int entry
 // Warps 0 to 3: loads, matrix products, and in the second pass clean V tiles.
 // One code for both passes: a second instance, though never run, made calls
 // between other kernels 6 to 8 us slower.
-template <typename T, int NKB, bool kPacked>
+template <typename T, int NKB, int kMode>
 __device__ __forceinline__ void window_feed(const WindowCtx& x, bool second, uint32_t bar0, const CUtensorMap& tm_q,
                                             const CUtensorMap& tm_k, const CUtensorMap& tm_v) {
   using P = WindowFwdPlan<NKB>;
@@ -389,7 +405,7 @@ __device__ __forceinline__ void window_feed(const WindowCtx& x, bool second, uin
   const int warp = x.warp, lane = x.lane;
   auto bar = [bar0](uint32_t i) -> uint32_t { return bar0 + 8u * i; };
   const int from = second ? x.again(0) : 0, to = second ? x.again(1) : 0x7fffffff;
-  const int items = window_items<kPacked>(p);
+  const int items = window_items<kMode>(p);
   if (warp == 0 && lane == 0) {
     // ---------------------------------------------------- K and V tiles
     const uint64_t keep = ptx::policy_evict_last();  // read again by other heads and rows
@@ -398,7 +414,7 @@ __device__ __forceinline__ void window_feed(const WindowCtx& x, bool second, uin
     // where entry st arrives: V in the second pass at warp 3's, which passes it on
     auto lands = [&](int st) { return bar(second && (st & 1) != 0 ? kWbVLanded + (st >> 1) : kWbKvFull + st); };
     for (int r = from, item; ok && r <= to && (item = window_entry(r)) < items; ++r) {
-      const WindowItem it = window_item<kPacked>(p, item);
+      const WindowItem it = window_item<kMode>(p, item);
       for (int i = 0; ok && i < it.n; ++i) {
         const int row = it.base + it.tile(i) * kTile;
         for (int kv = 0; kv < 2; ++kv, ++c) {
@@ -420,7 +436,7 @@ __device__ __forceinline__ void window_feed(const WindowCtx& x, bool second, uin
     const uint64_t once = ptx::policy_evict_first();
     uint32_t n_q = 0;
     for (int r = from, item; r <= to && (item = window_entry(r)) < items; ++r) {
-      const WindowItem it = window_item<kPacked>(p, item);
+      const WindowItem it = window_item<kMode>(p, item);
       if (it.n == 0) continue;
       if (n_q > 0 && !pipe.wait(bar(kWbQEmpty), (n_q - 1) & 1u, kSiteWinQ)) break;
       ptx::mbar_arrive_expect_tx(bar(kWbQFull), (it.on[0] && it.on[1] ? 2 : 1) * P::kTileBytes);
@@ -490,7 +506,7 @@ __device__ __forceinline__ void window_feed(const WindowCtx& x, bool second, uin
     uint32_t g = 0;  // key tiles of this block so far (modulo 2^32); K of tile g is ring entry 2 g, V 2 g + 1
     bool ok = true;
     for (int r = from, item; ok && r <= to && (item = window_entry(r)) < items; ++r) {
-      const WindowItem it = window_item<kPacked>(p, item);
+      const WindowItem it = window_item<kMode>(p, item);
       if (it.n == 0) continue;
       if (!(ok = pipe.wait_warp(bar(kWbQFull), n_q & 1u, kSiteWinMma))) break;
       ++n_q;
@@ -514,7 +530,7 @@ __device__ __forceinline__ void window_feed(const WindowCtx& x, bool second, uin
         }
         if (!(ok = wait_kv(2 * g + 1))) break;
         const int left = it.s.len - j * kTile;  // V rows of the sequence in this tile
-        if (left < kTile && (kPacked || it.s.len < p.w.n_keys)) {
+        if (left < kTile && (kMode != kPadded || it.s.len < p.w.n_keys)) {
           const uint32_t v = base_s + P::kOffKv + (2 * g + 1) % S * P::kTileBytes;
           for (int kb = 0; kb < NKB; ++kb)
             for (int y = left * 8 + lane; y < kTile * 8; y += 32)
@@ -545,7 +561,7 @@ __device__ __forceinline__ void window_feed(const WindowCtx& x, bool second, uin
     uint32_t g = 0, n_items = 0;  // tiles, items with tiles so far
     bool ok = true;
     for (int r = from, item; ok && r <= to && (item = window_entry(r)) < items; ++r) {
-      const WindowItem it = window_item<kPacked>(p, item);
+      const WindowItem it = window_item<kMode>(p, item);
       if (it.n == 0) continue;
       const WindowMasked masked(p.w, it);
       const uint32_t slot = n_items & 1u;
@@ -569,7 +585,7 @@ __device__ __forceinline__ void window_feed(const WindowCtx& x, bool second, uin
 }
 
 // Warps 4 to 11: softmax and results.
-template <typename T, int NKB, bool kSecond, bool kPacked>
+template <typename T, int NKB, bool kSecond, int kMode>
 __device__ __forceinline__ void window_soft(const WindowCtx& x, uint32_t bar0, const CUtensorMap& tm_o) {
   using P = WindowFwdPlan<NKB>;
   const WindowFwdParams& p = x.p;
@@ -585,13 +601,13 @@ __device__ __forceinline__ void window_soft(const WindowCtx& x, uint32_t bar0, c
   const uint32_t o_addr = tmem + lanes + P::kColO + t * P::kStrideO;
   const uint32_t stage_out = base_s + P::kOffOut + static_cast<uint32_t>(warp - 4) * 4096u;
   const uint64_t once = ptx::policy_evict_first();
-  const int D = p.w.dim, W = p.w.window, items = window_items<kPacked>(p);
+  const int D = p.w.dim, W = p.w.window, items = window_items<kMode>(p);
   uint32_t n_s = 0;  // tiles of this unit so far
   int n_out = 0;     // result boxes of this warp so far
   bool ok = true;
   uint32_t n_items = 0;  // second pass: items with tiles so far
   for (int round = kSecond ? x.again(0) : 0, item; ok && (!kSecond || round <= x.again(1)) && (item = window_entry(round)) < items; ++round) {
-    const WindowItem it = window_item<kPacked>(p, item);
+    const WindowItem it = window_item<kMode>(p, item);
     if (!(t == 0 ? it.on[0] : it.on[1])) {
       if (kSecond && it.n > 0) pipe_warp_arrive(bar(kWbNotesFree + (n_items++ & 1u)));
       continue;
@@ -699,7 +715,7 @@ __device__ __forceinline__ void window_soft(const WindowCtx& x, uint32_t bar0, c
       ++n_items;
       const uint32_t note = ptx::ld_shared_volatile(x.note_at(slot));
       pipe_warp_arrive(bar(kWbNotesFree + slot));
-      if (note != 0 && !u.empty()) window_add_back<T, kPacked>(p, item, t, note, o_addr);
+      if (note != 0 && !u.empty()) window_add_back<T, kMode>(p, item, t, note, o_addr);
     }
     const float inv = 1.0f / l;
     float check = 0.0f;  // NaN once an element is not finite
@@ -716,7 +732,7 @@ __device__ __forceinline__ void window_soft(const WindowCtx& x, uint32_t bar0, c
         if (c + 2 * e < D) check = fmaf(a, 0.0f, fmaf(b, 0.0f, check));
         y[e] = pack2<T>(a, b);
       }
-      if (kPacked && row0 + (warp & 3) * 32 + 32 > it.rows) {  // the rows behind are another sequence's
+      if (kMode != kPadded && row0 + (warp & 3) * 32 + 32 > it.rows) {  // the rows behind are another sequence's
         if (row0 + r < it.rows) {
           T* to = rows_at_mut<T>(p.out, 0, head, static_cast<long long>(it.base) + row0 + r) + c;
 #pragma unroll
@@ -745,7 +761,7 @@ __device__ __forceinline__ void window_soft(const WindowCtx& x, uint32_t bar0, c
     const int row = row0 + r;
     // finite weights, but not the result: was it a hidden element of V?
     if (!kSecond && __any_sync(0xffffffffu, row < it.rows && row_on && check != 0.0f && l - l == 0.0f) &&
-        window_leak<T, kPacked>(p, item, t) && lane == 0) {
+        window_leak<T, kMode>(p, item, t) && lane == 0) {
       asm volatile("red.shared.min.s32 [%0], %1;" ::"r"(pipe.at + kPipeBytes), "r"(round) : "memory");
       asm volatile("red.shared.max.s32 [%0], %1;" ::"r"(pipe.at + kPipeBytes + 4), "r"(round) : "memory");
     }
@@ -757,7 +773,7 @@ __device__ __forceinline__ void window_soft(const WindowCtx& x, uint32_t bar0, c
   if (lane == 0) ptx::bulk_wait_group_all();
 }
 
-template <typename T, int NKB, bool kPacked>
+template <typename T, int NKB, int kMode>
 __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
     vattn_window_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                             const __grid_constant__ CUtensorMap tm_k,
@@ -813,16 +829,21 @@ __global__ void __launch_bounds__(WindowFwdPlan<NKB>::kThreads, 1)
   ptx::tc_fence_after();
   const WindowCtx x{p, pipe, base_s, *tmem_slot, warp, lane};
   ptx::grid_dep_wait();  // what earlier kernels of the stream wrote is visible
+  if constexpr (kMode == kPackedFound) {
+    find_pairs({p.cu, p.n_seqs, p.w.n_queries, p.w.group, p.w.kv_heads, p.sms, p.kv_heads}, P::kThreads / 32,
+               [](int r) { return window_entry(r); });
+    __syncthreads();
+  }
 
   bool two = false;
   if (warp < 4) {
     ptx::regs_decrease<P::kRegsOther>();
     for (int pass = 0; pass == 0 || (pass == 1 && (two = x.second())); ++pass)
-      window_feed<T, NKB, kPacked>(x, pass != 0, bar0 + (pass != 0 ? 8u * kWbCount : 0u), tm_q, tm_k, tm_v);
+      window_feed<T, NKB, kMode>(x, pass != 0, bar0 + (pass != 0 ? 8u * kWbCount : 0u), tm_q, tm_k, tm_v);
   } else {
     ptx::regs_increase<P::kRegsSoftmax>();
-    window_soft<T, NKB, false, kPacked>(x, bar0, tm_o);
-    if (x.second()) window_soft<T, NKB, true, kPacked>(x, bar0 + 8u * kWbCount, tm_o);
+    window_soft<T, NKB, false, kMode>(x, bar0, tm_o);
+    if (x.second()) window_soft<T, NKB, true, kMode>(x, bar0 + 8u * kWbCount, tm_o);
   }
 
   ptx::tc_fence_before();
