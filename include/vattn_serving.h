@@ -93,8 +93,9 @@ vattn_status vattn_append_paged(const vattn_rows* k, const vattn_rows* v, const 
  * New token t's own key and value are cache row kv_len[b] - T + t, appended
  * before.  Sums and statistics are f32; q and the cache's values enter the
  * products exactly (bf16 q down to 2^-29 of its row's largest), the softmax
- * weights, times the values' scale, as f16.  Scales are positive; those of
- * one sequence's values lie within 2^100 of each other.  What rows that no
+ * weights, times the values' scale, as f16.  Scales are positive (powers of
+ * two or not), or 0, counted as 2^-64, for zeros; those of one sequence's
+ * values lie within 2^100 of each other.  What rows that no
  * query sees hold, bytes or scales, does not reach the result; a NaN reaches
  * the queries that see it.  Scores that are not finite: as in
  * vattn_forward_window.

@@ -204,6 +204,12 @@ def test_scales_far_apart(td):
             with_scale = cache[:3] + [v_scale] + cache[4:]
             out = vef.forward_paged(q, *with_scale, **how)
             against_the_oracle(out, q, with_scale, None, 0, None, how["scale"], name, f"2^{lo} .. 2^{hi}")
+        # a scale of 0: zeros
+        v_scale = cache[3].clone()
+        v_scale[cache[4][0, 2:5].long()] = 0
+        with_scale = cache[:3] + [v_scale] + cache[4:]
+        out = vef.forward_paged(q, *with_scale, **how)
+        against_the_oracle(out, q, with_scale, None, 0, None, how["scale"], name, "a scale of 0")
     # a page of zeros with the smallest scale, which takes nearly all of the weight
     case = ("bf16", (1, 1, 1, 1, 16), 16, [32], None, 0, False, "heads", "plain")
     q, cache, _, how = build(td, case, 1401)

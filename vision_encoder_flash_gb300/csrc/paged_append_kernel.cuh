@@ -14,6 +14,14 @@
 // again), and the next heads' come through a cp.async ring of its own in shared
 // memory.  The angles' sines and cosines serve all heads of the block, likewise from
 // shared memory that only their thread uses.
+//
+// 6 prompts of 16384 tokens together, 8 heads x 128 bf16, pages of 64: 27.1 us, 3.7
+// TB/s (56 % of the measured copy rate; 49.3 us with a block for each head and its own
+// angles).  Bound by instructions: 2.1 a cycle, some 15 an element pair, a third of
+// them per head and page (maximum over the block, scale, addresses) and per block
+// (angles, places).  Two slots a thread and 256 threads for a page of 64: with four 35
+// us, with one 37; three blocks a multiprocessor, at 80 registers, 42.  8 heads x 1
+// token: 3.5 us.
 #pragma once
 
 #include "e4m3.cuh"
