@@ -89,6 +89,8 @@ CASES = [
     ("f16", 2, 48, 112, 7, "heads", "packed"),      # an odd number of rotated dims
     ("f16", 1, 32, 1024, 32, "heads", "plain"),     # more of a page than the threads hold
     ("bf16", 1, 112, 256, 0, "both", "packed"),     # no rotation
+    ("bf16", 3, 80, 48, 40, "tokens", "packed"),    # halves that 8 bytes cut, and 16 do not
+    ("f16", 2, 48, 1024, 24, "heads", "plain"),     # such, and more of a page than the threads hold
 ]
 
 

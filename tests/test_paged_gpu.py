@@ -103,7 +103,7 @@ def test_against_the_oracle(td, i):
 
 
 @pytest.mark.parametrize("D", [16, 32, 48, 64, 80, 96, 112, 128])
-@pytest.mark.parametrize("H,T", [(1, 1), (4, 4), (5, 5), (8, 4), (11, 3), (7, 11)])
+@pytest.mark.parametrize("H,T", [(1, 1), (4, 4), (4, 6), (5, 5), (8, 4), (11, 3), (8, 7), (7, 11), (4, 31), (5, 50)])
 def test_rows_and_widths(td, H, T, D):
     """Rows for one, two and four groups of warps, of every width, boxes of 16, 32 and 64 rows."""
     torch, dev = td
@@ -294,6 +294,30 @@ def test_values_that_are_not_finite(td):
     same = torch.ones(out.shape[:3], dtype=torch.bool, device=dev)
     same[0, 0, 0] = same[0, 3, 2] = False
     assert torch.equal(out[same], clean[same])
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("H,T", [(4, 6), (4, 12), (4, 15), (4, 31)])
+def test_a_nan_in_wide_blocks(td, H, T, D):
+    """A NaN value among the new tokens of a tree: all of the rows that see it, and no others."""
+    torch, dev = td
+    case = ("f16", (2, H, 1, T, D), 32, [300, 77], 150, 5, True, "heads", "plain")
+    q, cache, words, how = build(td, case, 1580 + T + D)
+    clean = vef.forward_paged(q, *cache, **how)
+    against_the_oracle(clean, q, cache, 150, 5, words, how["scale"], "f16")
+    bad = list(cache)
+    bad[1] = cache[1].view(torch.uint8).clone()
+    at = [1, T - 2]  # of each sequence's new tokens
+    for b, n in enumerate(case[3]):
+        row = n - T + at[b]
+        bad[1][cache[4][b, row // 32].item(), 0, row % 32] = 0x7f
+    bad[1] = bad[1].view(cache[1].dtype)
+    out = vef.forward_paged(q, *bad, **how)
+    seen = torch.tensor([[bool(words[b][t] >> at[b] & 1) for t in range(T)] for b in range(2)], device=dev)
+    seen = seen[:, None, :, None].expand_as(out)
+    assert bool(seen.any()) and not bool(seen.all())
+    assert bool(torch.isnan(out[seen]).all())
+    against_the_oracle(torch.where(seen, clean, out), q, cache, 150, 5, words, how["scale"], "f16")
 
 
 def test_agrees_with_the_16_bit_cache(td):

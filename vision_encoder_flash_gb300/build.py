@@ -1,6 +1,6 @@
 """Build ``libvattn.so`` (the C-ABI library) in-tree with nvcc for sm_103a.
 
-Three translation units compiled in parallel, one ``-gencode`` (compute_103a -> sm_103a), CUDA
+Five translation units compiled in parallel, one ``-gencode`` (compute_103a -> sm_103a), CUDA
 runtime linked statically so the library loads on hosts without a GPU
 driver (the tests check its exported symbols there).
 """
@@ -14,7 +14,7 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-SOURCES = [os.path.join(CSRC, name) for name in ("vattn_api.cu", "decoder_api.cu", "serving_api.cu")]
+SOURCES = [os.path.join(CSRC, name) for name in ("vattn_api.cu", "decoder_api.cu", "serving_api.cu", "paged_f16.cu", "paged_bf16.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, "attn_kernel.cuh"), os.path.join(CSRC, "stage_kernel.cuh"),
                   os.path.join(CSRC, "rope_kernel.cuh"),
                   os.path.join(CSRC, "conv1d_kernel.cuh"),
@@ -30,6 +30,7 @@ DEPS = SOURCES + [os.path.join(CSRC, "attn_kernel.cuh"), os.path.join(CSRC, "sta
                   os.path.join(CSRC, "e4m3.cuh"), os.path.join(CSRC, "paged_append_kernel.cuh"),
                   os.path.join(CSRC, "paged_kernel.cuh"), os.path.join(CSRC, "packed_list_kernel.cuh"),
                   os.path.join(CSRC, "packed_find.cuh"),
+                  os.path.join(CSRC, "pages_host.h"), os.path.join(CSRC, "paged_launch.cuh"),
                   os.path.join(ROOT, "include", "vattn.h"),
                   os.path.join(ROOT, "include", "vattn_decoder.h"),
                   os.path.join(ROOT, "include", "vattn_serving.h")]

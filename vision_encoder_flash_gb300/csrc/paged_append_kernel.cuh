@@ -22,6 +22,10 @@
 // (angles, places).  Two slots a thread and 256 threads for a page of 64: with four 35
 // us, with one 37; three blocks a multiprocessor, at 80 registers, 42.  8 heads x 1
 // token: 3.5 us.
+//
+// V, elements of a slot's halves: 8, or 4 where the rotated dims or the strides do not
+// divide into 16 bytes (80 dims of which 40 are rotated), or 1, which reads all of
+// its rows twice.
 #pragma once
 
 #include "e4m3.cuh"
@@ -32,7 +36,6 @@
 namespace vattn {
 
 constexpr int kAppendThreads = 512;  // most
-constexpr int kAppendHold = 2;       // slots a thread holds
 constexpr int kAppendStages = 2;     // heads in its ring
 constexpr int kMinScaleExponent = -32;
 
@@ -90,16 +93,32 @@ __device__ __forceinline__ AppendSeq append_seq(const AppendParams& p, int item)
   return s;
 }
 
-// Shared memory of a block, bytes a thread: a held slot's eight (cos, sin), and its rows.
+// Slots that a thread holds.
 template <int V>
-constexpr int append_smem(int threads) { return V == 8 ? threads * kAppendHold * (64 + kAppendStages * 32) : 0; }
+constexpr int kAppendHold = V >= 4 ? 16 / V : 0;
+
+// Shared memory of a block: each held slot's V (cos, sin), and its rows.
+template <int V>
+constexpr int append_smem(int threads) { return threads * kAppendHold<V> * (8 * V + kAppendStages * 4 * V); }
+
+// V elements of 16 bits.
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> append_shared(uint32_t addr) {
+  if constexpr (V == 8) {
+    const float4 y = ptx::ld_shared_v4(addr);
+    return *reinterpret_cast<const Vec<T, V>*>(&y);
+  } else {
+    const float2 y = ptx::ld_shared_v2(addr);
+    return *reinterpret_cast<const Vec<T, V>*>(&y);
+  }
+}
 
 template <typename T, int V>
 __global__ void __launch_bounds__(kAppendThreads) vattn_append_paged_kernel(const __grid_constant__ AppendParams p) {
-  extern __shared__ float4 angle_s[];  // [4][held slot][thread]: cosines, cosines, sines, sines; then the rings
+  extern __shared__ float4 angle_s[];  // [V / 2][held slot][thread]: cosines, then sines; then the rings
   __shared__ uint64_t turn[kQkMaxDim / 2];
   __shared__ __align__(16) float top_s[2][kAppendThreads / 32];
-  constexpr int kHold = V == 8 ? kAppendHold : 0;
+  constexpr int kHold = kAppendHold<V>;
   ptx::grid_dep_wait();
   const int tid = static_cast<int>(threadIdx.x), threads = static_cast<int>(blockDim.x);
   uint32_t slice;
@@ -185,15 +204,15 @@ __global__ void __launch_bounds__(kAppendThreads) vattn_append_paged_kernel(cons
   long long to[kHold + 1];  // place in the page, from the head's first byte
   int apart[kHold + 1];     // elements from a slot's first half to its second
   bool rot[kHold + 1], on[kHold + 1];
-  const uint32_t ring = ptx::smem_addr(angle_s) + static_cast<uint32_t>(threads * kHold * 64 + tid * 16);
+  const uint32_t ring = ptx::smem_addr(angle_s) + static_cast<uint32_t>(threads * kHold * 8 * V + tid * 2 * V);
   // a head's rows: ring[stage][slot][a, b]
   auto ask = [&](int h) {
     if (h < h1) {
 #pragma unroll
       for (int n = 0; n < kHold; ++n) {
-        const uint32_t at = ring + static_cast<uint32_t>((((h - h0) % kAppendStages * kHold + n) * 2) * threads * 16);
-        ptx::cp_async<16>(at, from[n], on[n]);
-        ptx::cp_async<16>(at + threads * 16, from[n] + apart[n], on[n]);
+        const uint32_t at = ring + static_cast<uint32_t>((((h - h0) % kAppendStages * kHold + n) * 2) * threads * 2 * V);
+        ptx::cp_async<V == 8 ? 16 : 8>(at, from[n], on[n]);
+        ptx::cp_async<V == 8 ? 16 : 8>(at + threads * 2 * V, from[n] + apart[n], on[n]);
         from[n] += x.s[1];
       }
     }
@@ -225,7 +244,7 @@ __global__ void __launch_bounds__(kAppendThreads) vattn_append_paged_kernel(cons
 #pragma unroll
         for (int k = 0; k < V / 4; ++k) {
           angle_s[(k * kHold + n) * threads + tid] = make_float4(cs[4 * k], cs[4 * k + 1], cs[4 * k + 2], cs[4 * k + 3]);
-          angle_s[((k + 2) * kHold + n) * threads + tid] = make_float4(sn[4 * k], sn[4 * k + 1], sn[4 * k + 2], sn[4 * k + 3]);
+          angle_s[((k + V / 4) * kHold + n) * threads + tid] = make_float4(sn[4 * k], sn[4 * k + 1], sn[4 * k + 2], sn[4 * k + 3]);
         }
       }
     }
@@ -240,17 +259,14 @@ __global__ void __launch_bounds__(kAppendThreads) vattn_append_paged_kernel(cons
     if constexpr (kHold > 0) ptx::cp_async_wait<kAppendStages - 1>();
 #pragma unroll
     for (int n = 0; n < kHold; ++n) {
-      const uint32_t at = ring + static_cast<uint32_t>((((h - h0) % kAppendStages * kHold + n) * 2) * threads * 16);
-      Vec<T, V> ra, rb;
-      *reinterpret_cast<float4*>(&ra) = ptx::ld_shared_v4(at);
-      *reinterpret_cast<float4*>(&rb) = ptx::ld_shared_v4(at + threads * 16);
-      ra.widen(a[n]);
-      rb.widen(b[n]);
+      const uint32_t at = ring + static_cast<uint32_t>((((h - h0) % kAppendStages * kHold + n) * 2) * threads * 2 * V);
+      append_shared<T, V>(at).widen(a[n]);
+      append_shared<T, V>(at + threads * 2 * V).widen(b[n]);
       if (rot[n]) {
         float cs[V], sn[V];
 #pragma unroll
         for (int k = 0; k < V / 4; ++k) {
-          const float4 y = angle_s[(k * kHold + n) * threads + tid], z = angle_s[((k + 2) * kHold + n) * threads + tid];
+          const float4 y = angle_s[(k * kHold + n) * threads + tid], z = angle_s[((k + V / 4) * kHold + n) * threads + tid];
           cs[4 * k] = y.x;
           cs[4 * k + 1] = y.y;
           cs[4 * k + 2] = y.z;
@@ -337,6 +353,9 @@ __global__ void __launch_bounds__(kAppendThreads) vattn_append_paged_kernel(cons
             make_uint2(e4m3_pack4(ya[0], ya[1], ya[2], ya[3]), e4m3_pack4(ya[4], ya[5], ya[6], ya[7]));
         *reinterpret_cast<uint2*>(at_b) =
             make_uint2(e4m3_pack4(yb[0], yb[1], yb[2], yb[3]), e4m3_pack4(yb[4], yb[5], yb[6], yb[7]));
+      } else if constexpr (V == 4) {
+        *reinterpret_cast<uint32_t*>(at_a) = e4m3_pack4(ya[0], ya[1], ya[2], ya[3]);
+        *reinterpret_cast<uint32_t*>(at_b) = e4m3_pack4(yb[0], yb[1], yb[2], yb[3]);
       } else {
 #pragma unroll
         for (int e = 0; e < V; ++e) {

@@ -33,14 +33,18 @@
 // Shares of the keys, their joins by a cluster (up to four) or through a workspace,
 // as in cached_kernel.cuh.  Masks are made where a step holds the sequence's end, the
 // first keys' end, the window's edge or new tokens: one lane looks up 16 keys of one
-// row.  Values of keys that no row sees are cleared in registers; a NaN in one that
-// some rows see and others do not sends the step through loops over visible pairs.
+// row.  Values of keys that none of a warp's rows sees are cleared in registers; a NaN
+// in one that some see and others do not sends the step through loops over visible
+// pairs.
 //
 // 32 sequences x 8 key heads x up to 16385 keys of 128, one token of 32 heads, bf16:
-// 107 us, 6.8 TB/s, the measured copy rate.  One sequence of 200003 keys, one key head of 8: 13.6
-// us, 3.8 TB/s: 3 us before the first products, 4 for the join.  Where a call is
-// small a step is latency (1200 cycles alone on its scheduler), and so is the code
-// that runs once: rolled loops for q took 1 us off a call.
+// 107 us, 6.8 TB/s, the measured copy rate.  One sequence of 200003 keys, one key head
+// of 8: 13.6 us, 3.8 TB/s: 3 us before the first products, 4 for the join.  Where a
+// call is small a step is latency (1200 cycles alone on its scheduler), and so is the
+// code that runs once: rolled loops for q took 1 us off a call.  With many rows the
+// bound is the two warps a scheduler has: 22 cycles a product of 16 keys x 8 rows x 16
+// dims whatever else a step does, where the tensor core needs 8 (11 tokens of 4 heads,
+// 13 x 4 x 38131 keys of 128: 151 us, 2.3 TB/s).
 #pragma once
 
 #include "cached_kernel.cuh"
@@ -215,24 +219,30 @@ __device__ __forceinline__ void paged_math(const PagedParams& p, const Pipe& pip
   const int steps = (max(v1 - v0, 0) + (1 << log_boxes) - 1) >> log_boxes;
   ptx::named_barrier_sync(1, P::kThreads);  // barriers and rows are there
 
-  // ---- q as columns: lane / 4 of each eight rows
-  uint32_t qf[CH][NB][2];
+  // ---- q as columns: lane / 4 of each eight rows; held in registers where there is room
+  constexpr bool kHoldQ = NB <= 2;
+  constexpr int CQ = kHoldQ ? CH : 2;
+  uint32_t qf[CQ][NB][2];
+  auto load_q = [&](int ks) {  // of steps ks and ks + 1
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      uint32_t x[4];  // matrices: the two halves of step ks, and of the next
+      const int r = rw * 8 * NB + nb * 8 + (lane & 7);
+      ldmatrix_x4(q_s + static_cast<uint32_t>(r * 2 * DP + (paged_swizzled_q<DP>(r, 2 * ks + (lane >> 3)) << 4)), x);
+      qf[ks % CQ][nb][0] = x[0];
+      qf[ks % CQ][nb][1] = x[1];
+      qf[(ks + 1) % CQ][nb][0] = x[2];
+      qf[(ks + 1) % CQ][nb][1] = x[3];
+    }
+  };
   float row_c[NB][2];  // of rows 2 c4 and 2 c4 + 1: from a product's sum to log2 units, but for the key's scale
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    const int r0 = rw * 8 * NB + nb * 8;
+  for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-    for (int ks = 0; ks < CH; ks += 2) {  // matrices: the two halves of step ks, and of the next
-      uint32_t x[4];
-      const int r = r0 + (lane & 7);
-      ldmatrix_x4(q_s + static_cast<uint32_t>(r * 2 * DP + (paged_swizzled_q<DP>(r, 2 * ks + (lane >> 3)) << 4)), x);
-      qf[ks][nb][0] = x[0];
-      qf[ks][nb][1] = x[1];
-      qf[ks + 1][nb][0] = x[2];
-      qf[ks + 1][nb][1] = x[3];
-    }
+    for (int e = 0; e < 2; ++e) row_c[nb][e] = row_factor[rw * 8 * NB + nb * 8 + 2 * c4 + e];
+  if constexpr (kHoldQ) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) row_c[nb][e] = row_factor[r0 + 2 * c4 + e];
+    for (int ks = 0; ks < CH; ks += 2) load_q(ks);
   }
 
   float m[NB][2], l[NB][2];
@@ -290,15 +300,17 @@ __device__ __forceinline__ void paged_math(const PagedParams& p, const Pipe& pip
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[mb][nb][e] = s_odd[mb][nb][e] = 0.0f;
 #pragma unroll
-    for (int ks = 0; ks < CH; ++ks)
+    for (int ks = 0; ks < CH; ++ks) {
+      if (!kHoldQ && ks % 2 == 0) load_q(ks);
 #pragma unroll
       for (int mb = 0; mb < 2; ++mb) {
         const uint32_t a[4] = {e4m3_half2_lo(kf[ks][2 * mb]), e4m3_half2_lo(kf[ks][2 * mb + 1]),
                                e4m3_half2_hi(kf[ks][2 * mb]), e4m3_half2_hi(kf[ks][2 * mb + 1])};
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
-          mma_16816<__half>(ks % PART ? s_odd[mb][nb] : s[mb][nb], a, qf[ks][nb][0], qf[ks][nb][1]);
+          mma_16816<__half>(ks % PART ? s_odd[mb][nb] : s[mb][nb], a, qf[ks % CQ][nb][0], qf[ks % CQ][nb][1]);
       }
+    }
     if (PART == 2) {
 #pragma unroll
       for (int mb = 0; mb < 2; ++mb)
@@ -312,39 +324,44 @@ __device__ __forceinline__ void paged_math(const PagedParams& p, const Pipe& pip
     for (int n = 0; n < CH; ++n)
       ldmatrix_x4_trans(vs_s + static_cast<uint32_t>(lane * DP + (paged_swizzled<CH>(lane, n) << 4)), vf[n]);
     // ---- masks: at the sequence's end, the first keys' end, the window's edge, among
-    // the new tokens.  Lane i looks up row i % 16 (of the warp) and keys i / 16.
+    // the new tokens.  Lane i looks up rows i % 16 (+ 16) of the warp and keys i / 16.
     bool loops = false;
     uint32_t see[2][NB][2];  // of rows 2 c4 + e: 16 keys a word, where masked
     if (some) {
-      const int mb = lane >> 4, r = lane & (8 * NB - 1), j = mb ? j0[1] : j0[0];
-      const PagedRow y = rows[rw * 8 * NB + r];
-      const uint32_t mine = paged_sees(y, j, sp.base, w.sinks);
+      const int mb = lane >> 4, j = mb ? j0[1] : j0[0];
+      uint32_t mine[(NB + 1) / 2], any = 0, every = 0xffffu;
+#pragma unroll
+      for (int q = 0; q < (NB + 1) / 2; ++q) {
+        const int r = 16 * q + (lane & (NB - 2 * q == 1 ? 7 : 15));
+        const PagedRow y = rows[rw * 8 * NB + r];
+        mine[q] = paged_sees(y, j, sp.base, w.sinks);
+        const bool live = y.old_end != 0 || y.news != 0;
+        any |= live ? mine[q] : 0u;
+        every &= live ? mine[q] : 0xffffu;
+      }
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            see[k][nb][e] = __shfl_sync(0xffffffffu, mine, 16 * k + nb * 8 + 2 * c4 + e) >> g;  // its keys g and g + 8
+            see[k][nb][e] = __shfl_sync(0xffffffffu, mine[nb / 2], 16 * k + nb % 2 * 8 + 2 * c4 + e) >> g;  // its keys g and g + 8
 #pragma unroll
             for (int h = 0; h < 2; ++h)
               if (!((see[k][nb][e] >> (8 * h)) & 1u)) s[k][nb][2 * h + e] = -INFINITY;
           }
-      // V of keys that no query sees may hold anything: zeros
-      const uint32_t alive = bits_upto(sp.len - 1 - j, 0) & (~bits_upto(sp.first - 1 - j, 0) | bits_upto(w.sinks - 1 - j, 0));
+      const uint32_t half = mb ? 0xffff0000u : 0x0000ffffu;
+      const uint32_t any_w = __reduce_or_sync(0xffffffffu, (any << (16 * mb)) & half);
+      const uint32_t every_w = __reduce_and_sync(0xffffffffu, (every << (16 * mb)) | ~half);
+      // V of keys that none of the warp's rows sees may hold anything: zeros
 #pragma unroll
       for (int q = 0; q < 4; ++q) {  // keys 8 q + 2 c4, + 1: low and high halves
-        const uint32_t a = __shfl_sync(0xffffffffu, alive, 8 * q) >> (8 * (q & 1) + 2 * c4);
+        const uint32_t a = any_w >> (8 * q + 2 * c4);
         const uint32_t keep = (a & 1u ? 0xffffu : 0u) | (a & 2u ? 0xffff0000u : 0u);
 #pragma unroll
         for (int n = 0; n < CH; ++n) vf[n][q] &= keep;
       }
       // a NaN in a key that some rows see and others do not: loops over the visible pairs
-      const bool live = y.old_end != 0 || y.news != 0;
-      const uint32_t any = live ? mine : 0u, every = live ? mine : 0xffffu;
-      const uint32_t half = mb ? 0xffff0000u : 0x0000ffffu;
-      const uint32_t any_w = __reduce_or_sync(0xffffffffu, (any << (16 * mb)) & half);
-      const uint32_t every_w = __reduce_and_sync(0xffffffffu, (every << (16 * mb)) | ~half);
       if ((any_w & ~every_w) != 0) {
         uint32_t bad = 0;
 #pragma unroll

@@ -1,6 +1,6 @@
 // serving_api.cu -- the C ABI declared in include/vattn_serving.h: argument
 // checks, variant choice and launches of the calls on packed prompts and the
-// paged cache on sm_103a.
+// paged cache on sm_103a (paged_launch.cuh: attention over that cache).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -12,7 +12,7 @@
 #include "../../include/vattn_serving.h"
 #include "packed_list_kernel.cuh"
 #include "paged_append_kernel.cuh"
-#include "paged_kernel.cuh"
+#include "pages_host.h"
 #include "rope_turns.h"
 #include "window_fwd_kernel.cuh"
 #include "window_host.h"
@@ -21,21 +21,7 @@ namespace {
 
 using namespace vattn::host;
 
-vattn::FastDiv fast_div(int64_t d) { return vattn::FastDiv::make(static_cast<uint32_t>(std::max<int64_t>(1, d))); }
-
 // ------------------------------------------------------------ the cache
-// The two pools of a cache as tensors [n_pages, heads, page_size, head_dim] of bytes.
-struct Pools {
-  vattn_rows k_rows, v_rows;
-  Tensor k, v;
-  Pools(const vattn_pages* c, int64_t heads, int64_t dim)
-      : k_rows{c->k, {c->k_stride[0], c->k_stride[1], c->k_stride[2]}},
-        v_rows{c->v, {c->v_stride[0], c->v_stride[1], c->v_stride[2]}},
-        k{"k pages", &k_rows, {c->n_pages, heads, c->page_size}, dim, 1, true},
-        v{"v pages", &v_rows, {c->n_pages, heads, c->page_size}, dim, 1, true} {}
-  Pools(const Pools&) = delete;
-};
-
 vattn_status check_pages(const vattn_pages* c, const Pools& pools, int64_t batch, int64_t heads) {
   if (c->n_pages < 0 || c->n_pages >= INT32_MAX)
     return fail(VATTN_ERR_INVALID_ARG, "n_pages %lld outside [0, 2^31 - 1)", (long long)c->n_pages);
@@ -63,32 +49,6 @@ vattn_status check_pages(const vattn_pages* c, const Pools& pools, int64_t batch
   if (batch > 0 && c->max_pages > 0 && !c->table) return fail(VATTN_ERR_INVALID_ARG, "null table");
   if ((reinterpret_cast<uintptr_t>(c->kv_len) | reinterpret_cast<uintptr_t>(c->table)) & 3u)
     return fail(VATTN_ERR_MISALIGNED, "kv_len and table must be 4-byte aligned");
-  return VATTN_OK;
-}
-
-// Tensor map {dim, rows of a page, heads, pages} of bytes with boxes of `cols`
-// columns (32, 64 or 128: swizzled as wide) x `box` rows; what is outside reads 0.
-vattn_status make_pages_map(CUtensorMap* tm, const Tensor& x, int cols, int box) {
-  EncodeTiledFn enc = nullptr;
-  const vattn_status st = tensor_map_encoder(&enc);
-  if (st != VATTN_OK) return st;
-  cuuint64_t dims[4] = {static_cast<cuuint64_t>(x.dim), static_cast<cuuint64_t>(x.size[2]),
-                        static_cast<cuuint64_t>(x.size[1]), static_cast<cuuint64_t>(x.size[0])};
-  cuuint64_t strides[3];
-  const int order[3] = {2, 1, 0};
-  for (int i = 0; i < 3; ++i)
-    strides[i] = x.size[order[i]] <= 1 ? static_cast<cuuint64_t>(x.dim)
-                                       : static_cast<cuuint64_t>(x.t->stride[order[i]]);
-  const cuuint32_t boxes[4] = {static_cast<cuuint32_t>(cols), static_cast<cuuint32_t>(box), 1u, 1u};
-  const cuuint32_t steps[4] = {1u, 1u, 1u, 1u};
-  const CUresult r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, x.t->data, dims, strides, boxes, steps,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         cols == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
-                         : cols == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                      : CU_TENSOR_MAP_SWIZZLE_32B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS)
-    return fail(VATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed with CUresult %d", static_cast<int>(r));
   return VATTN_OK;
 }
 
@@ -125,115 +85,6 @@ vattn_status append_launch(const vattn::AppendParams& p, int64_t blocks, int thr
   if (st != VATTN_OK) return st;
   kernel<<<static_cast<unsigned>(blocks), threads, vattn::append_smem<V>(threads), stream>>>(p);
   return launched("cache append kernel launch");
-}
-
-// ------------------------------------------------------------ attention over the cache
-// Blocks of a kernel that a multiprocessor holds, asked once per device.
-template <typename K>
-vattn_status resident_blocks(K kernel, int threads, int smem, std::atomic<int>* known, int device, int* out) {
-  *out = known[device].load(std::memory_order_acquire);
-  if (*out > 0) return VATTN_OK;
-  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(out, kernel, threads, static_cast<size_t>(smem));
-  if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
-  *out = std::max(1, *out);
-  known[device].store(*out, std::memory_order_release);
-  return VATTN_OK;
-}
-
-template <typename T, int DP, int NB, int RW>
-vattn_status paged_launch(vattn::PagedParams p, const Pools& pools, int sms, int device, cudaStream_t stream) {
-  using P = vattn::PagedPlan<DP, NB, RW>;
-  auto kernel = vattn::vattn_paged_kernel<T, DP, NB, RW>;
-  static std::atomic<uint8_t> done[kMaxDevices];
-  static std::atomic<int> known[kMaxDevices];
-  vattn_status st = allow_smem(kernel, P::kSmemBytes, done, device);
-  if (st != VATTN_OK) return st;
-  int resident = 0;
-  if ((st = resident_blocks(kernel, P::kThreads, P::kSmemBytes, known, device, &resident)) != VATTN_OK) return st;
-  p.log_box = P::kLogStep;  // boxes as large as a step, if pages are
-  while (p.page % (1 << p.log_box) != 0) --p.log_box;
-  p.box = 1 << p.log_box;
-  const long long seqs = static_cast<long long>(p.w.batch) * p.w.kv_heads;
-  p.row_blocks = (p.rows + P::kRows - 1) / P::kRows;
-  if (seqs * p.row_blocks > kMaxRows || seqs * p.rows > INT32_MAX)
-    return fail(VATTN_ERR_UNSUPPORTED, "too many query rows");
-  // Shares of the keys: as many blocks as are resident at a time, of 256 keys at
-  // least, or of 128 where that makes no more than 32 shares.  Four, which a cluster
-  // joins, where that leaves a warp five steps at most and enough blocks: as fast as
-  // more shares and their join on the device, and 4 us less host time for a call.
-  const long long most_keys = std::min<long long>(p.w.n_keys, static_cast<long long>(p.w.sinks) + p.w.window + p.w.n_queries);
-  const long long blocks = seqs * p.row_blocks, room = static_cast<long long>(resident) * sms;
-  const long long fill = room / blocks >= 4 ? room / blocks : (room + blocks - 1) / blocks;
-  const long long fine = std::max(std::min(32LL, (most_keys + 127) / 128), (most_keys + 255) / 256);
-  p.splits = static_cast<int>(std::max(1LL, std::min({fill, fine, static_cast<long long>(vattn::kCachedMaxSplits)})));
-  if (p.splits > vattn::kPagedCluster && most_keys <= vattn::kPagedCluster * 5LL * P::kStepKeys && blocks * vattn::kPagedCluster >= sms / 4)
-    p.splits = vattn::kPagedCluster;
-  if (blocks * p.splits > kMaxRows) p.splits = 1;
-  p.d_splits = fast_div(p.splits);
-  p.d_row_blocks = fast_div(p.row_blocks);
-  Workspace ws;
-  const bool clustered = p.splits > 1 && p.splits <= vattn::kPagedCluster;
-  if (p.splits > 1 && !clustered) {
-    const size_t rows = static_cast<size_t>(blocks) * p.splits * P::kRows;
-    if ((st = ws.take(rows * (p.w.dim + 2) * 4, device, stream)) != VATTN_OK) return st;
-    p.part_o = reinterpret_cast<float*>(ws.data());
-    p.part_ml = p.part_o + rows * p.w.dim;
-  }
-  CUtensorMap tk, tv;
-  if (pools.k.empty()) {  // no box is ever loaded: any valid map does
-    vattn_rows any{const_cast<void*>(p.q.p), {0, 0, 0}};
-    const Tensor t{"q", &any, {1, 1, 1}, p.w.dim, 1, false};
-    if ((st = make_pages_map(&tk, t, DP, p.box)) != VATTN_OK) return st;
-    tv = tk;
-  } else if ((st = make_pages_map(&tk, pools.k, DP, p.box)) != VATTN_OK ||
-             (st = make_pages_map(&tv, pools.v, DP, p.box)) != VATTN_OK) {
-    return st;
-  }
-  const dim3 grid(static_cast<unsigned>(blocks * p.splits));
-  if (clustered) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(P::kThreads);
-    cfg.dynamicSmemBytes = P::kSmemBytes;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(p.splits);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tk, tv, p);
-    return e == cudaSuccess ? VATTN_OK : cuda_fail(e, "paged attention kernel launch");
-  }
-  kernel<<<grid, P::kThreads, P::kSmemBytes, stream>>>(tk, tv, p);
-  if ((st = launched("paged attention kernel launch")) != VATTN_OK) return st;
-  if (p.splits == 1) return VATTN_OK;
-  const long long out_rows = seqs * p.rows;
-  const long long join_blocks = out_rows * ((p.w.dim + 31) / 32);
-  if (p.splits <= 32 && join_blocks > 2 * sms)  // a warp a row, else blocks that share a row
-    st = launch_behind("paged attention join kernel launch", vattn::vattn_paged_join_few_kernel<T, P::kRows, P::kKw>,
-                       dim3(static_cast<unsigned>((out_rows + 7) / 8)), dim3(256), 0, stream, p);
-  else
-    st = launch_behind("paged attention join kernel launch", vattn::vattn_paged_join_kernel<T, P::kRows, P::kKw>,
-                       dim3(static_cast<unsigned>(out_rows), static_cast<unsigned>((p.w.dim + 31) / 32)), dim3(256), 0,
-                       stream, p);
-  if (st != VATTN_OK) return st;
-  return ws.release();
-}
-
-template <typename T, int DP>
-vattn_status paged_rows(const vattn::PagedParams& p, const Pools& pools, int sms, int device, cudaStream_t stream) {
-  if (p.rows <= 8) return paged_launch<T, DP, 1, 1>(p, pools, sms, device, stream);
-  if (p.rows <= 16) return paged_launch<T, DP, 2, 1>(p, pools, sms, device, stream);
-  if (p.rows <= 32) return paged_launch<T, DP, 2, 2>(p, pools, sms, device, stream);
-  return paged_launch<T, DP, 2, 4>(p, pools, sms, device, stream);
-}
-
-template <typename T>
-vattn_status paged_dispatch(const vattn::PagedParams& p, const Pools& pools, int sms, int device, cudaStream_t stream) {
-  if (p.w.dim <= 32) return paged_rows<T, 32>(p, pools, sms, device, stream);
-  if (p.w.dim <= 64) return paged_rows<T, 64>(p, pools, sms, device, stream);
-  return paged_rows<T, 128>(p, pools, sms, device, stream);
 }
 
 // ------------------------------------------------------------ packed prompts
@@ -310,13 +161,17 @@ vattn_status vattn_append_paged(const vattn_rows* k, const vattn_rows* v, const 
   p.half = static_cast<int>(a->rope_dims / 2);
   rope_turns(a->base, static_cast<int>(a->rope_dims), p.turns, p.turns_rest);
   for (int i = 0; i < p.half; ++i) p.turn[i] = vattn::qk_turn(p.turns, p.turns_rest, nullptr, i);
-  // 16-byte accesses where the rotated halves and the rest are cut evenly by them
-  bool wide = p.half % 8 == 0 && (p.D - 2 * p.half) % 16 == 0;
-  for (const Tensor* t : {&tk, &tv}) {
-    wide = wide && t->base() % 16 == 0;
-    for (int i = 0; i < 3; ++i) wide = wide && (t->size[i] <= 1 || t->t->stride[i] % 8 == 0);
-  }
-  p.slots = p.D / (wide ? 16 : 2);
+  // 16-byte accesses where the rotated halves and the rest are cut evenly by them, else of 8
+  auto cut_by = [&](int by) {
+    bool yes = p.half % by == 0 && (p.D - 2 * p.half) % (2 * by) == 0;
+    for (const Tensor* t : {&tk, &tv}) {
+      yes = yes && t->base() % (2 * by) == 0;
+      for (int i = 0; i < 3; ++i) yes = yes && (t->size[i] <= 1 || t->t->stride[i] % by == 0);
+    }
+    return yes;
+  };
+  const int cut = cut_by(8) ? 8 : (cut_by(4) ? 4 : 1), hold = cut == 1 ? 2 : 16 / cut;
+  p.slots = p.D / (2 * cut);
   // pages that n rows in a row can touch: one for the first, and for the others as if the next began
   p.items = p.n_tokens <= 1 ? 1 : (p.n_tokens - 2) / p.page + 2;
   const int64_t items = a->cu_seqlens ? a->n_tokens / p.page + 2 * a->batch : a->batch * p.items;
@@ -334,15 +189,16 @@ vattn_status vattn_append_paged(const vattn_rows* k, const vattn_rows* v, const 
   p.d_page = fast_div(p.page);
   p.d_slots = fast_div(p.slots);
   const int slots = std::min(p.page, p.n_tokens) * p.slots;
-  const int threads = std::min(vattn::kAppendThreads,
-                               (slots + 32 * vattn::kAppendHold - 1) / (32 * vattn::kAppendHold) * 32);
+  const int threads = std::min(vattn::kAppendThreads, (slots + 32 * hold - 1) / (32 * hold) * 32);
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   const int64_t grid = items * 2 * p.slices;
-  if (a->dtype == VATTN_F16)
-    return wide ? append_launch<__half, 8>(p, grid, threads, device, stream)
-                : append_launch<__half, 1>(p, grid, threads, device, stream);
-  return wide ? append_launch<__nv_bfloat16, 8>(p, grid, threads, device, stream)
-              : append_launch<__nv_bfloat16, 1>(p, grid, threads, device, stream);
+  auto go = [&](auto zero) {
+    using T = decltype(zero);
+    return cut == 8   ? append_launch<T, 8>(p, grid, threads, device, stream)
+           : cut == 4 ? append_launch<T, 4>(p, grid, threads, device, stream)
+                      : append_launch<T, 1>(p, grid, threads, device, stream);
+  };
+  return a->dtype == VATTN_F16 ? go(__half()) : go(__nv_bfloat16());
 }
 
 vattn_status vattn_forward_paged(const vattn_rows* q, const vattn_pages* cache, const vattn_rows* out,
