@@ -93,12 +93,12 @@ vattn_status vattn_append_paged(const vattn_rows* k, const vattn_rows* v, const 
  * New token t's own key and value are cache row kv_len[b] - T + t, appended
  * before.  Sums and statistics are f32; q and the cache's values enter the
  * products exactly (bf16 q down to 2^-29 of its row's largest), the softmax
- * weights, times the values' scale, as f16.  Scales are positive (powers of
- * two or not), or 0, counted as 2^-64, for zeros; those of one sequence's
- * values lie within 2^100 of each other.  What rows that no
- * query sees hold, bytes or scales, does not reach the result; a NaN reaches
- * the queries that see it.  Scores that are not finite: as in
- * vattn_forward_window.
+ * weights, times the values' scale, as f16.  Scales lie in 2^-100 .. 2^100
+ * (powers of two or not), those of one sequence's values within 2^100 of each
+ * other; a scale of 0 makes the page's rows zeros (of values, counted as
+ * 2^-64).  What rows that no query sees hold, bytes or scales, does not reach
+ * the result; a NaN byte reaches the queries that see it, and no others.
+ * Scores that are not finite: as in vattn_forward_window.
  *
  * q, out [batch, n_q_heads, T, head_dim]; alignment and strides as in
  * vattn_forward_window.

@@ -296,6 +296,26 @@ def test_values_that_are_not_finite(td):
     assert torch.equal(out[same], clean[same])
 
 
+def test_scales_of_pages_that_no_row_sees(td):
+    """A page of new tokens that see nothing and that nothing sees, its bytes and scales NaN."""
+    torch, dev = td
+    for T in (20, 40):
+        case = ("bf16", (1, 4, 1, T, 64), 16, [96], None, 0, False, "heads", "plain")
+        q, cache, _, how = build(td, case, 1570 + T)
+        words = [(1 << t) if t < T - 16 else 0 for t in range(T)]  # the last 16 fill the last page
+        how["tree_mask"] = torch.tensor([words], dtype=torch.int64, device=dev)
+        clean = vef.forward_paged(q, *cache, **how)
+        against_the_oracle(clean, q, cache, None, 0, [words], how["scale"], "bf16")
+        last = cache[4][0, 5].item()
+        for x in cache[:2]:
+            x.view(torch.uint8)[last] = 0x7f
+        for s in cache[2:4]:
+            s[last] = float("nan")
+        out = vef.forward_paged(q, *cache, **how)
+        assert torch.equal(out, clean)
+        assert not f64(out)[0, :, T - 16:].any()
+
+
 @pytest.mark.parametrize("D", [32, 64, 128])
 @pytest.mark.parametrize("H,T", [(4, 6), (4, 12), (4, 15), (4, 31)])
 def test_a_nan_in_wide_blocks(td, H, T, D):

@@ -353,7 +353,11 @@ __device__ __forceinline__ void paged_math(const PagedParams& p, const Pipe& pip
       const uint32_t half = mb ? 0xffff0000u : 0x0000ffffu;
       const uint32_t any_w = __reduce_or_sync(0xffffffffu, (any << (16 * mb)) & half);
       const uint32_t every_w = __reduce_and_sync(0xffffffffu, (every << (16 * mb)) | ~half);
-      // V of keys that none of the warp's rows sees may hold anything: zeros
+      // V of keys that none of the warp's rows sees may hold anything: zeros; and so may
+      // the scales of 16 such keys
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (((any_w >> (16 * k)) & 0xffffu) == 0) meta[k] = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {  // keys 8 q + 2 c4, + 1: low and high halves
         const uint32_t a = any_w >> (8 * q + 2 * c4);
