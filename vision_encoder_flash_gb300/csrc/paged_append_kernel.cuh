@@ -15,8 +15,8 @@
 // memory.  The angles' sines and cosines serve all heads of the block, likewise from
 // shared memory that only their thread uses.
 //
-// 6 prompts of 16384 tokens together, 8 heads x 128 bf16, pages of 64: 27.1 us, 3.7
-// TB/s (56 % of the measured copy rate; 49.3 us with a block for each head and its own
+// 6 prompts of 16384 tokens together, 8 heads x 128 bf16, pages of 64: 25.9 us, 3.9
+// TB/s (58 % of the measured copy rate; 49.3 us with a block for each head and its own
 // angles).  Bound by instructions: 2.1 a cycle, some 15 an element pair, a third of
 // them per head and page (maximum over the block, scale, addresses) and per block
 // (angles, places).  Two slots a thread and 256 threads for a page of 64: with four 35
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kAppendThreads) vattn_append_paged_kernel(cons
     }
     // (h - h0) & 1: the warps that are late still read the last head's
     auto over_block = [&](float m, float* to) {
-      m = warp_max(m);
+      m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));  // (none is negative, or NaN)
       if (threads == 32) return m;
       if ((tid & 31) == 0) to[tid >> 5] = m;
       __syncthreads();
@@ -337,7 +337,8 @@ __global__ void __launch_bounds__(kAppendThreads) vattn_append_paged_kernel(cons
         *to = y;
       }
     }
-    const float by = 1.0f / scale;
+    const uint32_t bits = __float_as_uint(scale);  // (a power of two, but for an old one that the caller made)
+    const float by = (bits & 0x7fffffu) == 0 && bits < 254u << 23 ? __uint_as_float((254u << 23) - bits) : 1.0f / scale;
     auto store = [&](uint8_t* at_a, uint8_t* at_b, float (&ya)[V], float (&yb)[V]) {
       vscale<V>(ya, ya, by);
       vscale<V>(yb, yb, by);
