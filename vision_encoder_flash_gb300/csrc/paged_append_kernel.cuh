@@ -17,11 +17,13 @@
 //
 // 6 prompts of 16384 tokens together, 8 heads x 128 bf16, pages of 64: 25.9 us, 3.9
 // TB/s (58 % of the measured copy rate; 49.3 us with a block for each head and its own
-// angles).  Bound by instructions: 2.1 a cycle, some 15 an element pair, a third of
-// them per head and page (maximum over the block, scale, addresses) and per block
-// (angles, places).  Two slots a thread and 256 threads for a page of 64: with four 35
-// us, with one 37; three blocks a multiprocessor, at 80 registers, 42.  8 heads x 1
-// token: 3.5 us.
+// angles).  Bound by instructions: 2.1 a cycle, some 15 an element pair, half of them
+// per head and page (maximum over the block, scale, addresses) and per block (angles,
+// places).  Two slots a thread and 256 threads for a page of 64: with four 35 us, with
+// one 37; three blocks a multiprocessor, at 80 registers, 42.  Pages of 128 32.7 us
+// (blocks of 512 threads, alone on their multiprocessor), of 256 53 (what the threads
+// do not hold is read and turned twice; parted over a cluster that joins its maxima
+// head by head 60.6).  8 heads x 1 token: 3.5 us.
 //
 // V, elements of a slot's halves: 8, or 4 where the rotated dims or the strides do not
 // divide into 16 bytes (80 dims of which 40 are rotated), or 1, which reads all of
