@@ -77,9 +77,9 @@ vattn_status check_append(const vattn_append_args* a) {
   return VATTN_OK;
 }
 
-template <typename T, int V>
+template <typename T, int V, bool kHeld>
 vattn_status append_launch(const vattn::AppendParams& p, int64_t blocks, int threads, int device, cudaStream_t stream) {
-  auto kernel = vattn::vattn_append_paged_kernel<T, V>;
+  auto kernel = vattn::vattn_append_paged_kernel<T, V, kHeld>;
   static std::atomic<uint8_t> done[kMaxDevices];
   const vattn_status st = allow_smem(kernel, vattn::append_smem<V>(vattn::kAppendThreads), done, device);
   if (st != VATTN_OK) return st;
@@ -175,28 +175,37 @@ vattn_status vattn_append_paged(const vattn_rows* k, const vattn_rows* v, const 
   // pages that n rows in a row can touch: one for the first, and for the others as if the next began
   p.items = p.n_tokens <= 1 ? 1 : (p.n_tokens - 2) / p.page + 2;
   const int64_t items = a->cu_seqlens ? a->n_tokens / p.page + 2 * a->batch : a->batch * p.items;
-  const int64_t blocks = items * p.heads * 2;
-  if (items > kMaxRows || blocks > INT32_MAX) return fail(VATTN_ERR_UNSUPPORTED, "too many pages and heads");
+  const int64_t units = items * p.heads * 2;
+  if (units >= kMaxRows) return fail(VATTN_ERR_UNSUPPORTED, "too many pages and heads");
   int device = 0, sms = 0;
   if ((st = current_device(&device)) != VATTN_OK) return st;
   if ((st = sm_count(device, &sms)) != VATTN_OK) return st;
-  // heads of a block: more share the angles, fewer make more blocks
-  const int64_t per = std::min<int64_t>(p.heads, std::max<int64_t>(1, blocks / (3LL * sms)));
-  p.slices = static_cast<int>((p.heads + per - 1) / per);
-  p.heads_per_slice = (p.heads + p.slices - 1) / p.slices;
-  p.d_slices = fast_div(p.slices);
+  p.units = static_cast<int>(units);
+  p.d_heads = fast_div(p.heads);
   p.d_items = fast_div(p.items);
   p.d_page = fast_div(p.page);
   p.d_slots = fast_div(p.slots);
   const int slots = std::min(p.page, p.n_tokens) * p.slots;
   const int threads = std::min(vattn::kAppendThreads, (slots + 32 * hold - 1) / (32 * hold) * 32);
+  const bool held = threads <= vattn::kAppendHeldThreads && slots <= threads * hold;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-  const int64_t grid = items * 2 * p.slices;
+  // As many blocks as are resident at a time (80 registers a thread where threads hold
+  // all, else 128), each with as many heads of consecutive pages: a block's first rows
+  // wait for three loads in a row, and a second round of blocks for a few was 12 % slower.
+  // (A packed sequence touches one page more than its rows fill, seldom two.)
+  const int64_t touched = a->cu_seqlens ? std::min<int64_t>(items, a->n_tokens / p.page + a->batch) : items;
+  const int64_t room = static_cast<int64_t>(sms) * std::max(1, 65536 / (held ? 80 : 128) / threads);
+  p.per_block = static_cast<int>((touched * p.heads * 2 + room - 1) / room);
+  const int64_t grid = (units + p.per_block - 1) / p.per_block;
   auto go = [&](auto zero) {
     using T = decltype(zero);
-    return cut == 8   ? append_launch<T, 8>(p, grid, threads, device, stream)
-           : cut == 4 ? append_launch<T, 4>(p, grid, threads, device, stream)
-                      : append_launch<T, 1>(p, grid, threads, device, stream);
+    if (cut == 8)
+      return held ? append_launch<T, 8, true>(p, grid, threads, device, stream)
+                  : append_launch<T, 8, false>(p, grid, threads, device, stream);
+    if (cut == 4)
+      return held ? append_launch<T, 4, true>(p, grid, threads, device, stream)
+                  : append_launch<T, 4, false>(p, grid, threads, device, stream);
+    return append_launch<T, 1, false>(p, grid, threads, device, stream);
   };
   return a->dtype == VATTN_F16 ? go(__half()) : go(__nv_bfloat16());
 }
