@@ -180,6 +180,22 @@ def test_values_that_are_not_finite(td):
     assert int(np.isnan(values(s.v)[:, :, :5]).sum()) == 2
 
 
+@pytest.mark.parametrize("rope", [128, 40])
+@pytest.mark.parametrize("page", [48, 128, 256, 1024])
+def test_not_finite_in_larger_pages(td, page, rope):
+    """Rows that a block holds, in 256 or 512 threads, and more of them; several pages a block."""
+    torch, dev = td
+    H, D, n = 5, 128, [2100, 900, 7]
+    most = 2200 // page + 2
+    s = Server(td, H, page, D, tables_for(3, most, 3 * most, 77 + page), 3 * most, "tokens")
+    for part, new in enumerate((n, [1, 30, 70])):
+        k, v = (normal(torch, (1, H, sum(new), D), "bf16", 61 + 2 * part + j, dev, 4.0 ** part) for j in range(2))
+        k[0, 1, 0, 3], k[0, 4, sum(new) - 1, 100] = float("inf"), float("nan")
+        v[0, 0, sum(new) // 2, 127], v[0, 3, 0, 0] = -float("inf"), float("inf")
+        s.append(k, v, new, rope, True)
+        s.check()
+
+
 def test_rows_that_have_no_place(td):
     """Missing pages, rows before 0 and behind the table are dropped; all other bytes stay."""
     torch, dev = td

@@ -20,9 +20,10 @@
 // angles; 25.9 with a block for a page, in two rounds).  Without the rotation 21.1: the
 // bound is latency, of some 300 instructions a head at 5 cycles each, twice a barrier
 // and the block's start, with 24 warps a multiprocessor.  Two slots a thread and 256
-// threads for a page of 64: with four 35 us, with one 37.  Pages of 128 27.2 us (blocks
-// of 512 threads, alone on their multiprocessor), of 256 56 (what the threads do not
-// hold is read and turned twice; parted over a cluster that joins its maxima head by
+// threads for a page of 64: with four 35 us, with one 37.  Pages of 128 26.2 us (blocks
+// of 512 threads, alone on their multiprocessor), of 256 42.2 (what the threads do not
+// hold is read and turned twice, its angles kept as far as twice the held slots; with
+// angles of the held slots only 56, parted over a cluster that joins its maxima head by
 // head 61).  8 heads x 1 token: 3.5 us.
 //
 // V, elements of a slot's halves: 8, or 4 where the rotated dims or the strides do not
@@ -37,8 +38,11 @@
 
 namespace vattn {
 
-constexpr int kAppendThreads = 512;      // most
-constexpr int kAppendHeldThreads = 256;  // most where they hold all
+// A page's new rows: all held by up to 256 threads, of which three blocks are resident,
+// or by up to 512, or more than those can hold.
+enum AppendForm : int { kAppendHeld256 = 0, kAppendHeld = 1, kAppendMore = 2 };
+constexpr int kAppendThreads = 512;  // most
+constexpr int kAppendFewThreads = 256;
 constexpr int kAppendStages = 2;         // heads in its ring
 constexpr int kMinScaleExponent = -32;
 
@@ -110,9 +114,15 @@ __device__ __forceinline__ AppendSeq append_seq(const AppendParams& p, int item)
 template <int V>
 constexpr int kAppendHold = V >= 4 ? 16 / V : 0;
 
-// Shared memory of a block: each held slot's V (cos, sin), and its rows.
-template <int V>
-constexpr int append_smem(int threads) { return threads * kAppendHold<V> * (8 * V + kAppendStages * 4 * V); }
+// Slots of a thread whose angles it keeps, where it cannot hold all of their values too.
+template <int V, int kForm>
+constexpr int kAppendAngles = kForm == kAppendMore ? 2 * kAppendHold<V> : kAppendHold<V>;
+
+// Shared memory of a block: V (cos, sin) of these, and the held slots' rows.
+template <int V, int kForm>
+constexpr int append_smem(int threads) {
+  return threads * (kAppendAngles<V, kForm> * 8 * V + kAppendHold<V> * kAppendStages * 4 * V);
+}
 
 // V elements of 16 bits.
 template <typename T, int V>
@@ -126,14 +136,15 @@ __device__ __forceinline__ Vec<T, V> append_shared(uint32_t addr) {
   }
 }
 
-// kHeld: the threads hold all of a page's new rows.
-template <typename T, int V, bool kHeld>
-__global__ void __launch_bounds__(kHeld ? kAppendHeldThreads : kAppendThreads, kHeld ? 3 : 1)
+template <typename T, int V, int kForm>
+__global__ void __launch_bounds__(kForm == kAppendHeld256 ? kAppendFewThreads : kAppendThreads,
+                                  kForm == kAppendHeld256 ? 3 : 1)
     vattn_append_paged_kernel(const __grid_constant__ AppendParams p) {
-  extern __shared__ float4 angle_s[];  // [V / 2][held slot][thread]: cosines, then sines; then the rings
+  extern __shared__ float4 angle_s[];  // [V / 2][slot][thread]: cosines, then sines; then the rings
   __shared__ uint64_t turn[kQkMaxDim / 2];
   __shared__ __align__(16) float top_s[2][kAppendThreads / 32];
-  constexpr int kHold = kAppendHold<V>;
+  constexpr int kHold = kAppendHold<V>, kAngles = kAppendAngles<V, kForm>;
+  constexpr bool kHeld = kForm != kAppendMore;
   ptx::grid_dep_wait();
   const int tid = static_cast<int>(threadIdx.x), threads = static_cast<int>(blockDim.x);
   if (tid < kAppendThreads / 16) top_s[tid & 1][tid >> 1] = 0.0f;
@@ -197,14 +208,29 @@ __global__ void __launch_bounds__(kHeld ? kAppendHeldThreads : kAppendThreads, k
       vfma<V>(a, minus, sn, x);
       vfma<V>(b, b, cs, y);
     };
-    // the f32 values of a slot that no thread holds
-    auto values = [&](const Slot& t, int h, float (&a)[V], float (&b)[V]) {
+    auto angles = [&](int n, float (&cs)[V], float (&sn)[V]) {  // of the thread's slot n
+#pragma unroll
+      for (int k = 0; k < V / 4; ++k) {
+        const float4 y = angle_s[(k * kAngles + n) * threads + tid], z = angle_s[((k + V / 4) * kAngles + n) * threads + tid];
+        cs[4 * k] = y.x;
+        cs[4 * k + 1] = y.y;
+        cs[4 * k + 2] = y.z;
+        cs[4 * k + 3] = y.w;
+        sn[4 * k] = z.x;
+        sn[4 * k + 1] = z.y;
+        sn[4 * k + 2] = z.z;
+        sn[4 * k + 3] = z.w;
+      }
+    };
+    // the f32 values of a slot that no thread holds, the thread's n-th
+    auto values = [&](const Slot& t, int n, int h, float (&a)[V], float (&b)[V]) {
       const T* from = first_row + t.row * x.s[2] + h * x.s[1];
       qk_load<T, V>(from, t.s.ia, t.s.here).widen(a);
       qk_load<T, V>(from, t.s.ib, t.s.pair).widen(b);
       if (!t.s.rot) return;
       float cs[V], sn[V];
-      qk_angles<V>(t.s, turn, t.c, position(t.row), cs, sn);
+      if (n < kAngles) angles(n, cs, sn);
+      else qk_angles<V>(t.s, turn, t.c, position(t.row), cs, sn);
       rotate(a, b, cs, sn);
     };
     auto largest = [](float m, const float (&a)[V], const float (&b)[V]) {  // (NaN is left out)
@@ -226,7 +252,7 @@ __global__ void __launch_bounds__(kHeld ? kAppendHeldThreads : kAppendThreads, k
     long long to[kHold + 1];  // place in the page, from the head's first byte
     int apart[kHold + 1];     // elements from a slot's first half to its second
     bool rot[kHold + 1], on[kHold + 1];
-    const uint32_t ring = ptx::smem_addr(angle_s) + static_cast<uint32_t>(threads * kHold * 8 * V + tid * 2 * V);
+    const uint32_t ring = ptx::smem_addr(angle_s) + static_cast<uint32_t>(threads * kAngles * 8 * V + tid * 2 * V);
     // a head's rows: ring[stage][slot][a, b]
     auto ask = [&](int h) {
       if (h < h1) {
@@ -255,15 +281,16 @@ __global__ void __launch_bounds__(kHeld ? kAppendHeldThreads : kAppendThreads, k
     if (half > 0) {
       if constexpr (kHold > 0) {
 #pragma unroll 1
-        for (int n = 0; n < kHold; ++n) {
+        for (int n = 0; n < kAngles; ++n) {
+          if (!kHeld && n * threads >= all) break;
           const Slot t = slot(min(tid + n * threads, all - 1));
           if (!t.s.rot) continue;
           float cs[V], sn[V];
           qk_angles<V>(t.s, turn, t.c, position(t.row), cs, sn);
 #pragma unroll
           for (int k = 0; k < V / 4; ++k) {
-            angle_s[(k * kHold + n) * threads + tid] = make_float4(cs[4 * k], cs[4 * k + 1], cs[4 * k + 2], cs[4 * k + 3]);
-            angle_s[((k + V / 4) * kHold + n) * threads + tid] = make_float4(sn[4 * k], sn[4 * k + 1], sn[4 * k + 2], sn[4 * k + 3]);
+            angle_s[(k * kAngles + n) * threads + tid] = make_float4(cs[4 * k], cs[4 * k + 1], cs[4 * k + 2], cs[4 * k + 3]);
+            angle_s[((k + V / 4) * kAngles + n) * threads + tid] = make_float4(sn[4 * k], sn[4 * k + 1], sn[4 * k + 2], sn[4 * k + 3]);
           }
         }
       }
@@ -283,18 +310,7 @@ __global__ void __launch_bounds__(kHeld ? kAppendHeldThreads : kAppendThreads, k
         append_shared<T, V>(at + threads * 2 * V).widen(b[n]);
         if (rot[n]) {
           float cs[V], sn[V];
-#pragma unroll
-          for (int k = 0; k < V / 4; ++k) {
-            const float4 y = angle_s[(k * kHold + n) * threads + tid], z = angle_s[((k + V / 4) * kHold + n) * threads + tid];
-            cs[4 * k] = y.x;
-            cs[4 * k + 1] = y.y;
-            cs[4 * k + 2] = y.z;
-            cs[4 * k + 3] = y.w;
-            sn[4 * k] = z.x;
-            sn[4 * k + 1] = z.y;
-            sn[4 * k + 2] = z.z;
-            sn[4 * k + 3] = z.w;
-          }
+          angles(n, cs, sn);
           rotate(a[n], b[n], cs, sn);
         }
         top = largest(top, a[n], b[n]);  // (zeros where there is no slot)
@@ -302,9 +318,9 @@ __global__ void __launch_bounds__(kHeld ? kAppendHeldThreads : kAppendThreads, k
       if constexpr (kHold > 0) ask(h + kAppendStages);
       if constexpr (!kHeld) {
 #pragma unroll 1
-        for (int at = tid + kHold * threads; at < all; at += threads) {
+        for (int at = tid + kHold * threads, n = kHold; at < all; at += threads, ++n) {
           float ya[V], yb[V];
-          values(slot(at), h, ya, yb);
+          values(slot(at), n, h, ya, yb);
           top = largest(top, ya, yb);
         }
       }
@@ -331,9 +347,9 @@ __global__ void __launch_bounds__(kHeld ? kAppendHeldThreads : kAppendThreads, k
 #pragma unroll
         for (int n = 0; n < kHold; ++n) m = largest_finite(m, a[n], b[n]);
         if constexpr (!kHeld) {
-          for (int at = tid + kHold * threads; at < all; at += threads) {
+          for (int at = tid + kHold * threads, n = kHold; at < all; at += threads, ++n) {
             float ya[V], yb[V];
-            values(slot(at), h, ya, yb);
+            values(slot(at), n, h, ya, yb);
             m = largest_finite(m, ya, yb);
           }
         }
@@ -398,10 +414,10 @@ __global__ void __launch_bounds__(kHeld ? kAppendHeldThreads : kAppendThreads, k
         if (on[n]) store(page + to[n], page + to[n] + apart[n], a[n], b[n]);
       if constexpr (!kHeld) {
 #pragma unroll 1
-        for (int at = tid + kHold * threads; at < all; at += threads) {
+        for (int at = tid + kHold * threads, n = kHold; at < all; at += threads, ++n) {
           float ya[V], yb[V];
           const Slot t = slot(at);
-          values(t, h, ya, yb);
+          values(t, n, h, ya, yb);
           uint8_t* const to = page + (t.row - row0) * row_stride;
           store(to + t.s.ia, to + t.s.ib, ya, yb);
         }

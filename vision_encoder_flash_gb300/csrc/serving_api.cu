@@ -8,6 +8,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/vattn_serving.h"
 #include "packed_list_kernel.cuh"
@@ -77,13 +78,13 @@ vattn_status check_append(const vattn_append_args* a) {
   return VATTN_OK;
 }
 
-template <typename T, int V, bool kHeld>
+template <typename T, int V, int kForm>
 vattn_status append_launch(const vattn::AppendParams& p, int64_t blocks, int threads, int device, cudaStream_t stream) {
-  auto kernel = vattn::vattn_append_paged_kernel<T, V, kHeld>;
+  auto kernel = vattn::vattn_append_paged_kernel<T, V, kForm>;
   static std::atomic<uint8_t> done[kMaxDevices];
-  const vattn_status st = allow_smem(kernel, vattn::append_smem<V>(vattn::kAppendThreads), done, device);
+  const vattn_status st = allow_smem(kernel, vattn::append_smem<V, kForm>(vattn::kAppendThreads), done, device);
   if (st != VATTN_OK) return st;
-  kernel<<<static_cast<unsigned>(blocks), threads, vattn::append_smem<V>(threads), stream>>>(p);
+  kernel<<<static_cast<unsigned>(blocks), threads, vattn::append_smem<V, kForm>(threads), stream>>>(p);
   return launched("cache append kernel launch");
 }
 
@@ -187,25 +188,27 @@ vattn_status vattn_append_paged(const vattn_rows* k, const vattn_rows* v, const 
   p.d_slots = fast_div(p.slots);
   const int slots = std::min(p.page, p.n_tokens) * p.slots;
   const int threads = std::min(vattn::kAppendThreads, (slots + 32 * hold - 1) / (32 * hold) * 32);
-  const bool held = threads <= vattn::kAppendHeldThreads && slots <= threads * hold;
+  const bool held = slots <= threads * hold, few = held && threads <= vattn::kAppendFewThreads;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-  // As many blocks as are resident at a time (80 registers a thread where threads hold
-  // all, else 128), each with as many heads of consecutive pages: a block's first rows
+  // As many blocks as are resident at a time (80 registers a thread in the form
+  // for three of them, else 128), each with as many heads of consecutive pages: a block's first rows
   // wait for three loads in a row, and a second round of blocks for a few was 12 % slower.
   // (A packed sequence touches one page more than its rows fill, seldom two.)
   const int64_t touched = a->cu_seqlens ? std::min<int64_t>(items, a->n_tokens / p.page + a->batch) : items;
-  const int64_t room = static_cast<int64_t>(sms) * std::max(1, 65536 / (held ? 80 : 128) / threads);
+  const int64_t room = static_cast<int64_t>(sms) * std::max(1, 65536 / (few && cut > 1 ? 80 : 128) / threads);
   p.per_block = static_cast<int>((touched * p.heads * 2 + room - 1) / room);
   const int64_t grid = (units + p.per_block - 1) / p.per_block;
   auto go = [&](auto zero) {
     using T = decltype(zero);
-    if (cut == 8)
-      return held ? append_launch<T, 8, true>(p, grid, threads, device, stream)
-                  : append_launch<T, 8, false>(p, grid, threads, device, stream);
-    if (cut == 4)
-      return held ? append_launch<T, 4, true>(p, grid, threads, device, stream)
-                  : append_launch<T, 4, false>(p, grid, threads, device, stream);
-    return append_launch<T, 1, false>(p, grid, threads, device, stream);
+    auto form = [&](auto width) {
+      constexpr int V = decltype(width)::value;
+      return few     ? append_launch<T, V, vattn::kAppendHeld256>(p, grid, threads, device, stream)
+             : held ? append_launch<T, V, vattn::kAppendHeld>(p, grid, threads, device, stream)
+                    : append_launch<T, V, vattn::kAppendMore>(p, grid, threads, device, stream);
+    };
+    if (cut == 8) return form(std::integral_constant<int, 8>());
+    if (cut == 4) return form(std::integral_constant<int, 4>());
+    return append_launch<T, 1, vattn::kAppendMore>(p, grid, threads, device, stream);
   };
   return a->dtype == VATTN_F16 ? go(__half()) : go(__nv_bfloat16());
 }
