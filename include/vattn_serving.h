@@ -115,11 +115,12 @@ vattn_status vattn_forward_paged(const vattn_rows* q, const vattn_pages* cache,
  *
  * cu_seqlens: [n_seqs + 1] on the device, ascending; its values are held to
  * [0, n_queries], and a sequence that ends before it begins is empty; if the
- * sequences then have more than n_queries rows together, none is computed.  q, out [1, n_q_heads, n_queries, head_dim], k and v [1,
- * n_kv_heads, n_queries, head_dim]: args->batch is 1, n_keys = n_queries,
- * kv_len, q_start and tree NULL; n_seqs < 2^24.  Rows in no sequence are left
- * as they are, in out and in lse (NULL, or f32 [n_q_heads, n_queries]).  All
- * else as in vattn_forward_window.
+ * sequences then have more than n_queries rows together, none is computed.
+ * q, out [1, n_q_heads, n_queries, head_dim], k and v [1, n_kv_heads,
+ * n_queries, head_dim]: args->batch is 1, n_keys = n_queries, kv_len, q_start
+ * and tree NULL; n_seqs < 2^24.  Rows in no sequence are left as they are, in
+ * out and in lse (NULL, or f32 [n_q_heads, n_queries]).  All else as in
+ * vattn_forward_window.
  */
 vattn_status vattn_forward_packed(const vattn_rows* q, const vattn_rows* k, const vattn_rows* v,
                                   const vattn_rows* out, float* lse, const int32_t* cu_seqlens,
