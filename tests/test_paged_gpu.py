@@ -181,6 +181,35 @@ def test_pages_that_are_not_there(td):
     assert not f64(vef.forward_paged(q, *cache[:4], cache[4][:, :0].contiguous(), cache[5], **how)).any()
 
 
+@pytest.mark.parametrize("D", [48, 80, 112])
+@pytest.mark.parametrize("H,T", [(1, 1), (4, 3), (4, 6), (4, 8), (4, 11), (4, 16), (8, 40)])
+def test_rows_behind_each_other_and_apart(td, H, T, D):
+    """Rows of an odd number of 16 bytes, contiguous in their page or not: the same bits, with
+    pages that are not there, and a NaN among the new tokens."""
+    torch, dev = td
+    for page, window, N in ((16, None, 700), (48, 90, 260), (256, None, 2900)):
+        case = ("bf16", (2, 2 * H, 2, T, D), page, [N, N - 77], window, 3, T > 2, "heads", "plain")
+        q, cache, words, how = build(td, case, 1360 + D + T)
+        gone = [x.clone() for x in cache]
+        gone[4][0, 0], gone[4][1, 1] = -1, 2 ** 31 - 1
+        row = N - 77 - 1  # the newest token of sequence 1
+        bad = [cache[0], cache[1].view(torch.uint8).clone().view(cache[1].dtype)] + list(cache[2:])
+        bad[1].view(torch.uint8)[cache[4][1, row // page].item(), 1, row % page, D - 1] = 0xff
+        for which in (cache, gone, bad):
+            apart = [x.transpose(1, 2).contiguous().transpose(1, 2) for x in which[:2]] + list(which[2:])
+            assert which[0].stride(2) == D and apart[0].stride(2) == 2 * D
+            out = vef.forward_paged(q, *which, **how)
+            other = vef.forward_paged(q, *apart, **how)
+            assert torch.equal(torch.isnan(out), torch.isnan(other))
+            assert torch.equal(out.nan_to_num(nan=3.0), other.nan_to_num(nan=3.0))
+            if which is bad:
+                assert bool(torch.isnan(out[1, H:, T - 1, D - 1]).all())
+                assert int(torch.isnan(out).sum()) == H
+            else:
+                against_the_oracle(out, q, which, window, 3, words, how["scale"], "bf16")
+    assert vef.device_status() == 0
+
+
 def test_pages_shared_by_sequences(td):
     torch, dev = td
     case = ("f16", (2, 4, 1, 1, 64), 16, [64, 64], None, 0, False, "heads", "plain")

@@ -59,6 +59,8 @@ constexpr int kPagedCluster = 4;  // shares that a cluster of blocks joins by it
 struct PagedParams {
   WindowParams w;  // n_keys: rows that the table has room for; kv_len: the cache's
   RowsTensor q, out;
+  const uint8_t* pool[2];  // k, v (kDim), and from page to page, head to head
+  long long ps[2][2];
   const float* k_scale;
   const float* v_scale;
   const int32_t* table;
@@ -161,12 +163,13 @@ __device__ __forceinline__ uint32_t paged_sees(const PagedRow& y, int j, int bas
 }
 
 // The math warps: all of the share's keys, then their results, joined.
-template <typename T, int DP, int NB, int RW>
+template <typename T, int DP, int NB, int RW, int kDim>
 __device__ __forceinline__ void paged_math(const PagedParams& p, const Pipe& pipe, uint8_t* smem, uint32_t smem_s,
                                            const PagedRow* rows, const PagedSpan& sp, uint32_t bk, int b,
                                            int kh, int rb, int split) {
   using P = PagedPlan<DP, NB, RW>;
-  constexpr int CH = DP / 16;  // 16-byte chunks of a shared row, 16-element steps of a product
+  constexpr bool kTight = kDim != 0;
+  constexpr int CH = (kTight ? kDim : DP) / 16;  // 16-byte chunks of a row, 16-element steps of a product
   constexpr int RS = P::kResultStride, S = P::kStages;
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   const int rw = warp % RW, kw = warp / RW;
@@ -175,6 +178,11 @@ __device__ __forceinline__ void paged_math(const PagedParams& p, const Pipe& pip
   auto empty = [bar0](int st) -> uint32_t { return bar0 + 8u * (S + st); };
   const WindowParams& w = p.w;
   const int D = w.dim, log_boxes = P::kLogStep - p.log_box;
+  // a shared row of K or V: DP bytes, swizzled, or just those that there are
+  constexpr int pitch = kTight ? kDim : DP;
+  auto tile_at = [](int r, int c) {
+    return static_cast<uint32_t>(kTight ? r * kDim + c * 16 : r * DP + (paged_swizzled<DP / 16>(r, c) << 4));
+  };
   const bool clustered = p.splits > 1 && p.splits <= kPagedCluster;
   float* const res = reinterpret_cast<float*>(smem);  // results, over the ring: [group of keys][kRows][RS]
   const int g = lane >> 2, c4 = lane & 3;
@@ -221,7 +229,7 @@ __device__ __forceinline__ void paged_math(const PagedParams& p, const Pipe& pip
 
   // ---- q as columns: lane / 4 of each eight rows; held in registers where there is room
   constexpr bool kHoldQ = NB <= 2;
-  constexpr int CQ = kHoldQ ? CH : 2;
+  constexpr int CQ = kHoldQ ? (CH + 1) / 2 * 2 : 2;
   uint32_t qf[CQ][NB][2];
   auto load_q = [&](int ks) {  // of steps ks and ks + 1
 #pragma unroll
@@ -267,12 +275,12 @@ __device__ __forceinline__ void paged_math(const PagedParams& p, const Pipe& pip
   uint32_t turn = 0;
   for (; step < steps; ++step) {
     if (!pipe.wait_warp(full(st), turn, kSitePagedMath)) break;
-    const uint32_t ks_s = smem_s + static_cast<uint32_t>(st * P::kStageBytes + kw * kPagedKeys * DP);
+    const uint32_t ks_s = smem_s + static_cast<uint32_t>(st * P::kStageBytes + kw * kPagedKeys * pitch);
     const uint32_t vs_s = ks_s + P::kTileBytes;
     uint32_t kf[CH][4];
 #pragma unroll
     for (int ks = 0; ks < CH; ++ks)  // matrices: keys 0-7, 8-15, 16-23, 24-31 by the 16 dims of chunk ks
-      ldmatrix_x4(ks_s + static_cast<uint32_t>(lane * DP + (paged_swizzled<CH>(lane, ks) << 4)), kf[ks]);
+      ldmatrix_x4(ks_s + tile_at(lane, ks), kf[ks]);
     // the warp's keys by 16: first of each in the sequence, scales; those that are
     // not there, or that no row sees, count as masked throughout
     int j0[2];
@@ -321,8 +329,7 @@ __device__ __forceinline__ void paged_math(const PagedParams& p, const Pipe& pip
     }
     uint32_t vf[CH][4];  // the same matrices of V, transposed by pairs of dims, ahead of their use
 #pragma unroll
-    for (int n = 0; n < CH; ++n)
-      ldmatrix_x4_trans(vs_s + static_cast<uint32_t>(lane * DP + (paged_swizzled<CH>(lane, n) << 4)), vf[n]);
+    for (int n = 0; n < CH; ++n) ldmatrix_x4_trans(vs_s + tile_at(lane, n), vf[n]);
     // ---- masks: at the sequence's end, the first keys' end, the window's edge, among
     // the new tokens.  Lane i looks up rows i % 16 (+ 16) of the warp and keys i / 16.
     bool loops = false;
@@ -466,8 +473,7 @@ __device__ __forceinline__ void paged_math(const PagedParams& p, const Pipe& pip
           const int r = 8 * h + y;
 #pragma unroll
           for (int n = 0; n < CH; ++n) {
-            const uint32_t z = *reinterpret_cast<const uint16_t*>(smem + (vs_s - smem_s) + r * DP +
-                                                                  (paged_swizzled<CH>(r, n) << 4) + g * 2);
+            const uint32_t z = *reinterpret_cast<const uint16_t*>(smem + (vs_s - smem_s) + tile_at(r, n) + g * 2);
             const uint32_t z2 = e4m3_half2_lo(z);
             const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&z2));
 #pragma unroll
@@ -596,11 +602,19 @@ __device__ __forceinline__ void paged_math(const PagedParams& p, const Pipe& pip
   ptx::grid_dep_launch();
 }
 
-template <typename T, int DP, int NB, int RW>
+// kDim: 0, or 48, 80 or 112 dims whose rows are one behind the other in a page: boxes as
+// untiled copies, and shared rows as they are.  As tiles of 64 or 128 columns such rows
+// begin and end inside the sectors that a copy reads: 32 x 8 key heads x up to 16000 keys
+// x 80 took 127 us and now 78, of 112 101 and 98, of 48 75 and 65 (96 and 64 dims take 89
+// and 63), and the products skip the chunks that are not there (200003 keys of one head x
+// 80 17.5 and 12.5).  An odd number of 16-byte chunks a row leaves ldmatrix without a
+// conflict, unswizzled.
+template <typename T, int DP, int NB, int RW, int kDim>
 __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads, 2)
     vattn_paged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const __grid_constant__ PagedParams p) {
   using P = PagedPlan<DP, NB, RW>;
+  constexpr bool kTight = kDim != 0;
   constexpr int S = P::kStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int kpos[VATTN_MAX_NEW_TOKENS];
@@ -628,8 +642,10 @@ __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads, 2)
     }
     pipe.init(w, p.status);
     ptx::fence_mbar_init();
-    ptx::prefetch_tensormap(&tm_k);
-    ptx::prefetch_tensormap(&tm_v);
+    if (!kTight) {
+      ptx::prefetch_tensormap(&tm_k);
+      ptx::prefetch_tensormap(&tm_v);
+    }
   }
   ptx::grid_dep_wait();
   const PagedSpan sp = PagedSpan::make(w, p.log_box, P::kKw, b, p.d_splits);
@@ -670,12 +686,19 @@ __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads, 2)
     Box now{}, next{};
     const uint64_t once = ptx::policy_evict_first();
     const CUtensorMap* const tm = (loader & 1) != 0 ? &tm_v : &tm_k;
+    const int box_bytes = (kTight ? kDim : DP) << p.log_box;
     // The copies of a step, whose boxes are with lanes l0, l0 + 1, ..., to place st.
     auto copies = [&](int st, int l0) {
       for (int i = loader >> 1; i < boxes; i += 2) {
         const int pg = __shfl_sync(0xffffffffu, now.page, l0 + i), row = __shfl_sync(0xffffffffu, now.row, l0 + i);
-        const uint32_t to = smem_s + static_cast<uint32_t>(st * P::kStageBytes + (loader & 1) * P::kTileBytes + i * (DP << p.log_box));
-        if (ptx::elect_one()) ptx::tma_load_4d_hint(to, tm, full(st), 0, row, kh, pg, once);
+        const uint32_t to = smem_s + static_cast<uint32_t>(st * P::kStageBytes + (loader & 1) * P::kTileBytes + i * box_bytes);
+        if constexpr (kTight) {  // (a page that is not there leaves the place as it was: its keys are masked)
+          const uint8_t* from = p.pool[loader & 1] + pg * p.ps[loader & 1][0] + kh * p.ps[loader & 1][1] + row * kDim;
+          if (pg < p.n_pages && ptx::elect_one())
+            ptx::bulk_load_hint(to, from, static_cast<uint32_t>(box_bytes), full(st), once);
+        } else if (ptx::elect_one()) {
+          ptx::tma_load_4d_hint(to, tm, full(st), 0, row, kh, pg, once);
+        }
       }
     };
     // What the products need beside them, and the barrier's count, which the copies may be ahead of.
@@ -684,9 +707,13 @@ __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads, 2)
       if (loader == 0 && which >= 0 && which < boxes)
         ptx::st_shared_v4(smem_s + P::kOffMeta + static_cast<uint32_t>((st * 8 + which) * 16), now.k, now.log2_v, now.inv_v,
                           __int_as_float(now.key0));
+      int copied = (mine + 1) >> 1;
+      if constexpr (kTight) {
+        const uint32_t here = __ballot_sync(0xffffffffu, now.page < p.n_pages) >> l0;
+        copied = __popc(here & ((1u << boxes) - 1u) & (loader >> 1 != 0 ? 0xaaaaaaaau : 0x55555555u));
+      }
       __syncwarp();
-      if (mine > 0 && ptx::elect_one())
-        ptx::mbar_arrive_expect_tx(full(st), static_cast<uint32_t>(((mine + 1) >> 1) * (DP << p.log_box)));
+      if (mine > 0 && ptx::elect_one()) ptx::mbar_arrive_expect_tx(full(st), static_cast<uint32_t>(copied * box_bytes));
     };
     place(lane, now);
     ptx::named_barrier_sync(3, P::kThreads - 32 * kPagedWarps);  // the barriers
@@ -746,7 +773,7 @@ __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads, 2)
     __syncwarp();
   } else {
     ptx::regs_increase<P::kRegsMath>();
-    paged_math<T, DP, NB, RW>(p, pipe, smem, smem_s, rows, sp, bk, b, kh, rb, split);
+    paged_math<T, DP, NB, RW, kDim>(p, pipe, smem, smem_s, rows, sp, bk, b, kh, rb, split);
   }
 }
 

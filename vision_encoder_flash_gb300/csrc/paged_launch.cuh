@@ -21,10 +21,10 @@ vattn_status resident_blocks(K kernel, int threads, int smem, std::atomic<int>* 
   return VATTN_OK;
 }
 
-template <typename T, int DP, int NB, int RW>
+template <typename T, int DP, int NB, int RW, int kDim>
 vattn_status paged_launch(PagedParams p, const Pools& pools, int sms, int device, cudaStream_t stream) {
   using P = PagedPlan<DP, NB, RW>;
-  auto kernel = vattn_paged_kernel<T, DP, NB, RW>;
+  auto kernel = vattn_paged_kernel<T, DP, NB, RW, kDim>;
   static std::atomic<uint8_t> done[kMaxDevices];
   static std::atomic<int> known[kMaxDevices];
   vattn_status st = allow_smem(kernel, P::kSmemBytes, done, device);
@@ -60,8 +60,15 @@ vattn_status paged_launch(PagedParams p, const Pools& pools, int sms, int device
     p.part_o = reinterpret_cast<float*>(ws.data());
     p.part_ml = p.part_o + rows * p.w.dim;
   }
-  CUtensorMap tk, tv;
-  if (pools.k.empty()) {  // no box is ever loaded: any valid map does
+  CUtensorMap tk{}, tv{};
+  if (kDim != 0) {
+    for (int i = 0; i < 2; ++i) {
+      const vattn_rows* t = i == 0 ? pools.k.t : pools.v.t;
+      p.pool[i] = static_cast<const uint8_t*>(t->data);
+      p.ps[i][0] = t->stride[0];
+      p.ps[i][1] = t->stride[1];
+    }
+  } else if (pools.k.empty()) {  // no box is ever loaded: any valid map does
     vattn_rows any{const_cast<void*>(p.q.p), {0, 0, 0}};
     const Tensor t{"q", &any, {1, 1, 1}, p.w.dim, 1, false};
     if ((st = make_pages_map(&tk, t, DP, p.box)) != VATTN_OK) return st;
@@ -111,27 +118,33 @@ vattn_status paged_launch(PagedParams p, const Pools& pools, int sms, int device
 // of one of four groups of 16 (head_dim 128: 128 rows 73.4 and 78.7 us, 64 rows 93.6 and
 // 67.2), and 0.75 of one of two groups of 32, for which smaller rows have room (head_dim
 // 64, 64 x 8000 keys, 64 rows: 41.1 us, in four of 16 46.4, in two blocks of 48 61.4).
-template <typename T, int DP>
+template <typename T, int DP, int kDim>
 vattn_status paged_rows(const PagedParams& p, const Pools& pools, int sms, int device, cudaStream_t stream) {
-  if (p.rows <= 8) return paged_launch<T, DP, 1, 1>(p, pools, sms, device, stream);
-  if (p.rows <= 16) return paged_launch<T, DP, 2, 1>(p, pools, sms, device, stream);
-  if (p.rows <= 24) return paged_launch<T, DP, 3, 1>(p, pools, sms, device, stream);
-  if (p.rows <= 32) return paged_launch<T, DP, 2, 2>(p, pools, sms, device, stream);
+  if (p.rows <= 8) return paged_launch<T, DP, 1, 1, kDim>(p, pools, sms, device, stream);
+  if (p.rows <= 16) return paged_launch<T, DP, 2, 1, kDim>(p, pools, sms, device, stream);
+  if (p.rows <= 24) return paged_launch<T, DP, 3, 1, kDim>(p, pools, sms, device, stream);
+  if (p.rows <= 32) return paged_launch<T, DP, 2, 2, kDim>(p, pools, sms, device, stream);
   const int by48 = (p.rows + 47) / 48, by64 = (p.rows + 63) / 64;
   if constexpr (DP <= 64) {
-    if (3 * by48 < 4 * by64) return paged_launch<T, DP, 3, 2>(p, pools, sms, device, stream);
-    return paged_launch<T, DP, 4, 2>(p, pools, sms, device, stream);
+    if (3 * by48 < 4 * by64) return paged_launch<T, DP, 3, 2, kDim>(p, pools, sms, device, stream);
+    return paged_launch<T, DP, 4, 2, kDim>(p, pools, sms, device, stream);
   } else {
-    if (2 * by48 <= 3 * by64) return paged_launch<T, DP, 3, 2>(p, pools, sms, device, stream);
-    return paged_launch<T, DP, 2, 4>(p, pools, sms, device, stream);
+    if (2 * by48 <= 3 * by64) return paged_launch<T, DP, 3, 2, kDim>(p, pools, sms, device, stream);
+    return paged_launch<T, DP, 2, 4, kDim>(p, pools, sms, device, stream);
   }
 }
 
 template <typename T>
 vattn_status paged_dispatch(const PagedParams& p, const Pools& pools, int sms, int device, cudaStream_t stream) {
-  if (p.w.dim <= 32) return paged_rows<T, 32>(p, pools, sms, device, stream);
-  if (p.w.dim <= 64) return paged_rows<T, 64>(p, pools, sms, device, stream);
-  return paged_rows<T, 128>(p, pools, sms, device, stream);
+  // rows of an odd number of 16 bytes that follow each other in their page: by untiled
+  // copies (both sides' times are at vattn_paged_kernel)
+  const bool tight = pools.k.t->stride[2] == p.w.dim && pools.v.t->stride[2] == p.w.dim;
+  if (p.w.dim <= 32) return paged_rows<T, 32, 0>(p, pools, sms, device, stream);
+  if (p.w.dim == 48 && tight) return paged_rows<T, 64, 48>(p, pools, sms, device, stream);
+  if (p.w.dim <= 64) return paged_rows<T, 64, 0>(p, pools, sms, device, stream);
+  if (p.w.dim == 80 && tight) return paged_rows<T, 128, 80>(p, pools, sms, device, stream);
+  if (p.w.dim == 112 && tight) return paged_rows<T, 128, 112>(p, pools, sms, device, stream);
+  return paged_rows<T, 128, 0>(p, pools, sms, device, stream);
 }
 
 }  // namespace host
