@@ -162,14 +162,17 @@ __device__ __forceinline__ uint32_t paged_sees(const PagedRow& y, int j, int bas
   return (old | static_cast<uint32_t>(at)) & 0xffffu;
 }
 
+// Are rows of kDim bytes copied untiled (see the kernel)?
+__host__ __device__ constexpr bool paged_tight(int kDim) { return kDim % 32 == 16; }
+
 // The math warps: all of the share's keys, then their results, joined.
 template <typename T, int DP, int NB, int RW, int kDim>
 __device__ __forceinline__ void paged_math(const PagedParams& p, const Pipe& pipe, uint8_t* smem, uint32_t smem_s,
                                            const PagedRow* rows, const PagedSpan& sp, uint32_t bk, int b,
                                            int kh, int rb, int split) {
   using P = PagedPlan<DP, NB, RW>;
-  constexpr bool kTight = kDim != 0;
-  constexpr int CH = (kTight ? kDim : DP) / 16;  // 16-byte chunks of a row, 16-element steps of a product
+  constexpr bool kTight = paged_tight(kDim);
+  constexpr int CH = (kDim != 0 ? kDim : DP) / 16;  // 16-byte chunks of a row, 16-element steps of a product
   constexpr int RS = P::kResultStride, S = P::kStages;
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   const int rw = warp % RW, kw = warp / RW;
@@ -608,13 +611,13 @@ __device__ __forceinline__ void paged_math(const PagedParams& p, const Pipe& pip
 // x 80 took 127 us and now 78, of 112 101 and 98, of 48 75 and 65 (96 and 64 dims take 89
 // and 63), and the products skip the chunks that are not there (200003 keys of one head x
 // 80 17.5 and 12.5).  An odd number of 16-byte chunks a row leaves ldmatrix without a
-// conflict, unswizzled.
+// conflict, unswizzled.  96: tiles, with the products of the chunks that are there.
 template <typename T, int DP, int NB, int RW, int kDim>
 __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads, 2)
     vattn_paged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const __grid_constant__ PagedParams p) {
   using P = PagedPlan<DP, NB, RW>;
-  constexpr bool kTight = kDim != 0;
+  constexpr bool kTight = paged_tight(kDim);
   constexpr int S = P::kStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int kpos[VATTN_MAX_NEW_TOKENS];

@@ -61,7 +61,7 @@ vattn_status paged_launch(PagedParams p, const Pools& pools, int sms, int device
     p.part_ml = p.part_o + rows * p.w.dim;
   }
   CUtensorMap tk{}, tv{};
-  if (kDim != 0) {
+  if (paged_tight(kDim)) {
     for (int i = 0; i < 2; ++i) {
       const vattn_rows* t = i == 0 ? pools.k.t : pools.v.t;
       p.pool[i] = static_cast<const uint8_t*>(t->data);
@@ -143,6 +143,7 @@ vattn_status paged_dispatch(const PagedParams& p, const Pools& pools, int sms, i
   if (p.w.dim == 48 && tight) return paged_rows<T, 64, 48>(p, pools, sms, device, stream);
   if (p.w.dim <= 64) return paged_rows<T, 64, 0>(p, pools, sms, device, stream);
   if (p.w.dim == 80 && tight) return paged_rows<T, 128, 80>(p, pools, sms, device, stream);
+  if (p.w.dim == 96) return paged_rows<T, 128, 96>(p, pools, sms, device, stream);
   if (p.w.dim == 112 && tight) return paged_rows<T, 128, 112>(p, pools, sms, device, stream);
   return paged_rows<T, 128, 0>(p, pools, sms, device, stream);
 }
