@@ -213,8 +213,9 @@ __device__ __forceinline__ void paged_math(const PagedParams& p, const Pipe& pip
       for (int f = 0; f < 8; ++f) most = fmaxf(most, fabsf(y[f]) < INFINITY ? fabsf(y[f]) : 0.0f);
 #pragma unroll
       for (int o = DP / 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-      // 2^k most in 2^14 .. 2^15 (of rows near either end of the range, as far as f32 goes)
-      const int k = most == 0.0f ? 0 : min(max(14 + 127 - static_cast<int>(__float_as_uint(most) >> 23), -110), 110);
+      // 2^k most in 2^14 .. 2^15 (2^127 takes k = -113); of small rows 2^k is 2^110, with
+      // which bf16's smallest step, 2^-133, is f16's 2^-23, so nothing is lost either
+      const int k = most == 0.0f ? 0 : min(14 + 127 - static_cast<int>(__float_as_uint(most) >> 23), 110);
       const float by = __int_as_float((127 + k) << 23);
       factor = p.scale_log2 * __int_as_float((127 - k) << 23);
 #pragma unroll
