@@ -28,7 +28,9 @@
 // exponent: t = score + log2(vs) for each key, m the running maximum of t, w = 2^(t
 // - m) the weight in the second product, O = sum w x, and l = sum w / vs, so out = O
 // / l.  One exponential a pair, and w has its digits relative to what the key may
-// add to the result, however far the pages' scales are apart (within 2^100).
+// add to the result, however far the pages' scales are apart (within 2^100).  w is
+// 2^15 at most, so over 2^29 keys with scales of 2^-100 l would pass 2^128: it is held
+// times 2^-18, which leaves it between 2^-111 and 2^126, and O / l below 2^127.
 //
 // Shares of the keys, their joins by a cluster (up to four) or through a workspace,
 // as in cached_kernel.cuh.  Masks are made where a step holds the sequence's end, the
@@ -55,6 +57,7 @@ namespace vattn {
 constexpr int kPagedKeys = 32;  // keys of a warp's part of a step
 constexpr int kPagedWarps = 4;  // math warps
 constexpr int kPagedCluster = 4;  // shares that a cluster of blocks joins by itself
+constexpr float kPagedSumScale = 0x1p-18f;  // l is held times this (above)
 
 struct PagedParams {
   WindowParams w;  // n_keys: rows that the table has room for; kv_len: the cache's
@@ -517,7 +520,7 @@ __device__ __forceinline__ void paged_math(const PagedParams& p, const Pipe& pip
     const bool none = sum == 0.0f || cached_word(w, b, t, sp.base) == 0;
     const float inv = 1.0f / sum;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = none ? 0.0f : acc[e] * inv;
+    for (int e = 0; e < 8; ++e) acc[e] = none ? 0.0f : acc[e] * inv * kPagedSumScale;
     reinterpret_cast<Vec<T, 8>*>(rows_at_mut<T>(p.out, b, kh * w.group + static_cast<int>(head), t) + d)->narrow(acc);
   };
   const bool alone = p.splits == 1 || (sp.one() && !clustered);
@@ -685,7 +688,7 @@ __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads, 2)
       if (v == 0.0f) v = 0x1p-64f;  // zeros, whatever the bytes: below any f16, and l stays finite
       x.k = p.k_scale[at];
       x.log2_v = log2f(v);
-      x.inv_v = 1.0f / v;
+      x.inv_v = kPagedSumScale / v;
     };
     Box now{}, next{};
     const uint64_t once = ptx::policy_evict_first();
@@ -872,7 +875,8 @@ __global__ void __launch_bounds__(256) vattn_paged_join_kernel(const __grid_cons
   }
   const float inv = 1.0f / sum;
   const bool zero = none || sum == 0.0f;
-  const float out[4] = {zero ? 0.0f : acc.x * inv, zero ? 0.0f : acc.y * inv, zero ? 0.0f : acc.z * inv, zero ? 0.0f : acc.w * inv};
+  const float out[4] = {zero ? 0.0f : acc.x * inv * kPagedSumScale, zero ? 0.0f : acc.y * inv * kPagedSumScale,
+                        zero ? 0.0f : acc.z * inv * kPagedSumScale, zero ? 0.0f : acc.w * inv * kPagedSumScale};
   reinterpret_cast<Vec<T, 4>*>(rows_at_mut<T>(p.out, b, kh * w.group + (rr - t * w.group), t) + d)->narrow(out);
 }
 
@@ -922,7 +926,8 @@ __global__ void __launch_bounds__(256) vattn_paged_join_few_kernel(const __grid_
   if (lane * 4 >= D) return;
   const float inv = 1.0f / sum;
   const bool zero = none || sum == 0.0f;
-  const float out[4] = {zero ? 0.0f : acc.x * inv, zero ? 0.0f : acc.y * inv, zero ? 0.0f : acc.z * inv, zero ? 0.0f : acc.w * inv};
+  const float out[4] = {zero ? 0.0f : acc.x * inv * kPagedSumScale, zero ? 0.0f : acc.y * inv * kPagedSumScale,
+                        zero ? 0.0f : acc.z * inv * kPagedSumScale, zero ? 0.0f : acc.w * inv * kPagedSumScale};
   reinterpret_cast<Vec<T, 4>*>(rows_at_mut<T>(p.out, b, kh * w.group + (rr - t * w.group), t) + lane * 4)->narrow(out);
 }
 
