@@ -95,9 +95,10 @@ vattn_status vattn_append_paged(const vattn_rows* k, const vattn_rows* v, const 
  * products exactly (bf16 q down to 2^-29 of its row's largest), the softmax
  * weights, times the values' scale, as f16.  Scales lie in 2^-100 .. 2^100
  * (powers of two or not), those of one sequence's values within 2^100 of each
- * other; a scale of 0 makes the page's rows zeros (of values, counted as
- * 2^-64).  What rows that no query sees hold, bytes or scales, does not reach
- * the result; a NaN byte reaches the queries that see it, and no others.
+ * other; a scale of 0 makes the page's keys zeros, or its values, these
+ * whatever the bytes and counted as 2^-100.  What rows that no query sees
+ * hold, bytes or scales, does not reach the result; any other NaN byte reaches
+ * the queries that see it, and no others.
  * Scores that are not finite: as in vattn_forward_window.
  *
  * q, out [batch, n_q_heads, T, head_dim]; alignment and strides as in

@@ -58,3 +58,67 @@ def test_scales_of_values_at_both_ends(td, n_seqs, exponent):  # noqa: F811
         against_the_oracle(out[s], q[s], cache[:4] + [cache[4][s], cache[5][s]], None, 0, None, scale, "bf16", f"sequence {b}")
     assert bool(out.any(-1).all())
     assert vef.device_status() == 0
+
+
+def zeros_for(torch, cache, pages, pools=(0, 1)):
+    """What the cache stands for where these pages' scales are 0: bytes of zeros, in units of the smallest
+    scale that is not."""
+    out = [t.clone() for t in cache]
+    for i in pools:
+        out[i].view(torch.uint8)[pages] = 0
+        left = out[2 + i][out[2 + i] > 0]
+        out[2 + i][pages] = float(left.min()) if left.numel() else 1.0
+    return out
+
+
+@pytest.mark.parametrize("name,exponent", [("f16", -6), ("bf16", -6), ("bf16", -90), ("bf16", 0)])
+@pytest.mark.parametrize("H,T,D", [(1, 1, 64), (8, 2, 128), (4, 5, 80), (4, 8, 32), (4, 11, 64), (8, 7, 128), (5, 20, 96)])
+def test_pages_whose_scale_is_zero(td, name, exponent, H, T, D):  # noqa: F811
+    """Scales of 0 in both pools, or in one: zeros whatever the bytes (of values, NaN among them), beside pages whose
+    scales are near 1 or far from it; first, in between and last; and a NaN of another page in the same step."""
+    torch, dev = td
+    for page, lens in ((16, [300, 90]), (64, [2500, 700])):
+        case = (name, (2, 2 * H, 2, T, D), page, lens, None, 0, False, "heads", "plain")
+        q, cache, _, how = build(td, case, 2100 + T)
+        cache[3] *= 2.0 ** exponent
+        last = [(n - 1) // page for n in lens]
+        gone = torch.cat([cache[4][0, [0, 1, 2, last[0]]], cache[4][1, [1, last[1]]]]).long()
+        for pools in ((0, 1), (1,), (0,)):
+            zero = [t.clone() for t in cache]
+            for i in pools:
+                zero[i].view(torch.uint8)[gone] = torch.randint(0, 0x7f, (1,) + zero[i].shape[1:], dtype=torch.uint8, device=dev)
+                if i == 1:
+                    zero[i].view(torch.uint8)[gone, :, 3] = 0x7f
+                zero[2 + i][gone] = 0
+            want = zeros_for(torch, cache, gone, pools)
+            out = vef.forward_paged(q, *zero, **how)
+            against_the_oracle(out, q, want, None, 0, None, how["scale"], name, f"pools {pools}, pages of {page}")
+        # a NaN in the last token's value: in the rows that see it alone, in a step that holds a page of zeros
+        P, row = int(cache[4][0, last[0] - 1]), page - 1
+        n = last[0] * page  # rows in use now: up to that one
+        zero[5] = ints(torch, [n, lens[1]], dev)
+        zero[3][gone] = 0
+        zero[1].view(torch.uint8)[gone, :, 5] = 0x7f
+        want = zeros_for(torch, cache, gone) if 0 in pools else zeros_for(torch, cache, gone, (1,))
+        want[5] = zero[5]
+        clean = vef.forward_paged(q, *zero, **how)
+        against_the_oracle(clean, q, want, None, 0, None, how["scale"], name, f"{n} rows")
+        zero[1].view(torch.uint8)[P, 0, row, 7] = 0xff
+        out = vef.forward_paged(q, *zero, **how)
+        bad = torch.isnan(out)
+        assert bool(bad[0, :H, T - 1, 7].all()) and int(bad.sum()) == H
+        against_the_oracle(torch.where(bad, clean, out), q, want, None, 0, None, how["scale"], name, f"{n} rows, a NaN")
+    assert vef.device_status() == 0
+
+
+@pytest.mark.parametrize("name", ["f16", "bf16"])
+def test_all_scales_zero(td, name):  # noqa: F811
+    """Every visible page of values in units of 0: zeros exactly."""
+    torch, dev = td
+    for T, lens in ((1, [3000]), (3, [100]), (9, [700])):
+        case = (name, (1, 8, 2, T, 64), 16, lens, None, 0, False, "tokens", "plain")
+        q, cache, _, how = build(td, case, 2200 + T)
+        cache[1].view(torch.uint8)[:, :, 2] = 0x7f
+        cache[3].zero_()
+        assert not bool(vef.forward_paged(q, *cache, **how).any())
+        assert not bool(torch.isnan(vef.forward_paged(q, *cache, **how)).any())

@@ -37,7 +37,8 @@
 // first keys' end, the window's edge or new tokens: one lane looks up 16 keys of one
 // row.  Values of keys that none of a warp's rows sees are cleared in registers; a NaN
 // in one that some see and others do not sends the step through loops over visible
-// pairs.
+// pairs.  A value whose scale is 0 counts as one that no row sees, but for its weight in
+// l: log2(vs) is -infinity, which marks it, and 2^-100 in its place.
 //
 // 32 sequences x 8 key heads x up to 16385 keys of 128, one token of 32 heads, bf16:
 // 107 us, 6.8 TB/s, the measured copy rate.  One sequence of 200003 keys, one key head
@@ -58,6 +59,7 @@ constexpr int kPagedKeys = 32;  // keys of a warp's part of a step
 constexpr int kPagedWarps = 4;  // math warps
 constexpr int kPagedCluster = 4;  // shares that a cluster of blocks joins by itself
 constexpr float kPagedSumScale = 0x1p-18f;  // l is held times this (above)
+constexpr float kPagedZeroLog2 = -100.0f;   // of the scale that counts for values of zeros
 
 struct PagedParams {
   WindowParams w;  // n_keys: rows that the table has room for; kv_len: the cache's
@@ -288,8 +290,9 @@ __device__ __forceinline__ void paged_math(const PagedParams& p, const Pipe& pip
 #pragma unroll
     for (int ks = 0; ks < CH; ++ks)  // matrices: keys 0-7, 8-15, 16-23, 24-31 by the 16 dims of chunk ks
       ldmatrix_x4(ks_s + tile_at(lane, ks), kf[ks]);
-    // the warp's keys by 16: first of each in the sequence, scales; those that are
-    // not there, or that no row sees, count as masked throughout
+    // the warp's keys by 16: first of each in the sequence (behind it if they are not
+    // there), scales; those that not all rows see count as masked, and those whose
+    // values are zeros (meta.x < 0)
     int j0[2];
     float4 meta[2];
     bool masked[2];
@@ -298,10 +301,8 @@ __device__ __forceinline__ void paged_math(const PagedParams& p, const Pipe& pip
       const int at = kw * kPagedKeys + mb * 16;
       meta[mb] = ptx::ld_shared_v4(smem_s + P::kOffMeta + static_cast<uint32_t>((st * 8 + (at >> p.log_box)) * 16));
       const int j = __float_as_int(meta[mb].w) + (at & (p.box - 1));
-      const bool on = !(meta[mb].x < 0.0f);
-      j0[mb] = on ? j : 1 << 30;
-      if (!on) meta[mb] = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
-      masked[mb] = !on || j + 15 >= free_end || (j < free_begin && j + 15 >= w.sinks);
+      j0[mb] = j;
+      masked[mb] = (meta[mb].x < 0.0f) | (j + 15 >= free_end) | ((j < free_begin) & (j + 15 >= w.sinks));
     }
     const bool some = masked[0] || masked[1];
     // ---- S = K Q^T, over the even and the odd chunks by themselves where that
@@ -341,6 +342,7 @@ __device__ __forceinline__ void paged_math(const PagedParams& p, const Pipe& pip
     // the new tokens.  Lane i looks up rows i % 16 (+ 16) of the warp and keys i / 16.
     bool loops = false;
     uint32_t see[2][NB][2];  // of rows 2 c4 + e: 16 keys a word, where masked
+    uint32_t any_w = 0;      // keys whose values some row takes
     if (some) {
       const int mb = lane >> 4, j = mb ? j0[1] : j0[0];
       uint32_t mine[(NB + 1) / 2], any = 0, every = 0xffffu;
@@ -364,14 +366,18 @@ __device__ __forceinline__ void paged_math(const PagedParams& p, const Pipe& pip
             for (int h = 0; h < 2; ++h)
               if (!((see[k][nb][e] >> (8 * h)) & 1u)) s[k][nb][2 * h + e] = -INFINITY;
           }
+      if ((mb ? meta[1].y : meta[0].y) == -INFINITY) any = 0;
       const uint32_t half = mb ? 0xffff0000u : 0x0000ffffu;
-      const uint32_t any_w = __reduce_or_sync(0xffffffffu, (any << (16 * mb)) & half);
+      any_w = __reduce_or_sync(0xffffffffu, (any << (16 * mb)) & half);
       const uint32_t every_w = __reduce_and_sync(0xffffffffu, (every << (16 * mb)) | ~half);
       // V of keys that none of the warp's rows sees may hold anything: zeros; and so may
-      // the scales of 16 such keys
+      // the scales of 16 such keys (c below has bounds of its own)
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        if (((any_w >> (16 * k)) & 0xffffu) == 0) meta[k] = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+        if (((any_w >> (16 * k)) & 0xffffu) == 0) {
+          meta[k].y = kPagedZeroLog2;
+          meta[k].z = kPagedSumScale * 0x1p100f;
+        }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {  // keys 8 q + 2 c4, + 1: low and high halves
         const uint32_t a = any_w >> (8 * q + 2 * c4);
@@ -401,7 +407,7 @@ __device__ __forceinline__ void paged_math(const PagedParams& p, const Pipe& pip
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int mb = 0; mb < 2; ++mb)  // not 0 or infinity, which -infinity or 0 make NaN
-          c[mb][nb][e] = fminf(fmaxf(row_c[nb][e] * meta[mb].x, 0x1p-126f), 0x1p127f);
+          c[mb][nb][e] = fminf(fmaxf(row_c[nb][e] * fabsf(meta[mb].x), 0x1p-126f), 0x1p127f);
         top[nb][e] = fmaxf(fmaf(fmaxf(s[0][nb][e], s[0][nb][e + 2]), c[0][nb][e], meta[0].y),
                            fmaf(fmaxf(s[1][nb][e], s[1][nb][e + 2]), c[1][nb][e], meta[1].y));
         grew |= top[nb][e] > m[nb][e] + kLazyLog2;
@@ -467,7 +473,7 @@ __device__ __forceinline__ void paged_math(const PagedParams& p, const Pipe& pip
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (!((see[k][nb][e & 1] >> (8 * (e >> 1))) & 1u)) s[k][nb][e] = -1.0f;
+            if (!((see[k][nb][e & 1] >> (8 * (e >> 1))) & 1u) || ((any_w >> (16 * k)) & 0xffffu) == 0) s[k][nb][e] = -1.0f;
 #pragma unroll 1
       for (int y = 0; y < 8; ++y)
 #pragma unroll
@@ -666,7 +672,7 @@ __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads, 2)
     const int loader = warp - kPagedWarps, mine = boxes - (loader >> 1);  // boxes loader / 2, + 2, ... of a step's K or V
     struct Box {
       int page, row, key0;          // page: behind the last if it is not there, and reads as zeros
-      float k, log2_v, inv_v;       // k < 0: the keys are not there
+      float k, log2_v, inv_v;       // k < 0: the values are zeros
     };
     auto place = [&](int i, Box& x) {  // of the share's box i
       x.key0 = sp.box(v0 + i) << p.log_box;
@@ -678,15 +684,16 @@ __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads, 2)
         if (id >= 0 && id < p.n_pages) x.page = id;
       }
       x.row = static_cast<int>(row);
+      if (x.page >= p.n_pages) x.key0 = 1 << 30;
     };
     auto scales = [&](Box& x) {  // (the first loader's)
-      x.k = -1.0f;
-      x.log2_v = x.inv_v = 0.0f;
+      x.k = x.inv_v = 1.0f;
+      x.log2_v = 0.0f;
       if (loader != 0 || x.page >= p.n_pages) return;
       const long long at = static_cast<long long>(x.page) * w.kv_heads + kh;
-      float v = p.v_scale[at];
-      if (v == 0.0f) v = 0x1p-64f;  // zeros, whatever the bytes: below any f16, and l stays finite
+      const float v = p.v_scale[at];
       x.k = p.k_scale[at];
+      if (v == 0.0f) x.k = -fmaxf(x.k, 0x1p-126f);
       x.log2_v = log2f(v);
       x.inv_v = kPagedSumScale / v;
     };
