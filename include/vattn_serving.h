@@ -76,9 +76,10 @@ typedef struct {
  * it was, rows behind kv_len among them.
  *
  * cu_seqlens ascends; its values are held to [0, n_tokens], and a sequence
- * that ends before it begins is empty.  Rows of k and v in no sequence are not
- * read.  The same call gives the same bits every time, and repeated, leaves
- * what it left.
+ * that ends before it begins is empty; if the sequences then have more than
+ * n_tokens rows together, nothing is appended.  Rows of k and v in no sequence
+ * are not read.  The same call gives the same bits every time, and repeated,
+ * leaves what it left.
  */
 vattn_status vattn_append_paged(const vattn_rows* k, const vattn_rows* v, const vattn_pages* cache,
                                 const vattn_append_args* args, void* stream);
