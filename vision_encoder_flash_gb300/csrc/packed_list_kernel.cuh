@@ -7,7 +7,9 @@
 // tiles follow, a counting sort puts the pairs of late row blocks first, and
 // pairs of one row block come in any order (no result depends on it).  Prompts that
 // together have more rows than there are (starts that do not ascend) make an empty
-// list: the room for it is that of prompts that do not overlap.
+// list: the room for it is that of prompts that do not overlap.  A warp stops where its
+// own prompts are too many already, so whatever the starts hold, its pairs are no more
+// than those of prompts that fit.
 #pragma once
 
 #include "window_pipe.cuh"
@@ -43,14 +45,18 @@ __global__ void __launch_bounds__(kListThreads) vattn_packed_list_kernel(const _
   auto block_of = [&](int rows, long long i) {
     return min((rows + kTile - 1) / kTile - 1, static_cast<int>((2 * i + 1) / p.group));
   };
-  auto each = [&](auto&& take) {
+  auto each = [&](auto&& take) {  // -> rows of the warp's prompts
+    long long sum = 0;
     for (int b0 = warp * at_a_time; b0 < p.n_seqs; b0 += warps * at_a_time) {
       const int b = b0 + lane;
       int first = 0, rows = 0;
       if (lane < at_a_time && b < p.n_seqs) {
         first = min(max(p.cu[b], 0), p.total);
-        rows = min(max(p.cu[b + 1], 0), p.total) - first;
+        rows = max(0, min(max(p.cu[b + 1], 0), p.total) - first);
       }
+      sum += __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(rows) & 0xffffu) +
+             (static_cast<long long>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(rows) >> 16)) << 16);
+      if (sum > p.total) break;
       const long long pairs = rows > 0 ? pairs_of(rows) : 0;
       const bool alone = pairs <= 8;
       if (alone)
@@ -62,14 +68,9 @@ __global__ void __launch_bounds__(kListThreads) vattn_packed_list_kernel(const _
         for (long long i = lane; i < all; i += 32) take(f, n, static_cast<int>(i), block_of(n, i));
       }
     }
+    return sum;
   };
-  long long mine = 0;  // rows of the prompts whose first pair this lane had
-  each([&](int, int rows, int pair, int block) {
-    if (pair == 0) mine += rows;
-    atomicAdd(&counts[block], 1);
-  });
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  const long long mine = each([&](int, int, int, int block) { atomicAdd(&counts[block], 1); });
   if (lane == 0) rows_s[warp] = mine;
   __syncthreads();
   // counts to places: behind the pairs of all later row blocks
