@@ -72,8 +72,9 @@ typedef struct {
  * with scale = need; else scale = max(scale, need), and the rows before the
  * new ones are rescaled to it, exactly but for values that leave e4m3's
  * normal range.  New values are x / scale rounded to nearest even, once, from
- * f32; an infinity or NaN becomes NaN.  Every other byte and scale stays as
- * it was, rows behind kv_len among them.
+ * f32; an infinity or NaN becomes NaN.  (bf16 values beyond 448 * 2^100 make
+ * scales that vattn_forward_paged does not take.)  Every other byte and scale
+ * stays as it was, rows behind kv_len among them.
  *
  * cu_seqlens ascends; its values are held to [0, n_tokens], and a sequence
  * that ends before it begins is empty; if the sequences then have more than

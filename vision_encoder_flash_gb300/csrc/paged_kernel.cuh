@@ -41,13 +41,13 @@
 // l: log2(vs) is -infinity, which marks it, and 2^-100 in its place.
 //
 // 32 sequences x 8 key heads x up to 16385 keys of 128, one token of 32 heads, bf16:
-// 107 us, 6.8 TB/s, the measured copy rate.  One sequence of 200003 keys, one key head
-// of 8: 13.6 us, 3.8 TB/s: 3 us before the first products, 4 for the join.  Where a
+// 106 us, 6.8 TB/s, the measured copy rate.  One sequence of 200003 keys, one key head
+// of 8: 13.7 us, 3.7 TB/s: 3 us before the first products, 4 for the join.  Where a
 // call is small a step is latency (1200 cycles alone on its scheduler), and so is the
 // code that runs once: rolled loops for q took 1 us off a call.  With many rows the
 // bound is the two warps a scheduler has: 22 cycles a product of 16 keys x 8 rows x 16
 // dims whatever else a step does, where the tensor core needs 8 (11 tokens of 4 heads,
-// 13 x 4 x 38131 keys of 128: 151 us, 2.3 TB/s).
+// 13 x 4 x 38131 keys of 128: 150 us, 2.3 TB/s).
 #pragma once
 
 #include "cached_kernel.cuh"
@@ -618,9 +618,9 @@ __device__ __forceinline__ void paged_math(const PagedParams& p, const Pipe& pip
 // kDim: 0, or 48, 80 or 112 dims whose rows are one behind the other in a page: boxes as
 // untiled copies, and shared rows as they are.  As tiles of 64 or 128 columns such rows
 // begin and end inside the sectors that a copy reads: 32 x 8 key heads x up to 16000 keys
-// x 80 took 127 us and now 78, of 112 101 and 98, of 48 75 and 65 (96 and 64 dims take 89
-// and 63), and the products skip the chunks that are not there (200003 keys of one head x
-// 80 17.5 and 12.5).  An odd number of 16-byte chunks a row leaves ldmatrix without a
+// x 80 took 127 us and now 79, of 112 101 and 99, of 48 75 and 60 (96 and 64 dims take 84
+// and 62), and the products skip the chunks that are not there (200003 keys of one head x
+// 80 17.5 and 11.8).  An odd number of 16-byte chunks a row leaves ldmatrix without a
 // conflict, unswizzled.  96: tiles, with the products of the chunks that are there.
 template <typename T, int DP, int NB, int RW, int kDim>
 __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads, 2)

@@ -38,10 +38,16 @@ vattn_status paged_launch(PagedParams p, const Pools& pools, int sms, int device
   p.row_blocks = (p.rows + P::kRows - 1) / P::kRows;
   if (seqs * p.row_blocks > kMaxRows || seqs * p.rows > INT32_MAX)
     return fail(VATTN_ERR_UNSUPPORTED, "too many query rows");
-  // Shares of the keys: as many blocks as are resident at a time, of 256 keys at
-  // least, or of 128 where that makes no more than 32 shares.  Four, which a cluster
-  // joins, where that leaves a warp five steps at most and enough blocks: as fast as
-  // more shares and their join on the device, and 4 us less host time for a call.
+  // Shares of the keys, as many for each sequence, from what the table has room for (lengths
+  // are on the device; shares behind a sequence's end are empty): as many blocks as are
+  // resident at a time, of 256 keys at least, or of 128 where that makes no more than 32
+  // shares.  Four, which a cluster joins, where that leaves a warp five steps at most and
+  // enough blocks: 4 us less host time for a call than more shares and their join on the
+  // device, and from 24 blocks on about the same device time (24 blocks of 600 to 2500 keys
+  // x 64 5.9 to 7.6 us, with more shares 6.4 to 7.5, x 128 6.8 to 8.9 and 6.1 to 8.3; 32
+  // blocks x 128 6.8 to 9.1 and 6.7 to 9.1).  With fewer blocks the device pays for it: 16
+  // of 2500 keys x 128 8.8 and 8.4, 10 8.8 and 7.2; with 4, where the rule does not hold,
+  // 8.7 and 6.2.
   const long long most_keys = std::min<long long>(p.w.n_keys, static_cast<long long>(p.w.sinks) + p.w.window + p.w.n_queries);
   const long long blocks = seqs * p.row_blocks, room = static_cast<long long>(resident) * sms;
   const long long fill = room / blocks >= 4 ? room / blocks : (room + blocks - 1) / blocks;
@@ -113,7 +119,7 @@ vattn_status paged_launch(PagedParams p, const Pools& pools, int sms, int device
 // serves, RW such groups; the warps left share the keys.  At head_dim 128 a warp's
 // registers hold 24 rows of O: 17 to 24 rows in two groups of 16 took 21.4 us where one of
 // 24 takes 19.6 (24 rows, 32 x 8000 keys; head_dim 64 16.4 and 14.1), 33 to 48 in four of
-// 16 took 204 us, in two of 24 151 (44 rows, 52 x 38131 keys).  Beyond, blocks of 48 rows
+// 16 took 204 us, in two of 24 150 (44 rows, 52 x 38131 keys).  Beyond, blocks of 48 rows
 // where they need little more time than those of 64: a block of 48 takes 0.62 to 0.72
 // of one of four groups of 16 (head_dim 128: 128 rows 73.4 and 78.7 us, 64 rows 93.6 and
 // 67.2), and 0.75 of one of two groups of 32, for which smaller rows have room (head_dim
