@@ -752,7 +752,7 @@ __global__ void __launch_bounds__(PagedPlan<DP, NB, RW>::kThreads, 2)
         y.lo = sp.base + __popcll(y.news) - 1 - w.window;
         if (w.tree == nullptr) {
           y.news &= ~bits64_upto(t - w.window) | bits64_upto(w.sinks - 1 - sp.base);
-        } else if (y.lo >= sp.base) {  // a window inside the tree
+        } else if (y.lo >= sp.base - 1) {  // a window inside the tree (tokens without bits are at base - 1)
           for (uint64_t left = y.news; left != 0; left &= left - 1) {
             const int u = __ffsll(static_cast<long long>(left)) - 1, at = kpos[u];
             if (at <= y.lo && at >= w.sinks) y.news &= ~(1ull << u);
